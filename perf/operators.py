@@ -187,30 +187,31 @@ def run(s):
 
 
 def _run_own(s, op):
-    from block_masked_token_gb300 import mars
+    from block_masked_token_gb300 import packed
     c = s.case
     if op == "append":
-        mars.mars_kv_append(s.k, s.v, s.cu, s.old, s.table, s.k_pool, s.v_pool,
-                            new_lens=s.new_lens, slots=s.slots, status=s.status)
+        packed.mars_kv_append(s.k, s.v, s.cu, s.old, s.table, s.k_pool, s.v_pool,
+                              new_lens=s.new_lens, slots=s.slots, status=s.status)
         return {"k_pool": s.k_pool, "v_pool": s.v_pool, "new_lens": s.new_lens, "slots": s.slots}
     if s.ws is None:         # the workspace that a program keeps for a batch of this shape
-        code = {"chunk": mars.OP_ATTN_CHUNK, "packed": mars.OP_ATTN_PACKED,
-                "train": mars.OP_ATTN_PACKED}[op]
-        size = mars.mars_packed_workspace_bytes(code, c["batch"], s.rows, c["hq"], c["hkv"],
-                                                c["d"], s.max_len)
+        code = {"chunk": packed.OP_ATTN_CHUNK, "packed": packed.OP_ATTN_PACKED,
+                "train": packed.OP_ATTN_PACKED}[op]
+        size = packed.mars_packed_workspace_bytes(code, c["batch"], s.rows, c["hq"], c["hkv"],
+                                                  c["d"], s.max_len)
         if op == "train":
-            size = max(size, mars.mars_packed_workspace_bytes(
-                mars.OP_ATTN_PACKED_GRAD, c["batch"], s.rows, c["hq"], c["hkv"], c["d"], s.max_len))
+            size = max(size, packed.mars_packed_workspace_bytes(
+                packed.OP_ATTN_PACKED_GRAD, c["batch"], s.rows, c["hq"], c["hkv"], c["d"],
+                s.max_len))
         s.ws = torch.empty(max(1, size), dtype=torch.uint8, device="cuda")
     if op == "chunk":
-        mars.mars_attn_chunk(s.q, s.k, s.v, s.cu, s.k_pool, s.v_pool, s.table, s.old, s.max_len,
-                             s.o, s.ws, status=s.status)
+        packed.mars_attn_chunk(s.q, s.k, s.v, s.cu, s.k_pool, s.v_pool, s.table, s.old,
+                               s.max_len, s.o, s.ws, status=s.status)
         return {"o": s.o}
-    mars.mars_attn_packed(s.q, s.k, s.v, s.cu, s.o, s.ws, lse=s.lse, status=s.status)
+    packed.mars_attn_packed(s.q, s.k, s.v, s.cu, s.o, s.ws, lse=s.lse, status=s.status)
     if op == "packed":
         return {"o": s.o, "lse": s.lse}
-    mars.mars_attn_packed_grad(s.q, s.k, s.v, s.o, s.d_o, s.lse, s.cu, s.dq, s.dk, s.dv, s.ws,
-                               status=s.status)
+    packed.mars_attn_packed_grad(s.q, s.k, s.v, s.o, s.d_o, s.lse, s.cu, s.dq, s.dk, s.dv, s.ws,
+                                 status=s.status)
     return {"o": s.o, "lse": s.lse, "dq": s.dq, "dk": s.dk, "dv": s.dv}
 
 
