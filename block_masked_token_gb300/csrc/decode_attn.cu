@@ -69,6 +69,7 @@ template <int D>
 struct DecodePolicy {
   static constexpr bool kHandOff = false;
   static constexpr bool kRowStats = false;
+  static constexpr bool kClearRows = false;
   const DecodeArgs* a;
   const int32_t* bt_row;
   float* part;           // [R][D + 4] records of this (sequence, kv head, split)

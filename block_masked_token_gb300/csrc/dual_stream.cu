@@ -35,6 +35,7 @@ template <int D>
 struct DualPolicy {
   static constexpr bool kHandOff = true;
   static constexpr bool kRowStats = true;
+  static constexpr bool kClearRows = false;
   static constexpr int kStageBoxes = D / 32 < 2 ? D / 32 : 2;
   const CUtensorMap* tm_o;   // O as [2*batch][L][hq][D] fp32, box [1][128][1][32]
   float* lse;                // optional: [batch][hq][2][Lp] row log-sum-exp (log2 units),

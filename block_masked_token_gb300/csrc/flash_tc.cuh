@@ -420,7 +420,8 @@ MARS_DEV void exp2_pack64(const uint32_t (&r)[BKV], int c0, float scale_log2, fl
 // every row sees every key of tile j, so no per-key test runs), cols(vis, tile) ->
 // ColRange (the columns of tile j visible to the row; a tile must admit only keys it
 // owns, so no key is counted twice), with kRowStats row_stats(row, m, l) once the row is
-// done, and either store_chunk(row, col, 32 fp32 of O, 1/l, m, l) or, with kHandOff,
+// done, with kClearRows key_read(tile, key) (false for a key of a tile with .clear set that
+// no row may read, see below), and either store_chunk(row, col, 32 fp32 of O, 1/l, m, l) or, with kHandOff,
 // hand_off(row, 1/l) for the epilogue warps (staged_epilogue below).
 // Each tile's S row is read from TMEM once (4 loads, one wait) into registers.
 //
@@ -511,6 +512,23 @@ MARS_DEV bool softmax_loop(Barriers& bar, uint8_t* smem, const Policy& pol, int 
       tmem_st32(p_addr + h * 32, packed);
     }
     l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+    // A key that no row may read has weight 0, but 0 times an infinity or NaN held in its V
+    // row would still reach O: thread t clears V row t of such keys before the PV MMA.
+    if constexpr (Policy::kClearRows) {
+      if (tile.clear) {
+        constexpr int VST = Policy::kVStages;
+        if (!(ok = warp_wait(&bar.v_full[jg % VST], (jg / VST) & 1))) break;
+        if (!pol.key_read(tile, row)) {
+          uint8_t* v = smem + S::OFF_V + (jg % VST) * S::KV_BYTES + row * 128;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4*>(v + x * (BKV * 128) + q * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+    }
     tmem_st_wait();
     tc_fence_before();
     mbar_arrive_warp(&bar.p_full[sb]);

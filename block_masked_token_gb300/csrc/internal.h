@@ -115,4 +115,37 @@ cudaError_t launch_dual_stream_dq(const uint16_t* q, const uint16_t* k, const ui
                                   float* dq, int batch, int L, int B, int hq, int hkv, int d,
                                   float scale, int32_t* status, cudaStream_t stream);
 
+// ---- Packed sequences: causal attention, without a cache or after a paged prefix.
+struct PackedAttn {
+  const uint16_t *q, *k, *v;            // [total][heads][d], row pitches in elements
+  long long q_stride, k_stride, v_stride;
+  const int32_t* cu;                    // [batch + 1]
+  const uint16_t *k_pool, *v_pool;      // with a cache
+  const int32_t *block_table, *seq_lens;   // seq_lens NULL: no cache
+  int num_pages, max_pages;
+  uint16_t* o;                          // [total][hq][d] bf16
+  float* lse;                           // [hq][total] or NULL
+  int batch, total, hq, hkv, d;
+  float scale;
+  int32_t* status;
+};
+struct PackedPlan {
+  int gp, tpt;             // heads and tokens of a row tile
+  int nsplit, split_tiles; // splits of a key list, 128-key tiles per split
+  long long ctas;
+  size_t ws_bytes;
+};
+// max_len: upper bound of a sequence's keys (cached and own) for which the splits are sized.
+PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len);
+cudaError_t launch_packed_attn(const PackedAttn& p, const PackedPlan& plan, void* workspace,
+                               cudaStream_t stream);
+
+// ---- K/V rows of packed sequences into the paged cache.
+cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, long long k_stride,
+                             long long v_stride, const int32_t* cu, const int32_t* seq_lens,
+                             int32_t* new_lens, const int32_t* block_table, int max_pages,
+                             uint16_t* k_pool, uint16_t* v_pool, int num_pages, int32_t* slots,
+                             int batch, int total, int hkv, int d, int32_t* status,
+                             cudaStream_t stream);
+
 }  // namespace mars

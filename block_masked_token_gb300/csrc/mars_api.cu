@@ -361,6 +361,158 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
                                            static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+// Sizes shared by the packed entry points.
+int check_packed(int batch, int total, int hq, int hkv, int d) {
+  if (batch < 0 || total < 0) return MARS_EINVAL;
+  int rc = check_heads(hq, hkv, d);
+  if (rc) return rc;
+  // sequence boundaries, tiles and statistics rows are counted in 32 bits
+  if ((long long)total + batch > 0x7fffffffLL - 256 || (long long)hq * d > 0x3fffffffLL)
+    return MARS_EINVAL;
+  return MARS_OK;
+}
+
+// A row pitch: at least the row, and a multiple of 16 bytes.
+int check_pitch(int stride, int heads, int d) {
+  if (stride < (long long)heads * d) return MARS_EINVAL;
+  return stride % 8 ? MARS_EALIGN : MARS_OK;
+}
+
+// Pages are addressed by 32-bit row and slot numbers.
+bool pool_fits(int num_pages, int hkv) {
+  return num_pages >= 0 && (long long)num_pages * hkv * mars::kPageSize <= 0x7fffffffLL;
+}
+
+int grid_fits(long long ctas) { return ctas <= 0x7fffffffLL ? MARS_OK : MARS_EUNSUPPORTED; }
+
+int packed_attn_checked(mars::PackedAttn p, int max_len, void* workspace, size_t ws_bytes,
+                        void* stream) {
+  if (p.batch == 0 || p.total == 0) return MARS_OK;
+  if (!p.q || !p.k || !p.v || !p.cu || !p.o) return MARS_EINVAL;
+  int rc = check_pitch((int)p.q_stride, p.hq, p.d);
+  if (!rc) rc = check_pitch((int)p.k_stride, p.hkv, p.d);
+  if (!rc) rc = check_pitch((int)p.v_stride, p.hkv, p.d);
+  if (rc) return rc;
+  if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.o) ||
+      !aligned16(p.k_pool) || !aligned16(p.v_pool) || !aligned16(workspace))
+    return MARS_EALIGN;
+  if (!(p.scale > 0.f)) p.scale = 1.0f / sqrtf((float)p.d);
+  if (isinf(p.scale)) return MARS_EINVAL;
+  const mars::PackedPlan plan = mars::plan_packed(p.batch, p.total, p.hq, p.hkv, p.d, max_len);
+  if ((rc = grid_fits(plan.ctas))) return rc;
+  if (ws_bytes < plan.ws_bytes) return MARS_ENOSPACE;
+  if (plan.ws_bytes && !workspace) return MARS_EINVAL;
+  return cuda_rc(mars::launch_packed_attn(p, plan, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+size_t mars_packed_workspace_bytes(int op, int batch, int total, int hq, int hkv, int d,
+                                   int max_len) {
+  if (check_packed(batch, total, hq, hkv, d) != MARS_OK || batch == 0 || total == 0) return 0;
+  if (op == MARS_OP_ATTN_PACKED)
+    return mars::plan_packed(batch, total, hq, hkv, d, total).ws_bytes;
+  if (op == MARS_OP_ATTN_CHUNK)
+    return max_len < 0 ? 0 : mars::plan_packed(batch, total, hq, hkv, d, max_len).ws_bytes;
+  return 0;
+}
+
+int mars_attn_packed(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
+                     const int32_t* cu_seqlens, mars_bf16* o, float* lse, int batch, int total,
+                     int hq, int hkv, int d, int q_stride, int k_stride, int v_stride,
+                     float scale, void* workspace, size_t ws_bytes, int32_t* status,
+                     void* stream) {
+  int rc = check_packed(batch, total, hq, hkv, d);
+  if (rc) return rc;
+  mars::PackedAttn p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.cu = cu_seqlens;
+  p.o = o;
+  p.lse = lse;
+  p.batch = batch;
+  p.total = total;
+  p.hq = hq;
+  p.hkv = hkv;
+  p.d = d;
+  p.scale = scale;
+  p.status = status;
+  return packed_attn_checked(p, total, workspace, ws_bytes, stream);
+}
+
+int mars_attn_chunk(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
+                    const int32_t* cu_seqlens, const mars_bf16* k_pool, const mars_bf16* v_pool,
+                    int num_pages, const int32_t* block_table, int max_pages_per_seq,
+                    const int32_t* seq_lens, int max_len_hint, mars_bf16* o, int batch,
+                    int total, int hq, int hkv, int d, int page_size, int q_stride,
+                    int k_stride, int v_stride, float scale, void* workspace, size_t ws_bytes,
+                    int32_t* status, void* stream) {
+  int rc = check_packed(batch, total, hq, hkv, d);
+  if (rc) return rc;
+  if (max_len_hint < 0 || max_pages_per_seq < 0 || !pool_fits(num_pages, hkv)) return MARS_EINVAL;
+  if (page_size != mars::kPageSize) return MARS_EUNSUPPORTED;
+  if (batch > 0 && total > 0) {
+    if (!seq_lens) return MARS_EINVAL;
+    if (max_pages_per_seq > 0 && (!block_table || (num_pages > 0 && (!k_pool || !v_pool))))
+      return MARS_EINVAL;
+  }
+  mars::PackedAttn p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.cu = cu_seqlens;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.num_pages = k_pool && v_pool ? num_pages : 0;
+  p.max_pages = block_table ? max_pages_per_seq : 0;
+  p.o = o;
+  p.batch = batch;
+  p.total = total;
+  p.hq = hq;
+  p.hkv = hkv;
+  p.d = d;
+  p.scale = scale;
+  p.status = status;
+  return packed_attn_checked(p, max_len_hint, workspace, ws_bytes, stream);
+}
+
+int mars_kv_append(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seqlens,
+                   const int32_t* seq_lens, int32_t* new_lens, const int32_t* block_table,
+                   int max_pages_per_seq, mars_bf16* k_pool, mars_bf16* v_pool, int num_pages,
+                   int32_t* slots, int batch, int total, int hkv, int d, int page_size,
+                   int k_stride, int v_stride, int32_t* status, void* stream) {
+  int rc = check_packed(batch, total, hkv, hkv, d);
+  if (rc) return rc;
+  if (max_pages_per_seq < 0 || !pool_fits(num_pages, hkv)) return MARS_EINVAL;
+  if (page_size != mars::kPageSize) return MARS_EUNSUPPORTED;
+  if (batch == 0) return MARS_OK;
+  if (!cu_seqlens || !seq_lens) return MARS_EINVAL;
+  if (total > 0 && (!k || !v || !block_table || !k_pool || !v_pool)) return MARS_EINVAL;
+  if (new_lens == seq_lens) return MARS_EINVAL;
+  if (total > 0) {
+    rc = check_pitch(k_stride, hkv, d);
+    if (!rc) rc = check_pitch(v_stride, hkv, d);
+    if (rc) return rc;
+  }
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
+    return MARS_EALIGN;
+  return cuda_rc(mars::launch_kv_append(k, v, k_stride, v_stride, cu_seqlens, seq_lens, new_lens,
+                                        block_table, block_table ? max_pages_per_seq : 0, k_pool,
+                                        v_pool, num_pages, slots, batch, total, hkv, d, status,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
 const char* mars_strerror(int code) {
   switch (code) {
     case MARS_OK: return "ok";

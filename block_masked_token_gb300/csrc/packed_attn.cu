@@ -1,0 +1,393 @@
+// Causal attention over packed sequences, without a cache (prompts) or after a paged prefix
+// (a chunk of new tokens over the cache).
+//
+//   O_i = sum_u softmax_u(scale q_i . k_u) v_u over the keys row i of its sequence sees: the
+//   P = seq_lens[s] cached keys (none without a cache) and the sequence's own keys 0 .. i;
+//   lse_i = log2 sum_u exp2(scale log2(e) q_i . k_u).
+//
+// A CTA takes a tile of up to 128 (token, query head) rows that share one KV head: row r is
+// token r / gp of the tile and head r % gp of the group, so that K and V are read once for the
+// group. It runs the tcgen05 flash engine (flash_tc.cuh) over the 128-key tiles its rows see:
+// prefix tiles gathered page by page from the pool, then tiles of the sequence's own keys,
+// the last of which are causal. Keys past a sequence's end (rows of the next sequence, free
+// slots of the last page, unmapped pages) are masked, and their V rows cleared, so that
+// whatever they hold stays out.
+//
+// With few tiles and long key lists the list is cut into splits: each CTA writes an
+// unnormalised partial (m in log2 units, l, O) and a second kernel merges them.
+#include <climits>
+
+#include "common.cuh"
+#include "flash_tc.cuh"
+#include "internal.h"
+#include "packed.cuh"
+
+namespace mars {
+
+namespace {
+
+using flash::BKV;
+using flash::BQ;
+
+constexpr int kPagesPerTile = BKV / kPageSize;   // 8
+constexpr int kVStages = 3;                      // as in the decode kernel: no O staging area
+constexpr int kMinSplitTiles = 4;                // key tiles a split takes at least
+
+struct AttnArgs {
+  const int32_t* cu;
+  const int32_t* seq_lens;     // NULL: no cache
+  const int32_t* block_table;
+  int num_pages, max_pages;
+  int batch, total, hq, hkv, gp, tpt, ngrp, nsplit, split_tiles;
+  float scale_log2;
+  uint16_t* o;                 // [total][hq][D] bf16
+  float* lse;                  // [hq][total] or NULL
+  float* part;                 // [nsplit][total][hq][D + 4] with several splits
+  int32_t* status;
+};
+
+template <int D>
+struct RowsPolicy {
+  static constexpr bool kHandOff = false;
+  static constexpr bool kRowStats = false;
+  static constexpr bool kClearRows = true;
+  static constexpr int kVStages = mars::kVStages;
+  const AttnArgs* a;
+  const int32_t* bt_row;
+  int base, n, tok0;           // sequence rows [base, base + n); first token of the tile
+  int P, np;                   // cached keys, prefix tiles
+  int h0;                      // first query head
+  int j0, split;               // first key tile of this split
+  int last_tok;                // last token of the tile
+
+  struct Tile {
+    int k0;              // first key: cached position, or token of the sequence
+    uint32_t pmask;      // 16-key groups that may be read
+    int count;           // keys that may be read
+    bool prefix, full, clear;
+  };
+  MARS_DEV int token(int row) const { return tok0 + row / a->gp; }
+  MARS_DEV bool row_valid(int row) const { return row < a->gp * a->tpt && token(row) < n; }
+  MARS_DEV flash::RowVis row_vis(int row) const { return {token(row) + 1, 0, -1}; }
+  MARS_DEV Tile tile(int jl) const {
+    Tile t;
+    const int j = j0 + jl;
+    t.prefix = j < np;
+    if (t.prefix) {
+      t.k0 = j * BKV;
+      t.count = min(P - t.k0, BKV);
+      t.pmask = 0;
+      for (int i = 0; i < kPagesPerTile; ++i) {
+        const int lp = t.k0 / kPageSize + i;
+        const int e = lp < a->max_pages ? bt_row[lp] : -1;
+        if (e >= 0 && e < a->num_pages) t.pmask |= 1u << i;
+      }
+      t.full = t.count == BKV && t.pmask == 0xffu;
+      t.clear = !t.full;
+    } else {
+      t.k0 = (j - np) * BKV;
+      t.count = min(last_tok + 1 - t.k0, BKV);
+      t.pmask = 0xffu;
+      t.full = t.k0 + BKV <= tok0 + 1;
+      t.clear = t.count < BKV;
+    }
+    return t;
+  }
+  MARS_DEV bool key_read(const Tile& t, int key) const {
+    return key < t.count && ((t.pmask >> (key / kPageSize)) & 1u);
+  }
+  MARS_DEV flash::ColRange cols(const flash::RowVis& v, const Tile& t) const {
+    return {t.prefix ? t.count : min(v.end1 - t.k0, t.count), BKV, -1, t.pmask};
+  }
+  MARS_DEV void store_chunk(int row, int col, const uint32_t (&r)[32], float inv, float m,
+                            float l) const {
+    const size_t tok = (size_t)base + token(row);
+    const int h = h0 + row % a->gp;
+    if (a->nsplit == 1) {
+      if (col == 0 && a->lse) a->lse[(size_t)h * a->total + tok] = l > 0.f ? m + log2f(l) : -INFINITY;
+      uint4* dst = reinterpret_cast<uint4*>(a->o + (tok * a->hq + h) * D + col);
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = flash::pack_bf16x2(__uint_as_float(r[e + 2 * i]) * inv,
+                                    __uint_as_float(r[e + 2 * i + 1]) * inv);
+        dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      return;
+    }
+    float* rec = a->part + (((size_t)split * a->total + tok) * a->hq + h) * (D + 4);
+    if (col == 0) {
+      rec[0] = m;
+      rec[1] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      *reinterpret_cast<float4*>(rec + 4 + col + e) =
+          make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
+                      __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(flash::NUM_THREADS, 1)
+packed_rows_kernel(const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_kp,
+                   const __grid_constant__ CUtensorMap tm_vp, AttnArgs a) {
+  using namespace sm100;
+  using S = flash::Smem<D, 0, kVStages>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ flash::Barriers bar;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int id = blockIdx.x;
+  const int sp = id % a.nsplit;
+  id /= a.nsplit;
+  const int grp = id % a.ngrp;
+  id /= a.ngrp;
+  const int kvh = id % a.hkv;
+  id /= a.hkv;
+  bool bad;
+  const packed::Seq sq = packed::find_tile(a.cu, a.batch, a.total, a.tpt, 0, id, bad);
+  if (bad && threadIdx.x == 0 && a.status) atomicOr(a.status, MARS_ST_BADSEQ);
+  if (sq.s < 0) return;
+
+  RowsPolicy<D> pol;
+  pol.a = &a;
+  pol.base = sq.base;
+  pol.n = sq.n;
+  pol.tok0 = sq.tile * a.tpt;
+  // cached keys; a length that the table cannot hold is cut to what it can
+  const int cached = a.seq_lens ? a.seq_lens[sq.s] : 0;
+  pol.P = (int)max(0LL, min((long long)cached, (long long)a.max_pages * kPageSize));
+  if (pol.P != cached && threadIdx.x == 0 && a.status) atomicOr(a.status, MARS_ST_OVERFLOW);
+  pol.np = (pol.P + BKV - 1) / BKV;
+  pol.bt_row = a.block_table ? a.block_table + (size_t)sq.s * a.max_pages : nullptr;
+  pol.h0 = (kvh * a.ngrp + grp) * a.gp;
+  pol.last_tok = min(pol.tok0 + a.tpt, sq.n) - 1;
+  const int all = pol.np + pol.last_tok / BKV + 1;
+  pol.split = sp;
+  pol.j0 = sp * a.split_tiles;
+  const int end = sp == a.nsplit - 1 ? all : min(all, pol.j0 + a.split_tiles);
+  const int n_total = end - pol.j0;
+  if (n_total <= 0) {                  // no keys in this split: empty partials
+    for (int r = threadIdx.x; r < BQ; r += blockDim.x)
+      if (pol.row_valid(r)) {
+        float* rec = a.part + (((size_t)sp * a.total + sq.base + pol.token(r)) * a.hq + pol.h0 +
+                               r % a.gp) * (D + 4);
+        rec[0] = -INFINITY;
+        rec[1] = 0.f;
+      }
+    return;
+  }
+
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  if (threadIdx.x == 0) flash::init_barriers(bar);
+  if (warp == 1) {
+    tmem_alloc(&bar.tmem_base, S::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem_base, 0);
+
+  if (warp == 0 || warp == flash::V_LOADER_WARP) {
+    const bool is_v = warp == flash::V_LOADER_WARP;
+    if (!is_v && lane == 0) {
+      mbar_arrive_expect_tx(&bar.q_full, a.gp * a.tpt * 128 * (D / 64));
+      for (int x = 0; x < D / 64; ++x)
+        tma_load_3d(smem + S::OFF_Q + x * (BQ * 128), &tm_q, &bar.q_full, x * 64, pol.h0,
+                    sq.base + pol.tok0);
+    }
+    int st_flags = 0;
+    const CUtensorMap* tm_pool = is_v ? &tm_vp : &tm_kp;
+    const CUtensorMap* tm_new = is_v ? &tm_v : &tm_k;
+    // block-table entry of this lane's page in key tile jl (-1 past the table), read one tile
+    // ahead of its use
+    auto entry = [&](int jl) -> int {
+      const int j = pol.j0 + jl;
+      if (jl >= n_total || j >= pol.np || lane >= kPagesPerTile) return 0;
+      const int lp = j * kPagesPerTile + lane;
+      return lp < a.max_pages ? pol.bt_row[lp] : -1;
+    };
+    int next_entry = entry(0);
+    auto issue = [&](int jl, uint8_t* dst, uint64_t* b) {
+      const int e = next_entry;
+      next_entry = entry(jl + 1);
+      const int j = pol.j0 + jl;
+      if (j < pol.np) {
+        if (lane < kPagesPerTile) {
+          // a page that may not be read loads page 0 (masked, V rows cleared), or with an empty
+          // pool the zeros past the end of its one-page map
+          int page = 0;
+          if (e >= 0 && e < a.num_pages)
+            page = e;
+          else if (j * BKV + lane * kPageSize < pol.P)
+            st_flags |= MARS_ST_NOPAGE;
+          const int row = a.num_pages > 0 ? (page * a.hkv + kvh) * kPageSize : kPageSize;
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_2d(dst + x * (BKV * 128) + lane * (kPageSize * 128), tm_pool, b, x * 64, row);
+        }
+      } else if (lane == 0) {
+        for (int x = 0; x < D / 64; ++x)
+          tma_load_3d(dst + x * (BKV * 128), tm_new, b, x * 64, kvh, sq.base + (j - pol.np) * BKV);
+      }
+    };
+    flash::load_ring<D, kVStages>(bar, smem, n_total, a.status, is_v, issue);
+    if (!is_v && lane == 0) mbar_wait(&bar.q_full, 0, nullptr, a.status);
+    if (st_flags && a.status) atomicOr(a.status, st_flags);
+  } else if (warp == 1 || warp == flash::PV_ISSUER_WARP) {
+    if (warp == 1 && lane == 0)
+      flash::single_issuer<D, kVStages>(bar, smem, n_total, tmem, a.status);
+  } else {
+    flash::softmax_loop<D>(bar, smem, pol, n_total, tmem, a.scale_log2, a.status);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::TMEM_COLS);
+  }
+}
+
+// One warp per (row, query head): merge the partials of the splits.
+template <int D>
+__global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
+  const long long gw = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const long long tok = gw / a.hq;
+  const int h = (int)(gw - tok * a.hq);
+  bool bad;
+  // rows behind the last sequence have no partials and stay as they are
+  const packed::Seq sq = packed::find_tile(a.cu, a.batch, a.total, 1, 0, INT_MAX, bad);
+  const int first = min(max(a.cu[0], 0), a.total);
+  if (tok < first || tok >= sq.base) return;
+  const size_t rec = D + 4, step = (size_t)a.total * a.hq * rec;
+  const float* base = a.part + ((size_t)tok * a.hq + h) * rec;
+  float m = -INFINITY;
+  for (int sp = 0; sp < a.nsplit; ++sp) m = fmaxf(m, base[sp * step]);
+  float l = 0.f;
+  float2 acc[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) acc[i] = make_float2(0.f, 0.f);
+  for (int sp = 0; sp < a.nsplit; ++sp) {
+    const float* pr = base + sp * step;
+    const float ms = pr[0];
+    if (ms == -INFINITY) continue;
+    const float w = exp2f(ms - m);
+    l += pr[1] * w;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const float2 v = *reinterpret_cast<const float2*>(pr + 4 + 2 * lane + 64 * i);
+      acc[i].x += v.x * w;
+      acc[i].y += v.y * w;
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (a.lse && lane == 0)
+    a.lse[(size_t)h * a.total + tok] = l > 0.f ? m + log2f(l) : -INFINITY;
+  uint32_t* orow = reinterpret_cast<uint32_t*>(a.o + ((size_t)tok * a.hq + h) * D);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+    orow[lane + 32 * i] = flash::pack_bf16x2(acc[i].x * inv, acc[i].y * inv);
+}
+
+// Tensor map of [total][heads][D] rows with a row pitch of `stride` elements.
+bool map_rows(CUtensorMap* m, const void* base, int d, int heads, int total, long long stride,
+              uint32_t box_heads, uint32_t box_rows) {
+  const uint64_t dims[3] = {(uint64_t)d, (uint64_t)heads, (uint64_t)total};
+  const uint64_t str[2] = {(uint64_t)d * 2, (uint64_t)stride * 2};
+  const uint32_t box[3] = {64, box_heads, box_rows};
+  return encode_tmap_bf16(m, base, 3, dims, str, box);
+}
+
+template <int D>
+cudaError_t launch_rows(const PackedAttn& p, const PackedPlan& plan, AttnArgs& a,
+                        cudaStream_t stream) {
+  using S = flash::Smem<D, 0, kVStages>;
+  static_assert(S::TOTAL + sizeof(flash::Barriers) <= 227 * 1024, "layout fits shared memory");
+  CUtensorMap tq, tk, tv, tkp, tvp;
+  if (!map_rows(&tq, p.q, D, p.hq, p.total, p.q_stride, a.gp, a.tpt) ||
+      !map_rows(&tk, p.k, D, p.hkv, p.total, p.k_stride, 1, BKV) ||
+      !map_rows(&tv, p.v, D, p.hkv, p.total, p.v_stride, 1, BKV))
+    return cudaErrorInvalidValue;
+  tkp = tk;
+  tvp = tv;
+  if (p.seq_lens) {
+    // an empty pool is never read: one page over q, and the loader's boxes start past its end
+    const bool any = p.num_pages > 0;
+    const uint64_t dims[2] = {(uint64_t)D, any ? (uint64_t)p.num_pages * p.hkv * kPageSize
+                                               : (uint64_t)kPageSize};
+    const uint64_t str[1] = {(uint64_t)D * 2};
+    const uint32_t box[2] = {64, (uint32_t)kPageSize};
+    if (!encode_tmap_bf16(&tkp, any ? p.k_pool : p.q, 2, dims, str, box) ||
+        !encode_tmap_bf16(&tvp, any ? p.v_pool : p.q, 2, dims, str, box))
+      return cudaErrorInvalidValue;
+  }
+  static std::atomic<int> attr[64];
+  const cudaError_t ea = set_smem_limit_once(packed_rows_kernel<D>, S::TOTAL, attr);
+  if (ea != cudaSuccess) return ea;
+  packed_rows_kernel<D><<<(unsigned)plan.ctas, flash::NUM_THREADS, S::TOTAL, stream>>>(
+      tq, tk, tv, tkp, tvp, a);
+  count_launches(1);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || plan.nsplit == 1) return e;
+  const long long warps = (long long)p.total * p.hq;
+  packed_merge_kernel<D><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len) {
+  PackedPlan p{};
+  const int G = hq / hkv;
+  p.gp = G <= BQ ? G : 1;
+  p.tpt = BQ / p.gp;
+  const long long items = packed::max_tiles(batch, total, p.tpt) * hkv * (G / p.gp);
+  const int tiles = (max_len + BKV - 1) / BKV + 1;
+  long long nsplit = 1;
+  if (items < num_sms()) {
+    nsplit = num_sms() / items;
+    nsplit = nsplit < tiles / kMinSplitTiles ? nsplit : tiles / kMinSplitTiles;
+    if (nsplit < 1) nsplit = 1;
+  }
+  p.split_tiles = (int)((tiles + nsplit - 1) / nsplit);
+  p.nsplit = (tiles + p.split_tiles - 1) / p.split_tiles;
+  p.ctas = items * p.nsplit;
+  p.ws_bytes =
+      p.nsplit > 1 ? (size_t)p.nsplit * total * hq * (size_t)(d + 4) * sizeof(float) : 0;
+  return p;
+}
+
+cudaError_t launch_packed_attn(const PackedAttn& p, const PackedPlan& plan, void* workspace,
+                               cudaStream_t stream) {
+  AttnArgs a{};
+  a.cu = p.cu;
+  a.seq_lens = p.seq_lens;
+  a.block_table = p.block_table;
+  a.num_pages = p.num_pages;
+  a.max_pages = p.max_pages;
+  a.batch = p.batch;
+  a.total = p.total;
+  a.hq = p.hq;
+  a.hkv = p.hkv;
+  a.gp = plan.gp;
+  a.tpt = plan.tpt;
+  a.ngrp = p.hq / p.hkv / plan.gp;
+  a.nsplit = plan.nsplit;
+  a.split_tiles = plan.split_tiles;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.o = p.o;
+  a.lse = p.lse;
+  a.part = static_cast<float*>(workspace);
+  a.status = p.status;
+  return p.d == 64 ? launch_rows<64>(p, plan, a, stream) : launch_rows<128>(p, plan, a, stream);
+}
+
+}  // namespace mars

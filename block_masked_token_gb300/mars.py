@@ -16,7 +16,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmars.so
 _lib = None
 
 OK, EINVAL, EALIGN, EUNSUPPORTED, ECUDA, ENOSPACE = 0, -1, -2, -3, -4, -5
-ST_NOPAGE, ST_OVERFLOW, ST_TIMEOUT, ST_BADTARGET = 1, 2, 4, 8
+ST_NOPAGE, ST_OVERFLOW, ST_TIMEOUT, ST_BADTARGET, ST_BADSEQ = 1, 2, 4, 8, 16
 OP_DECODE_ATTN, OP_HEAD_ACCEPT, OP_CE_LOSS, OP_CE_LOSS_GRAD, OP_DUAL_GRAD = 1, 2, 3, 4, 5
 PAGE_SIZE = 16
 BLOCK_SYNC_WORDS = 4
@@ -70,6 +70,14 @@ def lib() -> ctypes.CDLL:
                                                      P, P, S, P, P]
         L.mars_dual_stream_ce_loss_grad.restype = I
         L.mars_dual_stream_ce_loss_grad.argtypes = [P, P, P, P, I, I, I, I, P, P, P, S, P, P]
+        L.mars_packed_workspace_bytes.restype = S
+        L.mars_packed_workspace_bytes.argtypes = [I] * 7
+        L.mars_attn_packed.restype = I
+        L.mars_attn_packed.argtypes = [P] * 6 + [I] * 8 + [F, P, S, P, P]
+        L.mars_attn_chunk.restype = I
+        L.mars_attn_chunk.argtypes = [P] * 6 + [I, P, I, P, I, P] + [I] * 9 + [F, P, S, P, P]
+        L.mars_kv_append.restype = I
+        L.mars_kv_append.argtypes = [P] * 6 + [I, P, P, I, P] + [I] * 7 + [P, P]
         L.mars_check_wait_timeout.restype = I
         L.mars_check_wait_timeout.argtypes = [P, P]
         L.mars_strerror.restype = ctypes.c_char_p
@@ -88,6 +96,8 @@ EXPORTED = ("mars_workspace_bytes", "mars_attn_dual_stream", "mars_decode_attn",
             "mars_dual_stream_ce_loss",
             "mars_dual_stream_ce_loss_grad", "mars_attn_dual_stream_grad",
             "mars_attn_dual_stream_lse", "mars_attn_dual_stream_grad_lse",
+            "mars_packed_workspace_bytes", "mars_attn_packed", "mars_attn_chunk",
+            "mars_kv_append",
             "mars_check_wait_timeout", "mars_strerror",
             "mars_version", "mars_launch_count")
 

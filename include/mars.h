@@ -50,12 +50,17 @@ typedef uint16_t mars_bf16;
 #define MARS_ST_TIMEOUT 4       /* an in-kernel pipeline wait passed its time limit (2 s);
                                    the kernel stopped early and its outputs are invalid */
 #define MARS_ST_BADTARGET 8     /* a loss target outside [-1, vocab): that row is left out */
+#define MARS_ST_BADSEQ 16       /* sequence boundaries that decrease or leave [0, total]: they
+                                   were cut to the nearest valid ones */
 
 #define MARS_OP_DECODE_ATTN 1
 #define MARS_OP_HEAD_ACCEPT 2
 #define MARS_OP_CE_LOSS 3
 #define MARS_OP_CE_LOSS_GRAD 4
 #define MARS_OP_DUAL_GRAD 5
+#define MARS_OP_ATTN_PACKED 6        /* for mars_packed_workspace_bytes */
+#define MARS_OP_ATTN_CHUNK 7
+#define MARS_OP_ATTN_PACKED_GRAD 8
 
 /* Workspace (device scratch, caller-allocated, >= 256-byte aligned) needed by `op`.
  * MARS_OP_DECODE_ATTN uses batch, B, hq, hkv, d, max_len (the max_len_hint of the call);
@@ -343,6 +348,85 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
                                   int L, int hidden, int vocab, float* dh, float* dw,
                                   void* workspace, size_t ws_bytes, int32_t* status,
                                   void* stream);
+
+/* ---- Packed sequences: prompts, and chunks of new tokens over the paged cache.
+ *
+ * The paper decodes and trains from a prompt that is already in the cache, and continues
+ * training from an autoregressively trained checkpoint ([gist] 2.A and 2.D); these entry
+ * points are the prompt's side of both: they attend over whole prompts, put their K/V into
+ * the cache, extend them chunk by chunk, and give the gradient of an autoregressive
+ * training step. Conventions:
+ *   - The rows of `batch` sequences stand one after another in tensors of `total` rows:
+ *     cu_seqlens [batch + 1] int32 (device), sequence s owns rows cu_seqlens[s] ..
+ *     cu_seqlens[s + 1] - 1 (none is allowed). Rows outside every sequence are neither read
+ *     as keys nor written. Boundaries that decrease or leave [0, total] are cut to valid
+ *     ones and flagged MARS_ST_BADSEQ.
+ *   - q [total, hq, d], k and v [total, hkv, d] bf16 may be slices of a wider tensor (a fused
+ *     projection's output): q_stride, k_stride, v_stride are their row pitches in elements,
+ *     multiples of 8 and at least heads * d; the heads of a row are contiguous.
+ *   - Outputs o, dq, dk, dv are bf16 (what the next product reads); statistics are float.
+ *     Scores, softmax statistics and sums are held in 32 bits; the weights are rounded to
+ *     bf16 for the product with V.
+ *   - hq / hkv, d, scale and status as elsewhere; status may be NULL.
+ *   - A key that a sequence may not read (another sequence's row, a row behind the last
+ *     sequence, a free slot of a page, an unmapped page) has no effect whatever it holds,
+ *     NaN included. A NaN or infinity in a sequence's own v can reach the rows of that
+ *     sequence up to 127 places before it. */
+
+/* Workspace (device scratch, >= 256-byte aligned) of `op` (MARS_OP_ATTN_PACKED,
+ * MARS_OP_ATTN_CHUNK, MARS_OP_ATTN_PACKED_GRAD) for `total` rows of `batch` sequences;
+ * max_len: the max_len_hint of a mars_attn_chunk call, ignored by the others. 0 for an
+ * unknown op, invalid sizes, or an op that needs none. Calls whose kernels may overlap on the
+ * GPU, graph replays among them, each need a workspace of their own. */
+size_t mars_packed_workspace_bytes(int op, int batch, int total, int hq, int hkv, int d,
+                                   int max_len);
+
+/* Causal attention of whole prompts: row i of a sequence attends to its rows 0 .. i.
+ *   o   [total, hq, d] bf16 (written)
+ *   lse [hq, total] float or NULL (written): log2 of the sum over the visible keys of
+ *       exp2(scale * log2(e) * q.k), the statistic mars_attn_packed_grad needs
+ *   workspace >= mars_packed_workspace_bytes(MARS_OP_ATTN_PACKED, ...) bytes (NULL if 0) */
+int mars_attn_packed(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
+                     const int32_t* cu_seqlens, mars_bf16* o, float* lse, int batch, int total,
+                     int hq, int hkv, int d, int q_stride, int k_stride, int v_stride,
+                     float scale, void* workspace, size_t ws_bytes, int32_t* status,
+                     void* stream);
+
+/* Attention of a chunk of new tokens per sequence (one token, a prompt's next part, a whole
+ * prompt) over the paged cache: row i of sequence s attends to the P_s = seq_lens[s] tokens
+ * of its cache and to the chunk's rows 0 .. i, given in k and v. Chunks of any lengths may
+ * stand in one call. It reads the cache only: mars_kv_append puts the chunk into it, before
+ * or after (with seq_lens unchanged).
+ *   k_pool, v_pool, block_table, seq_lens, page_size   as mars_decode_attn
+ *   max_len_hint  host upper bound of P_s + the chunk's rows; it sizes the splits of long key
+ *                 lists. Longer ones are still computed correctly, only slower.
+ *   o   [total, hq, d] bf16 (written)
+ *   workspace >= mars_packed_workspace_bytes(MARS_OP_ATTN_CHUNK, ...) bytes (NULL if 0)
+ * A needed page that is unmapped is skipped and flags MARS_ST_NOPAGE; a length below 0 or
+ * beyond the table is cut and flags MARS_ST_OVERFLOW. */
+int mars_attn_chunk(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
+                    const int32_t* cu_seqlens, const mars_bf16* k_pool, const mars_bf16* v_pool,
+                    int num_pages, const int32_t* block_table, int max_pages_per_seq,
+                    const int32_t* seq_lens, int max_len_hint, mars_bf16* o, int batch,
+                    int total, int hq, int hkv, int d, int page_size, int q_stride,
+                    int k_stride, int v_stride, float scale, void* workspace, size_t ws_bytes,
+                    int32_t* status, void* stream);
+
+/* K/V of packed sequences into the paged cache: row i of sequence s goes to position
+ * pos = seq_lens[s] + i, page = block_table[s][pos / page_size], slot = pos % page_size, as in
+ * mars_kv_commit. seq_lens is read only (a model calls this once per layer):
+ *   new_lens [batch] int32 or NULL (written): seq_lens[s] + the rows appended; it may not be
+ *            seq_lens itself
+ *   slots    [total] int32 or NULL (written for the rows of the sequences): page * page_size +
+ *            slot, -1 for a row that was not appended
+ * The first row whose page is unmapped (entry < 0 or >= num_pages, or past max_pages_per_seq)
+ * ends the append of its sequence and flags MARS_ST_NOPAGE / MARS_ST_OVERFLOW; so does a
+ * negative seq_lens[s]. Two rows that map to the same slot leave either's values there. */
+int mars_kv_append(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seqlens,
+                   const int32_t* seq_lens, int32_t* new_lens, const int32_t* block_table,
+                   int max_pages_per_seq, mars_bf16* k_pool, mars_bf16* v_pool, int num_pages,
+                   int32_t* slots, int batch, int total, int hkv, int d, int page_size,
+                   int k_stride, int v_stride, int32_t* status, void* stream);
 
 /* Self-check of the in-kernel wait limit every pipeline relies on: enqueues one small
  * kernel that waits on an mbarrier nothing completes. The wait gives up after its time

@@ -6,10 +6,13 @@ import this package. The CUDA library never uses it.
 from .mars_oracle import (  # noqa: F401
     accept_count,
     ar_signal_fraction,
+    attn_chunk,
     attn_dual_stream,
     attn_dual_stream_grad,
     attn_dual_stream_grad_parts,
     attn_dual_stream_lse,
+    attn_packed,
+    attn_packed_grad,
     beta,
     ce_loss_dual,
     ce_loss_dual_grad,
@@ -19,6 +22,7 @@ from .mars_oracle import (  # noqa: F401
     head_accept,
     head_accept_per_request,
     head_logits,
+    kv_append,
     kv_commit,
     kv_commit_batch_sync,
     kv_commit_block,

@@ -524,3 +524,94 @@ def ce_loss_dual_grad(h, w_vocab_major, targets, batch: int, L: int):
     g[rows, y[rows]] -= 1.0
     g *= scale[:, None]
     return g @ w_vocab_major, g.T @ h, g
+
+
+# ---------------------------------------------------------------------------------------
+# Packed sequences: causal attention of prompts, of chunks over the paged cache, its
+# gradient, and the append of K/V. Sequence s owns rows cu[s] .. cu[s+1] - 1; rows outside
+# every sequence give NaN (no output).
+# ---------------------------------------------------------------------------------------
+
+def _packed_rows(cu):
+    return [(s, int(cu[s]), int(cu[s + 1])) for s in range(len(cu) - 1)]
+
+
+def attn_packed(q, k, v, cu, scale: float | None = None):
+    """Causal attention inside each sequence. q [n, Hq, D], k and v [n, Hkv, D]. Returns O
+    [n, Hq, D] and lse [Hq, n] = log2 sum_u exp(scale q.k_u) over the keys a row sees."""
+    n, Hq, D = q.shape
+    g = Hq // k.shape[1]
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    out, lse = np.full(q.shape, np.nan), np.full((Hq, n), np.nan)
+    for _, a, b in _packed_rows(cu):
+        i = np.arange(b - a)
+        vis = i[None, :] <= i[:, None]
+        for h in range(Hq if b > a else 0):
+            S = np.where(vis, scale * (q[a:b, h] @ k[a:b, h // g].T), -np.inf)
+            m = S.max(axis=1)
+            e = np.exp(S - m[:, None])
+            out[a:b, h] = (e / e.sum(axis=1, keepdims=True)) @ v[a:b, h // g]
+            lse[h, a:b] = (m + np.log(e.sum(axis=1))) / math.log(2.0)
+    return out, lse
+
+
+def attn_packed_grad(q, k, v, do, cu, scale: float | None = None):
+    """Gradient of sum(dO * O) for O = attn_packed: dq [n, Hq, D], dk and dv [n, Hkv, D]."""
+    n, Hq, D = q.shape
+    g = Hq // k.shape[1]
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    dq, dk, dv = np.full(q.shape, np.nan), np.full(k.shape, np.nan), np.full(v.shape, np.nan)
+    for _, a, b in _packed_rows(cu):
+        dk[a:b] = dv[a:b] = 0.0
+        i = np.arange(b - a)
+        vis = i[None, :] <= i[:, None]
+        for h in range(Hq if b > a else 0):
+            K, V, dO = k[a:b, h // g], v[a:b, h // g], do[a:b, h]
+            P = _masked_softmax_rows(scale * (q[a:b, h] @ K.T), vis)
+            dP = dO @ V.T
+            dS = P * (dP - (P * dP).sum(axis=1, keepdims=True))
+            dq[a:b, h] = scale * dS @ K
+            dk[a:b, h // g] += scale * dS.T @ q[a:b, h]
+            dv[a:b, h // g] += P.T @ dO
+    return dq, dk, dv
+
+
+def attn_chunk(q, k, v, cu, k_pool, v_pool, block_table, seq_lens, page_size: int,
+               scale: float | None = None):
+    """Row i of sequence s attends to its seq_lens[s] cached keys (those on mapped pages) and
+    to its own rows 0..i. Returns O [n, Hq, D]."""
+    n, Hq, D = q.shape
+    g = Hq // k.shape[1]
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    out = np.full(q.shape, np.nan)
+    for s, a, b in _packed_rows(cu):
+        pos = [(int(block_table[s][p // page_size]), p % page_size)
+               for p in range(int(seq_lens[s]))]
+        pos = [(e, c) for e, c in pos if 0 <= e < k_pool.shape[0]]
+        K = np.concatenate([np.array([k_pool[e, :, c] for e, c in pos]).reshape(-1, *k.shape[1:]),
+                            k[a:b]])
+        V = np.concatenate([np.array([v_pool[e, :, c] for e, c in pos]).reshape(-1, *v.shape[1:]),
+                            v[a:b]])
+        j, i = np.arange(len(K))[None, :], np.arange(b - a)[:, None]
+        vis = j < len(pos) + i + 1
+        for h in range(Hq if b > a else 0):
+            out[a:b, h] = _masked_softmax_rows(scale * (q[a:b, h] @ K[:, h // g].T), vis) @ V[:, h // g]
+    return out
+
+
+def kv_append(k, v, cu, seq_lens, block_table, k_pool, v_pool, page_size: int):
+    """Row i of sequence s goes to position seq_lens[s] + i of its pages; the first position
+    without a mapped page ends the append of its sequence. Returns new pools, the new lengths
+    and the slot of every row (-1 where none)."""
+    kp, vp = k_pool.copy(), v_pool.copy()
+    lens, slots = np.array(seq_lens, dtype=np.int64), np.full(k.shape[0], -1, dtype=np.int64)
+    for s, a, b in _packed_rows(cu):
+        for i in range(b - a):
+            p = int(seq_lens[s]) + i
+            page = int(block_table[s][p // page_size]) if 0 <= p // page_size < len(block_table[s]) else -1
+            if not 0 <= page < kp.shape[0]:
+                break
+            kp[page, :, p % page_size], vp[page, :, p % page_size] = k[a + i], v[a + i]
+            slots[a + i] = page * page_size + p % page_size
+            lens[s] += 1
+    return kp, vp, lens, slots

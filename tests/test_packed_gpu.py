@@ -1,0 +1,328 @@
+"""Packed prompts, chunks over the paged cache and the K/V append against the fp64 oracle
+(needs a GB300). Bounds are elementwise, from the error model of parity_util and packed_util."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from block_masked_token_gb300 import mars, packed
+from packed_util import (LSE_TOL, PAGE, causal_weights, cuda, f64, make, output_bound,
+                         run_chunk, run_packed, workspace)
+from parity_util import assert_within_bound
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(4, 2, 64), (7, 1, 128), (2, 2, 128), (14, 2, 64)]
+LENS = [[1], [0, 1, 0, 2], [127, 128, 129], [19, 0, 300, 5], [513], [17, 18, 19, 36, 37]]
+
+
+def check_packed(x, o, lse, fill=7.0, scale=None):
+    ref, ref_lse = oracle.attn_packed(f64(x["q"]), f64(x["k"]), f64(x["v"]), x["cu"].numpy(), scale)
+    o, lse, cu = f64(o), f64(lse), x["cu"].tolist()
+    g = x["q"].shape[1] // x["k"].shape[1]
+    for a, b in zip(cu, cu[1:]):
+        for h in range(x["q"].shape[1] if b > a else 0):
+            P = causal_weights(f64(x["q"][a:b, h]), f64(x["k"][a:b, h // g]), scale)
+            assert_within_bound(o[a:b, h], ref[a:b, h],
+                                output_bound(P, f64(x["v"][a:b, h // g]), ref[a:b, h]), f"o rows {a}:{b} head {h}")
+    live = ~np.isnan(ref_lse)
+    assert np.abs(lse[live] - ref_lse[live]).max(initial=0.0) <= LSE_TOL
+    # rows outside every sequence are left as they were
+    outside = np.ones(x["n"], dtype=bool)
+    outside[cu[0]:cu[-1]] = False
+    assert (o[outside] == fill).all() and (lse[:, outside] == fill).all()
+
+
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("lens", LENS, ids=str)
+def test_packed_matches_oracle(lens, heads):
+    x = make(lens, *heads, seed=len(lens), tail=3, fused=heads[0] != 4)
+    o, lse, st = run_packed(cuda(x))
+    assert st == 0
+    check_packed(x, o, lse)
+
+
+@pytest.mark.parametrize("heads", [(130, 1, 64), (96, 1, 64), (128, 1, 64), (5, 5, 64)], ids=str)
+def test_packed_group_sizes(heads):
+    x = make([40, 3], *heads, seed=5)
+    o, lse, st = run_packed(cuda(x))
+    assert st == 0
+    check_packed(x, o, lse)
+
+
+def test_packed_many_sequences_and_leading_rows():
+    x = make([(i * 7) % 23 for i in range(75)], 4, 2, 64, seed=6, lead=5, tail=4)
+    o, lse, st = run_packed(cuda(x))
+    assert st == 0
+    check_packed(x, o, lse)
+
+
+def test_packed_scale_and_large_scores():
+    """Scores of some tens: the running maximum has to be raised along a row."""
+    x = make([200, 90], 4, 2, 64, seed=7)
+    x["qkv"].mul_(2.0)
+    o, lse, st = run_packed(cuda(x), scale=0.25)
+    assert st == 0
+    ref, _ = oracle.attn_packed(f64(x["q"]), f64(x["k"]), f64(x["v"]), x["cu"].numpy(), 0.25)
+    # scores are 8 times those of the model's inputs, and so is its upstream error of a weight,
+    # 2^-14: the weights' sum of absolute errors is then at most 8 * 2^-14 * 2 max|v|
+    slack = 16 * 2.0 ** -14 * np.abs(f64(x["v"])).max()
+    o, cu = f64(o), x["cu"].tolist()
+    for a, b in zip(cu, cu[1:]):
+        for h in range(4):
+            P = causal_weights(f64(x["q"][a:b, h]), f64(x["k"][a:b, h // 2]), 0.25)
+            assert_within_bound(o[a:b, h], ref[a:b, h],
+                                output_bound(P, f64(x["v"][a:b, h // 2]), ref[a:b, h]) + slack, "o")
+
+
+def same(a, b):
+    return torch.equal(a.cpu(), b.cpu())
+
+
+def test_packed_other_rows_have_no_effect():
+    """NaN and infinities in another sequence and behind the last one stay there."""
+    x = make([70, 30, 150], 14, 2, 64, seed=8, tail=60)
+    o, lse, _ = run_packed(cuda(x))
+    x["qkv"][70:100] = float("nan")
+    x["qkv"][250:] = float("inf")
+    o2, lse2, st = run_packed(cuda(x))
+    assert st == 0
+    for rows in (slice(0, 70), slice(100, 250)):
+        assert same(o[rows], o2[rows]) and same(lse[:, rows], lse2[:, rows])
+
+
+def test_packed_later_keys_with_nan_scores_are_masked():
+    x = make([100], 2, 1, 64, seed=9)
+    o, lse, _ = run_packed(cuda(x))
+    x["k"][60:] = float("nan")
+    o2, lse2, _ = run_packed(cuda(x))
+    assert same(o[:60], o2[:60]) and same(lse[:, :60], lse2[:, :60])
+
+
+@pytest.mark.parametrize("cu, want", [([0, 40, 30, 90], [0, 40, 40, 90]),
+                                      ([-5, 20, 200, 90], [0, 20, 90, 90]),
+                                      ([0, 10, 50, 2000000000], [0, 10, 50, 90])])
+def test_packed_bad_boundaries_are_cut(cu, want):
+    x = make([20, 20, 50], 4, 2, 64, seed=10)
+    x["cu"] = torch.tensor(cu, dtype=torch.int32)
+    o, lse, st = run_packed(cuda(x))
+    assert st == mars.ST_BADSEQ
+    x["cu"] = torch.tensor(want, dtype=torch.int32)
+    o2, lse2, st = run_packed(cuda(x))
+    assert st == 0 and same(o, o2) and same(lse, lse2)
+
+
+# ------------------------------------------------------------------------------- chunks
+
+def check_chunk(x, o, mapped=None):
+    table = x["table"].numpy()
+    ref = oracle.attn_chunk(f64(x["q"]), f64(x["k"]), f64(x["v"]), x["cu"].numpy(),
+                            f64(x["k_pool"]), f64(x["v_pool"]), table, x["old"].numpy(), PAGE)
+    o, cu = f64(o), x["cu"].tolist()
+    hq, hkv = x["q"].shape[1], x["k"].shape[1]
+    kp, vp = f64(x["k_pool"]), f64(x["v_pool"])
+    for s, (a, b) in enumerate(zip(cu, cu[1:])):
+        pos = [(table[s, p // PAGE], p % PAGE) for p in range(int(x["old"][s]))]
+        pos = [(e, c) for e, c in pos if 0 <= e < len(kp)]
+        for h in range(hq if b > a else 0):
+            u = h // (hq // hkv)
+            K = np.concatenate([np.array([kp[e, u, c] for e, c in pos]).reshape(-1, kp.shape[-1]), f64(x["k"][a:b, u])])
+            V = np.concatenate([np.array([vp[e, u, c] for e, c in pos]).reshape(-1, kp.shape[-1]), f64(x["v"][a:b, u])])
+            P = causal_weights(f64(x["q"][a:b, h]), K)
+            assert_within_bound(o[a:b, h], ref[a:b, h], output_bound(P, V, ref[a:b, h]), f"seq {s} head {h}")
+    assert (o[cu[-1]:] == 7.0).all()
+
+
+CHUNKS = [([1], [50]), ([1], [0]), ([1, 1, 1], [128, 1, 2300]), ([5, 0, 140, 1], [0, 77, 129, 513]),
+          ([130], [1000]), ([19, 1], [127, 15]), ([1], [5000])]
+
+
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("lens, old", CHUNKS, ids=str)
+def test_chunk_matches_oracle(lens, old, heads):
+    x = make(lens, *heads, seed=sum(old), old=old, tail=2, fused=heads[0] != 4)
+    # free slots of the pages hold NaN, as memory that nothing wrote may
+    for s, p in enumerate(old):
+        for c in range(p, -(-(p + lens[s]) // PAGE) * PAGE):
+            x["k_pool"][x["table"][s, c // PAGE], :, c % PAGE] = float("nan")
+            x["v_pool"][x["table"][s, c // PAGE], :, c % PAGE] = float("nan")
+    x["k_pool"][x["unused"].long()] = float("nan")
+    x["v_pool"][x["unused"].long()] = float("nan")
+    o, st = run_chunk(cuda(x))
+    assert st == 0
+    check_chunk(x, o)
+
+
+@pytest.mark.parametrize("hint", [0, 100, 100000])
+def test_chunk_hint_only_sizes_the_splits(hint):
+    x = make([3, 1], 14, 2, 64, seed=3, old=[2000, 1300])
+    o, st = run_chunk(cuda(x), hint=hint)
+    assert st == 0
+    check_chunk(x, o)
+
+
+def test_chunk_unmapped_pages_are_skipped():
+    x = make([4, 2], 4, 2, 64, seed=4, old=[200, 300])
+    x["table"][0, 3] = -1
+    x["table"][1, 0] = 1 << 20
+    x["v_pool"][0] = float("nan") if 0 in x["unused"].tolist() else x["v_pool"][0]
+    o, st = run_chunk(cuda(x))
+    assert st == mars.ST_NOPAGE
+    check_chunk(x, o)
+
+
+def test_chunk_without_a_mapped_page_and_cut_lengths():
+    x = make([2, 3], 4, 2, 64, seed=5, old=[40, 30])
+    x["table"][:] = -1
+    o, st = run_chunk(cuda(x))
+    assert st == mars.ST_NOPAGE
+    check_chunk(x, o)
+    x = make([2, 3], 4, 2, 64, seed=5, old=[40, 30])
+    y = cuda(x)
+    y["old"] = torch.tensor([-3, 2000000000], dtype=torch.int32, device="cuda")
+    y["table"][1] = y["table"][1].clamp(min=0)
+    o, st = run_chunk(y, hint=100)
+    x["old"] = torch.tensor([0, x["table"].shape[1] * PAGE], dtype=torch.int32)
+    x["table"][1] = x["table"][1].clamp(min=0)
+    assert st == mars.ST_OVERFLOW
+    check_chunk(x, o)
+
+
+def test_chunk_empty_pool():
+    x = make([20, 1], 4, 2, 64, seed=6, old=[0, 0])
+    y = cuda(x)
+    y["k_pool"], y["v_pool"] = y["k_pool"][:0], y["v_pool"][:0]
+    o, st = run_chunk(y)
+    assert st == 0
+    check_chunk(x, o)
+
+
+# ------------------------------------------------------------------------------- append
+
+def run_append(y, **kw):
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lens = torch.full_like(y["old"], -9)
+    slots = torch.full((y["n"],), -9, dtype=torch.int32, device="cuda")
+    packed.mars_kv_append(y["k"], y["v"], y["cu"], y["old"], y["table"], y["k_pool"], y["v_pool"],
+                        new_lens=lens, slots=slots, status=st, **kw)
+    torch.cuda.synchronize()
+    return lens, slots, int(st.item())
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (7, 1, 128), (10, 5, 64)], ids=str)
+@pytest.mark.parametrize("lens, old", [([1], [50]), ([40, 0, 17, 1], [0, 31, 15, 16]), ([300, 16], [7, 0])], ids=str)
+@pytest.mark.parametrize("hole", [None, 0, 1])
+def test_append_matches_oracle(lens, old, heads, hole):
+    x = make(lens, *heads, seed=1, old=old, tail=3)
+    if hole is not None and hole < x["table"].shape[1]:
+        x["table"][0, hole] = -1
+    y = cuda(x)
+    got_lens, slots, st = run_append(y)
+    kp, vp, want_lens, want_slots = oracle.kv_append(
+        f64(x["k"]), f64(x["v"]), x["cu"].numpy(), x["old"].numpy(), x["table"].numpy(),
+        f64(x["k_pool"]), f64(x["v_pool"]), PAGE)
+    assert (f64(y["k_pool"]) == kp).all() and (f64(y["v_pool"]) == vp).all()
+    assert (got_lens.cpu().numpy() == want_lens).all()
+    n = int(x["cu"][-1])
+    assert (slots[:n].cpu().numpy() == want_slots[:n]).all() and (slots[n:] == -9).all()
+    assert st == (0 if want_lens.sum() == sum(old) + sum(lens) else mars.ST_NOPAGE)
+
+
+def test_append_past_the_table_and_negative_length():
+    x = make([40, 20], 4, 2, 64, seed=2, old=[10, 5])
+    x["table"] = x["table"][:, :2].contiguous()
+    y = cuda(x)
+    y["old"][1] = -1
+    before = y["k_pool"].clone()
+    lens, slots, st = run_append(y)
+    assert st == mars.ST_OVERFLOW and lens.tolist() == [32, -1]
+    assert (slots[22:40] == -1).all() and (slots[40:60] == -1).all()
+    mine = x["table"][0].long()
+    others = [i for i in range(before.shape[0]) if i not in mine.tolist()]
+    assert torch.equal(before[others], y["k_pool"][others])
+
+
+# -------------------------------------------------------------------- used together
+
+def prefill(x, parts, hq, hkv, d):
+    """A batch of prompts put into the cache in parts: attention of each part over what is
+    cached, then the append, lengths kept on the device."""
+    lens, n = x["lens"], x["n"]
+    y = cuda(x)
+    cur, new = torch.zeros(len(lens), dtype=torch.int32, device="cuda"), None
+    out = torch.zeros(n, hq, d, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    starts = x["cu"].tolist()
+    for part in range(parts):
+        cuts = [(m * part // parts, m * (part + 1) // parts) for m in lens]
+        rows = torch.cat([torch.arange(starts[s] + a, starts[s] + b) for s, (a, b) in enumerate(cuts)]).cuda()
+        cu = torch.tensor(np.cumsum([0] + [b - a for a, b in cuts]), dtype=torch.int32, device="cuda")
+        q, k, v = (y[c][rows].contiguous() for c in "qkv")
+        o = torch.empty(len(rows), hq, d, dtype=torch.bfloat16, device="cuda")
+        ws = workspace(packed.OP_ATTN_CHUNK, len(lens), len(rows), hq, hkv, d, max(lens))
+        packed.mars_attn_chunk(q, k, v, cu, y["k_pool"], y["v_pool"], y["table"], cur, max(lens), o,
+                             ws, status=st)
+        new = torch.empty_like(cur)
+        packed.mars_kv_append(k, v, cu, cur, y["table"], y["k_pool"], y["v_pool"], new_lens=new, status=st)
+        cur, out[rows] = new, o
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and cur.tolist() == lens
+    return y, out, cur
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (14, 2, 64), (7, 1, 128)], ids=str)
+def test_prefill_in_parts_then_decode(heads):
+    """A prompt's chunks, the append, then the framework's decode attention over the cache."""
+    hq, hkv, d = heads
+    lens, B = [150, 33, 260], 4
+    x = make(lens, hq, hkv, d, seed=11, old=[0, 0, 0], spare_pages=6)
+    y, out, cur = prefill(x, 3, hq, hkv, d)
+    o, lse, _ = run_packed(y, fill=0.0)
+    check_packed(x, out, lse, fill=0.0)        # the parts give the whole prompt's rows
+    g = torch.Generator().manual_seed(1)
+    q, kb, vb = (torch.randn(3, B, h, d, generator=g).to(torch.bfloat16) for h in (hq, hkv, hkv))
+    od = torch.empty(3, B, hq, d, dtype=torch.float32, device="cuda")
+    ws = torch.empty(mars.mars_workspace_bytes(mars.OP_DECODE_ATTN, 3, B, hq, hkv, d, max_len=260) + 16,
+                     dtype=torch.uint8, device="cuda")
+    # the decode kernel multiplies the free slots of the last page by weights of 0
+    mars.mars_decode_attn(q.cuda(), kb.cuda(), vb.cuda(), y["k_pool"], y["v_pool"], y["table"], cur,
+                          260, od, ws)
+    torch.cuda.synchronize()
+    cu, f = x["cu"].tolist(), f64
+    for s in range(3):
+        for h in range(hq):
+            u = h // (hq // hkv)
+            K = np.concatenate([f(x["k"][cu[s]:cu[s + 1], u]), f(kb[s, :, u])])
+            V = np.concatenate([f(x["v"][cu[s]:cu[s + 1], u]), f(vb[s, :, u])])
+            assert np.abs(causal_weights(f(q[s, :, h]), K) @ V - f(od[s, :, h])).max() <= 1e-2
+
+
+def test_calls_in_a_graph_and_on_another_stream():
+    x = make([40, 200], 14, 2, 64, seed=12, old=[2100, 300])
+    y = cuda(x)
+    want, _ = run_chunk(y, hint=2400)
+    want_p, want_lse, _ = run_packed(y)
+    n, hq, d = y["q"].shape
+    o, op = torch.zeros_like(want), torch.zeros_like(want_p)
+    lse = torch.zeros_like(want_lse)
+    ws = workspace(packed.OP_ATTN_CHUNK, 2, n, hq, 2, d, 2400)
+    wp = workspace(packed.OP_ATTN_PACKED, 2, n, hq, 2, d)
+
+    def step(stream=None):
+        packed.mars_attn_chunk(y["q"], y["k"], y["v"], y["cu"], y["k_pool"], y["v_pool"], y["table"],
+                             y["old"], 2400, o, ws, stream=stream)
+        packed.mars_attn_packed(y["q"], y["k"], y["v"], y["cu"], op, wp, lse=lse, stream=stream)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)
+    side.synchronize()
+    assert same(o, want) and same(op, want_p) and same(lse, want_lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        o.zero_(), op.zero_(), lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(o, want) and same(op, want_p) and same(lse, want_lse)
