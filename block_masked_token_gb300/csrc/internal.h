@@ -140,6 +140,20 @@ PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len
 cudaError_t launch_packed_attn(const PackedAttn& p, const PackedPlan& plan, void* workspace,
                                cudaStream_t stream);
 
+// ---- Gradient of the packed attention without a cache.
+struct PackedGrad {
+  const uint16_t *q, *k, *v, *o, *d_o;
+  long long q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride;
+  const float* lse;
+  const int32_t* cu;
+  uint16_t *dq, *dk, *dv;
+  int batch, total, hq, hkv, d;
+  float scale;
+  int32_t* status;
+};
+size_t packed_grad_workspace_bytes(int batch, int total, int hq, int hkv, int d);
+cudaError_t launch_packed_grad(const PackedGrad& p, void* workspace, cudaStream_t stream);
+
 // ---- K/V rows of packed sequences into the paged cache.
 cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, long long k_stride,
                              long long v_stride, const int32_t* cu, const int32_t* seq_lens,

@@ -416,6 +416,8 @@ size_t mars_packed_workspace_bytes(int op, int batch, int total, int hq, int hkv
     return mars::plan_packed(batch, total, hq, hkv, d, total).ws_bytes;
   if (op == MARS_OP_ATTN_CHUNK)
     return max_len < 0 ? 0 : mars::plan_packed(batch, total, hq, hkv, d, max_len).ws_bytes;
+  if (op == MARS_OP_ATTN_PACKED_GRAD)
+    return mars::packed_grad_workspace_bytes(batch, total, hq, hkv, d);
   return 0;
 }
 
@@ -485,6 +487,37 @@ int mars_attn_chunk(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
   p.scale = scale;
   p.status = status;
   return packed_attn_checked(p, max_len_hint, workspace, ws_bytes, stream);
+}
+
+int mars_attn_packed_grad(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
+                          const mars_bf16* o, const mars_bf16* d_o, const float* lse,
+                          const int32_t* cu_seqlens, mars_bf16* dq, mars_bf16* dk,
+                          mars_bf16* dv, int batch, int total, int hq, int hkv, int d,
+                          int q_stride, int k_stride, int v_stride, int dq_stride,
+                          int dk_stride, int dv_stride, float scale, void* workspace,
+                          size_t ws_bytes, int32_t* status, void* stream) {
+  int rc = check_packed(batch, total, hq, hkv, d);
+  if (rc) return rc;
+  if (batch == 0 || total == 0) return MARS_OK;
+  if (!q || !k || !v || !o || !d_o || !lse || !cu_seqlens || !dq || !dk || !dv || !workspace)
+    return MARS_EINVAL;
+  const int pitch[6] = {q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride};
+  for (int i = 0; i < 6; ++i)
+    if ((rc = check_pitch(pitch[i], i % 3 == 0 ? hq : hkv, d))) return rc;
+  const void* ptr[9] = {q, k, v, o, d_o, dq, dk, dv, workspace};
+  for (const void* x : ptr)
+    if (!aligned16(x)) return MARS_EALIGN;
+  if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)d);
+  if (isinf(scale)) return MARS_EINVAL;
+  // (tile, head) items are counted in 32 bits
+  if (((long long)total / 128 + batch) * hq > 0x7fffffffLL) return MARS_EUNSUPPORTED;
+  if (ws_bytes < mars::packed_grad_workspace_bytes(batch, total, hq, hkv, d))
+    return MARS_ENOSPACE;
+  const mars::PackedGrad p{q,         k,         v,         o,         d_o,   q_stride,
+                           k_stride,  v_stride,  dq_stride, dk_stride, dv_stride, lse,
+                           cu_seqlens, dq,       dk,        dv,        batch, total,
+                           hq,        hkv,       d,         scale,     status};
+  return cuda_rc(mars::launch_packed_grad(p, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 int mars_kv_append(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seqlens,

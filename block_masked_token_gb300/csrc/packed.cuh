@@ -67,5 +67,49 @@ MARS_DEV Seq find_tile(const int32_t* __restrict__ cu, int batch, int total, int
   return Seq{-1, 0, top, 0};
 }
 
+// A tile of a sequence in a plan's lists.
+struct alignas(16) Tile {
+  int base, n;    // first row and number of rows of its sequence
+  int tile;       // tile index inside the sequence
+  int id;         // sequence (by_cost of a forward plan) or global tile index (a gradient's)
+};
+
+// Lists of the tiles of a packed batch, made on the device (the boundaries are there), for
+// kernels that run many tiles per CTA: CTAs take a list's entries in turn, so each is sorted
+// by falling cost, the number of 128-key (or 128-row) tiles that an entry visits.
+struct Plan {
+  int32_t* count;     // number of tiles
+  Tile* first;        // by the keys a tile's rows see (forward, dQ)
+  Tile* second;       // gradient: by the rows that see a tile's keys (dK, dV)
+  Tile* in_order;     // gradient: by global tile index
+};
+
+inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Carve a plan out of a workspace at `off` (base may be null to size it).
+inline Plan carve_plan(void* base, size_t& off, int batch, int total, int rows, bool grad) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  auto take = [&](size_t bytes) {
+    uint8_t* at = p ? p + off : nullptr;
+    off += align256(bytes);
+    return at;
+  };
+  const size_t list = (size_t)max_tiles(batch, total, rows) * sizeof(Tile);
+  Plan r{};
+  r.count = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
+  r.first = reinterpret_cast<Tile*>(take(list));
+  if (grad) {
+    r.second = reinterpret_cast<Tile*>(take(list));
+    r.in_order = reinterpret_cast<Tile*>(take(list));
+  }
+  return r;
+}
+
+// Fill a plan. rows: rows per tile (128 for a gradient); seq_lens: cached keys per sequence
+// (NULL: none), cut to what max_pages pages hold.
+cudaError_t launch_plan(const Plan& plan, const int32_t* cu, const int32_t* seq_lens,
+                        int max_pages, int batch, int total, int rows, int32_t* status,
+                        cudaStream_t stream);
+
 }  // namespace packed
 }  // namespace mars

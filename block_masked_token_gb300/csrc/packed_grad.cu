@@ -1,0 +1,953 @@
+// Gradient of the causal attention of packed sequences (packed_attn.cu).
+//
+// With S = Q K^T, P = exp2(scale log2(e) S - lse) on the visible pairs (u <= t, same
+// sequence), dP = dO V^T and D_t = sum_c dO_tc O_tc:
+//   dV = P^T dO,   dS = P (dP - D),   dQ = scale dS K,   dK = scale dS^T Q.
+// Row 0 of a sequence sees one key, whose weight is 1 whatever the score: its dS is 0, and is
+// set so instead of being left to the cancellation of dP and D.
+//
+// Two tcgen05 kernels over 128-row tiles, neither storing a score block, each a persistent CTA
+// per SM that takes (tile, head) items in the order of falling cost (packed_plan.cu):
+//   - dkdv_kernel: an item is a key tile, a KV head and some of its query heads. Per pair with
+//     a query tile at or after it: S^T = K Q^T and dP^T = V dO^T (keys on TMEM lanes), then
+//     dV += P^T dO and dK += dS^T Q with P^T and dS^T as bf16 operands in TMEM, all in two
+//     halves of 64 queries with their own barriers. dV and dK stay in TMEM over the item.
+//     When the key tiles alone would leave SMs idle, the query heads of a group are divided
+//     among items, which write fp32 partials that merge_kernel adds in a fixed order: no
+//     atomics, the same result from run to run.
+//   - dq_kernel: an item is a query tile and a query head; S, dP and dQ += dS K per key tile.
+// P and dS are rounded to bf16 as MMA operands; dS is formed from the unrounded P. prep_kernel
+// computes D and lays lse and D out in 128-row blocks per (head, tile), for bulk copies.
+//
+// A pair's tile can reach past its sequence: scores there are masked, and the rows of dO, Q
+// (dkdv_kernel) or K (dq_kernel) that the masked weights of 0 would multiply are cleared in
+// shared memory, so that other sequences' rows have no effect whatever they hold.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "flash_tc.cuh"
+#include "internal.h"
+#include "packed.cuh"
+
+namespace mars {
+
+namespace {
+
+using namespace sm100;
+using packed::Tile;
+
+constexpr int GT = 128;                 // rows per key tile and per query tile
+constexpr int MATH_WARPS = 8;           // two per TMEM lane quadrant, 64 columns each
+constexpr int MATH_THREADS = 32 * MATH_WARPS;
+constexpr int NSTAGE = 2;               // Q / dO ring depth of dkdv_kernel
+
+struct GradArgs {
+  packed::Plan plan;
+  int batch, total, hq, hkv, G, nsplit;
+  long long pad;                        // padded rows per head: 128 * the bound of the tiles
+  float scale, scale_log2;
+  const uint16_t *o, *d_o;              // [total][hq][D]
+  const float* lse;                     // [hq][total]
+  float *lse_p, *d_p;                   // [hq][pad]
+  uint16_t *dq, *dk, *dv;
+  long long dq_stride, dk_stride, dv_stride;
+  float* part;                          // [nsplit][2][total][hkv][D] with several splits
+  int32_t* status;
+};
+
+// ------------------------------------------------------------------------------ prep
+
+// D and lse of a tile's rows, in 128-row blocks per head; rows past the sequence get zeros.
+// D / 8 lanes per (row, head).
+template <int D>
+__global__ void __launch_bounds__(256) prep_kernel(GradArgs a) {
+  constexpr int LANES = D / 8, PER = 256 / LANES;
+  if ((int)blockIdx.x >= *a.plan.count) return;
+  const Tile t = a.plan.in_order[blockIdx.x];
+  const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+  // heads vary fastest, as in memory
+  const int total = GT * a.hq;
+#pragma unroll 4
+  for (int i = sub + blockIdx.y * PER; i < total; i += PER * gridDim.y) {
+    const int r = i / a.hq, h = i - r * a.hq;
+    const int row = t.tile * GT + r;
+    float acc = 0.f;
+    if (row < t.n) {
+      const size_t at = ((size_t)(t.base + row) * a.hq + h) * D + lane * 8;
+      float x[8], y[8];
+      unpack8(*reinterpret_cast<const uint4*>(a.o + at), x);
+      unpack8(*reinterpret_cast<const uint4*>(a.d_o + at), y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc += x[e] * y[e];
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (lane == 0) {
+      const size_t p = (size_t)h * a.pad + (size_t)t.id * GT + r;
+      a.d_p[p] = acc;
+      a.lse_p[p] = row < t.n ? a.lse[(size_t)h * a.total + t.base + row] : 0.f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------- shared
+
+MARS_DEV uint32_t bits(int lo, int hi) { return flash::bit_range(lo, hi); }
+
+// Rows [first, 128) of a [128][D] operand tile (D / 64 swizzled regions) set to zero, by
+// `threads` threads of which this is number `id`; rows [lo, hi) of the tile are theirs.
+template <int D>
+MARS_DEV void clear_rows(uint8_t* tile, int first, int lo, int hi, int id, int threads) {
+  constexpr int VECS = D / 8;                       // 16-byte vectors per row
+  for (int i = max(first, lo) * VECS + id; i < hi * VECS; i += threads) {
+    const int r = i / VECS, c = i % VECS;
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * (GT * 128) + r * 128 + (c & 7) * 16) =
+        make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Item r of this CTA: rounds run forwards and backwards over the CTAs, so that the costs even out.
+struct Turns {
+  int total, rounds;
+  MARS_DEV explicit Turns(int n) : total(n), rounds((n + (int)gridDim.x - 1) / (int)gridDim.x) {}
+  MARS_DEV int at(int r) const {
+    const int g = gridDim.x, c = blockIdx.x;
+    const int id = r * g + ((r & 1) ? g - 1 - c : c);
+    return id < total ? id : -1;
+  }
+};
+
+// ---------------------------------------------------------------------- dK and dV
+
+template <int D>
+struct KSmem {
+  static constexpr int T_BYTES = GT * D * 2;
+  static constexpr int OFF_K = 0, OFF_V = T_BYTES, OFF_RING = 2 * T_BYTES;
+  // a stage: Q and dO [128][D], lse and D of its 128 rows
+  static constexpr int ST_Q = 0, ST_DO = T_BYTES, ST_LSE = 2 * T_BYTES, ST_D = ST_LSE + GT * 4;
+  static constexpr int STAGE = (ST_D + GT * 4 + 1023) / 1024 * 1024;
+  static constexpr int TOTAL = OFF_RING + NSTAGE * STAGE + 1024;
+  static constexpr int TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D, TM_COLS = 512;
+};
+
+struct KBar {
+  uint64_t kv_full, kv_empty;
+  uint64_t full[NSTAGE], empty[NSTAGE];
+  uint64_t s_full[2], dp_full[2], p_full[2], ds_full[2], dv_done[2], dk_done[2];
+  uint64_t acc_full, acc_free, drain, drain_ts;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// Key tile `t` of (kvh, split): query heads kvh*G + g, g in [g0, g0 + ng), query tiles
+// t.tile .. nt - 1 of its sequence.
+struct KItem {
+  Tile t;
+  int kvh, sp, g0, ng, nq, pairs;
+};
+
+MARS_DEV KItem k_item(const GradArgs& a, int id) {
+  KItem it;
+  it.sp = id % a.nsplit;
+  id /= a.nsplit;
+  it.kvh = id % a.hkv;
+  it.t = a.plan.second[id / a.hkv];
+  it.g0 = a.G * it.sp / a.nsplit;
+  it.ng = a.G * (it.sp + 1) / a.nsplit - it.g0;
+  it.nq = (it.t.n + GT - 1) / GT - it.t.tile;
+  it.pairs = it.ng * it.nq;
+  return it;
+}
+
+constexpr int K_THREADS = 96 + MATH_THREADS;     // loader, S/dP issuer, math, dV/dK issuer
+constexpr int K_TS_WARP = 2 + MATH_WARPS;
+
+// TMEM column of K-step k (16 queries) of P^T or dS^T: queries [0, 64) over columns [0, 32),
+// [64, 128) over [64, 96), the first half of each half's own fp32 columns.
+MARS_DEV uint32_t p_col(int k) { return (uint32_t)(8 * k + (k >= 4 ? 32 : 0)); }
+
+template <int D>
+__global__ void __launch_bounds__(K_THREADS, 1)
+dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+            const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+            GradArgs a) {
+  using S = KSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ KBar bar;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* ab = &bar.abort;
+  const Turns turns(*a.plan.count * a.hkv * a.nsplit);
+  if (turns.at(0) < 0) return;                         // more CTAs than items
+
+  if (threadIdx.x == 0) {
+    bar.abort = 0;
+    mbar_init(&bar.kv_full, 1);
+    mbar_init(&bar.kv_empty, 1);
+    for (int i = 0; i < NSTAGE; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&bar.s_full[h], 1);
+      mbar_init(&bar.dp_full[h], 1);
+      mbar_init(&bar.p_full[h], MATH_THREADS / 2);
+      mbar_init(&bar.ds_full[h], MATH_THREADS / 2);
+      mbar_init(&bar.dv_done[h], 1);
+      mbar_init(&bar.dk_done[h], 1);
+    }
+    mbar_init(&bar.acc_full, 1);
+    mbar_init(&bar.acc_free, MATH_THREADS);
+    mbar_init(&bar.drain, 1);
+    mbar_init(&bar.drain_ts, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar.tmem_base, S::TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem_base, 0);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      int gp = 0, ii = 0, nkv = 0;
+      bool ok = true;
+      for (int r = 0; r < turns.rounds && ok; ++r) {
+        const int id = turns.at(r);
+        if (id < 0) continue;
+        const KItem it = k_item(a, id);
+        if (ii > 0 && !(ok = mbar_wait(&bar.kv_empty, (ii - 1) & 1, ab, a.status))) break;
+        mbar_arrive_expect_tx(&bar.kv_full, 2 * S::T_BYTES);
+        const int z = it.t.base + GT * it.t.tile;
+        for (int x = 0; x < D / 64; ++x) {
+          tma_load_3d(smem + S::OFF_K + x * (GT * 128), &tm_k, &bar.kv_full, x * 64, it.kvh, z);
+          tma_load_3d(smem + S::OFF_V + x * (GT * 128), &tm_v, &bar.kv_full, x * 64, it.kvh, z);
+        }
+        ++nkv;
+        for (int p = 0; p < it.pairs; ++p, ++gp) {
+          const int st = gp % NSTAGE;
+          uint8_t* stage = smem + S::OFF_RING + st * S::STAGE;
+          if (!(ok = mbar_wait(&bar.empty[st], ((gp / NSTAGE) & 1) ^ 1, ab, a.status))) break;
+          const int h = it.kvh * a.G + it.g0 + p / it.nq, qi = p % it.nq;
+          const size_t rb = (size_t)h * a.pad + (size_t)(it.t.id + qi) * GT;
+          mbar_arrive_expect_tx(&bar.full[st], 2 * S::T_BYTES + 2 * GT * 4);
+          bulk_load(stage + S::ST_LSE, a.lse_p + rb, GT * 4, &bar.full[st]);
+          bulk_load(stage + S::ST_D, a.d_p + rb, GT * 4, &bar.full[st]);
+          for (int x = 0; x < D / 64; ++x) {
+            tma_load_3d(stage + S::ST_Q + x * (GT * 128), &tm_q, &bar.full[st], x * 64, h, z + GT * qi);
+            tma_load_3d(stage + S::ST_DO + x * (GT * 128), &tm_do, &bar.full[st], x * 64, h, z + GT * qi);
+          }
+        }
+        ++ii;
+      }
+      // wait (bounded) for the copies still in flight
+      if (nkv > 0) mbar_wait(&bar.kv_full, (nkv - 1) & 1, nullptr, a.status);
+      for (int k = 1; k <= NSTAGE && gp - k >= 0; ++k)
+        mbar_wait(&bar.full[(gp - k) % NSTAGE], ((gp - k) / NSTAGE) & 1, nullptr, a.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------- S^T and dP^T MMAs
+    if (lane == 0) {
+      const uint32_t id_qk = idesc_bf16_f32(GT, GT / 2, false);
+      const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_K), 16, 1024);
+      const uint64_t vd = sdesc_sw128(smem_u32(smem + S::OFF_V), 16, 1024);
+      // half h of S^T = K Q^T (or dP^T = V dO^T) of pair gp, once `done` says that the MMAs
+      // that read the buffer's previous P^T (dS^T) have completed
+      auto issue = [&](int gp, uint64_t ad, int st_off, int col, uint64_t* done, uint64_t* full) {
+        const uint64_t bd =
+            sdesc_sw128(smem_u32(smem + S::OFF_RING + (gp % NSTAGE) * S::STAGE + st_off), 16, 1024);
+        for (int h = 0; h < 2; ++h) {
+          if (gp > 0 && !mbar_wait(&done[h], (gp - 1) & 1, ab, a.status)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * (GT * 128) + (k & 3) * 32;
+            mma_bf16_ss(tmem + col + (GT / 2) * h, sdesc_advance(ad, off),
+                        sdesc_advance(bd, off + h * (GT / 2) * 128), id_qk, k != 0);
+          }
+          mma_commit(&full[h]);
+        }
+        return true;
+      };
+      int gp = 0, ii = 0;
+      bool ok = true;
+      for (int r = 0; r < turns.rounds && ok; ++r) {
+        const int id = turns.at(r);
+        if (id < 0) continue;
+        const int np = k_item(a, id).pairs;
+        if (!(ok = mbar_wait(&bar.kv_full, ii & 1, ab, a.status))) break;
+        for (int p = 0; p < np && ok; ++p, ++gp)
+          ok = mbar_wait(&bar.full[gp % NSTAGE], (gp / NSTAGE) & 1, ab, a.status) &&
+               issue(gp, kd, S::ST_Q, S::TM_S, bar.dv_done, bar.s_full) &&
+               issue(gp, vd, S::ST_DO, S::TM_DP, bar.dk_done, bar.dp_full);
+        if (!ok) break;
+        mma_commit(&bar.kv_empty);                     // only these MMAs read K and V
+        ++ii;
+      }
+      mma_commit(&bar.drain);
+      mbar_wait(&bar.drain, 0, nullptr, a.status);
+    }
+  } else if (warp == K_TS_WARP) {
+    // -------------------------------------------------------- dV and dK MMAs
+    if (lane == 0) {
+      const uint32_t id_acc = idesc_bf16_f32(GT, D, true);     // A from TMEM, B MN-major
+      int gp = 0, ii = 0;
+      bool ok = true;
+      for (int r = 0; r < turns.rounds && ok; ++r) {
+        const int id = turns.at(r);
+        if (id < 0) continue;
+        const int np = k_item(a, id).pairs;
+        for (int p = 0; p < np; ++p, ++gp) {
+          const int st = gp % NSTAGE;
+          const uint32_t sb = smem_u32(smem + S::OFF_RING + st * S::STAGE);
+          if (!(ok = mbar_wait(&bar.full[st], (gp / NSTAGE) & 1, ab, a.status))) break;
+          // the accumulators start from zero: the previous item's must have been read
+          if (p == 0 && ii > 0 && !(ok = mbar_wait(&bar.acc_free, (ii - 1) & 1, ab, a.status)))
+            break;
+          auto accumulate = [&](uint64_t* ready, uint64_t* done, int st_off, int src, int dst) {
+            const uint64_t bd = sdesc_sw128(sb + st_off, GT * 128, 1024);
+            for (int h = 0; h < 2; ++h) {
+              if (!mbar_wait(&ready[h], gp & 1, ab, a.status)) return false;
+              tc_fence_after();
+#pragma unroll
+              for (int kq = 0; kq < GT / 32; ++kq) {
+                const int k = (GT / 32) * h + kq;
+                mma_bf16_ts(tmem + dst, tmem + src + p_col(k), sdesc_advance(bd, k * 2048), id_acc,
+                            (p | k) != 0);
+              }
+              mma_commit(&done[h]);
+            }
+            return true;
+          };
+          if (!(ok = accumulate(bar.p_full, bar.dv_done, S::ST_DO, S::TM_S, S::TM_DV) &&
+                     accumulate(bar.ds_full, bar.dk_done, S::ST_Q, S::TM_DP, S::TM_DK)))
+            break;
+          // S^T and dP^T completed before the math warps formed dS^T, and those have read
+          // the stage's lse and D: the stage is free after dK
+          mma_commit(&bar.empty[st]);
+        }
+        if (!ok) break;
+        mma_commit(&bar.acc_full);
+        ++ii;
+      }
+      mma_commit(&bar.drain_ts);
+      mbar_wait(&bar.drain_ts, 0, nullptr, a.status);
+    }
+  } else {
+    // ------------------------------------------------- math (warps 2..9, two per quadrant)
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int row = quad * 32 + lane;                  // TMEM lane = key row of the tile
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    constexpr int HC = GT / 2, HD = D / 2;
+    auto warp_wait = [&](uint64_t* b, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(b, parity, ab, a.status));
+    };
+    int gp = 0, ii = 0;
+    bool ok = true;
+    for (int r = 0; r < turns.rounds && ok; ++r) {
+      const int id = turns.at(r);
+      if (id < 0) continue;
+      const KItem it = k_item(a, id);
+      const int kk = GT * it.t.tile + row;             // key position in its sequence
+      for (int p = 0; p < it.pairs; ++p, ++gp) {
+        const int st = gp % NSTAGE;
+        uint8_t* stage = smem + S::OFF_RING + st * S::STAGE;
+        const float* ls = reinterpret_cast<const float*>(stage + S::ST_LSE) + HC * half;
+        const float* dsv = reinterpret_cast<const float*>(stage + S::ST_D) + HC * half;
+        const int q0 = GT * (it.t.tile + p % it.nq);   // first query position
+        // query columns [lo, hi) of this half that see the key; none for a key past the end
+        const int live = it.t.n - q0;                  // query rows of the tile
+        const int lo = kk - q0 - HC * half;
+        const int hi = kk < it.t.n ? live - HC * half : -1;
+        const bool ragged = live < GT;                 // uniform over the CTA
+        if (!(ok = warp_wait(&bar.s_full[half], gp & 1))) break;
+        tc_fence_after();
+        uint32_t v[HC];
+#pragma unroll
+        for (int q = 0; q < HC / 32; ++q)
+          tmem_ld32(tmem + S::TM_S + HC * half + q * 32 + lane_off,
+                    *reinterpret_cast<uint32_t(*)[32]>(v + q * 32));
+        tmem_ld_wait();
+        if (ragged) {
+          // the half's rows of Q and dO past the sequence, once the MMAs that read them as S^T
+          // and dP^T operands have completed
+          if (!(ok = warp_wait(&bar.dp_full[half], gp & 1))) break;
+          const int tid = quad * 32 + lane;
+          clear_rows<D>(stage + S::ST_Q, live, HC * half, HC * half + HC, tid, 128);
+          clear_rows<D>(stage + S::ST_DO, live, HC * half, HC * half + HC, tid, 128);
+          fence_proxy_async_smem();
+        }
+        const bool whole = lo <= 0 && hi >= HC;
+        uint32_t mk[2] = {0xffffffffu, 0xffffffffu};
+        if (!whole) {
+#pragma unroll
+          for (int q = 0; q < HC / 32; ++q) {
+            mk[q] = bits(lo - 32 * q, hi - 32 * q);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((mk[q] >> e) & 1u)) v[32 * q + e] = 0xff800000u;
+          }
+        }
+        float pf[HC];
+        uint32_t pp[HC / 2];
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+#pragma unroll
+        for (int e = 0; e < HC; e += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(ls + e);
+          const float2 t01 = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                                        sc2, make_float2(-l4.x, -l4.y));
+          const float2 t23 = __ffma2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
+                                        sc2, make_float2(-l4.z, -l4.w));
+          pf[e] = flash::ex2_approx(t01.x);
+          pf[e + 1] = flash::ex2_approx(t01.y);
+          pf[e + 2] = flash::ex2_approx(t23.x);
+          pf[e + 3] = flash::ex2_approx(t23.y);
+          pp[e / 2] = flash::pack_bf16x2(pf[e], pf[e + 1]);
+          pp[e / 2 + 1] = flash::pack_bf16x2(pf[e + 2], pf[e + 3]);
+        }
+        tmem_st32(tmem + S::TM_S + HC * half + lane_off, *reinterpret_cast<uint32_t(*)[32]>(pp));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&bar.p_full[half]);
+        if (!(ok = warp_wait(&bar.dp_full[half], gp & 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < HC / 32; ++q)
+          tmem_ld32(tmem + S::TM_DP + HC * half + q * 32 + lane_off,
+                    *reinterpret_cast<uint32_t(*)[32]>(v + q * 32));
+        tmem_ld_wait();
+        if (!whole) {                                  // masked dP may hold anything
+#pragma unroll
+          for (int q = 0; q < HC / 32; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((mk[q] >> e) & 1u)) v[32 * q + e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < HC; e += 4) {
+          const float4 d4 = *reinterpret_cast<const float4*>(dsv + e);
+          const float2 s01 = __fmul2_rn(make_float2(pf[e], pf[e + 1]),
+                                        __fadd2_rn(make_float2(__uint_as_float(v[e]),
+                                                               __uint_as_float(v[e + 1])),
+                                                   make_float2(-d4.x, -d4.y)));
+          const float2 s23 = __fmul2_rn(make_float2(pf[e + 2], pf[e + 3]),
+                                        __fadd2_rn(make_float2(__uint_as_float(v[e + 2]),
+                                                               __uint_as_float(v[e + 3])),
+                                                   make_float2(-d4.z, -d4.w)));
+          pp[e / 2] = flash::pack_bf16x2(s01.x, s01.y);
+          pp[e / 2 + 1] = flash::pack_bf16x2(s23.x, s23.y);
+        }
+        if (q0 == 0 && half == 0) pp[0] &= 0xffff0000u;   // dS of row 0 is 0
+        tmem_st32(tmem + S::TM_DP + HC * half + lane_off, *reinterpret_cast<uint32_t(*)[32]>(pp));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&bar.ds_full[half]);
+      }
+      if (!ok) break;
+      // the item's dV and dK rows, this thread's half of the columns
+      if (!(ok = warp_wait(&bar.acc_full, ii & 1))) break;
+      tc_fence_after();
+      uint32_t dvr[HD], dkr[HD];
+#pragma unroll
+      for (int q = 0; q < HD / 32; ++q) {
+        tmem_ld32(tmem + S::TM_DV + HD * half + q * 32 + lane_off,
+                  *reinterpret_cast<uint32_t(*)[32]>(dvr + q * 32));
+        tmem_ld32(tmem + S::TM_DK + HD * half + q * 32 + lane_off,
+                  *reinterpret_cast<uint32_t(*)[32]>(dkr + q * 32));
+      }
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive_warp(&bar.acc_free);
+      if (kk < it.t.n) {
+        const size_t tok = (size_t)it.t.base + kk;
+        if (a.nsplit == 1) {
+          uint4* ov = reinterpret_cast<uint4*>(a.dv + tok * a.dv_stride + it.kvh * D + HD * half);
+          uint4* ok4 = reinterpret_cast<uint4*>(a.dk + tok * a.dk_stride + it.kvh * D + HD * half);
+#pragma unroll
+          for (int e = 0; e < HD; e += 8) {
+            uint32_t wv[4], wk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              wv[i] = flash::pack_bf16x2(__uint_as_float(dvr[e + 2 * i]),
+                                         __uint_as_float(dvr[e + 2 * i + 1]));
+              wk[i] = flash::pack_bf16x2(__uint_as_float(dkr[e + 2 * i]) * a.scale,
+                                         __uint_as_float(dkr[e + 2 * i + 1]) * a.scale);
+            }
+            ov[e / 8] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+            ok4[e / 8] = make_uint4(wk[0], wk[1], wk[2], wk[3]);
+          }
+        } else {
+          const size_t plane = (size_t)a.total * a.hkv * D;
+          float* ov = a.part + 2 * it.sp * plane + (tok * a.hkv + it.kvh) * D + HD * half;
+          float* ok4 = ov + plane;
+#pragma unroll
+          for (int e = 0; e < HD; e += 4) {
+            *reinterpret_cast<float4*>(ov + e) =
+                make_float4(__uint_as_float(dvr[e]), __uint_as_float(dvr[e + 1]),
+                            __uint_as_float(dvr[e + 2]), __uint_as_float(dvr[e + 3]));
+            *reinterpret_cast<float4*>(ok4 + e) = make_float4(
+                __uint_as_float(dkr[e]) * a.scale, __uint_as_float(dkr[e + 1]) * a.scale,
+                __uint_as_float(dkr[e + 2]) * a.scale, __uint_as_float(dkr[e + 3]) * a.scale);
+          }
+        }
+      }
+      ++ii;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::TM_COLS);
+  }
+}
+
+// dV and dK of a tile's rows: the sum of the splits' partials, in order, rounded to bf16.
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(GradArgs a) {
+  if ((int)blockIdx.x >= *a.plan.count) return;
+  const Tile t = a.plan.in_order[blockIdx.x];
+  const int rows = min(GT, t.n - t.tile * GT);
+  const size_t plane = (size_t)a.total * a.hkv * D;
+  const int per = a.hkv * D / 4;
+  for (int i = threadIdx.x + blockIdx.y * 256; i < 2 * rows * per; i += 256 * gridDim.y) {
+    const int which = i >= rows * per, j = which ? i - rows * per : i;
+    const int r = j / per, c = (j - r * per) * 4;
+    const size_t tok = (size_t)t.base + t.tile * GT + r;
+    const float* src = a.part + which * plane + tok * a.hkv * D + c;
+    float4 s = *reinterpret_cast<const float4*>(src);
+    for (int sp = 1; sp < a.nsplit; ++sp) {
+      const float4 u = *reinterpret_cast<const float4*>(src + 2 * sp * plane);
+      s.x += u.x;
+      s.y += u.y;
+      s.z += u.z;
+      s.w += u.w;
+    }
+    uint16_t* dst = which ? a.dk + tok * a.dk_stride + c : a.dv + tok * a.dv_stride + c;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(flash::pack_bf16x2(s.x, s.y), flash::pack_bf16x2(s.z, s.w));
+  }
+}
+
+// -------------------------------------------------------------------------------- dQ
+
+// K ring and V ring of flash_tc.cuh, Q and dO tiles; TMEM: S at 0, dP at 128, dQ at 256, dS
+// (bf16 pairs, 64 columns) at 384. Warps: 0 K loader, 1 TMEM owner and S/dP issuer (it also
+// loads Q and dO), 2..9 math, 10 V loader, 11 dQ issuer.
+constexpr int Q_THREADS = 32 * (4 + MATH_WARPS);
+constexpr int Q_V_WARP = 2 + MATH_WARPS, Q_TS_WARP = 3 + MATH_WARPS;
+
+struct QBar {
+  uint64_t s_full, dp_full, s_free, dp_free, ds_full, dq_done, acc_free;
+};
+
+struct QItem {
+  Tile t;
+  int h, n;      // query head, key tiles
+};
+
+MARS_DEV QItem q_item(const GradArgs& a, int id) {
+  QItem it;
+  it.h = id % a.hq;
+  it.t = a.plan.first[id / a.hq];
+  it.n = it.t.tile + 1;
+  return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(Q_THREADS, 1)
+dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+          GradArgs a) {
+  using S = flash::Smem<D, D / 64>;                 // the dO tile over the staging area
+  static_assert(D * GT * 2 <= (D / 64) * GT * 128, "dO tile fits the staging area");
+  constexpr int TM_S = 0, TM_DP = GT, TM_DQ = 2 * GT, TM_DS = 3 * GT;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ flash::Barriers bar;
+  __shared__ QBar qb;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Turns turns(*a.plan.count * a.hq);
+  if (turns.at(0) < 0) return;                         // more CTAs than items
+  if (threadIdx.x == 0) {
+    mbar_init(&qb.s_full, 1);
+    mbar_init(&qb.dp_full, 1);
+    mbar_init(&qb.dq_done, 1);
+    mbar_init(&qb.s_free, MATH_THREADS);
+    mbar_init(&qb.dp_free, MATH_THREADS);
+    mbar_init(&qb.ds_full, MATH_THREADS);
+    mbar_init(&qb.acc_free, MATH_THREADS);
+    flash::init_barriers(bar);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem_base, 0);
+  volatile int* ab = &bar.abort;
+
+  if (warp == 0 || warp == Q_V_WARP) {
+    const bool is_v = warp != 0;
+    int last_k[flash::K_STAGES], last_v[flash::V_STAGES];
+    for (int i = 0; i < flash::K_STAGES; ++i) last_k[i] = -1;
+    for (int i = 0; i < flash::V_STAGES; ++i) last_v[i] = -1;
+    int j0 = 0, z = 0, kvh = 0;
+    auto issue = [&](int j, uint8_t* dst, uint64_t* b) {
+      if (lane == 0)
+        for (int x = 0; x < D / 64; ++x)
+          tma_load_3d(dst + x * (GT * 128), is_v ? &tm_v : &tm_k, b, x * 64, kvh, z + j * GT);
+    };
+    auto ring = [&](int n, bool drain) {
+      return is_v ? flash::load_ring_item<D, flash::V_STAGES>(bar, smem, n, j0, last_v, drain,
+                                                              a.status, true, issue)
+                  : flash::load_ring_item<D, flash::K_STAGES>(bar, smem, n, j0, last_k, drain,
+                                                              a.status, false, issue);
+    };
+    for (int r = 0; r < turns.rounds; ++r) {
+      const int id = turns.at(r);
+      if (id < 0) continue;
+      const QItem it = q_item(a, id);
+      z = it.t.base;
+      kvh = it.h / a.G;
+      if (!ring(it.n, false)) break;
+      j0 += it.n;
+    }
+    ring(0, true);                                   // wait (bounded) for copies in flight
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16_f32(GT, GT, false);
+      const uint64_t qd = sdesc_sw128(smem_u32(smem + S::OFF_Q), 16, 1024);
+      const uint64_t dd = sdesc_sw128(smem_u32(smem + S::OFF_STAGE), 16, 1024);
+      int jg = 0, i = 0, nq = 0;
+      bool ok = true;
+      auto product = [&](uint64_t ad, int off_b, int col, uint64_t* full) {
+        const uint64_t bd = sdesc_sw128(smem_u32(smem + off_b), 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * (GT * 128) + (k & 3) * 32;
+          mma_bf16_ss(tmem + col, sdesc_advance(ad, off), sdesc_advance(bd, off), id_s, k != 0);
+        }
+        mma_commit(full);
+      };
+      for (int r = 0; r < turns.rounds && ok; ++r) {
+        const int id = turns.at(r);
+        if (id < 0) continue;
+        const QItem it = q_item(a, id);
+        // Q and dO are replaced once the previous item's S and dP MMAs have completed
+        if (i > 0 && !(ok = mbar_wait(&bar.q_empty, (i - 1) & 1, ab, a.status))) break;
+        mbar_arrive_expect_tx(&bar.q_full, 2 * S::Q_BYTES);
+        const int z = it.t.base + GT * it.t.tile;
+        for (int x = 0; x < D / 64; ++x) {
+          tma_load_3d(smem + S::OFF_Q + x * (GT * 128), &tm_q, &bar.q_full, x * 64, it.h, z);
+          tma_load_3d(smem + S::OFF_STAGE + x * (GT * 128), &tm_do, &bar.q_full, x * 64, it.h, z);
+        }
+        ++nq;
+        if (!(ok = mbar_wait(&bar.q_full, i & 1, ab, a.status))) break;
+        for (int j = 0; j < it.n && ok; ++j, ++jg) {
+          const int sk = jg % flash::K_STAGES, sv = jg % flash::V_STAGES;
+          // S and dP of the previous tile have been loaded by the math warps
+          ok = mbar_wait(&bar.k_full[sk], (jg / flash::K_STAGES) & 1, ab, a.status) &&
+               (jg == 0 || mbar_wait(&qb.s_free, (jg - 1) & 1, ab, a.status));
+          if (!ok) break;
+          tc_fence_after();
+          product(qd, S::OFF_K + sk * S::KV_BYTES, TM_S, &qb.s_full);
+          ok = mbar_wait(&bar.v_full[sv], (jg / flash::V_STAGES) & 1, ab, a.status) &&
+               (jg == 0 || mbar_wait(&qb.dp_free, (jg - 1) & 1, ab, a.status));
+          if (!ok) break;
+          tc_fence_after();
+          product(dd, S::OFF_V + sv * S::KV_BYTES, TM_DP, &qb.dp_full);
+          mma_commit(&bar.v_empty[sv]);
+        }
+        if (!ok) break;
+        mma_commit(&bar.q_empty);
+        ++i;
+      }
+      mma_commit(&bar.drain);
+      mbar_wait(&bar.drain, 0, nullptr, a.status);
+      if (nq > 0) mbar_wait(&bar.q_full, (nq - 1) & 1, nullptr, a.status);
+    }
+  } else if (warp == Q_TS_WARP) {
+    if (lane == 0) {
+      const uint32_t id_q = idesc_bf16_f32(GT, D, true);       // A from TMEM, B MN-major
+      int jg = 0, i = 0;
+      bool ok = true;
+      for (int r = 0; r < turns.rounds && ok; ++r) {
+        const int id = turns.at(r);
+        if (id < 0) continue;
+        const int n = q_item(a, id).n;
+        for (int j = 0; j < n; ++j, ++jg) {
+          const int st = jg % flash::K_STAGES;
+          // the previous item's accumulator has been read out
+          ok = (j > 0 || i == 0 || mbar_wait(&qb.acc_free, (i - 1) & 1, ab, a.status)) &&
+               mbar_wait(&bar.k_full[st], (jg / flash::K_STAGES) & 1, ab, a.status) &&
+               mbar_wait(&qb.ds_full, jg & 1, ab, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_K + st * S::KV_BYTES), GT * 128, 1024);
+#pragma unroll
+          for (int k = 0; k < GT / 16; ++k)
+            mma_bf16_ts(tmem + TM_DQ, tmem + TM_DS + 8 * k, sdesc_advance(kd, k * 2048), id_q,
+                        (j | k) != 0);
+          mma_commit(&qb.dq_done);
+          // S, which also read this stage, completed before the math warps wrote dS
+          mma_commit(&bar.k_empty[st]);
+        }
+        if (!ok) break;
+        mma_commit(&bar.o_final);
+        ++i;
+      }
+      mma_commit(&bar.drain_pv);
+      mbar_wait(&bar.drain_pv, 0, nullptr, a.status);
+    }
+  } else {
+    // math: thread = query row (TMEM lane), 64 key columns per warp
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    auto warp_wait = [&](uint64_t* b, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(b, parity, ab, a.status));
+    };
+    int jg = 0, i = 0;
+    bool ok = true;
+    for (int r = 0; r < turns.rounds && ok; ++r) {
+      const int id = turns.at(r);
+      if (id < 0) continue;
+      const QItem it = q_item(a, id);
+      const int live = it.t.n - GT * it.t.tile;         // query rows of the tile
+      const bool rv = row < live;
+      const size_t sr = (size_t)it.h * a.pad + (size_t)it.t.id * GT + row;
+      const float lse = a.lse_p[sr], dd = a.d_p[sr];    // zeros past the sequence
+      for (int j = 0; j < it.n; ++j, ++jg) {
+        const bool diag = j == it.t.tile;
+        if (!(ok = warp_wait(&qb.s_full, jg & 1))) break;
+        tc_fence_after();
+        uint32_t sv[64];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          tmem_ld32(tmem + TM_S + 64 * half + 32 * q + lane_off,
+                    *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * q));
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&qb.s_free);
+        // keys this row sees among the warp's columns: on the diagonal tile 0 .. row
+        uint32_t mk[2] = {0xffffffffu, 0xffffffffu};
+        if (diag || !rv) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            mk[q] = rv ? bits(0, row + 1 - 64 * half - 32 * q) : 0u;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((mk[q] >> e) & 1u)) sv[32 * q + e] = 0xff800000u;
+          }
+        }
+        float pf[64];
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+        const float2 nl2 = make_float2(-lse, -lse), nd2 = make_float2(-dd, -dd);
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const float2 t = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
+                                      sc2, nl2);
+          pf[e] = flash::ex2_approx(t.x);
+          pf[e + 1] = flash::ex2_approx(t.y);
+        }
+        if (!(ok = warp_wait(&qb.dp_full, jg & 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          tmem_ld32(tmem + TM_DP + 64 * half + 32 * q + lane_off,
+                    *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * q));
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&qb.dp_free);
+        if (diag || !rv) {                             // masked dP may hold anything
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((mk[q] >> e) & 1u)) sv[32 * q + e] = 0u;
+        }
+        if (diag && live < GT) {
+          // K rows past the sequence, which the MMA of S has read
+          clear_rows<D>(smem + S::OFF_K + (jg % flash::K_STAGES) * S::KV_BYTES, live, 0, GT,
+                        (warp - 2) * 32 + lane, MATH_THREADS);
+          fence_proxy_async_smem();
+        }
+        uint32_t ds[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const float2 x = __fmul2_rn(make_float2(pf[e], pf[e + 1]),
+                                      __fadd2_rn(make_float2(__uint_as_float(sv[e]),
+                                                             __uint_as_float(sv[e + 1])), nd2));
+          ds[e / 2] = flash::pack_bf16x2(x.x, x.y);
+        }
+        if (it.t.tile == 0 && row == 0 && half == 0) ds[0] = 0;   // dS of row 0 is 0
+        // dS has one buffer: the previous tile's dQ MMA must have read it
+        if (jg > 0 && !(ok = warp_wait(&qb.dq_done, (jg - 1) & 1))) break;
+        tc_fence_after();
+        tmem_st32(tmem + TM_DS + 32 * half + lane_off, ds);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&qb.ds_full);
+      }
+      if (!ok) break;
+      if (!(ok = warp_wait(&bar.o_final, i & 1))) break;
+      tc_fence_after();
+      constexpr int HD = D / 2;
+      uint32_t o[HD];
+#pragma unroll
+      for (int q = 0; q < HD / 32; ++q)
+        tmem_ld32(tmem + TM_DQ + HD * half + 32 * q + lane_off,
+                  *reinterpret_cast<uint32_t(*)[32]>(o + 32 * q));
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive_warp(&qb.acc_free);
+      if (rv) {
+        uint4* dst = reinterpret_cast<uint4*>(
+            a.dq + ((size_t)it.t.base + GT * it.t.tile + row) * a.dq_stride + it.h * D + HD * half);
+#pragma unroll
+        for (int e = 0; e < HD; e += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            w[c] = flash::pack_bf16x2(__uint_as_float(o[e + 2 * c]) * a.scale,
+                                      __uint_as_float(o[e + 2 * c + 1]) * a.scale);
+          dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      ++i;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------- host
+
+// Query-head splits of a KV head's items: enough items for about kWaves per SM, so that the
+// heaviest ones (the first keys of long sequences) can be evened out.
+constexpr int kWaves = 4;
+
+int grad_splits(int batch, int total, int hq, int hkv) {
+  const long long items = packed::max_tiles(batch, total, GT) * hkv;
+  const long long want = ((long long)kWaves * num_sms() + items - 1) / items;
+  return (int)std::min<long long>(hq / hkv, want);
+}
+
+struct GradSpace {
+  packed::Plan plan;
+  float *lse_p, *d_p, *part;
+  size_t bytes;
+};
+
+GradSpace carve(void* base, int batch, int total, int hq, int hkv, int d) {
+  GradSpace g{};
+  size_t off = 0;
+  g.plan = packed::carve_plan(base, off, batch, total, GT, true);
+  uint8_t* p = static_cast<uint8_t*>(base);
+  auto take = [&](size_t n) {
+    float* at = p ? reinterpret_cast<float*>(p + off) : nullptr;
+    off += packed::align256(n * sizeof(float));
+    return at;
+  };
+  const size_t rows = (size_t)packed::max_tiles(batch, total, GT) * GT;
+  g.lse_p = take(rows * hq);
+  g.d_p = take(rows * hq);
+  const int ns = grad_splits(batch, total, hq, hkv);
+  g.part = take(ns > 1 ? (size_t)ns * 2 * total * hkv * d : 0);
+  g.bytes = off;
+  return g;
+}
+
+bool map3(CUtensorMap* m, const void* base, int d, int heads, int total, long long stride) {
+  const uint64_t dims[3] = {(uint64_t)d, (uint64_t)heads, (uint64_t)total};
+  const uint64_t str[2] = {(uint64_t)d * 2, (uint64_t)stride * 2};
+  const uint32_t box[3] = {64, 1, GT};
+  return encode_tmap_bf16(m, base, 3, dims, str, box);
+}
+
+template <int D>
+cudaError_t launch_grad(const PackedGrad& p, GradArgs& a, cudaStream_t stream) {
+  CUtensorMap tq, tdo, tk, tv;
+  if (!map3(&tq, p.q, D, p.hq, p.total, p.q_stride) ||
+      !map3(&tdo, p.d_o, D, p.hq, p.total, (long long)p.hq * D) ||
+      !map3(&tk, p.k, D, p.hkv, p.total, p.k_stride) ||
+      !map3(&tv, p.v, D, p.hkv, p.total, p.v_stride))
+    return cudaErrorInvalidValue;
+  using SK = KSmem<D>;
+  using SQ = flash::Smem<D, D / 64>;
+  static_assert(SK::TOTAL + sizeof(KBar) <= 227 * 1024, "dK/dV layout fits shared memory");
+  static_assert(SQ::TOTAL + sizeof(flash::Barriers) + sizeof(QBar) <= 227 * 1024,
+                "dQ layout fits shared memory");
+  static std::atomic<int> attr_k[64], attr_q[64];
+  cudaError_t e = set_smem_limit_once(dkdv_kernel<D>, SK::TOTAL, attr_k);
+  if (e == cudaSuccess) e = set_smem_limit_once(dq_kernel<D>, SQ::TOTAL, attr_q);
+  if (e != cudaSuccess) return e;
+  const long long tiles = packed::max_tiles(p.batch, p.total, GT);
+  const dim3 by_tile((unsigned)tiles, tiles < num_sms() ? 8 : 2);
+  prep_kernel<D><<<by_tile, 256, 0, stream>>>(a);
+  const long long kitems = tiles * p.hkv * a.nsplit, qitems = tiles * p.hq;
+  dkdv_kernel<D><<<(unsigned)std::min<long long>(kitems, num_sms()), K_THREADS, SK::TOTAL, stream>>>(
+      tq, tdo, tk, tv, a);
+  if (a.nsplit > 1) merge_kernel<D><<<by_tile, 256, 0, stream>>>(a);
+  dq_kernel<D><<<(unsigned)std::min<long long>(qitems, num_sms()), Q_THREADS, SQ::TOTAL, stream>>>(
+      tq, tdo, tk, tv, a);
+  count_launches(a.nsplit > 1 ? 4 : 3);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t packed_grad_workspace_bytes(int batch, int total, int hq, int hkv, int d) {
+  return carve(nullptr, batch, total, hq, hkv, d).bytes;
+}
+
+cudaError_t launch_packed_grad(const PackedGrad& p, void* workspace, cudaStream_t stream) {
+  const GradSpace g = carve(workspace, p.batch, p.total, p.hq, p.hkv, p.d);
+  GradArgs a{};
+  a.plan = g.plan;
+  a.batch = p.batch;
+  a.total = p.total;
+  a.hq = p.hq;
+  a.hkv = p.hkv;
+  a.G = p.hq / p.hkv;
+  a.nsplit = grad_splits(p.batch, p.total, p.hq, p.hkv);
+  a.pad = packed::max_tiles(p.batch, p.total, GT) * GT;
+  a.scale = p.scale;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.o = p.o;
+  a.d_o = p.d_o;
+  a.lse = p.lse;
+  a.lse_p = g.lse_p;
+  a.d_p = g.d_p;
+  a.dq = p.dq;
+  a.dk = p.dk;
+  a.dv = p.dv;
+  a.dq_stride = p.dq_stride;
+  a.dk_stride = p.dk_stride;
+  a.dv_stride = p.dv_stride;
+  a.part = g.part;
+  a.status = p.status;
+  const cudaError_t e = packed::launch_plan(g.plan, p.cu, nullptr, 0, p.batch, p.total, GT,
+                                            p.status, stream);
+  if (e != cudaSuccess) return e;
+  return p.d == 64 ? launch_grad<64>(p, a, stream) : launch_grad<128>(p, a, stream);
+}
+
+}  // namespace mars

@@ -74,6 +74,8 @@ def lib() -> ctypes.CDLL:
         L.mars_packed_workspace_bytes.argtypes = [I] * 7
         L.mars_attn_packed.restype = I
         L.mars_attn_packed.argtypes = [P] * 6 + [I] * 8 + [F, P, S, P, P]
+        L.mars_attn_packed_grad.restype = I
+        L.mars_attn_packed_grad.argtypes = [P] * 10 + [I] * 11 + [F, P, S, P, P]
         L.mars_attn_chunk.restype = I
         L.mars_attn_chunk.argtypes = [P] * 6 + [I, P, I, P, I, P] + [I] * 9 + [F, P, S, P, P]
         L.mars_kv_append.restype = I
@@ -96,7 +98,7 @@ EXPORTED = ("mars_workspace_bytes", "mars_attn_dual_stream", "mars_decode_attn",
             "mars_dual_stream_ce_loss",
             "mars_dual_stream_ce_loss_grad", "mars_attn_dual_stream_grad",
             "mars_attn_dual_stream_lse", "mars_attn_dual_stream_grad_lse",
-            "mars_packed_workspace_bytes", "mars_attn_packed", "mars_attn_chunk",
+            "mars_packed_workspace_bytes", "mars_attn_packed", "mars_attn_packed_grad", "mars_attn_chunk",
             "mars_kv_append",
             "mars_check_wait_timeout", "mars_strerror",
             "mars_version", "mars_launch_count")

@@ -82,6 +82,23 @@ def mars_attn_packed(q, k, v, cu_seqlens, o, workspace, lse=None, scale: float =
                                _stream(stream)), "mars_attn_packed")
 
 
+def mars_attn_packed_grad(q, k, v, o, d_o, lse, cu_seqlens, dq, dk, dv, workspace,
+                          scale: float = 0.0, status=None, stream=None):
+    """dq, dk, dv (bf16) of mars_attn_packed for the upstream gradient d_o, from its o and lse
+    (see include/mars.h); dq, dk, dv may be slices of a wider tensor, like q, k, v."""
+    batch, total, hq, hkv, d, (qs, ks, vs) = _packed_args(q, k, v, cu_seqlens, o, workspace, status)
+    _check(d_o, "d_o", torch.bfloat16, (total, hq, d))
+    _check(lse, "lse", torch.float32, (hq, total))
+    dqs = _check_rows(dq, "dq", (total, hq, d))
+    dks, dvs = _check_rows(dk, "dk", (total, hkv, d)), _check_rows(dv, "dv", (total, hkv, d))
+    _check_one_device(stream, q=q, k=k, v=v, o=o, d_o=d_o, lse=lse, cu_seqlens=cu_seqlens, dq=dq,
+                      dk=dk, dv=dv, workspace=workspace, status=status)
+    _rc(lib().mars_attn_packed_grad(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(d_o), _ptr(lse), _ptr(cu_seqlens), _ptr(dq),
+        _ptr(dk), _ptr(dv), batch, total, hq, hkv, d, qs, ks, vs, dqs, dks, dvs, float(scale),
+        _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)), "mars_attn_packed_grad")
+
+
 def mars_attn_chunk(q, k, v, cu_seqlens, k_pool, v_pool, block_table, seq_lens,
                     max_len_hint: int, o, workspace, status=None, scale: float = 0.0,
                     stream=None):

@@ -370,8 +370,8 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
  *   - hq / hkv, d, scale and status as elsewhere; status may be NULL.
  *   - A key that a sequence may not read (another sequence's row, a row behind the last
  *     sequence, a free slot of a page, an unmapped page) has no effect whatever it holds,
- *     NaN included. A NaN or infinity in a sequence's own v can reach the rows of that
- *     sequence up to 127 places before it. */
+ *     NaN included. A NaN or infinity in a sequence's own rows can reach the outputs of
+ *     that sequence up to 127 rows before or after the rows that the formulas reach. */
 
 /* Workspace (device scratch, >= 256-byte aligned) of `op` (MARS_OP_ATTN_PACKED,
  * MARS_OP_ATTN_CHUNK, MARS_OP_ATTN_PACKED_GRAD) for `total` rows of `batch` sequences;
@@ -391,6 +391,23 @@ int mars_attn_packed(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
                      int hq, int hkv, int d, int q_stride, int k_stride, int v_stride,
                      float scale, void* workspace, size_t ws_bytes, int32_t* status,
                      void* stream);
+
+/* Gradient of mars_attn_packed for the upstream gradient d_o of o: with P the softmax weights,
+ * dP = d_o V^T and D the row sums of d_o * o, dS = P * (dP - D), dQ = scale dS K,
+ * dK = scale sum dS^T Q and dV = sum P^T d_o over the query heads of a KV head.
+ *   o, lse  as mars_attn_packed wrote them, with the same q, k, v, boundaries and scale
+ *   d_o     [total, hq, d] bf16
+ *   dq [total, hq, d], dk, dv [total, hkv, d] bf16 (written for the rows of the sequences),
+ *           row pitches dq_stride, dk_stride, dv_stride like those of q, k, v
+ *   workspace >= mars_packed_workspace_bytes(MARS_OP_ATTN_PACKED_GRAD, ...) bytes
+ * Sums run in a fixed order: repeated calls agree bit for bit. */
+int mars_attn_packed_grad(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
+                          const mars_bf16* o, const mars_bf16* d_o, const float* lse,
+                          const int32_t* cu_seqlens, mars_bf16* dq, mars_bf16* dk,
+                          mars_bf16* dv, int batch, int total, int hq, int hkv, int d,
+                          int q_stride, int k_stride, int v_stride, int dq_stride,
+                          int dk_stride, int dv_stride, float scale, void* workspace,
+                          size_t ws_bytes, int32_t* status, void* stream);
 
 /* Attention of a chunk of new tokens per sequence (one token, a prompt's next part, a whole
  * prompt) over the paged cache: row i of sequence s attends to the P_s = seq_lens[s] tokens

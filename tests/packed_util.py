@@ -102,3 +102,59 @@ def causal_weights(q, k, scale=None):
     z = np.where(i <= np.arange(n)[:, None], z, -np.inf)
     e = np.exp(z - z.max(axis=1, keepdims=True))
     return e / e.sum(axis=1, keepdims=True)
+
+
+def run_grad(y, o, lse, d_o, fill=7.0, scale=0.0, wide=True, ws=None, out=None, **kw):
+    """dq, dk, dv of run_packed's o and lse; `wide`: as slices of one tensor."""
+    n, hq, d = y["q"].shape
+    hkv = y["k"].shape[1]
+    if out is None:
+        all_ = torch.full((n, hq + 2 * hkv, d), fill, dtype=torch.bfloat16, device="cuda")
+        out = all_.split([hq, hkv, hkv], dim=1)
+        if not wide:
+            out = [t.contiguous() for t in out]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if ws is None:
+        ws = workspace(packed.OP_ATTN_PACKED_GRAD, len(y["cu"]) - 1, n, hq, hkv, d)
+    packed.mars_attn_packed_grad(y["q"], y["k"], y["v"], o, d_o, lse, y["cu"], *out, ws, status=st,
+                                 scale=scale, **kw)
+    torch.cuda.synchronize()
+    return [*out, int(st.item())]
+
+
+def gradient_bounds(x, a, b, u):
+    """Reference and elementwise bounds of dq [heads of group u], dk and dv of KV head u for the
+    sequence in rows [a, b). The model of parity_util with one rounding (dS is formed from the
+    unrounded P), to which D = rowsum(dO * o) adds: o carries output_bound, so D is off by at
+    most sum_c |dO_c| output_bound_c, which enters dS times P. The results are rounded to bf16."""
+    g = x["q"].shape[1] // x["k"].shape[1]
+    k, v = f64(x["k"][a:b, u]), f64(x["v"][a:b, u])
+    scale, n = 1.0 / np.sqrt(k.shape[1]), b - a
+    dq, dq_b = [], []
+    dk, dv = np.zeros_like(k), np.zeros_like(k)
+    s1 = {"k": 0.0, "v": 0.0}
+    s2 = {"k": 0.0, "v": 0.0}
+    up = 0.0
+    for h in range(u * g, u * g + g):
+        q, do = f64(x["q"][a:b, h]), f64(x["do"][a:b, h])
+        P = causal_weights(q, k)
+        dP = do @ v.T
+        D = (P * dP).sum(axis=1, keepdims=True)
+        dS = scale * P * (dP - D)
+        off = (np.abs(do) * output_bound(P, v, P @ v)).sum(axis=1, keepdims=True)
+        slack = scale * P * (UPSTREAM_REL * (np.abs(dP) + np.abs(D)) + off)
+        slack[0] = 0.0                                  # row 0: dS is 0, exactly
+        dq.append(dS @ k)
+        dq_b.append(product_error_bound(np.abs(dS) @ np.abs(k), dS ** 2 @ k ** 2, n, slack @ np.abs(k)))
+        dk, dv = dk + dS.T @ q, dv + P.T @ do
+        s1["k"], s2["k"] = s1["k"] + np.abs(dS).T @ np.abs(q), s2["k"] + (dS ** 2).T @ q ** 2
+        s1["v"], s2["v"] = s1["v"] + P.T @ np.abs(do), s2["v"] + (P ** 2).T @ do ** 2
+        up = up + slack.T @ np.abs(q)
+    dk_b = product_error_bound(s1["k"], s2["k"], g * n, up, extra_roundings=g)
+    dv_b = product_error_bound(s1["v"], s2["v"], g * n, extra_roundings=g)
+
+    def rounded(r, e):
+        return e + U_BF16 * (np.abs(r) + e)
+
+    return ([(r, rounded(r, e)) for r, e in zip(dq, dq_b)], (dk, rounded(dk, dk_b)),
+            (dv, rounded(dv, dv_b)))

@@ -6,8 +6,8 @@ import torch
 
 import oracle
 from block_masked_token_gb300 import mars, packed
-from packed_util import (LSE_TOL, PAGE, causal_weights, cuda, f64, make, output_bound,
-                         run_chunk, run_packed, workspace)
+from packed_util import (LSE_TOL, PAGE, causal_weights, cuda, f64, gradient_bounds, make,
+                         output_bound, run_chunk, run_grad, run_packed, workspace)
 from parity_util import assert_within_bound
 
 pytestmark = pytest.mark.gpu
@@ -110,6 +110,116 @@ def test_packed_bad_boundaries_are_cut(cu, want):
     x["cu"] = torch.tensor(want, dtype=torch.int32)
     o2, lse2, st = run_packed(cuda(x))
     assert st == 0 and same(o, o2) and same(lse, lse2)
+
+
+# ----------------------------------------------------------------------------- gradient
+
+def check_grad(x, dq, dk, dv, fill=7.0):
+    got, cu = {"q": f64(dq), "k": f64(dk), "v": f64(dv)}, x["cu"].tolist()
+    ref = oracle.attn_packed_grad(*(f64(x[c]) for c in ("q", "k", "v", "do")), x["cu"].numpy())
+    g = x["q"].shape[1] // x["k"].shape[1]
+    for a, b in zip(cu, cu[1:]):
+        for u in range(x["k"].shape[1] if b > a else 0):
+            qs, k, v = gradient_bounds(x, a, b, u)
+            np.testing.assert_allclose(k[0], ref[1][a:b, u], atol=1e-9)
+            for i, (r, e) in enumerate(qs):
+                assert_within_bound(got["q"][a:b, u * g + i], r, e, f"dq rows {a}:{b} head {u * g + i}")
+            assert_within_bound(got["k"][a:b, u], *k, f"dk rows {a}:{b} head {u}")
+            assert_within_bound(got["v"][a:b, u], *v, f"dv rows {a}:{b} head {u}")
+    outside = np.ones(x["n"], dtype=bool)
+    outside[cu[0]:cu[-1]] = False
+    assert all((t[outside] == fill).all() for t in got.values())
+
+
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("lens", LENS, ids=str)
+def test_gradient_matches_oracle(lens, heads):
+    x = make(lens, *heads, seed=len(lens), tail=3, lead=2, fused=heads[0] != 4)
+    y = cuda(x)
+    o, lse, _ = run_packed(y)
+    dq, dk, dv, st = run_grad(y, o, lse, y["do"], wide=heads[0] != 4)
+    assert st == 0
+    check_grad(x, dq, dk, dv)
+
+
+def test_gradient_without_splits():
+    """Enough key tiles that one item takes every query head of its KV head."""
+    x = make([(i * 5) % 37 for i in range(80)], 16, 8, 64, seed=21)
+    y = cuda(x)
+    o, lse, _ = run_packed(y)
+    dq, dk, dv, st = run_grad(y, o, lse, y["do"])
+    assert st == 0
+    check_grad(x, dq, dk, dv)
+
+
+def test_gradient_of_single_tokens_is_exact():
+    """One key: its weight is 1 whatever the score."""
+    x = make([1] * 9, 4, 2, 64, seed=22)
+    y = cuda(x)
+    o, lse, _ = run_packed(y)
+    dq, dk, dv, _ = run_grad(y, o, lse, y["do"])
+    assert (dq == 0).all() and (dk == 0).all()
+    assert same(dv, x["do"].float().view(9, 2, 2, 64).sum(2).to(torch.bfloat16))
+
+
+def test_gradient_other_rows_have_no_effect_and_runs_agree():
+    x = make([70, 30, 150], 14, 2, 64, seed=8, tail=60)
+    y = cuda(x)
+    o, lse, _ = run_packed(y)
+    first = run_grad(y, o, lse, y["do"], fill=0.0)
+    again = run_grad(y, o, lse, y["do"], fill=0.0)
+    assert all(same(a, b) for a, b in zip(first[:3], again[:3]))
+    for rows, bad in ((slice(70, 100), float("nan")), (slice(250, None), float("inf"))):
+        y["qkv"][rows] = bad
+        y["do"][rows] = bad
+        o[rows] = bad
+        lse[:, rows] = bad
+    got = run_grad(y, o, lse, y["do"], fill=0.0)
+    for a, b in zip(first[:3], got[:3]):
+        assert same(a[:70], b[:70]) and same(a[100:250], b[100:250])
+
+
+def test_gradient_bad_boundaries_are_cut():
+    x = make([20, 20, 50], 4, 2, 64, seed=10)
+    y = cuda(x)
+    got = []
+    for cu in ([0, 40, 30, 2000000], [0, 40, 40, 90]):
+        y["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        o, lse, _ = run_packed(y)
+        got.append(run_grad(y, o, lse, y["do"]))
+    assert got[0][3] == mars.ST_BADSEQ and got[1][3] == 0
+    assert all(same(a, b) for a, b in zip(got[0][:3], got[1][:3]))
+
+
+def test_training_step_in_a_graph_and_on_another_stream():
+    x = make([200, 1, 77], 14, 2, 64, seed=23)
+    y = cuda(x)
+    want_o, want_lse, _ = run_packed(y)
+    want = run_grad(y, want_o, want_lse, y["do"], wide=False)[:3]
+    o, lse = torch.zeros_like(want_o), torch.zeros_like(want_lse)
+    out = [torch.zeros_like(t) for t in want]
+    wf = workspace(packed.OP_ATTN_PACKED, 3, x["n"], 14, 2, 64)
+    wg = workspace(packed.OP_ATTN_PACKED_GRAD, 3, x["n"], 14, 2, 64)
+
+    def step(stream=None):
+        packed.mars_attn_packed(y["q"], y["k"], y["v"], y["cu"], o, wf, lse=lse, stream=stream)
+        packed.mars_attn_packed_grad(y["q"], y["k"], y["v"], o, y["do"], lse, y["cu"], *out, wg,
+                                     stream=stream)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)
+    side.synchronize()
+    assert all(same(a, b) for a, b in zip(out, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for t in (o, lse, *out):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(o, want_o) and all(same(a, b) for a, b in zip(out, want))
 
 
 # ------------------------------------------------------------------------------- chunks

@@ -119,6 +119,23 @@ def append(L, k=P, v=P, cu=P, lens=P, new=None, table=P, max_pages=4, kp=P, vp=P
                             total, hkv, d, page, *strides, None, None)
 
 
+def grad(L, q=P, k=P, v=P, o=P, d_o=P, lse=P, cu=P, dq=P, dk=P, dv=P, batch=2, total=40, hq=4,
+         hkv=2, d=64, strides=(512,) * 6, scale=0.0, ws=P, ws_bytes=1 << 30):
+    return L.mars_attn_packed_grad(q, k, v, o, d_o, lse, cu, dq, dk, dv, batch, total, hq, hkv, d,
+                                   *strides, scale, ws, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("change, code", [
+    *[({n: None}, mars.EINVAL) for n in ("q", "v", "o", "d_o", "lse", "cu", "dq", "dk", "dv", "ws")],
+    *[({n: BAD}, mars.EALIGN) for n in ("k", "o", "d_o", "dq", "dv", "ws")],
+    ({"strides": (512, 512, 512, 248, 512, 512)}, mars.EINVAL),
+    ({"strides": (512, 512, 512, 512, 512, 132)}, mars.EALIGN), ({"hq": 3}, mars.EINVAL),
+    ({"d": 32}, mars.EUNSUPPORTED), ({"total": -2}, mars.EINVAL), ({"ws_bytes": 64}, mars.ENOSPACE),
+    ({"scale": float("inf")}, mars.EINVAL), ({"total": 0}, mars.OK), ({"batch": 0}, mars.OK)], ids=str)
+def test_gradient_refusals(L, change, code):
+    assert grad(L, **change) == code
+
+
 SHARED = [({"q": None}, mars.EINVAL), ({"cu": None}, mars.EINVAL), ({"o": None}, mars.EINVAL),
           ({"k": BAD}, mars.EALIGN), ({"o": BAD}, mars.EALIGN), ({"ws": BAD}, mars.EALIGN),
           ({"batch": -1}, mars.EINVAL), ({"total": -1}, mars.EINVAL),
@@ -175,6 +192,7 @@ def test_bindings_refuse_host_tensors(L):
     q, k, ws = bf(4, 2, 64), bf(4, 1, 64), torch.zeros(64, dtype=torch.uint8)
     pool = bf(4, 1, 16, 64)
     for call in (lambda: packed.mars_attn_packed(q, k, k, i32(2), q, ws),
+                 lambda: packed.mars_attn_packed_grad(q, k, k, q, q, torch.zeros(2, 4), i32(2), q, k, k, ws),
                  lambda: packed.mars_attn_chunk(q, k, k, i32(2), pool, pool, i32(1, 4), i32(1), 9, q, ws),
                  lambda: packed.mars_kv_append(k, k, i32(2), i32(1), i32(1, 4), pool, pool)):
         with pytest.raises(ValueError, match="CUDA"):
