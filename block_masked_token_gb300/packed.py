@@ -7,96 +7,152 @@ from __future__ import annotations
 
 import torch
 
-from .mars import PAGE_SIZE, _check, _ptr, _rc, _stream, lib
+from .mars import MarsError, PAGE_SIZE, lib
 
 OP_ATTN_PACKED, OP_ATTN_CHUNK, OP_ATTN_PACKED_GRAD = 6, 7, 8
 
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
-def _check_rows(t, name, shape):
-    """A bf16 [total, heads, d] tensor whose rows may be slices of a wider tensor (the heads of
-    a row contiguous); returns its row pitch in elements."""
+# A step's smallest calls take a few microseconds on the GPU, so these checks are written for
+# few attribute reads per tensor, and pointers are passed as plain integers (0 for none).
+
+
+def _refuse(t, name, dtype, shape, dev):
+    """Raise for the first thing that is wrong with t (something is)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libmars has no CPU path)")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call goes to cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _ptr(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or
+            t.shape != shape or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, shape, dev):
+    return 0 if t is None else _ptr(t, name, dtype, shape, dev)
+
+
+def _rows(t, name, shape, dev):
+    """Address and row pitch, in elements, of a bf16 [total, heads, d] tensor whose rows may be
+    slices of a wider tensor (the heads of a row contiguous)."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != _BF16 or
+            t.shape != shape):
+        _refuse(t, name, _BF16, shape, dev)
     total, heads, d = shape
-    if t.numel() == 0:
-        return heads * d
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    pitch, head, one = t.stride()
+    if total == 0 or heads == 0 or d == 0:
+        return t.data_ptr(), heads * d
+    if (one != 1 and d > 1) or (head != d and heads > 1):
         raise ValueError(f"the heads of each row of {name} must be contiguous")
     if total == 1:
-        return heads * d
-    if t.stride(0) < heads * d or t.stride(0) % 8 or t.stride(0) > 0x7fffffff:
-        raise ValueError(f"{name} has row pitch {t.stride(0)}: it must be a multiple of 8, at "
-                         f"least {heads * d} and below 2^31")
-    return t.stride(0)
+        return t.data_ptr(), heads * d
+    if pitch < heads * d or pitch % 8 or pitch > 0x7fffffff:
+        raise ValueError(f"{name} has row pitch {pitch}: it must be a multiple of 8, at least "
+                         f"{heads * d} and below 2^31")
+    return t.data_ptr(), pitch
 
 
-def _check_one_device(stream, **tensors):
-    """Every tensor on the device whose stream the call goes to."""
-    want = torch.cuda.current_device() if stream is None else stream.device.index
-    for name, t in tensors.items():
-        if t is not None and t.device.index != want:
-            raise ValueError(f"{name} is on cuda:{t.device.index}, the stream's device is "
-                             f"cuda:{want}")
-    if want != torch.cuda.current_device():
-        raise ValueError(f"the stream is on cuda:{want}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+def _target(stream):
+    """Device and raw handle of the stream that a call goes to; the device has to be current
+    (the library launches there)."""
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device.index}, the current device is "
+                         f"cuda:{dev}")
+    return dev, stream.cuda_stream
+
+
+def _need_cuda(t, name):
+    """A host tensor is refused before the CUDA runtime is asked for anything."""
+    if isinstance(t, torch.Tensor) and not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libmars has no CPU path)")
+
+
+def _batch(cu_seqlens):
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must hold batch + 1 boundaries")
+    return cu_seqlens.shape[0] - 1
+
+
+def _table(block_table, batch, dev):
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages]")
+    width = block_table.shape[1]
+    return _ptr(block_table, "block_table", _I32, (batch, width), dev), width
+
+
+def _workspace(ws, dev):
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    size = ws.numel()
+    return _ptr(ws, "workspace", _U8, (size,), dev), size
+
+
+def _rc(code, where):
+    if code:
+        raise MarsError(code, where)
 
 
 def mars_packed_workspace_bytes(op, batch, total, hq=1, hkv=1, d=64, max_len=0):
     return int(lib().mars_packed_workspace_bytes(op, batch, total, hq, hkv, d, max_len))
 
 
-def _packed_args(q, k, v, cu_seqlens, o, workspace, status):
-    total, hq, d = q.shape
-    hkv = k.shape[1]
-    strides = (_check_rows(q, "q", (total, hq, d)), _check_rows(k, "k", (total, hkv, d)),
-               _check_rows(v, "v", (total, hkv, d)))
-    _check(cu_seqlens, "cu_seqlens", torch.int32)
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens must hold batch + 1 boundaries")
-    _check(o, "o", torch.bfloat16, (total, hq, d))
-    _check(workspace, "workspace", torch.uint8)
-    if status is not None:
-        _check(status, "status", torch.int32, (1,))
-    return cu_seqlens.shape[0] - 1, total, hq, hkv, d, strides
-
-
 def mars_attn_packed(q, k, v, cu_seqlens, o, workspace, lse=None, scale: float = 0.0,
                      status=None, stream=None):
     """o[total, hq, d] (bf16) = causal attention inside each sequence of a packed batch; lse
     [hq, total] (float32, optional) its log2 row statistics (see include/mars.h)."""
-    batch, total, hq, hkv, d, (qs, ks, vs) = _packed_args(q, k, v, cu_seqlens, o, workspace, status)
-    if lse is not None:
-        _check(lse, "lse", torch.float32, (hq, total))
-    _check_one_device(stream, q=q, k=k, v=v, cu_seqlens=cu_seqlens, o=o, lse=lse,
-                      workspace=workspace, status=status)
-    _rc(lib().mars_attn_packed(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(o), _ptr(lse),
-                               batch, total, hq, hkv, d, qs, ks, vs, float(scale),
-                               _ptr(workspace), workspace.numel(), _ptr(status),
-                               _stream(stream)), "mars_attn_packed")
+    _need_cuda(q, "q")
+    dev, raw = _target(stream)
+    total, hq, d = q.shape
+    hkv = k.shape[1]
+    batch = _batch(cu_seqlens)
+    qp, qs = _rows(q, "q", (total, hq, d), dev)
+    kp, ks = _rows(k, "k", (total, hkv, d), dev)
+    vp, vs = _rows(v, "v", (total, hkv, d), dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _rc(lib().mars_attn_packed(
+        qp, kp, vp, _ptr(cu_seqlens, "cu_seqlens", _I32, (batch + 1,), dev),
+        _ptr(o, "o", _BF16, (total, hq, d), dev), _opt(lse, "lse", _F32, (hq, total), dev), batch,
+        total, hq, hkv, d, qs, ks, vs, scale, ws, ws_bytes,
+        _opt(status, "status", _I32, (1,), dev), raw), "mars_attn_packed")
 
 
 def mars_attn_packed_grad(q, k, v, o, d_o, lse, cu_seqlens, dq, dk, dv, workspace,
                           scale: float = 0.0, status=None, stream=None):
     """dq, dk, dv (bf16) of mars_attn_packed for the upstream gradient d_o, from its o and lse
     (see include/mars.h); dq, dk, dv may be slices of a wider tensor, like q, k, v."""
-    batch, total, hq, hkv, d, (qs, ks, vs) = _packed_args(q, k, v, cu_seqlens, o, workspace, status)
-    _check(d_o, "d_o", torch.bfloat16, (total, hq, d))
-    _check(lse, "lse", torch.float32, (hq, total))
-    dqs = _check_rows(dq, "dq", (total, hq, d))
-    dks, dvs = _check_rows(dk, "dk", (total, hkv, d)), _check_rows(dv, "dv", (total, hkv, d))
-    _check_one_device(stream, q=q, k=k, v=v, o=o, d_o=d_o, lse=lse, cu_seqlens=cu_seqlens, dq=dq,
-                      dk=dk, dv=dv, workspace=workspace, status=status)
+    _need_cuda(q, "q")
+    dev, raw = _target(stream)
+    total, hq, d = q.shape
+    hkv = k.shape[1]
+    batch = _batch(cu_seqlens)
+    qp, qs = _rows(q, "q", (total, hq, d), dev)
+    kp, ks = _rows(k, "k", (total, hkv, d), dev)
+    vp, vs = _rows(v, "v", (total, hkv, d), dev)
+    dqp, dqs = _rows(dq, "dq", (total, hq, d), dev)
+    dkp, dks = _rows(dk, "dk", (total, hkv, d), dev)
+    dvp, dvs = _rows(dv, "dv", (total, hkv, d), dev)
+    ws, ws_bytes = _workspace(workspace, dev)
     _rc(lib().mars_attn_packed_grad(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(d_o), _ptr(lse), _ptr(cu_seqlens), _ptr(dq),
-        _ptr(dk), _ptr(dv), batch, total, hq, hkv, d, qs, ks, vs, dqs, dks, dvs, float(scale),
-        _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)), "mars_attn_packed_grad")
+        qp, kp, vp, _ptr(o, "o", _BF16, (total, hq, d), dev),
+        _ptr(d_o, "d_o", _BF16, (total, hq, d), dev), _ptr(lse, "lse", _F32, (hq, total), dev),
+        _ptr(cu_seqlens, "cu_seqlens", _I32, (batch + 1,), dev), dqp, dkp, dvp, batch, total, hq,
+        hkv, d, qs, ks, vs, dqs, dks, dvs, scale, ws, ws_bytes,
+        _opt(status, "status", _I32, (1,), dev), raw), "mars_attn_packed_grad")
 
 
 def mars_attn_chunk(q, k, v, cu_seqlens, k_pool, v_pool, block_table, seq_lens,
@@ -104,54 +160,43 @@ def mars_attn_chunk(q, k, v, cu_seqlens, k_pool, v_pool, block_table, seq_lens,
                     stream=None):
     """o[total, hq, d] (bf16) = attention of each sequence's new rows over its seq_lens[s]
     cached tokens and, causally, its own new keys (see include/mars.h)."""
-    batch, total, hq, hkv, d, (qs, ks, vs) = _packed_args(q, k, v, cu_seqlens, o, workspace, status)
-    num_pages = k_pool.shape[0]
-    _check(k_pool, "k_pool", torch.bfloat16, (num_pages, hkv, PAGE_SIZE, d))
-    _check(v_pool, "v_pool", torch.bfloat16, (num_pages, hkv, PAGE_SIZE, d))
-    _check(seq_lens, "seq_lens", torch.int32, (batch,))
-    _check(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [{batch}, "
-                         "max_pages]")
-    _check_one_device(stream, q=q, k=k, v=v, cu_seqlens=cu_seqlens, k_pool=k_pool, v_pool=v_pool,
-                      block_table=block_table, seq_lens=seq_lens, o=o, workspace=workspace,
-                      status=status)
-    _rc(lib().mars_attn_chunk(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(k_pool),
-                              _ptr(v_pool), num_pages, _ptr(block_table), block_table.shape[1],
-                              _ptr(seq_lens), int(max_len_hint), _ptr(o), batch, total, hq, hkv,
-                              d, PAGE_SIZE, qs, ks, vs, float(scale), _ptr(workspace),
-                              workspace.numel(), _ptr(status), _stream(stream)),
-        "mars_attn_chunk")
+    _need_cuda(q, "q")
+    dev, raw = _target(stream)
+    total, hq, d = q.shape
+    hkv = k.shape[1]
+    batch = _batch(cu_seqlens)
+    pages = k_pool.shape[0]
+    pool = (pages, hkv, PAGE_SIZE, d)
+    qp, qs = _rows(q, "q", (total, hq, d), dev)
+    kp, ks = _rows(k, "k", (total, hkv, d), dev)
+    vp, vs = _rows(v, "v", (total, hkv, d), dev)
+    table, width = _table(block_table, batch, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _rc(lib().mars_attn_chunk(
+        qp, kp, vp, _ptr(cu_seqlens, "cu_seqlens", _I32, (batch + 1,), dev),
+        _ptr(k_pool, "k_pool", _BF16, pool, dev), _ptr(v_pool, "v_pool", _BF16, pool, dev), pages,
+        table, width, _ptr(seq_lens, "seq_lens", _I32, (batch,), dev), max_len_hint,
+        _ptr(o, "o", _BF16, (total, hq, d), dev), batch, total, hq, hkv, d, PAGE_SIZE, qs, ks, vs,
+        scale, ws, ws_bytes, _opt(status, "status", _I32, (1,), dev), raw), "mars_attn_chunk")
 
 
 def mars_kv_append(k, v, cu_seqlens, seq_lens, block_table, k_pool, v_pool, new_lens=None,
                    slots=None, status=None, stream=None):
     """Copy each sequence's new K/V rows to its pages, after its seq_lens[s] cached tokens;
     new_lens [batch] and slots [total] (int32) are optional outputs (see include/mars.h)."""
+    _need_cuda(k, "k")
+    dev, raw = _target(stream)
     total, hkv, d = k.shape
-    num_pages = k_pool.shape[0]
-    ks, vs = _check_rows(k, "k", (total, hkv, d)), _check_rows(v, "v", (total, hkv, d))
-    _check(cu_seqlens, "cu_seqlens", torch.int32)
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens must hold batch + 1 boundaries")
-    batch = cu_seqlens.shape[0] - 1
-    _check(seq_lens, "seq_lens", torch.int32, (batch,))
-    _check(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [{batch}, "
-                         "max_pages]")
-    _check(k_pool, "k_pool", torch.bfloat16, (num_pages, hkv, PAGE_SIZE, d))
-    _check(v_pool, "v_pool", torch.bfloat16, (num_pages, hkv, PAGE_SIZE, d))
-    if new_lens is not None:
-        _check(new_lens, "new_lens", torch.int32, (batch,))
-    if slots is not None:
-        _check(slots, "slots", torch.int32, (total,))
-    if status is not None:
-        _check(status, "status", torch.int32, (1,))
-    _check_one_device(stream, k=k, v=v, cu_seqlens=cu_seqlens, seq_lens=seq_lens,
-                      block_table=block_table, k_pool=k_pool, v_pool=v_pool, new_lens=new_lens,
-                      slots=slots, status=status)
-    _rc(lib().mars_kv_append(_ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(new_lens),
-                             _ptr(block_table), block_table.shape[1], _ptr(k_pool), _ptr(v_pool),
-                             num_pages, _ptr(slots), batch, total, hkv, d, PAGE_SIZE, ks, vs,
-                             _ptr(status), _stream(stream)), "mars_kv_append")
+    batch = _batch(cu_seqlens)
+    pages = k_pool.shape[0]
+    pool = (pages, hkv, PAGE_SIZE, d)
+    kp, ks = _rows(k, "k", (total, hkv, d), dev)
+    vp, vs = _rows(v, "v", (total, hkv, d), dev)
+    table, width = _table(block_table, batch, dev)
+    _rc(lib().mars_kv_append(
+        kp, vp, _ptr(cu_seqlens, "cu_seqlens", _I32, (batch + 1,), dev),
+        _ptr(seq_lens, "seq_lens", _I32, (batch,), dev),
+        _opt(new_lens, "new_lens", _I32, (batch,), dev), table, width,
+        _ptr(k_pool, "k_pool", _BF16, pool, dev), _ptr(v_pool, "v_pool", _BF16, pool, dev), pages,
+        _opt(slots, "slots", _I32, (total,), dev), batch, total, hkv, d, PAGE_SIZE, ks, vs,
+        _opt(status, "status", _I32, (1,), dev), raw), "mars_kv_append")

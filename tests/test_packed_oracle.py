@@ -205,14 +205,21 @@ def test_bindings_refuse_host_tensors(L):
     (bf(5, 2, 64), "shape")], ids=["heads", "elements", "pitch", "broadcast", "shape"])
 def test_row_layouts_that_are_refused(monkeypatch, t, match):
     class Host:                       # a host tensor that says it is on the GPU
+        is_cuda = True
+
         def __init__(self, t):
             self.t = t
 
         def __getattr__(self, n):
-            return torch.device("cuda") if n == "device" else getattr(self.t, n)
+            return getattr(self.t, n)
 
-    monkeypatch.setattr(packed, "torch", type("T", (), {"Tensor": Host, "bfloat16": torch.bfloat16}))
+        def get_device(self):
+            return 0
+
+    monkeypatch.setattr(packed, "torch", type("T", (), {"Tensor": Host}))
     with pytest.raises(ValueError, match=match):
-        packed._check_rows(Host(t), "q", (4, 2, 64))
-    assert packed._check_rows(Host(bf(4, 6, 64)[:, 1:3]), "q", (4, 2, 64)) == 384
-    assert packed._check_rows(Host(bf(1, 2, 64)), "q", (1, 2, 64)) == 128
+        packed._rows(Host(t), "q", (4, 2, 64), 0)
+    with pytest.raises(ValueError, match="cuda:0"):
+        packed._rows(Host(bf(4, 2, 64)), "q", (4, 2, 64), 1)
+    assert packed._rows(Host(bf(4, 6, 64)[:, 1:3]), "q", (4, 2, 64), 0)[1] == 384
+    assert packed._rows(Host(bf(1, 2, 64)), "q", (1, 2, 64), 0)[1] == 128
