@@ -130,9 +130,10 @@ struct PackedAttn {
   int32_t* status;
 };
 struct PackedPlan {
+  bool pair;               // two row tiles per item, persistent CTAs over a plan's list
   int gp, tpt;             // heads and tokens of a row tile
   int nsplit, split_tiles; // splits of a key list, 128-key tiles per split
-  long long ctas;
+  long long items, ctas;
   size_t ws_bytes;
 };
 // max_len: upper bound of a sequence's keys (cached and own) for which the splits are sized.

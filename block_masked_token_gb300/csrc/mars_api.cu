@@ -401,7 +401,7 @@ int packed_attn_checked(mars::PackedAttn p, int max_len, void* workspace, size_t
   if (!(p.scale > 0.f)) p.scale = 1.0f / sqrtf((float)p.d);
   if (isinf(p.scale)) return MARS_EINVAL;
   const mars::PackedPlan plan = mars::plan_packed(p.batch, p.total, p.hq, p.hkv, p.d, max_len);
-  if ((rc = grid_fits(plan.ctas))) return rc;
+  if ((rc = grid_fits(plan.items))) return rc;
   if (ws_bytes < plan.ws_bytes) return MARS_ENOSPACE;
   if (plan.ws_bytes && !workspace) return MARS_EINVAL;
   return cuda_rc(mars::launch_packed_attn(p, plan, workspace, static_cast<cudaStream_t>(stream)));

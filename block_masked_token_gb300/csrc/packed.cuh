@@ -84,6 +84,17 @@ struct Plan {
   Tile* in_order;     // gradient: by global tile index
 };
 
+// The items of a persistent CTA, by round: rounds run forwards and backwards over the CTAs, so that the costs even out.
+struct Turns {
+  int total, rounds;
+  MARS_DEV explicit Turns(int n) : total(n), rounds((n + (int)gridDim.x - 1) / (int)gridDim.x) {}
+  MARS_DEV int at(int r) const {
+    const int g = gridDim.x, c = blockIdx.x;
+    const int id = r * g + ((r & 1) ? g - 1 - c : c);
+    return id < total ? id : -1;
+  }
+};
+
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Carve a plan out of a workspace at `off` (base may be null to size it).

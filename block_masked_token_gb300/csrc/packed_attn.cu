@@ -15,6 +15,8 @@
 //
 // With few tiles and long key lists the list is cut into splits: each CTA writes an
 // unnormalised partial (m in log2 units, l, O) and a second kernel merges them.
+//
+// Where the rows are many, pair_kernel takes two row tiles per CTA instead (see there).
 #include <climits>
 
 #include "common.cuh"
@@ -76,12 +78,10 @@ struct RowsPolicy {
     if (t.prefix) {
       t.k0 = j * BKV;
       t.count = min(P - t.k0, BKV);
-      t.pmask = 0;
-      for (int i = 0; i < kPagesPerTile; ++i) {
-        const int lp = t.k0 / kPageSize + i;
-        const int e = lp < a->max_pages ? bt_row[lp] : -1;
-        if (e >= 0 && e < a->num_pages) t.pmask |= 1u << i;
-      }
+      // one page per lane (the call is warp-uniform)
+      const int lp = t.k0 / kPageSize + (threadIdx.x & (kPagesPerTile - 1));
+      const int e = lp < a->max_pages ? bt_row[lp] : -1;
+      t.pmask = __ballot_sync(0xffffffffu, e >= 0 && e < a->num_pages) & 0xffu;
       t.full = t.count == BKV && t.pmask == 0xffu;
       t.clear = !t.full;
     } else {
@@ -296,6 +296,386 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
     orow[lane + 32 * i] = flash::pack_bf16x2(acc[i].x * inv, acc[i].y * inv);
 }
 
+// ------------------------------------------------------------------------ pair kernel
+//
+// Compute-bound calls: a persistent CTA per SM runs items of two row tiles (x = 0, 1) of the
+// same sequence and KV head over one key list, each with a softmax warpgroup of its own, so
+// that the tensor pipe works for one tile while the other's softmax runs, and each K and V
+// tile is loaded once for both. Items come from a plan (packed_plan.cu), costliest first.
+//   warp 0  loader: K_0, V_0, K_1, V_1, ... through one ring of kSlots tiles
+//   warp 1  TMEM owner; loads Q and issues S_x = Q_x K_j^T
+//   warp 2  issues O_x += P_x V_j, in two halves of 64 keys as P becomes ready
+//   warps 4..7, 8..11  softmax and output of row tile 0, 1 (thread = row)
+// TMEM: S_0, S_1, O_0, O_1, 128 columns each; P_x (bf16) over the upper half of S_x. S_x of the
+// next key tile is issued when the PV of this one has read P_x; so a softmax warpgroup that
+// sees S_x knows O_x to be complete up to there, and rescales it without a wait, and its
+// first P of an item says that it has read the O of the item before.
+constexpr int kSlots = 5;
+constexpr int PAIR_THREADS = 384;
+constexpr int PAIR_WG0_REGS = 80, PAIR_SOFTMAX_REGS = 208;
+static_assert(128 * (PAIR_WG0_REGS + 2 * PAIR_SOFTMAX_REGS) <=
+                  PAIR_THREADS * (65536 / PAIR_THREADS / 8 * 8),
+              "the register split fits the launch's register pool");
+
+template <int D>
+struct PairSmem {
+  static constexpr int TILE = BKV * D * 2;             // a Q, K or V tile
+  static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE;
+  static constexpr int TOTAL = OFF_RING + kSlots * TILE + 1024;
+  static constexpr int TM_S = 0, TM_O = 2 * BKV, P_OFF = BKV / 2;
+};
+
+struct PairBar {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2];
+  uint64_t drain[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+// An item: row tiles at tokens tok0 and tok0 + tpt of a sequence, and the key tiles that each
+// sees (0: no rows).
+struct PairItem {
+  int base, n, seq, tok0, h0, kvh, P, np, keys[2], tiles;
+};
+
+MARS_DEV PairItem pair_item(const AttnArgs& a, const packed::Plan& plan, int id) {
+  PairItem it;
+  const int heads = a.hkv * a.ngrp, g = id % heads;
+  const packed::Tile t = plan.first[id / heads];
+  it.base = t.base;
+  it.n = t.n;
+  it.seq = t.id;
+  it.kvh = g / a.ngrp;
+  it.h0 = g * a.gp;
+  it.tok0 = t.tile * 2 * a.tpt;
+  const long long cached = a.seq_lens ? a.seq_lens[t.id] : 0;
+  it.P = (int)max(0LL, min(cached, (long long)a.max_pages * kPageSize));
+  it.np = (it.P + BKV - 1) / BKV;
+  for (int x = 0; x < 2; ++x) {
+    const int first = it.tok0 + x * a.tpt;
+    it.keys[x] = first < it.n ? it.np + (min(first + a.tpt, it.n) - 1) / BKV + 1 : 0;
+  }
+  it.tiles = max(it.keys[0], it.keys[1]);
+  return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kp,
+            const __grid_constant__ CUtensorMap tm_vp, AttnArgs a, packed::Plan plan) {
+  using namespace sm100;
+  using S = PairSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PairBar bar;
+  const packed::Turns turns(*plan.count * a.hkv * a.ngrp);
+  if (turns.at(0) < 0) return;                         // more CTAs than items
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* ab = &bar.abort;
+  if (threadIdx.x == 0) {
+    bar.abort = 0;
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bar.q_full[x], 1);
+      mbar_init(&bar.q_empty[x], 1);
+      mbar_init(&bar.s_full[x], 1);
+      mbar_init(&bar.p_full[x][0], 128);
+      mbar_init(&bar.p_full[x][1], 128);
+      mbar_init(&bar.pv_done[x], 1);
+      mbar_init(&bar.drain[x], 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem_base, 0);
+
+  if (warp < 4) {
+    regs_lower<PAIR_WG0_REGS>();
+    if (warp == 0) {
+      // ------------------------------------------------------------------- loader
+      int g = 0, flags = 0;                            // tiles loaded (K and V counted apart)
+      bool ok = true;
+      for (int r = 0; r < turns.rounds && ok; ++r) {
+        const int id = turns.at(r);
+        if (id < 0) continue;
+        const PairItem it = pair_item(a, plan, id);
+        if (a.seq_lens && a.seq_lens[it.seq] != it.P) flags |= MARS_ST_OVERFLOW;
+        const int32_t* bt = a.block_table ? a.block_table + (size_t)it.seq * a.max_pages : nullptr;
+        // this lane's page of prefix tile j, read one tile ahead
+        auto entry = [&](int j) -> int {
+          const int lp = j * kPagesPerTile + lane;
+          return j < it.np && lane < kPagesPerTile && lp < a.max_pages ? bt[lp] : -1;
+        };
+        int next = entry(0);
+        for (int j = 0; j < it.tiles && ok; ++j) {
+          const int e = next;
+          next = entry(j + 1);
+          for (int v = 0; v < 2; ++v, ++g) {
+            const int st = g % kSlots;
+            int good = 1;
+            if (lane == 0) {
+              good = mbar_wait(&bar.empty[st], ((g / kSlots) & 1) ^ 1, ab, a.status);
+              if (good) mbar_arrive_expect_tx(&bar.full[st], S::TILE);
+            }
+            ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+            if (!ok) break;
+            uint8_t* dst = smem + S::OFF_RING + st * S::TILE;
+            if (j < it.np) {
+              if (lane < kPagesPerTile) {
+                // as in packed_rows_kernel: a page that may not be read loads page 0
+                int page = 0;
+                if (e >= 0 && e < a.num_pages)
+                  page = e;
+                else if (j * BKV + lane * kPageSize < it.P)
+                  flags |= MARS_ST_NOPAGE;
+                const int row = a.num_pages > 0 ? (page * a.hkv + it.kvh) * kPageSize : kPageSize;
+                for (int x = 0; x < D / 64; ++x)
+                  tma_load_2d(dst + x * (BKV * 128) + lane * (kPageSize * 128), v ? &tm_vp : &tm_kp,
+                              &bar.full[st], x * 64, row);
+              }
+            } else if (lane == 0) {
+              for (int x = 0; x < D / 64; ++x)
+                tma_load_3d(dst + x * (BKV * 128), v ? &tm_v : &tm_k, &bar.full[st], x * 64, it.kvh,
+                            it.base + (j - it.np) * BKV);
+            }
+          }
+        }
+      }
+      if (flags && a.status) atomicOr(a.status, flags);
+      // wait (bounded) for the copies still in flight
+      if (lane == 0)
+        for (int k = 1; k <= kSlots && g - k >= 0; ++k)
+          mbar_wait(&bar.full[(g - k) % kSlots], ((g - k) / kSlots) & 1, nullptr, a.status);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------- Q loads, S = Q K^T
+      if (lane == 0) {
+        const uint32_t idesc = idesc_bf16_f32(BQ, BKV, false);
+        int g = 0, done[2] = {0, 0}, items[2] = {0, 0};   // key tiles, tiles and items per x
+        bool ok = true;
+        for (int r = 0; r < turns.rounds && ok; ++r) {
+          const int id = turns.at(r);
+          if (id < 0) continue;
+          const PairItem it = pair_item(a, plan, id);
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (!it.keys[x]) continue;
+            // Q_x is replaced once the S MMAs of its previous item have completed
+            if (items[x] && !(ok = mbar_wait(&bar.q_empty[x], (items[x] - 1) & 1, ab, a.status)))
+              break;
+            mbar_arrive_expect_tx(&bar.q_full[x], a.gp * a.tpt * 128 * (D / 64));
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(smem + S::OFF_Q + x * S::TILE + c * (BQ * 128), &tm_q, &bar.q_full[x], c * 64,
+                          it.h0, it.base + it.tok0 + x * a.tpt);
+            ++items[x];
+          }
+          for (int j = 0; j < it.tiles && ok; ++j, ++g) {
+            const int st = (2 * g) % kSlots;
+            if (!(ok = mbar_wait(&bar.full[st], (2 * g / kSlots) & 1, ab, a.status))) break;
+            const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_RING + st * S::TILE), 16, 1024);
+            for (int x = 0; x < 2; ++x) {
+              if (j >= it.keys[x]) continue;
+              ok = (j > 0 || mbar_wait(&bar.q_full[x], (items[x] - 1) & 1, ab, a.status)) &&
+                   // the PV of this row tile's previous key tile has read P out of the buffer
+                   (done[x] == 0 || mbar_wait(&bar.pv_done[x], (done[x] - 1) & 1, ab, a.status));
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t qd = sdesc_sw128(smem_u32(smem + S::OFF_Q + x * S::TILE), 16, 1024);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * (BQ * 128) + (k & 3) * 32;
+                mma_bf16_ss(tmem + S::TM_S + x * BKV, sdesc_advance(qd, off), sdesc_advance(kd, off),
+                            idesc, k != 0);
+              }
+              mma_commit(&bar.s_full[x]);
+              if (j == it.keys[x] - 1) mma_commit(&bar.q_empty[x]);
+              ++done[x];
+            }
+            if (!ok) break;
+            mma_commit(&bar.empty[st]);
+          }
+        }
+        mma_commit(&bar.drain[0]);
+        mbar_wait(&bar.drain[0], 0, nullptr, a.status);
+        for (int x = 0; x < 2; ++x)
+          if (items[x]) mbar_wait(&bar.q_full[x], (items[x] - 1) & 1, nullptr, a.status);
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------------ O += P V
+      if (lane == 0) {
+        const uint32_t idesc = idesc_bf16_f32(BQ, D, true);
+        int g = 0, done[2] = {0, 0};
+        bool ok = true;
+        for (int r = 0; r < turns.rounds && ok; ++r) {
+          const int id = turns.at(r);
+          if (id < 0) continue;
+          const PairItem it = pair_item(a, plan, id);
+          for (int j = 0; j < it.tiles && ok; ++j, ++g) {
+            const int st = (2 * g + 1) % kSlots;
+            if (!(ok = mbar_wait(&bar.full[st], ((2 * g + 1) / kSlots) & 1, ab, a.status))) break;
+            const uint64_t vd = sdesc_sw128(smem_u32(smem + S::OFF_RING + st * S::TILE), BKV * 128, 1024);
+            for (int x = 0; x < 2 && ok; ++x) {
+              if (j >= it.keys[x]) continue;
+              for (int h = 0; h < 2; ++h) {
+                if (!(ok = mbar_wait(&bar.p_full[x][h], done[x] & 1, ab, a.status))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kq = 0; kq < BKV / 32; ++kq) {
+                  const int k = (BKV / 32) * h + kq;
+                  mma_bf16_ts(tmem + S::TM_O + x * BKV, tmem + S::TM_S + x * BKV + S::P_OFF + k * 8,
+                              sdesc_advance(vd, k * 2048), idesc, (j | k) != 0);
+                }
+              }
+              if (!ok) break;
+              mma_commit(&bar.pv_done[x]);
+              ++done[x];
+            }
+            if (!ok) break;
+            mma_commit(&bar.empty[st]);
+          }
+        }
+        mma_commit(&bar.drain[1]);
+        mbar_wait(&bar.drain[1], 0, nullptr, a.status);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax, output
+    regs_raise<PAIR_SOFTMAX_REGS>();
+    const int x = warp >= 8, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    auto warp_wait = [&](uint64_t* b, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(b, parity, ab, a.status));
+    };
+    const uint32_t s_addr = tmem + S::TM_S + x * BKV + lane_off;
+    const uint32_t o_addr = tmem + S::TM_O + x * BKV + lane_off;
+    int g = 0, done = 0;
+    bool ok = true;
+    for (int r = 0; r < turns.rounds && ok; ++r) {
+      const int id = turns.at(r);
+      if (id < 0) continue;
+      const PairItem it = pair_item(a, plan, id);
+      const int tiles = it.keys[x];
+      if (tiles == 0) {
+        g += it.tiles;
+        continue;
+      }
+      RowsPolicy<D> pol;
+      pol.a = &a;
+      pol.bt_row = a.block_table ? a.block_table + (size_t)it.seq * a.max_pages : nullptr;
+      pol.base = it.base;
+      pol.n = it.n;
+      pol.tok0 = it.tok0 + x * a.tpt;
+      pol.P = it.P;
+      pol.np = it.np;
+      pol.h0 = it.h0;
+      pol.j0 = 0;
+      pol.split = 0;
+      pol.last_tok = min(it.tok0 + 2 * a.tpt, it.n) - 1;   // of the item: V rows that neither tile reads
+      const bool rv = pol.row_valid(row);
+      const flash::RowVis vis = pol.row_vis(row);
+      float m = -INFINITY, l = 0.f;
+      typename RowsPolicy<D>::Tile next = pol.tile(0);
+      for (int j = 0; j < tiles; ++j, ++done) {
+        const typename RowsPolicy<D>::Tile tile = next;
+        if (j + 1 < tiles) next = pol.tile(j + 1);
+        if (!(ok = warp_wait(&bar.s_full[x], done & 1))) break;
+        tc_fence_after();
+        uint32_t v[BKV];
+#pragma unroll
+        for (int c = 0; c < BKV / 32; ++c)
+          tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + c * 32));
+        tmem_ld_wait();
+        if (!rv || !tile.full) {
+          const flash::ColRange cr = rv ? pol.cols(vis, tile) : flash::ColRange{0, BKV, -1, 0u};
+#pragma unroll
+          for (int c = 0; c < BKV / 32; ++c) {
+            const uint32_t mk = flash::chunk_mask(cr, c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((mk >> e) & 1u)) v[c * 32 + e] = 0xff800000u;
+          }
+        }
+        const float tmax = flash::row_max_log2(v, a.scale_log2);
+        // lazy rescale, as in flash_tc.cuh: only when the maximum grows by more than 2^8
+        const bool raise = tmax > m + flash::kRescaleLog2;
+        const bool rescale = raise && m != -INFINITY;
+        if (__any_sync(0xffffffffu, rescale)) {
+          const float alpha = rescale ? flash::ex2_approx(m - tmax) : 1.f;
+          l *= alpha;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(o_addr + c * 32, o);
+          }
+          tmem_st_wait();
+        }
+        if (raise) m = tmax;
+        const float neg_m = (m == -INFINITY) ? 0.f : -m;
+        if (tile.clear) {
+          // V rows that no row of the item may read (flash_tc.cuh, kClearRows); both row tiles'
+          // threads write the same zeros
+          const int gv = 2 * (g + j) + 1, st = gv % kSlots;
+          if (!(ok = warp_wait(&bar.full[st], (gv / kSlots) & 1))) break;
+          if (!pol.key_read(tile, row)) {
+            uint8_t* vr = smem + S::OFF_RING + st * S::TILE + row * 128;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint4*>(vr + c * (BKV * 128) + q * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t packed[32];
+          flash::exp2_pack64(v, h * 64, a.scale_log2, neg_m, packed, acc);
+          tmem_st32(s_addr + S::P_OFF + h * 32, packed);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive_warp(&bar.p_full[x][h]);
+        }
+        l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+      }
+      if (!ok) break;
+      g += it.tiles;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (!(ok = warp_wait(&bar.pv_done[x], (done - 1) & 1))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + c * 32, o);
+        tmem_ld_wait();
+        if (rv) pol.store_chunk(row, c * 32, o, inv, m, l);
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 // Tensor map of [total][heads][D] rows with a row pitch of `stride` elements.
 bool map_rows(CUtensorMap* m, const void* base, int d, int heads, int total, long long stride,
               uint32_t box_heads, uint32_t box_rows) {
@@ -307,7 +687,7 @@ bool map_rows(CUtensorMap* m, const void* base, int d, int heads, int total, lon
 
 template <int D>
 cudaError_t launch_rows(const PackedAttn& p, const PackedPlan& plan, AttnArgs& a,
-                        cudaStream_t stream) {
+                        void* workspace, cudaStream_t stream) {
   using S = flash::Smem<D, 0, kVStages>;
   static_assert(S::TOTAL + sizeof(flash::Barriers) <= 227 * 1024, "layout fits shared memory");
   CUtensorMap tq, tk, tv, tkp, tvp;
@@ -327,6 +707,23 @@ cudaError_t launch_rows(const PackedAttn& p, const PackedPlan& plan, AttnArgs& a
     if (!encode_tmap_bf16(&tkp, any ? p.k_pool : p.q, 2, dims, str, box) ||
         !encode_tmap_bf16(&tvp, any ? p.v_pool : p.q, 2, dims, str, box))
       return cudaErrorInvalidValue;
+  }
+  if (plan.pair) {
+    using SP = PairSmem<D>;
+    static_assert(SP::TOTAL + sizeof(PairBar) <= 227 * 1024, "pair layout fits shared memory");
+    static std::atomic<int> attr_pair[64];
+    cudaError_t e = set_smem_limit_once(pair_kernel<D>, SP::TOTAL, attr_pair);
+    if (e != cudaSuccess) return e;
+    size_t off = 0;
+    const packed::Plan list =
+        packed::carve_plan(workspace, off, p.batch, p.total, 2 * plan.tpt, false);
+    e = packed::launch_plan(list, p.cu, p.seq_lens, a.max_pages, p.batch, p.total, 2 * plan.tpt,
+                            p.status, stream);
+    if (e != cudaSuccess) return e;
+    pair_kernel<D><<<(unsigned)plan.ctas, PAIR_THREADS, SP::TOTAL, stream>>>(tq, tk, tv, tkp, tvp,
+                                                                             a, list);
+    count_launches(1);
+    return cudaGetLastError();
   }
   static std::atomic<int> attr[64];
   const cudaError_t ea = set_smem_limit_once(packed_rows_kernel<D>, S::TOTAL, attr);
@@ -351,6 +748,18 @@ PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len
   p.tpt = BQ / p.gp;
   const long long items = packed::max_tiles(batch, total, p.tpt) * hkv * (G / p.gp);
   const int tiles = (max_len + BKV - 1) / BKV + 1;
+  // Two row tiles per item where sequences have more rows than one on average and the items
+  // fill the GPU.
+  const long long pairs = packed::max_tiles(batch, total, 2 * p.tpt) * hkv * (G / p.gp);
+  if (total > (long long)batch * p.tpt && pairs >= num_sms()) {
+    p.pair = true;
+    p.nsplit = 1;
+    p.split_tiles = tiles;
+    p.items = pairs;
+    p.ctas = num_sms();
+    packed::carve_plan(nullptr, p.ws_bytes, batch, total, 2 * p.tpt, false);
+    return p;
+  }
   long long nsplit = 1;
   if (items < num_sms()) {
     nsplit = num_sms() / items;
@@ -359,7 +768,7 @@ PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len
   }
   p.split_tiles = (int)((tiles + nsplit - 1) / nsplit);
   p.nsplit = (tiles + p.split_tiles - 1) / p.split_tiles;
-  p.ctas = items * p.nsplit;
+  p.items = p.ctas = items * p.nsplit;
   p.ws_bytes =
       p.nsplit > 1 ? (size_t)p.nsplit * total * hq * (size_t)(d + 4) * sizeof(float) : 0;
   return p;
@@ -387,7 +796,8 @@ cudaError_t launch_packed_attn(const PackedAttn& p, const PackedPlan& plan, void
   a.lse = p.lse;
   a.part = static_cast<float*>(workspace);
   a.status = p.status;
-  return p.d == 64 ? launch_rows<64>(p, plan, a, stream) : launch_rows<128>(p, plan, a, stream);
+  return p.d == 64 ? launch_rows<64>(p, plan, a, workspace, stream)
+                   : launch_rows<128>(p, plan, a, workspace, stream);
 }
 
 }  // namespace mars

@@ -38,6 +38,7 @@ namespace {
 
 using namespace sm100;
 using packed::Tile;
+using packed::Turns;
 
 constexpr int GT = 128;                 // rows per key tile and per query tile
 constexpr int MATH_WARPS = 8;           // two per TMEM lane quadrant, 64 columns each
@@ -108,17 +109,6 @@ MARS_DEV void clear_rows(uint8_t* tile, int first, int lo, int hi, int id, int t
         make_uint4(0, 0, 0, 0);
   }
 }
-
-// Item r of this CTA: rounds run forwards and backwards over the CTAs, so that the costs even out.
-struct Turns {
-  int total, rounds;
-  MARS_DEV explicit Turns(int n) : total(n), rounds((n + (int)gridDim.x - 1) / (int)gridDim.x) {}
-  MARS_DEV int at(int r) const {
-    const int g = gridDim.x, c = blockIdx.x;
-    const int id = r * g + ((r & 1) ? g - 1 - c : c);
-    return id < total ? id : -1;
-  }
-};
 
 // ---------------------------------------------------------------------- dK and dV
 
