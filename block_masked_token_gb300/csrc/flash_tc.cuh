@@ -384,14 +384,16 @@ MARS_DEV float max3f(float a, float b, float c) {
   return d;
 }
 
-// Maximum of one row's 128 S values (fp32 bits), scaled to log2 units: 8 independent
-// chains of three-input max, then a short tree.
-MARS_DEV float row_max_log2(const uint32_t (&r)[BKV], float scale_log2) {
+// Maximum of N S values of one row (fp32 bits), scaled to log2 units: 8 independent chains of
+// three-input max, then a short tree.
+template <int N>
+MARS_DEV float row_max_log2(const uint32_t (&r)[N], float scale_log2) {
+  static_assert(N % 16 == 0, "pairs of 8 chains");
   float pm[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) pm[i] = fmaxf(__uint_as_float(r[i]), __uint_as_float(r[8 + i]));
 #pragma unroll
-  for (int k = 2; k < BKV / 8; k += 2)
+  for (int k = 2; k < N / 8; k += 2)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       pm[i] = max3f(pm[i], __uint_as_float(r[k * 8 + i]), __uint_as_float(r[(k + 1) * 8 + i]));
@@ -402,7 +404,8 @@ MARS_DEV float row_max_log2(const uint32_t (&r)[BKV], float scale_log2) {
 // P = exp2(S * scale_log2 - m) for 64 S values starting at r[c0], packed as 32 bf16 pairs
 // (even key in the low half); the fp32 values are added to acc (two lanes per float2).
 // The scale-and-shift and the sums run as packed f32x2 operations.
-MARS_DEV void exp2_pack64(const uint32_t (&r)[BKV], int c0, float scale_log2, float neg_m,
+template <int N>
+MARS_DEV void exp2_pack64(const uint32_t (&r)[N], int c0, float scale_log2, float neg_m,
                           uint32_t (&packed)[32], float2 (&acc)[2]) {
   const float2 sc = make_float2(scale_log2, scale_log2), sh = make_float2(neg_m, neg_m);
 #pragma unroll

@@ -69,7 +69,11 @@ struct RowsPolicy {
     bool prefix, full, clear;
   };
   MARS_DEV int token(int row) const { return tok0 + row / a->gp; }
-  MARS_DEV bool row_valid(int row) const { return row < a->gp * a->tpt && token(row) < n; }
+  // A row without a token (the tile's last rows, the tokens past the sequence) computes
+  // something that is not stored; masking it would cost its whole warp the masks of every tile
+  // (550 of 3900 cycles per key tile with 7 heads x 18 tokens = 126 rows).
+  MARS_DEV bool row_valid(int) const { return true; }
+  MARS_DEV bool has_token(int row) const { return row < a->gp * a->tpt && token(row) < n; }
   MARS_DEV flash::RowVis row_vis(int row) const { return {token(row) + 1, 0, -1}; }
   MARS_DEV Tile tile(int jl) const {
     Tile t;
@@ -101,6 +105,7 @@ struct RowsPolicy {
   }
   MARS_DEV void store_chunk(int row, int col, const uint32_t (&r)[32], float inv, float m,
                             float l) const {
+    if (!has_token(row)) return;
     const size_t tok = (size_t)base + token(row);
     const int h = h0 + row % a->gp;
     if (a->nsplit == 1) {
@@ -174,7 +179,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int n_total = end - pol.j0;
   if (n_total <= 0) {                  // no keys in this split: empty partials
     for (int r = threadIdx.x; r < BQ; r += blockDim.x)
-      if (pol.row_valid(r)) {
+      if (pol.has_token(r)) {
         float* rec = a.part + (((size_t)sp * a.total + sq.base + pol.token(r)) * a.hq + pol.h0 +
                                r % a.gp) * (D + 4);
         rec[0] = -INFINITY;
@@ -304,13 +309,16 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
 // tile is loaded once for both. Items come from a plan (packed_plan.cu), costliest first.
 //   warp 0  loader: K_0, V_0, K_1, V_1, ... through one ring of kSlots tiles
 //   warp 1  TMEM owner; loads Q and issues S_x = Q_x K_j^T
-//   warp 2  issues O_x += P_x V_j, in two halves of 64 keys as P becomes ready
+//   warp 2  issues O_x += P_x V_j
 //   warps 4..7, 8..11  softmax and output of row tile 0, 1 (thread = row)
-// TMEM: S_0, S_1, O_0, O_1, 128 columns each; P_x (bf16) over the upper half of S_x. S_x of the
-// next key tile is issued when the PV of this one has read P_x; so a softmax warpgroup that
-// sees S_x knows O_x to be complete up to there, and rescales it without a wait, and its
-// first P of an item says that it has read the O of the item before.
+// They work in steps of 64 keys. One step's chain, S, its softmax, PV and the hand-offs
+// between them, takes about 1,700 cycles, of which the tensor pipe works a third: four steps
+// have to be in flight, two per row tile, and TMEM holds just that many (two S buffers of 64
+// columns per row tile, P in bf16 over the upper half of each, and two O of 128). With 128-key
+// steps, one in flight per row tile, a pair of tiles took 4,000 cycles instead of 2,048.
+// A row tile's first P of an item also says that its warps have read the O of the item before.
 constexpr int kSlots = 5;
+constexpr int kStep = 64;                        // keys per step
 constexpr int PAIR_THREADS = 384;
 constexpr int PAIR_WG0_REGS = 80, PAIR_SOFTMAX_REGS = 208;
 static_assert(128 * (PAIR_WG0_REGS + 2 * PAIR_SOFTMAX_REGS) <=
@@ -322,21 +330,23 @@ struct PairSmem {
   static constexpr int TILE = BKV * D * 2;             // a Q, K or V tile
   static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE;
   static constexpr int TOTAL = OFF_RING + kSlots * TILE + 1024;
-  static constexpr int TM_S = 0, TM_O = 2 * BKV, P_OFF = BKV / 2;
+  static constexpr int TM_S = 0, TM_O = 2 * BKV, P_OFF = kStep / 2;
 };
 
 struct PairBar {
   uint64_t full[kSlots], empty[kSlots];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], pv_done[2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];     // [row tile][buffer]
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
 };
 
-// An item: row tiles at tokens tok0 and tok0 + tpt of a sequence, and the key tiles that each
-// sees (0: no rows).
+// An item: row tiles at tokens tok0 and tok0 + tpt of a sequence, the steps that each takes (0:
+// no rows; the last step is left out where a tile's own keys end in the first half of a key
+// tile), and the key tiles that are loaded.
 struct PairItem {
-  int base, n, seq, tok0, h0, kvh, P, np, keys[2], tiles;
+  int base, n, seq, tok0, h0, kvh, P, np, steps[2], tiles;
 };
 
 MARS_DEV PairItem pair_item(const AttnArgs& a, const packed::Plan& plan, int id) {
@@ -354,9 +364,9 @@ MARS_DEV PairItem pair_item(const AttnArgs& a, const packed::Plan& plan, int id)
   it.np = (it.P + BKV - 1) / BKV;
   for (int x = 0; x < 2; ++x) {
     const int first = it.tok0 + x * a.tpt;
-    it.keys[x] = first < it.n ? it.np + (min(first + a.tpt, it.n) - 1) / BKV + 1 : 0;
+    it.steps[x] = first < it.n ? 2 * it.np + (min(first + a.tpt, it.n) - 1) / kStep + 1 : 0;
   }
-  it.tiles = max(it.keys[0], it.keys[1]);
+  it.tiles = (max(it.steps[0], it.steps[1]) + 1) / 2;
   return it;
 }
 
@@ -384,10 +394,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar.q_full[x], 1);
       mbar_init(&bar.q_empty[x], 1);
-      mbar_init(&bar.s_full[x], 1);
-      mbar_init(&bar.p_full[x][0], 128);
-      mbar_init(&bar.p_full[x][1], 128);
-      mbar_init(&bar.pv_done[x], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar.s_full[x][i], 1);
+        mbar_init(&bar.p_full[x][i], 128);
+        mbar_init(&bar.pv_done[x][i], 1);
+      }
       mbar_init(&bar.drain[x], 1);
     }
     fence_barrier_init();
@@ -461,16 +472,16 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------- Q loads, S = Q K^T
-      if (lane == 0) {
-        const uint32_t idesc = idesc_bf16_f32(BQ, BKV, false);
-        int g = 0, done[2] = {0, 0}, items[2] = {0, 0};   // key tiles, tiles and items per x
+      if (elect_one()) {
+        const uint32_t idesc = idesc_bf16_f32(BQ, kStep, false);
+        int g = 0, done[2] = {0, 0}, items[2] = {0, 0};   // key tiles; steps and items per x
         bool ok = true;
         for (int r = 0; r < turns.rounds && ok; ++r) {
           const int id = turns.at(r);
           if (id < 0) continue;
           const PairItem it = pair_item(a, plan, id);
           for (int x = 0; x < 2 && ok; ++x) {
-            if (!it.keys[x]) continue;
+            if (!it.steps[x]) continue;
             // Q_x is replaced once the S MMAs of its previous item have completed
             if (items[x] && !(ok = mbar_wait(&bar.q_empty[x], (items[x] - 1) & 1, ab, a.status)))
               break;
@@ -484,22 +495,24 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int st = (2 * g) % kSlots;
             if (!(ok = mbar_wait(&bar.full[st], (2 * g / kSlots) & 1, ab, a.status))) break;
             const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_RING + st * S::TILE), 16, 1024);
-            for (int x = 0; x < 2; ++x) {
-              if (j >= it.keys[x]) continue;
-              ok = (j > 0 || mbar_wait(&bar.q_full[x], (items[x] - 1) & 1, ab, a.status)) &&
-                   // the PV of this row tile's previous key tile has read P out of the buffer
-                   (done[x] == 0 || mbar_wait(&bar.pv_done[x], (done[x] - 1) & 1, ab, a.status));
+            for (int hx = 0; hx < 4; ++hx) {
+              const int h = hx >> 1, x = hx & 1, u = 2 * j + h;
+              if (u >= it.steps[x]) continue;
+              const int c = done[x], b = c & 1;
+              ok = (u > 0 || mbar_wait(&bar.q_full[x], (items[x] - 1) & 1, ab, a.status)) &&
+                   // the PV of two steps before has read P out of the buffer
+                   (c < 2 || mbar_wait(&bar.pv_done[x][b], ((c >> 1) - 1) & 1, ab, a.status));
               if (!ok) break;
               tc_fence_after();
               const uint64_t qd = sdesc_sw128(smem_u32(smem + S::OFF_Q + x * S::TILE), 16, 1024);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = (k >> 2) * (BQ * 128) + (k & 3) * 32;
-                mma_bf16_ss(tmem + S::TM_S + x * BKV, sdesc_advance(qd, off), sdesc_advance(kd, off),
-                            idesc, k != 0);
+                mma_bf16_ss(tmem + S::TM_S + x * BKV + b * kStep, sdesc_advance(qd, off),
+                            sdesc_advance(kd, off + h * (kStep * 128)), idesc, k != 0);
               }
-              mma_commit(&bar.s_full[x]);
-              if (j == it.keys[x] - 1) mma_commit(&bar.q_empty[x]);
+              mma_commit(&bar.s_full[x][b]);
+              if (u == it.steps[x] - 1) mma_commit(&bar.q_empty[x]);
               ++done[x];
             }
             if (!ok) break;
@@ -513,7 +526,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------------ O += P V
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t idesc = idesc_bf16_f32(BQ, D, true);
         int g = 0, done[2] = {0, 0};
         bool ok = true;
@@ -525,20 +538,17 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int st = (2 * g + 1) % kSlots;
             if (!(ok = mbar_wait(&bar.full[st], ((2 * g + 1) / kSlots) & 1, ab, a.status))) break;
             const uint64_t vd = sdesc_sw128(smem_u32(smem + S::OFF_RING + st * S::TILE), BKV * 128, 1024);
-            for (int x = 0; x < 2 && ok; ++x) {
-              if (j >= it.keys[x]) continue;
-              for (int h = 0; h < 2; ++h) {
-                if (!(ok = mbar_wait(&bar.p_full[x][h], done[x] & 1, ab, a.status))) break;
-                tc_fence_after();
+            for (int hx = 0; hx < 4; ++hx) {
+              const int h = hx >> 1, x = hx & 1, u = 2 * j + h;
+              if (u >= it.steps[x]) continue;
+              const int c = done[x], b = c & 1;
+              if (!(ok = mbar_wait(&bar.p_full[x][b], (c >> 1) & 1, ab, a.status))) break;
+              tc_fence_after();
 #pragma unroll
-                for (int kq = 0; kq < BKV / 32; ++kq) {
-                  const int k = (BKV / 32) * h + kq;
-                  mma_bf16_ts(tmem + S::TM_O + x * BKV, tmem + S::TM_S + x * BKV + S::P_OFF + k * 8,
-                              sdesc_advance(vd, k * 2048), idesc, (j | k) != 0);
-                }
-              }
-              if (!ok) break;
-              mma_commit(&bar.pv_done[x]);
+              for (int k = 0; k < kStep / 16; ++k)
+                mma_bf16_ts(tmem + S::TM_O + x * BKV, tmem + S::TM_S + x * BKV + b * kStep + S::P_OFF + k * 8,
+                            sdesc_advance(vd, h * (kStep * 128) + k * 2048), idesc, (u | k) != 0);
+              mma_commit(&bar.pv_done[x][b]);
               ++done[x];
             }
             if (!ok) break;
@@ -565,8 +575,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       const int id = turns.at(r);
       if (id < 0) continue;
       const PairItem it = pair_item(a, plan, id);
-      const int tiles = it.keys[x];
-      if (tiles == 0) {
+      const int steps = it.steps[x];
+      if (steps == 0) {
         g += it.tiles;
         continue;
       }
@@ -582,56 +592,70 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       pol.j0 = 0;
       pol.split = 0;
       pol.last_tok = min(it.tok0 + 2 * a.tpt, it.n) - 1;   // of the item: V rows that neither tile reads
-      const bool rv = pol.row_valid(row);
       const flash::RowVis vis = pol.row_vis(row);
       float m = -INFINITY, l = 0.f;
-      typename RowsPolicy<D>::Tile next = pol.tile(0);
-      for (int j = 0; j < tiles; ++j, ++done) {
-        const typename RowsPolicy<D>::Tile tile = next;
-        if (j + 1 < tiles) next = pol.tile(j + 1);
-        if (!(ok = warp_wait(&bar.s_full[x], done & 1))) break;
+      typename RowsPolicy<D>::Tile tile, next = pol.tile(0);
+      for (int u = 0; u < steps; ++u, ++done) {
+        const int h = u & 1, b = done & 1;
+        if (h == 0) {
+          tile = next;
+          if (u + 2 < steps) next = pol.tile(u / 2 + 1);
+        }
+        const uint32_t sb = s_addr + b * kStep;
+        if (!(ok = warp_wait(&bar.s_full[x][b], (done >> 1) & 1))) break;
         tc_fence_after();
-        uint32_t v[BKV];
+        uint32_t v[kStep];
 #pragma unroll
-        for (int c = 0; c < BKV / 32; ++c)
-          tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + c * 32));
+        for (int c = 0; c < kStep / 32; ++c)
+          tmem_ld32(sb + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + c * 32));
         tmem_ld_wait();
-        if (!rv || !tile.full) {
-          const flash::ColRange cr = rv ? pol.cols(vis, tile) : flash::ColRange{0, BKV, -1, 0u};
+        if (!tile.full) {
+          const flash::ColRange cr = pol.cols(vis, tile);
 #pragma unroll
-          for (int c = 0; c < BKV / 32; ++c) {
-            const uint32_t mk = flash::chunk_mask(cr, c);
+          for (int c = 0; c < kStep / 32; ++c) {
+            const uint32_t mk = flash::chunk_mask(cr, 2 * h + c);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!((mk >> e) & 1u)) v[c * 32 + e] = 0xff800000u;
           }
         }
+        // P with the maximum so far, while the step's own maximum is being found; only where
+        // that one is larger by more than 2^8 (the lazy rescale of flash_tc.cuh, always on an
+        // item's first step) is it formed again
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t packed[32];
+        flash::exp2_pack64(v, 0, a.scale_log2, m == -INFINITY ? 0.f : -m, packed, acc);
         const float tmax = flash::row_max_log2(v, a.scale_log2);
-        // lazy rescale, as in flash_tc.cuh: only when the maximum grows by more than 2^8
         const bool raise = tmax > m + flash::kRescaleLog2;
-        const bool rescale = raise && m != -INFINITY;
-        if (__any_sync(0xffffffffu, rescale)) {
-          const float alpha = rescale ? flash::ex2_approx(m - tmax) : 1.f;
-          l *= alpha;
+        if (__any_sync(0xffffffffu, raise)) {
+          const bool rescale = raise && m != -INFINITY;
+          if (__any_sync(0xffffffffu, rescale)) {
+            // the PV of the step before must have landed in O
+            if (!(ok = warp_wait(&bar.pv_done[x][b ^ 1], ((done - 1) >> 1) & 1))) break;
+            tc_fence_after();
+            const float alpha = rescale ? flash::ex2_approx(m - tmax) : 1.f;
+            l *= alpha;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + c * 32, o);
-            tmem_ld_wait();
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + c * 32, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(o_addr + c * 32, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(o_addr + c * 32, o);
+            }
+            tmem_st_wait();
           }
-          tmem_st_wait();
+          if (raise) m = tmax;
+          acc[0] = acc[1] = make_float2(0.f, 0.f);
+          flash::exp2_pack64(v, 0, a.scale_log2, m == -INFINITY ? 0.f : -m, packed, acc);
         }
-        if (raise) m = tmax;
-        const float neg_m = (m == -INFINITY) ? 0.f : -m;
         if (tile.clear) {
-          // V rows that no row of the item may read (flash_tc.cuh, kClearRows); both row tiles'
-          // threads write the same zeros
-          const int gv = 2 * (g + j) + 1, st = gv % kSlots;
+          // V rows that no row of the item may read (flash_tc.cuh, kClearRows), the step's half
+          // of the tile; both row tiles' threads write the same zeros
+          const int gv = 2 * (g + u / 2) + 1, st = gv % kSlots;
           if (!(ok = warp_wait(&bar.full[st], (gv / kSlots) & 1))) break;
-          if (!pol.key_read(tile, row)) {
+          if (row / kStep == h && !pol.key_read(tile, row)) {
             uint8_t* vr = smem + S::OFF_RING + st * S::TILE + row * 128;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
@@ -641,29 +665,23 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           }
           fence_proxy_async_smem();
         }
-        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t packed[32];
-          flash::exp2_pack64(v, h * 64, a.scale_log2, neg_m, packed, acc);
-          tmem_st32(s_addr + S::P_OFF + h * 32, packed);
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive_warp(&bar.p_full[x][h]);
-        }
+        tmem_st32(sb + S::P_OFF, packed);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&bar.p_full[x][b]);
         l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
       }
       if (!ok) break;
       g += it.tiles;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      if (!(ok = warp_wait(&bar.pv_done[x], (done - 1) & 1))) break;
+      if (!(ok = warp_wait(&bar.pv_done[x][(done - 1) & 1], ((done - 1) >> 1) & 1))) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(o_addr + c * 32, o);
         tmem_ld_wait();
-        if (rv) pol.store_chunk(row, c * 32, o, inv, m, l);
+        pol.store_chunk(row, c * 32, o, inv, m, l);
       }
       tc_fence_before();
     }

@@ -242,6 +242,20 @@ MARS_DEV void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
                : "memory");
 }
 
+// True in one lane of the warp, chosen by the hardware; whole warp. A branch on it is known to
+// be taken by one thread, so that the code inside keeps tcgen05 operands in uniform registers: a
+// burst of eight MMAs is issued in 230-310 cycles, against 540-560 behind a test of the lane
+// index, which for short steps is longer than the MMAs themselves take.
+MARS_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---- Two-SM forms (cta_group::2, a cluster of two CTAs). A kernel uses either these or
 // the one-SM forms above for all of its tcgen05 allocation, MMA and commit instructions.
 // The allocation is collective: one warp of each CTA of the pair executes it, and both
