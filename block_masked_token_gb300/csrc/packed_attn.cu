@@ -308,8 +308,10 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
 // that the tensor pipe works for one tile while the other's softmax runs, and each K and V
 // tile is loaded once for both. Items come from a plan (packed_plan.cu), costliest first.
 //   warp 0  loader: K_0, V_0, K_1, V_1, ... through one ring of kSlots tiles
-//   warp 1  TMEM owner; loads Q and issues S_x = Q_x K_j^T
-//   warp 2  issues O_x += P_x V_j
+//   warps 1 (TMEM owner), 3  load Q_x and issue S_x = Q_x K_j^T for x = 0, 1. One thread for
+//           both was the bottleneck: a step's wait, eight MMAs, commit and loop took it about
+//           800 cycles, four times per key tile
+//   warp 2  issues O_x += P_x V_j for both
 //   warps 4..7, 8..11  softmax and output of row tile 0, 1 (thread = row)
 // They work in steps of 64 keys. One step's chain, S, its softmax, PV and the hand-offs
 // between them, takes about 1,700 cycles, of which the tensor pipe works a third: four steps
@@ -337,7 +339,7 @@ struct PairBar {
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];     // [row tile][buffer]
-  uint64_t drain[2];
+  uint64_t drain[3];
   uint32_t tmem_base;
   int abort;
 };
@@ -389,8 +391,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     bar.abort = 0;
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.empty[i], 2);
     }
+    mbar_init(&bar.drain[2], 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar.q_full[x], 1);
       mbar_init(&bar.q_empty[x], 1);
@@ -470,61 +473,59 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         for (int k = 1; k <= kSlots && g - k >= 0; ++k)
           mbar_wait(&bar.full[(g - k) % kSlots], ((g - k) / kSlots) & 1, nullptr, a.status);
       __syncwarp();
-    } else if (warp == 1) {
-      // ------------------------------------------------------- Q loads, S = Q K^T
+    } else if (warp != 2) {
+      // ------------------------------- warp 1, 3: Q_x loads, S_x = Q_x K^T for x = 0, 1
+      const int x = warp >> 1;
       if (elect_one()) {
         const uint32_t idesc = idesc_bf16_f32(BQ, kStep, false);
-        int g = 0, done[2] = {0, 0}, items[2] = {0, 0};   // key tiles; steps and items per x
+        const uint64_t qd = sdesc_sw128(smem_u32(smem + S::OFF_Q + x * S::TILE), 16, 1024);
+        const uint32_t ts = tmem + S::TM_S + x * BKV;
+        int g = 0, c = 0, items = 0;                   // key tiles; steps and items of x
         bool ok = true;
         for (int r = 0; r < turns.rounds && ok; ++r) {
           const int id = turns.at(r);
           if (id < 0) continue;
           const PairItem it = pair_item(a, plan, id);
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (!it.steps[x]) continue;
+          const int steps = x ? it.steps[1] : it.steps[0];
+          if (steps) {
             // Q_x is replaced once the S MMAs of its previous item have completed
-            if (items[x] && !(ok = mbar_wait(&bar.q_empty[x], (items[x] - 1) & 1, ab, a.status)))
-              break;
+            if (items && !(ok = mbar_wait(&bar.q_empty[x], (items - 1) & 1, ab, a.status))) break;
             mbar_arrive_expect_tx(&bar.q_full[x], a.gp * a.tpt * 128 * (D / 64));
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(smem + S::OFF_Q + x * S::TILE + c * (BQ * 128), &tm_q, &bar.q_full[x], c * 64,
-                          it.h0, it.base + it.tok0 + x * a.tpt);
-            ++items[x];
+            for (int cc = 0; cc < D / 64; ++cc)
+              tma_load_3d(smem + S::OFF_Q + x * S::TILE + cc * (BQ * 128), &tm_q, &bar.q_full[x],
+                          cc * 64, it.h0, it.base + it.tok0 + x * a.tpt);
+            if (!(ok = mbar_wait(&bar.q_full[x], items & 1, ab, a.status))) break;
+            ++items;
           }
           for (int j = 0; j < it.tiles && ok; ++j, ++g) {
             const int st = (2 * g) % kSlots;
             if (!(ok = mbar_wait(&bar.full[st], (2 * g / kSlots) & 1, ab, a.status))) break;
             const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_RING + st * S::TILE), 16, 1024);
-            for (int hx = 0; hx < 4; ++hx) {
-              const int h = hx >> 1, x = hx & 1, u = 2 * j + h;
-              if (u >= it.steps[x]) continue;
-              const int c = done[x], b = c & 1;
-              ok = (u > 0 || mbar_wait(&bar.q_full[x], (items[x] - 1) & 1, ab, a.status)) &&
-                   // the PV of two steps before has read P out of the buffer
-                   (c < 2 || mbar_wait(&bar.pv_done[x][b], ((c >> 1) - 1) & 1, ab, a.status));
-              if (!ok) break;
+            for (int u = 2 * j; u < min(2 * j + 2, steps); ++u, ++c) {
+              const int b = c & 1;
+              // the PV of two steps before has read P out of the buffer
+              if (c >= 2 && !(ok = mbar_wait(&bar.pv_done[x][b], ((c >> 1) - 1) & 1, ab, a.status)))
+                break;
               tc_fence_after();
-              const uint64_t qd = sdesc_sw128(smem_u32(smem + S::OFF_Q + x * S::TILE), 16, 1024);
+              const uint64_t kh = sdesc_advance(kd, (u & 1) * (kStep * 128));
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = (k >> 2) * (BQ * 128) + (k & 3) * 32;
-                mma_bf16_ss(tmem + S::TM_S + x * BKV + b * kStep, sdesc_advance(qd, off),
-                            sdesc_advance(kd, off + h * (kStep * 128)), idesc, k != 0);
+                mma_bf16_ss(ts + b * kStep, sdesc_advance(qd, off), sdesc_advance(kh, off), idesc,
+                            k != 0);
               }
               mma_commit(&bar.s_full[x][b]);
-              if (u == it.steps[x] - 1) mma_commit(&bar.q_empty[x]);
-              ++done[x];
+              if (u == steps - 1) mma_commit(&bar.q_empty[x]);
             }
             if (!ok) break;
-            mma_commit(&bar.empty[st]);
+            mma_commit(&bar.empty[st]);                // one of the two arrivals for a K slot
           }
         }
-        mma_commit(&bar.drain[0]);
-        mbar_wait(&bar.drain[0], 0, nullptr, a.status);
-        for (int x = 0; x < 2; ++x)
-          if (items[x]) mbar_wait(&bar.q_full[x], (items[x] - 1) & 1, nullptr, a.status);
+        mma_commit(&bar.drain[x]);
+        mbar_wait(&bar.drain[x], 0, nullptr, a.status);
+        if (items) mbar_wait(&bar.q_full[x], (items - 1) & 1, nullptr, a.status);
       }
-    } else if (warp == 2) {
+    } else {
       // ------------------------------------------------------------------ O += P V
       if (elect_one()) {
         const uint32_t idesc = idesc_bf16_f32(BQ, D, true);
@@ -552,11 +553,12 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               ++done[x];
             }
             if (!ok) break;
+            mma_commit(&bar.empty[st]);                // both arrivals for a V slot
             mma_commit(&bar.empty[st]);
           }
         }
-        mma_commit(&bar.drain[1]);
-        mbar_wait(&bar.drain[1], 0, nullptr, a.status);
+        mma_commit(&bar.drain[2]);
+        mbar_wait(&bar.drain[2], 0, nullptr, a.status);
       }
     }
   } else {
