@@ -130,7 +130,10 @@ struct PackedAttn {
   int32_t* status;
 };
 struct PackedPlan {
-  bool pair;               // two row tiles per item, persistent CTAs over a plan's list
+  bool pair;               // persistent CTAs over equal parts of the work
+  int xt;                  // row tiles per item (pair)
+  bool can_split;          // items may be divided among CTAs (pair)
+  size_t ticket_bytes;
   int gp, tpt;             // heads and tokens of a row tile
   int nsplit, split_tiles; // splits of a key list, 128-key tiles per split
   long long items, ctas;

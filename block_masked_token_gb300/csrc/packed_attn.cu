@@ -17,7 +17,6 @@
 // unnormalised partial (m in log2 units, l, O) and a second kernel merges them.
 //
 // Where the rows are many, pair_kernel takes two row tiles per CTA instead (see there).
-#include <climits>
 
 #include "common.cuh"
 #include "flash_tc.cuh"
@@ -41,10 +40,12 @@ struct AttnArgs {
   const int32_t* block_table;
   int num_pages, max_pages;
   int batch, total, hq, hkv, gp, tpt, ngrp, nsplit, split_tiles;
+  int xt, rows, can_split;     // pair kernel: row tiles and tokens per item, whether to split items
   float scale_log2;
   uint16_t* o;                 // [total][hq][D] bf16
   float* lse;                  // [hq][total] or NULL
-  float* part;                 // [nsplit][total][hq][D + 4] with several splits
+  float* part;                 // [nsplit][total][hq][D + 4] with several splits; pair kernel: partial()
+  int32_t* tickets;            // pair kernel: [ctas][2], zero at its start
   int32_t* status;
 };
 
@@ -68,6 +69,11 @@ struct RowsPolicy {
     int count;           // keys that may be read
     bool prefix, full, clear;
   };
+  int trow, hrow;              // token and head of this thread's row inside the tile
+  MARS_DEV void set_row(int row) {
+    trow = row / a->gp;
+    hrow = row - trow * a->gp;
+  }
   MARS_DEV int token(int row) const { return tok0 + row / a->gp; }
   // A row without a token (the tile's last rows, the tokens past the sequence) computes
   // something that is not stored; masking it would cost its whole warp the masks of every tile
@@ -303,11 +309,13 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
 
 // ------------------------------------------------------------------------ pair kernel
 //
-// Compute-bound calls: a persistent CTA per SM runs items of two row tiles (x = 0, 1) of the
-// same sequence and KV head over one key list, each with a softmax warpgroup of its own, so
-// that the tensor pipe works for one tile while the other's softmax runs, and each K and V
-// tile is loaded once for both. Items come from a plan (packed_plan.cu), costliest first.
-//   warp 0  loader: K_0, V_0, K_1, V_1, ... through one ring of kSlots tiles
+// A persistent CTA per SM takes items of two row tiles (x = 0, 1) of the same sequence and KV
+// head over one key list, each with a softmax warpgroup of its own, so that the tensor pipe
+// works for one tile while the other's softmax runs, and each K and V tile is loaded once for
+// both.
+//   warp 0  loader: V_0, K_0, V_1, K_1, ... into a ring for K and one for V. Every warp that waits
+//           on a ring waits for each of its tiles, needed or not: a wait for a phase whose
+//           predecessor is still open would pass at once, on the one before
 //   warps 1 (TMEM owner), 3  load Q_x and issue S_x = Q_x K_j^T for x = 0, 1. One thread for
 //           both was the bottleneck: a step's wait, eight MMAs, commit and loop took it about
 //           800 cycles, four times per key tile
@@ -317,12 +325,21 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
 // between them, takes about 1,700 cycles, of which the tensor pipe works a third: four steps
 // have to be in flight, two per row tile, and TMEM holds just that many (two S buffers of 64
 // columns per row tile, P in bf16 over the upper half of each, and two O of 128). With 128-key
-// steps, one in flight per row tile, a pair of tiles took 4,000 cycles instead of 2,048.
+// steps, one in flight per row tile, a pair of tiles took 4,000 cycles instead of 2,870.
 // A row tile's first P of an item also says that its warps have read the O of the item before.
-constexpr int kSlots = 5;
+//
+// Work is divided evenly, whatever the lengths: the items of all sequences are laid out on a
+// line, each as long as its work (its key tiles and a constant), and CTA c of E takes the part
+// from c/E to (c+1)/E of it. A cut inside an item with many key tiles splits its key list
+// there (Cut::j); the CTAs then write partials (m, l, O) and the last of them to finish, known
+// by a ticket, merges them in the order of the keys, so that results do not depend on which
+// one it was. Nothing waits for another CTA. Each CTA finds its part from the boundaries by
+// itself (find_part), for about a microsecond; a separate kernel that listed the items by
+// falling cost took 9, and left 228 long items on 152 SMs at 75 % of the rate.
+constexpr int kKSlots = 2, kVSlots = 3;          // ring depths, in tiles
 constexpr int kStep = 64;                        // keys per step
 constexpr int PAIR_THREADS = 384;
-constexpr int PAIR_WG0_REGS = 80, PAIR_SOFTMAX_REGS = 208;
+constexpr int PAIR_WG0_REGS = 88, PAIR_SOFTMAX_REGS = 208;
 static_assert(128 * (PAIR_WG0_REGS + 2 * PAIR_SOFTMAX_REGS) <=
                   PAIR_THREADS * (65536 / PAIR_THREADS / 8 * 8),
               "the register split fits the launch's register pool");
@@ -330,70 +347,368 @@ static_assert(128 * (PAIR_WG0_REGS + 2 * PAIR_SOFTMAX_REGS) <=
 template <int D>
 struct PairSmem {
   static constexpr int TILE = BKV * D * 2;             // a Q, K or V tile
-  static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE;
-  static constexpr int TOTAL = OFF_RING + kSlots * TILE + 1024;
+  static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = OFF_K + kKSlots * TILE;
+  static constexpr int TOTAL = OFF_V + kVSlots * TILE + 1024;
   static constexpr int TM_S = 0, TM_O = 2 * BKV, P_OFF = kStep / 2;
 };
 
+// An item as the loader hands it to the other warps.
+struct PairItem {
+  int s, base, n, P, np, tok0, h0;
+  int tiles, ja, jb;                 // key tiles; those that this CTA visits (jb = 0: no more items)
+  int all[2], steps[2];              // steps of the row tiles: over all key tiles, in this CTA
+  int c1, cuts;                      // a divided item: CTAs c1 .. c1 + cuts - 1 start inside it
+};
+constexpr int kItems = 3;            // items handed over and not yet taken by every warp
+
 struct PairBar {
-  uint64_t full[kSlots], empty[kSlots];
+  uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];     // [row tile][buffer]
   uint64_t drain[3];
   uint32_t tmem_base;
   int abort;
+  int last[2];                       // whether this CTA merges (per row tile)
+  uint64_t item_full[kItems], item_empty[kItems];
+  PairItem items[kItems];
 };
 
-// An item: row tiles at tokens tok0 and tok0 + tpt of a sequence, the steps that each takes (0:
-// no rows; the last step is left out where a tile's own keys end in the first half of a key
-// tile), and the key tiles that are loaded.
-struct PairItem {
-  int base, n, seq, tok0, h0, kvh, P, np, steps[2], tiles;
-};
+// Work of an item in units of 1/128 key tile: its key tiles, nearly, and kItemWork for its
+// start and output. Linear in the tile index t, so that sums have a closed form.
+constexpr long long kItemWork = 400;
+constexpr int kMinPart = 4;                      // key tiles of a part of a split item
 
-MARS_DEV PairItem pair_item(const AttnArgs& a, const packed::Plan& plan, int id) {
-  PairItem it;
-  const int heads = a.hkv * a.ngrp, g = id % heads;
-  const packed::Tile t = plan.first[id / heads];
-  it.base = t.base;
-  it.n = t.n;
-  it.seq = t.id;
-  it.kvh = g / a.ngrp;
-  it.h0 = g * a.gp;
-  it.tok0 = t.tile * 2 * a.tpt;
-  const long long cached = a.seq_lens ? a.seq_lens[t.id] : 0;
-  it.P = (int)max(0LL, min(cached, (long long)a.max_pages * kPageSize));
-  it.np = (it.P + BKV - 1) / BKV;
-  for (int x = 0; x < 2; ++x) {
-    const int first = it.tok0 + x * a.tpt;
-    it.steps[x] = first < it.n ? 2 * it.np + (min(first + a.tpt, it.n) - 1) / kStep + 1 : 0;
+// A sequence as the line of items sees it.
+struct Row {
+  int s, base, n, P;
+  long long pre;                     // work before the sequence
+
+  MARS_DEV int tiles_of(const AttnArgs& a) const { return (n + a.rows - 1) / a.rows; }
+  MARS_DEV int prefix() const { return (P + BKV - 1) / BKV; }
+  // work of one head's first t items
+  MARS_DEV long long upto(const AttnArgs& a, long long t) const {
+    return t * (128LL * prefix() + kItemWork) + a.rows * (t * (t + 1) / 2);
   }
-  it.tiles = (max(it.steps[0], it.steps[1]) + 1) / 2;
-  return it;
+};
+
+// Cached keys of a sequence: a length that the table cannot hold is cut to what it can.
+MARS_DEV int cached_keys(const AttnArgs& a, int s) {
+  if (!a.seq_lens) return 0;
+  return (int)max(0LL, min((long long)a.seq_lens[s], (long long)a.max_pages * kPageSize));
+}
+
+// Key tiles of item t of a sequence.
+MARS_DEV int key_tiles(const AttnArgs& a, const Row& q, int t) {
+  return q.prefix() + (int)((min((long long)(t + 1) * a.rows, (long long)q.n) - 1) / BKV) + 1;
+}
+
+// Where position `pos` cuts an item of `tiles` key tiles at [s0, s0 + work): before its key
+// tile j (0: before the item, tiles: after it). Items that are small beside a CTA's part, or
+// too short to split, are cut at the nearer end.
+MARS_DEV int cut_at(const AttnArgs& a, long long pos, long long s0, long long work, int tiles,
+                    long long part) {
+  const long long rem = pos - s0;
+  if (!a.can_split || tiles < 2 * kMinPart || 8 * work <= part) return 2 * rem >= work ? tiles : 0;
+  const int j = (int)(rem * tiles / work);
+  return j < kMinPart ? 0 : tiles - j < kMinPart ? tiles : j;
+}
+
+// A CTA's part of the line: from key tile j of item (q, g, t), to key tile end_j of the item
+// that starts at end_s0.
+struct PairPart {
+  Row q;
+  int g, t, j;
+  long long end_s0;
+  int end_j;
+  long long total, ctas;             // all work, CTAs that share it (0: none for this CTA)
+};
+
+// Scan scratch of find_part.
+struct PartScan {
+  long long sum[PAIR_THREADS / 32];
+  int top[PAIR_THREADS / 32];
+  long long work;
+  int tops, items;
+  Row at[2];
+  PairPart part;
+};
+
+// Every thread of the CTA: fill sc.part.
+MARS_DEV void find_part(const AttnArgs& a, PartScan& sc) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long heads = a.hkv * a.ngrp;
+  int bad = 0;
+  Row q{};
+  long long mine = 0;
+  // one chunk of sequences: q (with its work before it) and mine for this thread's
+  auto chunk = [&](int s0) {
+    const int s = s0 + tid, top0 = sc.tops;
+    const long long before = sc.work;
+    const int c = s < a.batch ? a.cu[s + 1] : top0;
+    q.P = s < a.batch ? cached_keys(a, s) : 0;
+    if (s < a.batch && a.seq_lens && q.P != a.seq_lens[s]) bad |= MARS_ST_OVERFLOW;
+    int end = max(min(max(c, 0), a.total), top0);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end = max(end, v);
+    }
+    if (lane == 31) sc.top[warp] = end;
+    __syncthreads();
+    int lead = top0;                               // the boundary before this warp
+    for (int w = 0; w < warp; ++w) lead = max(lead, sc.top[w]);
+    end = max(end, lead);
+    if (s < a.batch && c != end) bad |= MARS_ST_BADSEQ;
+    int begin = __shfl_up_sync(0xffffffffu, end, 1);
+    if (lane == 0) begin = lead;
+    q.s = s;
+    q.base = begin;
+    q.n = end - begin;
+    const int tiles = s < a.batch ? q.tiles_of(a) : 0;
+    mine = heads * q.upto(a, tiles);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sc.sum[warp] = incl;
+    if (tiles) atomicAdd(&sc.items, (int)(tiles * heads));
+    __syncthreads();
+    q.pre = before + incl - mine;
+    for (int w = 0; w < warp; ++w) q.pre += sc.sum[w];
+    __syncthreads();
+    if (tid == PAIR_THREADS - 1) {
+      sc.tops = end;
+      sc.work = q.pre + mine;
+    }
+    __syncthreads();
+  };
+  auto begin = [&] {
+    if (tid == 0) {
+      const int c0 = a.cu[0];
+      sc.tops = min(max(c0, 0), a.total);
+      if (c0 != sc.tops) bad |= MARS_ST_BADSEQ;
+      sc.work = 0;
+      sc.items = 0;
+    }
+    __syncthreads();
+  };
+  begin();
+  for (int s0 = 0; s0 < a.batch; s0 += PAIR_THREADS) chunk(s0);
+  const long long total = sc.work;
+  // CTAs that share the work: as many as there are, unless that leaves less than a part each
+  // and there are fewer items
+  const long long ctas = min((long long)gridDim.x,
+                             max((long long)sc.items, total / (160 * kMinPart)));
+  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
+  if ((long long)blockIdx.x >= ctas) {
+    if (tid == 0) sc.part.ctas = 0;
+    __syncthreads();
+    return;
+  }
+  const long long p0 = blockIdx.x * total / ctas, p1 = (blockIdx.x + 1) * total / ctas;
+  auto locate = [&] {
+    if (mine > 0 && p0 >= q.pre && p0 < q.pre + mine) sc.at[0] = q;
+    if (mine > 0 && p1 >= q.pre && p1 < q.pre + mine) sc.at[1] = q;
+  };
+  if (a.batch <= PAIR_THREADS) {
+    locate();
+  } else {
+    __syncthreads();                               // the totals have been read
+    begin();
+    for (int s0 = 0; s0 < a.batch; s0 += PAIR_THREADS) {
+      chunk(s0);
+      locate();
+    }
+  }
+  __syncthreads();
+  if (lane == 0 && warp < 2) {                     // warp 0: the start, warp 1: the end
+    const long long pos = warp ? p1 : p0;
+    PairPart& r = sc.part;
+    if (pos >= total) {
+      r.end_s0 = total;
+      r.end_j = 0;
+    } else {
+      const Row& f = sc.at[warp];
+      const long long one = f.upto(a, f.tiles_of(a));
+      const int g = (int)((pos - f.pre) / one);
+      const long long rem = (pos - f.pre) - g * one;
+      int lo = 0, hi = f.tiles_of(a);              // the item: upto(lo) <= rem < upto(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (f.upto(a, mid) <= rem) lo = mid; else hi = mid;
+      }
+      const long long s0 = f.pre + g * one + f.upto(a, lo);
+      const long long work = f.upto(a, lo + 1) - f.upto(a, lo);
+      const int tiles = key_tiles(a, f, lo);
+      const int j = cut_at(a, pos, s0, work, tiles, total / ctas);
+      if (warp == 0) {
+        r.q = f;
+        r.g = g;
+        r.t = lo;
+        r.j = j;
+        r.total = total;
+        r.ctas = ctas;
+      } else {
+        r.end_s0 = j == tiles ? s0 + work : s0;
+        r.end_j = j == tiles ? 0 : j;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// The items of a CTA's part, one after another (each role walks on its own): row tiles at
+// tokens tok0 and tok0 + tpt, the steps of 64 keys that each takes (the last is left out where
+// a tile's own keys end in the first half of a key tile), and the key tiles [ja, jb) of the
+// item's `tiles` that this CTA visits.
+struct PairWalk {
+  const AttnArgs& a;
+  const PairPart& p;
+  Row q;
+  int g, t, tok0, kvh, h0, np, tiles, ja, jb;
+  long long s0, work;
+  bool more;
+
+  MARS_DEV PairWalk(const AttnArgs& a_, const PairPart& p_) : a(a_), p(p_), q(p_.q), g(p_.g), t(p_.t) {
+    item();
+    ja = p.j;
+    if (ja == tiles) next(); else end();
+  }
+  MARS_DEV void item() {
+    np = q.prefix();
+    tiles = key_tiles(a, q, t);
+    tok0 = t * a.rows;
+    kvh = g / a.ngrp;
+    h0 = g * a.gp;
+    ja = 0;
+  }
+  MARS_DEV void end() {
+    const long long one = q.upto(a, q.tiles_of(a)), off = q.upto(a, t);
+    s0 = q.pre + g * one + off;
+    work = q.upto(a, t + 1) - off;
+    jb = s0 == p.end_s0 ? p.end_j : tiles;
+    more = s0 < p.end_s0 || (s0 == p.end_s0 && p.end_j > ja);
+  }
+  MARS_DEV void next() {
+    if (++t == q.tiles_of(a)) {
+      t = 0;
+      if (++g == a.hkv * a.ngrp) {
+        g = 0;
+        const long long after = q.pre + (long long)a.hkv * a.ngrp * q.upto(a, q.tiles_of(a));
+        q.pre = after;
+        do {                                       // the next sequence with rows
+          if (++q.s >= a.batch || after >= p.end_s0 + (p.end_j > 0)) {
+            more = false;
+            return;
+          }
+          q.base += q.n;
+          q.n = max(min(max(a.cu[q.s + 1], 0), a.total), q.base) - q.base;
+        } while (q.n == 0);
+        q.P = cached_keys(a, q.s);
+      }
+    }
+    item();
+    end();
+  }
+  MARS_DEV int first_token(int x) const { return tok0 + x * a.tpt; }
+  // steps of row tile x over all the item's key tiles; 0 if it has no rows
+  MARS_DEV int all_steps(int x) const {
+    if (x >= a.xt || first_token(x) >= q.n) return 0;
+    return 2 * np + (min(first_token(x) + a.tpt, q.n) - 1) / kStep + 1;
+  }
+  // its steps [first, last) in this CTA's key tiles
+  MARS_DEV int steps(int x) const { return max(min(all_steps(x), 2 * jb) - 2 * ja, 0); }
+  MARS_DEV PairItem describe() const {
+    PairItem d{q.s, q.base, q.n, q.P, np, tok0, h0, tiles, ja, jb,
+               {all_steps(0), all_steps(1)}, {steps(0), steps(1)}, 0, 0};
+    if (ja > 0 || jb < tiles) {
+      const long long part = p.total / p.ctas;
+      auto cut = [&](long long c) { return cut_at(a, c * p.total / p.ctas, s0, work, tiles, part); };
+      long long c1 = s0 * p.ctas / p.total;
+      while (c1 * p.total / p.ctas <= s0 || cut(c1) == 0) ++c1;
+      d.c1 = (int)c1;
+      d.cuts = 1;
+      while (c1 + d.cuts < p.ctas && (c1 + d.cuts) * p.total / p.ctas < s0 + work &&
+             cut(c1 + d.cuts) < tiles)
+        ++d.cuts;
+    }
+    return d;
+  }
+};
+
+template <int D>
+constexpr int PART4 = BQ * D / 4 + BQ / 2;       // float4 of a partial
+
+// Partials: [CTA][0: a part that starts inside its item, 1: at its start][row tile], each D / 4
+// rows of 128 float4 (a thread per row of the tile: its loads and stores are coalesced) and 128
+// pairs of m and l.
+template <int D>
+MARS_DEV float4* partial(const AttnArgs& a, int cta, bool inside, int x) {
+  return reinterpret_cast<float4*>(a.part) + (((size_t)cta * 2 + (inside ? 0 : 1)) * 2 + x) * PART4<D>;
+}
+
+// The next item of the loader's queue (number i), copied; false if the wait gave up. The
+// caller then arrives on item_empty, once per warp.
+MARS_DEV bool take_item(PairBar& bar, int i, PairItem& it, volatile int* ab, int32_t* status) {
+  if (!sm100::mbar_wait(&bar.item_full[i % kItems], (i / kItems) & 1, ab, status)) return false;
+  it = bar.items[i % kItems];
+  return true;
+}
+
+// In each group of 8 lanes: lane i's chunk j (4 words of w) becomes lane j's chunk i.
+MARS_DEV void transpose8(uint32_t (&w)[32], int lane) {
+#pragma unroll
+  for (int s = 4; s > 0; s >>= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i & s) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t &lo = w[4 * i + e], &hi = w[4 * (i | s) + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+        lo = up ? got : lo;
+        hi = up ? hi : got;
+      }
+    }
+  }
+}
+
+MARS_DEV void group_sync(int x) {                  // the 128 threads of a softmax warpgroup
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
 }
 
 template <int D>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kp,
-            const __grid_constant__ CUtensorMap tm_vp, AttnArgs a, packed::Plan plan) {
+            const __grid_constant__ CUtensorMap tm_vp, AttnArgs a) {
   using namespace sm100;
   using S = PairSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PairBar bar;
-  const packed::Turns turns(*plan.count * a.hkv * a.ngrp);
-  if (turns.at(0) < 0) return;                         // more CTAs than items
+  __shared__ PartScan scan;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* ab = &bar.abort;
   if (threadIdx.x == 0) {
     bar.abort = 0;
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], 2);
+    for (int i = 0; i < kKSlots; ++i) {
+      mbar_init(&bar.k_full[i], 1);
+      mbar_init(&bar.k_empty[i], 2);
+    }
+    for (int i = 0; i < kVSlots; ++i) {
+      mbar_init(&bar.v_full[i], 1);
+      mbar_init(&bar.v_empty[i], 1);
     }
     mbar_init(&bar.drain[2], 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_empty[i], 3 + 8);        // both S issuers, the PV issuer, softmax warps
+    }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar.q_full[x], 1);
       mbar_init(&bar.q_empty[x], 1);
@@ -406,6 +721,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     fence_barrier_init();
   }
+  find_part(a, scan);
+  if (scan.part.ctas == 0) return;
   if (warp == 1) {
     tmem_alloc(&bar.tmem_base, 512);
     tmem_relinquish();
@@ -419,59 +736,80 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     regs_lower<PAIR_WG0_REGS>();
     if (warp == 0) {
       // ------------------------------------------------------------------- loader
-      int g = 0, flags = 0;                            // tiles loaded (K and V counted apart)
+      int g = 0, flags = 0;                            // key tiles loaded
       bool ok = true;
-      for (int r = 0; r < turns.rounds && ok; ++r) {
-        const int id = turns.at(r);
-        if (id < 0) continue;
-        const PairItem it = pair_item(a, plan, id);
-        if (a.seq_lens && a.seq_lens[it.seq] != it.P) flags |= MARS_ST_OVERFLOW;
-        const int32_t* bt = a.block_table ? a.block_table + (size_t)it.seq * a.max_pages : nullptr;
+      int ni = 0, nk = 0, nv = 0;                      // items handed over; K and V tiles issued
+      auto publish = [&](const PairItem& d) {
+        int good = 1;
+        if (lane == 0) {
+          good = mbar_wait(&bar.item_empty[ni % kItems], ((ni / kItems) & 1) ^ 1, ab, a.status);
+          if (good) {
+            bar.items[ni % kItems] = d;
+            mbar_arrive(&bar.item_full[ni % kItems]);
+          }
+        }
+        ++ni;
+        return __shfl_sync(0xffffffffu, good, 0) != 0;
+      };
+      for (PairWalk it(a, scan.part); it.more && ok; it.next()) {
+        if (!(ok = publish(it.describe()))) break;
+        const int32_t* bt = a.block_table ? a.block_table + (size_t)it.q.s * a.max_pages : nullptr;
         // this lane's page of prefix tile j, read one tile ahead
         auto entry = [&](int j) -> int {
           const int lp = j * kPagesPerTile + lane;
           return j < it.np && lane < kPagesPerTile && lp < a.max_pages ? bt[lp] : -1;
         };
-        int next = entry(0);
-        for (int j = 0; j < it.tiles && ok; ++j) {
+        int next = entry(it.ja);
+        for (int j = it.ja; j < it.jb && ok; ++j) {
           const int e = next;
           next = entry(j + 1);
-          for (int v = 0; v < 2; ++v, ++g) {
-            const int st = g % kSlots;
+          for (int v = 1; v >= 0; --v) {                 // V first, see the softmax warps' clearing
+            const int n = v ? kVSlots : kKSlots, st = g % n;
+            uint64_t* full = v ? &bar.v_full[st] : &bar.k_full[st];
             int good = 1;
             if (lane == 0) {
-              good = mbar_wait(&bar.empty[st], ((g / kSlots) & 1) ^ 1, ab, a.status);
-              if (good) mbar_arrive_expect_tx(&bar.full[st], S::TILE);
+              good = mbar_wait(v ? &bar.v_empty[st] : &bar.k_empty[st], ((g / n) & 1) ^ 1, ab, a.status);
+              if (good) mbar_arrive_expect_tx(full, S::TILE);
             }
             ok = __shfl_sync(0xffffffffu, good, 0) != 0;
             if (!ok) break;
-            uint8_t* dst = smem + S::OFF_RING + st * S::TILE;
+            (v ? nv : nk) = g + 1;
+            uint8_t* dst = smem + (v ? S::OFF_V : S::OFF_K) + st * S::TILE;
             if (j < it.np) {
               if (lane < kPagesPerTile) {
                 // as in packed_rows_kernel: a page that may not be read loads page 0
                 int page = 0;
                 if (e >= 0 && e < a.num_pages)
                   page = e;
-                else if (j * BKV + lane * kPageSize < it.P)
+                else if (j * BKV + lane * kPageSize < it.q.P)
                   flags |= MARS_ST_NOPAGE;
                 const int row = a.num_pages > 0 ? (page * a.hkv + it.kvh) * kPageSize : kPageSize;
                 for (int x = 0; x < D / 64; ++x)
                   tma_load_2d(dst + x * (BKV * 128) + lane * (kPageSize * 128), v ? &tm_vp : &tm_kp,
-                              &bar.full[st], x * 64, row);
+                              full, x * 64, row);
               }
             } else if (lane == 0) {
               for (int x = 0; x < D / 64; ++x)
-                tma_load_3d(dst + x * (BKV * 128), v ? &tm_v : &tm_k, &bar.full[st], x * 64, it.kvh,
-                            it.base + (j - it.np) * BKV);
+                tma_load_3d(dst + x * (BKV * 128), v ? &tm_v : &tm_k, full, x * 64, it.kvh,
+                            it.q.base + (j - it.np) * BKV);
             }
           }
+          ++g;
         }
       }
+      if (ok) publish(PairItem{});                     // no more items
       if (flags && a.status) atomicOr(a.status, flags);
-      // wait (bounded) for the copies still in flight
-      if (lane == 0)
-        for (int k = 1; k <= kSlots && g - k >= 0; ++k)
-          mbar_wait(&bar.full[(g - k) % kSlots], ((g - k) / kSlots) & 1, nullptr, a.status);
+      // wait (bounded) for the copies still in flight, and for every arrival that releases a slot
+      if (lane == 0) {
+        for (int k = nk - 1; k >= max(nk - kKSlots, 0); --k) {
+          mbar_wait(&bar.k_full[k % kKSlots], (k / kKSlots) & 1, nullptr, a.status);
+          if (ok) mbar_wait(&bar.k_empty[k % kKSlots], (k / kKSlots) & 1, ab, a.status);
+        }
+        for (int k = nv - 1; k >= max(nv - kVSlots, 0); --k) {
+          mbar_wait(&bar.v_full[k % kVSlots], (k / kVSlots) & 1, nullptr, a.status);
+          if (ok) mbar_wait(&bar.v_empty[k % kVSlots], (k / kVSlots) & 1, ab, a.status);
+        }
+      }
       __syncwarp();
     } else if (warp != 2) {
       // ------------------------------- warp 1, 3: Q_x loads, S_x = Q_x K^T for x = 0, 1
@@ -482,10 +820,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint32_t ts = tmem + S::TM_S + x * BKV;
         int g = 0, c = 0, items = 0;                   // key tiles; steps and items of x
         bool ok = true;
-        for (int r = 0; r < turns.rounds && ok; ++r) {
-          const int id = turns.at(r);
-          if (id < 0) continue;
-          const PairItem it = pair_item(a, plan, id);
+        PairItem it;
+        for (int i = 0; ok && (ok = take_item(bar, i, it, ab, a.status)) && it.jb; ++i) {
+          mbar_arrive(&bar.item_empty[i % kItems]);
           const int steps = x ? it.steps[1] : it.steps[0];
           if (steps) {
             // Q_x is replaced once the S MMAs of its previous item have completed
@@ -497,10 +834,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (!(ok = mbar_wait(&bar.q_full[x], items & 1, ab, a.status))) break;
             ++items;
           }
-          for (int j = 0; j < it.tiles && ok; ++j, ++g) {
-            const int st = (2 * g) % kSlots;
-            if (!(ok = mbar_wait(&bar.full[st], (2 * g / kSlots) & 1, ab, a.status))) break;
-            const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_RING + st * S::TILE), 16, 1024);
+          for (int j = 0; j < it.jb - it.ja && ok; ++j, ++g) {
+            const int st = g % kKSlots;
+            if (!(ok = mbar_wait(&bar.k_full[st], (g / kKSlots) & 1, ab, a.status))) break;
+            const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_K + st * S::TILE), 16, 1024);
             for (int u = 2 * j; u < min(2 * j + 2, steps); ++u, ++c) {
               const int b = c & 1;
               // the PV of two steps before has read P out of the buffer
@@ -518,12 +855,23 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               if (u == steps - 1) mma_commit(&bar.q_empty[x]);
             }
             if (!ok) break;
-            mma_commit(&bar.empty[st]);                // one of the two arrivals for a K slot
+            // one of the two arrivals for a K slot: by a commit only where this thread's MMAs read
+            // it (a commit with nothing before it to wait for could arrive after the CTA has ended)
+            if (2 * j < steps)
+              mma_commit(&bar.k_empty[st]);
+            else
+              mbar_arrive(&bar.k_empty[st]);
           }
         }
-        mma_commit(&bar.drain[x]);
-        mbar_wait(&bar.drain[x], 0, nullptr, a.status);
-        if (items) mbar_wait(&bar.q_full[x], (items - 1) & 1, nullptr, a.status);
+        // wait (bounded) for this thread's MMAs and Q copies
+        if (c > 0) {
+          mma_commit(&bar.drain[x]);
+          mbar_wait(&bar.drain[x], 0, nullptr, a.status);
+        }
+        if (items) {
+          mbar_wait(&bar.q_full[x], (items - 1) & 1, nullptr, a.status);
+          if (ok) mbar_wait(&bar.q_empty[x], (items - 1) & 1, nullptr, a.status);
+        }
       }
     } else {
       // ------------------------------------------------------------------ O += P V
@@ -531,17 +879,17 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint32_t idesc = idesc_bf16_f32(BQ, D, true);
         int g = 0, done[2] = {0, 0};
         bool ok = true;
-        for (int r = 0; r < turns.rounds && ok; ++r) {
-          const int id = turns.at(r);
-          if (id < 0) continue;
-          const PairItem it = pair_item(a, plan, id);
-          for (int j = 0; j < it.tiles && ok; ++j, ++g) {
-            const int st = (2 * g + 1) % kSlots;
-            if (!(ok = mbar_wait(&bar.full[st], ((2 * g + 1) / kSlots) & 1, ab, a.status))) break;
-            const uint64_t vd = sdesc_sw128(smem_u32(smem + S::OFF_RING + st * S::TILE), BKV * 128, 1024);
+        PairItem it;
+        for (int i = 0; ok && (ok = take_item(bar, i, it, ab, a.status)) && it.jb; ++i) {
+          mbar_arrive(&bar.item_empty[i % kItems]);
+          const int steps[2] = {it.steps[0], it.steps[1]};
+          for (int j = 0; j < it.jb - it.ja && ok; ++j, ++g) {
+            const int st = g % kVSlots;
+            if (!(ok = mbar_wait(&bar.v_full[st], (g / kVSlots) & 1, ab, a.status))) break;
+            const uint64_t vd = sdesc_sw128(smem_u32(smem + S::OFF_V + st * S::TILE), BKV * 128, 1024);
             for (int hx = 0; hx < 4; ++hx) {
               const int h = hx >> 1, x = hx & 1, u = 2 * j + h;
-              if (u >= it.steps[x]) continue;
+              if (u >= (x ? steps[1] : steps[0])) continue;
               const int c = done[x], b = c & 1;
               if (!(ok = mbar_wait(&bar.p_full[x][b], (c >> 1) & 1, ab, a.status))) break;
               tc_fence_after();
@@ -553,12 +901,13 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               ++done[x];
             }
             if (!ok) break;
-            mma_commit(&bar.empty[st]);                // both arrivals for a V slot
-            mma_commit(&bar.empty[st]);
+            mma_commit(&bar.v_empty[st]);
           }
         }
-        mma_commit(&bar.drain[2]);
-        mbar_wait(&bar.drain[2], 0, nullptr, a.status);
+        if (done[0] + done[1] > 0) {                     // wait (bounded) for this thread's MMAs
+          mma_commit(&bar.drain[2]);
+          mbar_wait(&bar.drain[2], 0, nullptr, a.status);
+        }
       }
     }
   } else {
@@ -573,30 +922,35 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint32_t o_addr = tmem + S::TM_O + x * BKV + lane_off;
     int g = 0, done = 0;
     bool ok = true;
-    for (int r = 0; r < turns.rounds && ok; ++r) {
-      const int id = turns.at(r);
-      if (id < 0) continue;
-      const PairItem it = pair_item(a, plan, id);
-      const int steps = it.steps[x];
-      if (steps == 0) {
-        g += it.tiles;
+    RowsPolicy<D> pol;
+    pol.a = &a;
+    pol.set_row(row);
+    pol.j0 = pol.split = 0;
+    PairItem it;
+    for (int i = 0; ok; ++i) {
+      if (!(ok = __all_sync(0xffffffffu, take_item(bar, i, it, ab, a.status)))) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.item_empty[i % kItems]);
+      if (!it.jb) break;
+      const int steps = x ? it.steps[1] : it.steps[0];
+      if ((x ? it.all[1] : it.all[0]) == 0) {
+        g += it.jb - it.ja;
         continue;
       }
-      RowsPolicy<D> pol;
-      pol.a = &a;
-      pol.bt_row = a.block_table ? a.block_table + (size_t)it.seq * a.max_pages : nullptr;
+      pol.bt_row = a.block_table ? a.block_table + (size_t)it.s * a.max_pages : nullptr;
       pol.base = it.base;
       pol.n = it.n;
       pol.tok0 = it.tok0 + x * a.tpt;
       pol.P = it.P;
       pol.np = it.np;
       pol.h0 = it.h0;
-      pol.j0 = 0;
-      pol.split = 0;
-      pol.last_tok = min(it.tok0 + 2 * a.tpt, it.n) - 1;   // of the item: V rows that neither tile reads
-      const flash::RowVis vis = pol.row_vis(row);
+      pol.j0 = it.ja;
+      pol.last_tok = min(it.tok0 + a.rows, it.n) - 1;   // of the item: V rows that neither tile reads
+      const int tok = pol.tok0 + pol.trow;              // this thread's token
+      const flash::RowVis vis{tok + 1, 0, -1};
       float m = -INFINITY, l = 0.f;
       typename RowsPolicy<D>::Tile tile, next = pol.tile(0);
+#pragma unroll 1
       for (int u = 0; u < steps; ++u, ++done) {
         const int h = u & 1, b = done & 1;
         if (h == 0) {
@@ -622,10 +976,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           }
         }
         // P with the maximum so far, while the step's own maximum is being found; only where
-        // that one is larger by more than 2^8 (the lazy rescale of flash_tc.cuh, always on an
-        // item's first step) is it formed again
-        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // that one is larger by more than 2^8 (the lazy rescale of flash_tc.cuh) is it formed
+        // again
+        float2 acc[2];
         uint32_t packed[32];
+        acc[0] = acc[1] = make_float2(0.f, 0.f);
         flash::exp2_pack64(v, 0, a.scale_log2, m == -INFINITY ? 0.f : -m, packed, acc);
         const float tmax = flash::row_max_log2(v, a.scale_log2);
         const bool raise = tmax > m + flash::kRescaleLog2;
@@ -654,11 +1009,12 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         if (tile.clear) {
           // V rows that no row of the item may read (flash_tc.cuh, kClearRows), the step's half
-          // of the tile; both row tiles' threads write the same zeros
-          const int gv = 2 * (g + u / 2) + 1, st = gv % kSlots;
-          if (!(ok = warp_wait(&bar.full[st], (gv / kSlots) & 1))) break;
+          // of the tile; both row tiles' threads write the same zeros. K of this tile has
+          // landed, so V's copy, issued before it, is in this phase of its slot or later.
+          const int gv = g + u / 2, st = gv % kVSlots;
+          if (!(ok = warp_wait(&bar.v_full[st], (gv / kVSlots) & 1))) break;
           if (row / kStep == h && !pol.key_read(tile, row)) {
-            uint8_t* vr = smem + S::OFF_RING + st * S::TILE + row * 128;
+            uint8_t* vr = smem + S::OFF_V + st * S::TILE + row * 128;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
 #pragma unroll
@@ -674,16 +1030,98 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
       }
       if (!ok) break;
-      g += it.tiles;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      if (!(ok = warp_wait(&bar.pv_done[x][(done - 1) & 1], ((done - 1) >> 1) & 1))) break;
+      g += it.jb - it.ja;
+      if (steps && !(ok = warp_wait(&bar.pv_done[x][(done - 1) & 1], ((done - 1) >> 1) & 1))) break;
       tc_fence_after();
+      // where this thread's row goes, in elements (-1: no token)
+      const long long at =
+          pol.trow < a.tpt && tok < it.n ? (((long long)it.base + tok) * a.hq + it.h0 + pol.hrow) * D
+                                         : -1;
+      bool write = it.ja == 0 && it.jb == it.tiles;
+      if (!write) {
+        // a part of the item: its partial, and the merge by the last part to arrive
+        float4* rec = partial<D>(a, blockIdx.x, it.ja > 0, x);
+        reinterpret_cast<float2*>(rec + BQ * D / 4)[row] =
+            make_float2(steps ? m : -INFINITY, steps ? l : 0.f);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(o_addr + c * 32, o);
-        tmem_ld_wait();
-        pol.store_chunk(row, c * 32, o, inv, m, l);
+        for (int c = 0; c < (steps ? D / 32 : 0); ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            rec[(c * 8 + e / 4) * BQ + row] =
+                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                            __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+        }
+        __threadfence();
+        group_sync(x);
+        if (quad == 0 && lane == 0)
+          bar.last[x] = atomicAdd(a.tickets + 2 * it.c1 + x, 1) == it.cuts;
+        group_sync(x);
+        write = *reinterpret_cast<volatile int*>(&bar.last[x]) != 0;
+        if (write) __threadfence();
+      }
+      if (write) {
+        const bool merge = it.ja > 0 || it.jb < it.tiles;
+        auto rec_of = [&](int k) { return partial<D>(a, it.c1 - 1 + k, k > 0, x); };
+        auto ml_of = [&](int k) {
+          return __ldcg(reinterpret_cast<const float2*>(rec_of(k) + BQ * D / 4) + row);
+        };
+        if (merge) {
+          m = -INFINITY;
+          l = 0.f;
+          for (int k = 0; k <= it.cuts; ++k) m = fmaxf(m, ml_of(k).x);
+          for (int k = 0; k <= it.cuts; ++k) {
+            const float2 r = ml_of(k);
+            if (r.x > -INFINITY) l += r.y * exp2f(r.x - m);
+          }
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if (a.lse && at >= 0)
+          a.lse[(size_t)(it.h0 + pol.hrow) * a.total + it.base + tok] =
+              l > 0.f ? m + log2f(l) : -INFINITY;
+        // 64 columns at a time, exchanged in groups of 8 lanes so that these write 128 bytes of a
+        // row (a thread writing its own row took 5,000 cycles per item; staging in shared memory
+        // would take a fifth of the ring, which costs 9 %)
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          float o[64];
+          if (!merge) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              tmem_ld32(o_addr + c * 64 + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(o + 32 * k));
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) o[e] = 0.f;
+            for (int k = 0; k <= it.cuts; ++k) {
+              const float mk = ml_of(k).x;
+              const float wt = mk > -INFINITY ? exp2f(mk - m) : 0.f;
+              if (!__any_sync(0xffffffffu, wt > 0.f)) continue;   // an empty part wrote no O
+              const float4* r = rec_of(k) + c * 16 * BQ + row;
+#pragma unroll
+              for (int e = 0; e < 64; e += 4) {
+                const float4 v4 = __ldcg(r + (e / 4) * BQ);
+                o[e] += v4.x * wt;
+                o[e + 1] += v4.y * wt;
+                o[e + 2] += v4.z * wt;
+                o[e + 3] += v4.w * wt;
+              }
+            }
+          }
+          uint32_t w[32];                              // 8 chunks of 16 bytes
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = flash::pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+          transpose8(w, lane);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {                // w[4k..]: chunk lane & 7 of the group's row k
+            const long long to = __shfl_sync(0xffffffffu, at, (lane & 24) + k);
+            if (to >= 0)
+              *reinterpret_cast<uint4*>(a.o + to + c * 64 + (lane & 7) * 8) =
+                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
+        }
       }
       tc_fence_before();
     }
@@ -734,14 +1172,11 @@ cudaError_t launch_rows(const PackedAttn& p, const PackedPlan& plan, AttnArgs& a
     static std::atomic<int> attr_pair[64];
     cudaError_t e = set_smem_limit_once(pair_kernel<D>, SP::TOTAL, attr_pair);
     if (e != cudaSuccess) return e;
-    size_t off = 0;
-    const packed::Plan list =
-        packed::carve_plan(workspace, off, p.batch, p.total, 2 * plan.tpt, false);
-    e = packed::launch_plan(list, p.cu, p.seq_lens, a.max_pages, p.batch, p.total, 2 * plan.tpt,
-                            p.status, stream);
-    if (e != cudaSuccess) return e;
-    pair_kernel<D><<<(unsigned)plan.ctas, PAIR_THREADS, SP::TOTAL, stream>>>(tq, tk, tv, tkp, tvp,
-                                                                             a, list);
+    if (a.can_split) {
+      e = cudaMemsetAsync(a.tickets, 0, plan.ctas * 2 * sizeof(int32_t), stream);
+      if (e != cudaSuccess) return e;
+    }
+    pair_kernel<D><<<(unsigned)plan.ctas, PAIR_THREADS, SP::TOTAL, stream>>>(tq, tk, tv, tkp, tvp, a);
     count_launches(1);
     return cudaGetLastError();
   }
@@ -773,11 +1208,15 @@ PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len
   const long long pairs = packed::max_tiles(batch, total, 2 * p.tpt) * hkv * (G / p.gp);
   if (total > (long long)batch * p.tpt && pairs >= num_sms()) {
     p.pair = true;
+    p.xt = 2;
     p.nsplit = 1;
     p.split_tiles = tiles;
-    p.items = pairs;
+    p.items = packed::max_tiles(batch, total, p.xt * p.tpt) * hkv * (G / p.gp);
+    p.can_split = tiles >= 2 * kMinPart;
     p.ctas = num_sms();
-    packed::carve_plan(nullptr, p.ws_bytes, batch, total, 2 * p.tpt, false);
+    p.ticket_bytes = packed::align256(p.ctas * 2 * sizeof(int32_t));
+    if (p.can_split)
+      p.ws_bytes = p.ticket_bytes + (size_t)p.ctas * 4 * (BQ * (d + 2)) * sizeof(float);
     return p;
   }
   long long nsplit = 1;
@@ -814,7 +1253,11 @@ cudaError_t launch_packed_attn(const PackedAttn& p, const PackedPlan& plan, void
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.o = p.o;
   a.lse = p.lse;
-  a.part = static_cast<float*>(workspace);
+  a.xt = plan.xt;
+  a.rows = plan.xt * plan.tpt;
+  a.can_split = plan.can_split;
+  a.tickets = static_cast<int32_t*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.ticket_bytes);
   a.status = p.status;
   return p.d == 64 ? launch_rows<64>(p, plan, a, workspace, stream)
                    : launch_rows<128>(p, plan, a, workspace, stream);

@@ -50,6 +50,22 @@ def test_packed_group_sizes(heads):
     check_packed(x, o, lse)
 
 
+# Many rows: two row tiles per item, several items per SM and items divided among SMs.
+MANY = [([301, 40, 0, 517, 18, 19, 203, 37, 90, 200], (28, 4, 128)),
+        ([600, 1, 35, 36, 37, 0, 513, 300, 128, 127, 129, 400, 250, 77, 150], (14, 2, 64)),
+        ([1400], (28, 4, 128)), ([18] * 90, (28, 4, 128)), ([2000, 700], (4, 4, 64))]
+
+
+@pytest.mark.parametrize("lens, heads", MANY, ids=str)
+def test_packed_many_rows(lens, heads):
+    x = make(lens, *heads, seed=31, tail=5, lead=1)
+    o, lse, st = run_packed(cuda(x))
+    assert st == 0
+    check_packed(x, o, lse)
+    again, lse2, _ = run_packed(cuda(x))
+    assert same(o, again) and same(lse, lse2)
+
+
 def test_packed_many_sequences_and_leading_rows():
     x = make([(i * 7) % 23 for i in range(75)], 4, 2, 64, seed=6, lead=5, tail=4)
     o, lse, st = run_packed(cuda(x))
@@ -261,6 +277,23 @@ def test_chunk_matches_oracle(lens, old, heads):
     o, st = run_chunk(cuda(x))
     assert st == 0
     check_chunk(x, o)
+
+
+@pytest.mark.parametrize("lens, old, heads", [
+    ([301, 40, 0, 217, 18, 1, 203, 37, 590], [300, 0, 77, 1000, 513, 129, 5, 700, 16], (28, 4, 128)),
+    ([600, 1, 35, 36, 37, 0, 513, 300, 1, 127, 129, 400, 250, 77, 150],
+     [0, 900, 64, 1, 2000, 9, 128, 130, 3000, 40, 0, 15, 16, 17, 250], (14, 2, 64)),
+    ([1, 700, 1, 1], [4000, 1500, 17, 900], (28, 4, 128)), ([1] * 64, list(range(0, 1600, 25)), (28, 4, 128))],
+    ids=["ragged128", "ragged64", "mixed", "tokens"])
+def test_chunk_many_rows(lens, old, heads):
+    x = make(lens, *heads, seed=32, old=old, tail=3)
+    y = cuda(x)
+    o, st = run_chunk(y)
+    assert st == 0
+    check_chunk(x, o)
+    for _ in range(20):                   # back to back, with different neighbours in time
+        again, st = run_chunk(y)
+        assert st == 0 and same(o, again)
 
 
 @pytest.mark.parametrize("hint", [0, 100, 100000])
