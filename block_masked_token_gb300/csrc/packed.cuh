@@ -5,6 +5,8 @@
 // total / rows_per_tile + batch, which sizes the grids on the host.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 
 namespace mars {
@@ -84,16 +86,77 @@ struct Plan {
   Tile* in_order;     // gradient: by global tile index
 };
 
-// The items of a persistent CTA, by round: rounds run forwards and backwards over the CTAs, so that the costs even out.
-struct Turns {
-  int total, rounds;
-  MARS_DEV explicit Turns(int n) : total(n), rounds((n + (int)gridDim.x - 1) / (int)gridDim.x) {}
-  MARS_DEV int at(int r) const {
+// The items (tile of a list, head) of a persistent CTA. Rounds run forwards and backwards over
+// the CTAs, so that the costs even out. The next item's tile is read while the current one is
+// worked on: at its turn the read cost 800 cycles and more.
+struct Walk {
+  const Tile* list;
+  int heads, total, round, id;         // items per tile, items; the next item (id -1: none)
+  Tile tile;                           // tile of the next item
+  MARS_DEV Walk(const int32_t* count, const Tile* l, int heads_per_tile)
+      : list(l), heads(heads_per_tile), total(*count * heads_per_tile), round(0), id(-1) {
+    fetch();
+  }
+  MARS_DEV void fetch() {
     const int g = gridDim.x, c = blockIdx.x;
-    const int id = r * g + ((r & 1) ? g - 1 - c : c);
-    return id < total ? id : -1;
+    id = round * g + ((round & 1) ? g - 1 - c : c);
+    if (id >= total) id = -1;
+    if (id >= 0) tile = list[id / heads];
+  }
+  // The next item's tile and its number among the tile's items.
+  MARS_DEV bool take(Tile& t, int& head) {
+    if (id < 0) return false;
+    t = tile;
+    head = id % heads;
+    ++round;
+    fetch();
+    return true;
   }
 };
+
+// Transpose chunks of 16 bytes within groups of N lanes: before, lane i of the group holds the
+// N chunks of row i in w; after, w[4k ..] is chunk i of row k.
+template <int N>
+MARS_DEV void transpose_chunks(uint32_t (&w)[4 * N], int lane) {
+#pragma unroll
+  for (int s = N / 2; s > 0; s >>= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i & s) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t &lo = w[4 * i + e], &hi = w[4 * (i | s) + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+        lo = up ? got : lo;
+        hi = up ? hi : got;
+      }
+    }
+  }
+}
+
+// Store COLS values per lane, get(0) .. get(COLS - 1), as bf16 to out + at (at < 0: nowhere).
+// Whole warp. Lanes exchange chunks first, so that a store instruction writes runs of 2 COLS
+// bytes: with a row per lane it touched 32 lines for 512 bytes, and the output of a 128 x 128
+// tile by eight warps took about 2,500 cycles.
+template <int COLS, class F>
+MARS_DEV void store_rows(uint16_t* out, long long at, int lane, F get) {
+  constexpr int N = COLS / 8;                      // chunks per row
+  uint32_t w[COLS / 2];
+#pragma unroll
+  for (int e = 0; e < COLS / 2; ++e) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(get(2 * e), get(2 * e + 1));
+    w[e] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  transpose_chunks<N>(w, lane);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const long long to = __shfl_sync(0xffffffffu, at, (lane & (32 - N)) + k);
+    if (to >= 0)
+      *reinterpret_cast<uint4*>(out + to + (lane & (N - 1)) * 8) =
+          make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
+}
 
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 

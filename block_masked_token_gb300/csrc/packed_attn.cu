@@ -657,25 +657,6 @@ MARS_DEV bool take_item(PairBar& bar, int i, PairItem& it, volatile int* ab, int
   return true;
 }
 
-// In each group of 8 lanes: lane i's chunk j (4 words of w) becomes lane j's chunk i.
-MARS_DEV void transpose8(uint32_t (&w)[32], int lane) {
-#pragma unroll
-  for (int s = 4; s > 0; s >>= 1) {
-    const bool up = (lane & s) != 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i & s) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t &lo = w[4 * i + e], &hi = w[4 * (i | s) + e];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
-        lo = up ? got : lo;
-        hi = up ? hi : got;
-      }
-    }
-  }
-}
-
 MARS_DEV void group_sync(int x) {                  // the 128 threads of a softmax warpgroup
   asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
 }
@@ -1110,17 +1091,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               }
             }
           }
-          uint32_t w[32];                              // 8 chunks of 16 bytes
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = flash::pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-          transpose8(w, lane);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {                // w[4k..]: chunk lane & 7 of the group's row k
-            const long long to = __shfl_sync(0xffffffffu, at, (lane & 24) + k);
-            if (to >= 0)
-              *reinterpret_cast<uint4*>(a.o + to + c * 64 + (lane & 7) * 8) =
-                  make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-          }
+          packed::store_rows<64>(a.o + c * 64, at, lane, [&](int e) { return o[e] * inv; });
         }
       }
       tc_fence_before();

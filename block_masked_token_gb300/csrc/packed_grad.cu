@@ -38,7 +38,7 @@ namespace {
 
 using namespace sm100;
 using packed::Tile;
-using packed::Turns;
+using packed::Walk;
 
 constexpr int GT = 128;                 // rows per key tile and per query tile
 constexpr int MATH_WARPS = 8;           // two per TMEM lane quadrant, 64 columns each
@@ -55,7 +55,7 @@ struct GradArgs {
   float *lse_p, *d_p;                   // [hq][pad]
   uint16_t *dq, *dk, *dv;
   long long dq_stride, dk_stride, dv_stride;
-  float* part;                          // [nsplit][2][total][hkv][D] with several splits
+  float* part;                          // partial() with several splits
   int32_t* status;
 };
 
@@ -139,21 +139,32 @@ struct KItem {
   int kvh, sp, g0, ng, nq, pairs;
 };
 
-MARS_DEV KItem k_item(const GradArgs& a, int id) {
-  KItem it;
-  it.sp = id % a.nsplit;
-  id /= a.nsplit;
-  it.kvh = id % a.hkv;
-  it.t = a.plan.second[id / a.hkv];
+MARS_DEV Walk k_walk(const GradArgs& a) {
+  return Walk(a.plan.count, a.plan.second, a.hkv * a.nsplit);
+}
+
+MARS_DEV bool take(const GradArgs& a, Walk& w, KItem& it) {
+  int i;
+  if (!w.take(it.t, i)) return false;
+  it.kvh = i / a.nsplit;
+  it.sp = i % a.nsplit;
   it.g0 = a.G * it.sp / a.nsplit;
   it.ng = a.G * (it.sp + 1) / a.nsplit - it.g0;
   it.nq = (it.t.n + GT - 1) / GT - it.t.tile;
   it.pairs = it.ng * it.nq;
-  return it;
+  return true;
 }
 
 constexpr int K_THREADS = 96 + MATH_THREADS;     // loader, S/dP issuer, math, dV/dK issuer
 constexpr int K_TS_WARP = 2 + MATH_WARPS;
+
+// Partial dV (and D / 4 x 128 float4 further on dK) of an item: [column / 4][row], so that the
+// lanes of a warp, a row each, access consecutive places.
+template <int D>
+MARS_DEV float4* partial(const GradArgs& a, int tile, int kvh, int sp) {
+  return reinterpret_cast<float4*>(a.part) +
+         (((size_t)tile * a.hkv + kvh) * a.nsplit + sp) * (2 * GT * D / 4);
+}
 
 // TMEM column of K-step k (16 queries) of P^T or dS^T: queries [0, 64) over columns [0, 32),
 // [64, 128) over [64, 96), the first half of each half's own fp32 columns.
@@ -171,8 +182,8 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* ab = &bar.abort;
-  const Turns turns(*a.plan.count * a.hkv * a.nsplit);
-  if (turns.at(0) < 0) return;                         // more CTAs than items
+  Walk walk = k_walk(a);
+  if (walk.id < 0) return;                             // more CTAs than items
 
   if (threadIdx.x == 0) {
     bar.abort = 0;
@@ -210,10 +221,8 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (lane == 0) {
       int gp = 0, ii = 0, nkv = 0;
       bool ok = true;
-      for (int r = 0; r < turns.rounds && ok; ++r) {
-        const int id = turns.at(r);
-        if (id < 0) continue;
-        const KItem it = k_item(a, id);
+      KItem it;
+      while (ok && take(a, walk, it)) {
         if (ii > 0 && !(ok = mbar_wait(&bar.kv_empty, (ii - 1) & 1, ab, a.status))) break;
         mbar_arrive_expect_tx(&bar.kv_full, 2 * S::T_BYTES);
         const int z = it.t.base + GT * it.t.tile;
@@ -246,7 +255,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------- S^T and dP^T MMAs
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t id_qk = idesc_bf16_f32(GT, GT / 2, false);
       const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_K), 16, 1024);
       const uint64_t vd = sdesc_sw128(smem_u32(smem + S::OFF_V), 16, 1024);
@@ -270,10 +279,9 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       };
       int gp = 0, ii = 0;
       bool ok = true;
-      for (int r = 0; r < turns.rounds && ok; ++r) {
-        const int id = turns.at(r);
-        if (id < 0) continue;
-        const int np = k_item(a, id).pairs;
+      KItem it;
+      while (ok && take(a, walk, it)) {
+        const int np = it.pairs;
         if (!(ok = mbar_wait(&bar.kv_full, ii & 1, ab, a.status))) break;
         for (int p = 0; p < np && ok; ++p, ++gp)
           ok = mbar_wait(&bar.full[gp % NSTAGE], (gp / NSTAGE) & 1, ab, a.status) &&
@@ -288,14 +296,13 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
   } else if (warp == K_TS_WARP) {
     // -------------------------------------------------------- dV and dK MMAs
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t id_acc = idesc_bf16_f32(GT, D, true);     // A from TMEM, B MN-major
       int gp = 0, ii = 0;
       bool ok = true;
-      for (int r = 0; r < turns.rounds && ok; ++r) {
-        const int id = turns.at(r);
-        if (id < 0) continue;
-        const int np = k_item(a, id).pairs;
+      KItem it;
+      while (ok && take(a, walk, it)) {
+        const int np = it.pairs;
         for (int p = 0; p < np; ++p, ++gp) {
           const int st = gp % NSTAGE;
           const uint32_t sb = smem_u32(smem + S::OFF_RING + st * S::STAGE);
@@ -343,10 +350,8 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     };
     int gp = 0, ii = 0;
     bool ok = true;
-    for (int r = 0; r < turns.rounds && ok; ++r) {
-      const int id = turns.at(r);
-      if (id < 0) continue;
-      const KItem it = k_item(a, id);
+    KItem it;
+    while (ok && take(a, walk, it)) {
       const int kk = GT * it.t.tile + row;             // key position in its sequence
       for (int p = 0; p < it.pairs; ++p, ++gp) {
         const int st = gp % NSTAGE;
@@ -457,37 +462,24 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive_warp(&bar.acc_free);
-      if (kk < it.t.n) {
-        const size_t tok = (size_t)it.t.base + kk;
-        if (a.nsplit == 1) {
-          uint4* ov = reinterpret_cast<uint4*>(a.dv + tok * a.dv_stride + it.kvh * D + HD * half);
-          uint4* ok4 = reinterpret_cast<uint4*>(a.dk + tok * a.dk_stride + it.kvh * D + HD * half);
+      if (a.nsplit == 1) {
+        const long long tok = (long long)it.t.base + kk;
+        const int col = it.kvh * D + HD * half;
+        const bool rv = kk < it.t.n;
+        packed::store_rows<HD>(a.dv, rv ? tok * a.dv_stride + col : -1, lane,
+                               [&](int e) { return __uint_as_float(dvr[e]); });
+        packed::store_rows<HD>(a.dk, rv ? tok * a.dk_stride + col : -1, lane,
+                               [&](int e) { return __uint_as_float(dkr[e]) * a.scale; });
+      } else {
+        float4* pv = partial<D>(a, it.t.id, it.kvh, it.sp) + (HD / 4) * half * GT + row;
+        float4* pk = pv + GT * D / 4;
 #pragma unroll
-          for (int e = 0; e < HD; e += 8) {
-            uint32_t wv[4], wk[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              wv[i] = flash::pack_bf16x2(__uint_as_float(dvr[e + 2 * i]),
-                                         __uint_as_float(dvr[e + 2 * i + 1]));
-              wk[i] = flash::pack_bf16x2(__uint_as_float(dkr[e + 2 * i]) * a.scale,
-                                         __uint_as_float(dkr[e + 2 * i + 1]) * a.scale);
-            }
-            ov[e / 8] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
-            ok4[e / 8] = make_uint4(wk[0], wk[1], wk[2], wk[3]);
-          }
-        } else {
-          const size_t plane = (size_t)a.total * a.hkv * D;
-          float* ov = a.part + 2 * it.sp * plane + (tok * a.hkv + it.kvh) * D + HD * half;
-          float* ok4 = ov + plane;
-#pragma unroll
-          for (int e = 0; e < HD; e += 4) {
-            *reinterpret_cast<float4*>(ov + e) =
-                make_float4(__uint_as_float(dvr[e]), __uint_as_float(dvr[e + 1]),
-                            __uint_as_float(dvr[e + 2]), __uint_as_float(dvr[e + 3]));
-            *reinterpret_cast<float4*>(ok4 + e) = make_float4(
-                __uint_as_float(dkr[e]) * a.scale, __uint_as_float(dkr[e + 1]) * a.scale,
-                __uint_as_float(dkr[e + 2]) * a.scale, __uint_as_float(dkr[e + 3]) * a.scale);
-          }
+        for (int e = 0; e < HD; e += 4) {
+          pv[(e / 4) * GT] = make_float4(__uint_as_float(dvr[e]), __uint_as_float(dvr[e + 1]),
+                                         __uint_as_float(dvr[e + 2]), __uint_as_float(dvr[e + 3]));
+          pk[(e / 4) * GT] = make_float4(
+              __uint_as_float(dkr[e]) * a.scale, __uint_as_float(dkr[e + 1]) * a.scale,
+              __uint_as_float(dkr[e + 2]) * a.scale, __uint_as_float(dkr[e + 3]) * a.scale);
         }
       }
       ++ii;
@@ -506,25 +498,25 @@ template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(GradArgs a) {
   if ((int)blockIdx.x >= *a.plan.count) return;
   const Tile t = a.plan.in_order[blockIdx.x];
-  const int rows = min(GT, t.n - t.tile * GT);
-  const size_t plane = (size_t)a.total * a.hkv * D;
-  const int per = a.hkv * D / 4;
-  for (int i = threadIdx.x + blockIdx.y * 256; i < 2 * rows * per; i += 256 * gridDim.y) {
-    const int which = i >= rows * per, j = which ? i - rows * per : i;
-    const int r = j / per, c = (j - r * per) * 4;
-    const size_t tok = (size_t)t.base + t.tile * GT + r;
-    const float* src = a.part + which * plane + tok * a.hkv * D + c;
-    float4 s = *reinterpret_cast<const float4*>(src);
-    for (int sp = 1; sp < a.nsplit; ++sp) {
-      const float4 u = *reinterpret_cast<const float4*>(src + 2 * sp * plane);
-      s.x += u.x;
-      s.y += u.y;
-      s.z += u.z;
-      s.w += u.w;
+  constexpr int PLANE = GT * D / 4;
+  const int n = a.hkv * 2 * GT * D / 8;                // chunks of 8 columns of a row
+  for (int i = threadIdx.x + 256 * blockIdx.y; i < n; i += 256 * gridDim.y) {
+    const int row = i % GT, c = i / GT % (D / 8), which = i / (GT * D / 8) % 2;
+    const int kvh = i / (2 * GT * D / 8);
+    const int pos = GT * t.tile + row;
+    if (pos >= t.n) continue;
+    const float4* p = partial<D>(a, t.id, kvh, 0) + which * PLANE + 2 * c * GT + row;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (int sp = 0; sp < a.nsplit; ++sp, p += 2 * PLANE) {
+      const float4 u = p[0], v = p[GT];
+      x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+      y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
     }
-    uint16_t* dst = which ? a.dk + tok * a.dk_stride + c : a.dv + tok * a.dv_stride + c;
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(flash::pack_bf16x2(s.x, s.y), flash::pack_bf16x2(s.z, s.w));
+    const size_t tok = (size_t)t.base + pos;
+    uint16_t* dst = (which ? a.dk + tok * a.dk_stride : a.dv + tok * a.dv_stride) + kvh * D + 8 * c;
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(flash::pack_bf16x2(x.x, x.y), flash::pack_bf16x2(x.z, x.w),
+                   flash::pack_bf16x2(y.x, y.y), flash::pack_bf16x2(y.z, y.w));
   }
 }
 
@@ -545,12 +537,12 @@ struct QItem {
   int h, n;      // query head, key tiles
 };
 
-MARS_DEV QItem q_item(const GradArgs& a, int id) {
-  QItem it;
-  it.h = id % a.hq;
-  it.t = a.plan.first[id / a.hq];
+MARS_DEV Walk q_walk(const GradArgs& a) { return Walk(a.plan.count, a.plan.first, a.hq); }
+
+MARS_DEV bool take(Walk& w, QItem& it) {
+  if (!w.take(it.t, it.h)) return false;
   it.n = it.t.tile + 1;
-  return it;
+  return true;
 }
 
 template <int D>
@@ -567,8 +559,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Turns turns(*a.plan.count * a.hq);
-  if (turns.at(0) < 0) return;                         // more CTAs than items
+  Walk walk = q_walk(a);
+  if (walk.id < 0) return;                             // more CTAs than items
   if (threadIdx.x == 0) {
     mbar_init(&qb.s_full, 1);
     mbar_init(&qb.dp_full, 1);
@@ -606,10 +598,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                   : flash::load_ring_item<D, flash::K_STAGES>(bar, smem, n, j0, last_k, drain,
                                                               a.status, false, issue);
     };
-    for (int r = 0; r < turns.rounds; ++r) {
-      const int id = turns.at(r);
-      if (id < 0) continue;
-      const QItem it = q_item(a, id);
+    QItem it;
+    while (take(walk, it)) {
       z = it.t.base;
       kvh = it.h / a.G;
       if (!ring(it.n, false)) break;
@@ -617,7 +607,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     }
     ring(0, true);                                   // wait (bounded) for copies in flight
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t id_s = idesc_bf16_f32(GT, GT, false);
       const uint64_t qd = sdesc_sw128(smem_u32(smem + S::OFF_Q), 16, 1024);
       const uint64_t dd = sdesc_sw128(smem_u32(smem + S::OFF_STAGE), 16, 1024);
@@ -632,10 +622,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         }
         mma_commit(full);
       };
-      for (int r = 0; r < turns.rounds && ok; ++r) {
-        const int id = turns.at(r);
-        if (id < 0) continue;
-        const QItem it = q_item(a, id);
+      QItem it;
+      while (ok && take(walk, it)) {
         // Q and dO are replaced once the previous item's S and dP MMAs have completed
         if (i > 0 && !(ok = mbar_wait(&bar.q_empty, (i - 1) & 1, ab, a.status))) break;
         mbar_arrive_expect_tx(&bar.q_full, 2 * S::Q_BYTES);
@@ -670,15 +658,13 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       if (nq > 0) mbar_wait(&bar.q_full, (nq - 1) & 1, nullptr, a.status);
     }
   } else if (warp == Q_TS_WARP) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t id_q = idesc_bf16_f32(GT, D, true);       // A from TMEM, B MN-major
       int jg = 0, i = 0;
       bool ok = true;
-      for (int r = 0; r < turns.rounds && ok; ++r) {
-        const int id = turns.at(r);
-        if (id < 0) continue;
-        const int n = q_item(a, id).n;
-        for (int j = 0; j < n; ++j, ++jg) {
+      QItem it;
+      while (ok && take(walk, it)) {
+        for (int j = 0; j < it.n; ++j, ++jg) {
           const int st = jg % flash::K_STAGES;
           // the previous item's accumulator has been read out
           ok = (j > 0 || i == 0 || mbar_wait(&qb.acc_free, (i - 1) & 1, ab, a.status)) &&
@@ -712,14 +698,17 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     };
     int jg = 0, i = 0;
     bool ok = true;
-    for (int r = 0; r < turns.rounds && ok; ++r) {
-      const int id = turns.at(r);
-      if (id < 0) continue;
-      const QItem it = q_item(a, id);
+    // lse and D of this thread's row of an item (zeros past the sequence), read ahead
+    auto stats = [&](const Tile& t, int h) {
+      const size_t at = (size_t)h * a.pad + (size_t)t.id * GT + row;
+      return make_float2(a.lse_p[at], a.d_p[at]);
+    };
+    float2 ahead = stats(walk.tile, walk.id % a.hq);
+    QItem it;
+    while (ok && take(walk, it)) {
       const int live = it.t.n - GT * it.t.tile;         // query rows of the tile
       const bool rv = row < live;
-      const size_t sr = (size_t)it.h * a.pad + (size_t)it.t.id * GT + row;
-      const float lse = a.lse_p[sr], dd = a.d_p[sr];    // zeros past the sequence
+      const float lse = ahead.x, dd = ahead.y;
       for (int j = 0; j < it.n; ++j, ++jg) {
         const bool diag = j == it.t.tile;
         if (!(ok = warp_wait(&qb.s_full, jg & 1))) break;
@@ -793,6 +782,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         mbar_arrive_warp(&qb.ds_full);
       }
       if (!ok) break;
+      if (walk.id >= 0) ahead = stats(walk.tile, walk.id % a.hq);
       if (!(ok = warp_wait(&bar.o_final, i & 1))) break;
       tc_fence_after();
       constexpr int HD = D / 2;
@@ -804,19 +794,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive_warp(&qb.acc_free);
-      if (rv) {
-        uint4* dst = reinterpret_cast<uint4*>(
-            a.dq + ((size_t)it.t.base + GT * it.t.tile + row) * a.dq_stride + it.h * D + HD * half);
-#pragma unroll
-        for (int e = 0; e < HD; e += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            w[c] = flash::pack_bf16x2(__uint_as_float(o[e + 2 * c]) * a.scale,
-                                      __uint_as_float(o[e + 2 * c + 1]) * a.scale);
-          dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+      const long long at =
+          rv ? ((long long)it.t.base + GT * it.t.tile + row) * a.dq_stride + it.h * D + HD * half : -1;
+      packed::store_rows<HD>(a.dq, at, lane,
+                             [&](int e) { return __uint_as_float(o[e]) * a.scale; });
       ++i;
     }
   }
@@ -832,7 +813,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
 
 // Query-head splits of a KV head's items: enough items for about kWaves per SM, so that the
 // heaviest ones (the first keys of long sequences) can be evened out.
-constexpr int kWaves = 4;
+constexpr int kWaves = 2;
 
 int grad_splits(int batch, int total, int hq, int hkv) {
   const long long items = packed::max_tiles(batch, total, GT) * hkv;
@@ -860,7 +841,7 @@ GradSpace carve(void* base, int batch, int total, int hq, int hkv, int d) {
   g.lse_p = take(rows * hq);
   g.d_p = take(rows * hq);
   const int ns = grad_splits(batch, total, hq, hkv);
-  g.part = take(ns > 1 ? (size_t)ns * 2 * total * hkv * d : 0);
+  g.part = take(ns > 1 ? (size_t)ns * 2 * rows * hkv * d : 0);
   g.bytes = off;
   return g;
 }
