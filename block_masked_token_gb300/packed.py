@@ -34,10 +34,13 @@ def _refuse(t, name, dtype, shape, dev):
 
 def _ptr(t, name, dtype, shape, dev):
     """Address of a contiguous tensor."""
-    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or
-            t.shape != shape or not t.is_contiguous()):
-        _refuse(t, name, dtype, shape, dev)
-    return t.data_ptr()
+    try:
+        if (t.get_device() == dev and t.dtype is dtype and t.shape == shape and
+                t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:                       # not a tensor
+        pass
+    _refuse(t, name, dtype, shape, dev)
 
 
 def _opt(t, name, dtype, shape, dev):
@@ -47,8 +50,11 @@ def _opt(t, name, dtype, shape, dev):
 def _rows(t, name, shape, dev):
     """Address and row pitch, in elements, of a bf16 [total, heads, d] tensor whose rows may be
     slices of a wider tensor (the heads of a row contiguous)."""
-    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != _BF16 or
-            t.shape != shape):
+    try:
+        good = t.get_device() == dev and t.dtype is _BF16 and t.shape == shape
+    except AttributeError:
+        good = False
+    if not good:
         _refuse(t, name, _BF16, shape, dev)
     total, heads, d = shape
     pitch, head, one = t.stride()
@@ -64,10 +70,15 @@ def _rows(t, name, shape, dev):
     return t.data_ptr(), pitch
 
 
-def _target(stream):
+def _target(first, name, stream):
     """Device and raw handle of the stream that a call goes to; the device has to be current
-    (the library launches there)."""
-    dev = torch.cuda.current_device()
+    (the library launches there). first: a tensor argument, since a host tensor is refused
+    before the CUDA runtime is asked for anything."""
+    if not isinstance(first, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not first.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libmars has no CPU path)")
+    dev = torch._C._cuda_getDevice()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
     if stream.device.index != dev:
@@ -76,16 +87,14 @@ def _target(stream):
     return dev, stream.cuda_stream
 
 
-def _need_cuda(t, name):
-    """A host tensor is refused before the CUDA runtime is asked for anything."""
-    if isinstance(t, torch.Tensor) and not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (libmars has no CPU path)")
-
-
-def _batch(cu_seqlens):
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+def _batch(cu_seqlens, dev):
+    """Address of the boundaries and the number of sequences."""
+    if not isinstance(cu_seqlens, torch.Tensor):
         raise ValueError("cu_seqlens must hold batch + 1 boundaries")
-    return cu_seqlens.shape[0] - 1
+    shape = cu_seqlens.shape
+    if len(shape) != 1 or shape[0] < 1:
+        raise ValueError("cu_seqlens must hold batch + 1 boundaries")
+    return _ptr(cu_seqlens, "cu_seqlens", _I32, shape, dev), shape[0] - 1
 
 
 def _table(block_table, batch, dev):
@@ -115,17 +124,16 @@ def mars_attn_packed(q, k, v, cu_seqlens, o, workspace, lse=None, scale: float =
                      status=None, stream=None):
     """o[total, hq, d] (bf16) = causal attention inside each sequence of a packed batch; lse
     [hq, total] (float32, optional) its log2 row statistics (see include/mars.h)."""
-    _need_cuda(q, "q")
-    dev, raw = _target(stream)
+    dev, raw = _target(q, "q", stream)
     total, hq, d = q.shape
     hkv = k.shape[1]
-    batch = _batch(cu_seqlens)
+    cu, batch = _batch(cu_seqlens, dev)
     qp, qs = _rows(q, "q", (total, hq, d), dev)
     kp, ks = _rows(k, "k", (total, hkv, d), dev)
     vp, vs = _rows(v, "v", (total, hkv, d), dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _rc(lib().mars_attn_packed(
-        qp, kp, vp, _ptr(cu_seqlens, "cu_seqlens", _I32, (batch + 1,), dev),
+        qp, kp, vp, cu,
         _ptr(o, "o", _BF16, (total, hq, d), dev), _opt(lse, "lse", _F32, (hq, total), dev), batch,
         total, hq, hkv, d, qs, ks, vs, scale, ws, ws_bytes,
         _opt(status, "status", _I32, (1,), dev), raw), "mars_attn_packed")
@@ -135,11 +143,10 @@ def mars_attn_packed_grad(q, k, v, o, d_o, lse, cu_seqlens, dq, dk, dv, workspac
                           scale: float = 0.0, status=None, stream=None):
     """dq, dk, dv (bf16) of mars_attn_packed for the upstream gradient d_o, from its o and lse
     (see include/mars.h); dq, dk, dv may be slices of a wider tensor, like q, k, v."""
-    _need_cuda(q, "q")
-    dev, raw = _target(stream)
+    dev, raw = _target(q, "q", stream)
     total, hq, d = q.shape
     hkv = k.shape[1]
-    batch = _batch(cu_seqlens)
+    cu, batch = _batch(cu_seqlens, dev)
     qp, qs = _rows(q, "q", (total, hq, d), dev)
     kp, ks = _rows(k, "k", (total, hkv, d), dev)
     vp, vs = _rows(v, "v", (total, hkv, d), dev)
@@ -150,7 +157,7 @@ def mars_attn_packed_grad(q, k, v, o, d_o, lse, cu_seqlens, dq, dk, dv, workspac
     _rc(lib().mars_attn_packed_grad(
         qp, kp, vp, _ptr(o, "o", _BF16, (total, hq, d), dev),
         _ptr(d_o, "d_o", _BF16, (total, hq, d), dev), _ptr(lse, "lse", _F32, (hq, total), dev),
-        _ptr(cu_seqlens, "cu_seqlens", _I32, (batch + 1,), dev), dqp, dkp, dvp, batch, total, hq,
+        cu, dqp, dkp, dvp, batch, total, hq,
         hkv, d, qs, ks, vs, dqs, dks, dvs, scale, ws, ws_bytes,
         _opt(status, "status", _I32, (1,), dev), raw), "mars_attn_packed_grad")
 
@@ -160,11 +167,10 @@ def mars_attn_chunk(q, k, v, cu_seqlens, k_pool, v_pool, block_table, seq_lens,
                     stream=None):
     """o[total, hq, d] (bf16) = attention of each sequence's new rows over its seq_lens[s]
     cached tokens and, causally, its own new keys (see include/mars.h)."""
-    _need_cuda(q, "q")
-    dev, raw = _target(stream)
+    dev, raw = _target(q, "q", stream)
     total, hq, d = q.shape
     hkv = k.shape[1]
-    batch = _batch(cu_seqlens)
+    cu, batch = _batch(cu_seqlens, dev)
     pages = k_pool.shape[0]
     pool = (pages, hkv, PAGE_SIZE, d)
     qp, qs = _rows(q, "q", (total, hq, d), dev)
@@ -173,7 +179,7 @@ def mars_attn_chunk(q, k, v, cu_seqlens, k_pool, v_pool, block_table, seq_lens,
     table, width = _table(block_table, batch, dev)
     ws, ws_bytes = _workspace(workspace, dev)
     _rc(lib().mars_attn_chunk(
-        qp, kp, vp, _ptr(cu_seqlens, "cu_seqlens", _I32, (batch + 1,), dev),
+        qp, kp, vp, cu,
         _ptr(k_pool, "k_pool", _BF16, pool, dev), _ptr(v_pool, "v_pool", _BF16, pool, dev), pages,
         table, width, _ptr(seq_lens, "seq_lens", _I32, (batch,), dev), max_len_hint,
         _ptr(o, "o", _BF16, (total, hq, d), dev), batch, total, hq, hkv, d, PAGE_SIZE, qs, ks, vs,
@@ -184,17 +190,16 @@ def mars_kv_append(k, v, cu_seqlens, seq_lens, block_table, k_pool, v_pool, new_
                    slots=None, status=None, stream=None):
     """Copy each sequence's new K/V rows to its pages, after its seq_lens[s] cached tokens;
     new_lens [batch] and slots [total] (int32) are optional outputs (see include/mars.h)."""
-    _need_cuda(k, "k")
-    dev, raw = _target(stream)
+    dev, raw = _target(k, "k", stream)
     total, hkv, d = k.shape
-    batch = _batch(cu_seqlens)
+    cu, batch = _batch(cu_seqlens, dev)
     pages = k_pool.shape[0]
     pool = (pages, hkv, PAGE_SIZE, d)
     kp, ks = _rows(k, "k", (total, hkv, d), dev)
     vp, vs = _rows(v, "v", (total, hkv, d), dev)
     table, width = _table(block_table, batch, dev)
     _rc(lib().mars_kv_append(
-        kp, vp, _ptr(cu_seqlens, "cu_seqlens", _I32, (batch + 1,), dev),
+        kp, vp, cu,
         _ptr(seq_lens, "seq_lens", _I32, (batch,), dev),
         _opt(new_lens, "new_lens", _I32, (batch,), dev), table, width,
         _ptr(k_pool, "k_pool", _BF16, pool, dev), _ptr(v_pool, "v_pool", _BF16, pool, dev), pages,
