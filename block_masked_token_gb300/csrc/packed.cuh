@@ -69,22 +69,35 @@ MARS_DEV Seq find_tile(const int32_t* __restrict__ cu, int batch, int total, int
   return Seq{-1, 0, top, 0};
 }
 
-// A tile of a sequence in a plan's lists.
+constexpr int kTileRows = 128;
+
+// A 128-row tile of a sequence in a plan's lists.
 struct alignas(16) Tile {
   int base, n;    // first row and number of rows of its sequence
   int tile;       // tile index inside the sequence
-  int id;         // sequence (by_cost of a forward plan) or global tile index (a gradient's)
+  int id;         // index among all tiles, in the order of the sequences
 };
 
-// Lists of the tiles of a packed batch, made on the device (the boundaries are there), for
-// kernels that run many tiles per CTA: CTAs take a list's entries in turn, so each is sorted
-// by falling cost, the number of 128-key (or 128-row) tiles that an entry visits.
+// Lists of the tiles of a packed batch, made on the device (the boundaries are there), for the
+// gradient's kernels, which run many tiles per CTA.
 struct Plan {
   int32_t* count;     // number of tiles
-  Tile* first;        // by the keys a tile's rows see (forward, dQ)
-  Tile* second;       // gradient: by the rows that see a tile's keys (dK, dV)
-  Tile* in_order;     // gradient: by global tile index
+  Tile* by_cost;      // by falling number of keys that a tile's rows see (dQ)
+  Tile* in_order;     // by id
+  long long* before;  // [count + 1]: dK / dV work of one KV head before each tile, and of all
+  int32_t* tickets;   // zeroed
 };
+
+// Work of dK and dV of a key tile and a KV head with `groups` query heads: kPairWork for each
+// (query head, query tile) pair, 1 more for each on the diagonal (its masks), and kTileWork for
+// the tile's start and output; a unit is about 900 cycles.
+constexpr int kPairWork = 3, kTileWork = 6;
+
+// That of a tile with `after` query tiles, and of the first t of a sequence's tiles.
+MARS_DEV int tile_work(int groups, int after) { return groups * (kPairWork * after + 1) + kTileWork; }
+MARS_DEV long long work_before(int groups, long long tiles, long long t) {
+  return groups * (kPairWork * (t * tiles - t * (t - 1) / 2) + t) + kTileWork * t;
+}
 
 // The items (tile of a list, head) of a persistent CTA. Rounds run forwards and backwards over
 // the CTAs, so that the costs even out. The next item's tile is read while the current one is
@@ -161,29 +174,26 @@ MARS_DEV void store_rows(uint16_t* out, long long at, int lane, F get) {
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Carve a plan out of a workspace at `off` (base may be null to size it).
-inline Plan carve_plan(void* base, size_t& off, int batch, int total, int rows, bool grad) {
+inline Plan carve_plan(void* base, size_t& off, int batch, int total, int ntickets) {
   uint8_t* p = static_cast<uint8_t*>(base);
   auto take = [&](size_t bytes) {
     uint8_t* at = p ? p + off : nullptr;
     off += align256(bytes);
     return at;
   };
-  const size_t list = (size_t)max_tiles(batch, total, rows) * sizeof(Tile);
+  const size_t tiles = (size_t)max_tiles(batch, total, kTileRows);
   Plan r{};
   r.count = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
-  r.first = reinterpret_cast<Tile*>(take(list));
-  if (grad) {
-    r.second = reinterpret_cast<Tile*>(take(list));
-    r.in_order = reinterpret_cast<Tile*>(take(list));
-  }
+  r.by_cost = reinterpret_cast<Tile*>(take(tiles * sizeof(Tile)));
+  r.in_order = reinterpret_cast<Tile*>(take(tiles * sizeof(Tile)));
+  r.before = reinterpret_cast<long long*>(take((tiles + 1) * sizeof(long long)));
+  r.tickets = reinterpret_cast<int32_t*>(take(ntickets * sizeof(int32_t)));
   return r;
 }
 
-// Fill a plan. rows: rows per tile (128 for a gradient); seq_lens: cached keys per sequence
-// (NULL: none), cut to what max_pages pages hold.
-cudaError_t launch_plan(const Plan& plan, const int32_t* cu, const int32_t* seq_lens,
-                        int max_pages, int batch, int total, int rows, int32_t* status,
-                        cudaStream_t stream);
+// Fill a plan. groups: query heads per KV head.
+cudaError_t launch_plan(const Plan& plan, const int32_t* cu, int batch, int total, int groups,
+                        int ntickets, int32_t* status, cudaStream_t stream);
 
 }  // namespace packed
 }  // namespace mars

@@ -7,15 +7,18 @@
 // set so instead of being left to the cancellation of dP and D.
 //
 // Two tcgen05 kernels over 128-row tiles, neither storing a score block, each a persistent CTA
-// per SM that takes (tile, head) items in the order of falling cost (packed_plan.cu):
-//   - dkdv_kernel: an item is a key tile, a KV head and some of its query heads. Per pair with
-//     a query tile at or after it: S^T = K Q^T and dP^T = V dO^T (keys on TMEM lanes), then
-//     dV += P^T dO and dK += dS^T Q with P^T and dS^T as bf16 operands in TMEM, all in two
-//     halves of 64 queries with their own barriers. dV and dK stay in TMEM over the item.
-//     When the key tiles alone would leave SMs idle, the query heads of a group are divided
-//     among items, which write fp32 partials that merge_kernel adds in a fixed order: no
-//     atomics, the same result from run to run.
-//   - dq_kernel: an item is a query tile and a query head; S, dP and dQ += dS K per key tile.
+// per SM:
+//   - dkdv_kernel: an item is a key tile and a KV head. Per pair of it with a query head of the
+//     group and a query tile at or after it: S^T = K Q^T and dP^T = V dO^T (keys on TMEM
+//     lanes), then dV += P^T dO and dK += dS^T Q with P^T and dS^T as bf16 operands in TMEM, all
+//     in two halves of 64 queries with their own barriers. dV and dK stay in TMEM over the item.
+//     The pairs of all items are divided evenly among the CTAs, whatever the lengths (KWalk):
+//     an item that is cut leaves partials, and the last of its CTAs to finish adds them up in
+//     the order of the pairs, so that the result is the same from run to run. With whole items
+//     in turn, 4096 rows (28 heads over 4) kept the SMs busy for 44 % of the time, with an
+//     item's heads divided in three for 76 %.
+//   - dq_kernel: an item is a query tile and a query head, taken in turn by falling cost; S, dP
+//     and dQ += dS K per key tile.
 // P and dS are rounded to bf16 as MMA operands; dS is formed from the unrounded P. prep_kernel
 // computes D and lays lse and D out in 128-row blocks per (head, tile), for bulk copies.
 //
@@ -47,7 +50,7 @@ constexpr int NSTAGE = 2;               // Q / dO ring depth of dkdv_kernel
 
 struct GradArgs {
   packed::Plan plan;
-  int batch, total, hq, hkv, G, nsplit;
+  int total, hq, hkv, G;
   long long pad;                        // padded rows per head: 128 * the bound of the tiles
   float scale, scale_log2;
   const uint16_t *o, *d_o;              // [total][hq][D]
@@ -55,7 +58,7 @@ struct GradArgs {
   float *lse_p, *d_p;                   // [hq][pad]
   uint16_t *dq, *dk, *dv;
   long long dq_stride, dk_stride, dv_stride;
-  float* part;                          // partial() with several splits
+  float* part;                          // partial()
   int32_t* status;
 };
 
@@ -123,47 +126,131 @@ struct KSmem {
   static constexpr int TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + D, TM_COLS = 512;
 };
 
+// Part [pa, pb) of the `all` pairs of key tile t and a KV head: pair p is query head
+// kvh * G + p / nq and query tile t.tile + p % nq of its sequence.
+struct KItem {
+  Tile t;
+  int kvh, nq, all, pa, pb;
+  int first, cuts;                      // a divided item: CTAs first .. first + cuts share it
+};
+
+constexpr int K_ITEMS = 3;              // items handed over by the loader and not yet finished
+
 struct KBar {
   uint64_t kv_full, kv_empty;
   uint64_t full[NSTAGE], empty[NSTAGE];
   uint64_t s_full[2], dp_full[2], p_full[2], ds_full[2], dv_done[2], dk_done[2];
   uint64_t acc_full, acc_free, drain, drain_ts;
+  uint64_t stored, told;                // partials written; `last` set
+  uint64_t item_full[K_ITEMS], item_empty[K_ITEMS];
+  KItem items[K_ITEMS];
   uint32_t tmem_base;
   int abort;
+  int last;                             // whether this CTA adds up an item's partials
 };
 
-// Key tile `t` of (kvh, split): query heads kvh*G + g, g in [g0, g0 + ng), query tiles
-// t.tile .. nt - 1 of its sequence.
-struct KItem {
-  Tile t;
-  int kvh, sp, g0, ng, nq, pairs;
+constexpr int kMinPart = 2;             // pairs of a part of a divided item, at least
+// Work of a part of the line, at least. An item's pairs take more than half of its work (with
+// kMinPart pairs or more), so that two cuts of an item are at least a pair apart.
+constexpr int kMinWork = kMinPart * packed::kPairWork + packed::kTileWork;
+
+// The line of all items, KV head by KV head, tile by tile, each as long as its work; CTA c of
+// `parts` takes the part of it from cut(c) to cut(c + 1). (Cutting it so that the CTAs stay
+// near one another, for Q and dO in L2, saved as much as the further cuts cost.)
+struct KLine {
+  long long head, total;                // work of one KV head and of all
+  int parts;
+  MARS_DEV explicit KLine(const GradArgs& a)
+      : head(a.plan.before[*a.plan.count]), total(head * a.hkv) {
+    parts = (int)max(1LL, min((long long)gridDim.x, total / kMinWork));
+  }
+  MARS_DEV long long cut(int i) const { return i * total / parts; }
+  // The pair before which position pos cuts an item of `pairs` pairs and `work` at s0: 0 before
+  // the item, `pairs` after it.
+  MARS_DEV int inside(long long pos, long long s0, int work, int pairs) const {
+    const int j = (int)((pos - s0) * pairs / work);
+    return j < kMinPart ? 0 : pairs - j < kMinPart ? pairs : j;
+  }
 };
 
-MARS_DEV Walk k_walk(const GradArgs& a) {
-  return Walk(a.plan.count, a.plan.second, a.hkv * a.nsplit);
+// Where a part begins: pair pa of tile i of a KV head.
+struct KStart {
+  int kvh, i, pa;
+};
+
+// Query tiles at or after a key tile.
+MARS_DEV int after(const Tile& t) { return (t.n + GT - 1) / GT - t.tile; }
+
+// Every thread of the CTA; the caller synchronises.
+MARS_DEV void find_start(const GradArgs& a, const KLine& line, KStart& st) {
+  const long long p0 = line.cut(blockIdx.x);
+  const int kvh = (int)(p0 / line.head), n = *a.plan.count;
+  const long long x = p0 - kvh * line.head;
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    if (a.plan.before[i] <= x && x < a.plan.before[i + 1]) {
+      const int nq = after(a.plan.in_order[i]);
+      st = KStart{kvh, i, line.inside(p0, kvh * line.head + a.plan.before[i],
+                                      packed::tile_work(a.G, nq), a.G * nq)};
+    }
 }
 
-MARS_DEV bool take(const GradArgs& a, Walk& w, KItem& it) {
-  int i;
-  if (!w.take(it.t, i)) return false;
-  it.kvh = i / a.nsplit;
-  it.sp = i % a.nsplit;
-  it.g0 = a.G * it.sp / a.nsplit;
-  it.ng = a.G * (it.sp + 1) / a.nsplit - it.g0;
-  it.nq = (it.t.n + GT - 1) / GT - it.t.tile;
-  it.pairs = it.ng * it.nq;
-  return true;
-}
+// The items of a CTA's part. A tile is read while the item before it is worked on.
+struct KWalk {
+  const GradArgs& a;
+  long long s0, end;
+  int kvh, i, n, pa;
+  Tile tile;
+  MARS_DEV KWalk(const GradArgs& a_, const KLine& line, const KStart& st)
+      : a(a_), s0(st.kvh * line.head + a_.plan.before[st.i]), end(line.cut(blockIdx.x + 1)),
+        kvh(st.kvh), i(st.i), n(*a_.plan.count), pa(st.pa), tile(a_.plan.in_order[st.i]) {}
+  MARS_DEV void next(int work) {
+    s0 += work;
+    pa = 0;
+    if (++i == n) {
+      i = 0;
+      ++kvh;
+    }
+    if (s0 < end) tile = a.plan.in_order[i];
+  }
+  MARS_DEV bool take(const KLine& line, KItem& it) {
+    if (s0 >= end) return false;
+    int nq = after(tile);
+    if (pa == a.G * nq) {                // the part begins behind this item
+      next(packed::tile_work(a.G, nq));
+      if (s0 >= end) return false;
+      nq = after(tile);
+    }
+    const int all = a.G * nq, work = packed::tile_work(a.G, nq);
+    const int pb = end >= s0 + work ? all : line.inside(end, s0, work, all);
+    it = KItem{tile, kvh, nq, all, pa, pb, 0, 0};
+    if (pb - pa < all) {
+      int c = (int)(s0 * line.parts / line.total);
+      while (line.cut(c) <= s0 || line.inside(line.cut(c), s0, work, all) == 0) ++c;
+      it.first = c - 1;
+      while (c < line.parts && line.cut(c) < s0 + work &&
+             line.inside(line.cut(c), s0, work, all) < all)
+        ++c;
+      it.cuts = c - 1 - it.first;
+    }
+    next(work);
+    return pb > pa;
+  }
+};
 
-constexpr int K_THREADS = 96 + MATH_THREADS;     // loader, S/dP issuer, math, dV/dK issuer
-constexpr int K_TS_WARP = 2 + MATH_WARPS;
+// dkdv_kernel: warps 0 loader, 1 S / dP issuer and TMEM owner, 2 dV / dK issuer, 4 .. 11 math.
+// The first four give registers to the math warps, which hold 200 values in the sums.
+constexpr int K_THREADS = 128 + MATH_THREADS;
+constexpr int K_WG0_REGS = 88, K_MATH_REGS = 208;
+static_assert(128 * (K_WG0_REGS + 2 * K_MATH_REGS) <= K_THREADS * (65536 / K_THREADS / 8 * 8),
+              "the register split fits the launch's register pool");
 
-// Partial dV (and D / 4 x 128 float4 further on dK) of an item: [column / 4][row], so that the
+// Partial dV (and D / 4 x 128 float4 further on dK) of the item that a CTA's part starts inside
+// of, or of the one that it ends inside of and has the start of: [column / 4][row], so that the
 // lanes of a warp, a row each, access consecutive places.
 template <int D>
-MARS_DEV float4* partial(const GradArgs& a, int tile, int kvh, int sp) {
+MARS_DEV float4* partial(const GradArgs& a, int cta, bool inside) {
   return reinterpret_cast<float4*>(a.part) +
-         (((size_t)tile * a.hkv + kvh) * a.nsplit + sp) * (2 * GT * D / 4);
+         ((size_t)cta * 2 + (inside ? 0 : 1)) * (2 * GT * D / 4);
 }
 
 // TMEM column of K-step k (16 queries) of P^T or dS^T: queries [0, 64) over columns [0, 32),
@@ -182,8 +269,11 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* ab = &bar.abort;
-  Walk walk = k_walk(a);
-  if (walk.id < 0) return;                             // more CTAs than items
+  if (*a.plan.count == 0) return;
+  const KLine line(a);
+  if ((int)blockIdx.x >= line.parts) return;
+  __shared__ KStart start;
+  find_start(a, line, start);
 
   if (threadIdx.x == 0) {
     bar.abort = 0;
@@ -205,6 +295,12 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     mbar_init(&bar.acc_free, MATH_THREADS);
     mbar_init(&bar.drain, 1);
     mbar_init(&bar.drain_ts, 1);
+    mbar_init(&bar.stored, MATH_THREADS);
+    for (int i = 0; i < K_ITEMS; ++i) {
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_empty[i], 2 + MATH_WARPS);   // both issuers, the math warps
+    }
+    mbar_init(&bar.told, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -216,153 +312,190 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem_base, 0);
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- loads
-    if (lane == 0) {
-      int gp = 0, ii = 0, nkv = 0;
-      bool ok = true;
-      KItem it;
-      while (ok && take(a, walk, it)) {
-        if (ii > 0 && !(ok = mbar_wait(&bar.kv_empty, (ii - 1) & 1, ab, a.status))) break;
-        mbar_arrive_expect_tx(&bar.kv_full, 2 * S::T_BYTES);
-        const int z = it.t.base + GT * it.t.tile;
-        for (int x = 0; x < D / 64; ++x) {
-          tma_load_3d(smem + S::OFF_K + x * (GT * 128), &tm_k, &bar.kv_full, x * 64, it.kvh, z);
-          tma_load_3d(smem + S::OFF_V + x * (GT * 128), &tm_v, &bar.kv_full, x * 64, it.kvh, z);
-        }
-        ++nkv;
-        for (int p = 0; p < it.pairs; ++p, ++gp) {
-          const int st = gp % NSTAGE;
-          uint8_t* stage = smem + S::OFF_RING + st * S::STAGE;
-          if (!(ok = mbar_wait(&bar.empty[st], ((gp / NSTAGE) & 1) ^ 1, ab, a.status))) break;
-          const int h = it.kvh * a.G + it.g0 + p / it.nq, qi = p % it.nq;
-          const size_t rb = (size_t)h * a.pad + (size_t)(it.t.id + qi) * GT;
-          mbar_arrive_expect_tx(&bar.full[st], 2 * S::T_BYTES + 2 * GT * 4);
-          bulk_load(stage + S::ST_LSE, a.lse_p + rb, GT * 4, &bar.full[st]);
-          bulk_load(stage + S::ST_D, a.d_p + rb, GT * 4, &bar.full[st]);
+  if (warp < 4) {
+    regs_lower<K_WG0_REGS>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- loads
+      if (lane == 0) {
+        int gp = 0, ii = 0, nkv = 0;
+        bool ok = true;
+        KItem it;
+        int ni = 0;                                    // items handed over
+        auto publish = [&](const KItem& d) {
+          if (!mbar_wait(&bar.item_empty[ni % K_ITEMS], ((ni / K_ITEMS) & 1) ^ 1, ab, a.status))
+            return false;
+          bar.items[ni % K_ITEMS] = d;
+          mbar_arrive(&bar.item_full[ni % K_ITEMS]);
+          ++ni;
+          return true;
+        };
+        for (KWalk walk(a, line, start); ok && walk.take(line, it);) {
+          if (!(ok = publish(it))) break;
+          if (ii > 0 && !(ok = mbar_wait(&bar.kv_empty, (ii - 1) & 1, ab, a.status))) break;
+          mbar_arrive_expect_tx(&bar.kv_full, 2 * S::T_BYTES);
+          const int z = it.t.base + GT * it.t.tile;
           for (int x = 0; x < D / 64; ++x) {
-            tma_load_3d(stage + S::ST_Q + x * (GT * 128), &tm_q, &bar.full[st], x * 64, h, z + GT * qi);
-            tma_load_3d(stage + S::ST_DO + x * (GT * 128), &tm_do, &bar.full[st], x * 64, h, z + GT * qi);
+            tma_load_3d(smem + S::OFF_K + x * (GT * 128), &tm_k, &bar.kv_full, x * 64, it.kvh, z);
+            tma_load_3d(smem + S::OFF_V + x * (GT * 128), &tm_v, &bar.kv_full, x * 64, it.kvh, z);
           }
-        }
-        ++ii;
-      }
-      // wait (bounded) for the copies still in flight
-      if (nkv > 0) mbar_wait(&bar.kv_full, (nkv - 1) & 1, nullptr, a.status);
-      for (int k = 1; k <= NSTAGE && gp - k >= 0; ++k)
-        mbar_wait(&bar.full[(gp - k) % NSTAGE], ((gp - k) / NSTAGE) & 1, nullptr, a.status);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------- S^T and dP^T MMAs
-    if (elect_one()) {
-      const uint32_t id_qk = idesc_bf16_f32(GT, GT / 2, false);
-      const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_K), 16, 1024);
-      const uint64_t vd = sdesc_sw128(smem_u32(smem + S::OFF_V), 16, 1024);
-      // half h of S^T = K Q^T (or dP^T = V dO^T) of pair gp, once `done` says that the MMAs
-      // that read the buffer's previous P^T (dS^T) have completed
-      auto issue = [&](int gp, uint64_t ad, int st_off, int col, uint64_t* done, uint64_t* full) {
-        const uint64_t bd =
-            sdesc_sw128(smem_u32(smem + S::OFF_RING + (gp % NSTAGE) * S::STAGE + st_off), 16, 1024);
-        for (int h = 0; h < 2; ++h) {
-          if (gp > 0 && !mbar_wait(&done[h], (gp - 1) & 1, ab, a.status)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * (GT * 128) + (k & 3) * 32;
-            mma_bf16_ss(tmem + col + (GT / 2) * h, sdesc_advance(ad, off),
-                        sdesc_advance(bd, off + h * (GT / 2) * 128), id_qk, k != 0);
-          }
-          mma_commit(&full[h]);
-        }
-        return true;
-      };
-      int gp = 0, ii = 0;
-      bool ok = true;
-      KItem it;
-      while (ok && take(a, walk, it)) {
-        const int np = it.pairs;
-        if (!(ok = mbar_wait(&bar.kv_full, ii & 1, ab, a.status))) break;
-        for (int p = 0; p < np && ok; ++p, ++gp)
-          ok = mbar_wait(&bar.full[gp % NSTAGE], (gp / NSTAGE) & 1, ab, a.status) &&
-               issue(gp, kd, S::ST_Q, S::TM_S, bar.dv_done, bar.s_full) &&
-               issue(gp, vd, S::ST_DO, S::TM_DP, bar.dk_done, bar.dp_full);
-        if (!ok) break;
-        mma_commit(&bar.kv_empty);                     // only these MMAs read K and V
-        ++ii;
-      }
-      mma_commit(&bar.drain);
-      mbar_wait(&bar.drain, 0, nullptr, a.status);
-    }
-  } else if (warp == K_TS_WARP) {
-    // -------------------------------------------------------- dV and dK MMAs
-    if (elect_one()) {
-      const uint32_t id_acc = idesc_bf16_f32(GT, D, true);     // A from TMEM, B MN-major
-      int gp = 0, ii = 0;
-      bool ok = true;
-      KItem it;
-      while (ok && take(a, walk, it)) {
-        const int np = it.pairs;
-        for (int p = 0; p < np; ++p, ++gp) {
-          const int st = gp % NSTAGE;
-          const uint32_t sb = smem_u32(smem + S::OFF_RING + st * S::STAGE);
-          if (!(ok = mbar_wait(&bar.full[st], (gp / NSTAGE) & 1, ab, a.status))) break;
-          // the accumulators start from zero: the previous item's must have been read
-          if (p == 0 && ii > 0 && !(ok = mbar_wait(&bar.acc_free, (ii - 1) & 1, ab, a.status)))
-            break;
-          auto accumulate = [&](uint64_t* ready, uint64_t* done, int st_off, int src, int dst) {
-            const uint64_t bd = sdesc_sw128(sb + st_off, GT * 128, 1024);
-            for (int h = 0; h < 2; ++h) {
-              if (!mbar_wait(&ready[h], gp & 1, ab, a.status)) return false;
-              tc_fence_after();
-#pragma unroll
-              for (int kq = 0; kq < GT / 32; ++kq) {
-                const int k = (GT / 32) * h + kq;
-                mma_bf16_ts(tmem + dst, tmem + src + p_col(k), sdesc_advance(bd, k * 2048), id_acc,
-                            (p | k) != 0);
-              }
-              mma_commit(&done[h]);
+          ++nkv;
+          for (int p = it.pa; p < it.pb; ++p, ++gp) {
+            const int st = gp % NSTAGE;
+            uint8_t* stage = smem + S::OFF_RING + st * S::STAGE;
+            if (!(ok = mbar_wait(&bar.empty[st], ((gp / NSTAGE) & 1) ^ 1, ab, a.status))) break;
+            const int h = it.kvh * a.G + p / it.nq, qi = p % it.nq;
+            const size_t rb = (size_t)h * a.pad + (size_t)(it.t.id + qi) * GT;
+            mbar_arrive_expect_tx(&bar.full[st], 2 * S::T_BYTES + 2 * GT * 4);
+            bulk_load(stage + S::ST_LSE, a.lse_p + rb, GT * 4, &bar.full[st]);
+            bulk_load(stage + S::ST_D, a.d_p + rb, GT * 4, &bar.full[st]);
+            const int zq = z + GT * qi;
+            for (int x = 0; x < D / 64; ++x) {
+              uint8_t* to = stage + x * (GT * 128);
+              tma_load_3d(to + S::ST_Q, &tm_q, &bar.full[st], x * 64, h, zq);
+              tma_load_3d(to + S::ST_DO, &tm_do, &bar.full[st], x * 64, h, zq);
             }
-            return true;
-          };
-          if (!(ok = accumulate(bar.p_full, bar.dv_done, S::ST_DO, S::TM_S, S::TM_DV) &&
-                     accumulate(bar.ds_full, bar.dk_done, S::ST_Q, S::TM_DP, S::TM_DK)))
-            break;
-          // S^T and dP^T completed before the math warps formed dS^T, and those have read
-          // the stage's lse and D: the stage is free after dK
-          mma_commit(&bar.empty[st]);
+          }
+          ++ii;
         }
-        if (!ok) break;
-        mma_commit(&bar.acc_full);
-        ++ii;
+        if (ok) publish(KItem{});                      // no more items
+        // wait (bounded) for the copies still in flight
+        if (nkv > 0) mbar_wait(&bar.kv_full, (nkv - 1) & 1, nullptr, a.status);
+        for (int k = 1; k <= NSTAGE && gp - k >= 0; ++k)
+          mbar_wait(&bar.full[(gp - k) % NSTAGE], ((gp - k) / NSTAGE) & 1, nullptr, a.status);
       }
-      mma_commit(&bar.drain_ts);
-      mbar_wait(&bar.drain_ts, 0, nullptr, a.status);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------- S^T and dP^T MMAs
+      if (elect_one()) {
+        const uint32_t id_qk = idesc_bf16_f32(GT, GT / 2, false);
+        const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_K), 16, 1024);
+        const uint64_t vd = sdesc_sw128(smem_u32(smem + S::OFF_V), 16, 1024);
+        // half h of S^T = K Q^T (or dP^T = V dO^T) of pair gp, once `done` says that the MMAs
+        // that read the buffer's previous P^T (dS^T) have completed
+        auto issue = [&](int gp, uint64_t ad, int st_off, int col, uint64_t* done, uint64_t* full) {
+          const uint32_t sb = smem_u32(smem + S::OFF_RING + (gp % NSTAGE) * S::STAGE);
+          const uint64_t bd = sdesc_sw128(sb + st_off, 16, 1024);
+          for (int h = 0; h < 2; ++h) {
+            if (gp > 0 && !mbar_wait(&done[h], (gp - 1) & 1, ab, a.status)) return false;
+            tc_fence_after();
+  #pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * (GT * 128) + (k & 3) * 32;
+              mma_bf16_ss(tmem + col + (GT / 2) * h, sdesc_advance(ad, off),
+                          sdesc_advance(bd, off + h * (GT / 2) * 128), id_qk, k != 0);
+            }
+            mma_commit(&full[h]);
+          }
+          return true;
+        };
+        int gp = 0, ii = 0, items = 0;
+        bool ok = true;
+        // pairs of the next item, 0 at the end
+        auto next_pairs = [&](int& np) {
+          const int q = items % K_ITEMS;
+          if (!mbar_wait(&bar.item_full[q], (items / K_ITEMS) & 1, ab, a.status)) return false;
+          np = bar.items[q].pb - bar.items[q].pa;
+          mbar_arrive(&bar.item_empty[q]);
+          ++items;
+          return true;
+        };
+        int np;
+        while (ok && (ok = next_pairs(np)) && np) {
+          if (!(ok = mbar_wait(&bar.kv_full, ii & 1, ab, a.status))) break;
+          for (int p = 0; p < np && ok; ++p, ++gp)
+            ok = mbar_wait(&bar.full[gp % NSTAGE], (gp / NSTAGE) & 1, ab, a.status) &&
+                 issue(gp, kd, S::ST_Q, S::TM_S, bar.dv_done, bar.s_full) &&
+                 issue(gp, vd, S::ST_DO, S::TM_DP, bar.dk_done, bar.dp_full);
+          if (!ok) break;
+          mma_commit(&bar.kv_empty);                     // only these MMAs read K and V
+          ++ii;
+        }
+        mma_commit(&bar.drain);
+        mbar_wait(&bar.drain, 0, nullptr, a.status);
+      }
+    } else if (warp == 2) {
+      // -------------------------------------------------------- dV and dK MMAs
+      if (elect_one()) {
+        const uint32_t id_acc = idesc_bf16_f32(GT, D, true);     // A from TMEM, B MN-major
+        int gp = 0, ii = 0, items = 0;
+        bool ok = true;
+        // pairs of the next item, 0 at the end
+        auto next_pairs = [&](int& np) {
+          const int q = items % K_ITEMS;
+          if (!mbar_wait(&bar.item_full[q], (items / K_ITEMS) & 1, ab, a.status)) return false;
+          np = bar.items[q].pb - bar.items[q].pa;
+          mbar_arrive(&bar.item_empty[q]);
+          ++items;
+          return true;
+        };
+        int np;
+        while (ok && (ok = next_pairs(np)) && np) {
+          for (int p = 0; p < np; ++p, ++gp) {
+            const int st = gp % NSTAGE;
+            const uint32_t sb = smem_u32(smem + S::OFF_RING + st * S::STAGE);
+            if (!(ok = mbar_wait(&bar.full[st], (gp / NSTAGE) & 1, ab, a.status))) break;
+            // the accumulators start from zero: the previous item's must have been read
+            if (p == 0 && ii > 0 && !(ok = mbar_wait(&bar.acc_free, (ii - 1) & 1, ab, a.status)))
+              break;
+            auto accumulate = [&](uint64_t* ready, uint64_t* done, int st_off, int src, int dst) {
+              const uint64_t bd = sdesc_sw128(sb + st_off, GT * 128, 1024);
+              for (int h = 0; h < 2; ++h) {
+                if (!mbar_wait(&ready[h], gp & 1, ab, a.status)) return false;
+                tc_fence_after();
+  #pragma unroll
+                for (int kq = 0; kq < GT / 32; ++kq) {
+                  const int k = (GT / 32) * h + kq;
+                  mma_bf16_ts(tmem + dst, tmem + src + p_col(k), sdesc_advance(bd, k * 2048), id_acc,
+                              (p | k) != 0);
+                }
+                mma_commit(&done[h]);
+              }
+              return true;
+            };
+            if (!(ok = accumulate(bar.p_full, bar.dv_done, S::ST_DO, S::TM_S, S::TM_DV) &&
+                       accumulate(bar.ds_full, bar.dk_done, S::ST_Q, S::TM_DP, S::TM_DK)))
+              break;
+            // S^T and dP^T completed before the math warps formed dS^T, and those have read
+            // the stage's lse and D: the stage is free after dK
+            mma_commit(&bar.empty[st]);
+          }
+          if (!ok) break;
+          mma_commit(&bar.acc_full);
+          ++ii;
+        }
+        mma_commit(&bar.drain_ts);
+        mbar_wait(&bar.drain_ts, 0, nullptr, a.status);
+      }
     }
   } else {
-    // ------------------------------------------------- math (warps 2..9, two per quadrant)
-    const int quad = warp & 3, half = (warp - 2) >> 2;
+    regs_raise<K_MATH_REGS>();
+    // ------------------------------------------------------- math (two warps per quadrant)
+    const int quad = warp & 3, half = (warp - 4) >> 2;
     const int row = quad * 32 + lane;                  // TMEM lane = key row of the tile
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     constexpr int HC = GT / 2, HD = D / 2;
     auto warp_wait = [&](uint64_t* b, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(b, parity, ab, a.status));
     };
-    int gp = 0, ii = 0;
+    int gp = 0, ii = 0, cut_items = 0;
     bool ok = true;
-    KItem it;
-    while (ok && take(a, walk, it)) {
-      const int kk = GT * it.t.tile + row;             // key position in its sequence
-      for (int p = 0; p < it.pairs; ++p, ++gp) {
+    for (;; ++ii) {
+      // read where it is: a copy of the item would cost the key loop its registers
+      const volatile KItem& it = bar.items[ii % K_ITEMS];
+      if (!(ok = warp_wait(&bar.item_full[ii % K_ITEMS], (ii / K_ITEMS) & 1))) break;
+      const int pb = it.pb, nq = it.nq, n = it.t.n, tile0 = it.t.tile;
+      if (!pb) break;
+      const int kk = GT * tile0 + row;                 // key position in its sequence
+      for (int p = it.pa; p < pb; ++p, ++gp) {
         const int st = gp % NSTAGE;
         uint8_t* stage = smem + S::OFF_RING + st * S::STAGE;
         const float* ls = reinterpret_cast<const float*>(stage + S::ST_LSE) + HC * half;
         const float* dsv = reinterpret_cast<const float*>(stage + S::ST_D) + HC * half;
-        const int q0 = GT * (it.t.tile + p % it.nq);   // first query position
+        const int q0 = GT * (tile0 + p % nq);   // first query position
         // query columns [lo, hi) of this half that see the key; none for a key past the end
-        const int live = it.t.n - q0;                  // query rows of the tile
+        const int live = n - q0;                  // query rows of the tile
         const int lo = kk - q0 - HC * half;
-        const int hi = kk < it.t.n ? live - HC * half : -1;
+        const int hi = kk < n ? live - HC * half : -1;
         const bool ragged = live < GT;                 // uniform over the CTA
         if (!(ok = warp_wait(&bar.s_full[half], gp & 1))) break;
         tc_fence_after();
@@ -462,27 +595,64 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive_warp(&bar.acc_free);
-      if (a.nsplit == 1) {
-        const long long tok = (long long)it.t.base + kk;
-        const int col = it.kvh * D + HD * half;
-        const bool rv = kk < it.t.n;
-        packed::store_rows<HD>(a.dv, rv ? tok * a.dv_stride + col : -1, lane,
-                               [&](int e) { return __uint_as_float(dvr[e]); });
-        packed::store_rows<HD>(a.dk, rv ? tok * a.dk_stride + col : -1, lane,
-                               [&](int e) { return __uint_as_float(dkr[e]) * a.scale; });
-      } else {
-        float4* pv = partial<D>(a, it.t.id, it.kvh, it.sp) + (HD / 4) * half * GT + row;
-        float4* pk = pv + GT * D / 4;
+      bool write = it.pb - it.pa == it.all;
+      if (!write) {
+        // a part of the item: its partial, and the sum by the last part to arrive
+        float4* pv = partial<D>(a, blockIdx.x, it.pa > 0) + (HD / 4) * half * GT + row;
 #pragma unroll
         for (int e = 0; e < HD; e += 4) {
           pv[(e / 4) * GT] = make_float4(__uint_as_float(dvr[e]), __uint_as_float(dvr[e + 1]),
                                          __uint_as_float(dvr[e + 2]), __uint_as_float(dvr[e + 3]));
-          pk[(e / 4) * GT] = make_float4(
-              __uint_as_float(dkr[e]) * a.scale, __uint_as_float(dkr[e + 1]) * a.scale,
-              __uint_as_float(dkr[e + 2]) * a.scale, __uint_as_float(dkr[e + 3]) * a.scale);
+          pv[(D + e) / 4 * GT] =
+              make_float4(__uint_as_float(dkr[e]), __uint_as_float(dkr[e + 1]),
+                          __uint_as_float(dkr[e + 2]), __uint_as_float(dkr[e + 3]));
+        }
+        const int first = it.first, cuts = it.cuts;
+        __threadfence();
+        mbar_arrive_warp(&bar.stored);
+        if (warp == 4) {
+          if (!(ok = warp_wait(&bar.stored, cut_items & 1))) break;
+          if (lane == 0) {
+            bar.last = atomicAdd(a.plan.tickets + first, 1) == cuts;
+            mbar_arrive(&bar.told);
+          }
+        }
+        if (!(ok = warp_wait(&bar.told, cut_items & 1))) break;
+        ++cut_items;
+        write = *reinterpret_cast<volatile int*>(&bar.last) != 0;
+        if (write) {
+          __threadfence();
+#pragma unroll
+          for (int e = 0; e < HD; ++e) dvr[e] = dkr[e] = 0u;
+#pragma unroll 1
+          for (int k = 0; k <= cuts; ++k) {
+            const float4* r = partial<D>(a, first + k, k > 0) + (HD / 4) * half * GT + row;
+            auto add = [&](uint32_t* acc, const float4* from) {
+#pragma unroll
+              for (int e = 0; e < HD; e += 4) {
+                const float4 u = __ldcg(from + (e / 4) * GT);
+                acc[e] = __float_as_uint(__uint_as_float(acc[e]) + u.x);
+                acc[e + 1] = __float_as_uint(__uint_as_float(acc[e + 1]) + u.y);
+                acc[e + 2] = __float_as_uint(__uint_as_float(acc[e + 2]) + u.z);
+                acc[e + 3] = __float_as_uint(__uint_as_float(acc[e + 3]) + u.w);
+              }
+            };
+            add(dvr, r);
+            add(dkr, r + D / 4 * GT);
+          }
         }
       }
-      ++ii;
+      if (write) {
+        const long long tok = (long long)it.t.base + kk;
+        const int col = it.kvh * D + HD * half;
+        const bool rv = kk < n;
+        packed::store_rows<HD>(a.dv, rv ? tok * a.dv_stride + col : -1, lane,
+                               [&](int e) { return __uint_as_float(dvr[e]); });
+        packed::store_rows<HD>(a.dk, rv ? tok * a.dk_stride + col : -1, lane,
+                               [&](int e) { return __uint_as_float(dkr[e]) * a.scale; });
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.item_empty[ii % K_ITEMS]);
     }
   }
   tc_fence_before();
@@ -490,33 +660,6 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, S::TM_COLS);
-  }
-}
-
-// dV and dK of a tile's rows: the sum of the splits' partials, in order, rounded to bf16.
-template <int D>
-__global__ void __launch_bounds__(256) merge_kernel(GradArgs a) {
-  if ((int)blockIdx.x >= *a.plan.count) return;
-  const Tile t = a.plan.in_order[blockIdx.x];
-  constexpr int PLANE = GT * D / 4;
-  const int n = a.hkv * 2 * GT * D / 8;                // chunks of 8 columns of a row
-  for (int i = threadIdx.x + 256 * blockIdx.y; i < n; i += 256 * gridDim.y) {
-    const int row = i % GT, c = i / GT % (D / 8), which = i / (GT * D / 8) % 2;
-    const int kvh = i / (2 * GT * D / 8);
-    const int pos = GT * t.tile + row;
-    if (pos >= t.n) continue;
-    const float4* p = partial<D>(a, t.id, kvh, 0) + which * PLANE + 2 * c * GT + row;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    for (int sp = 0; sp < a.nsplit; ++sp, p += 2 * PLANE) {
-      const float4 u = p[0], v = p[GT];
-      x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
-      y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
-    }
-    const size_t tok = (size_t)t.base + pos;
-    uint16_t* dst = (which ? a.dk + tok * a.dk_stride : a.dv + tok * a.dv_stride) + kvh * D + 8 * c;
-    *reinterpret_cast<uint4*>(dst) =
-        make_uint4(flash::pack_bf16x2(x.x, x.y), flash::pack_bf16x2(x.z, x.w),
-                   flash::pack_bf16x2(y.x, y.y), flash::pack_bf16x2(y.z, y.w));
   }
 }
 
@@ -537,7 +680,7 @@ struct QItem {
   int h, n;      // query head, key tiles
 };
 
-MARS_DEV Walk q_walk(const GradArgs& a) { return Walk(a.plan.count, a.plan.first, a.hq); }
+MARS_DEV Walk q_walk(const GradArgs& a) { return Walk(a.plan.count, a.plan.by_cost, a.hq); }
 
 MARS_DEV bool take(Walk& w, QItem& it) {
   if (!w.take(it.t, it.h)) return false;
@@ -811,14 +954,13 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
 
 // ------------------------------------------------------------------------------- host
 
-// Query-head splits of a KV head's items: enough items for about kWaves per SM, so that the
-// heaviest ones (the first keys of long sequences) can be evened out.
-constexpr int kWaves = 2;
-
-int grad_splits(int batch, int total, int hq, int hkv) {
-  const long long items = packed::max_tiles(batch, total, GT) * hkv;
-  const long long want = ((long long)kWaves * num_sms() + items - 1) / items;
-  return (int)std::min<long long>(hq / hkv, want);
+// CTAs of dkdv_kernel: one per SM, or as many as the most work that `total` rows can make (one
+// sequence) feeds.
+int k_ctas(int batch, int total, int hq, int hkv) {
+  const long long tiles = packed::max_tiles(batch, total, GT);
+  const long long work = hq * (packed::kPairWork * (tiles * (tiles + 1) / 2) + tiles) +
+                         hkv * packed::kTileWork * tiles;
+  return (int)std::max(1LL, std::min<long long>(num_sms(), work / kMinWork));
 }
 
 struct GradSpace {
@@ -830,7 +972,8 @@ struct GradSpace {
 GradSpace carve(void* base, int batch, int total, int hq, int hkv, int d) {
   GradSpace g{};
   size_t off = 0;
-  g.plan = packed::carve_plan(base, off, batch, total, GT, true);
+  const int ctas = k_ctas(batch, total, hq, hkv);
+  g.plan = packed::carve_plan(base, off, batch, total, ctas);
   uint8_t* p = static_cast<uint8_t*>(base);
   auto take = [&](size_t n) {
     float* at = p ? reinterpret_cast<float*>(p + off) : nullptr;
@@ -840,8 +983,7 @@ GradSpace carve(void* base, int batch, int total, int hq, int hkv, int d) {
   const size_t rows = (size_t)packed::max_tiles(batch, total, GT) * GT;
   g.lse_p = take(rows * hq);
   g.d_p = take(rows * hq);
-  const int ns = grad_splits(batch, total, hq, hkv);
-  g.part = take(ns > 1 ? (size_t)ns * 2 * rows * hkv * d : 0);
+  g.part = take((size_t)ctas * 4 * GT * d);
   g.bytes = off;
   return g;
 }
@@ -871,15 +1013,15 @@ cudaError_t launch_grad(const PackedGrad& p, GradArgs& a, cudaStream_t stream) {
   if (e == cudaSuccess) e = set_smem_limit_once(dq_kernel<D>, SQ::TOTAL, attr_q);
   if (e != cudaSuccess) return e;
   const long long tiles = packed::max_tiles(p.batch, p.total, GT);
-  const dim3 by_tile((unsigned)tiles, tiles < num_sms() ? 8 : 2);
+  const long long share = std::max(2LL, std::min(32LL, 8LL * num_sms() / tiles));
+  const dim3 by_tile((unsigned)tiles, (unsigned)share);
   prep_kernel<D><<<by_tile, 256, 0, stream>>>(a);
-  const long long kitems = tiles * p.hkv * a.nsplit, qitems = tiles * p.hq;
-  dkdv_kernel<D><<<(unsigned)std::min<long long>(kitems, num_sms()), K_THREADS, SK::TOTAL, stream>>>(
-      tq, tdo, tk, tv, a);
-  if (a.nsplit > 1) merge_kernel<D><<<by_tile, 256, 0, stream>>>(a);
+  const long long qitems = tiles * p.hq;
+  const unsigned ctas = k_ctas(p.batch, p.total, p.hq, p.hkv);
+  dkdv_kernel<D><<<ctas, K_THREADS, SK::TOTAL, stream>>>(tq, tdo, tk, tv, a);
   dq_kernel<D><<<(unsigned)std::min<long long>(qitems, num_sms()), Q_THREADS, SQ::TOTAL, stream>>>(
       tq, tdo, tk, tv, a);
-  count_launches(a.nsplit > 1 ? 4 : 3);
+  count_launches(3);
   return cudaGetLastError();
 }
 
@@ -893,12 +1035,10 @@ cudaError_t launch_packed_grad(const PackedGrad& p, void* workspace, cudaStream_
   const GradSpace g = carve(workspace, p.batch, p.total, p.hq, p.hkv, p.d);
   GradArgs a{};
   a.plan = g.plan;
-  a.batch = p.batch;
   a.total = p.total;
   a.hq = p.hq;
   a.hkv = p.hkv;
   a.G = p.hq / p.hkv;
-  a.nsplit = grad_splits(p.batch, p.total, p.hq, p.hkv);
   a.pad = packed::max_tiles(p.batch, p.total, GT) * GT;
   a.scale = p.scale;
   a.scale_log2 = p.scale * 1.4426950408889634f;
@@ -915,8 +1055,9 @@ cudaError_t launch_packed_grad(const PackedGrad& p, void* workspace, cudaStream_
   a.dv_stride = p.dv_stride;
   a.part = g.part;
   a.status = p.status;
-  const cudaError_t e = packed::launch_plan(g.plan, p.cu, nullptr, 0, p.batch, p.total, GT,
-                                            p.status, stream);
+  const cudaError_t e = packed::launch_plan(g.plan, p.cu, p.batch, p.total, a.G,
+                                            k_ctas(p.batch, p.total, p.hq, p.hkv), p.status,
+                                            stream);
   if (e != cudaSuccess) return e;
   return p.d == 64 ? launch_grad<64>(p, a, stream) : launch_grad<128>(p, a, stream);
 }
