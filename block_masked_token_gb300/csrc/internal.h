@@ -131,7 +131,7 @@ struct PackedAttn {
 };
 struct PackedPlan {
   bool pair;               // persistent CTAs over equal parts of the work
-  int xt;                  // row tiles per item (pair)
+  int rows;                // tokens of an item (pair)
   bool can_split;          // items may be divided among CTAs (pair)
   size_t ticket_bytes;
   int gp, tpt;             // heads and tokens of a row tile

@@ -18,6 +18,8 @@
 //
 // Where the rows are many, pair_kernel takes two row tiles per CTA instead (see there).
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "flash_tc.cuh"
 #include "internal.h"
@@ -33,6 +35,7 @@ using flash::BQ;
 constexpr int kPagesPerTile = BKV / kPageSize;   // 8
 constexpr int kVStages = 3;                      // as in the decode kernel: no O staging area
 constexpr int kMinSplitTiles = 4;                // key tiles a split takes at least
+constexpr int kEvenSplitTiles = 16;              // where splits only even lengths out
 
 struct AttnArgs {
   const int32_t* cu;
@@ -40,7 +43,8 @@ struct AttnArgs {
   const int32_t* block_table;
   int num_pages, max_pages;
   int batch, total, hq, hkv, gp, tpt, ngrp, nsplit, split_tiles;
-  int xt, rows, can_split;     // pair kernel: row tiles and tokens per item, whether to split items
+  int rows;                    // pair kernel: tokens of an item
+  bool can_split;              // and whether items may be divided
   float scale_log2;
   uint16_t* o;                 // [total][hq][D] bf16
   float* lse;                  // [hq][total] or NULL
@@ -252,7 +256,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap tm_q,
     if (!is_v && lane == 0) mbar_wait(&bar.q_full, 0, nullptr, a.status);
     if (st_flags && a.status) atomicOr(a.status, st_flags);
   } else if (warp == 1 || warp == flash::PV_ISSUER_WARP) {
-    if (warp == 1 && lane == 0)
+    if (warp == 1 && elect_one())
       flash::single_issuer<D, kVStages>(bar, smem, n_total, tmem, a.status);
   } else {
     flash::softmax_loop<D>(bar, smem, pol, n_total, tmem, a.scale_log2, a.status);
@@ -368,6 +372,7 @@ struct PairBar {
   uint64_t drain[3];
   uint32_t tmem_base;
   int abort;
+  uint64_t stored[2], told[2];       // a partial has been written; `last` has been set
   int last[2];                       // whether this CTA merges (per row tile)
   uint64_t item_full[kItems], item_empty[kItems];
   PairItem items[kItems];
@@ -615,7 +620,7 @@ struct PairWalk {
   MARS_DEV int first_token(int x) const { return tok0 + x * a.tpt; }
   // steps of row tile x over all the item's key tiles; 0 if it has no rows
   MARS_DEV int all_steps(int x) const {
-    if (x >= a.xt || first_token(x) >= q.n) return 0;
+    if (first_token(x) >= q.n) return 0;
     return 2 * np + (min(first_token(x) + a.tpt, q.n) - 1) / kStep + 1;
   }
   // its steps [first, last) in this CTA's key tiles
@@ -657,10 +662,6 @@ MARS_DEV bool take_item(PairBar& bar, int i, PairItem& it, volatile int* ab, int
   return true;
 }
 
-MARS_DEV void group_sync(int x) {                  // the 128 threads of a softmax warpgroup
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -699,6 +700,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         mbar_init(&bar.pv_done[x][i], 1);
       }
       mbar_init(&bar.drain[x], 1);
+      mbar_init(&bar.stored[x], 128);
+      mbar_init(&bar.told[x], 1);
     }
     fence_barrier_init();
   }
@@ -901,7 +904,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     };
     const uint32_t s_addr = tmem + S::TM_S + x * BKV + lane_off;
     const uint32_t o_addr = tmem + S::TM_O + x * BKV + lane_off;
-    int g = 0, done = 0;
+    int g = 0, done = 0, parts = 0;                    // parts: of divided items
     bool ok = true;
     RowsPolicy<D> pol;
     pol.a = &a;
@@ -1036,10 +1039,16 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                             __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
         }
         __threadfence();
-        group_sync(x);
-        if (quad == 0 && lane == 0)
-          bar.last[x] = atomicAdd(a.tickets + 2 * it.c1 + x, 1) == it.cuts;
-        group_sync(x);
+        mbar_arrive_warp(&bar.stored[x]);
+        if (quad == 0) {
+          if (!(ok = warp_wait(&bar.stored[x], parts & 1))) break;
+          if (lane == 0) {
+            bar.last[x] = atomicAdd(a.tickets + 2 * it.c1 + x, 1) == it.cuts;
+            mbar_arrive(&bar.told[x]);
+          }
+        }
+        if (!(ok = warp_wait(&bar.told[x], parts & 1))) break;
+        ++parts;
         write = *reinterpret_cast<volatile int*>(&bar.last[x]) != 0;
         if (write) __threadfence();
       }
@@ -1179,10 +1188,10 @@ PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len
   const long long pairs = packed::max_tiles(batch, total, 2 * p.tpt) * hkv * (G / p.gp);
   if (total > (long long)batch * p.tpt && pairs >= num_sms()) {
     p.pair = true;
-    p.xt = 2;
+    p.rows = 2 * p.tpt;
     p.nsplit = 1;
     p.split_tiles = tiles;
-    p.items = packed::max_tiles(batch, total, p.xt * p.tpt) * hkv * (G / p.gp);
+    p.items = pairs;
     p.can_split = tiles >= 2 * kMinPart;
     p.ctas = num_sms();
     p.ticket_bytes = packed::align256(p.ctas * 2 * sizeof(int32_t));
@@ -1190,12 +1199,13 @@ PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len
       p.ws_bytes = p.ticket_bytes + (size_t)p.ctas * 4 * (BQ * (d + 2)) * sizeof(float);
     return p;
   }
-  long long nsplit = 1;
-  if (items < num_sms()) {
-    nsplit = num_sms() / items;
-    nsplit = nsplit < tiles / kMinSplitTiles ? nsplit : tiles / kMinSplitTiles;
-    if (nsplit < 1) nsplit = 1;
-  }
+  // Splits: with few items as many as fill the SMs once; with about as many as SMs, or more, so
+  // that there are two to three CTAs per SM, each with a good part of a list, to even lengths out
+  // (132 items of 16 to 61 key tiles, whole: 82 us, in 2, 3, 4 parts: 85, 74, 78).
+  const long long once = std::min<long long>(num_sms() / items, tiles / kMinSplitTiles);
+  const long long even = items <= num_sms() / 2 ? 1
+      : std::min<long long>(3LL * num_sms() / items, tiles / kEvenSplitTiles);
+  const long long nsplit = std::max(1LL, std::max(once, even));
   p.split_tiles = (int)((tiles + nsplit - 1) / nsplit);
   p.nsplit = (tiles + p.split_tiles - 1) / p.split_tiles;
   p.items = p.ctas = items * p.nsplit;
@@ -1224,8 +1234,7 @@ cudaError_t launch_packed_attn(const PackedAttn& p, const PackedPlan& plan, void
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.o = p.o;
   a.lse = p.lse;
-  a.xt = plan.xt;
-  a.rows = plan.xt * plan.tpt;
+  a.rows = plan.rows;
   a.can_split = plan.can_split;
   a.tickets = static_cast<int32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.ticket_bytes);
