@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libmars.so")
 
 SOURCES = ["mars_api.cu", "kv_commit.cu", "decode_attn.cu", "head_accept.cu", "dual_stream.cu",
            "tmap.cu", "head_accept_noalloc.cu", "ce_loss.cu", "dual_stream_grad.cu",
-           "packed_attn.cu", "packed_plan.cu", "packed_grad.cu", "kv_append.cu"]
+           "packed_attn.cu", "packed_grad.cu", "kv_append.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

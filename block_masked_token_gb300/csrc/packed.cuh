@@ -104,15 +104,16 @@ MARS_DEV long long work_before(int groups, long long tiles, long long t) {
 // worked on: at its turn the read cost 800 cycles and more.
 struct Walk {
   const Tile* list;
-  int heads, total, round, id;         // items per tile, items; the next item (id -1: none)
-  Tile tile;                           // tile of the next item
-  MARS_DEV Walk(const int32_t* count, const Tile* l, int heads_per_tile)
-      : list(l), heads(heads_per_tile), total(*count * heads_per_tile), round(0), id(-1) {
+  int heads, total, cta, ctas;         // items per tile, items; CTA and CTAs
+  int round, id;                       // the next item (id -1: none)
+  Tile tile;                           // and its tile
+  MARS_DEV Walk(const int32_t* count, const Tile* l, int heads_per_tile, int cta_, int ctas_)
+      : list(l), heads(heads_per_tile), total(*count * heads_per_tile), cta(cta_), ctas(ctas_),
+        round(0), id(-1) {
     fetch();
   }
   MARS_DEV void fetch() {
-    const int g = gridDim.x, c = blockIdx.x;
-    id = round * g + ((round & 1) ? g - 1 - c : c);
+    id = round * ctas + ((round & 1) ? ctas - 1 - cta : cta);
     if (id >= total) id = -1;
     if (id >= 0) tile = list[id / heads];
   }
@@ -190,10 +191,6 @@ inline Plan carve_plan(void* base, size_t& off, int batch, int total, int nticke
   r.tickets = reinterpret_cast<int32_t*>(take(ntickets * sizeof(int32_t)));
   return r;
 }
-
-// Fill a plan. groups: query heads per KV head.
-cudaError_t launch_plan(const Plan& plan, const int32_t* cu, int batch, int total, int groups,
-                        int ntickets, int32_t* status, cudaStream_t stream);
 
 }  // namespace packed
 }  // namespace mars

@@ -34,6 +34,7 @@
 #include "flash_tc.cuh"
 #include "internal.h"
 #include "packed.cuh"
+#include "packed_plan.cuh"
 
 namespace mars {
 
@@ -51,6 +52,7 @@ constexpr int NSTAGE = 2;               // Q / dO ring depth of dkdv_kernel
 struct GradArgs {
   packed::Plan plan;
   int total, hq, hkv, G;
+  int k_ctas, q_ctas;                   // CTAs for dK / dV and for dQ
   long long pad;                        // padded rows per head: 128 * the bound of the tiles
   float scale, scale_log2;
   const uint16_t *o, *d_o;              // [total][hq][D]
@@ -64,36 +66,65 @@ struct GradArgs {
 
 // ------------------------------------------------------------------------------ prep
 
-// D and lse of a tile's rows, in 128-row blocks per head; rows past the sequence get zeros.
-// D / 8 lanes per (row, head).
+// Block 0 lists the tiles. Each of the others computes D and lse of PREP_ROWS rows of a tile and
+// up to PREP_HEADS heads, in 128-row blocks per head; rows past the sequence get zeros. D / 8
+// lanes per (row, head), heads fastest, as O and dO lie in memory; the results go out over shared
+// memory with the rows fastest, as lse lies. It reads O and dO once, which bounds it.
+constexpr int PREP_ROWS = 16, PREP_HEADS = 64;
+
 template <int D>
-__global__ void __launch_bounds__(256) prep_kernel(GradArgs a) {
-  constexpr int LANES = D / 8, PER = 256 / LANES;
-  if ((int)blockIdx.x >= *a.plan.count) return;
-  const Tile t = a.plan.in_order[blockIdx.x];
+__global__ void __launch_bounds__(packed::kPlanThreads, 5)
+prep_kernel(GradArgs a, packed::PlanArgs plan) {
+  if (blockIdx.x == 0) {
+    packed::make_plan(plan);
+    return;
+  }
+  __shared__ float s_d[PREP_HEADS][PREP_ROWS + 1];
+  constexpr int LANES = D / 8, PER = packed::kPlanThreads / LANES;
+  constexpr int CHUNKS = GT / PREP_ROWS;
+  const int hchunks = (a.hq + PREP_HEADS - 1) / PREP_HEADS;
+  int id = blockIdx.x - 1;
+  const int h0 = id % hchunks * PREP_HEADS;
+  id /= hchunks;
+  const int chunk = id % CHUNKS;
+  id /= CHUNKS;
+  bool bad;                                            // reported with the plan
+  const packed::Seq t = packed::find_tile(plan.cu, plan.batch, a.total, GT, 0, id, bad);
+  if (t.s < 0) return;
   const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-  // heads vary fastest, as in memory
-  const int total = GT * a.hq;
-#pragma unroll 4
-  for (int i = sub + blockIdx.y * PER; i < total; i += PER * gridDim.y) {
-    const int r = i / a.hq, h = i - r * a.hq;
-    const int row = t.tile * GT + r;
-    float acc = 0.f;
-    if (row < t.n) {
-      const size_t at = ((size_t)(t.base + row) * a.hq + h) * D + lane * 8;
-      float x[8], y[8];
-      unpack8(*reinterpret_cast<const uint4*>(a.o + at), x);
-      unpack8(*reinterpret_cast<const uint4*>(a.d_o + at), y);
+  const int nh = min(PREP_HEADS, a.hq - h0), row0 = t.tile * GT + chunk * PREP_ROWS;
+  const int n = PREP_ROWS * nh;
+  constexpr int AHEAD = 4;                             // loads in flight per thread: 2 * AHEAD
+  for (int i0 = sub; i0 - sub < n; i0 += AHEAD * PER) {
+    uint4 x[AHEAD], y[AHEAD];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc += x[e] * y[e];
+    for (int u = 0; u < AHEAD; ++u) {
+      // past the end or the sequence: some row, whose result is not used
+      const int i = min(i0 + u * PER, n - 1), r = i / nh, h = i - r * nh;
+      const int row = min(row0 + r, t.n - 1);
+      const size_t at = ((size_t)(t.base + row) * a.hq + h0 + h) * D + lane * 8;
+      x[u] = *reinterpret_cast<const uint4*>(a.o + at);
+      y[u] = *reinterpret_cast<const uint4*>(a.d_o + at);
     }
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) {
-      const size_t p = (size_t)h * a.pad + (size_t)t.id * GT + r;
-      a.d_p[p] = acc;
-      a.lse_p[p] = row < t.n ? a.lse[(size_t)h * a.total + t.base + row] : 0.f;
+    for (int u = 0; u < AHEAD; ++u) {
+      float xf[8], yf[8], acc = 0.f;
+      unpack8(x[u], xf);
+      unpack8(y[u], yf);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc += xf[e] * yf[e];
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      const int i = i0 + u * PER;
+      if (lane == 0 && i < n) s_d[i % nh][i / nh] = acc;
     }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < PREP_ROWS * nh; i += packed::kPlanThreads) {
+    const int r = i % PREP_ROWS, h = i / PREP_ROWS;
+    const size_t p = (size_t)(h0 + h) * a.pad + (size_t)id * GT + chunk * PREP_ROWS + r;
+    a.d_p[p] = row0 + r < t.n ? s_d[h][r] : 0.f;
+    a.lse_p[p] = row0 + r < t.n ? a.lse[(size_t)(h0 + h) * a.total + t.base + row0 + r] : 0.f;
   }
 }
 
@@ -162,7 +193,7 @@ struct KLine {
   int parts;
   MARS_DEV explicit KLine(const GradArgs& a)
       : head(a.plan.before[*a.plan.count]), total(head * a.hkv) {
-    parts = (int)max(1LL, min((long long)gridDim.x, total / kMinWork));
+    parts = (int)max(1LL, min((long long)a.k_ctas, total / kMinWork));
   }
   MARS_DEV long long cut(int i) const { return i * total / parts; }
   // The pair before which position pos cuts an item of `pairs` pairs and `work` at s0: 0 before
@@ -258,12 +289,9 @@ MARS_DEV float4* partial(const GradArgs& a, int cta, bool inside) {
 MARS_DEV uint32_t p_col(int k) { return (uint32_t)(8 * k + (k >= 4 ? 32 : 0)); }
 
 template <int D>
-__global__ void __launch_bounds__(K_THREADS, 1)
-dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-            const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-            GradArgs a) {
+MARS_DEV void dkdv(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                   const CUtensorMap& tm_v, const GradArgs& a, uint8_t* smem_raw) {
   using S = KSmem<D>;
-  extern __shared__ uint8_t smem_raw[];
   __shared__ KBar bar;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -680,7 +708,9 @@ struct QItem {
   int h, n;      // query head, key tiles
 };
 
-MARS_DEV Walk q_walk(const GradArgs& a) { return Walk(a.plan.count, a.plan.by_cost, a.hq); }
+MARS_DEV Walk q_walk(const GradArgs& a) { 
+  return Walk(a.plan.count, a.plan.by_cost, a.hq, blockIdx.x - a.k_ctas, a.q_ctas);
+}
 
 MARS_DEV bool take(Walk& w, QItem& it) {
   if (!w.take(it.t, it.h)) return false;
@@ -689,14 +719,11 @@ MARS_DEV bool take(Walk& w, QItem& it) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(Q_THREADS, 1)
-dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-          GradArgs a) {
+MARS_DEV void dq(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                 const CUtensorMap& tm_v, const GradArgs& a, uint8_t* smem_raw) {
   using S = flash::Smem<D, D / 64>;                 // the dO tile over the staging area
   static_assert(D * GT * 2 <= (D / 64) * GT * 128, "dO tile fits the staging area");
   constexpr int TM_S = 0, TM_DP = GT, TM_DQ = 2 * GT, TM_DS = 3 * GT;
-  extern __shared__ uint8_t smem_raw[];
   __shared__ flash::Barriers bar;
   __shared__ QBar qb;
   const uint32_t raw = smem_u32(smem_raw);
@@ -952,6 +979,21 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   }
 }
 
+// The first k_ctas CTAs compute dK and dV, the others dQ: one launch, so that dQ's CTAs take over
+// the SMs as they become free, and small problems run side by side.
+template <int D>
+__global__ void __launch_bounds__(K_THREADS, 1)
+grad_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+            const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+            GradArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  static_assert(K_THREADS == Q_THREADS, "one launch for both");
+  if ((int)blockIdx.x < a.k_ctas)
+    dkdv<D>(tm_q, tm_do, tm_k, tm_v, a, smem_raw);
+  else
+    dq<D>(tm_q, tm_do, tm_k, tm_v, a, smem_raw);
+}
+
 // ------------------------------------------------------------------------------- host
 
 // CTAs of dkdv_kernel: one per SM, or as many as the most work that `total` rows can make (one
@@ -1005,23 +1047,19 @@ cudaError_t launch_grad(const PackedGrad& p, GradArgs& a, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   using SK = KSmem<D>;
   using SQ = flash::Smem<D, D / 64>;
-  static_assert(SK::TOTAL + sizeof(KBar) <= 227 * 1024, "dK/dV layout fits shared memory");
-  static_assert(SQ::TOTAL + sizeof(flash::Barriers) + sizeof(QBar) <= 227 * 1024,
-                "dQ layout fits shared memory");
-  static std::atomic<int> attr_k[64], attr_q[64];
-  cudaError_t e = set_smem_limit_once(dkdv_kernel<D>, SK::TOTAL, attr_k);
-  if (e == cudaSuccess) e = set_smem_limit_once(dq_kernel<D>, SQ::TOTAL, attr_q);
+  constexpr int kSmem = std::max<int>(SK::TOTAL, SQ::TOTAL);
+  static_assert(kSmem + sizeof(KBar) + sizeof(KStart) + sizeof(flash::Barriers) + sizeof(QBar) <=
+                    227 * 1024,
+                "both layouts fit shared memory");
+  static std::atomic<int> attr[64];
+  const cudaError_t e = set_smem_limit_once(grad_kernel<D>, kSmem, attr);
   if (e != cudaSuccess) return e;
   const long long tiles = packed::max_tiles(p.batch, p.total, GT);
-  const long long share = std::max(2LL, std::min(32LL, 8LL * num_sms() / tiles));
-  const dim3 by_tile((unsigned)tiles, (unsigned)share);
-  prep_kernel<D><<<by_tile, 256, 0, stream>>>(a);
-  const long long qitems = tiles * p.hq;
-  const unsigned ctas = k_ctas(p.batch, p.total, p.hq, p.hkv);
-  dkdv_kernel<D><<<ctas, K_THREADS, SK::TOTAL, stream>>>(tq, tdo, tk, tv, a);
-  dq_kernel<D><<<(unsigned)std::min<long long>(qitems, num_sms()), Q_THREADS, SQ::TOTAL, stream>>>(
-      tq, tdo, tk, tv, a);
-  count_launches(3);
+  const long long preps = tiles * (GT / PREP_ROWS) * ((p.hq + PREP_HEADS - 1) / PREP_HEADS);
+  prep_kernel<D><<<(unsigned)(1 + preps), packed::kPlanThreads, 0, stream>>>(
+      a, packed::PlanArgs{a.plan, p.cu, p.batch, p.total, a.G, a.k_ctas, p.status});
+  grad_kernel<D><<<(unsigned)(a.k_ctas + a.q_ctas), K_THREADS, kSmem, stream>>>(tq, tdo, tk, tv, a);
+  count_launches(2);
   return cudaGetLastError();
 }
 
@@ -1039,7 +1077,10 @@ cudaError_t launch_packed_grad(const PackedGrad& p, void* workspace, cudaStream_
   a.hq = p.hq;
   a.hkv = p.hkv;
   a.G = p.hq / p.hkv;
-  a.pad = packed::max_tiles(p.batch, p.total, GT) * GT;
+  const long long tiles = packed::max_tiles(p.batch, p.total, GT);
+  a.pad = tiles * GT;
+  a.k_ctas = k_ctas(p.batch, p.total, p.hq, p.hkv);
+  a.q_ctas = (int)std::min<long long>(num_sms(), tiles * p.hq);
   a.scale = p.scale;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.o = p.o;
@@ -1055,10 +1096,6 @@ cudaError_t launch_packed_grad(const PackedGrad& p, void* workspace, cudaStream_
   a.dv_stride = p.dv_stride;
   a.part = g.part;
   a.status = p.status;
-  const cudaError_t e = packed::launch_plan(g.plan, p.cu, p.batch, p.total, a.G,
-                                            k_ctas(p.batch, p.total, p.hq, p.hkv), p.status,
-                                            stream);
-  if (e != cudaSuccess) return e;
   return p.d == 64 ? launch_grad<64>(p, a, stream) : launch_grad<128>(p, a, stream);
 }
 

@@ -1,19 +1,18 @@
-// Tile lists of a packed batch for its gradient (packed.cuh): one CTA reads the sequence
-// boundaries, counts the 128-row tiles of each sequence and writes them out in their order, with
-// the work before each, and in the order of falling cost (a counting sort over kBuckets cost
-// classes, so that the list is sorted to about a two-thousandth of the largest cost). Entries of
-// one class come in any order: that moves work between CTAs, not results.
+// Tile lists of a packed batch for its gradient: one CTA reads the sequence boundaries, counts
+// the 128-row tiles of each sequence and writes them out in their order, with the work before
+// each, and in the order of falling cost (a counting sort over kBuckets cost classes, so that
+// the list is sorted to about a five-hundredth of the largest cost). Entries of one class come
+// in any order: that moves work between CTAs, not results.
+#pragma once
+
 #include "common.cuh"
-#include "internal.h"
 #include "packed.cuh"
 
 namespace mars {
 namespace packed {
 
-namespace {
-
-constexpr int kThreads = 1024;
-constexpr int kBuckets = 2048;
+constexpr int kPlanThreads = 256;
+constexpr int kBuckets = 2 * kPlanThreads;
 
 struct PlanArgs {
   Plan plan;
@@ -34,37 +33,28 @@ MARS_DEV T scan(T v, T* s_warp) {
   }
   if (lane == 31) s_warp[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    T w = s_warp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const T u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w = join(w, u);
-    }
-    s_warp[lane] = w;
-  }
-  __syncthreads();
-  if (warp > 0) v = join(v, s_warp[warp - 1]);
+  for (int w = 0; w < warp; ++w) v = join(v, s_warp[w]);
   __syncthreads();
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
-  __shared__ int s_warp[32];
-  __shared__ long long s_warp64[32];
+// One CTA of kPlanThreads threads: fill a.plan.
+MARS_DEV void make_plan(const PlanArgs& a) {
+  __shared__ int s_warp[kPlanThreads / 32];
+  __shared__ long long s_warp64[kPlanThreads / 32];
   __shared__ int s_hist[kBuckets];
-  __shared__ int s_base[kThreads], s_n[kThreads], s_off[kThreads];
-  __shared__ long long s_pre[kThreads], s_work;
+  __shared__ int s_base[kPlanThreads], s_n[kPlanThreads], s_off[kPlanThreads];
+  __shared__ long long s_pre[kPlanThreads], s_work;
   __shared__ int s_top, s_tiles, s_cost;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
   const auto tiles_of = [](int n) { return (n + kTileRows - 1) / kTileRows; };
 
-  // A pass over the sequences, kThreads at a time, calls f(base, n, first tile, tiles, work
+  // A pass over the sequences, kPlanThreads at a time, calls f(base, n, first tile, tiles, work
   // before) with one warp per sequence. The chunk's arrays are kept for the next pass where
   // there is one chunk only.
   auto each = [&](bool first, auto f) {
-    if (tid == 0 && (first || a.batch > kThreads)) {
+    if (tid == 0 && (first || a.batch > kPlanThreads)) {
       const int c0 = a.cu[0];
       s_top = min(max(c0, 0), a.total);
       s_tiles = 0;
@@ -72,8 +62,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
       bad |= c0 != s_top;
     }
     __syncthreads();
-    for (int s0 = 0; s0 < a.batch; s0 += kThreads) {
-      if (first || a.batch > kThreads) {
+    for (int s0 = 0; s0 < a.batch; s0 += kPlanThreads) {
+      if (first || a.batch > kPlanThreads) {
         const int s = s0 + tid, top = s_top, tiles0 = s_tiles;
         const long long work0 = s_work;
         const int c = s < a.batch ? a.cu[s + 1] : top;
@@ -91,21 +81,21 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
         s_n[tid] = n;
         s_off[tid] = tiles0 + incl - mine;
         s_pre[tid] = work0 + sum - work;
-        if (tid == kThreads - 1) {
+        if (tid == kPlanThreads - 1) {
           s_top = end;
           s_tiles = tiles0 + incl;
           s_work = work0 + sum;
         }
         __syncthreads();
       }
-      for (int i = warp; i < min(kThreads, a.batch - s0); i += kThreads / 32)
+      for (int i = warp; i < min(kPlanThreads, a.batch - s0); i += kPlanThreads / 32)
         f(s_base[i], s_n[i], s_off[i], tiles_of(s_n[i]), s_pre[i]);
       __syncthreads();
     }
   };
 
-  for (int i = tid; i < kBuckets; i += kThreads) s_hist[i] = 0;
-  for (int i = tid; i < a.ntickets; i += kThreads) a.plan.tickets[i] = 0;
+  for (int i = tid; i < kBuckets; i += kPlanThreads) s_hist[i] = 0;
+  for (int i = tid; i < a.ntickets; i += kPlanThreads) a.plan.tickets[i] = 0;
   if (tid == 0) s_cost = 1;
   __syncthreads();
   each(true, [&](int, int, int, int tiles, long long) {
@@ -123,7 +113,6 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
   const int2 v = *h;
   const int before = scan<false>(v.x + v.y, s_warp) - v.x - v.y;
   *h = make_int2(before, before + v.x);
-  static_assert(kBuckets == 2 * kThreads, "two classes per thread");
   __syncthreads();
   each(false, [&](int base, int n, int off, int tiles, long long pre) {
     for (int t = lane; t < tiles; t += 32) {
@@ -138,16 +127,6 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
     *a.plan.count = s_tiles;
   }
   if (bad && a.status) atomicOr(a.status, MARS_ST_BADSEQ);
-}
-
-}  // namespace
-
-cudaError_t launch_plan(const Plan& plan, const int32_t* cu, int batch, int total, int groups,
-                        int ntickets, int32_t* status, cudaStream_t stream) {
-  plan_kernel<<<1, kThreads, 0, stream>>>(
-      PlanArgs{plan, cu, batch, total, groups, ntickets, status});
-  count_launches(1);
-  return cudaGetLastError();
 }
 
 }  // namespace packed
