@@ -66,6 +66,13 @@ def test_packed_many_rows(lens, heads):
     assert same(o, again) and same(lse, lse2)
 
 
+def test_packed_many_rows_of_more_sequences_than_a_ctas_threads():
+    x = make([(i * 11) % 67 for i in range(500)], 14, 2, 64, seed=33, tail=2)
+    o, lse, st = run_packed(cuda(x))
+    assert st == 0
+    check_packed(x, o, lse)
+
+
 def test_packed_many_sequences_and_leading_rows():
     x = make([(i * 7) % 23 for i in range(75)], 4, 2, 64, seed=6, lead=5, tail=4)
     o, lse, st = run_packed(cuda(x))
@@ -166,6 +173,55 @@ def test_gradient_without_splits():
     dq, dk, dv, st = run_grad(y, o, lse, y["do"])
     assert st == 0
     check_grad(x, dq, dk, dv)
+
+
+# Items divided among several CTAs, more heads than a block of prep takes, more sequences than
+# the plan's CTA has threads.
+GRAD_MANY = [([1500], (28, 4, 128)), ([700, 0, 301, 65], (14, 2, 64)), ([130, 40], (130, 2, 64)),
+             ([(i * 11) % 67 for i in range(600)], (4, 2, 64))]
+
+
+@pytest.mark.parametrize("lens, heads", GRAD_MANY, ids=["one", "few", "heads", "sequences"])
+def test_gradient_of_many_rows(lens, heads):
+    x = make(lens, *heads, seed=34, tail=3, lead=1)
+    y = cuda(x)
+    o, lse, _ = run_packed(y)
+    dq, dk, dv, st = run_grad(y, o, lse, y["do"])
+    assert st == 0
+    check_grad(x, dq, dk, dv)
+    again = run_grad(y, o, lse, y["do"])
+    assert all(same(a, b) for a, b in zip((dq, dk, dv), again))
+
+
+def test_training_steps_at_once_on_two_streams():
+    """Calls with workspaces of their own do not disturb one another."""
+    xs = [make([600, 90], 28, 4, 128, seed=35), make([40, 333, 7], 14, 2, 64, seed=36)]
+    ys = [cuda(x) for x in xs]
+    want = []
+    for y in ys:
+        o, lse, _ = run_packed(y)
+        want.append([o, lse, *run_grad(y, o, lse, y["do"])[:3]])
+    streams = [torch.cuda.Stream() for _ in ys]
+    got = []
+    for y in ys:
+        n, hq, d = y["q"].shape
+        b, hkv = len(y["cu"]) - 1, y["k"].shape[1]
+        got.append([torch.full_like(y["do"], 7.0), torch.full((hq, n), 7.0, device="cuda"),
+                    *torch.full((n, hq + 2 * hkv, d), 7.0, dtype=torch.bfloat16,
+                                device="cuda").split([hq, hkv, hkv], dim=1),
+                    workspace(packed.OP_ATTN_PACKED, b, n, hq, hkv, d),
+                    workspace(packed.OP_ATTN_PACKED_GRAD, b, n, hq, hkv, d)])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for y, g, stream in zip(ys, got, streams):
+            o, lse, dq, dk, dv, ws, ws2 = g
+            with torch.cuda.stream(stream):
+                packed.mars_attn_packed(y["q"], y["k"], y["v"], y["cu"], o, ws, lse=lse)
+                packed.mars_attn_packed_grad(y["q"], y["k"], y["v"], o, y["do"], lse, y["cu"], dq,
+                                             dk, dv, ws2)
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(same(a, b) for a, b in zip(w, g))
 
 
 def test_gradient_of_single_tokens_is_exact():
