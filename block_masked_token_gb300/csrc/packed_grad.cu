@@ -70,7 +70,7 @@ struct GradArgs {
 // up to PREP_HEADS heads, in 128-row blocks per head; rows past the sequence get zeros. D / 8
 // lanes per (row, head), heads fastest, as O and dO lie in memory; the results go out over shared
 // memory with the rows fastest, as lse lies. It reads O and dO once, which bounds it.
-constexpr int PREP_ROWS = 16, PREP_HEADS = 64;
+constexpr int PREP_ROWS = 8, PREP_HEADS = 64;
 
 template <int D>
 __global__ void __launch_bounds__(packed::kPlanThreads, 5)
