@@ -155,6 +155,8 @@ struct PackedGrad {
   float scale;
   int32_t* status;
 };
+// The largest count of items or CTAs, which are 32-bit numbers.
+long long packed_grad_items(int batch, int total, int hq);
 size_t packed_grad_workspace_bytes(int batch, int total, int hq, int hkv, int d);
 cudaError_t launch_packed_grad(const PackedGrad& p, void* workspace, cudaStream_t stream);
 

@@ -509,8 +509,7 @@ int mars_attn_packed_grad(const mars_bf16* q, const mars_bf16* k, const mars_bf1
     if (!aligned16(x)) return MARS_EALIGN;
   if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)d);
   if (isinf(scale)) return MARS_EINVAL;
-  // (tile, head) items are counted in 32 bits
-  if (((long long)total / 128 + batch) * hq > 0x7fffffffLL) return MARS_EUNSUPPORTED;
+  if ((rc = grid_fits(mars::packed_grad_items(batch, total, hq)))) return rc;
   if (ws_bytes < mars::packed_grad_workspace_bytes(batch, total, hq, hkv, d))
     return MARS_ENOSPACE;
   const mars::PackedGrad p{q,         k,         v,         o,         d_o,   q_stride,

@@ -94,7 +94,9 @@ struct Plan {
 constexpr int kPairWork = 3, kTileWork = 6;
 
 // That of a tile with `after` query tiles, and of the first t of a sequence's tiles.
-MARS_DEV int tile_work(int groups, int after) { return groups * (kPairWork * after + 1) + kTileWork; }
+MARS_DEV int tile_work(int groups, int after) {
+  return groups * (kPairWork * after + 1) + kTileWork;
+}
 MARS_DEV long long work_before(int groups, long long tiles, long long t) {
   return groups * (kPairWork * (t * tiles - t * (t - 1) / 2) + t) + kTileWork * t;
 }

@@ -13,8 +13,11 @@
 // slots of the last page, unmapped pages) are masked, and their V rows cleared, so that
 // whatever they hold stays out.
 //
-// With few tiles and long key lists the list is cut into splits: each CTA writes an
-// unnormalised partial (m in log2 units, l, O) and a second kernel merges them.
+// With few tiles and long key lists the list is cut into splits (plan_packed): each CTA writes
+// an unnormalised partial (m in log2 units, l, O) and a second kernel merges them. One token for
+// each of 32 sequences (28 heads over 4 of 128, 158,000 cached keys, 325 MB) takes 69 us, 0.69
+// of the copy bandwidth; one SM takes in 16-token pages at 27 bytes per cycle, so a CTA that is
+// left alone with a long list bounds it.
 //
 // Where the rows are many, pair_kernel takes two row tiles per CTA instead (see there).
 
@@ -48,7 +51,7 @@ struct AttnArgs {
   float scale_log2;
   uint16_t* o;                 // [total][hq][D] bf16
   float* lse;                  // [hq][total] or NULL
-  float* part;                 // [nsplit][total][hq][D + 4] with several splits; pair kernel: partial()
+  float* part;                 // [nsplit][total][hq][D + 4]; pair kernel: partial()
   int32_t* tickets;            // pair kernel: [ctas][2], zero at its start
   int32_t* status;
 };
@@ -119,7 +122,8 @@ struct RowsPolicy {
     const size_t tok = (size_t)base + token(row);
     const int h = h0 + row % a->gp;
     if (a->nsplit == 1) {
-      if (col == 0 && a->lse) a->lse[(size_t)h * a->total + tok] = l > 0.f ? m + log2f(l) : -INFINITY;
+      if (col == 0 && a->lse)
+        a->lse[(size_t)h * a->total + tok] = l > 0.f ? m + log2f(l) : -INFINITY;
       uint4* dst = reinterpret_cast<uint4*>(a->o + (tok * a->hq + h) * D + col);
 #pragma unroll
       for (int e = 0; e < 32; e += 8) {
@@ -330,6 +334,10 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
 // have to be in flight, two per row tile, and TMEM holds just that many (two S buffers of 64
 // columns per row tile, P in bf16 over the upper half of each, and two O of 128). With 128-key
 // steps, one in flight per row tile, a pair of tiles took 4,000 cycles instead of 2,870.
+// What bounds those 2,870 is shared memory at 128 bytes per cycle: an S MMA of 64 keys reads 6 KB
+// for its 32 cycles of arithmetic, S 192 KB per pair, PV 64 KB, the copies write 64 KB: 2,500
+// cycles. One sequence of 8,000 rows (28 heads over 4) runs at 1.3 PFLOP/s, 0.67 of the GEMM rate.
+// The start and output of an item take about 7,000 cycles, which bounds short sequences.
 // A row tile's first P of an item also says that its warps have read the O of the item before.
 //
 // Work is divided evenly, whatever the lengths: the items of all sequences are laid out on a
@@ -359,7 +367,7 @@ struct PairSmem {
 // An item as the loader hands it to the other warps.
 struct PairItem {
   int s, base, n, P, np, tok0, h0;
-  int tiles, ja, jb;                 // key tiles; those that this CTA visits (jb = 0: no more items)
+  int tiles, ja, jb;                 // key tiles; this CTA's [ja, jb) (jb = 0: no more items)
   int all[2], steps[2];              // steps of the row tiles: over all key tiles, in this CTA
   int c1, cuts;                      // a divided item: CTAs c1 .. c1 + cuts - 1 start inside it
 };
@@ -564,10 +572,10 @@ MARS_DEV void find_part(const AttnArgs& a, PartScan& sc) {
   __syncthreads();
 }
 
-// The items of a CTA's part, one after another (each role walks on its own): row tiles at
-// tokens tok0 and tok0 + tpt, the steps of 64 keys that each takes (the last is left out where
-// a tile's own keys end in the first half of a key tile), and the key tiles [ja, jb) of the
-// item's `tiles` that this CTA visits.
+// The items of a CTA's part, one after another: row tiles at tokens tok0 and tok0 + tpt, the
+// steps of 64 keys that each takes (the last is left out where a tile's own keys end in the
+// first half of a key tile), and the key tiles [ja, jb) of the item's `tiles` that this CTA
+// visits. The loader walks and hands the items to the other warps.
 struct PairWalk {
   const AttnArgs& a;
   const PairPart& p;
@@ -576,7 +584,8 @@ struct PairWalk {
   long long s0, work;
   bool more;
 
-  MARS_DEV PairWalk(const AttnArgs& a_, const PairPart& p_) : a(a_), p(p_), q(p_.q), g(p_.g), t(p_.t) {
+  MARS_DEV PairWalk(const AttnArgs& a_, const PairPart& p_)
+      : a(a_), p(p_), q(p_.q), g(p_.g), t(p_.t) {
     item();
     ja = p.j;
     if (ja == tiles) next(); else end();
@@ -630,7 +639,9 @@ struct PairWalk {
                {all_steps(0), all_steps(1)}, {steps(0), steps(1)}, 0, 0};
     if (ja > 0 || jb < tiles) {
       const long long part = p.total / p.ctas;
-      auto cut = [&](long long c) { return cut_at(a, c * p.total / p.ctas, s0, work, tiles, part); };
+      auto cut = [&](long long c) {
+        return cut_at(a, c * p.total / p.ctas, s0, work, tiles, part);
+      };
       long long c1 = s0 * p.ctas / p.total;
       while (c1 * p.total / p.ctas <= s0 || cut(c1) == 0) ++c1;
       d.c1 = (int)c1;
@@ -651,7 +662,8 @@ constexpr int PART4 = BQ * D / 4 + BQ / 2;       // float4 of a partial
 // pairs of m and l.
 template <int D>
 MARS_DEV float4* partial(const AttnArgs& a, int cta, bool inside, int x) {
-  return reinterpret_cast<float4*>(a.part) + (((size_t)cta * 2 + (inside ? 0 : 1)) * 2 + x) * PART4<D>;
+  return reinterpret_cast<float4*>(a.part) +
+         (((size_t)cta * 2 + (inside ? 0 : 1)) * 2 + x) * PART4<D>;
 }
 
 // The next item of the loader's queue (number i), copied; false if the wait gave up. The
@@ -750,9 +762,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           for (int v = 1; v >= 0; --v) {                 // V first, see the softmax warps' clearing
             const int n = v ? kVSlots : kKSlots, st = g % n;
             uint64_t* full = v ? &bar.v_full[st] : &bar.k_full[st];
+            uint64_t* empty = v ? &bar.v_empty[st] : &bar.k_empty[st];
             int good = 1;
             if (lane == 0) {
-              good = mbar_wait(v ? &bar.v_empty[st] : &bar.k_empty[st], ((g / n) & 1) ^ 1, ab, a.status);
+              good = mbar_wait(empty, ((g / n) & 1) ^ 1, ab, a.status);
               if (good) mbar_arrive_expect_tx(full, S::TILE);
             }
             ok = __shfl_sync(0xffffffffu, good, 0) != 0;
@@ -870,7 +883,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           for (int j = 0; j < it.jb - it.ja && ok; ++j, ++g) {
             const int st = g % kVSlots;
             if (!(ok = mbar_wait(&bar.v_full[st], (g / kVSlots) & 1, ab, a.status))) break;
-            const uint64_t vd = sdesc_sw128(smem_u32(smem + S::OFF_V + st * S::TILE), BKV * 128, 1024);
+            const uint64_t vd =
+                sdesc_sw128(smem_u32(smem + S::OFF_V + st * S::TILE), BKV * 128, 1024);
             for (int hx = 0; hx < 4; ++hx) {
               const int h = hx >> 1, x = hx & 1, u = 2 * j + h;
               if (u >= (x ? steps[1] : steps[0])) continue;
@@ -879,7 +893,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               tc_fence_after();
 #pragma unroll
               for (int k = 0; k < kStep / 16; ++k)
-                mma_bf16_ts(tmem + S::TM_O + x * BKV, tmem + S::TM_S + x * BKV + b * kStep + S::P_OFF + k * 8,
+                mma_bf16_ts(tmem + S::TM_O + x * BKV,
+                            tmem + S::TM_S + x * BKV + b * kStep + S::P_OFF + k * 8,
                             sdesc_advance(vd, h * (kStep * 128) + k * 2048), idesc, (u | k) != 0);
               mma_commit(&bar.pv_done[x][b]);
               ++done[x];
@@ -929,7 +944,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       pol.np = it.np;
       pol.h0 = it.h0;
       pol.j0 = it.ja;
-      pol.last_tok = min(it.tok0 + a.rows, it.n) - 1;   // of the item: V rows that neither tile reads
+      pol.last_tok = min(it.tok0 + a.rows, it.n) - 1;   // of the item: neither tile reads on
       const int tok = pol.tok0 + pol.trow;              // this thread's token
       const flash::RowVis vis{tok + 1, 0, -1};
       float m = -INFINITY, l = 0.f;
@@ -1019,8 +1034,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       tc_fence_after();
       // where this thread's row goes, in elements (-1: no token)
       const long long at =
-          pol.trow < a.tpt && tok < it.n ? (((long long)it.base + tok) * a.hq + it.h0 + pol.hrow) * D
-                                         : -1;
+          pol.trow < a.tpt && tok < it.n
+              ? (((long long)it.base + tok) * a.hq + it.h0 + pol.hrow) * D : -1;
       bool write = it.ja == 0 && it.jb == it.tiles;
       if (!write) {
         // a part of the item: its partial, and the merge by the last part to arrive
@@ -1156,7 +1171,8 @@ cudaError_t launch_rows(const PackedAttn& p, const PackedPlan& plan, AttnArgs& a
       e = cudaMemsetAsync(a.tickets, 0, plan.ctas * 2 * sizeof(int32_t), stream);
       if (e != cudaSuccess) return e;
     }
-    pair_kernel<D><<<(unsigned)plan.ctas, PAIR_THREADS, SP::TOTAL, stream>>>(tq, tk, tv, tkp, tvp, a);
+    pair_kernel<D><<<(unsigned)plan.ctas, PAIR_THREADS, SP::TOTAL, stream>>>(tq, tk, tv, tkp,
+                                                                             tvp, a);
     count_launches(1);
     return cudaGetLastError();
   }

@@ -6,25 +6,33 @@
 // Row 0 of a sequence sees one key, whose weight is 1 whatever the score: its dS is 0, and is
 // set so instead of being left to the cancellation of dP and D.
 //
-// Two tcgen05 kernels over 128-row tiles, neither storing a score block, each a persistent CTA
-// per SM:
-//   - dkdv_kernel: an item is a key tile and a KV head. Per pair of it with a query head of the
-//     group and a query tile at or after it: S^T = K Q^T and dP^T = V dO^T (keys on TMEM
-//     lanes), then dV += P^T dO and dK += dS^T Q with P^T and dS^T as bf16 operands in TMEM, all
-//     in two halves of 64 queries with their own barriers. dV and dK stay in TMEM over the item.
+// Two tcgen05 pipelines over 128-row tiles, neither storing a score block, each a persistent CTA
+// per SM, in one launch:
+//   - dkdv: an item is a key tile and a KV head. Per pair of it with a query head of the group
+//     and a query tile at or after it: S^T = K Q^T and dP^T = V dO^T (keys on TMEM lanes), then
+//     dV += P^T dO and dK += dS^T Q with P^T and dS^T as bf16 operands in TMEM, all in two
+//     halves of 64 queries with their own barriers. dV and dK stay in TMEM over the item.
 //     The pairs of all items are divided evenly among the CTAs, whatever the lengths (KWalk):
 //     an item that is cut leaves partials, and the last of its CTAs to finish adds them up in
 //     the order of the pairs, so that the result is the same from run to run. With whole items
 //     in turn, 4096 rows (28 heads over 4) kept the SMs busy for 44 % of the time, with an
 //     item's heads divided in three for 76 %.
-//   - dq_kernel: an item is a query tile and a query head, taken in turn by falling cost; S, dP
-//     and dQ += dS K per key tile.
+//   - dq: an item is a query tile and a query head, taken in turn by falling cost; S, dP and
+//     dQ += dS K per key tile.
 // P and dS are rounded to bf16 as MMA operands; dS is formed from the unrounded P. prep_kernel
-// computes D and lays lse and D out in 128-row blocks per (head, tile), for bulk copies.
+// computes D, lays lse and D out in 128-row blocks per (head, tile), for bulk copies, and lists
+// the tiles.
+//
+// What bounds both is shared memory at 128 bytes per cycle (d = 128): a pair of dkdv reads 96 KB
+// each for S^T and dP^T (with halves of 64 queries an MMA reads its 4 KB of K or V again), 32 KB
+// each for dV and dK, and 64 KB are copied in: 2,500 cycles of the 2,900 measured; a tile of dq
+// 64 + 64 + 32 KB and 64 KB in: 1,750 of 1,850. Whole S^T and dP^T would save 64 KB a pair, but
+// then S^T of the next pair waits for all of dV: 5 % slower. 4096 rows (28 heads over 4) take 275
+// us: 1.1 PFLOP/s counting each product once, 1.5 (0.78 of the GEMM rate) as computed.
 //
 // A pair's tile can reach past its sequence: scores there are masked, and the rows of dO, Q
-// (dkdv_kernel) or K (dq_kernel) that the masked weights of 0 would multiply are cleared in
-// shared memory, so that other sequences' rows have no effect whatever they hold.
+// (dkdv) or K (dq) that the masked weights of 0 would multiply are cleared in shared memory, so
+// that other sequences' rows have no effect whatever they hold.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -47,7 +55,7 @@ using packed::Walk;
 constexpr int GT = 128;                 // rows per key tile and per query tile
 constexpr int MATH_WARPS = 8;           // two per TMEM lane quadrant, 64 columns each
 constexpr int MATH_THREADS = 32 * MATH_WARPS;
-constexpr int NSTAGE = 2;               // Q / dO ring depth of dkdv_kernel
+constexpr int NSTAGE = 2;               // Q / dO ring depth of dkdv
 
 struct GradArgs {
   packed::Plan plan;
@@ -268,7 +276,7 @@ struct KWalk {
   }
 };
 
-// dkdv_kernel: warps 0 loader, 1 S / dP issuer and TMEM owner, 2 dV / dK issuer, 4 .. 11 math.
+// dkdv: warps 0 loader, 1 S / dP issuer and TMEM owner, 2 dV / dK issuer, 4 .. 11 math.
 // The first four give registers to the math warps, which hold 200 values in the sums.
 constexpr int K_THREADS = 128 + MATH_THREADS;
 constexpr int K_WG0_REGS = 88, K_MATH_REGS = 208;
@@ -473,8 +481,8 @@ MARS_DEV void dkdv(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUte
   #pragma unroll
                 for (int kq = 0; kq < GT / 32; ++kq) {
                   const int k = (GT / 32) * h + kq;
-                  mma_bf16_ts(tmem + dst, tmem + src + p_col(k), sdesc_advance(bd, k * 2048), id_acc,
-                              (p | k) != 0);
+                  mma_bf16_ts(tmem + dst, tmem + src + p_col(k), sdesc_advance(bd, k * 2048),
+                              id_acc, (p | k) != 0);
                 }
                 mma_commit(&done[h]);
               }
@@ -559,10 +567,10 @@ MARS_DEV void dkdv(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUte
 #pragma unroll
         for (int e = 0; e < HC; e += 4) {
           const float4 l4 = *reinterpret_cast<const float4*>(ls + e);
-          const float2 t01 = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
-                                        sc2, make_float2(-l4.x, -l4.y));
-          const float2 t23 = __ffma2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
-                                        sc2, make_float2(-l4.z, -l4.w));
+          const float2 s01 = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+          const float2 t01 = __ffma2_rn(s01, sc2, make_float2(-l4.x, -l4.y));
+          const float2 s23 = make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+          const float2 t23 = __ffma2_rn(s23, sc2, make_float2(-l4.z, -l4.w));
           pf[e] = flash::ex2_approx(t01.x);
           pf[e + 1] = flash::ex2_approx(t01.y);
           pf[e + 2] = flash::ex2_approx(t23.x);
@@ -842,7 +850,8 @@ MARS_DEV void dq(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtens
                mbar_wait(&qb.ds_full, jg & 1, ab, a.status);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t kd = sdesc_sw128(smem_u32(smem + S::OFF_K + st * S::KV_BYTES), GT * 128, 1024);
+          const uint64_t kd =
+              sdesc_sw128(smem_u32(smem + S::OFF_K + st * S::KV_BYTES), GT * 128, 1024);
 #pragma unroll
           for (int k = 0; k < GT / 16; ++k)
             mma_bf16_ts(tmem + TM_DQ, tmem + TM_DS + 8 * k, sdesc_advance(kd, k * 2048), id_q,
@@ -907,8 +916,8 @@ MARS_DEV void dq(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtens
         const float2 nl2 = make_float2(-lse, -lse), nd2 = make_float2(-dd, -dd);
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
-          const float2 t = __ffma2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])),
-                                      sc2, nl2);
+          const float2 s2 = make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+          const float2 t = __ffma2_rn(s2, sc2, nl2);
           pf[e] = flash::ex2_approx(t.x);
           pf[e + 1] = flash::ex2_approx(t.y);
         }
@@ -964,8 +973,8 @@ MARS_DEV void dq(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtens
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive_warp(&qb.acc_free);
-      const long long at =
-          rv ? ((long long)it.t.base + GT * it.t.tile + row) * a.dq_stride + it.h * D + HD * half : -1;
+      const long long tok = (long long)it.t.base + GT * it.t.tile + row;
+      const long long at = rv ? tok * a.dq_stride + it.h * D + HD * half : -1;
       packed::store_rows<HD>(a.dq, at, lane,
                              [&](int e) { return __uint_as_float(o[e]) * a.scale; });
       ++i;
@@ -996,13 +1005,17 @@ grad_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 
 // ------------------------------------------------------------------------------- host
 
-// CTAs of dkdv_kernel: one per SM, or as many as the most work that `total` rows can make (one
+// CTAs of dkdv: one per SM, or as many as the most work that `total` rows can make (one
 // sequence) feeds.
 int k_ctas(int batch, int total, int hq, int hkv) {
   const long long tiles = packed::max_tiles(batch, total, GT);
   const long long work = hq * (packed::kPairWork * (tiles * (tiles + 1) / 2) + tiles) +
                          hkv * packed::kTileWork * tiles;
   return (int)std::max(1LL, std::min<long long>(num_sms(), work / kMinWork));
+}
+
+long long prep_ctas(long long tiles, int hq) {
+  return 1 + tiles * (GT / PREP_ROWS) * ((hq + PREP_HEADS - 1) / PREP_HEADS);
 }
 
 struct GradSpace {
@@ -1055,8 +1068,7 @@ cudaError_t launch_grad(const PackedGrad& p, GradArgs& a, cudaStream_t stream) {
   const cudaError_t e = set_smem_limit_once(grad_kernel<D>, kSmem, attr);
   if (e != cudaSuccess) return e;
   const long long tiles = packed::max_tiles(p.batch, p.total, GT);
-  const long long preps = tiles * (GT / PREP_ROWS) * ((p.hq + PREP_HEADS - 1) / PREP_HEADS);
-  prep_kernel<D><<<(unsigned)(1 + preps), packed::kPlanThreads, 0, stream>>>(
+  prep_kernel<D><<<(unsigned)prep_ctas(tiles, p.hq), packed::kPlanThreads, 0, stream>>>(
       a, packed::PlanArgs{a.plan, p.cu, p.batch, p.total, a.G, a.k_ctas, p.status});
   grad_kernel<D><<<(unsigned)(a.k_ctas + a.q_ctas), K_THREADS, kSmem, stream>>>(tq, tdo, tk, tv, a);
   count_launches(2);
@@ -1064,6 +1076,11 @@ cudaError_t launch_grad(const PackedGrad& p, GradArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+long long packed_grad_items(int batch, int total, int hq) {
+  const long long tiles = packed::max_tiles(batch, total, GT);
+  return std::max(tiles * hq, prep_ctas(tiles, hq));
+}
 
 size_t packed_grad_workspace_bytes(int batch, int total, int hq, int hkv, int d) {
   return carve(nullptr, batch, total, hq, hkv, d).bytes;

@@ -131,7 +131,10 @@ def grad(L, q=P, k=P, v=P, o=P, d_o=P, lse=P, cu=P, dq=P, dk=P, dv=P, batch=2, t
     ({"strides": (512, 512, 512, 248, 512, 512)}, mars.EINVAL),
     ({"strides": (512, 512, 512, 512, 512, 132)}, mars.EALIGN), ({"hq": 3}, mars.EINVAL),
     ({"d": 32}, mars.EUNSUPPORTED), ({"total": -2}, mars.EINVAL), ({"ws_bytes": 64}, mars.ENOSPACE),
-    ({"scale": float("inf")}, mars.EINVAL), ({"total": 0}, mars.OK), ({"batch": 0}, mars.OK)], ids=str)
+    ({"scale": float("inf")}, mars.EINVAL), ({"total": 0}, mars.OK), ({"batch": 0}, mars.OK),
+    # more tiles times heads, or blocks of rows, than 32 bits count
+    ({"batch": 1 << 29, "ws_bytes": 1 << 62}, mars.EUNSUPPORTED),
+    ({"batch": 1 << 28, "hq": 2, "ws_bytes": 1 << 62}, mars.EUNSUPPORTED)], ids=str)
 def test_gradient_refusals(L, change, code):
     assert grad(L, **change) == code
 
