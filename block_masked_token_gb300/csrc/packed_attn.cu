@@ -287,23 +287,39 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
   if (tok < first || tok >= sq.base) return;
   const size_t rec = D + 4, step = (size_t)a.total * a.hq * rec;
   const float* base = a.part + ((size_t)tok * a.hq + h) * rec;
-  float m = -INFINITY;
-  for (int sp = 0; sp < a.nsplit; ++sp) m = fmaxf(m, base[sp * step]);
-  float l = 0.f;
+  // m and l of 32 splits at a time, a lane each
+  float m = -INFINITY, l = 0.f;
   float2 acc[D / 64];
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) acc[i] = make_float2(0.f, 0.f);
-  for (int sp = 0; sp < a.nsplit; ++sp) {
-    const float* pr = base + sp * step;
-    const float ms = pr[0];
-    if (ms == -INFINITY) continue;
-    const float w = exp2f(ms - m);
-    l += pr[1] * w;
+  for (int s0 = 0; s0 < a.nsplit; s0 += 32) {
+    const int n = min(32, a.nsplit - s0);
+    const float* first = base + s0 * step;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = *reinterpret_cast<const float2*>(first + lane * step);
+    float mx = fmaxf(m, ml.x);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const float2 v = *reinterpret_cast<const float2*>(pr + 4 + 2 * lane + 64 * i);
-      acc[i].x += v.x * w;
-      acc[i].y += v.y * w;
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float old = m > -INFINITY ? exp2f(m - mx) : 0.f;
+    const float w = ml.x > -INFINITY ? exp2f(ml.x - mx) : 0.f;
+    float sum = ml.y * w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    m = mx;
+    l = l * old + sum;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) acc[i] = make_float2(acc[i].x * old, acc[i].y * old);
+#pragma unroll 4
+    for (int sp = 0; sp < n; ++sp) {
+      const float ws = __shfl_sync(0xffffffffu, w, sp);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const float2 v =
+            *reinterpret_cast<const float2*>(first + sp * step + 4 + 2 * lane + 64 * i);
+        // an empty part wrote no O
+        acc[i].x += ws > 0.f ? v.x * ws : 0.f;
+        acc[i].y += ws > 0.f ? v.y * ws : 0.f;
+      }
     }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
