@@ -397,7 +397,8 @@ struct PairBar {
   uint32_t tmem_base;
   int abort;
   uint64_t stored[2], told[2];       // a partial has been written; `last` has been set
-  int last[2];                       // whether this CTA merges (per row tile)
+  int last[2][4];                    // whether this CTA merges: per row tile, two questions for
+                                     // each of at most two divided items
   uint64_t item_full[kItems], item_empty[kItems];
   PairItem items[kItems];
 };
@@ -935,7 +936,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     };
     const uint32_t s_addr = tmem + S::TM_S + x * BKV + lane_off;
     const uint32_t o_addr = tmem + S::TM_O + x * BKV + lane_off;
-    int g = 0, done = 0, parts = 0;                    // parts: of divided items
+    int g = 0, done = 0, parts = 0, tells = 0;
     bool ok = true;
     RowsPolicy<D> pol;
     pol.a = &a;
@@ -1052,63 +1053,84 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       const long long at =
           pol.trow < a.tpt && tok < it.n
               ? (((long long)it.base + tok) * a.hq + it.h0 + pol.hrow) * D : -1;
-      bool write = it.ja == 0 && it.jb == it.tiles;
-      if (!write) {
-        // a part of the item: its partial, and the merge by the last part to arrive
-        float4* rec = partial<D>(a, blockIdx.x, it.ja > 0, x);
-        reinterpret_cast<float2*>(rec + BQ * D / 4)[row] =
-            make_float2(steps ? m : -INFINITY, steps ? l : 0.f);
-#pragma unroll 1
-        for (int c = 0; c < (steps ? D / 32 : 0); ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + c * 32, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            rec[(c * 8 + e / 4) * BQ + row] =
-                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                            __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-        }
-        __threadfence();
-        mbar_arrive_warp(&bar.stored[x]);
-        if (quad == 0) {
-          if (!(ok = warp_wait(&bar.stored[x], parts & 1))) break;
-          if (lane == 0) {
-            bar.last[x] = atomicAdd(a.tickets + 2 * it.c1 + x, 1) == it.cuts;
+      const bool whole = it.ja == 0 && it.jb == it.tiles;
+      if (!steps) {
+        m = -INFINITY;
+        l = 0.f;
+      }
+      const int own = blockIdx.x - (it.c1 - 1);        // this part of a divided item
+      bool write = true;
+      if (!whole) {
+        // A divided item: its last part to finish merges. A part that finds all others finished
+        // does so without writing its own partial; the others write theirs and count it.
+        int32_t* ticket = a.tickets + 2 * it.c1 + x;
+        auto tell = [&](auto f) {                      // one thread's answer for all 128
+          if (quad == 0 && lane == 0) {
+            bar.last[x][tells] = f();
             mbar_arrive(&bar.told[x]);
           }
+          ok = warp_wait(&bar.told[x], tells & 1);
+          const bool last = ok && *reinterpret_cast<volatile int*>(&bar.last[x][tells]) != 0;
+          ++tells;
+          return last;
+        };
+        write = tell([&] { return *reinterpret_cast<volatile int32_t*>(ticket) == it.cuts; });
+        if (!ok) break;
+        if (!write) {
+          float4* rec = partial<D>(a, blockIdx.x, it.ja > 0, x);
+          reinterpret_cast<float2*>(rec + BQ * D / 4)[row] = make_float2(m, l);
+#pragma unroll 1
+          for (int c = 0; c < (steps ? D / 32 : 0); ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              rec[(c * 8 + e / 4) * BQ + row] =
+                  make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                              __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+          }
+          __threadfence();
+          mbar_arrive_warp(&bar.stored[x]);
+          if (quad == 0 && !(ok = warp_wait(&bar.stored[x], parts & 1))) break;
+          ++parts;
+          write = tell([&] { return atomicAdd(ticket, 1) == it.cuts; });
+          if (!ok) break;
         }
-        if (!(ok = warp_wait(&bar.told[x], parts & 1))) break;
-        ++parts;
-        write = *reinterpret_cast<volatile int*>(&bar.last[x]) != 0;
         if (write) __threadfence();
       }
       if (write) {
-        const bool merge = it.ja > 0 || it.jb < it.tiles;
         auto rec_of = [&](int k) { return partial<D>(a, it.c1 - 1 + k, k > 0, x); };
         auto ml_of = [&](int k) {
+          if (k == own) return make_float2(m, l);
           return __ldcg(reinterpret_cast<const float2*>(rec_of(k) + BQ * D / 4) + row);
         };
-        if (merge) {
-          m = -INFINITY;
-          l = 0.f;
-          for (int k = 0; k <= it.cuts; ++k) m = fmaxf(m, ml_of(k).x);
-          for (int k = 0; k <= it.cuts; ++k) {
+        // weights of the parts' O; those of the first two are kept, an item has rarely more
+        float mw = m, lw = l, w0 = 1.f, w1 = 0.f;
+        auto weight = [&](float mk) { return mk > -INFINITY ? exp2f(mk - mw) : 0.f; };
+        if (!whole) {
+          const float2 a0 = ml_of(0), a1 = ml_of(1);
+          mw = fmaxf(a0.x, a1.x);
+          for (int k = 2; k <= it.cuts; ++k) mw = fmaxf(mw, ml_of(k).x);
+          w0 = weight(a0.x);
+          w1 = weight(a1.x);
+          lw = a0.y * w0 + a1.y * w1;
+          for (int k = 2; k <= it.cuts; ++k) {
             const float2 r = ml_of(k);
-            if (r.x > -INFINITY) l += r.y * exp2f(r.x - m);
+            lw += r.y * weight(r.x);
           }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = lw > 0.f ? 1.f / lw : 0.f;
         if (a.lse && at >= 0)
           a.lse[(size_t)(it.h0 + pol.hrow) * a.total + it.base + tok] =
-              l > 0.f ? m + log2f(l) : -INFINITY;
+              lw > 0.f ? mw + log2f(lw) : -INFINITY;
         // 64 columns at a time, exchanged in groups of 8 lanes so that these write 128 bytes of a
         // row (a thread writing its own row took 5,000 cycles per item; staging in shared memory
         // would take a fifth of the ring, which costs 9 %)
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           float o[64];
-          if (!merge) {
+          if (whole) {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               tmem_ld32(o_addr + c * 64 + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(o + 32 * k));
@@ -1117,9 +1139,19 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
             for (int e = 0; e < 64; ++e) o[e] = 0.f;
             for (int k = 0; k <= it.cuts; ++k) {
-              const float mk = ml_of(k).x;
-              const float wt = mk > -INFINITY ? exp2f(mk - m) : 0.f;
-              if (!__any_sync(0xffffffffu, wt > 0.f)) continue;   // an empty part wrote no O
+              const float wt = k == 0 ? w0 : k == 1 ? w1 : weight(ml_of(k).x);
+              if (!__any_sync(0xffffffffu, wt > 0.f)) continue;   // an empty part has no O
+              if (k == own) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  uint32_t v[32];
+                  tmem_ld32(o_addr + c * 64 + 32 * q, v);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[32 * q + e] += __uint_as_float(v[e]) * wt;
+                }
+                continue;
+              }
               const float4* r = rec_of(k) + c * 16 * BQ + row;
 #pragma unroll
               for (int e = 0; e < 64; e += 4) {
