@@ -22,6 +22,7 @@
 // Where the rows are many, pair_kernel takes two row tiles per CTA instead (see there).
 
 #include <algorithm>
+#include <climits>
 
 #include "common.cuh"
 #include "flash_tc.cuh"
@@ -453,18 +454,129 @@ struct PairPart {
   long long total, ctas;             // all work, CTAs that share it (0: none for this CTA)
 };
 
-// Scan scratch of find_part.
+// An undivided item of a CTA: token tile and (KV head, group) tg = t * heads + g.
+struct ListItem {
+  int s, base, n, tg;
+};
+constexpr int kListItems = 32;       // of a CTA
+constexpr int kListMax = 1024;       // (sequence, token tile) entries
+
+// What find_part leaves: `count` undivided items, or (count < 0) a part of the line; and its
+// scan scratch.
 struct PartScan {
   long long sum[PAIR_THREADS / 32];
   int top[PAIR_THREADS / 32];
   long long work;
-  int tops, items;
+  int tops, items, count;
   Row at[2];
   PairPart part;
+  ListItem list[kListItems];
 };
 
-// Every thread of the CTA: fill sc.part.
-MARS_DEV void find_part(const AttnArgs& a, PartScan& sc) {
+// Whole items, in turn by falling cost, where that leaves the CTAs within a tenth of one
+// another; false otherwise, or with too many of them (their ends then matter less). Every CTA
+// ranks all (sequence, tile) entries for itself, alike, in `scratch`: 2,000 cycles for 400.
+// Against equal parts of the line, which are a tile or two off where small items meet, and whose
+// divided items take 5,000 cycles more on each side, twelve prompts of 150 to 2,048 rows took
+// MEASURED.
+struct ListScratch {
+  int off[PAIR_THREADS + 1], base[PAIR_THREADS], n[PAIR_THREADS], P[PAIR_THREADS];
+  alignas(16) int key[kListMax];
+  int entry[kListMax], sorted_key[kListMax], sorted_entry[kListMax];
+  long long most[PAIR_THREADS / 32], all[PAIR_THREADS / 32];
+};
+
+MARS_DEV bool list_items(const AttnArgs& a, PartScan& sc, const Row& q, ListScratch& w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int heads = a.hkv * a.ngrp, ctas = gridDim.x, total = sc.items, n = total / heads;
+  const int rounds = (total + ctas - 1) / ctas;
+  if (a.batch > PAIR_THREADS || n == 0 || n > kListMax || rounds > kListItems) return false;
+  // entries of the sequences, one after another
+  const int mine = tid < a.batch ? q.tiles_of(a) : 0;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  __syncthreads();
+  if (lane == 31) sc.top[warp] = incl;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) incl += sc.top[i];
+  w.off[tid] = incl - mine;
+  w.base[tid] = q.base;
+  w.n[tid] = q.n;
+  w.P[tid] = q.P;
+  if (tid == 0) w.off[PAIR_THREADS] = n;
+  __syncthreads();
+  const int padded = (n + 3) / 4 * 4;
+  for (int e = tid; e < padded; e += PAIR_THREADS) {
+    int lo = 0, hi = PAIR_THREADS;                 // off[lo] <= e < off[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (w.off[mid] <= e) lo = mid; else hi = mid;
+    }
+    const Row r{lo, w.base[lo], w.n[lo], w.P[lo], 0};
+    const int t = e - w.off[lo];
+    // key tiles, and the entry's number so that no two are equal
+    const int tiles = min(key_tiles(a, r, t), INT_MAX / kListMax - 1);
+    w.key[e] = e < n ? tiles * kListMax + kListMax - 1 - e : -1;
+    if (e < n) w.entry[e] = lo << 16 | t;
+  }
+  __syncthreads();
+  for (int e = tid; e < n; e += PAIR_THREADS) {
+    const int k = w.key[e];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < padded; j += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(w.key + j);
+      rank += (v.x > k) + (v.y > k) + (v.z > k) + (v.w > k);
+    }
+    w.sorted_key[rank] = k / kListMax;
+    w.sorted_entry[rank] = w.entry[e];
+  }
+  __syncthreads();
+  // item of CTA c in round r; rounds run forwards and backwards
+  auto item = [&](int c, int r) { return r * ctas + ((r & 1) ? ctas - 1 - c : c); };
+  long long most = 0, all = 0;
+  for (int c = tid; c < ctas; c += PAIR_THREADS) {
+    long long sum = 0;
+    for (int r = 0; r < rounds; ++r) {
+      const int i = item(c, r);
+      if (i < total) sum += kItemWork - 64 + 128LL * w.sorted_key[i / heads];
+    }
+    most = max(most, sum);
+    all += sum;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 0) {
+    w.most[warp] = most;
+    w.all[warp] = all;
+  }
+  __syncthreads();
+  for (int i = 0; i < PAIR_THREADS / 32; ++i) {
+    most = max(most, w.most[i]);
+    all = i == 0 ? w.all[0] : all + w.all[i];
+  }
+  if (most * ctas * 10 > all * 11) return false;
+  if (tid < rounds) {
+    const int i = item(blockIdx.x, tid);
+    if (i < total) {
+      const int e = w.sorted_entry[i / heads], s = e >> 16;
+      sc.list[tid] = ListItem{s, w.base[s], w.n[s], (e & 0xffff) * heads + i % heads};
+    }
+    if (tid == rounds - 1) sc.count = rounds - (i >= total);
+  }
+  __syncthreads();
+  return true;
+}
+
+// Every thread of the CTA: fill sc.list or sc.part.
+MARS_DEV void find_part(const AttnArgs& a, PartScan& sc, ListScratch& scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long heads = a.hkv * a.ngrp;
   int bad = 0;
@@ -521,17 +633,19 @@ MARS_DEV void find_part(const AttnArgs& a, PartScan& sc) {
       if (c0 != sc.tops) bad |= MARS_ST_BADSEQ;
       sc.work = 0;
       sc.items = 0;
+      sc.count = -1;
     }
     __syncthreads();
   };
   begin();
   for (int s0 = 0; s0 < a.batch; s0 += PAIR_THREADS) chunk(s0);
+  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
+  if (list_items(a, sc, q, scratch)) return;
   const long long total = sc.work;
   // CTAs that share the work: as many as there are, unless that leaves less than a part each
   // and there are fewer items
   const long long ctas = min((long long)gridDim.x,
                              max((long long)sc.items, total / (160 * kMinPart)));
-  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
   if ((long long)blockIdx.x >= ctas) {
     if (tid == 0) sc.part.ctas = 0;
     __syncthreads();
@@ -595,14 +709,19 @@ MARS_DEV void find_part(const AttnArgs& a, PartScan& sc) {
 // visits. The loader walks and hands the items to the other warps.
 struct PairWalk {
   const AttnArgs& a;
+  const PartScan& sc;
   const PairPart& p;
   Row q;
-  int g, t, tok0, kvh, h0, np, tiles, ja, jb;
+  int i, g, t, tok0, kvh, h0, np, tiles, ja, jb;
   long long s0, work;
   bool more;
 
-  MARS_DEV PairWalk(const AttnArgs& a_, const PairPart& p_)
-      : a(a_), p(p_), q(p_.q), g(p_.g), t(p_.t) {
+  MARS_DEV PairWalk(const AttnArgs& a_, const PartScan& sc_)
+      : a(a_), sc(sc_), p(sc_.part), q(p.q), i(0), g(p.g), t(p.t) {
+    if (sc.count >= 0) {
+      listed();
+      return;
+    }
     item();
     ja = p.j;
     if (ja == tiles) next(); else end();
@@ -622,7 +741,22 @@ struct PairWalk {
     jb = s0 == p.end_s0 ? p.end_j : tiles;
     more = s0 < p.end_s0 || (s0 == p.end_s0 && p.end_j > ja);
   }
+  MARS_DEV void listed() {
+    more = i < sc.count;
+    if (!more) return;
+    const ListItem l = sc.list[i];
+    q = Row{l.s, l.base, l.n, cached_keys(a, l.s), 0};
+    t = l.tg / (a.hkv * a.ngrp);
+    g = l.tg % (a.hkv * a.ngrp);
+    item();
+    jb = tiles;
+  }
   MARS_DEV void next() {
+    if (sc.count >= 0) {
+      ++i;
+      listed();
+      return;
+    }
     if (++t == q.tiles_of(a)) {
       t = 0;
       if (++g == a.hkv * a.ngrp) {
@@ -734,8 +868,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     fence_barrier_init();
   }
-  find_part(a, scan);
-  if (scan.part.ctas == 0) return;
+  static_assert(sizeof(ListScratch) <= S::TOTAL - 1024, "the scratch fits the tiles' place");
+  find_part(a, scan, *reinterpret_cast<ListScratch*>(smem));
+  if (scan.count == 0 || (scan.count < 0 && scan.part.ctas == 0)) return;
+  fence_proxy_async_smem();                            // before copies into the scratch's place
   if (warp == 1) {
     tmem_alloc(&bar.tmem_base, 512);
     tmem_relinquish();
@@ -764,7 +900,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         ++ni;
         return __shfl_sync(0xffffffffu, good, 0) != 0;
       };
-      for (PairWalk it(a, scan.part); it.more && ok; it.next()) {
+      for (PairWalk it(a, scan); it.more && ok; it.next()) {
         if (!(ok = publish(it.describe()))) break;
         const int32_t* bt = a.block_table ? a.block_table + (size_t)it.q.s * a.max_pages : nullptr;
         // this lane's page of prefix tile j, read one tile ahead
@@ -1211,7 +1347,7 @@ cudaError_t launch_rows(const PackedAttn& p, const PackedPlan& plan, AttnArgs& a
   }
   if (plan.pair) {
     using SP = PairSmem<D>;
-    static_assert(SP::TOTAL + sizeof(PairBar) <= 227 * 1024, "pair layout fits shared memory");
+    static_assert(SP::TOTAL + sizeof(PairBar) + sizeof(PartScan) <= 227 * 1024, "pair layout fits shared memory");
     static std::atomic<int> attr_pair[64];
     cudaError_t e = set_smem_limit_once(pair_kernel<D>, SP::TOTAL, attr_pair);
     if (e != cudaSuccess) return e;
