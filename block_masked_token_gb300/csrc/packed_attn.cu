@@ -357,14 +357,14 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
 // The start and output of an item take about 7,000 cycles, which bounds short sequences.
 // A row tile's first P of an item also says that its warps have read the O of the item before.
 //
-// Work is divided evenly, whatever the lengths: the items of all sequences are laid out on a
-// line, each as long as its work (its key tiles and a constant), and CTA c of E takes the part
-// from c/E to (c+1)/E of it. A cut inside an item with many key tiles splits its key list
-// there (Cut::j); the CTAs then write partials (m, l, O) and the last of them to finish, known
-// by a ticket, merges them in the order of the keys, so that results do not depend on which
-// one it was. Nothing waits for another CTA. Each CTA finds its part from the boundaries by
-// itself (find_part), for about a microsecond; a separate kernel that listed the items by
-// falling cost took 9, and left 228 long items on 152 SMs at 75 % of the rate.
+// CTAs take whole items by falling cost (list_items) or, where that would not come out even,
+// equal parts of the work: the items of all sequences are laid out on a line, each as long as its
+// work (its key tiles and a constant), and CTA c of E takes the part from c/E to (c+1)/E of it. A
+// cut inside an item with many key tiles splits its key list there (cut_at); the CTAs then write
+// partials (m, l, O) and the last of them to finish, known by a ticket, merges them in the order
+// of the keys, so that results do not depend on which one it was. Nothing waits for another CTA.
+// Each CTA finds its items from the boundaries by itself (find_part), for 3 to 7 us of the
+// launch; a separate kernel that listed them took 9.
 constexpr int kKSlots = 2, kVSlots = 3;          // ring depths, in tiles
 constexpr int kStep = 64;                        // keys per step
 constexpr int PAIR_THREADS = 384;
@@ -473,12 +473,12 @@ struct PartScan {
   ListItem list[kListItems];
 };
 
-// Whole items, in turn by falling cost, where that leaves the CTAs within a tenth of one
-// another; false otherwise, or with too many of them (their ends then matter less). Every CTA
-// ranks all (sequence, tile) entries for itself, alike, in `scratch`: 2,000 cycles for 400.
-// Against equal parts of the line, which are a tile or two off where small items meet, and whose
-// divided items take 5,000 cycles more on each side, twelve prompts of 150 to 2,048 rows took
-// MEASURED.
+// Whole items, in turn by falling cost, where no CTA then has 15 % more than the average; false
+// otherwise, or with so many items that their ends hardly matter. Every CTA ranks all (sequence,
+// tile) entries for itself, alike, in `scratch`. Equal parts of the line are off by a few tiles
+// where they meet between items, and a divided item takes 5,000 cycles more on either side: twelve
+// prompts of 150 to 2,048 rows took 145 us so and take 137, chunks of 1 to 700 tokens over a cache
+// 109 and 100.
 struct ListScratch {
   int off[PAIR_THREADS + 1], base[PAIR_THREADS], n[PAIR_THREADS], P[PAIR_THREADS];
   alignas(16) int key[kListMax];
@@ -562,7 +562,7 @@ MARS_DEV bool list_items(const AttnArgs& a, PartScan& sc, const Row& q, ListScra
     most = max(most, w.most[i]);
     all = i == 0 ? w.all[0] : all + w.all[i];
   }
-  if (most * ctas * 10 > all * 11) return false;
+  if (most * ctas * 20 > all * 23) return false;
   if (tid < rounds) {
     const int i = item(blockIdx.x, tid);
     if (i < total) {
@@ -1347,7 +1347,8 @@ cudaError_t launch_rows(const PackedAttn& p, const PackedPlan& plan, AttnArgs& a
   }
   if (plan.pair) {
     using SP = PairSmem<D>;
-    static_assert(SP::TOTAL + sizeof(PairBar) + sizeof(PartScan) <= 227 * 1024, "pair layout fits shared memory");
+    static_assert(SP::TOTAL + sizeof(PairBar) + sizeof(PartScan) <= 227 * 1024,
+                  "pair layout fits shared memory");
     static std::atomic<int> attr_pair[64];
     cudaError_t e = set_smem_limit_once(pair_kernel<D>, SP::TOTAL, attr_pair);
     if (e != cudaSuccess) return e;

@@ -53,7 +53,9 @@ def test_packed_group_sizes(heads):
 # Many rows: two row tiles per item, several items per SM and items divided among SMs.
 MANY = [([301, 40, 0, 517, 18, 19, 203, 37, 90, 200], (28, 4, 128)),
         ([600, 1, 35, 36, 37, 0, 513, 300, 128, 127, 129, 400, 250, 77, 150], (14, 2, 64)),
-        ([1400], (28, 4, 128)), ([18] * 90, (28, 4, 128)), ([2000, 700], (4, 4, 64))]
+        ([1400], (28, 4, 128)), ([18] * 90, (28, 4, 128)), ([2000, 700], (4, 4, 64)),
+        ([(331 * i) % 500 + 40 for i in range(22)], (28, 4, 128)),
+        ([(97 * i) % 300 for i in range(60)], (28, 4, 64))]
 
 
 @pytest.mark.parametrize("lens, heads", MANY, ids=str)
@@ -339,8 +341,9 @@ def test_chunk_matches_oracle(lens, old, heads):
     ([301, 40, 0, 217, 18, 1, 203, 37, 590], [300, 0, 77, 1000, 513, 129, 5, 700, 16], (28, 4, 128)),
     ([600, 1, 35, 36, 37, 0, 513, 300, 1, 127, 129, 400, 250, 77, 150],
      [0, 900, 64, 1, 2000, 9, 128, 130, 3000, 40, 0, 15, 16, 17, 250], (14, 2, 64)),
-    ([1, 700, 1, 1], [4000, 1500, 17, 900], (28, 4, 128)), ([1] * 64, list(range(0, 1600, 25)), (28, 4, 128))],
-    ids=["ragged128", "ragged64", "mixed", "tokens"])
+    ([1, 700, 1, 1], [4000, 1500, 17, 900], (28, 4, 128)), ([1] * 64, list(range(0, 1600, 25)), (28, 4, 128)),
+    ([(331 * i) % 300 + 20 for i in range(28)], [(217 * i) % 900 for i in range(28)], (28, 4, 128))],
+    ids=["ragged128", "ragged64", "mixed", "tokens", "whole"])
 def test_chunk_many_rows(lens, old, heads):
     x = make(lens, *heads, seed=32, old=old, tail=3)
     y = cuda(x)
