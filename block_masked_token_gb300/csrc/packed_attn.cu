@@ -15,7 +15,7 @@
 //
 // With few tiles and long key lists the list is cut into splits (plan_packed): each CTA writes
 // an unnormalised partial (m in log2 units, l, O) and a second kernel merges them. One token for
-// each of 32 sequences (28 heads over 4 of 128, 158,000 cached keys, 325 MB) takes 69 us, 0.69
+// each of 32 sequences (28 heads over 4 of 128, 158,000 cached keys, 325 MB) takes 69 us, 0.70
 // of the copy bandwidth; one SM takes in 16-token pages at 27 bytes per cycle, so a CTA that is
 // left alone with a long list bounds it.
 //
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
 // steps, one in flight per row tile, a pair of tiles took 4,000 cycles instead of 2,870.
 // What bounds those 2,870 is shared memory at 128 bytes per cycle: an S MMA of 64 keys reads 6 KB
 // for its 32 cycles of arithmetic, S 192 KB per pair, PV 64 KB, the copies write 64 KB: 2,500
-// cycles. One sequence of 8,000 rows (28 heads over 4) runs at 1.3 PFLOP/s, 0.67 of the GEMM rate.
+// cycles. One sequence of 8,191 rows (28 heads over 4) runs at 1.36 PFLOP/s, 0.69 of the GEMM rate.
 // The start and output of an item take about 7,000 cycles, which bounds short sequences.
 // A row tile's first P of an item also says that its warps have read the O of the item before.
 //
