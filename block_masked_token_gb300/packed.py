@@ -2,8 +2,14 @@
 prompts and its gradient, attention of new tokens over the paged cache, and the append of
 their K/V. Like mars.py, argument marshalling only; the rows of q, k and v may be slices of a
 wider tensor (a fused projection's output).
+
+A call for the current stream goes through csrc/packed_calls.c, which checks its arguments in C
+and declines what is not right (or not of the plainest kind: an integer scale, a workspace of
+2 GiB or more); the checks here then raise the error, or make the call.
 """
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
@@ -13,8 +19,26 @@ OP_ATTN_PACKED, OP_ATTN_CHUNK, OP_ATTN_PACKED_GRAD = 6, 7, 8
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
-# A step's smallest calls take a few microseconds on the GPU, so these checks are written for
-# few attribute reads per tensor, and pointers are passed as plain integers (0 for none).
+_calls = None
+
+
+def _ready(first):
+    """Load the C form of the calls, once there is a CUDA tensor to call it for."""
+    global _calls
+    if not (isinstance(first, torch.Tensor) and first.is_cuda):
+        return False
+    from . import _packed_calls
+    entry = lib()
+    _packed_calls.setup(torch.Tensor, _BF16, _I32, _F32, _U8, torch._C._cuda_getDevice,
+                        torch._C._cuda_getCurrentRawStream,
+                        *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                            entry.mars_attn_packed, entry.mars_attn_packed_grad,
+                            entry.mars_attn_chunk, entry.mars_kv_append)))
+    _calls = _packed_calls
+    return True
+
+
+# Pointers are passed as plain integers (0 for none).
 
 
 def _refuse(t, name, dtype, shape, dev):
@@ -94,6 +118,8 @@ def _batch(cu_seqlens, dev):
     shape = cu_seqlens.shape
     if len(shape) != 1 or shape[0] < 1:
         raise ValueError("cu_seqlens must hold batch + 1 boundaries")
+    if shape[0] > 0x7fffffff:
+        raise ValueError("cu_seqlens holds more boundaries than 31 bits count")
     return _ptr(cu_seqlens, "cu_seqlens", _I32, shape, dev), shape[0] - 1
 
 
@@ -124,6 +150,10 @@ def mars_attn_packed(q, k, v, cu_seqlens, o, workspace, lse=None, scale: float =
                      status=None, stream=None):
     """o[total, hq, d] (bf16) = causal attention inside each sequence of a packed batch; lse
     [hq, total] (float32, optional) its log2 row statistics (see include/mars.h)."""
+    if stream is None and (_calls is not None or _ready(q)):
+        rc = _calls.attn_packed(q, k, v, cu_seqlens, o, workspace, lse, scale, status)
+        if rc is not None:
+            return _rc(rc, "mars_attn_packed")
     dev, raw = _target(q, "q", stream)
     total, hq, d = q.shape
     hkv = k.shape[1]
@@ -143,6 +173,11 @@ def mars_attn_packed_grad(q, k, v, o, d_o, lse, cu_seqlens, dq, dk, dv, workspac
                           scale: float = 0.0, status=None, stream=None):
     """dq, dk, dv (bf16) of mars_attn_packed for the upstream gradient d_o, from its o and lse
     (see include/mars.h); dq, dk, dv may be slices of a wider tensor, like q, k, v."""
+    if stream is None and (_calls is not None or _ready(q)):
+        rc = _calls.attn_packed_grad(q, k, v, o, d_o, lse, cu_seqlens, dq, dk, dv, workspace,
+                                     scale, status)
+        if rc is not None:
+            return _rc(rc, "mars_attn_packed_grad")
     dev, raw = _target(q, "q", stream)
     total, hq, d = q.shape
     hkv = k.shape[1]
@@ -167,7 +202,14 @@ def mars_attn_chunk(q, k, v, cu_seqlens, k_pool, v_pool, block_table, seq_lens,
                     stream=None):
     """o[total, hq, d] (bf16) = attention of each sequence's new rows over its seq_lens[s]
     cached tokens and, causally, its own new keys (see include/mars.h)."""
+    if stream is None and (_calls is not None or _ready(q)):
+        rc = _calls.attn_chunk(q, k, v, cu_seqlens, k_pool, v_pool, block_table, seq_lens,
+                               max_len_hint, o, workspace, status, scale, PAGE_SIZE)
+        if rc is not None:
+            return _rc(rc, "mars_attn_chunk")
     dev, raw = _target(q, "q", stream)
+    if max_len_hint > 0x7fffffff:
+        raise ValueError("max_len_hint is beyond 31 bits")
     total, hq, d = q.shape
     hkv = k.shape[1]
     cu, batch = _batch(cu_seqlens, dev)
@@ -190,6 +232,11 @@ def mars_kv_append(k, v, cu_seqlens, seq_lens, block_table, k_pool, v_pool, new_
                    slots=None, status=None, stream=None):
     """Copy each sequence's new K/V rows to its pages, after its seq_lens[s] cached tokens;
     new_lens [batch] and slots [total] (int32) are optional outputs (see include/mars.h)."""
+    if stream is None and (_calls is not None or _ready(k)):
+        rc = _calls.kv_append(k, v, cu_seqlens, k_pool, v_pool, block_table, seq_lens, new_lens,
+                              slots, status, PAGE_SIZE)
+        if rc is not None:
+            return _rc(rc, "mars_kv_append")
     dev, raw = _target(k, "k", stream)
     total, hkv, d = k.shape
     cu, batch = _batch(cu_seqlens, dev)

@@ -528,3 +528,33 @@ def test_calls_in_a_graph_and_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert same(o, want) and same(op, want_p) and same(lse, want_lse)
+
+
+def test_bindings_refuse_what_the_calls_in_c_decline():
+    """The same errors whether the call goes through C first (current stream) or not."""
+    x = make([20, 3], 4, 2, 64, seed=40, old=[30, 5])
+    y = cuda(x)
+    n = y["n"]
+    o, ws = torch.zeros_like(y["do"]), torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    base = dict(q=y["q"], k=y["k"], v=y["v"], cu_seqlens=y["cu"], k_pool=y["k_pool"],
+                v_pool=y["v_pool"], block_table=y["table"], seq_lens=y["old"], max_len_hint=50, o=o,
+                workspace=ws)
+    packed.mars_attn_chunk(**base)
+    want = o.clone()
+    # an integer scale is declined in C and taken here
+    packed.mars_attn_chunk(**base, scale=0)
+    assert same(o, want)
+    bad = [("q", y["q"].float(), TypeError), ("k", y["k"][:-1], ValueError), ("v", None, TypeError),
+           ("o", o.cpu(), ValueError), ("o", o.transpose(0, 1), ValueError),
+           ("cu_seqlens", y["cu"].long(), TypeError), ("seq_lens", y["old"][:1], ValueError),
+           ("block_table", y["table"][0], ValueError), ("k_pool", y["k_pool"][:, :1], ValueError),
+           ("workspace", ws.float(), TypeError), ("max_len_hint", 1 << 31, ValueError),
+           ("max_len_hint", -1, mars.MarsError), ("workspace", ws[:0], mars.MarsError)]
+    side = torch.cuda.current_stream()
+    for name, value, error in bad:
+        hint = {"max_len_hint": 100000} if name == "workspace" else {}
+        for stream in (None, side):
+            with pytest.raises(error):
+                packed.mars_attn_chunk(**{**base, **hint, name: value}, stream=stream)
+    torch.cuda.synchronize()
+    assert same(o, want) and n == len(o)
