@@ -2,10 +2,10 @@
 // row i of sequence s goes to position seq_lens[s] + i, i.e. slot pos % 16 of page
 // block_table[s][pos / 16]. An unmapped page ends the append of its sequence.
 //
-// A pure copy: 4 hkv d bytes read and written per row; 43 MB in all take 12 us, of which the
-// chain of boundaries, length, page and row loads is about 3 and the launch 2 (with the rows
-// loaded before the pages are known, at the registers that takes, it is no faster). A CTA takes kRows rows of one
-// sequence. It first finds the sequence's first unmapped page at or before its rows (a scan
+// A pure copy: 4 hkv d bytes read and written per row. 43 MB in all take 12 us, of which the chain
+// of boundary, length, page and row loads is about 3 and the launch 2 (with the rows loaded before
+// the pages are known, at the registers that takes, it is no faster). A CTA takes kRows rows of
+// one sequence. It first finds the sequence's first unmapped page at or before its rows (a scan
 // of the block-table row, which stays in L2), then copies with 16-byte vectors.
 #include <climits>
 
