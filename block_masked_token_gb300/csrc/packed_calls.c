@@ -205,7 +205,7 @@ static PyObject* attn_chunk(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int total = -1, hq = -1, hkv = -1, d = -1, batch, qs, ks, vs, pages, width, bytes, one = 1;
   if (n != 14 || !PyLong_Check(a[8]) || !PyFloat_Check(a[12])) return decline();
   const long long hint = PyLong_AsLongLong(a[8]), page = PyLong_AsLongLong(a[13]);
-  if (hint < 0 || hint > INT_MAX || !target(a[0], &dev, &stream) ||
+  if (hint < 0 || hint > INT_MAX || page <= 0 || page > INT_MAX || !target(a[0], &dev, &stream) ||
       !rows(a[0], dev, &total, &hq, &d, &q, &qs) || !rows(a[1], dev, &total, &hkv, &d, &k, &ks) ||
       !rows(a[2], dev, &total, &hkv, &d, &v, &vs) || !boundaries(a[3], dev, &batch, &cu) ||
       !cache(a + 4, dev, batch, hkv, (int)page, d, &pages, &width, &kp, &vp, &table, &lens))
@@ -226,7 +226,8 @@ static PyObject* kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int total = -1, hkv = -1, d = -1, batch, ks, vs, pages, width, one = 1;
   if (n != 11) return decline();
   const long long page = PyLong_AsLongLong(a[10]);
-  if (!target(a[0], &dev, &stream) || !rows(a[0], dev, &total, &hkv, &d, &k, &ks) ||
+  if (page <= 0 || page > INT_MAX || !target(a[0], &dev, &stream) ||
+      !rows(a[0], dev, &total, &hkv, &d, &k, &ks) ||
       !rows(a[1], dev, &total, &hkv, &d, &v, &vs) || !boundaries(a[2], dev, &batch, &cu) ||
       !cache(a + 3, dev, batch, hkv, (int)page, d, &pages, &width, &kp, &vp, &table, &lens) ||
       !flat_or_none(a[7], d_i32, dev, 1, &batch, &new_lens) ||

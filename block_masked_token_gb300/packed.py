@@ -27,8 +27,12 @@ def _ready(first):
     global _calls
     if not (isinstance(first, torch.Tensor) and first.is_cuda):
         return False
-    from . import _packed_calls
     entry = lib()
+    try:
+        from . import _packed_calls
+    except ImportError as e:
+        raise RuntimeError("the C form of the packed calls is not built; run "
+                           "`python -m block_masked_token_gb300.build`") from e
     _packed_calls.setup(torch.Tensor, _BF16, _I32, _F32, _U8, torch._C._cuda_getDevice,
                         torch._C._cuda_getCurrentRawStream,
                         *(ctypes.cast(f, ctypes.c_void_p).value for f in (

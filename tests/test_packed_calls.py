@@ -127,6 +127,8 @@ def test_every_wrong_argument_is_declined(calls, name):
             assert call(*given[:i], None, *given[i + 1:]) is None, i
     assert not made
     assert call(*given[:-1]) is None and call() is None
+    if name in ("attn_chunk", "kv_append"):
+        assert all(call(*given[:-1], page) is None for page in (0, -1, 1 << 31, 32, "x"))
     assert not made
 
 
