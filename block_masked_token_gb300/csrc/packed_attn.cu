@@ -281,13 +281,19 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 31;
   const long long tok = gw / a.hq;
   const int h = (int)(gw - tok * a.hq);
+  if (tok >= a.total) return;
+  const size_t rec = D + 4, step = (size_t)a.total * a.hq * rec;
+  const float* base = a.part + ((size_t)tok * a.hq + h) * rec;
+  auto stats = [&](int sp) {
+    return sp < a.nsplit ? *reinterpret_cast<const float2*>(base + sp * step)
+                         : make_float2(-INFINITY, 0.f);
+  };
+  float2 ml = stats(lane);                           // on its way while the boundaries are read
   bool bad;
   // rows behind the last sequence have no partials and stay as they are
   const packed::Seq sq = packed::find_tile(a.cu, a.batch, a.total, 1, 0, INT_MAX, bad);
-  const int first = min(max(a.cu[0], 0), a.total);
-  if (tok < first || tok >= sq.base) return;
-  const size_t rec = D + 4, step = (size_t)a.total * a.hq * rec;
-  const float* base = a.part + ((size_t)tok * a.hq + h) * rec;
+  const int first_row = min(max(a.cu[0], 0), a.total);
+  if (tok < first_row || tok >= sq.base) return;
   // m and l of 32 splits at a time, a lane each
   float m = -INFINITY, l = 0.f;
   float2 acc[D / 64];
@@ -296,8 +302,7 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
   for (int s0 = 0; s0 < a.nsplit; s0 += 32) {
     const int n = min(32, a.nsplit - s0);
     const float* first = base + s0 * step;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < n) ml = *reinterpret_cast<const float2*>(first + lane * step);
+    if (s0) ml = stats(s0 + lane);
     float mx = fmaxf(m, ml.x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
