@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   __shared__ int s_slot[kRows];
   bool bad;
   const packed::Seq sq =
-      packed::find_tile(a.cu, a.batch, a.total, kRows, 1, (long long)blockIdx.x, bad);
+      packed::find_tile(a.cu, a.batch, a.total, kRows, 1, (long long)blockIdx.x, bad, a.seq_lens);
   if (threadIdx.x == 0) {
     s_bad = INT_MAX;
     if (bad && a.status) atomicOr(a.status, MARS_ST_BADSEQ);
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   if (sq.s < 0) return;
   __syncthreads();
   const int r0 = sq.tile * kRows, nr = min(kRows, sq.n - r0);
-  const long long P = a.seq_lens[sq.s];
+  const long long P = sq.len;
   const int32_t* bt = a.block_table + (size_t)sq.s * a.max_pages;
   // pages of positions P .. P + r0 + nr - 1
   const long long first = P / kPageSize;

@@ -16,6 +16,7 @@ struct Seq {
   int s;          // sequence, or -1: no such tile
   int tile;       // tile index inside the sequence
   int base, n;    // first row and number of rows of the sequence
+  int len;        // lens[s]
 };
 
 inline long long max_tiles(int batch, int total, int rows_per_tile) {
@@ -24,9 +25,10 @@ inline long long max_tiles(int batch, int total, int rows_per_tile) {
 
 // The sequence and tile of global tile index i (tiles of the sequences in order, each of
 // `rows` rows and at least `least` tiles per sequence). Whole warp; the result is uniform.
-// end = the last boundary, bad = whether cu was malformed (only where the scan got to).
+// bad = whether cu was malformed (only where the scan got to). lens [batch] or NULL is read with
+// the boundaries: after them it would be a further trip to memory before the tile can start.
 MARS_DEV Seq find_tile(const int32_t* __restrict__ cu, int batch, int total, int rows, int least,
-                       long long i, bool& bad) {
+                       long long i, bool& bad, const int32_t* lens = nullptr) {
   const int lane = threadIdx.x & 31;
   long long tiles = 0;                         // tiles of the sequences before this group
   const int c0 = cu[0];
@@ -35,6 +37,7 @@ MARS_DEV Seq find_tile(const int32_t* __restrict__ cu, int batch, int total, int
   for (int s0 = 0; s0 < batch; s0 += 32) {
     const int s = s0 + lane;
     const int c = s < batch ? cu[s + 1] : top;
+    const int len = lens && s < batch ? lens[s] : 0;
     int e = min(max(c, 0), total);
     int m = max(e, top);
 #pragma unroll
@@ -61,12 +64,13 @@ MARS_DEV Seq find_tile(const int32_t* __restrict__ cu, int batch, int total, int
       q.tile = (int)(i - tiles) - __shfl_sync(0xffffffffu, incl - mine, l);
       q.base = __shfl_sync(0xffffffffu, begin, l);
       q.n = __shfl_sync(0xffffffffu, n, l);
+      q.len = __shfl_sync(0xffffffffu, len, l);
       return q;
     }
     tiles += __shfl_sync(0xffffffffu, incl, 31);
     top = __shfl_sync(0xffffffffu, m, 31);
   }
-  return Seq{-1, 0, top, 0};
+  return Seq{-1, 0, top, 0, 0};
 }
 
 constexpr int kTileRows = 128;

@@ -15,7 +15,7 @@
 //
 // With few tiles and long key lists the list is cut into splits (plan_packed): each CTA writes
 // an unnormalised partial (m in log2 units, l, O) and a second kernel merges them. One token for
-// each of 32 sequences (28 heads over 4 of 128, 158,000 cached keys, 325 MB) takes 69 us, 0.70
+// each of 32 sequences (28 heads over 4 of 128, 158,000 cached keys, 325 MB) takes 67 us, 0.72
 // of the copy bandwidth; one SM takes in 16-token pages at 27 bytes per cycle, so a CTA that is
 // left alone with a long list bounds it.
 //
@@ -170,7 +170,8 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int kvh = id % a.hkv;
   id /= a.hkv;
   bool bad;
-  const packed::Seq sq = packed::find_tile(a.cu, a.batch, a.total, a.tpt, 0, id, bad);
+  const packed::Seq sq =
+      packed::find_tile(a.cu, a.batch, a.total, a.tpt, 0, id, bad, a.seq_lens);
   if (bad && threadIdx.x == 0 && a.status) atomicOr(a.status, MARS_ST_BADSEQ);
   if (sq.s < 0) return;
 
@@ -180,7 +181,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap tm_q,
   pol.n = sq.n;
   pol.tok0 = sq.tile * a.tpt;
   // cached keys; a length that the table cannot hold is cut to what it can
-  const int cached = a.seq_lens ? a.seq_lens[sq.s] : 0;
+  const int cached = sq.len;
   pol.P = (int)max(0LL, min((long long)cached, (long long)a.max_pages * kPageSize));
   if (pol.P != cached && threadIdx.x == 0 && a.status) atomicOr(a.status, MARS_ST_OVERFLOW);
   pol.np = (pol.P + BKV - 1) / BKV;
