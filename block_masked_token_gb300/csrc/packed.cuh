@@ -19,6 +19,13 @@ struct Seq {
   int len;        // lens[s]
 };
 
+// 128-key tiles of `keys` keys. Rounding up by adding 127 first would pass 31 bits for the last 127
+// counts that an int holds, which a max_len_hint ("no bound") or a length may have.
+__host__ __device__ constexpr int key_tiles(int keys) { return keys / 128 + (keys % 128 != 0); }
+static_assert(key_tiles(0x7fffffff) == 1 << 24 && key_tiles(0x7fffff80) == (1 << 24) - 1 &&
+                  key_tiles(1) == 1 && key_tiles(0) == 0,
+              "tiles of any int");
+
 inline long long max_tiles(int batch, int total, int rows_per_tile) {
   return (long long)total / rows_per_tile + batch;
 }

@@ -37,6 +37,7 @@ using flash::BKV;
 using flash::BQ;
 
 constexpr int kPagesPerTile = BKV / kPageSize;   // 8
+static_assert(BKV == 128, "packed::key_tiles");
 constexpr int kVStages = 3;                      // as in the decode kernel: no O staging area
 constexpr int kMinSplitTiles = 4;                // key tiles a split takes at least
 constexpr int kEvenSplitTiles = 16;              // where splits only even lengths out
@@ -184,7 +185,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int cached = sq.len;
   pol.P = (int)max(0LL, min((long long)cached, (long long)a.max_pages * kPageSize));
   if (pol.P != cached && threadIdx.x == 0 && a.status) atomicOr(a.status, MARS_ST_OVERFLOW);
-  pol.np = (pol.P + BKV - 1) / BKV;
+  pol.np = packed::key_tiles(pol.P);
   pol.bt_row = a.block_table ? a.block_table + (size_t)sq.s * a.max_pages : nullptr;
   pol.h0 = (kvh * a.ngrp + grp) * a.gp;
   pol.last_tok = min(pol.tok0 + a.tpt, sq.n) - 1;
@@ -421,7 +422,7 @@ struct Row {
   long long pre;                     // work before the sequence
 
   MARS_DEV int tiles_of(const AttnArgs& a) const { return (n + a.rows - 1) / a.rows; }
-  MARS_DEV int prefix() const { return (P + BKV - 1) / BKV; }
+  MARS_DEV int prefix() const { return packed::key_tiles(P); }
   // work of one head's first t items
   MARS_DEV long long upto(const AttnArgs& a, long long t) const {
     return t * (128LL * prefix() + kItemWork) + a.rows * (t * (t + 1) / 2);
@@ -1389,7 +1390,7 @@ PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len
   p.gp = G <= BQ ? G : 1;
   p.tpt = BQ / p.gp;
   const long long items = packed::max_tiles(batch, total, p.tpt) * hkv * (G / p.gp);
-  const int tiles = (max_len + BKV - 1) / BKV + 1;
+  const int tiles = packed::key_tiles(max_len) + 1;
   // Two row tiles per item where sequences have more rows than one on average and the items
   // fill the GPU.
   const long long pairs = packed::max_tiles(batch, total, 2 * p.tpt) * hkv * (G / p.gp);

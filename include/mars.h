@@ -416,7 +416,8 @@ int mars_attn_packed_grad(const mars_bf16* q, const mars_bf16* k, const mars_bf1
  * or after (with seq_lens unchanged).
  *   k_pool, v_pool, block_table, seq_lens, page_size   as mars_decode_attn
  *   max_len_hint  host upper bound of P_s + the chunk's rows; it sizes the splits of long key
- *                 lists. Longer ones are still computed correctly, only slower.
+ *                 lists. Longer ones are still computed correctly, only slower; any value up
+ *                 to INT_MAX is taken.
  *   o   [total, hq, d] bf16 (written)
  *   workspace >= mars_packed_workspace_bytes(MARS_OP_ATTN_CHUNK, ...) bytes (NULL if 0)
  * A needed page that is unmapped is skipped and flags MARS_ST_NOPAGE; a length below 0 or

@@ -558,3 +558,20 @@ def test_bindings_refuse_what_the_calls_in_c_decline():
                 packed.mars_attn_chunk(**{**base, **hint, name: value}, stream=stream)
     torch.cuda.synchronize()
     assert same(o, want) and n == len(o)
+
+
+# ------------------------------------------------------------------- ends of the ranges
+
+# few rows (packed_rows_kernel), and many (pair_kernel)
+HINTED = [([3, 1], [2000, 1300], (14, 2, 64)),
+          ([301, 40, 0, 217, 18, 1, 203, 37, 590], [300, 0, 77, 1000, 513, 129, 5, 2700, 16], (28, 4, 128))]
+
+
+@pytest.mark.parametrize("hint", [0, 1, (1 << 31) - 127, (1 << 31) - 1])
+@pytest.mark.parametrize("lens, old, heads", HINTED, ids=["few", "many"])
+def test_chunk_hints_of_nothing_and_without_bound(lens, old, heads, hint):
+    """Too small a hint leaves lists whole, the largest sizes the splits for lists of 2^31 keys."""
+    x = make(lens, *heads, seed=41, old=old, tail=2)
+    o, st = run_chunk(cuda(x), hint=hint)
+    assert st == 0
+    check_chunk(x, o)

@@ -226,3 +226,12 @@ def test_row_layouts_that_are_refused(monkeypatch, t, match):
         packed._rows(Host(bf(4, 2, 64)), "q", (4, 2, 64), 1)
     assert packed._rows(Host(bf(4, 6, 64)[:, 1:3]), "q", (4, 2, 64), 0)[1] == 384
     assert packed._rows(Host(bf(1, 2, 64)), "q", (1, 2, 64), 0)[1] == 128
+
+
+@pytest.mark.parametrize("batch, total, hq, hkv, d", [(1, 1, 4, 2, 64), (32, 32, 28, 4, 128), (3, 4000, 28, 4, 128)])
+def test_workspace_of_the_largest_hints(L, batch, total, hq, hkv, d):
+    """The splits of the longest lists that a hint can name: their number, and with it the
+    workspace, no longer changes there."""
+    sizes = {packed.mars_packed_workspace_bytes(packed.OP_ATTN_CHUNK, batch, total, hq, hkv, d, h)
+             for h in (1 << 30, (1 << 31) - 129, (1 << 31) - 128, (1 << 31) - 127, (1 << 31) - 1)}
+    assert len(sizes) == 1 and sizes.pop() > 0
