@@ -109,10 +109,11 @@ MARS_DEV void make_plan(const PlanArgs& a) {
   each(false, [&](int, int, int, int tiles, long long) {
     for (int t = lane; t < tiles; t += 32) atomicAdd(&s_hist[bucket(t)], 1);
   });
-  int2* h = reinterpret_cast<int2*>(s_hist) + tid;     // first place of each class
-  const int2 v = *h;
-  const int before = scan<false>(v.x + v.y, s_warp) - v.x - v.y;
-  *h = make_int2(before, before + v.x);
+  int* h = s_hist + 2 * tid;                           // first place of each class
+  const int v0 = h[0], v1 = h[1];
+  const int before = scan<false>(v0 + v1, s_warp) - v0 - v1;
+  h[0] = before;
+  h[1] = before + v0;
   __syncthreads();
   each(false, [&](int base, int n, int off, int tiles, long long pre) {
     for (int t = lane; t < tiles; t += 32) {
