@@ -368,8 +368,9 @@ int check_packed(int batch, int total, int hq, int hkv, int d) {
   if (batch < 0 || total < 0) return MARS_EINVAL;
   int rc = check_heads(hq, hkv, d);
   if (rc) return rc;
-  // sequence boundaries, tiles and statistics rows are counted in 32 bits
-  if ((long long)total + batch > 0x7fffffffLL - 256 || (long long)hq * d > 0x3fffffffLL)
+  // sequence boundaries, tiles and statistics rows are counted in 32 bits, and so are the 16-byte
+  // vectors of an append's 16 rows, with the 1,024 that its threads step by
+  if ((long long)total + batch > 0x7fffffffLL - 256 || (long long)hq * d > 1LL << 29)
     return MARS_EINVAL;
   return MARS_OK;
 }

@@ -363,7 +363,8 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
  *     ones and flagged MARS_ST_BADSEQ.
  *   - q [total, hq, d], k and v [total, hkv, d] bf16 may be slices of a wider tensor (a fused
  *     projection's output): q_stride, k_stride, v_stride are their row pitches in elements,
- *     multiples of 8 and at least heads * d; the heads of a row are contiguous.
+ *     multiples of 8 and at least heads * d; the heads of a row are contiguous, and
+ *     heads * d is at most 2^29.
  *   - Outputs o, dq, dk, dv are bf16 (what the next product reads); statistics are float.
  *     Scores, softmax statistics and sums are held in 32 bits; the weights are rounded to
  *     bf16 for the product with V.

@@ -235,3 +235,13 @@ def test_workspace_of_the_largest_hints(L, batch, total, hq, hkv, d):
     sizes = {packed.mars_packed_workspace_bytes(packed.OP_ATTN_CHUNK, batch, total, hq, hkv, d, h)
              for h in (1 << 30, (1 << 31) - 129, (1 << 31) - 128, (1 << 31) - 127, (1 << 31) - 1)}
     assert len(sizes) == 1 and sizes.pop() > 0
+
+
+def test_rows_wider_than_the_kernels_count_are_refused(L):
+    """The append counts the 16-byte vectors of 16 rows in 31 bits: rows of up to 2^29 elements."""
+    wide = (1 << 23) + 1
+    assert append(L, hkv=wide, pages=1, batch=0, strides=(64 * wide,) * 2) == mars.EINVAL
+    assert append(L, hkv=wide - 1, pages=1, batch=0, strides=(64 * wide,) * 2) == mars.OK
+    for call in (attn_packed, attn_chunk, grad):
+        assert call(L, hq=wide, hkv=1, batch=0) == mars.EINVAL
+        assert call(L, hq=wide - 1, hkv=1, batch=0) == mars.OK
