@@ -58,6 +58,15 @@ struct AttnArgs {
   int32_t* status;
 };
 
+// lse of a row, and the factor of its O. l is 0 where every score is -infinity (O is then 0), and
+// NaN where a score is NaN or +infinity: such a row is NaN in lse and, through the factor, in O,
+// whatever a merge of partials made of its O.
+MARS_DEV float statistic(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
+MARS_DEV float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+// l of a split without keys, which writes no O.
+constexpr float kNoKeys = -1.f;
+
 template <int D>
 struct RowsPolicy {
   static constexpr bool kHandOff = false;
@@ -125,7 +134,7 @@ struct RowsPolicy {
     const int h = h0 + row % a->gp;
     if (a->nsplit == 1) {
       if (col == 0 && a->lse)
-        a->lse[(size_t)h * a->total + tok] = l > 0.f ? m + log2f(l) : -INFINITY;
+        a->lse[(size_t)h * a->total + tok] = statistic(m, l);
       uint4* dst = reinterpret_cast<uint4*>(a->o + (tok * a->hq + h) * D + col);
 #pragma unroll
       for (int e = 0; e < 32; e += 8) {
@@ -200,7 +209,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap tm_q,
         float* rec = a.part + (((size_t)sp * a.total + sq.base + pol.token(r)) * a.hq + pol.h0 +
                                r % a.gp) * (D + 4);
         rec[0] = -INFINITY;
-        rec[1] = 0.f;
+        rec[1] = kNoKeys;
       }
     return;
   }
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
   const float* base = a.part + ((size_t)tok * a.hq + h) * rec;
   auto stats = [&](int sp) {
     return sp < a.nsplit ? *reinterpret_cast<const float2*>(base + sp * step)
-                         : make_float2(-INFINITY, 0.f);
+                         : make_float2(-INFINITY, kNoKeys);
   };
   float2 ml = stats(lane);                           // on its way while the boundaries are read
   bool bad;
@@ -309,8 +318,9 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float old = m > -INFINITY ? exp2f(m - mx) : 0.f;
-    const float w = ml.x > -INFINITY ? exp2f(ml.x - mx) : 0.f;
-    float sum = ml.y * w;
+    // kNoKeys also marks the weight of a split that wrote no O; m = +infinity gives NaN
+    const float w = ml.y == kNoKeys ? kNoKeys : ml.x > -INFINITY ? exp2f(ml.x - mx) : 0.f;
+    float sum = w == kNoKeys ? 0.f : ml.y * w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     m = mx;
@@ -324,15 +334,13 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
       for (int i = 0; i < D / 64; ++i) {
         const float2 v =
             *reinterpret_cast<const float2*>(first + sp * step + 4 + 2 * lane + 64 * i);
-        // an empty part wrote no O
-        acc[i].x += ws > 0.f ? v.x * ws : 0.f;
-        acc[i].y += ws > 0.f ? v.y * ws : 0.f;
+        acc[i].x += ws == kNoKeys ? 0.f : v.x * ws;
+        acc[i].y += ws == kNoKeys ? 0.f : v.y * ws;
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  if (a.lse && lane == 0)
-    a.lse[(size_t)h * a.total + tok] = l > 0.f ? m + log2f(l) : -INFINITY;
+  const float inv = reciprocal(l);
+  if (a.lse && lane == 0) a.lse[(size_t)h * a.total + tok] = statistic(m, l);
   uint32_t* orow = reinterpret_cast<uint32_t*>(a.o + ((size_t)tok * a.hq + h) * D);
 #pragma unroll
   for (int i = 0; i < D / 64; ++i)
@@ -1263,10 +1271,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             lw += r.y * weight(r.x);
           }
         }
-        const float inv = lw > 0.f ? 1.f / lw : 0.f;
+        const float inv = reciprocal(lw);
         if (a.lse && at >= 0)
-          a.lse[(size_t)(it.h0 + pol.hrow) * a.total + it.base + tok] =
-              lw > 0.f ? mw + log2f(lw) : -INFINITY;
+          a.lse[(size_t)(it.h0 + pol.hrow) * a.total + it.base + tok] = statistic(mw, lw);
         // 64 columns at a time, exchanged in groups of 8 lanes so that these write 128 bytes of a
         // row (a thread writing its own row took 5,000 cycles per item; staging in shared memory
         // would take a fifth of the ring, which costs 9 %)
@@ -1283,7 +1290,6 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             for (int e = 0; e < 64; ++e) o[e] = 0.f;
             for (int k = 0; k <= it.cuts; ++k) {
               const float wt = k == 0 ? w0 : k == 1 ? w1 : weight(ml_of(k).x);
-              if (!__any_sync(0xffffffffu, wt > 0.f)) continue;   // an empty part has no O
               if (k == own) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {

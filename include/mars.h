@@ -372,7 +372,9 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
  *   - A key that a sequence may not read (another sequence's row, a row behind the last
  *     sequence, a free slot of a page, an unmapped page) has no effect whatever it holds,
  *     NaN included. A NaN or infinity in a sequence's own rows can reach the outputs of
- *     that sequence up to 127 rows before or after the rows that the formulas reach. */
+ *     that sequence up to 127 rows before or after the rows that the formulas reach. It never
+ *     vanishes: a row one of whose scores is NaN or +infinity is NaN in o and lse. A row all
+ *     of whose scores are -infinity has lse -infinity and weights of 0. */
 
 /* Workspace (device scratch, >= 256-byte aligned) of `op` (MARS_OP_ATTN_PACKED,
  * MARS_OP_ATTN_CHUNK, MARS_OP_ATTN_PACKED_GRAD) for `total` rows of `batch` sequences;

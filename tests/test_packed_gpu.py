@@ -575,3 +575,76 @@ def test_chunk_hints_of_nothing_and_without_bound(lens, old, heads, hint):
     o, st = run_chunk(cuda(x), hint=hint)
     assert st == 0
     check_chunk(x, o)
+
+
+# ------------------------------------------------- NaN, infinities, maxima that grow and fall
+#
+# The same on every form: lists that are whole, split (packed_rows_kernel) or divided among CTAs
+# (pair_kernel). `old` None: mars_attn_packed.
+FORMS = {"few-whole": ([200, 90], None, (4, 2, 64)), "few-split-packed": ([900], None, (4, 1, 64)),
+         "one-token-split": ([1, 1, 1], [128, 1, 2300], (14, 2, 64)),
+         "few-split": ([130, 2], [1000, 1700], (7, 1, 128)),
+         "many-divided": ([1400], None, (28, 4, 128)),
+         "many-whole": ([(331 * i) % 500 + 40 for i in range(22)], None, (28, 4, 128)),
+         "many-chunks-divided": HINTED[1],
+         "many-chunks-whole": ([(331 * i) % 300 + 20 for i in range(28)],
+                               [(217 * i) % 900 for i in range(28)], (28, 4, 128))}
+
+
+def run_form(x):
+    """(o, lse or None)"""
+    y = cuda(x)
+    if "old" in x:
+        o, st = run_chunk(y)
+        lse = None
+    else:
+        o, lse, st = run_packed(y)
+    assert st == 0
+    return o, lse
+
+
+def positive(x):
+    """The first coordinate of every query positive, so that an infinite key coordinate there gives
+    infinite scores."""
+    x["q"][..., 0] = x["q"][..., 0].abs() + 0.25
+
+
+def assert_only(rows, before, after):
+    """NaN in these rows, all others bit-equal to the run before."""
+    (o, lse), (o2, lse2) = before, after
+    hit = torch.zeros(len(o), dtype=torch.bool)
+    hit[rows] = True
+    assert o2.cpu()[hit].isnan().all() and same(o[~hit.to(o.device)], o2[~hit.to(o.device)])
+    if lse is not None:
+        assert lse2.cpu()[:, hit].isnan().all()
+        assert same(lse[:, ~hit.to(o.device)], lse2[:, ~hit.to(o.device)])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_a_query_of_nan_gives_nan(form):
+    lens, old, heads = FORMS[form]
+    x = make(lens, *heads, seed=43, old=old, tail=1)
+    before = run_form(x)
+    row = int(x["cu"][1]) - 1
+    x["q"][row] = float("nan")
+    assert_only([row], before, run_form(x))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("form", FORMS)
+def test_a_score_of_nan_or_infinity_gives_nan(form, value):
+    """One of the sequence's own keys: the rows from it on; a cached one: all of them."""
+    lens, old, heads = FORMS[form]
+    x = make(lens, *heads, seed=44, old=old, tail=1)
+    positive(x)
+    before = run_form(x)
+    s = max(range(len(lens)), key=lambda i: lens[i])
+    a, b = int(x["cu"][s]), int(x["cu"][s + 1])
+    key = (a + b) // 2
+    keep = x["k"][key, :, 0].clone()
+    x["k"][key, :, 0] = value
+    assert_only(list(range(key, b)), before, run_form(x))
+    if old is not None and old[s] > 70:
+        x["k"][key, :, 0] = keep
+        x["k_pool"][x["table"][s, 70 // PAGE], :, 70 % PAGE, 0] = value
+        assert_only(list(range(a, b)), before, run_form(x))
