@@ -577,6 +577,27 @@ def test_chunk_hints_of_nothing_and_without_bound(lens, old, heads, hint):
     check_chunk(x, o)
 
 
+def poison_page_zero(x):
+    """Page 0, which is loaded in the place of a page that may not be read, is unused and holds NaN."""
+    other = int(x["unused"][0])
+    if other:
+        x["table"][x["table"] == 0] = other
+    assert not (x["table"] == 0).any()
+    x["k_pool"][0] = x["v_pool"][0] = float("nan")
+
+
+@pytest.mark.parametrize("lens, old, heads", HINTED, ids=["few", "many"])
+def test_chunk_a_page_loaded_for_an_unmapped_one_has_no_effect(lens, old, heads):
+    x = make(lens, *heads, seed=42, old=old, tail=2)
+    poison_page_zero(x)
+    x["table"][0, 3] = -1
+    x["table"][0, 7] = x["k_pool"].shape[0]
+    x["table"][1 if old[1] else 3, 0] = 1 << 20
+    o, st = run_chunk(cuda(x))
+    assert st == mars.ST_NOPAGE
+    check_chunk(x, o)
+
+
 # ------------------------------------------------- NaN, infinities, maxima that grow and fall
 #
 # The same on every form: lists that are whole, split (packed_rows_kernel) or divided among CTAs
@@ -648,3 +669,61 @@ def test_a_score_of_nan_or_infinity_gives_nan(form, value):
         x["k"][key, :, 0] = keep
         x["k_pool"][x["table"][s, 70 // PAGE], :, 70 % PAGE, 0] = value
         assert_only(list(range(a, b)), before, run_form(x))
+
+
+def slope(x, profile, top=100.0):
+    """Scores that rise by `top` along the keys, fall by it, or rise and fall again (in natural
+    units, on top of the normal ones)."""
+    d = x["q"].shape[2]
+    x["q"][..., 0] = 4.0
+    unit = top * np.sqrt(d) / 4.0
+    for s, m in enumerate(x["lens"]):
+        p = int(x["old"][s]) if "old" in x else 0
+        at = np.arange(p + m) / max(p + m - 1, 1)
+        z = {"rising": at, "falling": 1.0 - at, "bump": 1.0 - np.abs(2.0 * at - 1.0)}[profile]
+        z = torch.tensor(unit * z).to(torch.bfloat16)
+        a = int(x["cu"][s])
+        x["k"][a:a + m, :, 0] = z[p:, None]
+        for t in range(p):
+            x["k_pool"][x["table"][s, t // PAGE], :, t % PAGE, 0] = z[t]
+
+
+@pytest.mark.parametrize("profile", ["rising", "falling", "bump"])
+@pytest.mark.parametrize("form", FORMS)
+def test_maxima_that_grow_and_fall_along_the_keys(form, profile):
+    """Rows whose maximum grows by far more than the 2^8 from which O is rescaled, and parts of a
+    list with very different maxima.
+
+    A score is a sum of d products in 32 bits, exact before the sum: with |z| its scaled absolute
+    sum, z is off by at most E = (d / 16 + 16) 2^-23 |z| (a step of 16 products each, up to 16
+    roundings inside a step, each of at most a unit in the last place). Weights then change by
+    factors within 1 +- E before and after they are normalised: a row of O by at most 2 E max|v|,
+    the log2 statistic by log2(e) E."""
+    lens, old, heads = FORMS[form]
+    x = make(lens, *heads, seed=45, old=old, tail=1)
+    slope(x, profile)
+    o, lse = run_form(x)
+    o, cu, (hq, hkv, d) = f64(o), x["cu"].tolist(), heads
+    step = (d / 16 + 16) * 2.0 ** -23
+    for s, (a, b) in enumerate(zip(cu, cu[1:])):
+        p = old[s] if old is not None else 0
+        at = [(int(x["table"][s, t // PAGE]), t % PAGE) for t in range(p)]
+        for h in range(hq if b > a else 0):
+            u = h // (hq // hkv)
+            K, V = f64(x["k"][a:b, u]), f64(x["v"][a:b, u])
+            if p:
+                pages, slots = (torch.tensor(c) for c in zip(*at))
+                K = np.concatenate([f64(x["k_pool"][pages, u, slots]), K])
+                V = np.concatenate([f64(x["v_pool"][pages, u, slots]), V])
+            q = f64(x["q"][a:b, h])
+            P = causal_weights(q, K)
+            E = step * (np.abs(q) @ np.abs(K).T).max() / np.sqrt(d)
+            ref = P @ V
+            assert_within_bound(o[a:b, h], ref, output_bound(P, V, ref) + 2 * E * np.abs(V).max(),
+                                f"seq {s} head {h}")
+            if lse is not None:
+                z = np.where(np.tri(b - a, dtype=bool), q @ K.T / np.sqrt(d), -np.inf)
+                m = z.max(axis=1)
+                want = (m + np.log(np.exp(z - m[:, None]).sum(axis=1))) / np.log(2.0)
+                err = np.abs(f64(lse[h, a:b]) - want).max()
+                assert err <= LSE_TOL + 1.4426950408889634 * E + 256 * 2.0 ** -24, (s, h)
