@@ -4,7 +4,7 @@
 // sequence), dP = dO V^T and D_t = sum_c dO_tc O_tc:
 //   dV = P^T dO,   dS = P (dP - D),   dQ = scale dS K,   dK = scale dS^T Q.
 // Row 0 of a sequence sees one key, whose weight is 1 whatever the score: its dS is 0, and is
-// set so instead of being left to the cancellation of dP and D.
+// set so instead of being left to the cancellation of dP and D, unless it is infinite or NaN.
 //
 // Two tcgen05 pipelines over 128-row tiles, neither storing a score block, each a persistent CTA
 // per SM, in one launch:
@@ -139,6 +139,9 @@ prep_kernel(GradArgs a, packed::PlanArgs plan) {
 // ---------------------------------------------------------------------------- shared
 
 MARS_DEV uint32_t bits(int lo, int hi) { return flash::bit_range(lo, hi); }
+
+// Two bf16, the low one set to 0 if it is finite.
+MARS_DEV uint32_t clear_low(uint32_t w) { return (~w & 0x7f80u) ? w & 0xffff0000u : w; }
 
 // Rows [first, 128) of a [128][D] operand tile (D / 64 swizzled regions) set to zero, by
 // `threads` threads of which this is number `id`; rows [lo, hi) of the tile are theirs.
@@ -610,7 +613,7 @@ MARS_DEV void dkdv(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUte
           pp[e / 2] = flash::pack_bf16x2(s01.x, s01.y);
           pp[e / 2 + 1] = flash::pack_bf16x2(s23.x, s23.y);
         }
-        if (q0 == 0 && half == 0) pp[0] &= 0xffff0000u;   // dS of row 0 is 0
+        if (q0 == 0 && half == 0) pp[0] = clear_low(pp[0]);   // dS of row 0 is 0
         tmem_st32(tmem + S::TM_DP + HC * half + lane_off, *reinterpret_cast<uint32_t(*)[32]>(pp));
         tmem_st_wait();
         tc_fence_before();
@@ -951,7 +954,7 @@ MARS_DEV void dq(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtens
                                                              __uint_as_float(sv[e + 1])), nd2));
           ds[e / 2] = flash::pack_bf16x2(x.x, x.y);
         }
-        if (it.t.tile == 0 && row == 0 && half == 0) ds[0] = 0;   // dS of row 0 is 0
+        if (it.t.tile == 0 && row == 0 && half == 0) ds[0] = clear_low(ds[0]);   // dS of row 0 is 0
         // dS has one buffer: the previous tile's dQ MMA must have read it
         if (jg > 0 && !(ok = warp_wait(&qb.dq_done, (jg - 1) & 1))) break;
         tc_fence_after();

@@ -727,3 +727,25 @@ def test_maxima_that_grow_and_fall_along_the_keys(form, profile):
                 want = (m + np.log(np.exp(z - m[:, None]).sum(axis=1))) / np.log(2.0)
                 err = np.abs(f64(lse[h, a:b]) - want).max()
                 assert err <= LSE_TOL + 1.4426950408889634 * E + 256 * 2.0 ** -24, (s, h)
+
+
+@pytest.mark.parametrize("which", ["q", "do"])
+@pytest.mark.parametrize("row", [0, 77, 299])
+@pytest.mark.parametrize("lens, heads", [([300, 40], (4, 2, 64)), ([300, 1200], (14, 2, 128))], ids=str)
+def test_gradient_of_a_nan_row_is_nan(lens, heads, row, which):
+    """dq of the row, dk and dv of the keys that it sees; dq of the others and the other sequence
+    stay as they were (dk and dv of the rows behind it may be NaN)."""
+    x = make(lens, *heads, seed=46, tail=2)
+    got = []
+    for bad in (False, True):
+        if bad:
+            x[which][row] = float("nan")
+        y = cuda(x)
+        o, lse, _ = run_packed(y)
+        got.append(run_grad(y, o, lse, y["do"]))
+        assert got[-1][3] == 0
+    (dq, dk, dv, _), (dq2, dk2, dv2, _) = got
+    assert dq2[row].isnan().all() and dk2[:row + 1].isnan().all() and dv2[:row + 1].isnan().all()
+    others = [i for i in range(x["n"]) if i != row]
+    assert same(dq[others], dq2[others])
+    assert same(dk[lens[0]:], dk2[lens[0]:]) and same(dv[lens[0]:], dv2[lens[0]:])
