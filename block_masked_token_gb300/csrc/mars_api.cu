@@ -531,7 +531,9 @@ int mars_kv_append(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seq
   if (page_size != mars::kPageSize) return MARS_EUNSUPPORTED;
   if (batch == 0) return MARS_OK;
   if (!cu_seqlens || !seq_lens) return MARS_EINVAL;
-  if (total > 0 && (!k || !v || !block_table || !k_pool || !v_pool)) return MARS_EINVAL;
+  if (total > 0 && (!k || !v || (max_pages_per_seq > 0 && !block_table) ||
+                    (num_pages > 0 && (!k_pool || !v_pool))))
+    return MARS_EINVAL;                            // an empty table or pool has no address
   if (new_lens == seq_lens) return MARS_EINVAL;
   if (total > 0) {
     rc = check_pitch(k_stride, hkv, d);

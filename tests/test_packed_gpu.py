@@ -749,3 +749,20 @@ def test_gradient_of_a_nan_row_is_nan(lens, heads, row, which):
     others = [i for i in range(x["n"]) if i != row]
     assert same(dq[others], dq2[others])
     assert same(dk[lens[0]:], dk2[lens[0]:]) and same(dv[lens[0]:], dv2[lens[0]:])
+
+
+@pytest.mark.parametrize("what", ["table", "pool", "both"])
+def test_append_to_an_empty_pool_or_table(what):
+    """Nothing can be written: the lengths stay, no row has a slot, and the status says why."""
+    x = make([20, 0, 3], 4, 2, 64, seed=47, old=[5, 7, 16])
+    y = cuda(x)
+    if what != "pool":
+        y["table"] = y["table"][:, :0].contiguous()
+    if what != "table":
+        y["k_pool"], y["v_pool"] = y["k_pool"][:0], y["v_pool"][:0]
+    before = y["k_pool"].clone(), y["v_pool"].clone()
+    for stream in (None, torch.cuda.current_stream()):
+        lens, slots, st = run_append(y, stream=stream)
+        assert st == (mars.ST_NOPAGE if what == "pool" else mars.ST_OVERFLOW)
+        assert lens.tolist() == [5, 7, 16] and (slots == -1).all()
+    assert same(before[0], y["k_pool"]) and same(before[1], y["v_pool"])
