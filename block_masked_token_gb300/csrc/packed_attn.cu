@@ -1198,17 +1198,15 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       }
       if (!ok) break;
       g += it.jb - it.ja;
-      if (steps && !(ok = warp_wait(&bar.pv_done[x][(done - 1) & 1], ((done - 1) >> 1) & 1))) break;
+      // there were steps: a part has four key tiles or more, and begins as many before the end of
+      // the item, which is at most one behind that of either row tile
+      if (!(ok = warp_wait(&bar.pv_done[x][(done - 1) & 1], ((done - 1) >> 1) & 1))) break;
       tc_fence_after();
       // where this thread's row goes, in elements (-1: no token)
       const long long at =
           pol.trow < a.tpt && tok < it.n
               ? (((long long)it.base + tok) * a.hq + it.h0 + pol.hrow) * D : -1;
       const bool whole = it.ja == 0 && it.jb == it.tiles;
-      if (!steps) {
-        m = -INFINITY;
-        l = 0.f;
-      }
       const int own = blockIdx.x - (it.c1 - 1);        // this part of a divided item
       bool write = true;
       if (!whole) {
@@ -1231,7 +1229,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           float4* rec = partial<D>(a, blockIdx.x, it.ja > 0, x);
           reinterpret_cast<float2*>(rec + BQ * D / 4)[row] = make_float2(m, l);
 #pragma unroll 1
-          for (int c = 0; c < (steps ? D / 32 : 0); ++c) {
+          for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(o_addr + c * 32, o);
             tmem_ld_wait();
