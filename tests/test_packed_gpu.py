@@ -766,3 +766,116 @@ def test_append_to_an_empty_pool_or_table(what):
         assert st == (mars.ST_NOPAGE if what == "pool" else mars.ST_OVERFLOW)
         assert lens.tolist() == [5, 7, 16] and (slots == -1).all()
     assert same(before[0], y["k_pool"]) and same(before[1], y["v_pool"])
+
+
+# ------------------------------------------------- groups, offsets, a replayed serving loop
+
+@pytest.mark.parametrize("lens, heads", [([300, 77, 1], (96, 1, 64)), ([377, 40], (130, 1, 64)),
+                                         ([500, 3, 130], (33, 1, 128)), ([700, 260, 5], (40, 40, 64)),
+                                         ([301, 90], (128, 1, 128))], ids=str)
+def test_packed_many_rows_of_other_groups(lens, heads):
+    """pair_kernel with row tiles of one token, of 128 and in between, and its gradient."""
+    x = make(lens, *heads, seed=48, tail=1)
+    y = cuda(x)
+    o, lse, st = run_packed(y)
+    assert st == 0
+    check_packed(x, o, lse)
+    dq, dk, dv, st = run_grad(y, o, lse, y["do"])
+    assert st == 0
+    check_grad(x, dq, dk, dv)
+    z = make(lens, *heads, seed=49, tail=1, old=[70 * i + 200 for i in range(len(lens))])
+    o, st = run_chunk(cuda(z))
+    assert st == 0
+    check_chunk(z, o)
+
+
+def part_of(x, names, rows, **more):
+    """The rows of a sequence on the CPU as a batch of their own."""
+    y = {c: x[c][rows].cpu() for c in names}
+    n = len(y["q"])
+    return {**y, "n": n, "cu": torch.tensor([0, n], dtype=torch.int32), **more}
+
+
+def test_rows_whose_offsets_pass_32_bits():
+    """q, o, d_o and dq of more than 2^31 elements; the first sequence and the last."""
+    hq, hkv, d, m, batch = 28, 4, 128, 650, 960
+    n = m * batch + 3
+    assert n * hq * d > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(50)
+    y = {c: torch.empty(n, h, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+         for c, h in (("q", hq), ("k", hkv), ("v", hkv), ("do", hq))}
+    y["cu"] = torch.arange(0, n - 2, m, dtype=torch.int32, device="cuda")
+    o, lse, st = run_packed(y)
+    assert st == 0 and (o[-3:] == 7.0).all()
+    dq, dk, dv, st = run_grad(y, o, lse, y["do"], wide=False)
+    assert st == 0 and (dq[-3:] == 7.0).all() and (dv[-3:] == 7.0).all()
+    for a in (0, n - 3 - m):
+        rows = slice(a, a + m)
+        x = part_of(y, ("q", "k", "v", "do"), rows)
+        check_packed(x, o[rows], lse[:, rows])
+        check_grad(x, dq[rows], dk[rows], dv[rows])
+
+
+def test_pools_whose_offsets_pass_32_bits():
+    """Pools of more than 2^31 elements: an append to their last pages and a chunk over them."""
+    lens, old, (hq, hkv, d) = [40, 3], [100, 33], (28, 4, 128)
+    x = make(lens, hq, hkv, d, seed=51, old=old)
+    pages = (1 << 31) // (hkv * PAGE * d) + 64
+    small, shift = x["k_pool"].shape[0], pages - x["k_pool"].shape[0]
+    y = cuda(x)
+    y["table"] = torch.where(y["table"] >= 0, y["table"] + shift, y["table"])
+    for c in ("k_pool", "v_pool"):
+        big = torch.empty(pages, hkv, PAGE, d, dtype=torch.bfloat16, device="cuda")
+        assert big.numel() > 1 << 31
+        big[shift:] = y[c]
+        y[c] = big
+    o, st = run_chunk(y)
+    assert st == 0
+    check_chunk(x, o)
+    new_lens, slots, st = run_append(y)
+    kp, vp, want_lens, want_slots = oracle.kv_append(
+        f64(x["k"]), f64(x["v"]), x["cu"].numpy(), x["old"].numpy(), x["table"].numpy(),
+        f64(x["k_pool"]), f64(x["v_pool"]), PAGE)
+    assert st == 0 and (new_lens.cpu().numpy() == want_lens).all()
+    assert (slots.cpu().numpy() == want_slots + shift * PAGE).all() and small + shift == pages
+    assert (f64(y["k_pool"][shift:]) == kp).all() and (f64(y["v_pool"][shift:]) == vp).all()
+
+
+def test_a_captured_step_over_growing_caches():
+    """A token per sequence and step, captured once: lengths live on the device and grow past the
+    hint; every replay gives what the calls give one by one."""
+    hq, hkv, d, steps, old = 14, 2, 64, 40, [250, 0, 15, 1030]
+    x = make([steps] * 4, hq, hkv, d, seed=52, old=old)
+    y = cuda(x)
+    cu = torch.arange(5, dtype=torch.int32, device="cuda")
+    ws = workspace(packed.OP_ATTN_CHUNK, 4, 4, hq, hkv, d, 1032)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, v = (torch.zeros(4, h, d, dtype=torch.bfloat16, device="cuda") for h in (hq, hkv, hkv))
+    o, cur, new = torch.zeros_like(q), y["old"].clone(), torch.zeros_like(y["old"])
+
+    def step(kp, vp):
+        packed.mars_attn_chunk(q, k, v, cu, kp, vp, y["table"], cur, 1032, o, ws, status=st)
+        packed.mars_kv_append(k, v, cu, cur, y["table"], kp, vp, new_lens=new, status=st)
+        cur.copy_(new)
+
+    def loop(f):
+        out = []
+        cur.copy_(y["old"])
+        for i in range(steps):
+            for t, c in ((q, "q"), (k, "k"), (v, "v")):
+                t.copy_(y[c][i::steps])
+            f()
+            out.append(o.clone())
+        torch.cuda.synchronize()
+        assert cur.tolist() == [p + steps for p in old] and int(st.item()) == 0
+        return torch.stack(out, 1).flatten(0, 1)          # rows of a sequence together
+
+    eager = y["k_pool"].clone(), y["v_pool"].clone()
+    want = loop(lambda: step(*eager))
+    pools = y["k_pool"].clone(), y["v_pool"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*pools)
+    got = loop(graph.replay)
+    assert same(got, want) and same(eager[0], pools[0]) and same(eager[1], pools[1])
+    check_chunk(x, want)                                   # the same rows as one chunk
