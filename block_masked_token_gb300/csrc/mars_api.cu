@@ -534,7 +534,10 @@ int mars_kv_append(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seq
   if (total > 0 && (!k || !v || (max_pages_per_seq > 0 && !block_table) ||
                     (num_pages > 0 && (!k_pool || !v_pool))))
     return MARS_EINVAL;                            // an empty table or pool has no address
-  if (new_lens == seq_lens) return MARS_EINVAL;
+  // every CTA of a sequence reads its length, the last one writes the new one
+  const uintptr_t at = reinterpret_cast<uintptr_t>(seq_lens), to = reinterpret_cast<uintptr_t>(new_lens);
+  if (new_lens && (to > at ? to - at : at - to) < sizeof(int32_t) * (size_t)batch)
+    return MARS_EINVAL;
   if (total > 0) {
     rc = check_pitch(k_stride, hkv, d);
     if (!rc) rc = check_pitch(v_stride, hkv, d);

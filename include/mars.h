@@ -368,7 +368,8 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
  *   - Outputs o, dq, dk, dv are bf16 (what the next product reads); statistics are float.
  *     Scores, softmax statistics and sums are held in 32 bits; the weights are rounded to
  *     bf16 for the product with V.
- *   - hq / hkv, d, scale and status as elsewhere; status may be NULL.
+ *   - hq / hkv, d, scale and status as elsewhere; status may be NULL. Outputs and workspaces
+ *     overlap no input.
  *   - A key that a sequence may not read (another sequence's row, a row behind the last
  *     sequence, a free slot of a page, an unmapped page) has no effect whatever it holds,
  *     NaN included. A NaN or infinity in a sequence's own rows can reach the outputs of
@@ -436,8 +437,8 @@ int mars_attn_chunk(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
 /* K/V of packed sequences into the paged cache: row i of sequence s goes to position
  * pos = seq_lens[s] + i, page = block_table[s][pos / page_size], slot = pos % page_size, as in
  * mars_kv_commit. seq_lens is read only (a model calls this once per layer):
- *   new_lens [batch] int32 or NULL (written): seq_lens[s] + the rows appended; it may not be
- *            seq_lens itself
+ *   new_lens [batch] int32 or NULL (written): seq_lens[s] + the rows appended; it may not
+ *            overlap seq_lens
  *   slots    [total] int32 or NULL (written for the rows of the sequences): page * page_size +
  *            slot, -1 for a row that was not appended
  * The first row whose page is unmapped (entry < 0 or >= num_pages, or past max_pages_per_seq)

@@ -245,3 +245,8 @@ def test_rows_wider_than_the_kernels_count_are_refused(L):
     for call in (attn_packed, attn_chunk, grad):
         assert call(L, hq=wide, hkv=1, batch=0) == mars.EINVAL
         assert call(L, hq=wide - 1, hkv=1, batch=0) == mars.OK
+
+
+@pytest.mark.parametrize("at", [4092, 4096, 4100])
+def test_append_refuses_new_lengths_over_the_old_ones(L, at):
+    assert append(L, new=ctypes.c_void_p(at)) == mars.EINVAL
