@@ -17,6 +17,7 @@ from .mars import MarsError, PAGE_SIZE, lib
 
 OP_ATTN_PACKED, OP_ATTN_CHUNK, OP_ATTN_PACKED_GRAD = 6, 7, 8
 
+_INT_MAX = 0x7fffffff
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 
 _calls = None
@@ -60,6 +61,12 @@ def _refuse(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _counts(name, shape):
+    """The library counts in 31 bits, and ctypes would pass on the low ones of more."""
+    if max(shape) > _INT_MAX:
+        raise ValueError(f"{name} has a size that 31 bits do not count")
+
+
 def _ptr(t, name, dtype, shape, dev):
     """Address of a contiguous tensor."""
     try:
@@ -82,9 +89,10 @@ def _rows(t, name, shape, dev):
         good = t.get_device() == dev and t.dtype is _BF16 and t.shape == shape
     except AttributeError:
         good = False
+    total, heads, d = shape
+    _counts(name, shape)
     if not good:
         _refuse(t, name, _BF16, shape, dev)
-    total, heads, d = shape
     pitch, head, one = t.stride()
     if total == 0 or heads == 0 or d == 0:
         return t.data_ptr(), heads * d
@@ -92,7 +100,7 @@ def _rows(t, name, shape, dev):
         raise ValueError(f"the heads of each row of {name} must be contiguous")
     if total == 1:
         return t.data_ptr(), heads * d
-    if pitch < heads * d or pitch % 8 or pitch > 0x7fffffff:
+    if pitch < heads * d or pitch % 8 or pitch > _INT_MAX:
         raise ValueError(f"{name} has row pitch {pitch}: it must be a multiple of 8, at least "
                          f"{heads * d} and below 2^31")
     return t.data_ptr(), pitch
@@ -122,8 +130,7 @@ def _batch(cu_seqlens, dev):
     shape = cu_seqlens.shape
     if len(shape) != 1 or shape[0] < 1:
         raise ValueError("cu_seqlens must hold batch + 1 boundaries")
-    if shape[0] > 0x7fffffff:
-        raise ValueError("cu_seqlens holds more boundaries than 31 bits count")
+    _counts("cu_seqlens", shape)
     return _ptr(cu_seqlens, "cu_seqlens", _I32, shape, dev), shape[0] - 1
 
 
@@ -131,6 +138,7 @@ def _table(block_table, batch, dev):
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_pages]")
     width = block_table.shape[1]
+    _counts("block_table", block_table.shape)
     return _ptr(block_table, "block_table", _I32, (batch, width), dev), width
 
 
@@ -147,7 +155,10 @@ def _rc(code, where):
 
 
 def mars_packed_workspace_bytes(op, batch, total, hq=1, hkv=1, d=64, max_len=0):
-    return int(lib().mars_packed_workspace_bytes(op, batch, total, hq, hkv, d, max_len))
+    sizes = (batch, total, hq, hkv, d, max_len)
+    if not all(-1 <= n <= _INT_MAX for n in sizes):
+        return 0
+    return int(lib().mars_packed_workspace_bytes(op, *sizes))
 
 
 def mars_attn_packed(q, k, v, cu_seqlens, o, workspace, lse=None, scale: float = 0.0,
@@ -212,7 +223,7 @@ def mars_attn_chunk(q, k, v, cu_seqlens, k_pool, v_pool, block_table, seq_lens,
         if rc is not None:
             return _rc(rc, "mars_attn_chunk")
     dev, raw = _target(q, "q", stream)
-    if max_len_hint > 0x7fffffff:
+    if max_len_hint > _INT_MAX:
         raise ValueError("max_len_hint is beyond 31 bits")
     total, hq, d = q.shape
     hkv = k.shape[1]

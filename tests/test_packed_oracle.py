@@ -250,3 +250,20 @@ def test_rows_wider_than_the_kernels_count_are_refused(L):
 @pytest.mark.parametrize("at", [4092, 4096, 4100])
 def test_append_refuses_new_lengths_over_the_old_ones(L, at):
     assert append(L, new=ctypes.c_void_p(at)) == mars.EINVAL
+
+
+def test_bindings_refuse_counts_beyond_31_bits(L):
+    """ctypes would pass on their low 32 bits."""
+    size, big = packed.mars_packed_workspace_bytes, 1 << 32
+    good = dict(batch=1, total=1, hq=28, hkv=4, d=128, max_len=8192)
+    assert size(packed.OP_ATTN_CHUNK, **good) > 0
+    for name in good:
+        assert size(packed.OP_ATTN_CHUNK, **{**good, name: good[name] + big}) == 0
+        assert size(packed.OP_ATTN_CHUNK, **{**good, name: good[name] - big}) == 0
+    meta = dict(device="meta")
+    with pytest.raises(ValueError, match="31 bits"):
+        packed._table(torch.empty(1, big + 5, dtype=torch.int32, **meta), 1, 0)
+    with pytest.raises(ValueError, match="31 bits"):
+        packed._rows(torch.empty(big + 5, 1, 64, dtype=torch.bfloat16, **meta), "k", (big + 5, 1, 64), 0)
+    with pytest.raises(ValueError, match="31 bits"):
+        packed._batch(torch.empty(big + 5, dtype=torch.int32, **meta), 0)
