@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(256) packed_merge_kernel(AttnArgs a) {
 // steps, one in flight per row tile, a pair of tiles took 4,000 cycles instead of 2,870.
 // What bounds those 2,870 is shared memory at 128 bytes per cycle: an S MMA of 64 keys reads 6 KB
 // for its 32 cycles of arithmetic, S 192 KB per pair, PV 64 KB, the copies write 64 KB: 2,500
-// cycles. One sequence of 8,191 rows (28 heads over 4) runs at 1.36 PFLOP/s, 0.69 of the GEMM rate.
+// cycles. One sequence of 8,191 rows (28 heads over 4) runs at 1.35 PFLOP/s, 0.69 of the GEMM rate.
 // The start and output of an item take about 7,000 cycles, which bounds short sequences.
 // A row tile's first P of an item also says that its warps have read the O of the item before.
 //
@@ -1396,7 +1396,13 @@ PackedPlan plan_packed(int batch, int total, int hq, int hkv, int d, int max_len
   const long long items = packed::max_tiles(batch, total, p.tpt) * hkv * (G / p.gp);
   const int tiles = packed::key_tiles(max_len) + 1;
   // Two row tiles per item where sequences have more rows than one on average and the items
-  // fill the GPU.
+  // fill the GPU. Both forms, in us, 28 heads over 4 of 128 (rows | pair; the rule's border is at
+  // about 1,330 rows): one prompt of 512 rows 16 | 23, 1,024: 27 | 31, 1,300: 33 | 34, 1,400: 37 | 36,
+  // 2,048: 51 | 43; six and eight prompts of 200: 22.5 | 23.6 and 28.7 | 27.6; chunks of 100 over
+  // 1,000 cached, ten and fourteen: 37 | 46 and 49 | 50; one chunk over 8,192 cached of 256 rows 47 |
+  // 62, 512: 90 | 77, 1,024: 131 | 118, 1,300: 137 | 136, 1,400: 195 | 146. 14 heads over 2 of 64
+  // (border at about 2,700 rows): prompts of 2,600 rows 39 | 42, 2,800: 45 | 45, 4,096: 70 | 63; one chunk
+  // over 8,192 cached of 512 rows 45 | 50, 2,800: 199 | 144.
   const long long pairs = packed::max_tiles(batch, total, 2 * p.tpt) * hkv * (G / p.gp);
   if (total > (long long)batch * p.tpt && pairs >= num_sms()) {
     p.pair = true;

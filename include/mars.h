@@ -114,6 +114,9 @@ int mars_attn_dual_stream_lse(const mars_bf16* q, const mars_bf16* k, const mars
  *   workspace   >= mars_workspace_bytes(MARS_OP_DECODE_ATTN, ...) bytes
  *   status      may be NULL; MARS_ST_NOPAGE / MARS_ST_OVERFLOW when a needed page is
  *               unmapped (those keys are then skipped).
+ * Every value of the pool has to be finite, those of free slots too (zero a pool when it is
+ * allocated): what stands behind the prefix in the last 128 keys, and page 0 in the place
+ * of a page that is unmapped, is multiplied by weights of 0.
  * page_size must be 16. */
 int mars_decode_attn(const mars_bf16* q, const mars_bf16* k_blk, const mars_bf16* v_blk,
                      const mars_bf16* k_pool, const mars_bf16* v_pool, int num_pages,
@@ -367,7 +370,8 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
  *     heads * d is at most 2^29.
  *   - Outputs o, dq, dk, dv are bf16 (what the next product reads); statistics are float.
  *     Scores, softmax statistics and sums are held in 32 bits; the weights are rounded to
- *     bf16 for the product with V.
+ *     bf16 for the products with V and d_o, dS (below) for those with K and Q. The gradient's
+ *     D comes from o as given, rounded to bf16.
  *   - hq / hkv, d, scale and status as elsewhere; status may be NULL. Outputs and workspaces
  *     overlap no input.
  *   - A key that a sequence may not read (another sequence's row, a row behind the last
@@ -443,7 +447,8 @@ int mars_attn_chunk(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
  *            slot, -1 for a row that was not appended
  * The first row whose page is unmapped (entry < 0 or >= num_pages, or past max_pages_per_seq)
  * ends the append of its sequence and flags MARS_ST_NOPAGE / MARS_ST_OVERFLOW; so does a
- * negative seq_lens[s]. Two rows that map to the same slot leave either's values there. */
+ * negative seq_lens[s]. An empty pool (num_pages 0) or table (max_pages_per_seq 0) may be NULL.
+ * Two rows that map to the same slot leave either's values there. */
 int mars_kv_append(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seqlens,
                    const int32_t* seq_lens, int32_t* new_lens, const int32_t* block_table,
                    int max_pages_per_seq, mars_bf16* k_pool, mars_bf16* v_pool, int num_pages,
