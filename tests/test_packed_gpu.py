@@ -605,6 +605,8 @@ def test_chunk_a_page_loaded_for_an_unmapped_one_has_no_effect(lens, old, heads)
 FORMS = {"few-whole": ([200, 90], None, (4, 2, 64)), "few-split-packed": ([900], None, (4, 1, 64)),
          "one-token-split": ([1, 1, 1], [128, 1, 2300], (14, 2, 64)),
          "few-split": ([130, 2], [1000, 1700], (7, 1, 128)),
+         "one-token-63-splits": ([1, 2], [40000, 17], (2, 1, 64)),
+         "many-divided-64": ([2800], None, (14, 2, 64)),
          "many-divided": ([1400], None, (28, 4, 128)),
          "many-whole": ([(331 * i) % 500 + 40 for i in range(22)], None, (28, 4, 128)),
          "many-chunks-divided": HINTED[1],
@@ -879,3 +881,19 @@ def test_a_captured_step_over_growing_caches():
     got = loop(graph.replay)
     assert same(got, want) and same(eager[0], pools[0]) and same(eager[1], pools[1])
     check_chunk(x, want)                                   # the same rows as one chunk
+
+
+@pytest.mark.parametrize("what", ["table", "pool"])
+@pytest.mark.parametrize("lens, old, heads", HINTED, ids=["few", "many"])
+def test_chunk_over_lengths_without_any_page(lens, old, heads, what):
+    """An empty pool, or a table without a column: the chunk's own keys are what is left."""
+    x = make(lens, *heads, seed=53, old=old, tail=2)
+    y = cuda(x)
+    if what == "table":
+        y["table"] = y["table"][:, :0].contiguous()
+    else:
+        y["k_pool"], y["v_pool"] = y["k_pool"][:0], y["v_pool"][:0]
+    o, st = run_chunk(y)
+    assert st == (mars.ST_OVERFLOW if what == "table" else mars.ST_NOPAGE)
+    x["old"].zero_()
+    check_chunk(x, o)
