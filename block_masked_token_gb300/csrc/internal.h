@@ -168,4 +168,44 @@ cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, long long k_s
                              int batch, int total, int hkv, int d, int32_t* status,
                              cudaStream_t stream);
 
+// ---- Rotary positions of packed rows.
+struct Rotary {
+  const uint16_t *q, *k;
+  uint16_t *q_out, *k_out;
+  long long q_stride, k_stride, qo_stride, ko_stride;
+  const int32_t *cu, *seq_lens;         // seq_lens NULL: all 0
+  const float* inv_freq;                // [rot / 2]
+  int batch, total, hq, hkv, d, rot;
+  float factor;
+  bool inverse, in_place;               // in place: what is not rotated is not copied
+  int32_t* status;
+};
+cudaError_t launch_rotary(const Rotary& a, bool interleaved, cudaStream_t stream);
+
+// ---- K/V rows of packed sequences into the 8-bit paged cache.
+struct AppendQ8 {
+  const uint16_t *k, *v;
+  long long k_stride, v_stride;
+  const int32_t *cu, *seq_lens, *counts, *block_table;
+  int32_t *new_lens, *slots, *status;
+  uint8_t *k_pool, *v_pool, *k_scale, *v_scale;
+  int num_pages, max_pages, batch, total, hkv;
+};
+long long append_q8_ctas(int batch, int total);
+cudaError_t launch_kv_append_q8(const AppendQ8& a, int d, cudaStream_t stream);
+
+// ---- Attention of new tokens over the 8-bit paged cache.
+struct ChunkQ8 {
+  PackedAttn attn;                      // its pools stay NULL
+  const uint8_t *k_pool, *v_pool, *k_scale, *v_scale;
+};
+struct ChunkQ8Plan {
+  PackedPlan wide;                      // over the pages in bf16
+  int pages;                            // pages per sequence that the workspace has room for
+  size_t ws_bytes;
+};
+ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_len);
+cudaError_t launch_chunk_q8(const ChunkQ8& p, const ChunkQ8Plan& plan, void* workspace,
+                            cudaStream_t stream);
+
 }  // namespace mars

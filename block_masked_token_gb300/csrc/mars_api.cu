@@ -386,11 +386,16 @@ bool pool_fits(int num_pages, int hkv) {
   return num_pages >= 0 && (long long)num_pages * hkv * mars::kPageSize <= 0x7fffffffLL;
 }
 
+// Whether two arrays of n int32 share memory (NULL shares none).
+bool overlap(const int32_t* x, const int32_t* y, int n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return x && y && (a > b ? a - b : b - a) < sizeof(int32_t) * (size_t)n;
+}
+
 int grid_fits(long long ctas) { return ctas <= 0x7fffffffLL ? MARS_OK : MARS_EUNSUPPORTED; }
 
-int packed_attn_checked(mars::PackedAttn p, int max_len, void* workspace, size_t ws_bytes,
-                        void* stream) {
-  if (p.batch == 0 || p.total == 0) return MARS_OK;
+// Checks what the forms of the packed attention share, and fills in the default scale.
+int check_attn(mars::PackedAttn& p, const void* workspace) {
   if (!p.q || !p.k || !p.v || !p.cu || !p.o) return MARS_EINVAL;
   int rc = check_pitch((int)p.q_stride, p.hq, p.d);
   if (!rc) rc = check_pitch((int)p.k_stride, p.hkv, p.d);
@@ -400,7 +405,14 @@ int packed_attn_checked(mars::PackedAttn p, int max_len, void* workspace, size_t
       !aligned16(p.k_pool) || !aligned16(p.v_pool) || !aligned16(workspace))
     return MARS_EALIGN;
   if (!(p.scale > 0.f)) p.scale = 1.0f / sqrtf((float)p.d);
-  if (isinf(p.scale)) return MARS_EINVAL;
+  return isinf(p.scale) ? MARS_EINVAL : MARS_OK;
+}
+
+int packed_attn_checked(mars::PackedAttn p, int max_len, void* workspace, size_t ws_bytes,
+                        void* stream) {
+  if (p.batch == 0 || p.total == 0) return MARS_OK;
+  int rc = check_attn(p, workspace);
+  if (rc) return rc;
   const mars::PackedPlan plan = mars::plan_packed(p.batch, p.total, p.hq, p.hkv, p.d, max_len);
   if ((rc = grid_fits(plan.items))) return rc;
   if (ws_bytes < plan.ws_bytes) return MARS_ENOSPACE;
@@ -419,6 +431,8 @@ size_t mars_packed_workspace_bytes(int op, int batch, int total, int hq, int hkv
     return max_len < 0 ? 0 : mars::plan_packed(batch, total, hq, hkv, d, max_len).ws_bytes;
   if (op == MARS_OP_ATTN_PACKED_GRAD)
     return mars::packed_grad_workspace_bytes(batch, total, hq, hkv, d);
+  if (op == MARS_OP_ATTN_CHUNK_Q8)
+    return max_len < 0 ? 0 : mars::plan_chunk_q8(batch, total, hq, hkv, d, max_len).ws_bytes;
   return 0;
 }
 
@@ -535,9 +549,7 @@ int mars_kv_append(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seq
                     (num_pages > 0 && (!k_pool || !v_pool))))
     return MARS_EINVAL;                            // an empty table or pool has no address
   // every CTA of a sequence reads its length, the last one writes the new one
-  const uintptr_t at = reinterpret_cast<uintptr_t>(seq_lens), to = reinterpret_cast<uintptr_t>(new_lens);
-  if (new_lens && (to > at ? to - at : at - to) < sizeof(int32_t) * (size_t)batch)
-    return MARS_EINVAL;
+  if (overlap(new_lens, seq_lens, batch)) return MARS_EINVAL;
   if (total > 0) {
     rc = check_pitch(k_stride, hkv, d);
     if (!rc) rc = check_pitch(v_stride, hkv, d);
@@ -549,6 +561,113 @@ int mars_kv_append(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seq
                                         block_table, block_table ? max_pages_per_seq : 0, k_pool,
                                         v_pool, num_pages, slots, batch, total, hkv, d, status,
                                         static_cast<cudaStream_t>(stream)));
+}
+
+int mars_rotary(const mars_bf16* q, const mars_bf16* k, const int32_t* cu_seqlens,
+                const int32_t* seq_lens, const float* inv_freq, mars_bf16* q_out,
+                mars_bf16* k_out, int batch, int total, int hq, int hkv, int d, int rot,
+                int interleaved, int inverse, float factor, int q_stride, int k_stride,
+                int q_out_stride, int k_out_stride, int32_t* status, void* stream) {
+  int rc = check_packed(batch, total, hq, hkv, d);
+  if (rc) return rc;
+  if (rot < 2 || rot > d || !isfinite(factor)) return MARS_EINVAL;
+  if (rot % 16) return MARS_EUNSUPPORTED;
+  if (batch == 0 || total == 0) return MARS_OK;
+  if (!q || !k || !cu_seqlens || !inv_freq || !q_out || !k_out) return MARS_EINVAL;
+  if (!(rc = check_pitch(q_stride, hq, d)) && !(rc = check_pitch(k_stride, hkv, d)) &&
+      !(rc = check_pitch(q_out_stride, hq, d)))
+    rc = check_pitch(k_out_stride, hkv, d);
+  if (rc) return rc;
+  if ((q_out == q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride))
+    return MARS_EINVAL;
+  const void* ptr[4] = {q, k, q_out, k_out};
+  for (const void* x : ptr)
+    if (!aligned16(x)) return MARS_EALIGN;
+  const mars::Rotary a{q,        k,        q_out,        k_out, q_stride, k_stride, q_out_stride,
+                       k_out_stride, cu_seqlens, seq_lens, inv_freq, batch,    total, hq,
+                       hkv,      d,        rot,          factor, inverse != 0,
+                       q_out == q && k_out == k, status};
+  return cuda_rc(mars::launch_rotary(a, interleaved != 0, static_cast<cudaStream_t>(stream)));
+}
+
+int mars_kv_append_q8(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seqlens,
+                      const int32_t* seq_lens, const int32_t* counts, int32_t* new_lens,
+                      const int32_t* block_table, int max_pages_per_seq, uint8_t* k_pool,
+                      uint8_t* v_pool, uint8_t* k_scale, uint8_t* v_scale, int num_pages,
+                      int32_t* slots, int batch, int total, int hkv, int d, int page_size,
+                      int k_stride, int v_stride, int32_t* status, void* stream) {
+  int rc = check_packed(batch, total, hkv, hkv, d);
+  if (rc) return rc;
+  if (max_pages_per_seq < 0 || !pool_fits(num_pages, hkv)) return MARS_EINVAL;
+  if (page_size != mars::kPageSize) return MARS_EUNSUPPORTED;
+  if (batch == 0) return MARS_OK;
+  if (!cu_seqlens || !seq_lens) return MARS_EINVAL;
+  if (total > 0 && (!k || !v || (max_pages_per_seq > 0 && !block_table) ||
+                    (num_pages > 0 && (!k_pool || !v_pool || !k_scale || !v_scale))))
+    return MARS_EINVAL;                            // an empty table or pool has no address
+  if (overlap(new_lens, seq_lens, batch) || overlap(new_lens, counts, batch)) return MARS_EINVAL;
+  if (total > 0) {
+    rc = check_pitch(k_stride, hkv, d);
+    if (!rc) rc = check_pitch(v_stride, hkv, d);
+    if (rc) return rc;
+  }
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool))
+    return MARS_EALIGN;
+  if ((rc = grid_fits(mars::append_q8_ctas(batch, total)))) return rc;
+  const mars::AppendQ8 a{k,        v,      k_stride, v_stride, cu_seqlens, seq_lens, counts,
+                         block_table, new_lens, slots, status,  k_pool,     v_pool,   k_scale,
+                         v_scale,  num_pages, block_table ? max_pages_per_seq : 0, batch, total,
+                         hkv};
+  return cuda_rc(mars::launch_kv_append_q8(a, d, static_cast<cudaStream_t>(stream)));
+}
+
+int mars_attn_chunk_q8(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
+                       const int32_t* cu_seqlens, const uint8_t* k_pool, const uint8_t* v_pool,
+                       const uint8_t* k_scale, const uint8_t* v_scale, int num_pages,
+                       const int32_t* block_table, int max_pages_per_seq,
+                       const int32_t* seq_lens, int max_len_hint, mars_bf16* o, int batch,
+                       int total, int hq, int hkv, int d, int page_size, int q_stride,
+                       int k_stride, int v_stride, float scale, void* workspace,
+                       size_t ws_bytes, int32_t* status, void* stream) {
+  int rc = check_packed(batch, total, hq, hkv, d);
+  if (rc) return rc;
+  if (max_len_hint < 0 || max_pages_per_seq < 0 || !pool_fits(num_pages, hkv)) return MARS_EINVAL;
+  if (page_size != mars::kPageSize) return MARS_EUNSUPPORTED;
+  if (batch == 0 || total == 0) return MARS_OK;
+  if (!seq_lens) return MARS_EINVAL;
+  if (max_pages_per_seq > 0 &&
+      (!block_table || (num_pages > 0 && (!k_pool || !v_pool || !k_scale || !v_scale))))
+    return MARS_EINVAL;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return MARS_EALIGN;
+  mars::ChunkQ8 p{};
+  p.attn.q = q;
+  p.attn.k = k;
+  p.attn.v = v;
+  p.attn.q_stride = q_stride;
+  p.attn.k_stride = k_stride;
+  p.attn.v_stride = v_stride;
+  p.attn.cu = cu_seqlens;
+  p.attn.block_table = block_table;
+  p.attn.seq_lens = seq_lens;
+  p.attn.num_pages = k_pool && v_pool && k_scale && v_scale ? num_pages : 0;
+  p.attn.max_pages = block_table ? max_pages_per_seq : 0;
+  p.attn.o = o;
+  p.attn.batch = batch;
+  p.attn.total = total;
+  p.attn.hq = hq;
+  p.attn.hkv = hkv;
+  p.attn.d = d;
+  p.attn.scale = scale;
+  p.attn.status = status;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  if ((rc = check_attn(p.attn, workspace))) return rc;
+  const mars::ChunkQ8Plan plan = mars::plan_chunk_q8(batch, total, hq, hkv, d, max_len_hint);
+  if (ws_bytes < plan.ws_bytes) return MARS_ENOSPACE;
+  if (plan.ws_bytes && !workspace) return MARS_EINVAL;
+  return cuda_rc(mars::launch_chunk_q8(p, plan, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 const char* mars_strerror(int code) {

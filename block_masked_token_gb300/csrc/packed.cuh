@@ -34,8 +34,10 @@ inline long long max_tiles(int batch, int total, int rows_per_tile) {
 // `rows` rows and at least `least` tiles per sequence). Whole warp; the result is uniform.
 // bad = whether cu was malformed (only where the scan got to). lens [batch] or NULL is read with
 // the boundaries: after them it would be a further trip to memory before the tile can start.
-MARS_DEV Seq find_tile(const int32_t* __restrict__ cu, int batch, int total, int rows, int least,
-                       long long i, bool& bad, const int32_t* lens = nullptr) {
+// find_tile_by takes the number of tiles of a sequence from tiles(s, n, lens[s]).
+template <class F>
+MARS_DEV Seq find_tile_by(const int32_t* __restrict__ cu, int batch, int total, long long i,
+                          bool& bad, const int32_t* lens, F tiles_of) {
   const int lane = threadIdx.x & 31;
   long long tiles = 0;                         // tiles of the sequences before this group
   const int c0 = cu[0];
@@ -56,7 +58,7 @@ MARS_DEV Seq find_tile(const int32_t* __restrict__ cu, int batch, int total, int
     int begin = __shfl_up_sync(0xffffffffu, m, 1);
     if (lane == 0) begin = top;
     const int n = m - begin;
-    const int mine = s < batch ? max((n + rows - 1) / rows, least) : 0;
+    const int mine = s < batch ? tiles_of(s, n, len) : 0;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -78,6 +80,13 @@ MARS_DEV Seq find_tile(const int32_t* __restrict__ cu, int batch, int total, int
     top = __shfl_sync(0xffffffffu, m, 31);
   }
   return Seq{-1, 0, top, 0, 0};
+}
+
+MARS_DEV Seq find_tile(const int32_t* __restrict__ cu, int batch, int total, int rows, int least,
+                       long long i, bool& bad, const int32_t* lens = nullptr) {
+  return find_tile_by(cu, batch, total, i, bad, lens, [=](int, int n, int) {
+    return max((n + rows - 1) / rows, least);
+  });
 }
 
 constexpr int kTileRows = 128;

@@ -18,6 +18,10 @@ static __typeof__(&mars_attn_packed) p_packed;
 static __typeof__(&mars_attn_packed_grad) p_grad;
 static __typeof__(&mars_attn_chunk) p_chunk;
 static __typeof__(&mars_kv_append) p_append;
+static PyObject* d_e4m3;
+static __typeof__(&mars_rotary) p_rotary;
+static __typeof__(&mars_kv_append_q8) p_append_q8;
+static __typeof__(&mars_attn_chunk_q8) p_chunk_q8;
 
 static PyObject* method(PyObject* t, PyObject* name) {
   PyObject* args[2] = {NULL, t};
@@ -238,6 +242,107 @@ static PyObject* kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
                 (int)page, ks, vs, status, stream));
 }
 
+/* q, k, cu_seqlens, inv_freq, q_out, k_out, seq_lens, interleaved, factor, inverse, status */
+static PyObject* rotary(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  long long dev;
+  void *stream, *q, *k, *cu, *freq, *qo, *ko, *lens, *status;
+  int total = -1, hq = -1, hkv = -1, d = -1, batch, qs, ks, qos, kos, half = -1, one = 1;
+  if (n != 11 || !p_rotary || !PyBool_Check(a[7]) || !PyFloat_Check(a[8]) || !PyBool_Check(a[9]) ||
+      !target(a[0], &dev, &stream) || !rows(a[0], dev, &total, &hq, &d, &q, &qs) ||
+      !rows(a[1], dev, &total, &hkv, &d, &k, &ks) || !boundaries(a[2], dev, &batch, &cu) ||
+      !flat(a[3], d_f32, dev, 1, &half, &freq) || half > d ||
+      !rows(a[4], dev, &total, &hq, &d, &qo, &qos) ||
+      !rows(a[5], dev, &total, &hkv, &d, &ko, &kos) ||
+      !flat_or_none(a[6], d_i32, dev, 1, &batch, &lens) ||
+      !flat_or_none(a[10], d_i32, dev, 1, &one, &status))
+    return decline();
+  const float factor = (float)PyFloat_AS_DOUBLE(a[8]);
+  CALL(p_rotary(q, k, cu, lens, freq, qo, ko, batch, total, hq, hkv, d, 2 * half, a[7] == Py_True,
+                a[9] == Py_True, factor, qs, ks, qos, kos, status, stream));
+}
+
+/* k_pool, v_pool [pages, hkv, page, d] codes, k_scale, v_scale [pages, hkv], block_table
+ * [batch, width], seq_lens [batch] */
+static int cache_q8(PyObject* const* a, long long dev, int batch, int hkv, int page, int d,
+                    int* pages, int* width, void** kp, void** vp, void** ks, void** vs,
+                    void** table, void** lens) {
+  int ps[4] = {-1, hkv, page, d}, ss[2], ts[2] = {batch, -1};
+  if (!flat(a[0], d_e4m3, dev, 4, ps, kp) || !flat(a[1], d_e4m3, dev, 4, ps, vp)) return 0;
+  ss[0] = *pages = ps[0];
+  ss[1] = hkv;
+  if (!flat(a[2], d_u8, dev, 2, ss, ks) || !flat(a[3], d_u8, dev, 2, ss, vs) ||
+      !flat(a[4], d_i32, dev, 2, ts, table) || !flat(a[5], d_i32, dev, 1, &batch, lens))
+    return 0;
+  *width = ts[1];
+  return 1;
+}
+
+/* k, v, cu_seqlens, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, counts, new_lens,
+ * slots, status, page */
+static PyObject* kv_append_q8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  long long dev;
+  void *stream, *k, *v, *cu, *kp, *vp, *kc, *vc, *table, *lens, *counts, *new_lens, *slots, *status;
+  int total = -1, hkv = -1, d = -1, batch, ks, vs, pages, width, one = 1;
+  if (n != 14 || !p_append_q8) return decline();
+  const long long page = PyLong_AsLongLong(a[13]);
+  if (page <= 0 || page > INT_MAX || !target(a[0], &dev, &stream) ||
+      !rows(a[0], dev, &total, &hkv, &d, &k, &ks) ||
+      !rows(a[1], dev, &total, &hkv, &d, &v, &vs) || !boundaries(a[2], dev, &batch, &cu) ||
+      !cache_q8(a + 3, dev, batch, hkv, (int)page, d, &pages, &width, &kp, &vp, &kc, &vc, &table,
+                &lens) ||
+      !flat_or_none(a[9], d_i32, dev, 1, &batch, &counts) ||
+      !flat_or_none(a[10], d_i32, dev, 1, &batch, &new_lens) ||
+      !flat_or_none(a[11], d_i32, dev, 1, &total, &slots) ||
+      !flat_or_none(a[12], d_i32, dev, 1, &one, &status))
+    return decline();
+  CALL(p_append_q8(k, v, cu, lens, counts, new_lens, table, width, kp, vp, kc, vc, pages, slots,
+                   batch, total, hkv, d, (int)page, ks, vs, status, stream));
+}
+
+/* q, k, v, cu_seqlens, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, max_len_hint, o,
+ * workspace, status, scale, page */
+static PyObject* attn_chunk_q8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  long long dev;
+  void *stream, *q, *k, *v, *cu, *kp, *vp, *kc, *vc, *table, *lens, *o, *ws, *status;
+  int total = -1, hq = -1, hkv = -1, d = -1, batch, qs, ks, vs, pages, width, bytes, one = 1;
+  if (n != 16 || !p_chunk_q8 || !PyLong_Check(a[10]) || !PyFloat_Check(a[14])) return decline();
+  const long long hint = PyLong_AsLongLong(a[10]), page = PyLong_AsLongLong(a[15]);
+  if (hint < 0 || hint > INT_MAX || page <= 0 || page > INT_MAX || !target(a[0], &dev, &stream) ||
+      !rows(a[0], dev, &total, &hq, &d, &q, &qs) || !rows(a[1], dev, &total, &hkv, &d, &k, &ks) ||
+      !rows(a[2], dev, &total, &hkv, &d, &v, &vs) || !boundaries(a[3], dev, &batch, &cu) ||
+      !cache_q8(a + 4, dev, batch, hkv, (int)page, d, &pages, &width, &kp, &vp, &kc, &vc, &table,
+                &lens))
+    return decline();
+  int os[3] = {total, hq, d};
+  if (!flat(a[11], d_bf16, dev, 3, os, &o) || !scratch(a[12], dev, &bytes, &ws) ||
+      !flat_or_none(a[13], d_i32, dev, 1, &one, &status))
+    return decline();
+  const float scale = (float)PyFloat_AS_DOUBLE(a[14]);
+  CALL(p_chunk_q8(q, k, v, cu, kp, vp, kc, vc, pages, table, width, lens, (int)hint, o, batch,
+                  total, hq, hkv, d, (int)page, qs, ks, vs, scale, ws, (size_t)bytes, status,
+                  stream));
+}
+
+/* What the calls above need beside setup's: the dtype of the codes, and the addresses of the
+ * three entry points. */
+static PyObject* setup_q8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  void* p[3];
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "setup_q8: four arguments");
+    return NULL;
+  }
+  for (int i = 0; i < 3; ++i) {
+    p[i] = PyLong_AsVoidPtr(a[1 + i]);
+    if (PyErr_Occurred()) return NULL;
+  }
+  Py_INCREF(a[0]);
+  Py_XSETREF(d_e4m3, a[0]);
+  p_rotary = (__typeof__(p_rotary))p[0];
+  p_append_q8 = (__typeof__(p_append_q8))p[1];
+  p_chunk_q8 = (__typeof__(p_chunk_q8))p[2];
+  Py_RETURN_NONE;
+}
+
 /* Tensor type, the dtypes bf16, int32, float32, uint8, the functions giving the current device
  * and a device's raw current stream, and the addresses of the four entry points. */
 static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
@@ -264,7 +369,9 @@ static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(setup),      METHOD(attn_packed), METHOD(attn_packed_grad),
-                                METHOD(attn_chunk), METHOD(kv_append),   {NULL, NULL, 0, NULL}};
+                                METHOD(attn_chunk), METHOD(kv_append),   METHOD(setup_q8),
+                                METHOD(rotary),     METHOD(kv_append_q8), METHOD(attn_chunk_q8),
+                                {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_packed_calls", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};
 

@@ -80,6 +80,12 @@ def lib() -> ctypes.CDLL:
         L.mars_attn_chunk.argtypes = [P] * 6 + [I, P, I, P, I, P] + [I] * 9 + [F, P, S, P, P]
         L.mars_kv_append.restype = I
         L.mars_kv_append.argtypes = [P] * 6 + [I, P, P, I, P] + [I] * 7 + [P, P]
+        L.mars_rotary.restype = I
+        L.mars_rotary.argtypes = [P] * 7 + [I] * 8 + [F] + [I] * 4 + [P, P]
+        L.mars_kv_append_q8.restype = I
+        L.mars_kv_append_q8.argtypes = [P] * 7 + [I] + [P] * 4 + [I, P] + [I] * 7 + [P, P]
+        L.mars_attn_chunk_q8.restype = I
+        L.mars_attn_chunk_q8.argtypes = [P] * 8 + [I, P, I, P, I, P] + [I] * 9 + [F, P, S, P, P]
         L.mars_check_wait_timeout.restype = I
         L.mars_check_wait_timeout.argtypes = [P, P]
         L.mars_strerror.restype = ctypes.c_char_p
@@ -99,7 +105,7 @@ EXPORTED = ("mars_workspace_bytes", "mars_attn_dual_stream", "mars_decode_attn",
             "mars_dual_stream_ce_loss_grad", "mars_attn_dual_stream_grad",
             "mars_attn_dual_stream_lse", "mars_attn_dual_stream_grad_lse",
             "mars_packed_workspace_bytes", "mars_attn_packed", "mars_attn_packed_grad", "mars_attn_chunk",
-            "mars_kv_append",
+            "mars_kv_append", "mars_rotary", "mars_kv_append_q8", "mars_attn_chunk_q8",
             "mars_check_wait_timeout", "mars_strerror",
             "mars_version", "mars_launch_count")
 

@@ -1,7 +1,8 @@
 """ctypes binding of libmars' packed-sequence entry points (include/mars.h): attention of whole
 prompts and its gradient, attention of new tokens over the paged cache, and the append of
-their K/V. Like mars.py, argument marshalling only; the rows of q, k and v may be slices of a
-wider tensor (a fused projection's output).
+their K/V; rotary positions; and the append to, and attention over, the 8-bit paged cache. Like
+mars.py, argument marshalling only (but for rotary_frequencies, which makes a table); the rows of
+q, k and v may be slices of a wider tensor (a fused projection's output).
 
 A call for the current stream goes through csrc/packed_calls.c, which checks its arguments in C
 and declines what is not right (or not of the plainest kind: an integer scale, a workspace of
@@ -10,15 +11,17 @@ and declines what is not right (or not of the plainest kind: an integer scale, a
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
 from .mars import MarsError, PAGE_SIZE, lib
 
-OP_ATTN_PACKED, OP_ATTN_CHUNK, OP_ATTN_PACKED_GRAD = 6, 7, 8
+OP_ATTN_PACKED, OP_ATTN_CHUNK, OP_ATTN_PACKED_GRAD, OP_ATTN_CHUNK_Q8 = 6, 7, 8, 9
 
 _INT_MAX = 0x7fffffff
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_E4M3 = torch.float8_e4m3fn
 
 _calls = None
 
@@ -39,6 +42,8 @@ def _ready(first):
                         *(ctypes.cast(f, ctypes.c_void_p).value for f in (
                             entry.mars_attn_packed, entry.mars_attn_packed_grad,
                             entry.mars_attn_chunk, entry.mars_kv_append)))
+    _packed_calls.setup_q8(_E4M3, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        entry.mars_rotary, entry.mars_kv_append_q8, entry.mars_attn_chunk_q8)))
     _calls = _packed_calls
     return True
 
@@ -267,3 +272,133 @@ def mars_kv_append(k, v, cu_seqlens, seq_lens, block_table, k_pool, v_pool, new_
         _ptr(k_pool, "k_pool", _BF16, pool, dev), _ptr(v_pool, "v_pool", _BF16, pool, dev), pages,
         _opt(slots, "slots", _I32, (total,), dev), batch, total, hkv, d, PAGE_SIZE, ks, vs,
         _opt(status, "status", _I32, (1,), dev), raw), "mars_kv_append")
+
+
+def rotary_frequencies(rot, base: float = 10000.0, scaling=None, stretch: float = 1.0,
+                       trained: int = 0, low: float = 1.0, high: float = 32.0):
+    """(inv_freq [rot / 2] float32 on the host, factor) for mars_rotary: pair j turns by
+    base^(-2j / rot) radians per position, for contexts of up to `stretch` times those trained on
+    changed by `scaling`:
+      None       not at all
+      "linear"   every frequency divided by stretch (positions squeezed into the trained range)
+      "base"     base times stretch^(rot / (rot - 2)): the slowest pair is divided by stretch, the
+                 fastest not at all
+      "parts"    a pair that turns fewer than `low` times over the `trained` positions is divided
+                 by stretch, one that turns more than `high` times is not, and between the two the
+                 share falls linearly; factor = 1 + 0.1 ln(stretch) keeps the softmax as sharp."""
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot is {rot}: it must be even and at least 2")
+    if not base > 0 or not stretch >= 1:
+        raise ValueError("base must be positive and stretch at least 1")
+    if scaling not in (None, "linear", "base", "parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling == "base" and rot == 2:
+        raise ValueError("one pair has no base to scale")
+    if scaling == "base":
+        base = base * stretch ** (rot / (rot - 2))
+    freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    factor = 1.0
+    if scaling == "linear":
+        freq = freq / stretch
+    elif scaling == "parts":
+        if trained < 1 or not 0 < low < high:
+            raise ValueError("parts needs the number of trained positions, and 0 < low < high")
+        turns = trained * freq / (2 * math.pi)
+        kept = ((turns - low) / (high - low)).clamp(0, 1)
+        freq = freq * kept + freq / stretch * (1 - kept)
+        factor = 1.0 + 0.1 * math.log(stretch)
+    return freq.float(), factor
+
+
+def mars_rotary(q, k, cu_seqlens, inv_freq, q_out, k_out, seq_lens=None, interleaved: bool = False,
+                factor: float = 1.0, inverse: bool = False, status=None, stream=None):
+    """q_out, k_out = q and k with their pairs turned by their positions, seq_lens[s] + row;
+    inverse gives the gradient. q_out may be q and k_out k (see include/mars.h)."""
+    if stream is None and (_calls is not None or _ready(q)):
+        rc = _calls.rotary(q, k, cu_seqlens, inv_freq, q_out, k_out, seq_lens, interleaved, factor,
+                           inverse, status)
+        if rc is not None:
+            return _rc(rc, "mars_rotary")
+    dev, raw = _target(q, "q", stream)
+    total, hq, d = q.shape
+    hkv = k.shape[1]
+    cu, batch = _batch(cu_seqlens, dev)
+    qp, qs = _rows(q, "q", (total, hq, d), dev)
+    kp, ks = _rows(k, "k", (total, hkv, d), dev)
+    qop, qos = _rows(q_out, "q_out", (total, hq, d), dev)
+    kop, kos = _rows(k_out, "k_out", (total, hkv, d), dev)
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1 or inv_freq.shape[0] > d // 2:
+        raise ValueError("inv_freq must hold a frequency for each pair, d / 2 at most")
+    half = inv_freq.shape[0]
+    _rc(lib().mars_rotary(
+        qp, kp, cu, _opt(seq_lens, "seq_lens", _I32, (batch,), dev),
+        _ptr(inv_freq, "inv_freq", _F32, (half,), dev), qop, kop, batch, total, hq, hkv, d,
+        2 * half, bool(interleaved), bool(inverse), factor, qs, ks, qos, kos,
+        _opt(status, "status", _I32, (1,), dev), raw), "mars_rotary")
+
+
+def _cache_q8(k_pool, v_pool, k_scale, v_scale, hkv, d, dev):
+    """Addresses of an 8-bit cache's four tensors, and its pages."""
+    for t, name, dim in ((k_pool, "k_pool", 4), (v_pool, "v_pool", 4)):
+        if not isinstance(t, torch.Tensor) or t.dim() != dim:
+            raise ValueError(f"{name} must be [pages, hkv, {PAGE_SIZE}, d]")
+    pages = k_pool.shape[0]
+    _counts("k_pool", k_pool.shape)
+    pool = (pages, hkv, PAGE_SIZE, d)
+    return (_ptr(k_pool, "k_pool", _E4M3, pool, dev), _ptr(v_pool, "v_pool", _E4M3, pool, dev),
+            _ptr(k_scale, "k_scale", _U8, (pages, hkv), dev),
+            _ptr(v_scale, "v_scale", _U8, (pages, hkv), dev)), pages
+
+
+def mars_kv_append_q8(k, v, cu_seqlens, seq_lens, block_table, k_pool, v_pool, k_scale, v_scale,
+                      counts=None, new_lens=None, slots=None, status=None, stream=None):
+    """mars_kv_append into the 8-bit cache: float8_e4m3fn pools and uint8 scales [pages, hkv];
+    counts [batch] (int32, optional): how many of a sequence's rows (see include/mars.h)."""
+    if stream is None and (_calls is not None or _ready(k)):
+        rc = _calls.kv_append_q8(k, v, cu_seqlens, k_pool, v_pool, k_scale, v_scale, block_table,
+                                 seq_lens, counts, new_lens, slots, status, PAGE_SIZE)
+        if rc is not None:
+            return _rc(rc, "mars_kv_append_q8")
+    dev, raw = _target(k, "k", stream)
+    total, hkv, d = k.shape
+    cu, batch = _batch(cu_seqlens, dev)
+    kp, ks = _rows(k, "k", (total, hkv, d), dev)
+    vp, vs = _rows(v, "v", (total, hkv, d), dev)
+    table, width = _table(block_table, batch, dev)
+    cache, pages = _cache_q8(k_pool, v_pool, k_scale, v_scale, hkv, d, dev)
+    _rc(lib().mars_kv_append_q8(
+        kp, vp, cu, _ptr(seq_lens, "seq_lens", _I32, (batch,), dev),
+        _opt(counts, "counts", _I32, (batch,), dev),
+        _opt(new_lens, "new_lens", _I32, (batch,), dev), table, width, *cache, pages,
+        _opt(slots, "slots", _I32, (total,), dev), batch, total, hkv, d, PAGE_SIZE, ks, vs,
+        _opt(status, "status", _I32, (1,), dev), raw), "mars_kv_append_q8")
+
+
+def mars_attn_chunk_q8(q, k, v, cu_seqlens, k_pool, v_pool, k_scale, v_scale, block_table,
+                       seq_lens, max_len_hint: int, o, workspace, status=None, scale: float = 0.0,
+                       stream=None):
+    """mars_attn_chunk over the 8-bit cache (see include/mars.h); its workspace is that of
+    OP_ATTN_CHUNK_Q8."""
+    if stream is None and (_calls is not None or _ready(q)):
+        rc = _calls.attn_chunk_q8(q, k, v, cu_seqlens, k_pool, v_pool, k_scale, v_scale,
+                                  block_table, seq_lens, max_len_hint, o, workspace, status, scale,
+                                  PAGE_SIZE)
+        if rc is not None:
+            return _rc(rc, "mars_attn_chunk_q8")
+    dev, raw = _target(q, "q", stream)
+    if max_len_hint > _INT_MAX:
+        raise ValueError("max_len_hint is beyond 31 bits")
+    total, hq, d = q.shape
+    hkv = k.shape[1]
+    cu, batch = _batch(cu_seqlens, dev)
+    qp, qs = _rows(q, "q", (total, hq, d), dev)
+    kp, ks = _rows(k, "k", (total, hkv, d), dev)
+    vp, vs = _rows(v, "v", (total, hkv, d), dev)
+    table, width = _table(block_table, batch, dev)
+    cache, pages = _cache_q8(k_pool, v_pool, k_scale, v_scale, hkv, d, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _rc(lib().mars_attn_chunk_q8(
+        qp, kp, vp, cu, *cache, pages, table, width,
+        _ptr(seq_lens, "seq_lens", _I32, (batch,), dev), max_len_hint,
+        _ptr(o, "o", _BF16, (total, hq, d), dev), batch, total, hq, hkv, d, PAGE_SIZE, qs, ks, vs,
+        scale, ws, ws_bytes, _opt(status, "status", _I32, (1,), dev), raw), "mars_attn_chunk_q8")

@@ -61,6 +61,7 @@ typedef uint16_t mars_bf16;
 #define MARS_OP_ATTN_PACKED 6        /* for mars_packed_workspace_bytes */
 #define MARS_OP_ATTN_CHUNK 7
 #define MARS_OP_ATTN_PACKED_GRAD 8
+#define MARS_OP_ATTN_CHUNK_Q8 9
 
 /* Workspace (device scratch, caller-allocated, >= 256-byte aligned) needed by `op`.
  * MARS_OP_DECODE_ATTN uses batch, B, hq, hkv, d, max_len (the max_len_hint of the call);
@@ -382,8 +383,9 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
  *     of whose scores are -infinity has lse -infinity and weights of 0. */
 
 /* Workspace (device scratch, >= 256-byte aligned) of `op` (MARS_OP_ATTN_PACKED,
- * MARS_OP_ATTN_CHUNK, MARS_OP_ATTN_PACKED_GRAD) for `total` rows of `batch` sequences;
- * max_len: the max_len_hint of a mars_attn_chunk call, ignored by the others. 0 for an
+ * MARS_OP_ATTN_CHUNK, MARS_OP_ATTN_PACKED_GRAD, MARS_OP_ATTN_CHUNK_Q8) for `total` rows of
+ * `batch` sequences; max_len: the max_len_hint of a mars_attn_chunk or mars_attn_chunk_q8 call,
+ * ignored by the others. 0 for an
  * unknown op, invalid sizes, or an op that needs none. Calls whose kernels may overlap on the
  * GPU, graph replays among them, each need a workspace of their own. */
 size_t mars_packed_workspace_bytes(int op, int batch, int total, int hq, int hkv, int d,
@@ -454,6 +456,68 @@ int mars_kv_append(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seq
                    int max_pages_per_seq, mars_bf16* k_pool, mars_bf16* v_pool, int num_pages,
                    int32_t* slots, int batch, int total, int hkv, int d, int page_size,
                    int k_stride, int v_stride, int32_t* status, void* stream);
+
+/* Rotary positions of the queries and keys of packed sequences (conventions above): row i of
+ * sequence s stands at position p = seq_lens[s] + i, and pair j of each of its heads, (a, b),
+ * becomes factor * (a cos t - b sin t, a sin t + b cos t) with t = p * inv_freq[j]. The first
+ * `rot` elements of a head take part: pair j is elements j and j + rot / 2, or with
+ * `interleaved` elements 2j and 2j + 1. The others are copied as they are.
+ *   seq_lens [batch] int32 or NULL (all 0): tokens before each sequence's rows; a negative one
+ *            counts as 0 and flags MARS_ST_OVERFLOW
+ *   inv_freq [rot / 2] float (device): radians per position; scalings for long contexts are in
+ *            these and in factor. A pair whose frequency is not finite becomes NaN.
+ *   rot      a multiple of 16, 16 .. d
+ *   inverse  not 0: t is negated. That is the gradient: with q and k the upstream gradients of
+ *            the outputs, q_out and k_out are those of the inputs.
+ *   q_out [total, hq, d], k_out [total, hkv, d] bf16 (written for the rows of the sequences),
+ *            row pitches like those of q and k. In place is allowed: q_out == q with the same
+ *            pitch, k_out == k with the same pitch; no other overlap is.
+ * Angles are reduced to a turn in 64-bit fixed point, so that far positions lose nothing; the
+ * products and sums are formed in 32 bits and rounded once to bf16. */
+int mars_rotary(const mars_bf16* q, const mars_bf16* k, const int32_t* cu_seqlens,
+                const int32_t* seq_lens, const float* inv_freq, mars_bf16* q_out,
+                mars_bf16* k_out, int batch, int total, int hq, int hkv, int d, int rot,
+                int interleaved, int inverse, float factor, int q_stride, int k_stride,
+                int q_out_stride, int k_out_stride, int32_t* status, void* stream);
+
+/* ---- The 8-bit paged cache: half the bytes of the bf16 one.
+ *   k_pool, v_pool   [num_pages, hkv, page_size, d] e4m3 codes
+ *   k_scale, v_scale [num_pages, hkv] uint8: byte x stands for the scale 2^(x - 127) of a page and
+ *                    KV head; bytes below 87 count as 87, beyond 167 as 167
+ * A token's element is its code times its page's scale. Pages and scales need no
+ * initialisation, and a free slot may hold anything. */
+
+/* mars_kv_append into the 8-bit cache. The scale of a page and KV head that new rows fall on
+ * becomes the smallest power of two (2^-40 .. 2^40) under which the largest finite magnitude of
+ * its new rows needs no code beyond 448, or stays what it was where the page held tokens of the
+ * sequence before (seq_lens[s] % page_size of them) and that one is larger. Codes are the nearest
+ * to row / scale, ties to even; finite values beyond the range end at its border, infinities and
+ * NaN become NaN. Where the scale of a page with tokens grows, their codes are rounded again,
+ * over the new scale (exactly, but for what falls among the smallest codes).
+ *   counts [batch] int32 or NULL: only the first counts[s] rows of sequence s are appended (the
+ *          accepted positions of a decoded block), cut to 0 .. its rows; NULL: all
+ *   new_lens, slots  as mars_kv_append; new_lens may overlap neither seq_lens nor counts
+ * A sequence's first unmapped page ends its append as in mars_kv_append. Sequences that append
+ * to the same page leave it undefined: a page shared by sequences is full, or copied first. */
+int mars_kv_append_q8(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_seqlens,
+                      const int32_t* seq_lens, const int32_t* counts, int32_t* new_lens,
+                      const int32_t* block_table, int max_pages_per_seq, uint8_t* k_pool,
+                      uint8_t* v_pool, uint8_t* k_scale, uint8_t* v_scale, int num_pages,
+                      int32_t* slots, int batch, int total, int hkv, int d, int page_size,
+                      int k_stride, int v_stride, int32_t* status, void* stream);
+
+/* mars_attn_chunk over the 8-bit cache: row i of sequence s attends to the P_s = seq_lens[s]
+ * cached tokens and to the chunk's rows 0 .. i, given in k and v in bf16. Arguments, errors and
+ * what other keys may hold as mars_attn_chunk; the pools and scales as above.
+ *   workspace >= mars_packed_workspace_bytes(MARS_OP_ATTN_CHUNK_Q8, ...) bytes (NULL if 0) */
+int mars_attn_chunk_q8(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
+                       const int32_t* cu_seqlens, const uint8_t* k_pool, const uint8_t* v_pool,
+                       const uint8_t* k_scale, const uint8_t* v_scale, int num_pages,
+                       const int32_t* block_table, int max_pages_per_seq,
+                       const int32_t* seq_lens, int max_len_hint, mars_bf16* o, int batch,
+                       int total, int hq, int hkv, int d, int page_size, int q_stride,
+                       int k_stride, int v_stride, float scale, void* workspace,
+                       size_t ws_bytes, int32_t* status, void* stream);
 
 /* Self-check of the in-kernel wait limit every pipeline relies on: enqueues one small
  * kernel that waits on an mbarrier nothing completes. The wait gives up after its time
