@@ -26,6 +26,12 @@ MARS_DEV int scale_for(uint32_t amax) {
   return min(max(x, kLeast), kMost);
 }
 
+// Two floats as halves.
+MARS_DEV uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // Codes of two floats; beyond the range they end at its border, NaN stays.
 MARS_DEV uint32_t encode2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);

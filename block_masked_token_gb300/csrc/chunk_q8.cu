@@ -1,9 +1,33 @@
-// Attention of new tokens over the 8-bit paged cache (cache_q8.cuh): the pages that the sequences
-// read are written out in bf16, which holds every code times its scale exactly, and attended to by
-// packed_attn.cu.
+// Attention of new tokens over the 8-bit paged cache (cache_q8.cuh).
+//
+//   O_i = sum_u softmax_u(scale q_i . k_u) v_u over the keys row i of its sequence sees: the
+//   P = seq_lens[s] cached keys, each its code times its page's scale, and the sequence's own keys
+//   0 .. i in bf16.
+//
+// chunk_kernel works on the codes. A persistent CTA per SM takes an equal part of all key tiles of
+// all items; an item is a tile of up to 128 (token, query head) rows that share a KV head, as in
+// packed_attn.cu, with the 128-key tiles that its rows see: the sequence's own keys first, then the
+// cached ones. The products run on f16, which holds every code exactly (bf16 would too, but takes
+// five instructions for what one conversion does):
+//   - Q is divided by a power of two per row (its largest magnitude then lies in [1, 2)), an own
+//     key or value by one per 16 tokens, so that 11 bits hold them like bf16's 8 do;
+//   - scores get the row's power and the K scale of their 16 keys as one factor in 32 bits;
+//   - with V = 2^e c, a weight's power goes the other way: P' = 2^(s + e - m') is the A operand,
+//     m' the running maximum of s + e instead of s, and the row sum takes P' 2^-e. P' is then as
+//     large as what it contributes, whatever the pages' scales are; 2^7 P' is stored, so that small
+//     ones keep their bits.
+//
+// Roles (384 threads): warp 0 walks the items and reads block table and scales ahead of the others
+// (infos); warp 1 copies whole pages into a ring, 2 KB each; warps 8..11 turn raw tiles of K and V
+// into swizzled f16 tiles, zero where no key may be read; warps 2 and 3 issue S = Q K^T and O += P' V;
+// warps 4..7 run the softmax (thread = row), load Q and store O.
+//
+// A cut inside an item leaves partials (m', l, O) that merge_kernel joins in the order of the keys.
 #include <algorithm>
+#include <climits>
 
 #include "cache_q8.cuh"
+#include "flash_tc.cuh"
 #include "internal.h"
 #include "packed.cuh"
 
@@ -11,37 +35,990 @@ namespace mars {
 
 namespace {
 
-constexpr int kThreads = 256;
+using flash::BKV;
+using flash::BQ;
+
+constexpr int kThreads = 384;
+constexpr int kSoftmaxWarp = 4, kConvertWarp = 8, kConvertWarps = 4;
+constexpr int kControlRegs = 80, kSoftmaxRegs = 232, kConvertRegs = 184;
+static_assert(128 * (kControlRegs + kSoftmaxRegs + kConvertRegs) <=
+                  kThreads * (65536 / kThreads / 8 * 8),
+              "the register split fits the launch's register pool");
+constexpr int kRaw = 4;              // ring of raw tiles (K and V in turn)
+constexpr int kTiles = 2;            // f16 tiles of K, and of V
+constexpr int kBufs = 3;             // S buffers in TMEM
+constexpr int kInfos = 8;            // tiles that the walk may be ahead
+constexpr int kPagesPerTile = BKV / kPageSize;
+constexpr int kMinPart = 4;          // key tiles of a part of a divided item
+constexpr long long kUnit = 8, kItemWork = 12;   // work of a key tile and of an item's start and end
+constexpr int kOwnMost = 207;        // largest scale byte of 16 own rows: 2^80
+constexpr float kLift = 7.f;         // log2 of what P' is multiplied by
+constexpr float kNoKeys = -1.f;      // l of a part without keys, which has no O
+
+struct Args {
+  const uint16_t *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  const int32_t *cu, *seq_lens, *block_table;
+  const uint8_t *k_pool, *v_pool, *k_scale, *v_scale;
+  int num_pages, max_pages, batch, total, hq, hkv, gp, tpt, heads;   // heads: KV heads x groups
+  bool can_split;
+  int skip_pages;                    // sequences of more than tpt rows and at most so many pages
+                                     // are left to the wide form (-1: none)
+  float scale_log2;
+  uint16_t* o;
+  struct Record* rec;                // [CTA]
+  float4* part;                      // [CTA][2][kPart]
+  int32_t* status;
+};
+
+// What merge_kernel needs of a CTA: the item that it begins and does not end, if any, and whether
+// all of its part lies inside an item that goes on in the next CTA.
+struct Record {
+  int begins, inside, base, tok0, tokens, h0, pad[2];
+};
+
+// ---------------------------------------------------------------------------- the line of items
+
+struct Row {
+  int s, base, n, P;
+  long long pre;                     // work before the sequence
+  MARS_DEV int own() const { return (n + BKV - 1) / BKV; }
+  // own and cached tiles of every item of the sequence (an item's own tiles behind its last
+  // token, which it skips, counted too)
+  MARS_DEV int tiles() const { return own() + packed::key_tiles(P); }
+  MARS_DEV long long unit() const { return kUnit * tiles() + kItemWork; }
+};
+
+MARS_DEV bool left_out(int skip_pages, int tpt, int n, int P) {
+  return n > tpt && P / kPageSize + (P % kPageSize != 0) <= skip_pages;
+}
+MARS_DEV int cached(const Args& a, int len) {
+  return (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize));
+}
+MARS_DEV long long items_of(const Args& a, const Row& q) {
+  if (q.n <= 0 || left_out(a.skip_pages, a.tpt, q.n, q.P)) return 0;
+  return (long long)((q.n + a.tpt - 1) / a.tpt) * a.heads;
+}
+
+struct Scan {
+  long long sum[kThreads / 32], count[kThreads / 32];
+  int top[kThreads / 32];
+  Row at[2];
+  long long total, ctas;
+};
+
+// Every thread of the CTA: the work of all, how many CTAs share it, and the sequences where this
+// CTA's part begins and ends. A thread takes ceil(batch / threads) sequences.
+MARS_DEV void find_part(const Args& a, Scan& sc) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  const int lo = (int)min((long long)tid * per, (long long)a.batch), hi = min(lo + per, a.batch);
+  auto clamped = [&](int s) { return min(max(a.cu[s], 0), a.total); };
+  int bad = 0, m = 0;
+  for (int s = lo; s < hi; ++s) m = max(m, clamped(s + 1));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, m, o);
+    if (lane >= o) m = max(m, v);
+  }
+  if (lane == 31) sc.top[warp] = m;
+  __syncthreads();
+  int lead = clamped(0);                             // the boundary before this thread's sequences
+  if (tid == 0 && lead != a.cu[0]) bad = MARS_ST_BADSEQ;
+  for (int w = 0; w < warp; ++w) lead = max(lead, sc.top[w]);
+  m = __shfl_up_sync(0xffffffffu, m, 1);
+  if (lane > 0) lead = max(lead, m);
+  auto each = [&](auto f) {
+    Row q{};
+    q.base = lead;
+    for (int s = lo; s < hi; ++s) {
+      const int end = max(clamped(s + 1), q.base), len = a.seq_lens[s];
+      q.s = s;
+      q.n = end - q.base;
+      q.P = cached(a, len);
+      if (end != a.cu[s + 1]) bad |= MARS_ST_BADSEQ;
+      if (q.P != len && q.n > 0) bad |= MARS_ST_OVERFLOW;
+      const long long items = items_of(a, q);
+      f(q, items);
+      q.pre += items * q.unit();
+      q.base = end;
+    }
+  };
+  long long mine = 0, count = 0;
+  each([&](const Row& q, long long items) {
+    mine += items * q.unit();
+    count += items;
+  });
+  long long incl = mine, sum = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  if (lane == 31) {
+    sc.sum[warp] = incl;
+    sc.count[warp] = sum;
+  }
+  __syncthreads();
+  long long pre = incl - mine, total = 0, items = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) pre += sc.sum[w];
+    total += sc.sum[w];
+    items += sc.count[w];
+  }
+  // as many CTAs as there are, unless that leaves less than a part each and there are fewer items
+  const long long ctas =
+      min((long long)gridDim.x, max(items, total / (kUnit * kMinPart + kItemWork)));
+  if (tid == 0) {
+    sc.total = total;
+    sc.ctas = ctas;
+  }
+  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
+  if ((long long)blockIdx.x < ctas) {
+    const long long p0 = blockIdx.x * total / ctas, p1 = (blockIdx.x + 1) * total / ctas;
+    if (mine > 0 && ((p0 >= pre && p0 < pre + mine) || (p1 >= pre && p1 < pre + mine)))
+      each([&](const Row& q, long long n) {
+        Row r = q;
+        r.pre += pre;
+        if (n > 0 && p0 >= r.pre && p0 < r.pre + n * q.unit()) sc.at[0] = r;
+        if (n > 0 && p1 >= r.pre && p1 < r.pre + n * q.unit()) sc.at[1] = r;
+      });
+  }
+  __syncthreads();
+}
+
+// Item i of the sequence and its tile j at which position `pos` of the line cuts; not within
+// kMinPart tiles of an item's ends.
+MARS_DEV void cut_at(const Args& a, const Row& q, long long pos, long long& i, int& j) {
+  const long long rem = pos - q.pre;
+  i = rem / q.unit();
+  const int tiles = q.tiles();
+  j = (int)min(max((rem - i * q.unit() - kItemWork / 2) / kUnit, 0LL), (long long)tiles);
+  const int least = a.can_split ? kMinPart : tiles / 2;
+  if (j < least || !a.can_split) {
+    const bool up = j >= least && j > 0;
+    i += up;
+    j = 0;
+  } else if (tiles - j < kMinPart) {
+    ++i;
+    j = 0;
+  }
+}
+
+// Sequences one after another, 32 of them read at once. Whole warp.
+struct Window {
+  const Args& a;
+  int s0, begin, end, len;           // first sequence; this lane's
+  MARS_DEV Window(const Args& a_, const Row& q) : a(a_), s0(0), begin(0), end(0), len(0) {
+    load(q.s, q.base);
+  }
+  MARS_DEV void load(int s, int base) {
+    const int lane = threadIdx.x & 31;
+    s0 = s;
+    const int mine = s + lane;
+    end = mine < a.batch ? min(max(a.cu[mine + 1], 0), a.total) : 0;
+    len = mine < a.batch ? a.seq_lens[mine] : 0;
+    end = max(end, base);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end = max(end, v);
+    }
+    begin = __shfl_up_sync(0xffffffffu, end, 1);
+    if (lane == 0) begin = base;
+  }
+  // the sequence after q, which is not the last one
+  MARS_DEV Row after(const Row& q) {
+    const int s = q.s + 1;
+    if (s >= s0 + 32) load(s, q.base + q.n);
+    const int l = s - s0;
+    Row r{};
+    r.s = s;
+    r.base = __shfl_sync(0xffffffffu, begin, l);
+    r.n = __shfl_sync(0xffffffffu, end, l) - r.base;
+    r.P = cached(a, __shfl_sync(0xffffffffu, len, l));
+    return r;
+  }
+};
+
+// --------------------------------------------------------------------------------- the pipeline
+
+enum : int { kFirst = 1, kLast = 2, kOwn = 4, kEnd = 8 };
+
+// A key tile as the walk hands it to the other warps.
+struct alignas(16) Info {
+  int flags;
+  int base, n, tok0, h0, kvh;        // its item
+  int slot;                          // of the partial, -1: the item is whole
+  int k0, count;                     // first key (own: token of the sequence), keys that there are
+  int pad[3];
+  alignas(16) int page[kPagesPerTile];         // -1: not to be read
+  alignas(8) uint8_t k_byte[kPagesPerTile];    // scale bytes; own tiles: written by the converters
+  alignas(8) uint8_t v_byte[kPagesPerTile];    // 0: no such keys
+};
+
+struct Bar {
+  uint64_t info_full[kInfos], info_empty[kInfos];
+  uint64_t raw_full[kRaw], raw_empty[kRaw];
+  uint64_t f_full[2][kTiles], f_empty[2][kTiles];      // K, V
+  uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
+  uint64_t q_full, drain[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+struct Layout {
+  static constexpr int RAW = BKV * D, TILE = BKV * D * 2, PAGE = kPageSize * D;
+  static constexpr int OFF_Q = 0, OFF_F = TILE;                      // f16 tiles: K ring, V ring
+  static constexpr int OFF_RAW = OFF_F + 2 * kTiles * TILE;
+  static constexpr int TOTAL = OFF_RAW + kRaw * RAW + 1024;          // + alignment slack
+  static constexpr int TM_S = 0, TM_O = kBufs * BKV, P_OFF = BKV / 2;
+  static constexpr int PART = BQ * D / 4 + BQ / 2;                   // float4 of a partial
+  static MARS_DEV uint8_t* tile(uint8_t* smem, int is_v, int t) {
+    return smem + OFF_F + (is_v * kTiles + t % kTiles) * TILE;
+  }
+};
+
+struct Pipe {
+  const Args& a;
+  Bar& bar;
+  Info* infos;
+  uint8_t* smem;
+  uint32_t tmem;
+
+  // waits of one thread, and of a whole warp
+  MARS_DEV bool wait(uint64_t* b, uint32_t parity) const {
+    return sm100::mbar_wait(b, parity, &bar.abort, a.status);
+  }
+  MARS_DEV bool warp_wait(uint64_t* b, uint32_t parity) const {
+    return __all_sync(0xffffffffu, wait(b, parity));
+  }
+  MARS_DEV Info& info(int t) const { return infos[t % kInfos]; }
+  MARS_DEV uint64_t* info_full(int t, uint32_t& parity) const {
+    parity = (t / kInfos) & 1;
+    return &bar.info_full[t % kInfos];
+  }
+  MARS_DEV bool wait_info(int t) const {
+    uint32_t p;
+    uint64_t* b = info_full(t, p);
+    return wait(b, p);
+  }
+  MARS_DEV bool warp_wait_info(int t) const { return __all_sync(0xffffffffu, wait_info(t)); }
+  MARS_DEV void warp_done(int t) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&bar.info_empty[t % kInfos]);
+  }
+};
+
+// Warp 0: this CTA's tiles, one after another.
+template <int D>
+MARS_DEV void walk(const Pipe& p, const Scan& sc) {
+  using namespace sm100;
+  const Args& a = p.a;
+  const int lane = threadIdx.x & 31;
+  Record rec{};
+  int t = 0, flags = 0;
+  bool ok = true;
+  // wait until `n` entries from t on are free
+  auto room = [&](int n) {
+    int good = 1;
+    if (lane < n) good = p.wait(&p.bar.info_empty[(t + lane) % kInfos], (((t + lane) / kInfos) & 1) ^ 1);
+    return __all_sync(0xffffffffu, good) != 0;
+  };
+  auto publish = [&](int n) {
+    __syncwarp();
+    if (lane < n) mbar_arrive(&p.bar.info_full[(t + lane) % kInfos]);
+    t += n;
+  };
+  const long long p0 = blockIdx.x * sc.total / sc.ctas, p1 = (blockIdx.x + 1) * sc.total / sc.ctas;
+  Row q = sc.at[0];
+  long long i, ei = 0;
+  int j, es = a.batch, ej = 0;
+  cut_at(a, q, p0, i, j);
+  if (p1 < sc.total) {
+    es = sc.at[1].s;
+    cut_at(a, sc.at[1], p1, ei, ej);
+  }
+  Window window(a, q);
+  for (;; ++i, j = 0) {
+    if (i >= items_of(a, q)) {
+      i = 0;
+      j = 0;
+      bool more;
+      do {
+        more = q.s + 1 < a.batch && q.s + 1 <= es;
+        if (more) q = window.after(q);
+      } while (more && items_of(a, q) == 0);
+      if (!more) break;
+    }
+    if (q.s > es || (q.s == es && (i > ei || (i == ei && j >= ej)))) break;
+    const int tiles = q.tiles(), jb = q.s == es && i == ei ? ej : tiles;
+    const int rt = (int)(i / a.heads), hg = (int)(i % a.heads);
+    const int tok0 = rt * a.tpt, last_tok = min(tok0 + a.tpt, q.n) - 1;
+    const int slot = j > 0 ? 0 : jb < tiles ? 1 : -1;
+    const int kvh = hg / (a.heads / a.hkv), h0 = hg * a.gp;
+    if (slot == 1) rec = Record{1, rec.inside, q.base, tok0, last_tok + 1 - tok0, h0, {0, 0}};
+    if (slot == 0 && jb < tiles) rec.inside = 1;
+    // own tiles [j, own), cached tiles [c0, c1)
+    const int own = min(min(jb, q.own()), last_tok / BKV + 1);
+    const int c0 = max(j - q.own(), 0), c1 = max(jb - q.own(), 0);
+    int left = max(own - j, 0) + c1 - c0;
+    if (left == 0) {                                 // its own tiles here are behind the last token
+      float2* ml = reinterpret_cast<float2*>(a.part + ((size_t)blockIdx.x * 2 + slot) * Layout<D>::PART +
+                                             BQ * D / 4);
+      for (int r = lane; r < BQ; r += 32) ml[r] = make_float2(-INFINITY, kNoKeys);
+      continue;
+    }
+    int first = kFirst;
+    auto entry = [&](Info& e, int k0, int count, int f) {
+      e.flags = f;
+      e.base = q.base;
+      e.n = q.n;
+      e.tok0 = tok0;
+      e.h0 = h0;
+      e.kvh = kvh;
+      e.slot = slot;
+      e.k0 = k0;
+      e.count = count;
+    };
+    for (int x = j; x < own && ok; ++x) {
+      if (!(ok = room(1))) break;
+      if (lane == 0)
+        entry(p.info(t), x * BKV, min(last_tok + 1 - x * BKV, BKV),
+              kOwn | first | (left == 1 ? kLast : 0));
+      first = 0;
+      --left;
+      publish(1);
+    }
+    // four cached tiles at a time, a page per lane; table entries are read a step ahead
+    const int32_t* table = a.block_table + (size_t)q.s * a.max_pages;
+    auto page_of = [&](int x) {
+      const long long lp = (long long)x * kPagesPerTile + lane;
+      return x + lane / kPagesPerTile < c1 && lp * kPageSize < q.P ? table[lp] : -1;
+    };
+    int next = page_of(c0);
+    for (int x = c0; x < c1 && ok; x += 4) {
+      const int n = min(4, c1 - x), e = next, mine = x + lane / kPagesPerTile;
+      next = page_of(x + 4);
+      const bool needed = mine < c1 && (mine * kPagesPerTile + lane % kPagesPerTile) * (long long)kPageSize < q.P;
+      const bool readable = needed && e >= 0 && e < a.num_pages;
+      if (needed && !readable) flags |= MARS_ST_NOPAGE;
+      uint8_t kb = 127, vb = 0;
+      if (readable) {
+        const size_t at = (size_t)e * a.hkv + kvh;
+        kb = (uint8_t)q8::scale_byte(a.k_scale[at]);
+        vb = (uint8_t)q8::scale_byte(a.v_scale[at]);
+      }
+      if (!(ok = room(n))) break;
+      if (lane < n * kPagesPerTile) {
+        const int g = lane % kPagesPerTile, u = lane / kPagesPerTile;
+        Info& f = p.info(t + u);
+        f.page[g] = readable ? e : -1;
+        f.k_byte[g] = kb;
+        f.v_byte[g] = vb;
+        if (g == 0)
+          entry(f, mine * BKV, min(q.P - mine * BKV, BKV),
+                (u == 0 ? first : 0) | (u + 1 == left ? kLast : 0));
+      }
+      first = 0;
+      left -= n;
+      publish(n);
+    }
+    if (!ok) break;
+  }
+  if (ok && room(1)) {
+    if (lane == 0) p.info(t).flags = kEnd;
+    publish(1);
+  }
+  if (lane == 0 && a.rec) a.rec[blockIdx.x] = rec;
+  if (flags && a.status) atomicOr(a.status, flags);
+}
+
+// Warp 1: raw tiles, K and V in turn, a copy per page.
+template <int D>
+MARS_DEV void load_raw(const Pipe& p) {
+  using namespace sm100;
+  using L = Layout<D>;
+  const Args& a = p.a;
+  const int lane = threadIdx.x & 31;
+  int last[kRaw];
+#pragma unroll
+  for (int i = 0; i < kRaw; ++i) last[i] = -1;
+  int c = 0;
+  for (int t = 0;; ++t) {
+    if (!p.warp_wait_info(t)) break;
+    const Info& f = p.info(t);
+    const int flags = f.flags;
+    if (flags & kEnd) break;
+    bool ok = true;
+    if (!(flags & kOwn)) {
+      const int page = lane < kPagesPerTile ? f.page[lane] : -1;
+      const int pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
+      const size_t at = ((size_t)max(page, 0) * a.hkv + f.kvh) * L::PAGE;
+#pragma unroll
+      for (int h = 0; h < 2; ++h, ++c) {
+        const int st = c % kRaw;
+        int good = 1;
+        if (lane == 0) {
+          good = p.wait(&p.bar.raw_empty[st], ((c / kRaw) & 1) ^ 1);
+          if (good) mbar_arrive_expect_tx(&p.bar.raw_full[st], pages * L::PAGE);
+        }
+        if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
+        if (page >= 0)
+          bulk_load(p.smem + L::OFF_RAW + st * L::RAW + lane * L::PAGE, (h ? a.v_pool : a.k_pool) + at,
+                    L::PAGE, &p.bar.raw_full[st]);
+#pragma unroll
+        for (int i = 0; i < kRaw; ++i)
+          if (i == st) last[i] = c;
+      }
+    }
+    if (!ok) break;
+    p.warp_done(t);
+  }
+  // no copy is in flight when the CTA ends
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < kRaw; ++i)
+      if (last[i] >= 0) mbar_wait(&p.bar.raw_full[i], (last[i] / kRaw) & 1, nullptr, a.status);
+  __syncwarp();
+}
+
+// 16 bytes of an f16 tile: chunk c (8 elements) of row r. Regions of 64 elements, 128-byte swizzle.
+MARS_DEV uint8_t* chunk_at(uint8_t* tile, int r, int c) {
+  return tile + (c >> 3) * (BKV * 128) + flash::sw_off(r, c & 7);
+}
+
+// One converter warp's share of a raw tile: 16-token groups 2w and 2w + 1.
+template <int D>
+MARS_DEV void convert_raw(const uint8_t* raw, uint8_t* tile, const Info& f, int w) {
+  constexpr int kLanes = D / 16, kStep = 32 / kLanes, kIts = 2 * kPageSize / kStep;
+  const int lane = threadIdx.x & 31, c = lane % kLanes, r0 = 2 * w * kPageSize + lane / kLanes;
+  const int count = f.count;
+  uint4 x[kIts];
+#pragma unroll
+  for (int i = 0; i < kIts; ++i) {
+    const int r = r0 + i * kStep;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (r < count && f.page[r / kPageSize] >= 0)
+      x[i] = *reinterpret_cast<const uint4*>(raw + r * D + c * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < kIts; ++i) {
+    const int r = r0 + i * kStep;
+    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = q8::decode2((in[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+    // lanes of the second region store their chunks in the other order: the eight lanes of a row
+    // then hit eight different chunks
+    const int up = D == 128 ? c >> 2 : 0;
+    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+    *reinterpret_cast<uint4*>(chunk_at(tile, r, 2 * c + up)) = up ? hi : lo;
+    *reinterpret_cast<uint4*>(chunk_at(tile, r, 2 * c + 1 - up)) = up ? lo : hi;
+  }
+}
+
+// The same share of a tile of the sequence's own rows: each group over a power of two of its own,
+// its largest finite magnitude in [2^8, 2^9).
+template <int D>
+MARS_DEV void convert_own(const uint16_t* __restrict__ rows, long long stride, uint8_t* tile,
+                          int count, uint8_t* bytes, int w) {
+  constexpr int kChunks = D / 8, kStep = 32 / kChunks, kIts = kPageSize / kStep;
+  const int lane = threadIdx.x & 31, c = lane % kChunks;
+#pragma unroll 1
+  for (int g = 2 * w; g < 2 * w + 2; ++g) {
+    const int r0 = g * kPageSize + lane / kChunks;
+    uint4 x[kIts];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kIts; ++i) {
+      const int r = r0 + i * kStep;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (r < count) x[i] = *reinterpret_cast<const uint4*>(rows + r * stride + c * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kIts; ++i) {
+      const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t m = v[e] & 0x7fff7fffu;
+        top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+    const int byte = min(max((int)(top >> 7) - 8, q8::kLeast), kOwnMost);
+    if (lane == 0) bytes[g] = (uint8_t)byte;
+    const float f = q8::inverse_power(byte);
+#pragma unroll
+    for (int i = 0; i < kIts; ++i) {
+      float e[8];
+      unpack8(x[i], e);
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = q8::pack_f16x2(e[2 * k] * f, e[2 * k + 1] * f);
+      *reinterpret_cast<uint4*>(chunk_at(tile, r0 + i * kStep, c)) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+
+// Warps 8 ..: f16 tiles of K and V.
+template <int D>
+MARS_DEV void convert(const Pipe& p) {
+  using namespace sm100;
+  using L = Layout<D>;
+  const Args& a = p.a;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kConvertWarp;
+  static_assert(kConvertWarps * 2 == kPagesPerTile, "two groups a warp");
+  int c = 0;
+  for (int t = 0;; ++t) {
+    if (!p.warp_wait_info(t)) break;
+    Info& f = p.info(t);
+    const int flags = f.flags;
+    if (flags & kEnd) break;
+    bool ok = true;
+    for (int h = 0; h < 2; ++h) {
+      const int st = c % kRaw, ts = t % kTiles;
+      const bool own = flags & kOwn;
+      if (!own && !(ok = p.warp_wait(&p.bar.raw_full[st], (c / kRaw) & 1))) break;
+      if (!(ok = p.warp_wait(&p.bar.f_empty[h][ts], ((t / kTiles) & 1) ^ 1))) break;
+      uint8_t* tile = L::tile(p.smem, h, t);
+      if (own) {
+        const long long stride = h ? a.v_stride : a.k_stride;
+        convert_own<D>((h ? a.v : a.k) + ((size_t)f.base + f.k0) * stride + f.kvh * D, stride, tile,
+                       f.count, h ? f.v_byte : f.k_byte, w);
+      } else {
+        convert_raw<D>(p.smem + L::OFF_RAW + st * L::RAW, tile, f, w);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p.bar.raw_empty[st]);
+        ++c;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p.bar.f_full[h][ts]);
+    }
+    if (!ok) break;
+    p.warp_done(t);
+  }
+}
+
+// One thread: S_t = Q K_t^T.
+template <int D>
+MARS_DEV void issue_s(const Pipe& p) {
+  using namespace sm100;
+  using L = Layout<D>;
+  const uint32_t idesc = idesc_f16_f32(BQ, BKV, false);
+  const uint64_t qd = sdesc_sw128(smem_u32(p.smem + L::OFF_Q), 16, 1024);
+  for (int t = 0, items = 0; p.wait_info(t); ++t) {
+    const int flags = p.info(t).flags;
+    if (flags & kEnd) break;
+    mbar_arrive(&p.bar.info_empty[t % kInfos]);
+    const int sb = t % kBufs;
+    if ((flags & kFirst) && !p.wait(&p.bar.q_full, items++ & 1)) break;
+    if (!p.wait(&p.bar.f_full[0][t % kTiles], (t / kTiles) & 1)) break;
+    // S buffer sb last held tile t - kBufs, whose P the PV of that tile read from it
+    if (t >= kBufs && !p.wait(&p.bar.pv_done[sb], (t / kBufs - 1) & 1)) break;
+    tc_fence_after();
+    const uint64_t kd = sdesc_sw128(smem_u32(L::tile(p.smem, 0, t)), 16, 1024);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t off = (k >> 2) * (BQ * 128) + (k & 3) * 32;
+      mma_bf16_ss(p.tmem + L::TM_S + sb * BKV, sdesc_advance(qd, off), sdesc_advance(kd, off), idesc,
+                  k != 0);
+    }
+    mma_commit(&p.bar.s_full[sb]);
+    mma_commit(&p.bar.f_empty[0][t % kTiles]);
+  }
+  mma_commit(&p.bar.drain[0]);
+  mbar_wait(&p.bar.drain[0], 0, nullptr, p.a.status);
+}
+
+// One thread: O += P'_t V_t.
+template <int D>
+MARS_DEV void issue_pv(const Pipe& p) {
+  using namespace sm100;
+  using L = Layout<D>;
+  const uint32_t idesc = idesc_f16_f32(BQ, D, true);
+  for (int t = 0; p.wait_info(t); ++t) {
+    const int flags = p.info(t).flags;
+    if (flags & kEnd) break;
+    mbar_arrive(&p.bar.info_empty[t % kInfos]);
+    const int pb = t % kBufs;
+    if (!p.wait(&p.bar.f_full[1][t % kTiles], (t / kTiles) & 1)) break;
+    if (!p.wait(&p.bar.p_full[pb], (t / kBufs) & 1)) break;
+    tc_fence_after();
+    const uint64_t vd = sdesc_sw128(smem_u32(L::tile(p.smem, 1, t)), BKV * 128, 1024);
+#pragma unroll
+    for (int k = 0; k < BKV / 16; ++k)
+      mma_bf16_ts(p.tmem + L::TM_O, p.tmem + L::TM_S + pb * BKV + L::P_OFF + k * 8,
+                  sdesc_advance(vd, k * 2048), idesc, k != 0 || !(flags & kFirst));
+    mma_commit(&p.bar.pv_done[pb]);
+    mma_commit(&p.bar.f_empty[1][t % kTiles]);
+  }
+  mma_commit(&p.bar.drain[1]);
+  mbar_wait(&p.bar.drain[1], 0, nullptr, p.a.status);
+}
+
+// This thread's query row of the item that tile t begins, as f16 into Q; returns the factor of its
+// scores. A row without a token is zero.
+template <int D>
+MARS_DEV float load_q(const Pipe& p, int t, int row) {
+  using L = Layout<D>;
+  const Args& a = p.a;
+  const Info& f = p.info(t);
+  const int tok = f.tok0 + row / a.gp, h = f.h0 + row % a.gp;
+  const bool has = row < a.gp * a.tpt && tok < f.n;
+  uint4 x[D / 8];
+  const uint16_t* src = a.q + ((size_t)f.base + tok) * a.q_stride + (size_t)h * D;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c)
+    x[c] = has ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t m = v[e] & 0x7fff7fffu;
+      top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+    }
+  }
+  top = max(top >> 16, top & 0xffffu);
+  // exponent of the row's largest finite magnitude (rows of next to nothing: 2^-60)
+  const int byte = top ? min(max((int)(top >> 7), 67), 253) : 127;
+  const float inv = q8::inverse_power(byte);
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    float e[8];
+    unpack8(x[c], e);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = q8::pack_f16x2(e[2 * k] * inv, e[2 * k + 1] * inv);
+    *reinterpret_cast<uint4*>(chunk_at(p.smem + L::OFF_Q, row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  sm100::fence_proxy_async_smem();
+  sm100::mbar_arrive_warp(&p.bar.q_full);
+  return a.scale_log2 * q8::power(byte);
+}
+
+// lse-like statistics of a row: l is 0 where every score is -infinity (O is then 0), NaN where one
+// is NaN or +infinity.
+MARS_DEV float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+// Warps 4..7: softmax and output; thread = row.
+template <int D>
+MARS_DEV void softmax(const Pipe& p) {
+  using namespace sm100;
+  using L = Layout<D>;
+  const Args& a = p.a;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
+  const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+  const uint32_t o_addr = p.tmem + L::TM_O + lane_off;
+  if (!p.warp_wait_info(0) || (p.info(0).flags & kEnd)) return;
+  float factor = load_q<D>(p, 0, row);
+  float m = -INFINITY, l = 0.f;
+  int tok = 0;
+  bool has = false, busy = false;
+  for (int t = 0;; ++t) {
+    if (!p.warp_wait_info(t)) return;
+    const Info& f = p.info(t);
+    const int flags = f.flags;
+    if (flags & kEnd) return;
+    if (flags & kFirst) {
+      m = -INFINITY;
+      l = 0.f;
+      tok = f.tok0 + row / a.gp;
+      has = row < a.gp * a.tpt && tok < f.n;
+      busy = __any_sync(0xffffffffu, has);       // a warp without rows only keeps step
+    }
+    const int sb = t % kBufs;
+    // the converters have left the scales of own rows
+    if ((flags & kOwn) && !p.warp_wait(&p.bar.f_full[1][t % kTiles], (t / kTiles) & 1)) return;
+    const int limit = (flags & kOwn) ? min(f.count, tok + 1 - f.k0) : f.count;
+    const uint2 kb = *reinterpret_cast<const uint2*>(f.k_byte);
+    const uint2 vb = *reinterpret_cast<const uint2*>(f.v_byte);
+    if (!p.warp_wait(&p.bar.s_full[sb], (t / kBufs) & 1)) return;
+    tc_fence_after();
+    if (busy) {
+      const uint32_t s_addr = p.tmem + L::TM_S + sb * BKV + lane_off;
+      uint32_t r[BKV];
+#pragma unroll
+      for (int c = 0; c < BKV / 32; ++c)
+        tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
+      tmem_ld_wait();
+      if (__any_sync(0xffffffffu, limit < BKV)) {
+#pragma unroll
+        for (int e = 0; e < BKV; ++e)
+          if (e >= limit) r[e] = 0xff800000u;
+      }
+      // factor of the scores of 16 keys (never 0 or infinite: it meets infinite scores), and their
+      // exponent of V
+      auto mul_of = [&](int g) {
+        const int b = ((g < 4 ? kb.x : kb.y) >> (8 * (g & 3))) & 255;
+        return fminf(fmaxf(factor * q8::power(b), 1e-38f), 3e38f);
+      };
+      auto byte_of = [&](int g) { return (int)(((g < 4 ? vb.x : vb.y) >> (8 * (g & 3))) & 255); };
+      auto add_of = [&](int g) { return byte_of(g) ? (float)(byte_of(g) - q8::kBias) : -INFINITY; };
+      float top = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < kPagesPerTile; ++g) {
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[16 * g + e]);
+        const float y = flash::max3f(flash::max3f(x[0], x[1], x[2]), flash::max3f(x[3], x[4], x[5]),
+                                     flash::max3f(x[6], x[7], x[8]));
+        const float z = flash::max3f(flash::max3f(x[9], x[10], x[11]), flash::max3f(x[12], x[13], x[14]), x[15]);
+        top = fmaxf(top, fmaf(fmaxf(y, z), mul_of(g), add_of(g)));
+      }
+      // lazy rescale (flash_tc.cuh)
+      const bool raise = top > m + flash::kRescaleLog2;
+      const bool rescale = raise && m != -INFINITY;
+      if (__any_sync(0xffffffffu, rescale)) {
+        if (!p.warp_wait(&p.bar.pv_done[(t - 1) % kBufs], ((t - 1) / kBufs) & 1)) return;
+        tc_fence_after();
+        const float alpha = rescale ? flash::ex2_approx(m - top) : 1.f;
+        l *= alpha;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(o_addr + c * 32, o);
+        }
+        tmem_st_wait();
+      }
+      if (raise) m = top;
+      const float shift = kLift - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t packed[32];
+#pragma unroll
+        for (int g = 4 * h; g < 4 * h + 4; ++g) {
+          const float mul = mul_of(g), add = add_of(g) + shift;
+          const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
+          float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[16 * g + e]),
+                                                    __uint_as_float(r[16 * g + e + 1])), mul2, add2);
+            const float2 w = make_float2(flash::ex2_approx(x.x), flash::ex2_approx(x.y));
+            packed[(g & 3) * 8 + e / 2] = q8::pack_f16x2(w.x, w.y);
+            acc = __fadd2_rn(acc, w);
+          }
+          l = fmaf(acc.x + acc.y, byte_of(g) ? q8::inverse_power(byte_of(g)) : 1.f, l);
+        }
+        tmem_st32(s_addr + L::P_OFF + 32 * h, packed);
+      }
+      tmem_st_wait();
+    }
+    const bool last = flags & kLast;
+    const int slot = f.slot, base = f.base, h0 = f.h0;
+    tc_fence_before();
+    mbar_arrive_warp(&p.bar.p_full[sb]);
+    p.warp_done(t);
+    if (!last) continue;
+    // every S of the item is done: Q of the next one, then this one's O
+    if (!p.warp_wait_info(t + 1)) return;
+    if (!(p.info(t + 1).flags & kEnd)) factor = load_q<D>(p, t + 1, row);
+    if (!p.warp_wait(&p.bar.pv_done[sb], (t / kBufs) & 1)) return;
+    tc_fence_after();
+    if (!busy) continue;
+    if (slot < 0) {
+      const float inv = reciprocal(l);
+      const long long at =
+          has ? (((long long)base + tok) * a.hq + h0 + row % a.gp) * D : -1;
+#pragma unroll 1
+      for (int c = 0; c < D / 64; ++c) {
+        float o[64];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          tmem_ld32(o_addr + c * 64 + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(o + 32 * k));
+        tmem_ld_wait();
+        packed::store_rows<64>(a.o + c * 64, at, lane, [&](int e) { return o[e] * inv; });
+      }
+    } else {
+      float4* rec = a.part + ((size_t)blockIdx.x * 2 + slot) * L::PART;
+      if (has) reinterpret_cast<float2*>(rec + BQ * D / 4)[row] = make_float2(m, l);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + c * 32, o);
+        tmem_ld_wait();
+        if (has) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            rec[(c * 8 + e / 4) * BQ + row] =
+                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                            __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+        }
+      }
+    }
+    tc_fence_before();
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Args a) {
+  using namespace sm100;
+  using L = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bar bar;
+  __shared__ Info infos[kInfos];
+  __shared__ Scan scan;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    bar.abort = 0;
+    for (int i = 0; i < kInfos; ++i) {
+      mbar_init(&bar.info_full[i], 1);
+      // loader, both issuers, the converters' warps, the softmax's
+      mbar_init(&bar.info_empty[i], 3 + kConvertWarps + 4);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&bar.raw_full[i], 1);
+      mbar_init(&bar.raw_empty[i], kConvertWarps);
+    }
+    for (int h = 0; h < 2; ++h) {
+      for (int i = 0; i < kTiles; ++i) {
+        mbar_init(&bar.f_full[h][i], kConvertWarps);
+        mbar_init(&bar.f_empty[h][i], 1);
+      }
+      mbar_init(&bar.drain[h], 1);
+    }
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 128);
+      mbar_init(&bar.pv_done[i], 1);
+    }
+    mbar_init(&bar.q_full, 128);
+    fence_barrier_init();
+  }
+  find_part(a, scan);
+  if ((long long)blockIdx.x >= scan.ctas) {
+    if (threadIdx.x == 0 && a.rec) a.rec[blockIdx.x] = Record{};
+    return;
+  }
+  if (warp == 2) {
+    tmem_alloc(&bar.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Pipe p{a, bar, infos, smem, __shfl_sync(0xffffffffu, bar.tmem_base, 0)};
+  if (warp < kSoftmaxWarp) {
+    regs_lower<kControlRegs>();
+    if (warp == 0) {
+      walk<D>(p, scan);
+    } else if (warp == 1) {
+      load_raw<D>(p);
+    } else if (elect_one()) {
+      if (warp == 2) issue_s<D>(p); else issue_pv<D>(p);
+    }
+  } else if (warp < kConvertWarp) {
+    regs_raise<kSoftmaxRegs>();
+    softmax<D>(p);
+  } else {
+    regs_raise<kConvertRegs>();
+    convert<D>(p);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(p.tmem, 512);
+  }
+}
+
+// Joins the parts of divided items. Block (x, y): the item that CTA x begins and does not end, a
+// thread per (row, four columns).
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(Args a, int ctas) {
+  constexpr int PART = Layout<D>::PART;
+  const int x = blockIdx.x, lane = threadIdx.x & 31;
+  const Record rec = a.rec[x];
+  if (!rec.begins) return;
+  const int rows = rec.tokens * a.gp;
+  // its parts: CTA x's, those that lie inside it, and the one that ends it
+  int parts = 2;
+  for (int c = x + 1;; c += 32) {
+    const bool inside = c + lane < ctas && a.rec[c + lane].inside;
+    const uint32_t out = __ballot_sync(0xffffffffu, !inside);
+    parts += out ? __ffs(out) - 1 : 32;
+    if (out) break;
+  }
+  const float4* first = a.part + ((size_t)x * 2 + 1) * PART;
+  auto part = [&](int k) { return k == 0 ? first : a.part + (size_t)(x + k) * 2 * PART; };
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += gridDim.y * 256) {
+    const int row = i % rows, c = i / rows;
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k)
+      m = fmaxf(m, reinterpret_cast<const float2*>(part(k) + BQ * D / 4)[row].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float2 ml = reinterpret_cast<const float2*>(part(k) + BQ * D / 4)[row];
+      if (ml.y == kNoKeys) continue;
+      const float4 v = part(k)[c * BQ + row];
+      const float w = ml.x > -INFINITY ? exp2f(ml.x - m) : 0.f;     // m = +infinity gives NaN
+      l = fmaf(ml.y, w, l);
+      o = make_float4(fmaf(v.x, w, o.x), fmaf(v.y, w, o.y), fmaf(v.z, w, o.z), fmaf(v.w, w, o.w));
+    }
+    const float inv = reciprocal(l);
+    const size_t tok = (size_t)rec.base + rec.tok0 + row / a.gp;
+    uint32_t* to = reinterpret_cast<uint32_t*>(a.o + (tok * a.hq + rec.h0 + row % a.gp) * D + 4 * c);
+    to[0] = flash::pack_bf16x2(o.x * inv, o.y * inv);
+    to[1] = flash::pack_bf16x2(o.z * inv, o.w * inv);
+  }
+}
+
+// ------------------------------------------------------------------------------ the wide form
+//
+// Where the rows are many, a sequence's pages are written out in bf16 (exact too), once, and
+// attended to by packed_attn.cu, whose CTAs would otherwise each convert them again.
 
 struct UnpackArgs {
   const int32_t *cu, *seq_lens, *block_table;
   const uint8_t *k_pool, *v_pool, *k_scale, *v_scale;
   uint16_t *k_out, *v_out;
   int32_t *lens, *table, *status;
-  int num_pages, max_pages, pages, batch, total, hkv;
+  int num_pages, max_pages, pages, tpt, batch, total, hkv;
 };
+constexpr int kUnpackThreads = 256;
 
 // A CTA writes one page of a sequence out: page j of sequence s becomes page s * pages + j.
+// Sequences that chunk_kernel takes get no keys here; what the wide kernels then make of their
+// rows is written over.
 template <int D>
-__global__ void __launch_bounds__(kThreads) unpack_kernel(UnpackArgs a) {
-  const int s = blockIdx.x / a.pages, j = blockIdx.x % a.pages;
-  const int len = a.seq_lens[s];
-  const int P = (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize));
-  if (j == 0 && threadIdx.x == 0) {
-    a.lens[s] = min(P, a.pages * kPageSize);
-    if (a.status && P != len) atomicOr(a.status, MARS_ST_OVERFLOW);
-  }
-  if (j * kPageSize >= P) return;
-  const int page = a.block_table[(size_t)s * a.max_pages + j];
+__global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(UnpackArgs a) {
+  auto cut = [&](int len) { return (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize)); };
+  bool bad;
+  const packed::Seq sq = packed::find_tile_by(
+      a.cu, a.batch, a.total, (long long)blockIdx.x, bad, a.seq_lens, [&](int, int n, int len) {
+        const int P = cut(len);
+        return left_out(a.pages, a.tpt, n, P) ? max(1, (P + kPageSize - 1) / kPageSize) : 1;
+      });
+  if (sq.s < 0) return;
+  const int P = left_out(a.pages, a.tpt, sq.n, cut(sq.len)) ? cut(sq.len) : 0;
+  if (sq.tile == 0 && threadIdx.x == 0) a.lens[sq.s] = P;
+  if (sq.tile * kPageSize >= P) return;
+  const int page = a.block_table[(size_t)sq.s * a.max_pages + sq.tile];
   const bool mapped = page >= 0 && page < a.num_pages;
-  if (threadIdx.x == 0) a.table[(size_t)s * a.pages + j] = mapped ? (int)blockIdx.x : -1;
+  const size_t out_page = (size_t)sq.s * a.pages + sq.tile;
+  if (threadIdx.x == 0) a.table[out_page] = mapped ? (int)out_page : -1;
   if (!mapped) return;
   constexpr int kVectors = kPageSize * D / 16;     // of 16 codes, per head
-  for (int i = threadIdx.x; i < 2 * a.hkv * kVectors; i += kThreads) {
+  for (int i = threadIdx.x; i < 2 * a.hkv * kVectors; i += kUnpackThreads) {
     const int w = i / kVectors, c = i - w * kVectors;
     const bool is_v = w >= a.hkv;
     const int h = is_v ? w - a.hkv : w;
-    const size_t at = (size_t)page * a.hkv + h, to = (size_t)blockIdx.x * a.hkv + h;
+    const size_t at = (size_t)page * a.hkv + h, to = out_page * a.hkv + h;
     const uint4 x = reinterpret_cast<const uint4*>((is_v ? a.v_pool : a.k_pool) + at * (kPageSize * D))[c];
     const float f = q8::power(q8::scale_byte((is_v ? a.v_scale : a.k_scale)[at]));
     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
@@ -49,8 +1026,7 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(UnpackArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float2 v = q8::decode2_f32((in[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v.x * f, v.y * f);
-      out[e] = *reinterpret_cast<const uint32_t*>(&b);
+      out[e] = flash::pack_bf16x2(v.x * f, v.y * f);
     }
     uint4* dst = reinterpret_cast<uint4*>((is_v ? a.v_out : a.k_out) + to * (kPageSize * D)) + 2 * c;
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
@@ -58,18 +1034,94 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(UnpackArgs a) {
   }
 }
 
-// Parts of the workspace, in bytes from its start.
-struct Layout {
-  size_t lens, table, k, v, end;
+// Parts of the workspace, in bytes from its start: the wide form's, then chunk_kernel's.
+struct Places {
+  size_t lens, table, k, v, rec, part, end;
 };
-Layout layout(const ChunkQ8Plan& plan, int batch, int hkv, int d) {
-  Layout l;
-  l.lens = packed::align256(plan.wide.ws_bytes);
-  l.table = l.lens + packed::align256((size_t)batch * sizeof(int32_t));
-  l.k = l.table + packed::align256((size_t)batch * plan.pages * sizeof(int32_t));
-  l.v = l.k + (size_t)batch * plan.pages * hkv * kPageSize * d * 2;
-  l.end = l.v + (l.v - l.k);
+Places places(const ChunkQ8Plan& plan, int batch, int hkv, int d) {
+  Places l{};
+  if (plan.pages) {
+    l.lens = packed::align256(plan.wide.ws_bytes);
+    l.table = l.lens + packed::align256((size_t)batch * sizeof(int32_t));
+    l.k = l.table + packed::align256((size_t)batch * plan.pages * sizeof(int32_t));
+    l.v = l.k + (size_t)batch * plan.pages * hkv * kPageSize * d * 2;
+    l.rec = l.v + (l.v - l.k);
+  }
+  l.part = l.end = l.rec;
+  if (plan.can_split) {
+    l.part = l.rec + packed::align256(plan.ctas * sizeof(Record));
+    l.end = l.part + (size_t)plan.ctas * 2 * (BQ * (size_t)d + 2 * BQ) * sizeof(float);
+  }
   return l;
+}
+
+template <int D>
+cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaStream_t stream) {
+  const PackedAttn& t = p.attn;
+  const Places l = places(plan, t.batch, t.hkv, D);
+  if (plan.pages) {
+    UnpackArgs u{t.cu, t.seq_lens, t.block_table, p.k_pool, p.v_pool, p.k_scale, p.v_scale,
+                 reinterpret_cast<uint16_t*>(ws + l.k), reinterpret_cast<uint16_t*>(ws + l.v),
+                 reinterpret_cast<int32_t*>(ws + l.lens), reinterpret_cast<int32_t*>(ws + l.table),
+                 t.status, t.num_pages, t.max_pages, plan.pages, plan.tpt, t.batch, t.total, t.hkv};
+    unpack_kernel<D><<<(unsigned)((long long)t.batch * plan.pages), kUnpackThreads, 0, stream>>>(u);
+    count_launches(1);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    PackedAttn wide = t;
+    wide.k_pool = u.k_out;
+    wide.v_pool = u.v_out;
+    wide.seq_lens = u.lens;
+    wide.block_table = u.table;
+    wide.num_pages = t.batch * plan.pages;
+    wide.max_pages = plan.pages;
+    e = launch_packed_attn(wide, plan.wide, ws, stream);
+    if (e != cudaSuccess) return e;
+  }
+  Args a{};
+  a.q = t.q;
+  a.k = t.k;
+  a.v = t.v;
+  a.q_stride = t.q_stride;
+  a.k_stride = t.k_stride;
+  a.v_stride = t.v_stride;
+  a.cu = t.cu;
+  a.seq_lens = t.seq_lens;
+  a.block_table = t.block_table;
+  a.k_pool = p.k_pool;
+  a.v_pool = p.v_pool;
+  a.k_scale = p.k_scale;
+  a.v_scale = p.v_scale;
+  a.num_pages = t.num_pages;
+  a.max_pages = t.max_pages;
+  a.batch = t.batch;
+  a.total = t.total;
+  a.hq = t.hq;
+  a.hkv = t.hkv;
+  a.gp = plan.gp;
+  a.tpt = plan.tpt;
+  a.heads = t.hq / plan.gp;
+  a.can_split = plan.can_split;
+  a.skip_pages = plan.pages ? plan.pages : -1;
+  a.scale_log2 = t.scale * 1.4426950408889634f;
+  a.o = t.o;
+  a.rec = plan.can_split ? reinterpret_cast<Record*>(ws + l.rec) : nullptr;
+  a.part = plan.can_split ? reinterpret_cast<float4*>(ws + l.part) : nullptr;
+  a.status = t.status;
+  using L = Layout<D>;
+  static_assert(L::TOTAL + sizeof(Bar) + kInfos * sizeof(Info) + sizeof(Scan) + 256 <= 227 * 1024,
+                "layout fits shared memory");
+  static std::atomic<int> attr[64];
+  cudaError_t e = set_smem_limit_once(chunk_kernel<D>, L::TOTAL, attr);
+  if (e != cudaSuccess) return e;
+  chunk_kernel<D><<<plan.ctas, kThreads, L::TOTAL, stream>>>(a);
+  count_launches(1);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !plan.can_split) return e;
+  const int rows = std::min(plan.gp * std::min(plan.tpt, t.total), BQ);
+  merge_kernel<D><<<dim3(plan.ctas, (rows * (D / 4) + 255) / 256), 256, 0, stream>>>(a, plan.ctas);
+  count_launches(1);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -77,36 +1129,26 @@ Layout layout(const ChunkQ8Plan& plan, int batch, int hkv, int d) {
 ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_len) {
   ChunkQ8Plan p{};
   p.wide = plan_packed(batch, total, hq, hkv, d, max_len);
-  p.pages = std::max(1, max_len / kPageSize + (max_len % kPageSize != 0));
-  p.ws_bytes = layout(p, batch, hkv, d).end;
+  p.gp = p.wide.gp;
+  p.tpt = p.wide.tpt;
+  // The wide form where packed_attn.cu would take pairs of row tiles (plan_packed), unless its pages
+  // could not be counted or took more than 4 GB.
+  const long long pages = std::max(1, max_len / kPageSize + (max_len % kPageSize != 0));
+  const long long rows = pages * batch * hkv * kPageSize;
+  if (p.wide.pair && rows <= INT_MAX && rows * d * 4 <= 1LL << 32) p.pages = (int)pages;
+  // CTAs: as many as the items and their parts can keep busy, by the hint
+  const int tiles = packed::key_tiles(max_len) + 1;
+  const long long items = packed::max_tiles(batch, total, p.tpt) * (hq / p.gp);
+  p.can_split = tiles >= 2 * kMinPart;
+  p.ctas = (int)std::min<long long>(num_sms(), items * std::max(1, tiles / kMinPart));
+  p.ws_bytes = places(p, batch, hkv, d).end;
   return p;
 }
 
 cudaError_t launch_chunk_q8(const ChunkQ8& p, const ChunkQ8Plan& plan, void* workspace,
                             cudaStream_t stream) {
-  const PackedAttn& t = p.attn;
-  const Layout l = layout(plan, t.batch, t.hkv, t.d);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  UnpackArgs a{t.cu, t.seq_lens, t.block_table, p.k_pool, p.v_pool, p.k_scale, p.v_scale,
-               reinterpret_cast<uint16_t*>(ws + l.k), reinterpret_cast<uint16_t*>(ws + l.v),
-               reinterpret_cast<int32_t*>(ws + l.lens), reinterpret_cast<int32_t*>(ws + l.table),
-               t.status, t.num_pages, t.max_pages, plan.pages, t.batch, t.total, t.hkv};
-  const unsigned ctas = (unsigned)((long long)t.batch * plan.pages);
-  if (t.d == 64)
-    unpack_kernel<64><<<ctas, kThreads, 0, stream>>>(a);
-  else
-    unpack_kernel<128><<<ctas, kThreads, 0, stream>>>(a);
-  count_launches(1);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  PackedAttn wide = t;
-  wide.k_pool = a.k_out;
-  wide.v_pool = a.v_out;
-  wide.seq_lens = a.lens;
-  wide.block_table = a.table;
-  wide.num_pages = t.batch * plan.pages;
-  wide.max_pages = plan.pages;
-  return launch_packed_attn(wide, plan.wide, workspace, stream);
+  return p.attn.d == 64 ? launch<64>(p, plan, ws, stream) : launch<128>(p, plan, ws, stream);
 }
 
 }  // namespace mars

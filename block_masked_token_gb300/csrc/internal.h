@@ -200,8 +200,11 @@ struct ChunkQ8 {
   const uint8_t *k_pool, *v_pool, *k_scale, *v_scale;
 };
 struct ChunkQ8Plan {
-  PackedPlan wide;                      // over the pages in bf16
-  int pages;                            // pages per sequence that the workspace has room for
+  int gp, tpt;             // heads and tokens of a row tile
+  int ctas;
+  bool can_split;          // items may be divided among CTAs
+  int pages;               // the wide form's pages per sequence (0: without it)
+  PackedPlan wide;
   size_t ws_bytes;
 };
 ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_len);

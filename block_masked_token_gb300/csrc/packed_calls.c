@@ -250,7 +250,7 @@ static PyObject* rotary(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (n != 11 || !p_rotary || !PyBool_Check(a[7]) || !PyFloat_Check(a[8]) || !PyBool_Check(a[9]) ||
       !target(a[0], &dev, &stream) || !rows(a[0], dev, &total, &hq, &d, &q, &qs) ||
       !rows(a[1], dev, &total, &hkv, &d, &k, &ks) || !boundaries(a[2], dev, &batch, &cu) ||
-      !flat(a[3], d_f32, dev, 1, &half, &freq) || half > d ||
+      !flat(a[3], d_f32, dev, 1, &half, &freq) || half > d / 2 ||
       !rows(a[4], dev, &total, &hq, &d, &qo, &qos) ||
       !rows(a[5], dev, &total, &hkv, &d, &ko, &kos) ||
       !flat_or_none(a[6], d_i32, dev, 1, &batch, &lens) ||

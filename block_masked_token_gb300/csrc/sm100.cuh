@@ -428,6 +428,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_ma
          | ((uint32_t)(M >> 4) << 24);           // M / 16
 }
 
+// The same with f16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
 // 128-byte swizzle as TMA applies it: the 16-byte chunk index (address bits 4..6) is
 // XORed with the 128-byte row index within the 1024-byte atom (bits 7..9). Used when a
 // kernel writes an operand tile into shared memory itself.

@@ -615,3 +615,86 @@ def kv_append(k, v, cu, seq_lens, block_table, k_pool, v_pool, page_size: int):
             slots[a + i] = page * page_size + p % page_size
             lens[s] += 1
     return kp, vp, lens, slots
+
+
+# ------------------------------------------------------------------- rotary positions
+
+
+def rotary(x, cu, seq_lens, inv_freq, interleaved: bool = False, factor: float = 1.0,
+           inverse: bool = False):
+    """x [n, H, D] with pair j of the first 2 len(inv_freq) elements of each head turned by
+    (seq_lens[s] + i) inv_freq[j] radians and multiplied by factor."""
+    y, half = np.array(x, dtype=np.float64), len(inv_freq)
+    first = np.arange(0, 2 * half, 2) if interleaved else np.arange(half)
+    second = first + (1 if interleaved else half)
+    for s, a, b in _packed_rows(cu):
+        t = np.outer(int(seq_lens[s]) + np.arange(b - a), np.asarray(inv_freq, dtype=np.float64))
+        c, d = factor * np.cos(t)[:, None], factor * np.sin(t)[:, None] * (-1 if inverse else 1)
+        u, v = x[a:b][..., first], x[a:b][..., second]
+        y[a:b][..., first], y[a:b][..., second] = u * c - v * d, u * d + v * c
+    return y
+
+
+# ------------------------------------------------------------------- 8-bit paged cache
+
+Q8_TOP, Q8_BIAS, Q8_LEAST, Q8_MOST = 448.0, 127, 87, 167
+
+
+def e4m3(x):
+    """Nearest value with four significant bits and exponents from -6 on (a multiple of 2^-9
+    below them), ties to even, of magnitude at most 448; NaN for what is not finite."""
+    x = np.asarray(x, dtype=np.float64)
+    mag = np.where(np.isfinite(x), np.abs(x), 1.0)
+    step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(mag, 2.0 ** -9))), -6) - 3)
+    r = np.minimum(np.rint(mag / step) * step, Q8_TOP)
+    return np.where(np.isfinite(x), np.copysign(r, x), np.nan)
+
+
+def q8_scale(rows):
+    """Scale byte of rows that share one: the smallest power of two under which the largest
+    finite magnitude is at most 448."""
+    mag = np.abs(rows[np.isfinite(rows)])
+    top = mag.max() if mag.size else 0.0
+    for byte in range(Q8_LEAST, Q8_MOST):
+        if top <= Q8_TOP * 2.0 ** (byte - Q8_BIAS):
+            return byte
+    return Q8_MOST
+
+
+def q8_values(pool, scale):
+    """What a pool of codes [pages, hkv, page, D] and scale bytes [pages, hkv] stands for."""
+    e = np.clip(np.asarray(scale, dtype=np.int64), Q8_LEAST, Q8_MOST) - Q8_BIAS
+    return np.asarray(pool, dtype=np.float64) * np.exp2(e)[..., None, None]
+
+
+def kv_append_q8(k, v, cu, seq_lens, block_table, k_pool, v_pool, k_scale, v_scale,
+                 page_size: int, counts=None):
+    """kv_append of the first counts[s] rows into pools of codes (as values) and scale bytes.
+    Returns the pools, the scales, the new lengths and the slots."""
+    out = [np.array(k_pool, dtype=np.float64), np.array(v_pool, dtype=np.float64),
+           np.array(k_scale), np.array(v_scale)]
+    lens, slots = np.array(seq_lens, dtype=np.int64), np.full(k.shape[0], -1, dtype=np.int64)
+    for s, a, b in _packed_rows(cu):
+        P = int(seq_lens[s])
+        n = b - a if counts is None else min(max(int(counts[s]), 0), b - a)
+        pages = {}                                  # logical page: rows that fall on it
+        for i in range(n if P >= 0 else 0):
+            lp = (P + i) // page_size
+            if lp >= len(block_table[s]) or not 0 <= int(block_table[s][lp]) < len(out[0]):
+                break
+            pages.setdefault(lp, []).append(i)
+            lens[s] += 1
+            slots[a + i] = int(block_table[s][lp]) * page_size + (P + i) % page_size
+        for lp, rows in pages.items():
+            page, held = int(block_table[s][lp]), max(0, P - lp * page_size)
+            for x, pool, scale in ((k, out[0], out[2]), (v, out[1], out[3])):
+                for h in range(x.shape[1]):
+                    new = x[a + rows[0]:a + rows[-1] + 1, h]
+                    byte = q8_scale(new)
+                    if held:
+                        was = min(max(int(scale[page, h]), Q8_LEAST), Q8_MOST)
+                        byte = max(byte, was)
+                        pool[page, h, :held] = e4m3(pool[page, h, :held] * 2.0 ** (was - byte))
+                    pool[page, h, held:held + len(rows)] = e4m3(new * 2.0 ** (Q8_BIAS - byte))
+                    scale[page, h] = byte
+    return (*out, lens, slots)
