@@ -17,10 +17,14 @@
 //     large as what it contributes, whatever the pages' scales are; 2^7 P' is stored, so that small
 //     ones keep their bits.
 //
-// Roles (384 threads): warp 0 walks the items and reads block table and scales ahead of the others
-// (infos); warp 1 copies whole pages into a ring, 2 KB each; warps 8..11 turn raw tiles of K and V
-// into swizzled f16 tiles, zero where no key may be read; warps 2 and 3 issue S = Q K^T and O += P' V;
-// warps 4..7 run the softmax (thread = row), load Q and store O.
+// Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
+// (infos); warps 12..15 (K) and 16..19 (V) each copy two pages of every tile into a ring of their own
+// and turn them into 32 rows of a swizzled f16 tile, zero where no key may be read; warps 2 and 3 issue
+// S = Q K^T and O += P' V; warps 4..11 run the softmax, load Q and store O: a thread has a row, warps
+// 4..7 the first half of its keys and columns, 8..11 the second, and the two of a row exchange their
+// maxima and sums. What a warp runs per tile is kept short: with one warp per row, whose code for 128
+// keys no other shared, the code of all roles left the instruction cache within every tile, and a
+// tile took 5,000 cycles.
 //
 // A cut inside an item leaves partials (m', l, O) that merge_kernel joins in the order of the keys.
 #include <algorithm>
@@ -38,16 +42,21 @@ namespace {
 using flash::BKV;
 using flash::BQ;
 
-constexpr int kThreads = 384;
-constexpr int kSoftmaxWarp = 4, kConvertWarp = 8, kConvertWarps = 4;
-constexpr int kControlRegs = 80, kSoftmaxRegs = 232, kConvertRegs = 184;
-static_assert(128 * (kControlRegs + kSoftmaxRegs + kConvertRegs) <=
+constexpr int kThreads = 640;
+constexpr int kSoftmaxWarp = 4, kSoftmaxWarps = 8, kConvertWarp = 12, kConvertWarps = 8;
+constexpr int kControlRegs = 64, kSoftmaxRegs = 128, kConvertRegs = 80;
+static_assert(128 * (kControlRegs + 2 * kSoftmaxRegs + 2 * kConvertRegs) <=
                   kThreads * (65536 / kThreads / 8 * 8),
               "the register split fits the launch's register pool");
-constexpr int kRaw = 4;              // ring of raw tiles (K and V in turn)
+constexpr int kRaw = 2;              // ring of raw tiles
+constexpr int kAhead = 3;            // tiles that copies may be ahead of the conversion
 constexpr int kTiles = 2;            // f16 tiles of K, and of V
 constexpr int kBufs = 3;             // S buffers in TMEM
-constexpr int kInfos = 8;            // tiles that the walk may be ahead
+// Tiles that the walk may be ahead. It publishes up to four at once, the converters wait for up to
+// kAhead more than they have released, and with this many the slots that it then needs belong to
+// tiles that every converter has released.
+constexpr int kInfos = 8;
+static_assert(kInfos > kAhead + 4, "the walk and the converters do not wait for each other");
 constexpr int kPagesPerTile = BKV / kPageSize;
 constexpr int kMinPart = 4;          // key tiles of a part of a divided item
 constexpr long long kUnit = 8, kItemWork = 12;   // work of a key tile and of an item's start and end
@@ -260,20 +269,31 @@ struct alignas(16) Info {
 
 struct Bar {
   uint64_t info_full[kInfos], info_empty[kInfos];
-  uint64_t raw_full[kRaw], raw_empty[kRaw];
+  uint64_t raw_full[kConvertWarps][kRaw];              // of a warp's two pages
   uint64_t f_full[2][kTiles], f_empty[2][kTiles];      // K, V
   uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
   uint64_t q_full, drain[2];
+  uint64_t pair[4];                  // the two warps of 32 rows
   uint32_t tmem_base;
   int abort;
+  uint16_t exchange[2][2][BQ];       // [use][half][row]
 };
+
+// All that is not a tile. Its size keeps what follows, the tiles, aligned to 1024 bytes: they leave
+// no room for aligning them at run time.
+struct alignas(1024) Shared {
+  Bar bar;
+  Info infos[kInfos];
+  Scan scan;
+};
+static_assert(sizeof(Shared) == 3072, "with the tiles, all of the shared memory of a CTA");
 
 template <int D>
 struct Layout {
   static constexpr int RAW = BKV * D, TILE = BKV * D * 2, PAGE = kPageSize * D;
   static constexpr int OFF_Q = 0, OFF_F = TILE;                      // f16 tiles: K ring, V ring
   static constexpr int OFF_RAW = OFF_F + 2 * kTiles * TILE;
-  static constexpr int TOTAL = OFF_RAW + kRaw * RAW + 1024;          // + alignment slack
+  static constexpr int TOTAL = OFF_RAW + kRaw * 2 * RAW;
   static constexpr int TM_S = 0, TM_O = kBufs * BKV, P_OFF = BKV / 2;
   static constexpr int PART = BQ * D / 4 + BQ / 2;                   // float4 of a partial
   static MARS_DEV uint8_t* tile(uint8_t* smem, int is_v, int t) {
@@ -288,7 +308,8 @@ struct Pipe {
   uint8_t* smem;
   uint32_t tmem;
 
-  // waits of one thread, and of a whole warp
+  // waits of one thread, and of a whole warp (by all lanes: behind a test of the lane a wait that
+  // is over takes 250 cycles instead of 100)
   MARS_DEV bool wait(uint64_t* b, uint32_t parity) const {
     return sm100::mbar_wait(b, parity, &bar.abort, a.status);
   }
@@ -305,7 +326,11 @@ struct Pipe {
     uint64_t* b = info_full(t, p);
     return wait(b, p);
   }
-  MARS_DEV bool warp_wait_info(int t) const { return __all_sync(0xffffffffu, wait_info(t)); }
+  MARS_DEV bool warp_wait_info(int t) const {
+    uint32_t p;
+    uint64_t* b = info_full(t, p);
+    return warp_wait(b, p);
+  }
   MARS_DEV void warp_done(int t) const {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&bar.info_empty[t % kInfos]);
@@ -411,6 +436,17 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
         kb = (uint8_t)q8::scale_byte(a.k_scale[at]);
         vb = (uint8_t)q8::scale_byte(a.v_scale[at]);
       }
+      // The pages' lines are asked for here, to be in L2 when warp 1 copies them: a copy out of DRAM
+      // takes some 4,500 cycles, which the ring of raw tiles could not cover.
+      constexpr int kLines = Layout<D>::PAGE / 128;
+      const size_t from = ((size_t)max(e, 0) * a.hkv + kvh) * Layout<D>::PAGE;
+      const uint32_t pages = __ballot_sync(0xffffffffu, readable);
+#pragma unroll 1
+      for (uint32_t left_pages = pages; left_pages; left_pages &= left_pages - 1) {
+        const size_t at = __shfl_sync(0xffffffffu, from, __ffs(left_pages) - 1);
+        if (lane < 2 * kLines)
+          prefetch_l2((lane < kLines ? a.k_pool : a.v_pool) + at + (lane % kLines) * 128);
+      }
       if (!(ok = room(n))) break;
       if (lane < n * kPagesPerTile) {
         const int g = lane % kPagesPerTile, u = lane / kPagesPerTile;
@@ -436,171 +472,156 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
   if (flags && a.status) atomicOr(a.status, flags);
 }
 
-// Warp 1: raw tiles, K and V in turn, a copy per page.
-template <int D>
-MARS_DEV void load_raw(const Pipe& p) {
-  using namespace sm100;
-  using L = Layout<D>;
-  const Args& a = p.a;
-  const int lane = threadIdx.x & 31;
-  int last[kRaw];
-#pragma unroll
-  for (int i = 0; i < kRaw; ++i) last[i] = -1;
-  int c = 0;
-  for (int t = 0;; ++t) {
-    if (!p.warp_wait_info(t)) break;
-    const Info& f = p.info(t);
-    const int flags = f.flags;
-    if (flags & kEnd) break;
-    bool ok = true;
-    if (!(flags & kOwn)) {
-      const int page = lane < kPagesPerTile ? f.page[lane] : -1;
-      const int pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
-      const size_t at = ((size_t)max(page, 0) * a.hkv + f.kvh) * L::PAGE;
-#pragma unroll
-      for (int h = 0; h < 2; ++h, ++c) {
-        const int st = c % kRaw;
-        int good = 1;
-        if (lane == 0) {
-          good = p.wait(&p.bar.raw_empty[st], ((c / kRaw) & 1) ^ 1);
-          if (good) mbar_arrive_expect_tx(&p.bar.raw_full[st], pages * L::PAGE);
-        }
-        if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
-        if (page >= 0)
-          bulk_load(p.smem + L::OFF_RAW + st * L::RAW + lane * L::PAGE, (h ? a.v_pool : a.k_pool) + at,
-                    L::PAGE, &p.bar.raw_full[st]);
-#pragma unroll
-        for (int i = 0; i < kRaw; ++i)
-          if (i == st) last[i] = c;
-      }
-    }
-    if (!ok) break;
-    p.warp_done(t);
-  }
-  // no copy is in flight when the CTA ends
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < kRaw; ++i)
-      if (last[i] >= 0) mbar_wait(&p.bar.raw_full[i], (last[i] / kRaw) & 1, nullptr, a.status);
-  __syncwarp();
-}
-
 // 16 bytes of an f16 tile: chunk c (8 elements) of row r. Regions of 64 elements, 128-byte swizzle.
 MARS_DEV uint8_t* chunk_at(uint8_t* tile, int r, int c) {
   return tile + (c >> 3) * (BKV * 128) + flash::sw_off(r, c & 7);
 }
 
-// One converter warp's share of a raw tile: 16-token groups 2w and 2w + 1.
+// Two raw pages as rows r0 .. r0 + 31 of an f16 tile; of each only the first valid[i] rows, zero
+// for the others.
 template <int D>
-MARS_DEV void convert_raw(const uint8_t* raw, uint8_t* tile, const Info& f, int w) {
+MARS_DEV void convert_raw(const uint8_t* raw, uint8_t* tile, int r0, int valid0, int valid1) {
   constexpr int kLanes = D / 16, kStep = 32 / kLanes, kIts = 2 * kPageSize / kStep;
-  const int lane = threadIdx.x & 31, c = lane % kLanes, r0 = 2 * w * kPageSize + lane / kLanes;
-  const int count = f.count;
+  const int lane = threadIdx.x & 31, c = lane % kLanes, first = lane / kLanes;
   uint4 x[kIts];
 #pragma unroll
   for (int i = 0; i < kIts; ++i) {
-    const int r = r0 + i * kStep;
+    const int r = first + i * kStep;
     x[i] = make_uint4(0, 0, 0, 0);
-    if (r < count && f.page[r / kPageSize] >= 0)
+    if (2 * i < kIts ? r < valid0 : r - kPageSize < valid1)
       x[i] = *reinterpret_cast<const uint4*>(raw + r * D + c * 16);
   }
+  // lanes of the second region store their chunks in the other order: the eight lanes of a row
+  // then hit eight different chunks
+  const int up = D == 128 ? c >> 2 : 0;
 #pragma unroll
   for (int i = 0; i < kIts; ++i) {
-    const int r = r0 + i * kStep;
-    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint32_t h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = q8::decode2((in[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-    // lanes of the second region store their chunks in the other order: the eight lanes of a row
-    // then hit eight different chunks
-    const int up = D == 128 ? c >> 2 : 0;
+    q8::decode4(x[i].x, h[0], h[1]);
+    q8::decode4(x[i].y, h[2], h[3]);
+    q8::decode4(x[i].z, h[4], h[5]);
+    q8::decode4(x[i].w, h[6], h[7]);
+    const int r = r0 + first + i * kStep;
     const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
     *reinterpret_cast<uint4*>(chunk_at(tile, r, 2 * c + up)) = up ? hi : lo;
     *reinterpret_cast<uint4*>(chunk_at(tile, r, 2 * c + 1 - up)) = up ? lo : hi;
   }
 }
 
-// The same share of a tile of the sequence's own rows: each group over a power of two of its own,
-// its largest finite magnitude in [2^8, 2^9).
+// 16 of the sequence's own rows as rows r0 .. of an f16 tile: over a power of two, which brings
+// their largest finite magnitude into [2^8, 2^9). Returns its scale byte.
 template <int D>
-MARS_DEV void convert_own(const uint16_t* __restrict__ rows, long long stride, uint8_t* tile,
-                          int count, uint8_t* bytes, int w) {
+MARS_DEV int convert_own(const uint16_t* __restrict__ rows, long long stride, uint8_t* tile, int r0,
+                         int count) {
   constexpr int kChunks = D / 8, kStep = 32 / kChunks, kIts = kPageSize / kStep;
   const int lane = threadIdx.x & 31, c = lane % kChunks;
-#pragma unroll 1
-  for (int g = 2 * w; g < 2 * w + 2; ++g) {
-    const int r0 = g * kPageSize + lane / kChunks;
-    uint4 x[kIts];
-    uint32_t top = 0;
+  r0 += lane / kChunks;
+  uint4 x[kIts];
+  uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kIts; ++i) {
-      const int r = r0 + i * kStep;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (r < count) x[i] = *reinterpret_cast<const uint4*>(rows + r * stride + c * 8);
-    }
+  for (int i = 0; i < kIts; ++i) {
+    const int r = r0 + i * kStep;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (r < count) x[i] = *reinterpret_cast<const uint4*>(rows + r * stride + c * 8);
+  }
 #pragma unroll
-    for (int i = 0; i < kIts; ++i) {
-      const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+  for (int i = 0; i < kIts; ++i) {
+    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t m = v[e] & 0x7fff7fffu;
-        top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
-      }
-    }
-    top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
-    const int byte = min(max((int)(top >> 7) - 8, q8::kLeast), kOwnMost);
-    if (lane == 0) bytes[g] = (uint8_t)byte;
-    const float f = q8::inverse_power(byte);
-#pragma unroll
-    for (int i = 0; i < kIts; ++i) {
-      float e[8];
-      unpack8(x[i], e);
-      uint32_t h[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = q8::pack_f16x2(e[2 * k] * f, e[2 * k + 1] * f);
-      *reinterpret_cast<uint4*>(chunk_at(tile, r0 + i * kStep, c)) = make_uint4(h[0], h[1], h[2], h[3]);
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t m = v[e] & 0x7fff7fffu;
+      top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
     }
   }
+  top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+  const int byte = min(max((int)(top >> 7) - 8, q8::kLeast), kOwnMost);
+  const float f = q8::inverse_power(byte);
+#pragma unroll
+  for (int i = 0; i < kIts; ++i) {
+    float e[8];
+    unpack8(x[i], e);
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = q8::pack_f16x2(e[2 * k] * f, e[2 * k + 1] * f);
+    *reinterpret_cast<uint4*>(chunk_at(tile, r0 + i * kStep, c)) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  return byte;
 }
 
-// Warps 8 ..: f16 tiles of K and V.
+// Warps 12 ..: copies of their two pages of every tile of K or V, and f16 tiles from them.
 template <int D>
 MARS_DEV void convert(const Pipe& p) {
   using namespace sm100;
   using L = Layout<D>;
   const Args& a = p.a;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kConvertWarp;
-  static_assert(kConvertWarps * 2 == kPagesPerTile, "two groups a warp");
-  int c = 0;
-  for (int t = 0;; ++t) {
-    if (!p.warp_wait_info(t)) break;
-    Info& f = p.info(t);
-    const int flags = f.flags;
-    if (flags & kEnd) break;
-    bool ok = true;
-    for (int h = 0; h < 2; ++h) {
-      const int st = c % kRaw, ts = t % kTiles;
-      const bool own = flags & kOwn;
-      if (!own && !(ok = p.warp_wait(&p.bar.raw_full[st], (c / kRaw) & 1))) break;
-      if (!(ok = p.warp_wait(&p.bar.f_empty[h][ts], ((t / kTiles) & 1) ^ 1))) break;
-      uint8_t* tile = L::tile(p.smem, h, t);
-      if (own) {
-        const long long stride = h ? a.v_stride : a.k_stride;
-        convert_own<D>((h ? a.v : a.k) + ((size_t)f.base + f.k0) * stride + f.kvh * D, stride, tile,
-                       f.count, h ? f.v_byte : f.k_byte, w);
-      } else {
-        convert_raw<D>(p.smem + L::OFF_RAW + st * L::RAW, tile, f, w);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p.bar.raw_empty[st]);
-        ++c;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp;
+  const int is_v = warp / 4, g = warp % 4 * 2;       // first page in the tile
+  static_assert(kConvertWarps == kPagesPerTile, "four warps for K, four for V, two pages each");
+  uint64_t* const full = p.bar.raw_full[warp];
+  uint8_t* const ring = p.smem + L::OFF_RAW + warp * kRaw * 2 * L::PAGE;
+  const uint8_t* const pool = is_v ? a.v_pool : a.k_pool;
+  // the next copy: its number and tile; `converted`: copies that have left the ring
+  int copies = 0, next = 0, converted = 0;
+  bool more = true, ok = true;
+  auto copy_ahead = [&](int t) {
+    while (more && next <= t + kAhead && copies < converted + kRaw) {
+      if (!(ok = p.warp_wait_info(next))) break;
+      const Info& f = p.info(next);
+      const int flags = f.flags;
+      ++next;
+      if (flags & kEnd) more = false;
+      if (flags & (kEnd | kOwn)) continue;
+      if (lane == 0) {
+        const int2 page = *reinterpret_cast<const int2*>(f.page + g);
+        const int st = copies % kRaw;
+        uint8_t* dst = ring + st * 2 * L::PAGE;
+        mbar_arrive_expect_tx(&full[st], ((page.x >= 0) + (page.y >= 0)) * L::PAGE);
+        if (page.x >= 0)
+          bulk_load(dst, pool + ((size_t)page.x * a.hkv + f.kvh) * L::PAGE, L::PAGE, &full[st]);
+        if (page.y >= 0)
+          bulk_load(dst + L::PAGE, pool + ((size_t)page.y * a.hkv + f.kvh) * L::PAGE, L::PAGE, &full[st]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p.bar.f_full[h][ts]);
+      ++copies;
     }
+  };
+  for (int t = 0;; ++t) {
+    copy_ahead(t);                                   // has waited for tile t, if not earlier
     if (!ok) break;
-    p.warp_done(t);
+    Info& f = p.info(t);
+    const int flags = f.flags, ts = t % kTiles;
+    if (flags & kEnd) break;
+    uint8_t* tile = L::tile(p.smem, is_v, t);
+    if (!(flags & kOwn) && !(ok = p.warp_wait(&full[converted % kRaw], (converted / kRaw) & 1))) break;
+    if (!(ok = p.warp_wait(&p.bar.f_empty[is_v][ts], ((t / kTiles) & 1) ^ 1))) break;
+    if (flags & kOwn) {
+      const long long stride = is_v ? a.v_stride : a.k_stride;
+      const uint16_t* rows =
+          (is_v ? a.v : a.k) + ((size_t)f.base + f.k0) * stride + f.kvh * D;
+#pragma unroll 1
+      for (int i = g; i < g + 2; ++i) {
+        const int byte = convert_own<D>(rows, stride, tile, i * kPageSize, f.count);
+        if (lane == 0) (is_v ? f.v_byte : f.k_byte)[i] = (uint8_t)byte;
+      }
+    } else {
+      const int2 page = *reinterpret_cast<const int2*>(f.page + g);
+      const int count = f.count - g * kPageSize;
+      convert_raw<D>(ring + converted % kRaw * 2 * L::PAGE, tile, g * kPageSize,
+                     page.x >= 0 ? count : 0, page.y >= 0 ? count - kPageSize : 0);
+      ++converted;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&p.bar.f_full[is_v][ts]);
+      mbar_arrive(&p.bar.info_empty[t % kInfos]);
+    }
   }
+  // no copy is in flight when the CTA ends
+  __syncwarp();
+  if (lane == 0)
+#pragma unroll 1
+    for (int i = converted; i < copies; ++i) mbar_wait(&full[i % kRaw], (i / kRaw) & 1, nullptr, a.status);
+  __syncwarp();
 }
 
 // One thread: S_t = Q K_t^T.
@@ -660,23 +681,49 @@ MARS_DEV void issue_pv(const Pipe& p) {
   mbar_wait(&p.bar.drain[1], 0, nullptr, p.a.status);
 }
 
-// This thread's query row of the item that tile t begins, as f16 into Q; returns the factor of its
-// scores. A row without a token is zero.
+// The two threads of a row. Warps of a pair call it alike; false if the wait gave up.
+struct Pair {
+  const Pipe& p;
+  int row, half, uses;
+  MARS_DEV bool meet() {
+    uint64_t* b = &p.bar.pair[row / 32];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(b);
+    return p.warp_wait(b, uses++ & 1);
+  }
+  // 16 bits for the other thread, and its own
+  MARS_DEV void give(uint32_t mine) {
+    p.bar.exchange[uses & 1][half][row] = (uint16_t)mine;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&p.bar.pair[row / 32]);
+  }
+  MARS_DEV bool take(uint32_t& other) {
+    const int u = uses++ & 1;
+    if (!p.warp_wait(&p.bar.pair[row / 32], u)) return false;
+    other = p.bar.exchange[u][half ^ 1][row];
+    return true;
+  }
+};
+
+// This thread's half of its query row of the item that tile t begins, as f16 into Q; factor: of the
+// row's scores. A row without a token is zero.
 template <int D>
-MARS_DEV float load_q(const Pipe& p, int t, int row) {
+MARS_DEV bool load_q(const Pipe& p, Pair& pair, int t, float& factor) {
   using L = Layout<D>;
+  constexpr int kChunks = D / 16;                    // of 8 elements, of the half
   const Args& a = p.a;
   const Info& f = p.info(t);
-  const int tok = f.tok0 + row / a.gp, h = f.h0 + row % a.gp;
+  const int row = pair.row, tok = f.tok0 + row / a.gp, h = f.h0 + row % a.gp;
   const bool has = row < a.gp * a.tpt && tok < f.n;
-  uint4 x[D / 8];
-  const uint16_t* src = a.q + ((size_t)f.base + tok) * a.q_stride + (size_t)h * D;
-#pragma unroll
-  for (int c = 0; c < D / 8; ++c)
-    x[c] = has ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
+  uint4 x[kChunks];
+  const uint16_t* src =
+      a.q + ((size_t)f.base + tok) * a.q_stride + (size_t)h * D + pair.half * (D / 2);
   uint32_t top = 0;
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
+  for (int c = 0; c < kChunks; ++c)
+    x[c] = has ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
     const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -685,92 +732,163 @@ MARS_DEV float load_q(const Pipe& p, int t, int row) {
     }
   }
   top = max(top >> 16, top & 0xffffu);
+  uint32_t other;
+  pair.give(top);
+  if (!pair.take(other)) return false;
+  top = max(top, other);
   // exponent of the row's largest finite magnitude (rows of next to nothing: 2^-60)
   const int byte = top ? min(max((int)(top >> 7), 67), 253) : 127;
   const float inv = q8::inverse_power(byte);
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
+  for (int c = 0; c < kChunks; ++c) {
     float e[8];
     unpack8(x[c], e);
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = q8::pack_f16x2(e[2 * k] * inv, e[2 * k + 1] * inv);
-    *reinterpret_cast<uint4*>(chunk_at(p.smem + L::OFF_Q, row, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(chunk_at(p.smem + L::OFF_Q, row, pair.half * kChunks + c)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
   }
   sm100::fence_proxy_async_smem();
   sm100::mbar_arrive_warp(&p.bar.q_full);
-  return a.scale_log2 * q8::power(byte);
+  factor = a.scale_log2 * q8::power(byte);
+  return true;
 }
 
-// lse-like statistics of a row: l is 0 where every score is -infinity (O is then 0), NaN where one
-// is NaN or +infinity.
+// Factor of a row's O. l is 0 where every score is -infinity (O is then 0), NaN where one is NaN or
+// +infinity.
 MARS_DEV float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
-// Warps 4..7: softmax and output; thread = row.
+// This thread's half of its row of O out of TMEM: divided by the row's sum to where the row is (at),
+// or into a partial.
+template <int D>
+MARS_DEV void store_o(const Pipe& p, const Pair& pair, int slot, bool has, long long at, float m,
+                      float l) {
+  using namespace sm100;
+  using L = Layout<D>;
+  const Args& a = p.a;
+  const int row = pair.row;
+  const uint32_t o_addr = p.tmem + L::TM_O + ((uint32_t)(row & ~31) << 16);
+  const float inv = reciprocal(l);
+  float4* part = a.part + ((size_t)blockIdx.x * 2 + slot) * L::PART;
+  if (slot >= 0 && has && pair.half == 0)
+    reinterpret_cast<float2*>(part + BQ * D / 4)[row] = make_float2(m, l);
+#pragma unroll 1
+  for (int c = pair.half * (D / 64); c < (pair.half + 1) * (D / 64); ++c) {
+    uint32_t o[32];
+    tmem_ld32(o_addr + c * 32, o);
+    tmem_ld_wait();
+    if (slot < 0) {
+      packed::store_rows<32>(a.o + c * 32, has ? at : -1, threadIdx.x & 31,
+                             [&](int e) { return __uint_as_float(o[e]) * inv; });
+    } else if (has) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        part[(c * 8 + e / 4) * BQ + row] =
+            make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                        __uint_as_float(o[e + 3]));
+    }
+  }
+}
+
+// Softmax and output.
 template <int D>
 MARS_DEV void softmax(const Pipe& p) {
   using namespace sm100;
   using L = Layout<D>;
+  constexpr int kKeys = BKV / 2, kGroups = kPagesPerTile / 2;       // of a thread
   const Args& a = p.a;
-  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + lane;
+  const int warp = (threadIdx.x >> 5) - kSoftmaxWarp, quad = warp & 3;
+  Pair pair{p, quad * 32 + (int)(threadIdx.x & 31), warp >> 2, 0};
+  const int row = pair.row, half = pair.half;
   const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-  const uint32_t o_addr = p.tmem + L::TM_O + lane_off;
-  if (!p.warp_wait_info(0) || (p.info(0).flags & kEnd)) return;
-  float factor = load_q<D>(p, 0, row);
-  float m = -INFINITY, l = 0.f;
-  int tok = 0;
-  bool has = false, busy = false;
-  for (int t = 0;; ++t) {
+  float factor = 0.f, m = -INFINITY, l = 0.f;
+  int tok = 0, t = -1, slot = -1, base = 0, h0 = 0;
+  bool has = false, busy = false, between = true;
+  for (;;) {
+    if (between) {
+      // every S of the item is done: Q of the next one, then this one's O
+      if (!p.warp_wait_info(t + 1)) return;
+      const bool end = p.info(t + 1).flags & kEnd;
+      // the row's sum, through its place in Q, which is free now
+      *reinterpret_cast<float*>(chunk_at(p.smem + L::OFF_Q, row, half)) = l;
+      if (!pair.meet()) return;
+      const float sum = *reinterpret_cast<const float*>(chunk_at(p.smem + L::OFF_Q, row, 0)) +
+                        *reinterpret_cast<const float*>(chunk_at(p.smem + L::OFF_Q, row, 1));
+      if (!end && !load_q<D>(p, pair, t + 1, factor)) return;
+      if (t >= 0 && !p.warp_wait(&p.bar.pv_done[t % kBufs], (t / kBufs) & 1)) return;
+      if (busy) {
+        tc_fence_after();
+        store_o<D>(p, pair, slot, has, (((long long)base + tok) * a.hq + h0 + row % a.gp) * D, m, sum);
+        tc_fence_before();
+      }
+      if (end) return;
+    }
+    ++t;
     if (!p.warp_wait_info(t)) return;
     const Info& f = p.info(t);
     const int flags = f.flags;
-    if (flags & kEnd) return;
-    if (flags & kFirst) {
+    if (between) {
       m = -INFINITY;
       l = 0.f;
+      slot = f.slot;
+      base = f.base;
+      h0 = f.h0;
       tok = f.tok0 + row / a.gp;
       has = row < a.gp * a.tpt && tok < f.n;
-      busy = __any_sync(0xffffffffu, has);       // a warp without rows only keeps step
+      busy = __any_sync(0xffffffffu, has);       // warps without rows only keep step
     }
+    between = flags & kLast;
     const int sb = t % kBufs;
-    // the converters have left the scales of own rows
+    // the converters have left the scales of own rows (K's before S, this is for V's)
     if ((flags & kOwn) && !p.warp_wait(&p.bar.f_full[1][t % kTiles], (t / kTiles) & 1)) return;
-    const int limit = (flags & kOwn) ? min(f.count, tok + 1 - f.k0) : f.count;
-    const uint2 kb = *reinterpret_cast<const uint2*>(f.k_byte);
-    const uint2 vb = *reinterpret_cast<const uint2*>(f.v_byte);
+    // keys of this thread that its row sees
+    const int limit = ((flags & kOwn) ? min(f.count, tok + 1 - f.k0) : f.count) - half * kKeys;
     if (!p.warp_wait(&p.bar.s_full[sb], (t / kBufs) & 1)) return;
     tc_fence_after();
+    const uint32_t kb = *reinterpret_cast<const uint32_t*>(f.k_byte + half * kGroups);
+    const uint32_t vb = *reinterpret_cast<const uint32_t*>(f.v_byte + half * kGroups);
     if (busy) {
       const uint32_t s_addr = p.tmem + L::TM_S + sb * BKV + lane_off;
-      uint32_t r[BKV];
+      uint32_t r[kKeys];
 #pragma unroll
-      for (int c = 0; c < BKV / 32; ++c)
-        tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
-      tmem_ld_wait();
-      if (__any_sync(0xffffffffu, limit < BKV)) {
-#pragma unroll
-        for (int e = 0; e < BKV; ++e)
-          if (e >= limit) r[e] = 0xff800000u;
-      }
+      for (int c = 0; c < kKeys / 32; ++c)
+        tmem_ld32(s_addr + half * kKeys + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
       // factor of the scores of 16 keys (never 0 or infinite: it meets infinite scores), and their
       // exponent of V
-      auto mul_of = [&](int g) {
-        const int b = ((g < 4 ? kb.x : kb.y) >> (8 * (g & 3))) & 255;
-        return fminf(fmaxf(factor * q8::power(b), 1e-38f), 3e38f);
-      };
-      auto byte_of = [&](int g) { return (int)(((g < 4 ? vb.x : vb.y) >> (8 * (g & 3))) & 255); };
-      auto add_of = [&](int g) { return byte_of(g) ? (float)(byte_of(g) - q8::kBias) : -INFINITY; };
-      float top = -INFINITY;
+      float mul[kGroups], add[kGroups];
 #pragma unroll
-      for (int g = 0; g < kPagesPerTile; ++g) {
-        float x[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[16 * g + e]);
-        const float y = flash::max3f(flash::max3f(x[0], x[1], x[2]), flash::max3f(x[3], x[4], x[5]),
-                                     flash::max3f(x[6], x[7], x[8]));
-        const float z = flash::max3f(flash::max3f(x[9], x[10], x[11]), flash::max3f(x[12], x[13], x[14]), x[15]);
-        top = fmaxf(top, fmaf(fmaxf(y, z), mul_of(g), add_of(g)));
+      for (int g = 0; g < kGroups; ++g) {
+        const int k = (kb >> (8 * g)) & 255, v = (vb >> (8 * g)) & 255;
+        mul[g] = fminf(fmaxf(factor * q8::power(k), 1e-38f), 3e38f);
+        // 2^23 + byte is exact
+        add[g] = v ? __int_as_float(0x4b000000 | v) - (8388608.f + q8::kBias) : -INFINITY;
       }
+      tmem_ld_wait();
+      if (__any_sync(0xffffffffu, limit < kKeys)) {
+#pragma unroll
+        for (int e = 0; e < kKeys; ++e)
+          if (e >= limit) r[e] = 0xff800000u;
+      }
+      // s + e, in place, and its maximum
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float2 mul2 = make_float2(mul[g], mul[g]), add2 = make_float2(add[g], add[g]);
+#pragma unroll
+        for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                      mul2, add2);
+          r[e] = __float_as_uint(x.x);
+          r[e + 1] = __float_as_uint(x.y);
+        }
+      }
+      float top = flash::row_max_log2(r, 1.f);
+      // the row's maximum as bf16, rounded up: any number near it serves
+      const uint32_t bits = __float_as_uint(top), mine = (top > 0.f ? bits + 0xffffu : bits) >> 16;
+      uint32_t other;
+      pair.give(mine);
+      if (!pair.take(other)) return;
+      top = fmaxf(__uint_as_float(mine << 16), __uint_as_float(other << 16));
       // lazy rescale (flash_tc.cuh)
       const bool raise = top > m + flash::kRescaleLog2;
       const bool rescale = raise && m != -INFINITY;
@@ -780,83 +898,40 @@ MARS_DEV void softmax(const Pipe& p) {
         const float alpha = rescale ? flash::ex2_approx(m - top) : 1.f;
         l *= alpha;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + c * 32, o);
+        for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
+          const uint32_t o_addr = p.tmem + L::TM_O + lane_off + c * 16;
+          uint32_t o[16];
+          tmem_ld16(o_addr, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(o_addr + c * 32, o);
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st16(o_addr, o);
         }
         tmem_st_wait();
       }
       if (raise) m = top;
       const float shift = kLift - (m == -INFINITY ? 0.f : m);
+      const float2 shift2 = make_float2(shift, shift);
+      uint32_t packed[kKeys / 2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t packed[32];
+      for (int g = 0; g < kGroups; ++g) {
+        float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int g = 4 * h; g < 4 * h + 4; ++g) {
-          const float mul = mul_of(g), add = add_of(g) + shift;
-          const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
-          float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[16 * g + e]),
-                                                    __uint_as_float(r[16 * g + e + 1])), mul2, add2);
-            const float2 w = make_float2(flash::ex2_approx(x.x), flash::ex2_approx(x.y));
-            packed[(g & 3) * 8 + e / 2] = q8::pack_f16x2(w.x, w.y);
-            acc = __fadd2_rn(acc, w);
-          }
-          l = fmaf(acc.x + acc.y, byte_of(g) ? q8::inverse_power(byte_of(g)) : 1.f, l);
+        for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+          const float2 x = __fadd2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), shift2);
+          const float2 w = make_float2(flash::ex2_approx(x.x), flash::ex2_approx(x.y));
+          packed[e / 2] = q8::pack_f16x2(w.x, w.y);
+          acc = __fadd2_rn(acc, w);
         }
-        tmem_st32(s_addr + L::P_OFF + 32 * h, packed);
+        // 2^-e; where there are no keys, the bits of some finite number, times 0
+        l = fmaf(acc.x + acc.y, q8::inverse_power((vb >> (8 * g)) & 255), l);
       }
+      tmem_st32(s_addr + L::P_OFF + half * (kKeys / 2), packed);
       tmem_st_wait();
     }
-    const bool last = flags & kLast;
-    const int slot = f.slot, base = f.base, h0 = f.h0;
     tc_fence_before();
     mbar_arrive_warp(&p.bar.p_full[sb]);
     p.warp_done(t);
-    if (!last) continue;
-    // every S of the item is done: Q of the next one, then this one's O
-    if (!p.warp_wait_info(t + 1)) return;
-    if (!(p.info(t + 1).flags & kEnd)) factor = load_q<D>(p, t + 1, row);
-    if (!p.warp_wait(&p.bar.pv_done[sb], (t / kBufs) & 1)) return;
-    tc_fence_after();
-    if (!busy) continue;
-    if (slot < 0) {
-      const float inv = reciprocal(l);
-      const long long at =
-          has ? (((long long)base + tok) * a.hq + h0 + row % a.gp) * D : -1;
-#pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        float o[64];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          tmem_ld32(o_addr + c * 64 + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(o + 32 * k));
-        tmem_ld_wait();
-        packed::store_rows<64>(a.o + c * 64, at, lane, [&](int e) { return o[e] * inv; });
-      }
-    } else {
-      float4* rec = a.part + ((size_t)blockIdx.x * 2 + slot) * L::PART;
-      if (has) reinterpret_cast<float2*>(rec + BQ * D / 4)[row] = make_float2(m, l);
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(o_addr + c * 32, o);
-        tmem_ld_wait();
-        if (has) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            rec[(c * 8 + e / 4) * BQ + row] =
-                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                            __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-        }
-      }
-    }
-    tc_fence_before();
   }
 }
 
@@ -864,37 +939,37 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Args a) {
   using namespace sm100;
   using L = Layout<D>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ Bar bar;
-  __shared__ Info infos[kInfos];
-  __shared__ Scan scan;
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ Shared shared;
+  Bar& bar = shared.bar;
+  Scan& scan = shared.scan;
   const int warp = threadIdx.x >> 5;
+  if (smem_u32(smem_raw) % 1024) {                   // see Shared
+    if (a.status) atomicOr(a.status, MARS_ST_TIMEOUT);
+    return;
+  }
   if (threadIdx.x == 0) {
     bar.abort = 0;
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&bar.info_full[i], 1);
-      // loader, both issuers, the converters' warps, the softmax's
-      mbar_init(&bar.info_empty[i], 3 + kConvertWarps + 4);
+      // both issuers, the converters' warps, the softmax's
+      mbar_init(&bar.info_empty[i], 2 + kConvertWarps + kSoftmaxWarps);
     }
-    for (int i = 0; i < kRaw; ++i) {
-      mbar_init(&bar.raw_full[i], 1);
-      mbar_init(&bar.raw_empty[i], kConvertWarps);
-    }
+    for (int i = 0; i < kConvertWarps * kRaw; ++i) mbar_init(&bar.raw_full[i / kRaw][i % kRaw], 1);
     for (int h = 0; h < 2; ++h) {
       for (int i = 0; i < kTiles; ++i) {
-        mbar_init(&bar.f_full[h][i], kConvertWarps);
+        mbar_init(&bar.f_full[h][i], kConvertWarps / 2);
         mbar_init(&bar.f_empty[h][i], 1);
       }
       mbar_init(&bar.drain[h], 1);
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 128);
+      mbar_init(&bar.p_full[i], 32 * kSoftmaxWarps);
       mbar_init(&bar.pv_done[i], 1);
     }
-    mbar_init(&bar.q_full, 128);
+    mbar_init(&bar.q_full, 32 * kSoftmaxWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
     fence_barrier_init();
   }
   find_part(a, scan);
@@ -909,21 +984,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Args a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Pipe p{a, bar, infos, smem, __shfl_sync(0xffffffffu, bar.tmem_base, 0)};
+  const Pipe p{a, bar, shared.infos, smem_raw, __shfl_sync(0xffffffffu, bar.tmem_base, 0)};
   if (warp < kSoftmaxWarp) {
     regs_lower<kControlRegs>();
     if (warp == 0) {
       walk<D>(p, scan);
-    } else if (warp == 1) {
-      load_raw<D>(p);
-    } else if (elect_one()) {
+    } else if (warp > 1 && elect_one()) {
       if (warp == 2) issue_s<D>(p); else issue_pv<D>(p);
     }
   } else if (warp < kConvertWarp) {
     regs_raise<kSoftmaxRegs>();
     softmax<D>(p);
   } else {
-    regs_raise<kConvertRegs>();
+    regs_lower<kConvertRegs>();
     convert<D>(p);
   }
   tc_fence_before();
@@ -1024,9 +1097,14 @@ __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(UnpackArgs a) {
     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
     uint32_t out[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 v = q8::decode2_f32((in[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-      out[e] = flash::pack_bf16x2(v.x * f, v.y * f);
+    for (int e = 0; e < 4; ++e) {
+      uint32_t h[2];
+      q8::decode4(in[e], h[0], h[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 v = q8::halves(h[k]);
+        out[2 * e + k] = flash::pack_bf16x2(v.x * f, v.y * f);
+      }
     }
     uint4* dst = reinterpret_cast<uint4*>((is_v ? a.v_out : a.k_out) + to * (kPageSize * D)) + 2 * c;
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
@@ -1109,7 +1187,7 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   a.part = plan.can_split ? reinterpret_cast<float4*>(ws + l.part) : nullptr;
   a.status = t.status;
   using L = Layout<D>;
-  static_assert(L::TOTAL + sizeof(Bar) + kInfos * sizeof(Info) + sizeof(Scan) + 256 <= 227 * 1024,
+  static_assert(L::TOTAL + sizeof(Shared) <= 227 * 1024,
                 "layout fits shared memory");
   static std::atomic<int> attr[64];
   cudaError_t e = set_smem_limit_once(chunk_kernel<D>, L::TOTAL, attr);

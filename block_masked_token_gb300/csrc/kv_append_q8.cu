@@ -78,10 +78,14 @@ MARS_DEV void append_head(const uint16_t* __restrict__ rows, long long stride, u
     } else if (slot < held && byte > byte0) {
       const uint32_t w[2] = {old[i].x, old[i].y};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 v = q8::decode2_f32((w[k >> 1] >> (16 * (k & 1))) & 0xffffu);
-        e[2 * k] = v.x * g;
-        e[2 * k + 1] = v.y * g;
+      for (int k = 0; k < 2; ++k) {
+        uint32_t lo, hi;
+        q8::decode4(w[k], lo, hi);
+        const float2 a = q8::halves(lo), b = q8::halves(hi);
+        e[4 * k] = a.x * g;
+        e[4 * k + 1] = a.y * g;
+        e[4 * k + 2] = b.x * g;
+        e[4 * k + 3] = b.y * g;
       }
     } else {
       continue;

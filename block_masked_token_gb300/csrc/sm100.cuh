@@ -117,6 +117,25 @@ MARS_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
   return mbar_test_wait(bar, parity) || mbar_wait_suspending(bar, parity, abort, status);
 }
 
+// The same without suspending, for waits on copies: a thread suspended on a barrier that bytes
+// complete was woken some 2 us late (a ring of four 16 KB stages of 2 KB copies took in 914 GB/s on
+// all SMs with mbar_wait and 4,280 GB/s with this).
+MARS_DEV bool mbar_wait_spinning(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                 int32_t* status) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_test_wait(bar, parity)) return true;
+    if (abort && *abort) return false;
+    if (globaltimer() - t0 > kWaitNs) {
+      if (abort) *abort = 1;
+      if (status) atomicOr(status, MARS_ST_TIMEOUT);
+      return false;
+    }
+  }
+}
 
 // ------------------------------------------------------------------------------ TMA
 
@@ -198,6 +217,11 @@ MARS_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* ba
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
+}
+
+// Ask for the line at p to be brought into L2.
+MARS_DEV void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 // Per-thread register count of the calling warpgroup (all 128 threads, warp-uniform):
@@ -375,6 +399,26 @@ MARS_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
         "=r"(r[31])
       : "r"(taddr));
+}
+
+// The same for 16 columns.
+MARS_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+MARS_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
 }
 
 MARS_DEV void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
