@@ -7,20 +7,25 @@
 // chunk_kernel works on the codes. A persistent CTA per SM takes an equal part of all key tiles of
 // all items; an item is a tile of up to 128 (token, query head) rows that share a KV head, as in
 // packed_attn.cu, with the 128-key tiles that its rows see: the sequence's own keys first, then the
-// cached ones. The products run on f16, which holds every code exactly (bf16 would too, but takes
-// five instructions for what one conversion does):
-//   - Q is divided by a power of two per row (its largest magnitude then lies in [1, 2)), an own
-//     key or value by one per 16 tokens, so that 11 bits hold them like bf16's 8 do;
-//   - scores get the row's power and the K scale of their 16 keys as one factor in 32 bits;
-//   - with V = 2^e c, a weight's power goes the other way: P' = 2^(s + e - m') is the A operand,
+// cached ones.
+//   - S = Q K^T takes K's codes as they are, in 8 bits. A row of Q, over a power of two that brings
+//     its largest magnitude into [128, 256), is the sum of two e4m3 numbers (bf16 has 8 significant
+//     bits, e4m3 4): exactly down to 2^-10 of that magnitude, to 2^-17 of it below. Own keys are two
+//     such numbers too, over a power of two per 16 tokens.
+//   - Scores get the row's power and the K scale of their 16 keys as one factor in 32 bits.
+//   - O += P V runs on f16, which holds every code exactly (bf16 would too, but takes five
+//     instructions for what one conversion does), and own values over a power of two per 16 tokens.
+//     With V = 2^e c, a weight's power goes the other way: P' = 2^(s + e - m') is the A operand,
 //     m' the running maximum of s + e instead of s, and the row sum takes P' 2^-e. P' is then as
 //     large as what it contributes, whatever the pages' scales are; 2^7 P' is stored, so that small
 //     ones keep their bits.
+// Shared memory moves 128 bytes per cycle: the copies of a tile's codes take 256 cycles, S 512, the
+// conversion of V 384, P V 256. (With K converted to f16 as well, 1,800 cycles per tile.)
 //
-// Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
-// (infos); warps 12..15 (K) and 16..19 (V) each copy two pages of every tile into a ring of their own
-// and turn them into 32 rows of a swizzled f16 tile, zero where no key may be read; warps 2 and 3 issue
-// S = Q K^T and O += P' V; warps 4..11 run the softmax, load Q and store O: a thread has a row, warps
+// Roles (512 threads): warp 0 walks the items and reads block table and scales ahead of the others
+// (infos); warp 1 copies K; warps 12..15 copy two pages of V each into a ring of their own and turn
+// them into 32 rows of a swizzled f16 tile, zero where no key may be read; warps 2 and 3 issue
+// S and O += P' V; warps 4..11 run the softmax, load Q and store O: a thread has a row, warps
 // 4..7 the first half of its keys and columns, 8..11 the second, and the two of a row exchange their
 // maxima and sums. What a warp runs per tile is kept short: with one warp per row, whose code for 128
 // keys no other shared, the code of all roles left the instruction cache within every tile, and a
@@ -42,15 +47,16 @@ namespace {
 using flash::BKV;
 using flash::BQ;
 
-constexpr int kThreads = 640;
-constexpr int kSoftmaxWarp = 4, kSoftmaxWarps = 8, kConvertWarp = 12, kConvertWarps = 8;
-constexpr int kControlRegs = 64, kSoftmaxRegs = 128, kConvertRegs = 80;
-static_assert(128 * (kControlRegs + 2 * kSoftmaxRegs + 2 * kConvertRegs) <=
+constexpr int kThreads = 512;
+constexpr int kSoftmaxWarp = 4, kSoftmaxWarps = 8, kConvertWarp = 12, kConvertWarps = 4;
+constexpr int kControlRegs = 88, kSoftmaxRegs = 152, kConvertRegs = 120;
+static_assert(128 * (kControlRegs + 2 * kSoftmaxRegs + kConvertRegs) <=
                   kThreads * (65536 / kThreads / 8 * 8),
               "the register split fits the launch's register pool");
-constexpr int kRaw = 2;              // ring of raw tiles
+constexpr int kRaw = 4;              // ring of raw tiles of V
+constexpr int kSlots = 4;            // ring of tiles of K's codes; an own tile takes two slots
 constexpr int kAhead = 3;            // tiles that copies may be ahead of the conversion
-constexpr int kTiles = 2;            // f16 tiles of K, and of V
+constexpr int kTiles = 2;            // f16 tiles of V
 constexpr int kBufs = 3;             // S buffers in TMEM
 // Tiles that the walk may be ahead. It publishes up to four at once, the converters wait for up to
 // kAhead more than they have released, and with this many the slots that it then needs belong to
@@ -104,16 +110,16 @@ MARS_DEV bool left_out(int skip_pages, int tpt, int n, int P) {
 MARS_DEV int cached(const Args& a, int len) {
   return (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize));
 }
-MARS_DEV long long items_of(const Args& a, const Row& q) {
+MARS_DEV int items_of(const Args& a, const Row& q) {
   if (q.n <= 0 || left_out(a.skip_pages, a.tpt, q.n, q.P)) return 0;
-  return (long long)((q.n + a.tpt - 1) / a.tpt) * a.heads;
+  return (q.n + a.tpt - 1) / a.tpt * a.heads;
 }
 
 struct Scan {
   long long sum[kThreads / 32], count[kThreads / 32];
   int top[kThreads / 32];
   Row at[2];
-  long long total, ctas;
+  long long total, ctas, p0, p1;
 };
 
 // Every thread of the CTA: the work of all, how many CTAs share it, and the sequences where this
@@ -137,9 +143,15 @@ MARS_DEV void find_part(const Args& a, Scan& sc) {
   for (int w = 0; w < warp; ++w) lead = max(lead, sc.top[w]);
   m = __shfl_up_sync(0xffffffffu, m, 1);
   if (lane > 0) lead = max(lead, m);
-  auto each = [&](auto f) {
+  // pass 0 sums up, pass 1 finds the sequences of the ends
+  long long mine = 0, pre = 0, p0 = -1, p1 = -1;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    long long count = 0;
     Row q{};
     q.base = lead;
+    q.pre = pre;
+#pragma unroll 1
     for (int s = lo; s < hi; ++s) {
       const int end = max(clamped(s + 1), q.base), len = a.seq_lens[s];
       q.s = s;
@@ -147,61 +159,60 @@ MARS_DEV void find_part(const Args& a, Scan& sc) {
       q.P = cached(a, len);
       if (end != a.cu[s + 1]) bad |= MARS_ST_BADSEQ;
       if (q.P != len && q.n > 0) bad |= MARS_ST_OVERFLOW;
-      const long long items = items_of(a, q);
-      f(q, items);
-      q.pre += items * q.unit();
+      const int items = items_of(a, q);
+      const long long work = items * q.unit();
+      if (p0 >= q.pre && p0 < q.pre + work) sc.at[0] = q;
+      if (p1 >= q.pre && p1 < q.pre + work) sc.at[1] = q;
+      count += items;
+      q.pre += work;
       q.base = end;
     }
-  };
-  long long mine = 0, count = 0;
-  each([&](const Row& q, long long items) {
-    mine += items * q.unit();
-    count += items;
-  });
-  long long incl = mine, sum = count;
+    if (pass) break;
+    mine = q.pre;
+    long long incl = mine, sum = count;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
-  if (lane == 31) {
-    sc.sum[warp] = incl;
-    sc.count[warp] = sum;
-  }
-  __syncthreads();
-  long long pre = incl - mine, total = 0, items = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) pre += sc.sum[w];
-    total += sc.sum[w];
-    items += sc.count[w];
-  }
-  // as many CTAs as there are, unless that leaves less than a part each and there are fewer items
-  const long long ctas =
-      min((long long)gridDim.x, max(items, total / (kUnit * kMinPart + kItemWork)));
-  if (tid == 0) {
-    sc.total = total;
-    sc.ctas = ctas;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (lane == 31) {
+      sc.sum[warp] = incl;
+      sc.count[warp] = sum;
+    }
+    __syncthreads();
+    pre = incl - mine;
+    long long total = 0, items = 0;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) pre += sc.sum[w];
+      total += sc.sum[w];
+      items += sc.count[w];
+    }
+    // as many CTAs as there are, unless that leaves less than a part each and there are fewer items
+    const long long ctas =
+        min((long long)gridDim.x, max(items, total / (kUnit * kMinPart + kItemWork)));
+    if (tid == 0) {
+      sc.total = total;
+      sc.ctas = ctas;
+    }
+    if ((long long)blockIdx.x >= ctas) break;
+    p0 = blockIdx.x * total / ctas;
+    p1 = (blockIdx.x + 1) * total / ctas;
+    if (tid == 0) {
+      sc.p0 = p0;
+      sc.p1 = p1;
+    }
   }
   if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, bad);
-  if ((long long)blockIdx.x < ctas) {
-    const long long p0 = blockIdx.x * total / ctas, p1 = (blockIdx.x + 1) * total / ctas;
-    if (mine > 0 && ((p0 >= pre && p0 < pre + mine) || (p1 >= pre && p1 < pre + mine)))
-      each([&](const Row& q, long long n) {
-        Row r = q;
-        r.pre += pre;
-        if (n > 0 && p0 >= r.pre && p0 < r.pre + n * q.unit()) sc.at[0] = r;
-        if (n > 0 && p1 >= r.pre && p1 < r.pre + n * q.unit()) sc.at[1] = r;
-      });
-  }
   __syncthreads();
 }
 
 // Item i of the sequence and its tile j at which position `pos` of the line cuts; not within
 // kMinPart tiles of an item's ends.
-MARS_DEV void cut_at(const Args& a, const Row& q, long long pos, long long& i, int& j) {
+MARS_DEV void cut_at(const Args& a, const Row& q, long long pos, int& i, int& j) {
   const long long rem = pos - q.pre;
-  i = rem / q.unit();
+  i = (int)(rem / q.unit());
   const int tiles = q.tiles();
   j = (int)min(max((rem - i * q.unit() - kItemWork / 2) / kUnit, 0LL), (long long)tiles);
   const int least = a.can_split ? kMinPart : tiles / 2;
@@ -219,9 +230,7 @@ MARS_DEV void cut_at(const Args& a, const Row& q, long long pos, long long& i, i
 struct Window {
   const Args& a;
   int s0, begin, end, len;           // first sequence; this lane's
-  MARS_DEV Window(const Args& a_, const Row& q) : a(a_), s0(0), begin(0), end(0), len(0) {
-    load(q.s, q.base);
-  }
+  MARS_DEV explicit Window(const Args& a_) : a(a_), s0(INT_MIN / 2), begin(0), end(0), len(0) {}
   MARS_DEV void load(int s, int base) {
     const int lane = threadIdx.x & 31;
     s0 = s;
@@ -253,7 +262,7 @@ struct Window {
 
 // --------------------------------------------------------------------------------- the pipeline
 
-enum : int { kFirst = 1, kLast = 2, kOwn = 4, kEnd = 8 };
+enum : int { kFirst = 1, kLast = 2, kOwn = 4, kEnd = 8, kHoles = 16 };
 
 // A key tile as the walk hands it to the other warps.
 struct alignas(16) Info {
@@ -270,7 +279,11 @@ struct alignas(16) Info {
 struct Bar {
   uint64_t info_full[kInfos], info_empty[kInfos];
   uint64_t raw_full[kConvertWarps][kRaw];              // of a warp's two pages
-  uint64_t f_full[2][kTiles], f_empty[2][kTiles];      // K, V
+  // own_free: two slots are free for an own tile, own_full: its scales and K are there. (Barriers of
+  // their own: a wait for a phase of a ring whose last one is still open would pass at once. Two of
+  // each: the slots let two own tiles be under way.)
+  uint64_t k_full[kSlots], k_empty[kSlots], own_free[2], own_full[2];
+  uint64_t v_full[kTiles], v_empty[kTiles];
   uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
   uint64_t q_full, drain[2];
   uint64_t pair[4];                  // the two warps of 32 rows
@@ -291,13 +304,19 @@ static_assert(sizeof(Shared) == 3072, "with the tiles, all of the shared memory 
 template <int D>
 struct Layout {
   static constexpr int RAW = BKV * D, TILE = BKV * D * 2, PAGE = kPageSize * D;
-  static constexpr int OFF_Q = 0, OFF_F = TILE;                      // f16 tiles: K ring, V ring
-  static constexpr int OFF_RAW = OFF_F + 2 * kTiles * TILE;
-  static constexpr int TOTAL = OFF_RAW + kRaw * 2 * RAW;
+  // both parts of Q; K's codes; f16 tiles of V; raw ones
+  static constexpr int OFF_Q = 0, OFF_K = 2 * RAW, OFF_V = OFF_K + kSlots * RAW;
+  static constexpr int OFF_RAW = OFF_V + kTiles * TILE;
+  static constexpr int TOTAL = OFF_RAW + kRaw * RAW;
   static constexpr int TM_S = 0, TM_O = kBufs * BKV, P_OFF = BKV / 2;
   static constexpr int PART = BQ * D / 4 + BQ / 2;                   // float4 of a partial
-  static MARS_DEV uint8_t* tile(uint8_t* smem, int is_v, int t) {
-    return smem + OFF_F + (is_v * kTiles + t % kTiles) * TILE;
+  // 8-bit operands: rows of D bytes, 16-byte chunk c of row r, swizzled over D bytes
+  static MARS_DEV uint32_t code_at(int r, int c) {
+    return r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+  }
+  static MARS_DEV uint64_t code_desc(const uint8_t* at) {
+    return D == 128 ? sm100::sdesc_sw128(sm100::smem_u32(at), 16, 1024)
+                    : sm100::sdesc_sw64(sm100::smem_u32(at), 16, 512);
   }
 };
 
@@ -308,13 +327,26 @@ struct Pipe {
   uint8_t* smem;
   uint32_t tmem;
 
-  // waits of one thread, and of a whole warp (by all lanes: behind a test of the lane a wait that
-  // is over takes 250 cycles instead of 100)
+  // Waits of one thread, and of a whole warp (by all lanes: behind a test of the lane a wait that is
+  // over takes 250 cycles instead of 100). They give up after 2^31 cycles, a second or more, and end
+  // all others through `abort`, for which the kernel's end sets the status: these few instructions are
+  // at thirty places of code that has to stay in the instruction cache.
   MARS_DEV bool wait(uint64_t* b, uint32_t parity) const {
-    return sm100::mbar_wait(b, parity, &bar.abort, a.status);
+    if (sm100::mbar_test_wait(b, parity)) return true;
+    const uint32_t t0 = (uint32_t)clock();
+    do {
+      if (sm100::mbar_try_wait(b, parity)) return true;
+    } while (!*(volatile int*)&bar.abort && (uint32_t)clock() - t0 < 1u << 31);
+    *(volatile int*)&bar.abort = 1;
+    return false;
   }
   MARS_DEV bool warp_wait(uint64_t* b, uint32_t parity) const {
     return __all_sync(0xffffffffu, wait(b, parity));
+  }
+  // the same for what a thread has in flight when it ends, aborted or not
+  MARS_DEV void drain(uint64_t* b, uint32_t parity) const {
+    const uint32_t t0 = (uint32_t)clock();
+    while (!sm100::mbar_try_wait(b, parity) && (uint32_t)clock() - t0 < 1u << 31) {}
   }
   MARS_DEV Info& info(int t) const { return infos[t % kInfos]; }
   MARS_DEV uint64_t* info_full(int t, uint32_t& parity) const {
@@ -357,16 +389,18 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
     if (lane < n) mbar_arrive(&p.bar.info_full[(t + lane) % kInfos]);
     t += n;
   };
-  const long long p0 = blockIdx.x * sc.total / sc.ctas, p1 = (blockIdx.x + 1) * sc.total / sc.ctas;
   Row q = sc.at[0];
-  long long i, ei = 0;
-  int j, es = a.batch, ej = 0;
-  cut_at(a, q, p0, i, j);
-  if (p1 < sc.total) {
-    es = sc.at[1].s;
-    cut_at(a, sc.at[1], p1, ei, ej);
+  int i = 0, j = 0, es = a.batch, ei = 0, ej = 0;
+  if (sc.p1 < sc.total) es = sc.at[1].s;
+#pragma unroll 1
+  for (int end = es < a.batch; end >= 0; --end) {    // the end, if it is not that of all, then the start
+    cut_at(a, sc.at[end], end ? sc.p1 : sc.p0, i, j);
+    if (end) {
+      ei = i;
+      ej = j;
+    }
   }
-  Window window(a, q);
+  Window window(a);
   for (;; ++i, j = 0) {
     if (i >= items_of(a, q)) {
       i = 0;
@@ -380,7 +414,7 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
     }
     if (q.s > es || (q.s == es && (i > ei || (i == ei && j >= ej)))) break;
     const int tiles = q.tiles(), jb = q.s == es && i == ei ? ej : tiles;
-    const int rt = (int)(i / a.heads), hg = (int)(i % a.heads);
+    const int rt = i / a.heads, hg = i % a.heads;
     const int tok0 = rt * a.tpt, last_tok = min(tok0 + a.tpt, q.n) - 1;
     const int slot = j > 0 ? 0 : jb < tiles ? 1 : -1;
     const int kvh = hg / (a.heads / a.hkv), h0 = hg * a.gp;
@@ -430,6 +464,7 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
       const bool needed = mine < c1 && (mine * kPagesPerTile + lane % kPagesPerTile) * (long long)kPageSize < q.P;
       const bool readable = needed && e >= 0 && e < a.num_pages;
       if (needed && !readable) flags |= MARS_ST_NOPAGE;
+      const uint32_t holes = __ballot_sync(0xffffffffu, needed && !readable);
       uint8_t kb = 127, vb = 0;
       if (readable) {
         const size_t at = (size_t)e * a.hkv + kvh;
@@ -456,7 +491,8 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
         f.v_byte[g] = vb;
         if (g == 0)
           entry(f, mine * BKV, min(q.P - mine * BKV, BKV),
-                (u == 0 ? first : 0) | (u + 1 == left ? kLast : 0));
+                (u == 0 ? first : 0) | (u + 1 == left ? kLast : 0) |
+                    (((holes >> lane) & 0xffu) ? kHoles : 0));
       }
       first = 0;
       left -= n;
@@ -477,6 +513,45 @@ MARS_DEV uint8_t* chunk_at(uint8_t* tile, int r, int c) {
   return tile + (c >> 3) * (BKV * 128) + flash::sw_off(r, c & 7);
 }
 
+// Warp 1: K's codes, a copy per page. The slots of an own tile are only taken, for the converters.
+template <int D>
+MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map) {
+  using namespace sm100;
+  using L = Layout<D>;
+  const Args& a = p.a;
+  const int lane = threadIdx.x & 31;
+  int c = 0, own = 0;                                // slots taken, own tiles
+  bool ok = true;
+  for (int t = 0; ok && p.warp_wait_info(t); ++t) {
+    const Info& f = p.info(t);
+    const int flags = f.flags;
+    if (flags & kEnd) break;
+    const int page = lane < kPagesPerTile && !(flags & kOwn) ? f.page[lane] : -1;
+    const int pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
+    const int row = (max(page, 0) * a.hkv + f.kvh) * kPageSize;
+#pragma unroll 1
+    for (int i = 0; i < (flags & kOwn ? 2 : 1); ++i, ++c) {
+      const int st = c % kSlots;
+      if (!(ok = p.warp_wait(&p.bar.k_empty[st], ((c / kSlots) & 1) ^ 1))) break;
+      if (lane == 0) mbar_arrive_expect_tx(&p.bar.k_full[st], pages * L::PAGE);
+      __syncwarp();
+      if (page >= 0)
+        tma_load_2d(p.smem + L::OFF_K + st * L::RAW + lane * L::PAGE, &map, &p.bar.k_full[st], 0, row);
+    }
+    if (ok && (flags & kOwn)) {
+      if (lane == 0) mbar_arrive(&p.bar.own_free[own & 1]);
+      ++own;
+    }
+    if (ok) p.warp_done(t);
+  }
+  // no copy is in flight when the CTA ends
+  if (lane == 0)
+#pragma unroll 1
+    for (int i = max(0, c - kSlots); i < c; ++i)
+      p.drain(&p.bar.k_full[i % kSlots], (i / kSlots) & 1);
+  __syncwarp();
+}
+
 // Two raw pages as rows r0 .. r0 + 31 of an f16 tile; of each only the first valid[i] rows, zero
 // for the others.
 template <int D>
@@ -489,7 +564,7 @@ MARS_DEV void convert_raw(const uint8_t* raw, uint8_t* tile, int r0, int valid0,
     const int r = first + i * kStep;
     x[i] = make_uint4(0, 0, 0, 0);
     if (2 * i < kIts ? r < valid0 : r - kPageSize < valid1)
-      x[i] = *reinterpret_cast<const uint4*>(raw + r * D + c * 16);
+      x[i] = *reinterpret_cast<const uint4*>(raw + Layout<D>::code_at(r, c));
   }
   // lanes of the second region store their chunks in the other order: the eight lanes of a row
   // then hit eight different chunks
@@ -508,60 +583,104 @@ MARS_DEV void convert_raw(const uint8_t* raw, uint8_t* tile, int r0, int valid0,
   }
 }
 
-// 16 of the sequence's own rows as rows r0 .. of an f16 tile: over a power of two, which brings
-// their largest finite magnitude into [2^8, 2^9). Returns its scale byte.
+// Largest finite magnitude, as bf16 bits, of the halves of a word and `top`, in both halves.
+MARS_DEV uint32_t finite_max(uint32_t top, uint32_t word) {
+  const uint32_t m = word & 0x7fff7fffu;
+  return __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+}
+
+// Sixteen bf16 times f as two e4m3 numbers each: the nearest, and the nearest to what that leaves.
+// An infinity becomes NaN (a finite value's second product adds nothing).
+MARS_DEV void split16(const uint4& x, const uint4& y, float f, uint8_t* first, uint8_t* second) {
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    float e[8];
+    unpack8(h ? y : x, e);
+    uint32_t u[2], v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float* w = e + 4 * i;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = fmaf(w[k], 0.f, w[k] * f);
+      u[i] = q8::encode2(w[0], w[1]) | (q8::encode2(w[2], w[3]) << 16);
+      uint32_t lo, hi;
+      q8::decode4(u[i], lo, hi);
+      const float2 a = q8::halves(lo), b = q8::halves(hi);
+      v[i] = q8::encode2(w[0] - a.x, w[1] - a.y) | (q8::encode2(w[2] - b.x, w[3] - b.y) << 16);
+    }
+    reinterpret_cast<uint2*>(first)[h] = make_uint2(u[0], u[1]);
+    reinterpret_cast<uint2*>(second)[h] = make_uint2(v[0], v[1]);
+  }
+}
+
+// The power of two for rows r0 .. r0 + 15 of the sequence's own, as a scale byte: it brings their
+// largest finite magnitude into [2^less, 2^(less + 1)). Whole warp.
 template <int D>
-MARS_DEV int convert_own(const uint16_t* __restrict__ rows, long long stride, uint8_t* tile, int r0,
-                         int count) {
-  constexpr int kChunks = D / 8, kStep = 32 / kChunks, kIts = kPageSize / kStep;
-  const int lane = threadIdx.x & 31, c = lane % kChunks;
-  r0 += lane / kChunks;
-  uint4 x[kIts];
+MARS_DEV int own_byte(const uint16_t* __restrict__ rows, long long stride, int r0, int count, int less) {
+  constexpr int kLanes = D / 16, kStep = 32 / kLanes;
+  const int lane = threadIdx.x & 31;
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kIts; ++i) {
-    const int r = r0 + i * kStep;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r < count) x[i] = *reinterpret_cast<const uint4*>(rows + r * stride + c * 8);
-  }
-#pragma unroll
-  for (int i = 0; i < kIts; ++i) {
-    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t m = v[e] & 0x7fff7fffu;
-      top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+  for (int i = 0; i < kPageSize / kStep; ++i) {
+    const int r = r0 + lane / kLanes + i * kStep;
+    if (r < count) {
+      const uint4* from = reinterpret_cast<const uint4*>(rows + r * stride + lane % kLanes * 16);
+      const uint4 x = from[0], y = from[1];
+      top = finite_max(finite_max(finite_max(finite_max(top, x.x), x.y), x.z), x.w);
+      top = finite_max(finite_max(finite_max(finite_max(top, y.x), y.y), y.z), y.w);
     }
   }
   top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
-  const int byte = min(max((int)(top >> 7) - 8, q8::kLeast), kOwnMost);
-  const float f = q8::inverse_power(byte);
-#pragma unroll
-  for (int i = 0; i < kIts; ++i) {
-    float e[8];
-    unpack8(x[i], e);
-    uint32_t h[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = q8::pack_f16x2(e[2 * k] * f, e[2 * k + 1] * f);
-    *reinterpret_cast<uint4*>(chunk_at(tile, r0 + i * kStep, c)) = make_uint4(h[0], h[1], h[2], h[3]);
-  }
-  return byte;
+  return min(max((int)(top >> 7) - less, q8::kLeast), kOwnMost);
 }
 
-// Warps 12 ..: copies of their two pages of every tile of K or V, and f16 tiles from them.
+// The same rows over that power of two as rows r0 .. of a tile: V as f16, K as two e4m3 tiles. (They
+// are read again, out of L1 or L2: code that keeps them is as long as that for a tile of the cache.)
+template <int D, bool kV>
+MARS_DEV void convert_own(const uint16_t* __restrict__ rows, long long stride, uint8_t* tile,
+                          uint8_t* second, int r0, int count, int byte) {
+  using L = Layout<D>;
+  constexpr int kLanes = D / 16, kStep = 32 / kLanes;
+  const int lane = threadIdx.x & 31, c = lane % kLanes;         // 16 elements of a row
+  const float f = q8::inverse_power(byte);
+#pragma unroll 1
+  for (int i = 0; i < kPageSize / kStep; ++i) {
+    const int r = r0 + lane / kLanes + i * kStep;
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (r < count) {
+      const uint4* from = reinterpret_cast<const uint4*>(rows + r * stride + c * 16);
+      x = from[0];
+      y = from[1];
+    }
+    if (kV) {
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        float e[8];
+        unpack8(k ? y : x, e);
+        *reinterpret_cast<uint4*>(chunk_at(tile, r, 2 * c + k)) =
+            make_uint4(q8::pack_f16x2(e[0] * f, e[1] * f), q8::pack_f16x2(e[2] * f, e[3] * f),
+                       q8::pack_f16x2(e[4] * f, e[5] * f), q8::pack_f16x2(e[6] * f, e[7] * f));
+      }
+    } else {
+      split16(x, y, f, tile + L::code_at(r, c), second + L::code_at(r, c));
+    }
+  }
+}
+
+// Warps 12 ..: copies of their two pages of every tile of V and f16 tiles from them, and the
+// sequence's own K and V.
 template <int D>
-MARS_DEV void convert(const Pipe& p) {
+MARS_DEV void convert(const Pipe& p, const CUtensorMap& map) {
   using namespace sm100;
   using L = Layout<D>;
   const Args& a = p.a;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp;
-  const int is_v = warp / 4, g = warp % 4 * 2;       // first page in the tile
-  static_assert(kConvertWarps == kPagesPerTile, "four warps for K, four for V, two pages each");
+  const int g = warp * 2;                            // first page in the tile
+  static_assert(kConvertWarps * 2 == kPagesPerTile, "two pages a warp");
   uint64_t* const full = p.bar.raw_full[warp];
   uint8_t* const ring = p.smem + L::OFF_RAW + warp * kRaw * 2 * L::PAGE;
-  const uint8_t* const pool = is_v ? a.v_pool : a.k_pool;
   // the next copy: its number and tile; `converted`: copies that have left the ring
-  int copies = 0, next = 0, converted = 0;
+  int copies = 0, next = 0, converted = 0, slots = 0, own = 0;
   bool more = true, ok = true;
   auto copy_ahead = [&](int t) {
     while (more && next <= t + kAhead && copies < converted + kRaw) {
@@ -576,10 +695,9 @@ MARS_DEV void convert(const Pipe& p) {
         const int st = copies % kRaw;
         uint8_t* dst = ring + st * 2 * L::PAGE;
         mbar_arrive_expect_tx(&full[st], ((page.x >= 0) + (page.y >= 0)) * L::PAGE);
-        if (page.x >= 0)
-          bulk_load(dst, pool + ((size_t)page.x * a.hkv + f.kvh) * L::PAGE, L::PAGE, &full[st]);
+        if (page.x >= 0) tma_load_2d(dst, &map, &full[st], 0, (page.x * a.hkv + f.kvh) * kPageSize);
         if (page.y >= 0)
-          bulk_load(dst + L::PAGE, pool + ((size_t)page.y * a.hkv + f.kvh) * L::PAGE, L::PAGE, &full[st]);
+          tma_load_2d(dst + L::PAGE, &map, &full[st], 0, (page.y * a.hkv + f.kvh) * kPageSize);
       }
       ++copies;
     }
@@ -590,19 +708,37 @@ MARS_DEV void convert(const Pipe& p) {
     Info& f = p.info(t);
     const int flags = f.flags, ts = t % kTiles;
     if (flags & kEnd) break;
-    uint8_t* tile = L::tile(p.smem, is_v, t);
-    if (!(flags & kOwn) && !(ok = p.warp_wait(&full[converted % kRaw], (converted / kRaw) & 1))) break;
-    if (!(ok = p.warp_wait(&p.bar.f_empty[is_v][ts], ((t / kTiles) & 1) ^ 1))) break;
+    uint8_t* tile = p.smem + L::OFF_V + ts * L::TILE;
     if (flags & kOwn) {
-      const long long stride = is_v ? a.v_stride : a.k_stride;
-      const uint16_t* rows =
-          (is_v ? a.v : a.k) + ((size_t)f.base + f.k0) * stride + f.kvh * D;
+      // both scales and K before S, for which warp 1 has taken two slots; V before P V
+      const size_t at = (size_t)f.base + f.k0;
+      const uint16_t* const rows[2] = {a.k + at * a.k_stride + f.kvh * D, a.v + at * a.v_stride + f.kvh * D};
 #pragma unroll 1
-      for (int i = g; i < g + 2; ++i) {
-        const int byte = convert_own<D>(rows, stride, tile, i * kPageSize, f.count);
-        if (lane == 0) (is_v ? f.v_byte : f.k_byte)[i] = (uint8_t)byte;
+      for (int i = 0; i < 4; ++i) {
+        const int byte = own_byte<D>(i & 1 ? rows[1] : rows[0], i & 1 ? a.v_stride : a.k_stride,
+                                     (g + i / 2) * kPageSize, f.count, i & 1 ? 8 : 7);
+        if (lane == 0) (i & 1 ? f.v_byte : f.k_byte)[g + i / 2] = (uint8_t)byte;
       }
+      __syncwarp();
+      if (!(ok = p.warp_wait(&p.bar.own_free[own & 1], (own >> 1) & 1))) break;
+#pragma unroll 1
+      for (int i = g; i < g + 2; ++i)
+        convert_own<D, false>(rows[0], a.k_stride, p.smem + L::OFF_K + slots % kSlots * L::RAW,
+                              p.smem + L::OFF_K + (slots + 1) % kSlots * L::RAW, i * kPageSize, f.count,
+                              f.k_byte[i]);
+      slots += 2;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p.bar.own_full[own & 1]);
+      ++own;
+      if (!(ok = p.warp_wait(&p.bar.v_empty[ts], ((t / kTiles) & 1) ^ 1))) break;
+#pragma unroll 1
+      for (int i = g; i < g + 2; ++i)
+        convert_own<D, true>(rows[1], a.v_stride, tile, nullptr, i * kPageSize, f.count, f.v_byte[i]);
     } else {
+      ++slots;
+      if (!(ok = p.warp_wait(&full[converted % kRaw], (converted / kRaw) & 1))) break;
+      if (!(ok = p.warp_wait(&p.bar.v_empty[ts], ((t / kTiles) & 1) ^ 1))) break;
       const int2 page = *reinterpret_cast<const int2*>(f.page + g);
       const int count = f.count - g * kPageSize;
       convert_raw<D>(ring + converted % kRaw * 2 * L::PAGE, tile, g * kPageSize,
@@ -612,7 +748,7 @@ MARS_DEV void convert(const Pipe& p) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&p.bar.f_full[is_v][ts]);
+      mbar_arrive(&p.bar.v_full[ts]);
       mbar_arrive(&p.bar.info_empty[t % kInfos]);
     }
   }
@@ -620,39 +756,51 @@ MARS_DEV void convert(const Pipe& p) {
   __syncwarp();
   if (lane == 0)
 #pragma unroll 1
-    for (int i = converted; i < copies; ++i) mbar_wait(&full[i % kRaw], (i / kRaw) & 1, nullptr, a.status);
+    for (int i = converted; i < copies; ++i) p.drain(&full[i % kRaw], (i / kRaw) & 1);
   __syncwarp();
 }
 
-// One thread: S_t = Q K_t^T.
+// One thread: S_t = Q K_t^T, the sum over the parts of Q and K.
 template <int D>
 MARS_DEV void issue_s(const Pipe& p) {
   using namespace sm100;
   using L = Layout<D>;
-  const uint32_t idesc = idesc_f16_f32(BQ, BKV, false);
-  const uint64_t qd = sdesc_sw128(smem_u32(p.smem + L::OFF_Q), 16, 1024);
-  for (int t = 0, items = 0; p.wait_info(t); ++t) {
+  const uint32_t idesc = idesc_e4m3_f32(BQ, BKV);
+  const uint64_t qd = L::code_desc(p.smem + L::OFF_Q);
+  int slots = 0, items = 0, own = 0;
+  for (int t = 0; p.wait_info(t); ++t) {
     const int flags = p.info(t).flags;
     if (flags & kEnd) break;
     mbar_arrive(&p.bar.info_empty[t % kInfos]);
     const int sb = t % kBufs;
     if ((flags & kFirst) && !p.wait(&p.bar.q_full, items++ & 1)) break;
-    if (!p.wait(&p.bar.f_full[0][t % kTiles], (t / kTiles) & 1)) break;
+    if (flags & kOwn) {
+      if (!p.wait(&p.bar.own_full[own & 1], (own >> 1) & 1)) break;
+      ++own;
+    }
     // S buffer sb last held tile t - kBufs, whose P the PV of that tile read from it
     if (t >= kBufs && !p.wait(&p.bar.pv_done[sb], (t / kBufs - 1) & 1)) break;
-    tc_fence_after();
-    const uint64_t kd = sdesc_sw128(smem_u32(L::tile(p.smem, 0, t)), 16, 1024);
+    const int parts = flags & kOwn ? 2 : 1;
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < parts; ++i, ++slots) {
+      const int st = slots % kSlots;
+      if (!(ok = p.wait(&p.bar.k_full[st], (slots / kSlots) & 1))) break;
+      tc_fence_after();
+      const uint64_t kd = L::code_desc(p.smem + L::OFF_K + st * L::RAW);
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k >> 2) * (BQ * 128) + (k & 3) * 32;
-      mma_bf16_ss(p.tmem + L::TM_S + sb * BKV, sdesc_advance(qd, off), sdesc_advance(kd, off), idesc,
-                  k != 0);
+      for (int k = 0; k < 2 * (D / 32); ++k) {
+        const uint32_t off = k % (D / 32) * 32;
+        mma_f8_ss(p.tmem + L::TM_S + sb * BKV, sdesc_advance(qd, off + k / (D / 32) * L::RAW),
+                  sdesc_advance(kd, off), idesc, k != 0 || i != 0);
+      }
+      mma_commit(&p.bar.k_empty[st]);
     }
+    if (!ok) break;
     mma_commit(&p.bar.s_full[sb]);
-    mma_commit(&p.bar.f_empty[0][t % kTiles]);
   }
   mma_commit(&p.bar.drain[0]);
-  mbar_wait(&p.bar.drain[0], 0, nullptr, p.a.status);
+  p.drain(&p.bar.drain[0], 0);
 }
 
 // One thread: O += P'_t V_t.
@@ -666,19 +814,20 @@ MARS_DEV void issue_pv(const Pipe& p) {
     if (flags & kEnd) break;
     mbar_arrive(&p.bar.info_empty[t % kInfos]);
     const int pb = t % kBufs;
-    if (!p.wait(&p.bar.f_full[1][t % kTiles], (t / kTiles) & 1)) break;
+    if (!p.wait(&p.bar.v_full[t % kTiles], (t / kTiles) & 1)) break;
     if (!p.wait(&p.bar.p_full[pb], (t / kBufs) & 1)) break;
     tc_fence_after();
-    const uint64_t vd = sdesc_sw128(smem_u32(L::tile(p.smem, 1, t)), BKV * 128, 1024);
+    const uint64_t vd =
+        sdesc_sw128(smem_u32(p.smem + L::OFF_V + t % kTiles * L::TILE), BKV * 128, 1024);
 #pragma unroll
     for (int k = 0; k < BKV / 16; ++k)
       mma_bf16_ts(p.tmem + L::TM_O, p.tmem + L::TM_S + pb * BKV + L::P_OFF + k * 8,
                   sdesc_advance(vd, k * 2048), idesc, k != 0 || !(flags & kFirst));
     mma_commit(&p.bar.pv_done[pb]);
-    mma_commit(&p.bar.f_empty[1][t % kTiles]);
+    mma_commit(&p.bar.v_empty[t % kTiles]);
   }
   mma_commit(&p.bar.drain[1]);
-  mbar_wait(&p.bar.drain[1], 0, nullptr, p.a.status);
+  p.drain(&p.bar.drain[1], 0);
 }
 
 // The two threads of a row. Warps of a pair call it alike; false if the wait gave up.
@@ -705,30 +854,24 @@ struct Pair {
   }
 };
 
-// This thread's half of its query row of the item that tile t begins, as f16 into Q; factor: of the
-// row's scores. A row without a token is zero.
+// This thread's half of its query row of the item that tile t begins, as two e4m3 numbers each into
+// Q; factor: of the row's scores. A row without a token is zero.
 template <int D>
 MARS_DEV bool load_q(const Pipe& p, Pair& pair, int t, float& factor) {
   using L = Layout<D>;
-  constexpr int kChunks = D / 16;                    // of 8 elements, of the half
+  constexpr int kChunks = D / 32;                    // of 16 elements, of the half
   const Args& a = p.a;
   const Info& f = p.info(t);
   const int row = pair.row, tok = f.tok0 + row / a.gp, h = f.h0 + row % a.gp;
   const bool has = row < a.gp * a.tpt && tok < f.n;
-  uint4 x[kChunks];
-  const uint16_t* src =
-      a.q + ((size_t)f.base + tok) * a.q_stride + (size_t)h * D + pair.half * (D / 2);
+  const uint4* src = reinterpret_cast<const uint4*>(
+      a.q + ((size_t)f.base + tok) * a.q_stride + (size_t)h * D + pair.half * (D / 2));
   uint32_t top = 0;
+  if (has) {
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c)
-    x[c] = has ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t m = v[e] & 0x7fff7fffu;
-      top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+    for (int c = 0; c < 2 * kChunks; ++c) {
+      const uint4 x = src[c];
+      top = finite_max(finite_max(finite_max(finite_max(top, x.x), x.y), x.z), x.w);
     }
   }
   top = max(top >> 16, top & 0xffffu);
@@ -736,18 +879,16 @@ MARS_DEV bool load_q(const Pipe& p, Pair& pair, int t, float& factor) {
   pair.give(top);
   if (!pair.take(other)) return false;
   top = max(top, other);
-  // exponent of the row's largest finite magnitude (rows of next to nothing: 2^-60)
-  const int byte = top ? min(max((int)(top >> 7), 67), 253) : 127;
+  // the power of two that brings the row's largest finite magnitude into [128, 256) (rows of next to
+  // nothing: 2^-53)
+  const int byte = top ? min(max((int)(top >> 7), 74), 253) - 7 : 127;
   const float inv = q8::inverse_power(byte);
-#pragma unroll
+  uint8_t* to = p.smem + L::OFF_Q;
+#pragma unroll 1
   for (int c = 0; c < kChunks; ++c) {
-    float e[8];
-    unpack8(x[c], e);
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = q8::pack_f16x2(e[2 * k] * inv, e[2 * k + 1] * inv);
-    *reinterpret_cast<uint4*>(chunk_at(p.smem + L::OFF_Q, row, pair.half * kChunks + c)) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+    const uint32_t at = L::code_at(row, pair.half * kChunks + c);
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    split16(has ? src[2 * c] : none, has ? src[2 * c + 1] : none, inv, to + at, to + L::RAW + at);
   }
   sm100::fence_proxy_async_smem();
   sm100::mbar_arrive_warp(&p.bar.q_full);
@@ -811,10 +952,10 @@ MARS_DEV void softmax(const Pipe& p) {
       if (!p.warp_wait_info(t + 1)) return;
       const bool end = p.info(t + 1).flags & kEnd;
       // the row's sum, through its place in Q, which is free now
-      *reinterpret_cast<float*>(chunk_at(p.smem + L::OFF_Q, row, half)) = l;
+      float* sums = reinterpret_cast<float*>(p.smem + L::OFF_Q + row * D);
+      sums[half] = l;
       if (!pair.meet()) return;
-      const float sum = *reinterpret_cast<const float*>(chunk_at(p.smem + L::OFF_Q, row, 0)) +
-                        *reinterpret_cast<const float*>(chunk_at(p.smem + L::OFF_Q, row, 1));
+      const float sum = sums[0] + sums[1];
       if (!end && !load_q<D>(p, pair, t + 1, factor)) return;
       if (t >= 0 && !p.warp_wait(&p.bar.pv_done[t % kBufs], (t / kBufs) & 1)) return;
       if (busy) {
@@ -840,8 +981,6 @@ MARS_DEV void softmax(const Pipe& p) {
     }
     between = flags & kLast;
     const int sb = t % kBufs;
-    // the converters have left the scales of own rows (K's before S, this is for V's)
-    if ((flags & kOwn) && !p.warp_wait(&p.bar.f_full[1][t % kTiles], (t / kTiles) & 1)) return;
     // keys of this thread that its row sees
     const int limit = ((flags & kOwn) ? min(f.count, tok + 1 - f.k0) : f.count) - half * kKeys;
     if (!p.warp_wait(&p.bar.s_full[sb], (t / kBufs) & 1)) return;
@@ -865,10 +1004,14 @@ MARS_DEV void softmax(const Pipe& p) {
         add[g] = v ? __int_as_float(0x4b000000 | v) - (8388608.f + q8::kBias) : -INFINITY;
       }
       tmem_ld_wait();
-      if (__any_sync(0xffffffffu, limit < kKeys)) {
+      if (__any_sync(0xffffffffu, limit < kKeys) || (flags & kHoles)) {
 #pragma unroll
-        for (int e = 0; e < kKeys; ++e)
-          if (e >= limit) r[e] = 0xff800000u;
+        for (int g = 0; g < kGroups; ++g) {
+          const int seen = ((vb >> (8 * g)) & 255) ? limit - 16 * g : 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (e >= seen) r[16 * g + e] = 0xff800000u;
+        }
       }
       // s + e, in place, and its maximum
 #pragma unroll
@@ -936,7 +1079,9 @@ MARS_DEV void softmax(const Pipe& p) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, 1)
+chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+             Args a) {
   using namespace sm100;
   using L = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -952,17 +1097,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Args a) {
     bar.abort = 0;
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&bar.info_full[i], 1);
-      // both issuers, the converters' warps, the softmax's
-      mbar_init(&bar.info_empty[i], 2 + kConvertWarps + kSoftmaxWarps);
+      // the copies of K, both issuers, the converters' warps, the softmax's
+      mbar_init(&bar.info_empty[i], 3 + kConvertWarps + kSoftmaxWarps);
     }
     for (int i = 0; i < kConvertWarps * kRaw; ++i) mbar_init(&bar.raw_full[i / kRaw][i % kRaw], 1);
-    for (int h = 0; h < 2; ++h) {
-      for (int i = 0; i < kTiles; ++i) {
-        mbar_init(&bar.f_full[h][i], kConvertWarps / 2);
-        mbar_init(&bar.f_empty[h][i], 1);
-      }
-      mbar_init(&bar.drain[h], 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bar.k_full[i], 1);
+      mbar_init(&bar.k_empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.own_free[i], 1);
+      mbar_init(&bar.own_full[i], kConvertWarps);
+    }
+    for (int i = 0; i < kTiles; ++i) {
+      mbar_init(&bar.v_full[i], kConvertWarps);
+      mbar_init(&bar.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.drain[i], 1);
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_full[i], 32 * kSoftmaxWarps);
@@ -989,7 +1140,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Args a) {
     regs_lower<kControlRegs>();
     if (warp == 0) {
       walk<D>(p, scan);
-    } else if (warp > 1 && elect_one()) {
+    } else if (warp == 1) {
+      load_k<D>(p, tm_k);
+    } else if (elect_one()) {
       if (warp == 2) issue_s<D>(p); else issue_pv<D>(p);
     }
   } else if (warp < kConvertWarp) {
@@ -997,10 +1150,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Args a) {
     softmax<D>(p);
   } else {
     regs_lower<kConvertRegs>();
-    convert<D>(p);
+    convert<D>(p, tm_v);
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && bar.abort && a.status) atomicOr(a.status, MARS_ST_TIMEOUT);
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(p.tmem, 512);
@@ -1192,7 +1346,17 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   static std::atomic<int> attr[64];
   cudaError_t e = set_smem_limit_once(chunk_kernel<D>, L::TOTAL, attr);
   if (e != cudaSuccess) return e;
-  chunk_kernel<D><<<plan.ctas, kThreads, L::TOTAL, stream>>>(a);
+  // a page and KV head is 16 rows of the maps; an empty pool is never read (one page over q)
+  CUtensorMap map_k, map_v;
+  const bool any = t.num_pages > 0;
+  const uint64_t dims[2] = {(uint64_t)D, (any ? (uint64_t)t.num_pages * t.hkv : 1) * kPageSize};
+  const uint64_t pitch[1] = {(uint64_t)D};
+  const uint32_t box[2] = {(uint32_t)D, (uint32_t)kPageSize};
+  const void* none = t.q;
+  if (!encode_tmap_u8(&map_k, any ? p.k_pool : none, 2, dims, pitch, box) ||
+      !encode_tmap_u8(&map_v, any ? p.v_pool : none, 2, dims, pitch, box))
+    return cudaErrorInvalidValue;
+  chunk_kernel<D><<<plan.ctas, kThreads, L::TOTAL, stream>>>(map_k, map_v, a);
   count_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess || !plan.can_split) return e;

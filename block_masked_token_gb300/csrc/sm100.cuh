@@ -342,6 +342,17 @@ MARS_DEV void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint3
       : "memory");
 }
 
+// The same with 8-bit operands, kind::f8f6f4 (K = 32 per instruction).
+MARS_DEV void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16. A (M = 128 rows) lives in TMEM with
 // row = lane and two bf16 per 32-bit column (even element in the low half): one K = 16
 // step spans 8 columns.
@@ -456,6 +467,12 @@ MARS_DEV uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return d;
 }
 
+// The same for a K-major tile of 64-byte rows in 64-byte swizzle: 8-row atoms of 512 bytes, chunks
+// of 16 bytes XORed with address bits 7..8.
+MARS_DEV uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (sdesc_sw128(saddr, lbo, sbo) & ~((uint64_t)7 << 61)) | (uint64_t)4 << 61;
+}
+
 // The descriptor of the same layout `bytes` further on: only the start-address field
 // changes (shared-memory addresses stay below 256 KB, so the field does not carry).
 MARS_DEV uint64_t sdesc_advance(uint64_t desc, uint32_t bytes) {
@@ -472,7 +489,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_ma
          | ((uint32_t)(M >> 4) << 24);           // M / 16
 }
 
-// The same with f16 A and B.
+// e4m3 A and B (kind::f8f6f4), fp32 D, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same as idesc_bf16_f32 with f16 A and B.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
   return idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
@@ -492,5 +514,8 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64
                       const uint64_t* strides_bytes, const uint32_t* box);
 bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                      const uint64_t* strides_bytes, const uint32_t* box);
+// Bytes, in boxes whose rows are box[0] bytes (64 or 128), swizzled over as many.
+bool encode_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides_bytes, const uint32_t* box);
 
 }  // namespace mars

@@ -27,7 +27,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 namespace {
 
 bool encode_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank,
-                 const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box) {
+                 const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto fn = encode_fn();
   if (!fn || rank < 1 || rank > 5) return false;
   cuuint64_t gdim[5], gstride[4];
@@ -39,7 +40,7 @@ bool encode_tmap(CUtensorMap* map, CUtensorMapDataType type, const void* base, i
   }
   for (int i = 0; i + 1 < rank; ++i) gstride[i] = strides_bytes[i];
   CUresult r = fn(map, type, (cuuint32_t)rank, const_cast<void*>(base), gdim, gstride, bdim,
-                  estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -54,6 +55,12 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64
 bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                      const uint64_t* strides_bytes, const uint32_t* box) {
   return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, rank, dims, strides_bytes, box);
+}
+
+bool encode_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides_bytes, const uint32_t* box) {
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides_bytes, box,
+                     box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace mars
