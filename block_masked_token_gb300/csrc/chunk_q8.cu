@@ -54,7 +54,8 @@ static_assert(128 * (kControlRegs + 2 * kSoftmaxRegs + kConvertRegs) <=
                   kThreads * (65536 / kThreads / 8 * 8),
               "the register split fits the launch's register pool");
 constexpr int kRaw = 4;              // ring of raw tiles of V
-constexpr int kSlots = 4;            // ring of tiles of K's codes; an own tile takes two slots
+constexpr int kSlots = 4;            // ring of tiles of K's codes; an own tile takes two slots, and so
+                                     // does an item's Q in bf16, before its first tile
 constexpr int kAhead = 3;            // tiles that copies may be ahead of the conversion
 constexpr int kTiles = 2;            // f16 tiles of V
 constexpr int kBufs = 3;             // S buffers in TMEM
@@ -270,7 +271,8 @@ struct alignas(16) Info {
   int base, n, tok0, h0, kvh;        // its item
   int slot;                          // of the partial, -1: the item is whole
   int k0, count;                     // first key (own: token of the sequence), keys that there are
-  int pad[3];
+  int q_slot;                        // first tile of a part: where its Q lies in K's ring
+  int pad[2];
   alignas(16) int page[kPagesPerTile];         // -1: not to be read
   alignas(8) uint8_t k_byte[kPagesPerTile];    // scale bytes; own tiles: written by the converters
   alignas(8) uint8_t v_byte[kPagesPerTile];    // 0: no such keys
@@ -285,11 +287,12 @@ struct Bar {
   uint64_t k_full[kSlots], k_empty[kSlots], own_free[2], own_full[2];
   uint64_t v_full[kTiles], v_empty[kTiles];
   uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
-  uint64_t q_full, drain[2];
+  uint64_t q_raw, q_full, drain[2];
   uint64_t pair[4];                  // the two warps of 32 rows
   uint32_t tmem_base;
   int abort;
   uint16_t exchange[2][2][BQ];       // [use][half][row]
+  uint8_t q_byte[2][BQ];             // [item][row]: scale bytes of Q
 };
 
 // All that is not a tile. Its size keeps what follows, the tiles, aligned to 1024 bytes: they leave
@@ -376,7 +379,7 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
   const Args& a = p.a;
   const int lane = threadIdx.x & 31;
   Record rec{};
-  int t = 0, flags = 0;
+  int t = 0, flags = 0, slots = 0;
   bool ok = true;
   // wait until `n` entries from t on are free
   auto room = [&](int n) {
@@ -441,12 +444,14 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
       e.slot = slot;
       e.k0 = k0;
       e.count = count;
+      e.q_slot = slots % kSlots;
     };
     for (int x = j; x < own && ok; ++x) {
       if (!(ok = room(1))) break;
       if (lane == 0)
         entry(p.info(t), x * BKV, min(last_tok + 1 - x * BKV, BKV),
               kOwn | first | (left == 1 ? kLast : 0));
+      slots += first ? 4 : 2;
       first = 0;
       --left;
       publish(1);
@@ -471,17 +476,6 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
         kb = (uint8_t)q8::scale_byte(a.k_scale[at]);
         vb = (uint8_t)q8::scale_byte(a.v_scale[at]);
       }
-      // The pages' lines are asked for here, to be in L2 when warp 1 copies them: a copy out of DRAM
-      // takes some 4,500 cycles, which the ring of raw tiles could not cover.
-      constexpr int kLines = Layout<D>::PAGE / 128;
-      const size_t from = ((size_t)max(e, 0) * a.hkv + kvh) * Layout<D>::PAGE;
-      const uint32_t pages = __ballot_sync(0xffffffffu, readable);
-#pragma unroll 1
-      for (uint32_t left_pages = pages; left_pages; left_pages &= left_pages - 1) {
-        const size_t at = __shfl_sync(0xffffffffu, from, __ffs(left_pages) - 1);
-        if (lane < 2 * kLines)
-          prefetch_l2((lane < kLines ? a.k_pool : a.v_pool) + at + (lane % kLines) * 128);
-      }
       if (!(ok = room(n))) break;
       if (lane < n * kPagesPerTile) {
         const int g = lane % kPagesPerTile, u = lane / kPagesPerTile;
@@ -494,6 +488,7 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
                 (u == 0 ? first : 0) | (u + 1 == left ? kLast : 0) |
                     (((holes >> lane) & 0xffu) ? kHoles : 0));
       }
+      slots += first ? n + 2 : n;
       first = 0;
       left -= n;
       publish(n);
@@ -513,14 +508,15 @@ MARS_DEV uint8_t* chunk_at(uint8_t* tile, int r, int c) {
   return tile + (c >> 3) * (BKV * 128) + flash::sw_off(r, c & 7);
 }
 
-// Warp 1: K's codes, a copy per page. The slots of an own tile are only taken, for the converters.
+// Warp 1: K's codes, a copy per page, and before an item's first tile its Q in bf16, half of the
+// elements of its rows in either of two slots. Those of an own tile are only taken, for the converters.
 template <int D>
-MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map) {
+MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& map_q) {
   using namespace sm100;
   using L = Layout<D>;
   const Args& a = p.a;
   const int lane = threadIdx.x & 31;
-  int c = 0, own = 0;                                // slots taken, own tiles
+  int c = 0, own = 0, q_loads = 0;                   // slots taken, own tiles, halves of Q
   bool ok = true;
   for (int t = 0; ok && p.warp_wait_info(t); ++t) {
     const Info& f = p.info(t);
@@ -529,14 +525,26 @@ MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map) {
     const int page = lane < kPagesPerTile && !(flags & kOwn) ? f.page[lane] : -1;
     const int pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
     const int row = (max(page, 0) * a.hkv + f.kvh) * kPageSize;
+    // slots for: halves of Q (i < 0), then the tile
+    const int q = flags & kFirst ? 2 : 0;
 #pragma unroll 1
-    for (int i = 0; i < (flags & kOwn ? 2 : 1); ++i, ++c) {
+    for (int i = -q; i < (flags & kOwn ? 2 : 1); ++i, ++c) {
       const int st = c % kSlots;
+      uint8_t* dst = p.smem + L::OFF_K + st * L::RAW;
       if (!(ok = p.warp_wait(&p.bar.k_empty[st], ((c / kSlots) & 1) ^ 1))) break;
-      if (lane == 0) mbar_arrive_expect_tx(&p.bar.k_full[st], pages * L::PAGE);
+      // both slots before the first half, so that the second always follows
+      if (i == -2 && !(ok = p.warp_wait(&p.bar.k_empty[(c + 1) % kSlots], (((c + 1) / kSlots) & 1) ^ 1))) break;
+      if (lane == 0) mbar_arrive_expect_tx(&p.bar.k_full[st], i < 0 ? 0 : pages * L::PAGE);
       __syncwarp();
-      if (page >= 0)
-        tma_load_2d(p.smem + L::OFF_K + st * L::RAW + lane * L::PAGE, &map, &p.bar.k_full[st], 0, row);
+      if (i < 0) {
+        if (lane == 0) {
+          if (i == -2) mbar_arrive_expect_tx(&p.bar.q_raw, a.gp * a.tpt * D * 2);
+          tma_load_3d(dst, &map_q, &p.bar.q_raw, (i + 2) * (D / 2), f.h0, f.base + f.tok0);
+        }
+        ++q_loads;
+      } else if (page >= 0) {
+        tma_load_2d(dst + lane * L::PAGE, &map, &p.bar.k_full[st], 0, row);
+      }
     }
     if (ok && (flags & kOwn)) {
       if (lane == 0) mbar_arrive(&p.bar.own_free[own & 1]);
@@ -549,6 +557,7 @@ MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map) {
 #pragma unroll 1
     for (int i = max(0, c - kSlots); i < c; ++i)
       p.drain(&p.bar.k_full[i % kSlots], (i / kSlots) & 1);
+  if (lane == 0 && q_loads > 0) p.drain(&p.bar.q_raw, (q_loads / 2 - 1) & 1);
   __syncwarp();
 }
 
@@ -708,6 +717,7 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map) {
     Info& f = p.info(t);
     const int flags = f.flags, ts = t % kTiles;
     if (flags & kEnd) break;
+    if (flags & kFirst) slots += 2;                  // Q's
     uint8_t* tile = p.smem + L::OFF_V + ts * L::TILE;
     if (flags & kOwn) {
       // both scales and K before S, for which warp 1 has taken two slots; V before P V
@@ -773,7 +783,17 @@ MARS_DEV void issue_s(const Pipe& p) {
     if (flags & kEnd) break;
     mbar_arrive(&p.bar.info_empty[t % kInfos]);
     const int sb = t % kBufs;
-    if ((flags & kFirst) && !p.wait(&p.bar.q_full, items++ & 1)) break;
+    if (flags & kFirst) {
+      // the softmax has turned Q's two slots into its parts
+      if (!p.wait(&p.bar.q_full, items++ & 1)) break;
+      bool here = true;
+#pragma unroll 1
+      for (int i = 0; here && i < 2; ++i, ++slots) {
+        here = p.wait(&p.bar.k_full[slots % kSlots], (slots / kSlots) & 1);
+        mbar_arrive(&p.bar.k_empty[slots % kSlots]);
+      }
+      if (!here) break;
+    }
     if (flags & kOwn) {
       if (!p.wait(&p.bar.own_full[own & 1], (own >> 1) & 1)) break;
       ++own;
@@ -834,12 +854,6 @@ MARS_DEV void issue_pv(const Pipe& p) {
 struct Pair {
   const Pipe& p;
   int row, half, uses;
-  MARS_DEV bool meet() {
-    uint64_t* b = &p.bar.pair[row / 32];
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(b);
-    return p.warp_wait(b, uses++ & 1);
-  }
   // 16 bits for the other thread, and its own
   MARS_DEV void give(uint32_t mine) {
     p.bar.exchange[uses & 1][half][row] = (uint16_t)mine;
@@ -854,54 +868,72 @@ struct Pair {
   }
 };
 
-// This thread's half of its query row of the item that tile t begins, as two e4m3 numbers each into
-// Q; factor: of the row's scores. A row without a token is zero.
+// Q of the item that tile t begins (its `item`-th), out of K's ring: each row over the power of two
+// that brings its largest finite magnitude into [128, 256), as two e4m3 numbers. A warp takes every
+// eighth row, a lane D / 32 elements of it; rows without a token stay what they are. (Short, because
+// it runs once per item: loads and stores of a thread's own row, unrolled, took 25,000 cycles, most
+// of them for instructions.)
 template <int D>
-MARS_DEV bool load_q(const Pipe& p, Pair& pair, int t, float& factor) {
+MARS_DEV bool convert_q(const Pipe& p, int t, int item) {
+  using namespace sm100;
   using L = Layout<D>;
-  constexpr int kChunks = D / 32;                    // of 16 elements, of the half
   const Args& a = p.a;
   const Info& f = p.info(t);
-  const int row = pair.row, tok = f.tok0 + row / a.gp, h = f.h0 + row % a.gp;
-  const bool has = row < a.gp * a.tpt && tok < f.n;
-  const uint4* src = reinterpret_cast<const uint4*>(
-      a.q + ((size_t)f.base + tok) * a.q_stride + (size_t)h * D + pair.half * (D / 2));
-  uint32_t top = 0;
-  if (has) {
-#pragma unroll
-    for (int c = 0; c < 2 * kChunks; ++c) {
-      const uint4 x = src[c];
-      top = finite_max(finite_max(finite_max(finite_max(top, x.x), x.y), x.z), x.w);
-    }
-  }
-  top = max(top >> 16, top & 0xffffu);
-  uint32_t other;
-  pair.give(top);
-  if (!pair.take(other)) return false;
-  top = max(top, other);
-  // the power of two that brings the row's largest finite magnitude into [128, 256) (rows of next to
-  // nothing: 2^-53)
-  const int byte = top ? min(max((int)(top >> 7), 74), 253) - 7 : 127;
-  const float inv = q8::inverse_power(byte);
+  const int warp = (threadIdx.x >> 5) - kSoftmaxWarp, lane = threadIdx.x & 31;
+  if (!p.warp_wait(&p.bar.q_raw, item & 1)) return false;
+  const int rows = a.gp * min(a.tpt, f.n - f.tok0), byte_in = lane % 16 * (D / 16), byte_out = lane * (D / 32);
+  const uint8_t* from = p.smem + L::OFF_K + (f.q_slot + lane / 16) % kSlots * L::RAW;
   uint8_t* to = p.smem + L::OFF_Q;
-#pragma unroll 1
-  for (int c = 0; c < kChunks; ++c) {
-    const uint32_t at = L::code_at(row, pair.half * kChunks + c);
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    split16(has ? src[2 * c] : none, has ? src[2 * c + 1] : none, inv, to + at, to + L::RAW + at);
+#pragma unroll 2
+  for (int r = warp; r < rows; r += kSoftmaxWarps) {
+    const uint8_t* src = from + L::code_at(r, byte_in / 16) + byte_in % 16;
+    uint32_t w[2] = {0u, 0u};
+    if (D == 128) {
+      const uint2 x = *reinterpret_cast<const uint2*>(src);
+      w[0] = x.x;
+      w[1] = x.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(src);
+    }
+    uint32_t top = finite_max(finite_max(0u, w[0]), w[1]);
+    top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+    // (a row of next to nothing: 2^-53)
+    const int byte = top ? min(max((int)(top >> 7), 74), 253) - 7 : q8::kBias;
+    const float inv = q8::inverse_power(byte);
+    uint32_t u[2], v[2];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      // an infinity becomes NaN (a finite value's second product adds nothing)
+      const float x = __uint_as_float(w[i] << 16), y = __uint_as_float(w[i] & 0xffff0000u);
+      const float e0 = fmaf(x, 0.f, x * inv), e1 = fmaf(y, 0.f, y * inv);
+      u[i] = q8::encode2(e0, e1);
+      uint32_t lo, hi;
+      q8::decode4(u[i], lo, hi);
+      const float2 near = q8::halves(lo);
+      v[i] = q8::encode2(e0 - near.x, e1 - near.y);
+    }
+    uint8_t* dst = to + L::code_at(r, byte_out / 16) + byte_out % 16;
+    if (D == 128) {
+      *reinterpret_cast<uint32_t*>(dst) = u[0] | (u[1] << 16);
+      *reinterpret_cast<uint32_t*>(dst + L::RAW) = v[0] | (v[1] << 16);
+    } else {
+      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)u[0];
+      *reinterpret_cast<uint16_t*>(dst + L::RAW) = (uint16_t)v[0];
+    }
+    if (lane == 0) p.bar.q_byte[item & 1][r] = (uint8_t)byte;
   }
-  sm100::fence_proxy_async_smem();
-  sm100::mbar_arrive_warp(&p.bar.q_full);
-  factor = a.scale_log2 * q8::power(byte);
-  return true;
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&p.bar.q_full);
+  return p.warp_wait(&p.bar.q_full, item & 1);
 }
 
 // Factor of a row's O. l is 0 where every score is -infinity (O is then 0), NaN where one is NaN or
 // +infinity.
 MARS_DEV float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
-// This thread's half of its row of O out of TMEM: divided by the row's sum to where the row is (at),
-// or into a partial.
+// This thread's half of its row of O out of TMEM: divided by the row's sum to where the row is, or
+// into a partial.
 template <int D>
 MARS_DEV void store_o(const Pipe& p, const Pair& pair, int slot, bool has, long long at, float m,
                       float l) {
@@ -915,17 +947,23 @@ MARS_DEV void store_o(const Pipe& p, const Pair& pair, int slot, bool has, long 
   if (slot >= 0 && has && pair.half == 0)
     reinterpret_cast<float2*>(part + BQ * D / 4)[row] = make_float2(m, l);
 #pragma unroll 1
-  for (int c = pair.half * (D / 64); c < (pair.half + 1) * (D / 64); ++c) {
-    uint32_t o[32];
-    tmem_ld32(o_addr + c * 32, o);
+  for (int c = pair.half * (D / 32); c < (pair.half + 1) * (D / 32); ++c) {
+    uint32_t o[16];
+    tmem_ld16(o_addr + c * 16, o);
     tmem_ld_wait();
+    if (!has) continue;
     if (slot < 0) {
-      packed::store_rows<32>(a.o + c * 32, has ? at : -1, threadIdx.x & 31,
-                             [&](int e) { return __uint_as_float(o[e]) * inv; });
-    } else if (has) {
+      uint32_t w[8];
 #pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        part[(c * 8 + e / 4) * BQ + row] =
+      for (int e = 0; e < 8; ++e)
+        w[e] = flash::pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+      uint4* to = reinterpret_cast<uint4*>(a.o + at + c * 16);
+      to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        part[(c * 4 + e / 4) * BQ + row] =
             make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                         __uint_as_float(o[e + 3]));
     }
@@ -944,49 +982,26 @@ MARS_DEV void softmax(const Pipe& p) {
   const int row = pair.row, half = pair.half;
   const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
   float factor = 0.f, m = -INFINITY, l = 0.f;
-  int tok = 0, t = -1, slot = -1, base = 0, h0 = 0;
-  bool has = false, busy = false, between = true;
+  int tok = 0, t = -1, slot = -1, base = 0, h0 = 0, items = 0, flags = kLast;
+  bool has = false, busy = false;
   for (;;) {
-    if (between) {
-      // every S of the item is done: Q of the next one, then this one's O
-      if (!p.warp_wait_info(t + 1)) return;
-      const bool end = p.info(t + 1).flags & kEnd;
-      // the row's sum, through its place in Q, which is free now
-      float* sums = reinterpret_cast<float*>(p.smem + L::OFF_Q + row * D);
-      sums[half] = l;
-      if (!pair.meet()) return;
-      const float sum = sums[0] + sums[1];
-      if (!end && !load_q<D>(p, pair, t + 1, factor)) return;
-      if (t >= 0 && !p.warp_wait(&p.bar.pv_done[t % kBufs], (t / kBufs) & 1)) return;
-      if (busy) {
-        tc_fence_after();
-        store_o<D>(p, pair, slot, has, (((long long)base + tok) * a.hq + h0 + row % a.gp) * D, m, sum);
-        tc_fence_before();
-      }
-      if (end) return;
-    }
-    ++t;
-    if (!p.warp_wait_info(t)) return;
-    const Info& f = p.info(t);
-    const int flags = f.flags;
-    if (between) {
-      m = -INFINITY;
-      l = 0.f;
-      slot = f.slot;
-      base = f.base;
-      h0 = f.h0;
-      tok = f.tok0 + row / a.gp;
-      has = row < a.gp * a.tpt && tok < f.n;
-      busy = __any_sync(0xffffffffu, has);       // warps without rows only keep step
-    }
-    between = flags & kLast;
+    // tile t; before the first one t = -1
     const int sb = t % kBufs;
-    // keys of this thread that its row sees
-    const int limit = ((flags & kOwn) ? min(f.count, tok + 1 - f.k0) : f.count) - half * kKeys;
-    if (!p.warp_wait(&p.bar.s_full[sb], (t / kBufs) & 1)) return;
-    tc_fence_after();
-    const uint32_t kb = *reinterpret_cast<const uint32_t*>(f.k_byte + half * kGroups);
-    const uint32_t vb = *reinterpret_cast<const uint32_t*>(f.v_byte + half * kGroups);
+    if (t >= 0) {
+      if (!p.warp_wait(&p.bar.s_full[sb], (t / kBufs) & 1)) return;
+      tc_fence_after();
+    }
+    if (flags & kLast) {
+      // every S of the item is done: the next one's Q, so that its S runs beside what follows here
+      if (!p.warp_wait_info(t + 1)) return;
+      if (!(p.info(t + 1).flags & kEnd) && !convert_q<D>(p, t + 1, items++)) return;
+    }
+    if (t >= 0) {
+      const Info& f = p.info(t);
+      // keys of this thread that its row sees
+      const int limit = ((flags & kOwn) ? min(f.count, tok + 1 - f.k0) : f.count) - half * kKeys;
+      const uint32_t kb = *reinterpret_cast<const uint32_t*>(f.k_byte + half * kGroups);
+      const uint32_t vb = *reinterpret_cast<const uint32_t*>(f.v_byte + half * kGroups);
     if (busy) {
       const uint32_t s_addr = p.tmem + L::TM_S + sb * BKV + lane_off;
       uint32_t r[kKeys];
@@ -1072,16 +1087,46 @@ MARS_DEV void softmax(const Pipe& p) {
       tmem_st32(s_addr + L::P_OFF + half * (kKeys / 2), packed);
       tmem_st_wait();
     }
-    tc_fence_before();
-    mbar_arrive_warp(&p.bar.p_full[sb]);
-    p.warp_done(t);
+      tc_fence_before();
+      mbar_arrive_warp(&p.bar.p_full[sb]);
+      p.warp_done(t);
+      if ((flags & kLast) && busy) {
+        // the row's sum
+        const uint32_t mine = __float_as_uint(l);
+        uint32_t lo, hi;
+        pair.give(mine & 0xffffu);
+        if (!pair.take(lo)) return;
+        pair.give(mine >> 16);
+        if (!pair.take(hi) || !p.warp_wait(&p.bar.pv_done[sb], (t / kBufs) & 1)) return;
+        tc_fence_after();
+        store_o<D>(p, pair, slot, has, (((long long)base + tok) * a.hq + h0 + row % a.gp) * D, m,
+                   l + __uint_as_float(lo | (hi << 16)));
+        tc_fence_before();
+      }
+    }
+    ++t;
+    if (!p.warp_wait_info(t)) return;
+    const Info& f = p.info(t);
+    flags = f.flags;
+    if (flags & kEnd) return;
+    if (flags & kFirst) {
+      m = -INFINITY;
+      l = 0.f;
+      slot = f.slot;
+      base = f.base;
+      h0 = f.h0;
+      tok = f.tok0 + row / a.gp;
+      has = row < a.gp * a.tpt && tok < f.n;
+      busy = __any_sync(0xffffffffu, has);       // warps without rows only keep step
+      factor = has ? a.scale_log2 * q8::power(p.bar.q_byte[(items - 1) & 1][row]) : 1.f;
+    }
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-             Args a) {
+             const __grid_constant__ CUtensorMap tm_q, Args a) {
   using namespace sm100;
   using L = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1119,7 +1164,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       mbar_init(&bar.p_full[i], 32 * kSoftmaxWarps);
       mbar_init(&bar.pv_done[i], 1);
     }
-    mbar_init(&bar.q_full, 32 * kSoftmaxWarps);
+    mbar_init(&bar.q_raw, 1);
+    mbar_init(&bar.q_full, kSoftmaxWarps);
     for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
     fence_barrier_init();
   }
@@ -1141,7 +1187,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     if (warp == 0) {
       walk<D>(p, scan);
     } else if (warp == 1) {
-      load_k<D>(p, tm_k);
+      load_k<D>(p, tm_k, tm_q);
     } else if (elect_one()) {
       if (warp == 2) issue_s<D>(p); else issue_pv<D>(p);
     }
@@ -1347,7 +1393,7 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   cudaError_t e = set_smem_limit_once(chunk_kernel<D>, L::TOTAL, attr);
   if (e != cudaSuccess) return e;
   // a page and KV head is 16 rows of the maps; an empty pool is never read (one page over q)
-  CUtensorMap map_k, map_v;
+  CUtensorMap map_k, map_v, map_q;
   const bool any = t.num_pages > 0;
   const uint64_t dims[2] = {(uint64_t)D, (any ? (uint64_t)t.num_pages * t.hkv : 1) * kPageSize};
   const uint64_t pitch[1] = {(uint64_t)D};
@@ -1356,7 +1402,11 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   if (!encode_tmap_u8(&map_k, any ? p.k_pool : none, 2, dims, pitch, box) ||
       !encode_tmap_u8(&map_v, any ? p.v_pool : none, 2, dims, pitch, box))
     return cudaErrorInvalidValue;
-  chunk_kernel<D><<<plan.ctas, kThreads, L::TOTAL, stream>>>(map_k, map_v, a);
+  const uint64_t q_dims[3] = {(uint64_t)D, (uint64_t)t.hq, (uint64_t)t.total};
+  const uint64_t q_pitch[2] = {(uint64_t)D * 2, (uint64_t)t.q_stride * 2};
+  const uint32_t q_box[3] = {D / 2, (uint32_t)plan.gp, (uint32_t)plan.tpt};
+  if (!encode_tmap_bf16_rows(&map_q, t.q, 3, q_dims, q_pitch, q_box)) return cudaErrorInvalidValue;
+  chunk_kernel<D><<<plan.ctas, kThreads, L::TOTAL, stream>>>(map_k, map_v, map_q, a);
   count_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess || !plan.can_split) return e;

@@ -219,11 +219,6 @@ MARS_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* ba
       : "memory");
 }
 
-// Ask for the line at p to be brought into L2.
-MARS_DEV void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
 // Per-thread register count of the calling warpgroup (all 128 threads, warp-uniform):
 // raise to or lower to N (a multiple of 8 in [24, 256]). Raises draw on the registers the
 // block was launched with (threads x registers per thread), which the lowered warpgroups
@@ -514,6 +509,9 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64
                       const uint64_t* strides_bytes, const uint32_t* box);
 bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                      const uint64_t* strides_bytes, const uint32_t* box);
+// bf16 in boxes whose rows are box[0] = 32 or 64 elements, swizzled over as many bytes.
+bool encode_tmap_bf16_rows(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                           const uint64_t* strides_bytes, const uint32_t* box);
 // Bytes, in boxes whose rows are box[0] bytes (64 or 128), swizzled over as many.
 bool encode_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                     const uint64_t* strides_bytes, const uint32_t* box);
