@@ -25,11 +25,12 @@
 // Roles (512 threads): warp 0 walks the items and reads block table and scales ahead of the others
 // (infos); warp 1 copies K; warps 12..15 copy two pages of V each into a ring of their own and turn
 // them into 32 rows of a swizzled f16 tile, zero where no key may be read; warps 2 and 3 issue
-// S and O += P' V; warps 4..11 run the softmax, load Q and store O: a thread has a row, warps
-// 4..7 the first half of its keys and columns, 8..11 the second, and the two of a row exchange their
-// maxima and sums. What a warp runs per tile is kept short: with one warp per row, whose code for 128
-// keys no other shared, the code of all roles left the instruction cache within every tile, and a
-// tile took 5,000 cycles.
+// S and O += P' V; warps 4..7 run the softmax of even tiles, 8..11 that of odd ones, a thread per
+// row, each with an S buffer, an O, a maximum and a sum of its own, which are joined at an item's end.
+// (With half of every tile's keys each, the exchange of maxima and the waits took longer than the
+// softmax.) What a warp runs per tile is kept short: the code of all roles has to stay in some 32 KB
+// of instruction cache. When it did not, a tile took 5,000 cycles; and what runs once per item
+// costs some 40 cycles per instruction.
 //
 // A cut inside an item leaves partials (m', l, O) that merge_kernel joins in the order of the keys.
 #include <algorithm>
@@ -58,7 +59,7 @@ constexpr int kSlots = 4;            // ring of tiles of K's codes; an own tile 
                                      // does an item's Q in bf16, before its first tile
 constexpr int kAhead = 3;            // tiles that copies may be ahead of the conversion
 constexpr int kTiles = 2;            // f16 tiles of V
-constexpr int kBufs = 3;             // S buffers in TMEM
+constexpr int kBufs = 2;             // S buffers, and O's, in TMEM: of even and odd tiles
 // Tiles that the walk may be ahead. It publishes up to four at once, the converters wait for up to
 // kAhead more than they have released, and with this many the slots that it then needs belong to
 // tiles that every converter has released.
@@ -263,7 +264,7 @@ struct Window {
 
 // --------------------------------------------------------------------------------- the pipeline
 
-enum : int { kFirst = 1, kLast = 2, kOwn = 4, kEnd = 8, kHoles = 16 };
+enum : int { kFirst = 1, kLast = 2, kOwn = 4, kEnd = 8, kHoles = 16, kSecond = 32 };
 
 // A key tile as the walk hands it to the other warps.
 struct alignas(16) Info {
@@ -281,17 +282,17 @@ struct alignas(16) Info {
 struct Bar {
   uint64_t info_full[kInfos], info_empty[kInfos];
   uint64_t raw_full[kConvertWarps][kRaw];              // of a warp's two pages
-  // own_free: two slots are free for an own tile, own_full: its scales and K are there. (Barriers of
-  // their own: a wait for a phase of a ring whose last one is still open would pass at once. Two of
-  // each: the slots let two own tiles be under way.)
-  uint64_t k_full[kSlots], k_empty[kSlots], own_free[2], own_full[2];
+  // own_raw: an own tile's K in bf16 is in its two slots, own_full: its scales and its two parts are.
+  // (Barriers of their own: a wait for a phase of a ring whose last one is still open would pass at
+  // once. Two of each: the slots let two own tiles be under way.)
+  uint64_t k_full[kSlots], k_empty[kSlots], own_raw[2], own_full[2], own_v[2];
   uint64_t v_full[kTiles], v_empty[kTiles];
   uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
-  uint64_t q_raw, q_full, drain[2];
+  uint64_t q_raw, q_full, o_free, drain[2];
   uint64_t pair[4];                  // the two warps of 32 rows
   uint32_t tmem_base;
   int abort;
-  uint16_t exchange[2][2][BQ];       // [use][half][row]
+  float exchange[2][BQ];             // [even or odd tiles][row]
   uint8_t q_byte[2][BQ];             // [item][row]: scale bytes of Q
 };
 
@@ -311,7 +312,7 @@ struct Layout {
   static constexpr int OFF_Q = 0, OFF_K = 2 * RAW, OFF_V = OFF_K + kSlots * RAW;
   static constexpr int OFF_RAW = OFF_V + kTiles * TILE;
   static constexpr int TOTAL = OFF_RAW + kRaw * RAW;
-  static constexpr int TM_S = 0, TM_O = kBufs * BKV, P_OFF = BKV / 2;
+  static constexpr int TM_S = 0, TM_O = kBufs * BKV, P_OFF = BKV / 2;    // O: D columns each
   static constexpr int PART = BQ * D / 4 + BQ / 2;                   // float4 of a partial
   // 8-bit operands: rows of D bytes, 16-byte chunk c of row r, swizzled over D bytes
   static MARS_DEV uint32_t code_at(int r, int c) {
@@ -451,8 +452,8 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
       if (lane == 0)
         entry(p.info(t), x * BKV, min(last_tok + 1 - x * BKV, BKV),
               kOwn | first | (left == 1 ? kLast : 0));
-      slots += first ? 4 : 2;
-      first = 0;
+      slots += first & kFirst ? 4 : 2;
+      first = first & kFirst ? kSecond : 0;
       --left;
       publish(1);
     }
@@ -485,11 +486,11 @@ MARS_DEV void walk(const Pipe& p, const Scan& sc) {
         f.v_byte[g] = vb;
         if (g == 0)
           entry(f, mine * BKV, min(q.P - mine * BKV, BKV),
-                (u == 0 ? first : 0) | (u + 1 == left ? kLast : 0) |
+                (u == 0 ? first : u == 1 && first == kFirst ? kSecond : 0) | (u + 1 == left ? kLast : 0) |
                     (((holes >> lane) & 0xffu) ? kHoles : 0));
       }
-      slots += first ? n + 2 : n;
-      first = 0;
+      slots += first & kFirst ? n + 2 : n;
+      first = first & kFirst && n == 1 ? kSecond : 0;
       left -= n;
       publish(n);
     }
@@ -508,15 +509,16 @@ MARS_DEV uint8_t* chunk_at(uint8_t* tile, int r, int c) {
   return tile + (c >> 3) * (BKV * 128) + flash::sw_off(r, c & 7);
 }
 
-// Warp 1: K's codes, a copy per page, and before an item's first tile its Q in bf16, half of the
-// elements of its rows in either of two slots. Those of an own tile are only taken, for the converters.
+// Warp 1: K's codes, a copy per page. Before an item's first tile its Q, and for an own tile K, in
+// bf16: half of the elements of the rows in either of two slots.
 template <int D>
-MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& map_q) {
+MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& map_q,
+                     const CUtensorMap& map_own) {
   using namespace sm100;
   using L = Layout<D>;
   const Args& a = p.a;
   const int lane = threadIdx.x & 31;
-  int c = 0, own = 0, q_loads = 0;                   // slots taken, own tiles, halves of Q
+  int c = 0, own = 0, qs = 0;                        // slots taken, own tiles, items
   bool ok = true;
   for (int t = 0; ok && p.warp_wait_info(t); ++t) {
     const Info& f = p.info(t);
@@ -525,30 +527,31 @@ MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& m
     const int page = lane < kPagesPerTile && !(flags & kOwn) ? f.page[lane] : -1;
     const int pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
     const int row = (max(page, 0) * a.hkv + f.kvh) * kPageSize;
-    // slots for: halves of Q (i < 0), then the tile
+    // slots for: halves of Q (i < 0), then the tile, or halves of own rows
     const int q = flags & kFirst ? 2 : 0;
 #pragma unroll 1
     for (int i = -q; i < (flags & kOwn ? 2 : 1); ++i, ++c) {
-      const int st = c % kSlots;
+      const int st = c % kSlots, half = i & 1;
+      const bool halves = i < 0 || (flags & kOwn);
       uint8_t* dst = p.smem + L::OFF_K + st * L::RAW;
       if (!(ok = p.warp_wait(&p.bar.k_empty[st], ((c / kSlots) & 1) ^ 1))) break;
       // both slots before the first half, so that the second always follows
-      if (i == -2 && !(ok = p.warp_wait(&p.bar.k_empty[(c + 1) % kSlots], (((c + 1) / kSlots) & 1) ^ 1))) break;
-      if (lane == 0) mbar_arrive_expect_tx(&p.bar.k_full[st], i < 0 ? 0 : pages * L::PAGE);
+      if (halves && !half &&
+          !(ok = p.warp_wait(&p.bar.k_empty[(c + 1) % kSlots], (((c + 1) / kSlots) & 1) ^ 1)))
+        break;
+      if (lane == 0) mbar_arrive_expect_tx(&p.bar.k_full[st], halves ? 0 : pages * L::PAGE);
       __syncwarp();
-      if (i < 0) {
+      if (halves) {
+        uint64_t* raw = i < 0 ? &p.bar.q_raw : &p.bar.own_raw[own & 1];
         if (lane == 0) {
-          if (i == -2) mbar_arrive_expect_tx(&p.bar.q_raw, a.gp * a.tpt * D * 2);
-          tma_load_3d(dst, &map_q, &p.bar.q_raw, (i + 2) * (D / 2), f.h0, f.base + f.tok0);
+          if (!half) mbar_arrive_expect_tx(raw, (i < 0 ? a.gp * a.tpt : BKV) * D * 2);
+          tma_load_3d(dst, i < 0 ? &map_q : &map_own, raw, half * (D / 2), i < 0 ? f.h0 : f.kvh,
+                      f.base + (i < 0 ? f.tok0 : f.k0));
         }
-        ++q_loads;
+        if (half) (i < 0 ? qs : own) += 1;
       } else if (page >= 0) {
         tma_load_2d(dst + lane * L::PAGE, &map, &p.bar.k_full[st], 0, row);
       }
-    }
-    if (ok && (flags & kOwn)) {
-      if (lane == 0) mbar_arrive(&p.bar.own_free[own & 1]);
-      ++own;
     }
     if (ok) p.warp_done(t);
   }
@@ -557,7 +560,11 @@ MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& m
 #pragma unroll 1
     for (int i = max(0, c - kSlots); i < c; ++i)
       p.drain(&p.bar.k_full[i % kSlots], (i / kSlots) & 1);
-  if (lane == 0 && q_loads > 0) p.drain(&p.bar.q_raw, (q_loads / 2 - 1) & 1);
+  if (lane == 0) {
+    if (qs > 0) p.drain(&p.bar.q_raw, (qs - 1) & 1);
+#pragma unroll 1
+    for (int i = max(0, own - 2); i < own; ++i) p.drain(&p.bar.own_raw[i & 1], (i >> 1) & 1);
+  }
   __syncwarp();
 }
 
@@ -600,86 +607,118 @@ MARS_DEV uint32_t finite_max(uint32_t top, uint32_t word) {
 
 // Sixteen bf16 times f as two e4m3 numbers each: the nearest, and the nearest to what that leaves.
 // An infinity becomes NaN (a finite value's second product adds nothing).
-MARS_DEV void split16(const uint4& x, const uint4& y, float f, uint8_t* first, uint8_t* second) {
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    float e[8];
-    unpack8(h ? y : x, e);
-    uint32_t u[2], v[2];
+MARS_DEV void split16(const uint4& x, const uint4& y, float f, uint4& first, uint4& second) {
+  uint32_t u[4], v[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float* w = e + 4 * i;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = i == 0 ? x.x : i == 1 ? x.z : i == 2 ? y.x : y.z;
+    const uint32_t b = i == 0 ? x.y : i == 1 ? x.w : i == 2 ? y.y : y.w;
+    float w[4] = {__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
+                  __uint_as_float(b & 0xffff0000u)};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = fmaf(w[k], 0.f, w[k] * f);
-      u[i] = q8::encode2(w[0], w[1]) | (q8::encode2(w[2], w[3]) << 16);
-      uint32_t lo, hi;
-      q8::decode4(u[i], lo, hi);
-      const float2 a = q8::halves(lo), b = q8::halves(hi);
-      v[i] = q8::encode2(w[0] - a.x, w[1] - a.y) | (q8::encode2(w[2] - b.x, w[3] - b.y) << 16);
-    }
-    reinterpret_cast<uint2*>(first)[h] = make_uint2(u[0], u[1]);
-    reinterpret_cast<uint2*>(second)[h] = make_uint2(v[0], v[1]);
+    for (int k = 0; k < 4; ++k) w[k] = fmaf(w[k], 0.f, w[k] * f);
+    u[i] = q8::encode2(w[0], w[1]) | (q8::encode2(w[2], w[3]) << 16);
+    uint32_t lo, hi;
+    q8::decode4(u[i], lo, hi);
+    const float2 p = q8::halves(lo), q = q8::halves(hi);
+    v[i] = q8::encode2(w[0] - p.x, w[1] - p.y) | (q8::encode2(w[2] - q.x, w[3] - q.y) << 16);
   }
+  first = make_uint4(u[0], u[1], u[2], u[3]);
+  second = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// The power of two for rows r0 .. r0 + 15 of the sequence's own, as a scale byte: it brings their
-// largest finite magnitude into [2^less, 2^(less + 1)). Whole warp.
+// Rows in bf16 as two slots of K's ring hold them: the first half of a row's elements in either one's
+// row. Lane c of a row's D / 16 has 16 of them, and its place among the codes of either part.
 template <int D>
-MARS_DEV int own_byte(const uint16_t* __restrict__ rows, long long stride, int r0, int count, int less) {
-  constexpr int kLanes = D / 16, kStep = 32 / kLanes;
-  const int lane = threadIdx.x & 31;
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kPageSize / kStep; ++i) {
-    const int r = r0 + lane / kLanes + i * kStep;
-    if (r < count) {
-      const uint4* from = reinterpret_cast<const uint4*>(rows + r * stride + lane % kLanes * 16);
-      const uint4 x = from[0], y = from[1];
-      top = finite_max(finite_max(finite_max(finite_max(top, x.x), x.y), x.z), x.w);
-      top = finite_max(finite_max(finite_max(finite_max(top, y.x), y.y), y.z), y.w);
-    }
+struct Halves {
+  using L = Layout<D>;
+  static constexpr int kLanes = D / 16, kRows = 32 / kLanes;         // lanes of a row, rows of a warp
+  const uint8_t *lo, *hi;
+  MARS_DEV int lane() const { return threadIdx.x % kLanes; }
+  MARS_DEV int row() const { return threadIdx.x % 32 / kLanes; }
+  MARS_DEV void get(int r, uint4& x, uint4& y) const {
+    const uint8_t* from = lane() < kLanes / 2 ? lo : hi;
+    const int c = lane() % (kLanes / 2) * 2;
+    x = *reinterpret_cast<const uint4*>(from + L::code_at(r, c));
+    y = *reinterpret_cast<const uint4*>(from + L::code_at(r, c + 1));
   }
+  static MARS_DEV uint32_t top(const uint4& x, const uint4& y) {
+    const uint32_t t = finite_max(finite_max(finite_max(finite_max(0u, x.x), x.y), x.z), x.w);
+    return finite_max(finite_max(finite_max(finite_max(t, y.x), y.y), y.z), y.w);
+  }
+};
+
+// The power of two over which 16 own rows with a largest finite magnitude of `top` (bf16 bits, of
+// either half of a lane's word) go, as a scale byte: it then lies in [2^less, 2^(less + 1)). Whole warp.
+MARS_DEV int own_byte(uint32_t top, int less) {
   top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
   return min(max((int)(top >> 7) - less, q8::kLeast), kOwnMost);
 }
 
-// The same rows over that power of two as rows r0 .. of a tile: V as f16, K as two e4m3 tiles. (They
-// are read again, out of L1 or L2: code that keeps them is as long as that for a tile of the cache.)
-template <int D, bool kV>
-MARS_DEV void convert_own(const uint16_t* __restrict__ rows, long long stride, uint8_t* tile,
-                          uint8_t* second, int r0, int count, int byte) {
-  using L = Layout<D>;
-  constexpr int kLanes = D / 16, kStep = 32 / kLanes;
-  const int lane = threadIdx.x & 31, c = lane % kLanes;         // 16 elements of a row
+// Rows r0 .. r0 + 15 of an own tile's K, in place: two parts in e4m3, the first in `lo`. Those from
+// `count` on are not keys and stay what they are. Returns the scale byte.
+template <int D>
+MARS_DEV int own_k(uint8_t* lo, uint8_t* hi, int r0, int count) {
+  using H = Halves<D>;
+  const H h{lo, hi};
+  const int end = min(r0 + kPageSize, count);
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int r = r0 + h.row(); r < end; r += H::kRows) {
+    uint4 x, y;
+    h.get(r, x, y);
+    top = __vmaxu2(top, H::top(x, y));
+  }
+  __syncwarp();
+  const int byte = own_byte(top, 7);
   const float f = q8::inverse_power(byte);
 #pragma unroll 1
-  for (int i = 0; i < kPageSize / kStep; ++i) {
-    const int r = r0 + lane / kLanes + i * kStep;
-    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-    if (r < count) {
-      const uint4* from = reinterpret_cast<const uint4*>(rows + r * stride + c * 16);
-      x = from[0];
-      y = from[1];
-    }
-    if (kV) {
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k) {
-        float e[8];
-        unpack8(k ? y : x, e);
-        *reinterpret_cast<uint4*>(chunk_at(tile, r, 2 * c + k)) =
-            make_uint4(q8::pack_f16x2(e[0] * f, e[1] * f), q8::pack_f16x2(e[2] * f, e[3] * f),
-                       q8::pack_f16x2(e[4] * f, e[5] * f), q8::pack_f16x2(e[6] * f, e[7] * f));
-      }
-    } else {
-      split16(x, y, f, tile + L::code_at(r, c), second + L::code_at(r, c));
-    }
+  for (int r = r0 + h.row(); r - h.row() < end; r += H::kRows) {
+    uint4 x, y, u, v;
+    h.get(r, x, y);                                  // of 16 rows that a tile has, whatever they hold
+    split16(x, y, f, u, v);
+    __syncwarp();                                    // all of the rows has been read
+    *reinterpret_cast<uint4*>(lo + Layout<D>::code_at(r, h.lane())) = u;
+    *reinterpret_cast<uint4*>(hi + Layout<D>::code_at(r, h.lane())) = v;
   }
+  return byte;
+}
+
+// Rows r0 .. r0 + 15 of an own tile's V, in place: bf16 to f16, zero from `count` on. Returns the
+// scale byte.
+template <int D>
+MARS_DEV int own_v(uint8_t* tile, int r0, int count) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31, c = lane % kLanes, first = r0 + lane / kLanes;
+  const int end = min(r0 + kPageSize, count);
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int r = first; r < end; r += kRows) {
+    const uint4 x = *reinterpret_cast<const uint4*>(chunk_at(tile, r, c));
+    top = finite_max(finite_max(finite_max(finite_max(top, x.x), x.y), x.z), x.w);
+  }
+  __syncwarp();
+  const int byte = own_byte(top, 8);
+  const float f = q8::inverse_power(byte);
+#pragma unroll 1
+  for (int r = first; r < r0 + kPageSize; r += kRows) {
+    uint4* at = reinterpret_cast<uint4*>(chunk_at(tile, r, c));
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (r < end) {
+      float e[8];
+      unpack8(*at, e);
+      y = make_uint4(q8::pack_f16x2(e[0] * f, e[1] * f), q8::pack_f16x2(e[2] * f, e[3] * f),
+                     q8::pack_f16x2(e[4] * f, e[5] * f), q8::pack_f16x2(e[6] * f, e[7] * f));
+    }
+    *at = y;
+  }
+  return byte;
 }
 
 // Warps 12 ..: copies of their two pages of every tile of V and f16 tiles from them, and the
 // sequence's own K and V.
 template <int D>
-MARS_DEV void convert(const Pipe& p, const CUtensorMap& map) {
+MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& map_own) {
   using namespace sm100;
   using L = Layout<D>;
   const Args& a = p.a;
@@ -689,7 +728,7 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map) {
   uint64_t* const full = p.bar.raw_full[warp];
   uint8_t* const ring = p.smem + L::OFF_RAW + warp * kRaw * 2 * L::PAGE;
   // the next copy: its number and tile; `converted`: copies that have left the ring
-  int copies = 0, next = 0, converted = 0, slots = 0, own = 0;
+  int copies = 0, next = 0, converted = 0, slots = 0, own = 0, own_copies = 0;
   bool more = true, ok = true;
   auto copy_ahead = [&](int t) {
     while (more && next <= t + kAhead && copies < converted + kRaw) {
@@ -720,31 +759,34 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map) {
     if (flags & kFirst) slots += 2;                  // Q's
     uint8_t* tile = p.smem + L::OFF_V + ts * L::TILE;
     if (flags & kOwn) {
-      // both scales and K before S, for which warp 1 has taken two slots; V before P V
-      const size_t at = (size_t)f.base + f.k0;
-      const uint16_t* const rows[2] = {a.k + at * a.k_stride + f.kvh * D, a.v + at * a.v_stride + f.kvh * D};
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int byte = own_byte<D>(i & 1 ? rows[1] : rows[0], i & 1 ? a.v_stride : a.k_stride,
-                                     (g + i / 2) * kPageSize, f.count, i & 1 ? 8 : 7);
-        if (lane == 0) (i & 1 ? f.v_byte : f.k_byte)[g + i / 2] = (uint8_t)byte;
+      // warp 1 has brought K. V's copy goes to its place in the tile; S also waits for V's scales,
+      // which its softmax needs
+      if (!(ok = p.warp_wait(&p.bar.v_empty[ts], ((t / kTiles) & 1) ^ 1))) break;
+      if (warp == 0 && lane == 0) {
+        ++own_copies;
+        mbar_arrive_expect_tx(&p.bar.own_v[own & 1], BKV * D * 2);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+          tma_load_3d(tile + x * (BKV * 128), &map_own, &p.bar.own_v[own & 1], x * 64, f.kvh, f.base + f.k0);
       }
-      __syncwarp();
-      if (!(ok = p.warp_wait(&p.bar.own_free[own & 1], (own >> 1) & 1))) break;
+      if (!(ok = p.warp_wait(&p.bar.own_raw[own & 1], (own >> 1) & 1))) break;
 #pragma unroll 1
-      for (int i = g; i < g + 2; ++i)
-        convert_own<D, false>(rows[0], a.k_stride, p.smem + L::OFF_K + slots % kSlots * L::RAW,
-                              p.smem + L::OFF_K + (slots + 1) % kSlots * L::RAW, i * kPageSize, f.count,
-                              f.k_byte[i]);
+      for (int i = g; i < g + 2; ++i) {
+        const int byte = own_k<D>(p.smem + L::OFF_K + slots % kSlots * L::RAW,
+                                  p.smem + L::OFF_K + (slots + 1) % kSlots * L::RAW, i * kPageSize, f.count);
+        if (lane == 0) f.k_byte[i] = (uint8_t)byte;
+      }
+      if (!(ok = p.warp_wait(&p.bar.own_v[own & 1], (own >> 1) & 1))) break;
+#pragma unroll 1
+      for (int i = g; i < g + 2; ++i) {
+        const int byte = own_v<D>(tile, i * kPageSize, f.count);
+        if (lane == 0) f.v_byte[i] = (uint8_t)byte;
+      }
       slots += 2;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p.bar.own_full[own & 1]);
       ++own;
-      if (!(ok = p.warp_wait(&p.bar.v_empty[ts], ((t / kTiles) & 1) ^ 1))) break;
-#pragma unroll 1
-      for (int i = g; i < g + 2; ++i)
-        convert_own<D, true>(rows[1], a.v_stride, tile, nullptr, i * kPageSize, f.count, f.v_byte[i]);
     } else {
       ++slots;
       if (!(ok = p.warp_wait(&full[converted % kRaw], (converted / kRaw) & 1))) break;
@@ -767,6 +809,7 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map) {
   if (lane == 0)
 #pragma unroll 1
     for (int i = converted; i < copies; ++i) p.drain(&full[i % kRaw], (i / kRaw) & 1);
+  if (lane == 0 && own_copies > 0) p.drain(&p.bar.own_v[(own_copies - 1) & 1], ((own_copies - 1) >> 1) & 1);
   __syncwarp();
 }
 
@@ -798,7 +841,7 @@ MARS_DEV void issue_s(const Pipe& p) {
       if (!p.wait(&p.bar.own_full[own & 1], (own >> 1) & 1)) break;
       ++own;
     }
-    // S buffer sb last held tile t - kBufs, whose P the PV of that tile read from it
+    // S buffer sb last held tile t - 2, whose P the PV of that tile read from it
     if (t >= kBufs && !p.wait(&p.bar.pv_done[sb], (t / kBufs - 1) & 1)) break;
     const int parts = flags & kOwn ? 2 : 1;
     bool ok = true;
@@ -829,11 +872,13 @@ MARS_DEV void issue_pv(const Pipe& p) {
   using namespace sm100;
   using L = Layout<D>;
   const uint32_t idesc = idesc_f16_f32(BQ, D, true);
-  for (int t = 0; p.wait_info(t); ++t) {
+  for (int t = 0, items = 0; p.wait_info(t); ++t) {
     const int flags = p.info(t).flags;
     if (flags & kEnd) break;
     mbar_arrive(&p.bar.info_empty[t % kInfos]);
     const int pb = t % kBufs;
+    // the O of the item before have been read
+    if ((flags & kFirst) && items++ && !p.wait(&p.bar.o_free, items & 1)) break;
     if (!p.wait(&p.bar.v_full[t % kTiles], (t / kTiles) & 1)) break;
     if (!p.wait(&p.bar.p_full[pb], (t / kBufs) & 1)) break;
     tc_fence_after();
@@ -841,8 +886,8 @@ MARS_DEV void issue_pv(const Pipe& p) {
         sdesc_sw128(smem_u32(p.smem + L::OFF_V + t % kTiles * L::TILE), BKV * 128, 1024);
 #pragma unroll
     for (int k = 0; k < BKV / 16; ++k)
-      mma_bf16_ts(p.tmem + L::TM_O, p.tmem + L::TM_S + pb * BKV + L::P_OFF + k * 8,
-                  sdesc_advance(vd, k * 2048), idesc, k != 0 || !(flags & kFirst));
+      mma_bf16_ts(p.tmem + L::TM_O + pb * D, p.tmem + L::TM_S + pb * BKV + L::P_OFF + k * 8,
+                  sdesc_advance(vd, k * 2048), idesc, k != 0 || !(flags & (kFirst | kSecond)));
     mma_commit(&p.bar.pv_done[pb]);
     mma_commit(&p.bar.v_empty[t % kTiles]);
   }
@@ -850,77 +895,35 @@ MARS_DEV void issue_pv(const Pipe& p) {
   p.drain(&p.bar.drain[1], 0);
 }
 
-// The two threads of a row. Warps of a pair call it alike; false if the wait gave up.
-struct Pair {
-  const Pipe& p;
-  int row, half, uses;
-  // 16 bits for the other thread, and its own
-  MARS_DEV void give(uint32_t mine) {
-    p.bar.exchange[uses & 1][half][row] = (uint16_t)mine;
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&p.bar.pair[row / 32]);
-  }
-  MARS_DEV bool take(uint32_t& other) {
-    const int u = uses++ & 1;
-    if (!p.warp_wait(&p.bar.pair[row / 32], u)) return false;
-    other = p.bar.exchange[u][half ^ 1][row];
-    return true;
-  }
-};
-
 // Q of the item that tile t begins (its `item`-th), out of K's ring: each row over the power of two
-// that brings its largest finite magnitude into [128, 256), as two e4m3 numbers. A warp takes every
-// eighth row, a lane D / 32 elements of it; rows without a token stay what they are. (Short, because
-// it runs once per item: loads and stores of a thread's own row, unrolled, took 25,000 cycles, most
-// of them for instructions.)
+// that brings its largest finite magnitude into [128, 256), as two e4m3 numbers. Rows without a token
+// stay what they are.
 template <int D>
 MARS_DEV bool convert_q(const Pipe& p, int t, int item) {
   using namespace sm100;
   using L = Layout<D>;
+  using H = Halves<D>;
   const Args& a = p.a;
   const Info& f = p.info(t);
   const int warp = (threadIdx.x >> 5) - kSoftmaxWarp, lane = threadIdx.x & 31;
   if (!p.warp_wait(&p.bar.q_raw, item & 1)) return false;
-  const int rows = a.gp * min(a.tpt, f.n - f.tok0), byte_in = lane % 16 * (D / 16), byte_out = lane * (D / 32);
-  const uint8_t* from = p.smem + L::OFF_K + (f.q_slot + lane / 16) % kSlots * L::RAW;
+  const int rows = a.gp * min(a.tpt, f.n - f.tok0);
   uint8_t* to = p.smem + L::OFF_Q;
-#pragma unroll 2
-  for (int r = warp; r < rows; r += kSoftmaxWarps) {
-    const uint8_t* src = from + L::code_at(r, byte_in / 16) + byte_in % 16;
-    uint32_t w[2] = {0u, 0u};
-    if (D == 128) {
-      const uint2 x = *reinterpret_cast<const uint2*>(src);
-      w[0] = x.x;
-      w[1] = x.y;
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(src);
-    }
-    uint32_t top = finite_max(finite_max(0u, w[0]), w[1]);
-    top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+  const H h{p.smem + L::OFF_K + f.q_slot * L::RAW, p.smem + L::OFF_K + (f.q_slot + 1) % kSlots * L::RAW};
+#pragma unroll 1
+  for (int r = warp * H::kRows + h.row(); r - h.row() < rows; r += kSoftmaxWarps * H::kRows) {
+    uint4 x, y, u, v;
+    h.get(r, x, y);
+    uint32_t top = H::top(x, y);
+    top = max(top >> 16, top & 0xffffu);
+#pragma unroll
+    for (int o = 1; o < H::kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     // (a row of next to nothing: 2^-53)
     const int byte = top ? min(max((int)(top >> 7), 74), 253) - 7 : q8::kBias;
-    const float inv = q8::inverse_power(byte);
-    uint32_t u[2], v[2];
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      // an infinity becomes NaN (a finite value's second product adds nothing)
-      const float x = __uint_as_float(w[i] << 16), y = __uint_as_float(w[i] & 0xffff0000u);
-      const float e0 = fmaf(x, 0.f, x * inv), e1 = fmaf(y, 0.f, y * inv);
-      u[i] = q8::encode2(e0, e1);
-      uint32_t lo, hi;
-      q8::decode4(u[i], lo, hi);
-      const float2 near = q8::halves(lo);
-      v[i] = q8::encode2(e0 - near.x, e1 - near.y);
-    }
-    uint8_t* dst = to + L::code_at(r, byte_out / 16) + byte_out % 16;
-    if (D == 128) {
-      *reinterpret_cast<uint32_t*>(dst) = u[0] | (u[1] << 16);
-      *reinterpret_cast<uint32_t*>(dst + L::RAW) = v[0] | (v[1] << 16);
-    } else {
-      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)u[0];
-      *reinterpret_cast<uint16_t*>(dst + L::RAW) = (uint16_t)v[0];
-    }
-    if (lane == 0) p.bar.q_byte[item & 1][r] = (uint8_t)byte;
+    split16(x, y, q8::inverse_power(byte), u, v);
+    *reinterpret_cast<uint4*>(to + L::code_at(r, h.lane())) = u;
+    *reinterpret_cast<uint4*>(to + L::RAW + L::code_at(r, h.lane())) = v;
+    if (h.lane() == 0) p.bar.q_byte[item & 1][r] = (uint8_t)byte;
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -928,67 +931,44 @@ MARS_DEV bool convert_q(const Pipe& p, int t, int item) {
   return p.warp_wait(&p.bar.q_full, item & 1);
 }
 
+// Factor of the scores of 16 keys (never 0 or infinite: it meets infinite scores), and the exponent
+// of their V; by their scale bytes, the low ones of k and v.
+MARS_DEV float k_factor(float factor, uint32_t k) {
+  return fminf(fmaxf(factor * q8::power((int)(k & 255u)), 1e-38f), 3e38f);
+}
+MARS_DEV float v_exponent(uint32_t v) {              // 2^23 + byte is exact
+  return (v & 255u) ? __int_as_float(0x4b000000 | (int)(v & 255u)) - (8388608.f + q8::kBias) : -INFINITY;
+}
+
 // Factor of a row's O. l is 0 where every score is -infinity (O is then 0), NaN where one is NaN or
 // +infinity.
 MARS_DEV float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
-
-// This thread's half of its row of O out of TMEM: divided by the row's sum to where the row is, or
-// into a partial.
-template <int D>
-MARS_DEV void store_o(const Pipe& p, const Pair& pair, int slot, bool has, long long at, float m,
-                      float l) {
-  using namespace sm100;
-  using L = Layout<D>;
-  const Args& a = p.a;
-  const int row = pair.row;
-  const uint32_t o_addr = p.tmem + L::TM_O + ((uint32_t)(row & ~31) << 16);
-  const float inv = reciprocal(l);
-  float4* part = a.part + ((size_t)blockIdx.x * 2 + slot) * L::PART;
-  if (slot >= 0 && has && pair.half == 0)
-    reinterpret_cast<float2*>(part + BQ * D / 4)[row] = make_float2(m, l);
-#pragma unroll 1
-  for (int c = pair.half * (D / 32); c < (pair.half + 1) * (D / 32); ++c) {
-    uint32_t o[16];
-    tmem_ld16(o_addr + c * 16, o);
-    tmem_ld_wait();
-    if (!has) continue;
-    if (slot < 0) {
-      uint32_t w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        w[e] = flash::pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-      uint4* to = reinterpret_cast<uint4*>(a.o + at + c * 16);
-      to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        part[(c * 4 + e / 4) * BQ + row] =
-            make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                        __uint_as_float(o[e + 3]));
-    }
-  }
-}
 
 // Softmax and output.
 template <int D>
 MARS_DEV void softmax(const Pipe& p) {
   using namespace sm100;
   using L = Layout<D>;
-  constexpr int kKeys = BKV / 2, kGroups = kPagesPerTile / 2;       // of a thread
+  constexpr int kKeys = BKV / 2, kGroups = kPagesPerTile / 2;       // at a time
   const Args& a = p.a;
-  const int warp = (threadIdx.x >> 5) - kSoftmaxWarp, quad = warp & 3;
-  Pair pair{p, quad * 32 + (int)(threadIdx.x & 31), warp >> 2, 0};
-  const int row = pair.row, half = pair.half;
+  const int warp = (threadIdx.x >> 5) - kSoftmaxWarp, quad = warp & 3, odd = warp >> 2;
+  const int row = quad * 32 + (int)(threadIdx.x & 31);
   const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+  const uint32_t s_addr = p.tmem + L::TM_S + odd * BKV + lane_off;
+  const uint32_t o_addr = p.tmem + L::TM_O + lane_off;              // of even tiles
   float factor = 0.f, m = -INFINITY, l = 0.f;
-  int tok = 0, t = -1, slot = -1, base = 0, h0 = 0, items = 0, flags = kLast;
+  int tok = 0, tiles = 0, items = 0, flags = kLast, uses = 0;
   bool has = false, busy = false;
-  for (;;) {
-    // tile t; before the first one t = -1
-    const int sb = t % kBufs;
-    if (t >= 0) {
-      if (!p.warp_wait(&p.bar.s_full[sb], (t / kBufs) & 1)) return;
+  // The two warps of 32 rows meet; what either wrote before is there after.
+  auto meet = [&]() -> bool {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&p.bar.pair[quad]);
+    return p.warp_wait(&p.bar.pair[quad], uses++ & 1);
+  };
+  for (int t = -1;;) {                               // before the first tile t = -1
+    const bool mine = t >= 0 && (t & 1) == odd;
+    if (mine || (t >= 0 && (flags & kLast))) {
+      if (!p.warp_wait(&p.bar.s_full[t & 1], (t / kBufs) & 1)) return;
       tc_fence_after();
     }
     if (flags & kLast) {
@@ -996,127 +976,169 @@ MARS_DEV void softmax(const Pipe& p) {
       if (!p.warp_wait_info(t + 1)) return;
       if (!(p.info(t + 1).flags & kEnd) && !convert_q<D>(p, t + 1, items++)) return;
     }
-    if (t >= 0) {
-      const Info& f = p.info(t);
-      // keys of this thread that its row sees
-      const int limit = ((flags & kOwn) ? min(f.count, tok + 1 - f.k0) : f.count) - half * kKeys;
-      const uint32_t kb = *reinterpret_cast<const uint32_t*>(f.k_byte + half * kGroups);
-      const uint32_t vb = *reinterpret_cast<const uint32_t*>(f.v_byte + half * kGroups);
-    if (busy) {
-      const uint32_t s_addr = p.tmem + L::TM_S + sb * BKV + lane_off;
-      uint32_t r[kKeys];
+    const Info& f = p.info(max(t, 0));
+    if (mine && busy) {
+      // keys that the row sees
+      const int limit = (flags & kOwn) ? min(f.count, tok + 1 - f.k0) : f.count;
+      const uint2 kbs = *reinterpret_cast<const uint2*>(f.k_byte);
+      const uint2 vbs = *reinterpret_cast<const uint2*>(f.v_byte);
+      const bool masked = __any_sync(0xffffffffu, limit < BKV) || (flags & kHoles);
+      // the largest s + e
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t kb = h ? kbs.y : kbs.x, vb = h ? vbs.y : vbs.x;
+        uint32_t r[kKeys];
 #pragma unroll
-      for (int c = 0; c < kKeys / 32; ++c)
-        tmem_ld32(s_addr + half * kKeys + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
-      // factor of the scores of 16 keys (never 0 or infinite: it meets infinite scores), and their
-      // exponent of V
-      float mul[kGroups], add[kGroups];
+        for (int c = 0; c < kKeys / 32; ++c)
+          tmem_ld32(s_addr + h * kKeys + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
+        tmem_ld_wait();
+        if (masked) {                                // once, for the second pass too
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const int k = (kb >> (8 * g)) & 255, v = (vb >> (8 * g)) & 255;
-        mul[g] = fminf(fmaxf(factor * q8::power(k), 1e-38f), 3e38f);
-        // 2^23 + byte is exact
-        add[g] = v ? __int_as_float(0x4b000000 | v) - (8388608.f + q8::kBias) : -INFINITY;
-      }
-      tmem_ld_wait();
-      if (__any_sync(0xffffffffu, limit < kKeys) || (flags & kHoles)) {
+          for (int g = 0; g < kGroups; ++g) {
+            const int seen = ((vb >> (8 * g)) & 255) ? limit - h * kKeys - 16 * g : 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e >= seen) r[16 * g + e] = 0xff800000u;
+          }
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c)
+            tmem_st32(s_addr + h * kKeys + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
+          tmem_st_wait();
+        }
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-          const int seen = ((vb >> (8 * g)) & 255) ? limit - 16 * g : 0;
+          float x[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e >= seen) r[16 * g + e] = 0xff800000u;
+          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[16 * g + e]);
+          const float y = flash::max3f(flash::max3f(x[0], x[1], x[2]), flash::max3f(x[3], x[4], x[5]),
+                                       flash::max3f(x[6], x[7], x[8]));
+          const float z = flash::max3f(flash::max3f(x[9], x[10], x[11]), flash::max3f(x[12], x[13], x[14]), x[15]);
+          top = fmaxf(top, fmaf(fmaxf(y, z), k_factor(factor, kb >> (8 * g)), v_exponent(vb >> (8 * g))));
         }
       }
-      // s + e, in place, and its maximum
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const float2 mul2 = make_float2(mul[g], mul[g]), add2 = make_float2(add[g], add[g]);
-#pragma unroll
-        for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
-                                      mul2, add2);
-          r[e] = __float_as_uint(x.x);
-          r[e + 1] = __float_as_uint(x.y);
-        }
-      }
-      float top = flash::row_max_log2(r, 1.f);
-      // the row's maximum as bf16, rounded up: any number near it serves
-      const uint32_t bits = __float_as_uint(top), mine = (top > 0.f ? bits + 0xffffu : bits) >> 16;
-      uint32_t other;
-      pair.give(mine);
-      if (!pair.take(other)) return;
-      top = fmaxf(__uint_as_float(mine << 16), __uint_as_float(other << 16));
-      // lazy rescale (flash_tc.cuh)
+      // lazy rescale (flash_tc.cuh); the PV of this O's last tile came before S of this one
       const bool raise = top > m + flash::kRescaleLog2;
       const bool rescale = raise && m != -INFINITY;
       if (__any_sync(0xffffffffu, rescale)) {
-        if (!p.warp_wait(&p.bar.pv_done[(t - 1) % kBufs], ((t - 1) / kBufs) & 1)) return;
-        tc_fence_after();
         const float alpha = rescale ? flash::ex2_approx(m - top) : 1.f;
         l *= alpha;
 #pragma unroll 1
-        for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
-          const uint32_t o_addr = p.tmem + L::TM_O + lane_off + c * 16;
+        for (int c = odd * D; c < odd * D + D; c += 16) {
           uint32_t o[16];
-          tmem_ld16(o_addr, o);
+          tmem_ld16(o_addr + c, o);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st16(o_addr, o);
+          tmem_st16(o_addr + c, o);
         }
         tmem_st_wait();
       }
       if (raise) m = top;
       const float shift = kLift - (m == -INFINITY ? 0.f : m);
-      const float2 shift2 = make_float2(shift, shift);
-      uint32_t packed[kKeys / 2];
+      // P', the second half first: it lies over the scores of the second half
+#pragma unroll 1
+      for (int h = 1; h >= 0; --h) {
+        const uint32_t kb = h ? kbs.y : kbs.x, vb = h ? vbs.y : vbs.x;
+        uint32_t r[kKeys], packed[kKeys / 2];
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        float2 acc = make_float2(0.f, 0.f);
+        for (int c = 0; c < kKeys / 32; ++c)
+          tmem_ld32(s_addr + h * kKeys + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
+        tmem_ld_wait();
 #pragma unroll
-        for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-          const float2 x = __fadd2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), shift2);
-          const float2 w = make_float2(flash::ex2_approx(x.x), flash::ex2_approx(x.y));
-          packed[e / 2] = q8::pack_f16x2(w.x, w.y);
-          acc = __fadd2_rn(acc, w);
+        for (int g = 0; g < kGroups; ++g) {
+          const float mul = k_factor(factor, kb >> (8 * g)), add = v_exponent(vb >> (8 * g)) + shift;
+          const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
+          float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), mul2, add2);
+            const float2 w = make_float2(flash::ex2_approx(x.x), flash::ex2_approx(x.y));
+            packed[e / 2] = q8::pack_f16x2(w.x, w.y);
+            acc = __fadd2_rn(acc, w);
+          }
+          // 2^-e; where there are no keys, the bits of some finite number, times 0
+          l = fmaf(acc.x + acc.y, q8::inverse_power((vb >> (8 * g)) & 255), l);
         }
-        // 2^-e; where there are no keys, the bits of some finite number, times 0
-        l = fmaf(acc.x + acc.y, q8::inverse_power((vb >> (8 * g)) & 255), l);
+        tmem_st32(s_addr + L::P_OFF + h * (kKeys / 2), packed);
       }
-      tmem_st32(s_addr + L::P_OFF + half * (kKeys / 2), packed);
       tmem_st_wait();
     }
+    if (mine) {
       tc_fence_before();
-      mbar_arrive_warp(&p.bar.p_full[sb]);
-      p.warp_done(t);
-      if ((flags & kLast) && busy) {
-        // the row's sum
-        const uint32_t mine = __float_as_uint(l);
-        uint32_t lo, hi;
-        pair.give(mine & 0xffffu);
-        if (!pair.take(lo)) return;
-        pair.give(mine >> 16);
-        if (!pair.take(hi) || !p.warp_wait(&p.bar.pv_done[sb], (t / kBufs) & 1)) return;
+      mbar_arrive_warp(&p.bar.p_full[odd]);
+    }
+    if (t >= 0 && (flags & kLast)) {
+      if (busy) {
+        // maxima and sums of the row's even and odd tiles, once both have left the item before
+        float (&x)[2][BQ] = p.bar.exchange;
+        if (!meet()) return;
+        x[odd][row] = m;
+        if (!meet()) return;
+        const float other = x[odd ^ 1][row], top = fmaxf(m, other);
+        // (m = +infinity gives NaN)
+        const float w = m > -INFINITY ? exp2f(m - top) : 0.f, w_other = other > -INFINITY ? exp2f(other - top) : 0.f;
+        if (!meet()) return;
+        x[odd][row] = l * w;
+        if (!meet()) return;
+        l = x[0][row] + x[1][row];
+        m = top;
+        // the last two PVs, this thread's own first: the other's is known by what that one implies
+        const bool two = tiles > 1;
+        const int first = two && !mine ? t - 1 : t;
+        if (!p.warp_wait(&p.bar.pv_done[first & 1], (first / kBufs) & 1)) return;
+        const int second = 2 * t - 1 - first;
+        if (two && !p.warp_wait(&p.bar.pv_done[second & 1], (second / kBufs) & 1)) return;
         tc_fence_after();
-        store_o<D>(p, pair, slot, has, (((long long)base + tok) * a.hq + h0 + row % a.gp) * D, m,
-                   l + __uint_as_float(lo | (hi << 16)));
+        // the row's O, half of the columns each: over its sum to where the row is, or into a partial
+        const float w_even = odd ? w_other : w, w_odd = odd ? w : w_other;
+        const bool even = two || !(t & 1), odds = two || (t & 1);
+        const int slot = f.slot;
+        const float inv = slot < 0 ? reciprocal(l) : 1.f;
+        float4* part = a.part + ((size_t)blockIdx.x * 2 + slot) * L::PART;
+        if (slot >= 0 && has && odd == 0) reinterpret_cast<float2*>(part + BQ * D / 4)[row] = make_float2(m, l);
+        uint16_t* to = a.o + (((size_t)f.base + tok) * a.hq + f.h0 + row % a.gp) * D;
+#pragma unroll 1
+        for (int c = odd * (D / 2); c < (odd + 1) * (D / 2); c += 16) {
+          uint32_t u[16], v[16];
+          tmem_ld16(o_addr + c, u);
+          tmem_ld16(o_addr + D + c, v);
+          tmem_ld_wait();
+          float o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[e] = ((even ? __uint_as_float(u[e]) * w_even : 0.f) + (odds ? __uint_as_float(v[e]) * w_odd : 0.f)) * inv;
+          if (!has) continue;
+          if (slot < 0) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4*>(to + c + e) =
+                  make_uint4(flash::pack_bf16x2(o[e], o[e + 1]), flash::pack_bf16x2(o[e + 2], o[e + 3]),
+                             flash::pack_bf16x2(o[e + 4], o[e + 5]), flash::pack_bf16x2(o[e + 6], o[e + 7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              part[(c + e) / 4 * BQ + row] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
         tc_fence_before();
       }
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&p.bar.o_free);
     }
+    if (t >= 0) p.warp_done(t);
     ++t;
     if (!p.warp_wait_info(t)) return;
-    const Info& f = p.info(t);
-    flags = f.flags;
+    const Info& n = p.info(t);
+    flags = n.flags;
     if (flags & kEnd) return;
+    ++tiles;
     if (flags & kFirst) {
       m = -INFINITY;
       l = 0.f;
-      slot = f.slot;
-      base = f.base;
-      h0 = f.h0;
-      tok = f.tok0 + row / a.gp;
-      has = row < a.gp * a.tpt && tok < f.n;
+      tiles = 1;
+      tok = n.tok0 + row / a.gp;
+      has = row < a.gp * a.tpt && tok < n.n;
       busy = __any_sync(0xffffffffu, has);       // warps without rows only keep step
       factor = has ? a.scale_log2 * q8::power(p.bar.q_byte[(items - 1) & 1][row]) : 1.f;
     }
@@ -1126,7 +1148,8 @@ MARS_DEV void softmax(const Pipe& p) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-             const __grid_constant__ CUtensorMap tm_q, Args a) {
+             const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_own_k,
+             const __grid_constant__ CUtensorMap tm_own_v, Args a) {
   using namespace sm100;
   using L = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1151,7 +1174,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       mbar_init(&bar.k_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.own_free[i], 1);
+      mbar_init(&bar.own_raw[i], 1);
+      mbar_init(&bar.own_v[i], 1);
       mbar_init(&bar.own_full[i], kConvertWarps);
     }
     for (int i = 0; i < kTiles; ++i) {
@@ -1161,11 +1185,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     for (int i = 0; i < 2; ++i) mbar_init(&bar.drain[i], 1);
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 32 * kSoftmaxWarps);
+      mbar_init(&bar.p_full[i], 128);
       mbar_init(&bar.pv_done[i], 1);
     }
     mbar_init(&bar.q_raw, 1);
     mbar_init(&bar.q_full, kSoftmaxWarps);
+    mbar_init(&bar.o_free, kSoftmaxWarps);
     for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
     fence_barrier_init();
   }
@@ -1187,7 +1212,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     if (warp == 0) {
       walk<D>(p, scan);
     } else if (warp == 1) {
-      load_k<D>(p, tm_k, tm_q);
+      load_k<D>(p, tm_k, tm_q, tm_own_k);
     } else if (elect_one()) {
       if (warp == 2) issue_s<D>(p); else issue_pv<D>(p);
     }
@@ -1196,7 +1221,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     softmax<D>(p);
   } else {
     regs_lower<kConvertRegs>();
-    convert<D>(p, tm_v);
+    convert<D>(p, tm_v, tm_own_v);
   }
   tc_fence_before();
   __syncthreads();
@@ -1393,7 +1418,7 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   cudaError_t e = set_smem_limit_once(chunk_kernel<D>, L::TOTAL, attr);
   if (e != cudaSuccess) return e;
   // a page and KV head is 16 rows of the maps; an empty pool is never read (one page over q)
-  CUtensorMap map_k, map_v, map_q;
+  CUtensorMap map_k, map_v, map_q, map_own_k, map_own_v;
   const bool any = t.num_pages > 0;
   const uint64_t dims[2] = {(uint64_t)D, (any ? (uint64_t)t.num_pages * t.hkv : 1) * kPageSize};
   const uint64_t pitch[1] = {(uint64_t)D};
@@ -1402,16 +1427,23 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   if (!encode_tmap_u8(&map_k, any ? p.k_pool : none, 2, dims, pitch, box) ||
       !encode_tmap_u8(&map_v, any ? p.v_pool : none, 2, dims, pitch, box))
     return cudaErrorInvalidValue;
-  const uint64_t q_dims[3] = {(uint64_t)D, (uint64_t)t.hq, (uint64_t)t.total};
-  const uint64_t q_pitch[2] = {(uint64_t)D * 2, (uint64_t)t.q_stride * 2};
-  const uint32_t q_box[3] = {D / 2, (uint32_t)plan.gp, (uint32_t)plan.tpt};
-  if (!encode_tmap_bf16_rows(&map_q, t.q, 3, q_dims, q_pitch, q_box)) return cudaErrorInvalidValue;
-  chunk_kernel<D><<<plan.ctas, kThreads, L::TOTAL, stream>>>(map_k, map_v, map_q, a);
+  auto rows = [&](CUtensorMap* m, const uint16_t* base, int heads, long long stride, int elements,
+                  int box_heads, int box_rows) {
+    const uint64_t dims3[3] = {(uint64_t)D, (uint64_t)heads, (uint64_t)t.total};
+    const uint64_t pitch2[2] = {(uint64_t)D * 2, (uint64_t)stride * 2};
+    const uint32_t box3[3] = {(uint32_t)elements, (uint32_t)box_heads, (uint32_t)box_rows};
+    return encode_tmap_bf16_rows(m, base, 3, dims3, pitch2, box3);
+  };
+  if (!rows(&map_q, t.q, t.hq, t.q_stride, D / 2, plan.gp, plan.tpt) ||
+      !rows(&map_own_k, t.k, t.hkv, t.k_stride, D / 2, 1, BKV) ||
+      !rows(&map_own_v, t.v, t.hkv, t.v_stride, 64, 1, BKV))
+    return cudaErrorInvalidValue;
+  chunk_kernel<D><<<plan.ctas, kThreads, L::TOTAL, stream>>>(map_k, map_v, map_q, map_own_k, map_own_v, a);
   count_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess || !plan.can_split) return e;
-  const int rows = std::min(plan.gp * std::min(plan.tpt, t.total), BQ);
-  merge_kernel<D><<<dim3(plan.ctas, (rows * (D / 4) + 255) / 256), 256, 0, stream>>>(a, plan.ctas);
+  const int most = std::min(plan.gp * std::min(plan.tpt, t.total), BQ);      // rows of an item
+  merge_kernel<D><<<dim3(plan.ctas, (most * (D / 4) + 255) / 256), 256, 0, stream>>>(a, plan.ctas);
   count_launches(1);
   return cudaGetLastError();
 }
