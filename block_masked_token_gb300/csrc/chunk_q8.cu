@@ -22,9 +22,9 @@
 // Shared memory moves 128 bytes per cycle: the copies of a tile's codes take 256 cycles, S 512, the
 // conversion of V 384, P V 256. (With K converted to f16 as well, 1,800 cycles per tile.)
 //
-// Roles (512 threads): warp 0 walks the items and reads block table and scales ahead of the others
-// (infos); warp 1 copies K; warps 12..15 copy two pages of V each into a ring of their own and turn
-// them into 32 rows of a swizzled f16 tile, zero where no key may be read; warps 2 and 3 issue
+// Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
+// (infos); warp 1 copies K; warps 12..19 copy a page of V each into a ring of their own and turn
+// it into 16 rows of a swizzled f16 tile, zero where no key may be read; warps 2 and 3 issue
 // S and O += P' V; warps 4..7 run the softmax of even tiles, 8..11 that of odd ones, a thread per
 // row, each with an S buffer, an O, a maximum and a sum of its own, which are joined at an item's end.
 // (With half of every tile's keys each, the exchange of maxima and the waits took longer than the
@@ -48,10 +48,10 @@ namespace {
 using flash::BKV;
 using flash::BQ;
 
-constexpr int kThreads = 512;
-constexpr int kSoftmaxWarp = 4, kSoftmaxWarps = 8, kConvertWarp = 12, kConvertWarps = 4;
-constexpr int kControlRegs = 88, kSoftmaxRegs = 152, kConvertRegs = 120;
-static_assert(128 * (kControlRegs + 2 * kSoftmaxRegs + kConvertRegs) <=
+constexpr int kThreads = 640;
+constexpr int kSoftmaxWarp = 4, kSoftmaxWarps = 8, kConvertWarp = 12, kConvertWarps = 8;
+constexpr int kControlRegs = 72, kSoftmaxRegs = 136, kConvertRegs = 64;
+static_assert(128 * (kControlRegs + 2 * kSoftmaxRegs + 2 * kConvertRegs) <=
                   kThreads * (65536 / kThreads / 8 * 8),
               "the register split fits the launch's register pool");
 constexpr int kRaw = 4;              // ring of raw tiles of V
@@ -133,7 +133,7 @@ MARS_DEV void find_part(const Args& a, Scan& sc) {
   auto clamped = [&](int s) { return min(max(a.cu[s], 0), a.total); };
   int bad = 0, m = 0;
   for (int s = lo; s < hi; ++s) m = max(m, clamped(s + 1));
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, m, o);
     if (lane >= o) m = max(m, v);
@@ -172,7 +172,7 @@ MARS_DEV void find_part(const Args& a, Scan& sc) {
     if (pass) break;
     mine = q.pre;
     long long incl = mine, sum = count;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
@@ -199,8 +199,11 @@ MARS_DEV void find_part(const Args& a, Scan& sc) {
       sc.ctas = ctas;
     }
     if ((long long)blockIdx.x >= ctas) break;
-    p0 = blockIdx.x * total / ctas;
-    p1 = (blockIdx.x + 1) * total / ctas;
+    const int n = (int)ctas;
+    const long long share = total / n;
+    const int rest = (int)(total - share * n);       // cuts at floor(x total / n)
+    p0 = blockIdx.x * share + blockIdx.x * rest / n;
+    p1 = (blockIdx.x + 1) * share + (blockIdx.x + 1) * rest / n;
     if (tid == 0) {
       sc.p0 = p0;
       sc.p1 = p1;
@@ -240,7 +243,7 @@ struct Window {
     end = mine < a.batch ? min(max(a.cu[mine + 1], 0), a.total) : 0;
     len = mine < a.batch ? a.seq_lens[mine] : 0;
     end = max(end, base);
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, end, o);
       if (lane >= o) end = max(end, v);
@@ -281,7 +284,7 @@ struct alignas(16) Info {
 
 struct Bar {
   uint64_t info_full[kInfos], info_empty[kInfos];
-  uint64_t raw_full[kConvertWarps][kRaw];              // of a warp's two pages
+  uint64_t raw_full[kConvertWarps][kRaw];              // of a warp's page
   // own_raw: an own tile's K in bf16 is in its two slots, own_full: its scales and its two parts are.
   // (Barriers of their own: a wait for a phase of a ring whose last one is still open would pass at
   // once. Two of each: the slots let two own tiles be under way.)
@@ -292,7 +295,6 @@ struct Bar {
   uint64_t pair[4];                  // the two warps of 32 rows
   uint32_t tmem_base;
   int abort;
-  float exchange[2][BQ];             // [even or odd tiles][row]
   uint8_t q_byte[2][BQ];             // [item][row]: scale bytes of Q
 };
 
@@ -301,7 +303,10 @@ struct Bar {
 struct alignas(1024) Shared {
   Bar bar;
   Info infos[kInfos];
-  Scan scan;
+  union {
+    Scan scan;                       // until the walk has published its first tile
+    float exchange[2][BQ];           // [even or odd tiles][row], at the end of items
+  };
 };
 static_assert(sizeof(Shared) == 3072, "with the tiles, all of the shared memory of a CTA");
 
@@ -328,30 +333,39 @@ struct Pipe {
   const Args& a;
   Bar& bar;
   Info* infos;
+  float (&exchange)[2][BQ];
   uint8_t* smem;
   uint32_t tmem;
 
   // Waits of one thread, and of a whole warp (by all lanes: behind a test of the lane a wait that is
-  // over takes 250 cycles instead of 100). They give up after 2^31 cycles, a second or more, and end
-  // all others through `abort`, for which the kernel's end sets the status: these few instructions are
-  // at thirty places of code that has to stay in the instruction cache.
+  // over takes 250 cycles instead of 100). They give up after 2^20 attempts of a microsecond at most,
+  // and the kernel's end then sets the status. These instructions are at thirty places of code that
+  // has to stay in the instruction cache.
   MARS_DEV bool wait(uint64_t* b, uint32_t parity) const {
-    if (sm100::mbar_test_wait(b, parity)) return true;
-    const uint32_t t0 = (uint32_t)clock();
-    do {
-      if (sm100::mbar_try_wait(b, parity)) return true;
-    } while (!*(volatile int*)&bar.abort && (uint32_t)clock() - t0 < 1u << 31);
-    *(volatile int*)&bar.abort = 1;
-    return false;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 0;\n\t"
+        "TRY:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "@p bra DONE;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 p, n, 1048576;\n\t"
+        "@p bra TRY;\n\t"
+        "setp.ne.u32 p, n, n;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(sm100::smem_u32(b)), "r"(parity)
+        : "memory");
+    if (!ok) *(volatile int*)&bar.abort = 1;
+    return ok != 0;
   }
   MARS_DEV bool warp_wait(uint64_t* b, uint32_t parity) const {
     return __all_sync(0xffffffffu, wait(b, parity));
   }
-  // the same for what a thread has in flight when it ends, aborted or not
-  MARS_DEV void drain(uint64_t* b, uint32_t parity) const {
-    const uint32_t t0 = (uint32_t)clock();
-    while (!sm100::mbar_try_wait(b, parity) && (uint32_t)clock() - t0 < 1u << 31) {}
-  }
+  // the same for what a thread has in flight when it ends
+  MARS_DEV void drain(uint64_t* b, uint32_t parity) const { wait(b, parity); }
   MARS_DEV Info& info(int t) const { return infos[t % kInfos]; }
   MARS_DEV uint64_t* info_full(int t, uint32_t& parity) const {
     parity = (t / kInfos) & 1;
@@ -568,34 +582,28 @@ MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& m
   __syncwarp();
 }
 
-// Two raw pages as rows r0 .. r0 + 31 of an f16 tile; of each only the first valid[i] rows, zero
-// for the others.
+// A raw page as rows r0 .. r0 + 15 of an f16 tile, zero from row `valid` of the page on.
 template <int D>
-MARS_DEV void convert_raw(const uint8_t* raw, uint8_t* tile, int r0, int valid0, int valid1) {
-  constexpr int kLanes = D / 16, kStep = 32 / kLanes, kIts = 2 * kPageSize / kStep;
-  const int lane = threadIdx.x & 31, c = lane % kLanes, first = lane / kLanes;
-  uint4 x[kIts];
-#pragma unroll
-  for (int i = 0; i < kIts; ++i) {
-    const int r = first + i * kStep;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (2 * i < kIts ? r < valid0 : r - kPageSize < valid1)
-      x[i] = *reinterpret_cast<const uint4*>(raw + Layout<D>::code_at(r, c));
-  }
+MARS_DEV void convert_raw(const uint8_t* raw, uint8_t* tile, int r0, int valid) {
+  constexpr int kLanes = D / 16, kStep = 32 / kLanes, kIts = kPageSize / kStep;
+  const int lane = threadIdx.x & 31, c = lane % kLanes;
   // lanes of the second region store their chunks in the other order: the eight lanes of a row
   // then hit eight different chunks
   const int up = D == 128 ? c >> 2 : 0;
 #pragma unroll
   for (int i = 0; i < kIts; ++i) {
+    const int r = lane / kLanes + i * kStep;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < valid)
+      x = *reinterpret_cast<const uint4*>(raw + Layout<D>::code_at(r, c));
     uint32_t h[8];
-    q8::decode4(x[i].x, h[0], h[1]);
-    q8::decode4(x[i].y, h[2], h[3]);
-    q8::decode4(x[i].z, h[4], h[5]);
-    q8::decode4(x[i].w, h[6], h[7]);
-    const int r = r0 + first + i * kStep;
+    q8::decode4(x.x, h[0], h[1]);
+    q8::decode4(x.y, h[2], h[3]);
+    q8::decode4(x.z, h[4], h[5]);
+    q8::decode4(x.w, h[6], h[7]);
     const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-    *reinterpret_cast<uint4*>(chunk_at(tile, r, 2 * c + up)) = up ? hi : lo;
-    *reinterpret_cast<uint4*>(chunk_at(tile, r, 2 * c + 1 - up)) = up ? lo : hi;
+    *reinterpret_cast<uint4*>(chunk_at(tile, r0 + r, 2 * c + up)) = up ? hi : lo;
+    *reinterpret_cast<uint4*>(chunk_at(tile, r0 + r, 2 * c + 1 - up)) = up ? lo : hi;
   }
 }
 
@@ -605,16 +613,15 @@ MARS_DEV uint32_t finite_max(uint32_t top, uint32_t word) {
   return __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
 }
 
-// Sixteen bf16 times f as two e4m3 numbers each: the nearest, and the nearest to what that leaves.
-// An infinity becomes NaN (a finite value's second product adds nothing).
-MARS_DEV void split16(const uint4& x, const uint4& y, float f, uint4& first, uint4& second) {
-  uint32_t u[4], v[4];
+// Eight bf16 times f as two e4m3 numbers each: the nearest, and the nearest to what that leaves. An
+// infinity becomes NaN (a finite value's second product adds nothing).
+MARS_DEV void split8(const uint4& x, float f, uint2& first, uint2& second) {
+  float e[8];
+  unpack8(x, e);
+  uint32_t u[2], v[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = i == 0 ? x.x : i == 1 ? x.z : i == 2 ? y.x : y.z;
-    const uint32_t b = i == 0 ? x.y : i == 1 ? x.w : i == 2 ? y.y : y.w;
-    float w[4] = {__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
-                  __uint_as_float(b & 0xffff0000u)};
+  for (int i = 0; i < 2; ++i) {
+    float* w = e + 4 * i;
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = fmaf(w[k], 0.f, w[k] * f);
     u[i] = q8::encode2(w[0], w[1]) | (q8::encode2(w[2], w[3]) << 16);
@@ -623,28 +630,26 @@ MARS_DEV void split16(const uint4& x, const uint4& y, float f, uint4& first, uin
     const float2 p = q8::halves(lo), q = q8::halves(hi);
     v[i] = q8::encode2(w[0] - p.x, w[1] - p.y) | (q8::encode2(w[2] - q.x, w[3] - q.y) << 16);
   }
-  first = make_uint4(u[0], u[1], u[2], u[3]);
-  second = make_uint4(v[0], v[1], v[2], v[3]);
+  first = make_uint2(u[0], u[1]);
+  second = make_uint2(v[0], v[1]);
 }
 
 // Rows in bf16 as two slots of K's ring hold them: the first half of a row's elements in either one's
-// row. Lane c of a row's D / 16 has 16 of them, and its place among the codes of either part.
+// row. Lane c of a row's D / 8 has 8 of them, and its place among the codes of either part.
 template <int D>
 struct Halves {
   using L = Layout<D>;
-  static constexpr int kLanes = D / 16, kRows = 32 / kLanes;         // lanes of a row, rows of a warp
+  static constexpr int kLanes = D / 8, kRows = 32 / kLanes;          // lanes of a row, rows of a warp
   const uint8_t *lo, *hi;
   MARS_DEV int lane() const { return threadIdx.x % kLanes; }
   MARS_DEV int row() const { return threadIdx.x % 32 / kLanes; }
-  MARS_DEV void get(int r, uint4& x, uint4& y) const {
-    const uint8_t* from = lane() < kLanes / 2 ? lo : hi;
-    const int c = lane() % (kLanes / 2) * 2;
-    x = *reinterpret_cast<const uint4*>(from + L::code_at(r, c));
-    y = *reinterpret_cast<const uint4*>(from + L::code_at(r, c + 1));
+  MARS_DEV uint4 get(int r) const {
+    return *reinterpret_cast<const uint4*>((lane() < kLanes / 2 ? lo : hi) +
+                                           L::code_at(r, lane() % (kLanes / 2)));
   }
-  static MARS_DEV uint32_t top(const uint4& x, const uint4& y) {
-    const uint32_t t = finite_max(finite_max(finite_max(finite_max(0u, x.x), x.y), x.z), x.w);
-    return finite_max(finite_max(finite_max(finite_max(t, y.x), y.y), y.z), y.w);
+  MARS_DEV uint32_t code_at(int r) const { return L::code_at(r, lane() / 2) + (lane() & 1) * 8; }
+  static MARS_DEV uint32_t top(const uint4& x) {
+    return finite_max(finite_max(finite_max(finite_max(0u, x.x), x.y), x.z), x.w);
   }
 };
 
@@ -664,22 +669,17 @@ MARS_DEV int own_k(uint8_t* lo, uint8_t* hi, int r0, int count) {
   const int end = min(r0 + kPageSize, count);
   uint32_t top = 0;
 #pragma unroll 1
-  for (int r = r0 + h.row(); r < end; r += H::kRows) {
-    uint4 x, y;
-    h.get(r, x, y);
-    top = __vmaxu2(top, H::top(x, y));
-  }
+  for (int r = r0 + h.row(); r < end; r += H::kRows) top = __vmaxu2(top, H::top(h.get(r)));
   __syncwarp();
   const int byte = own_byte(top, 7);
   const float f = q8::inverse_power(byte);
 #pragma unroll 1
   for (int r = r0 + h.row(); r - h.row() < end; r += H::kRows) {
-    uint4 x, y, u, v;
-    h.get(r, x, y);                                  // of 16 rows that a tile has, whatever they hold
-    split16(x, y, f, u, v);
+    uint2 u, v;
+    split8(h.get(r), f, u, v);                       // of 16 rows that a tile has, whatever they hold
     __syncwarp();                                    // all of the rows has been read
-    *reinterpret_cast<uint4*>(lo + Layout<D>::code_at(r, h.lane())) = u;
-    *reinterpret_cast<uint4*>(hi + Layout<D>::code_at(r, h.lane())) = v;
+    *reinterpret_cast<uint2*>(lo + h.code_at(r)) = u;
+    *reinterpret_cast<uint2*>(hi + h.code_at(r)) = v;
   }
   return byte;
 }
@@ -715,18 +715,17 @@ MARS_DEV int own_v(uint8_t* tile, int r0, int count) {
   return byte;
 }
 
-// Warps 12 ..: copies of their two pages of every tile of V and f16 tiles from them, and the
-// sequence's own K and V.
+// Warps 12 ..: copies of their page of every tile of V and f16 tiles from them, and the sequence's own
+// K and V.
 template <int D>
 MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& map_own) {
   using namespace sm100;
   using L = Layout<D>;
   const Args& a = p.a;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp;
-  const int g = warp * 2;                            // first page in the tile
-  static_assert(kConvertWarps * 2 == kPagesPerTile, "two pages a warp");
+  static_assert(kConvertWarps == kPagesPerTile, "a page a warp");
   uint64_t* const full = p.bar.raw_full[warp];
-  uint8_t* const ring = p.smem + L::OFF_RAW + warp * kRaw * 2 * L::PAGE;
+  uint8_t* const ring = p.smem + L::OFF_RAW + warp * kRaw * L::PAGE;
   // the next copy: its number and tile; `converted`: copies that have left the ring
   int copies = 0, next = 0, converted = 0, slots = 0, own = 0, own_copies = 0;
   bool more = true, ok = true;
@@ -739,13 +738,9 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
       if (flags & kEnd) more = false;
       if (flags & (kEnd | kOwn)) continue;
       if (lane == 0) {
-        const int2 page = *reinterpret_cast<const int2*>(f.page + g);
-        const int st = copies % kRaw;
-        uint8_t* dst = ring + st * 2 * L::PAGE;
-        mbar_arrive_expect_tx(&full[st], ((page.x >= 0) + (page.y >= 0)) * L::PAGE);
-        if (page.x >= 0) tma_load_2d(dst, &map, &full[st], 0, (page.x * a.hkv + f.kvh) * kPageSize);
-        if (page.y >= 0)
-          tma_load_2d(dst + L::PAGE, &map, &full[st], 0, (page.y * a.hkv + f.kvh) * kPageSize);
+        const int page = f.page[warp], st = copies % kRaw;
+        mbar_arrive_expect_tx(&full[st], page >= 0 ? L::PAGE : 0);
+        if (page >= 0) tma_load_2d(ring + st * L::PAGE, &map, &full[st], 0, (page * a.hkv + f.kvh) * kPageSize);
       }
       ++copies;
     }
@@ -770,17 +765,13 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
           tma_load_3d(tile + x * (BKV * 128), &map_own, &p.bar.own_v[own & 1], x * 64, f.kvh, f.base + f.k0);
       }
       if (!(ok = p.warp_wait(&p.bar.own_raw[own & 1], (own >> 1) & 1))) break;
-#pragma unroll 1
-      for (int i = g; i < g + 2; ++i) {
-        const int byte = own_k<D>(p.smem + L::OFF_K + slots % kSlots * L::RAW,
-                                  p.smem + L::OFF_K + (slots + 1) % kSlots * L::RAW, i * kPageSize, f.count);
-        if (lane == 0) f.k_byte[i] = (uint8_t)byte;
-      }
+      const int k_byte = own_k<D>(p.smem + L::OFF_K + slots % kSlots * L::RAW,
+                                  p.smem + L::OFF_K + (slots + 1) % kSlots * L::RAW, warp * kPageSize, f.count);
       if (!(ok = p.warp_wait(&p.bar.own_v[own & 1], (own >> 1) & 1))) break;
-#pragma unroll 1
-      for (int i = g; i < g + 2; ++i) {
-        const int byte = own_v<D>(tile, i * kPageSize, f.count);
-        if (lane == 0) f.v_byte[i] = (uint8_t)byte;
+      const int v_byte = own_v<D>(tile, warp * kPageSize, f.count);
+      if (lane == 0) {
+        f.k_byte[warp] = (uint8_t)k_byte;
+        f.v_byte[warp] = (uint8_t)v_byte;
       }
       slots += 2;
       fence_proxy_async_smem();
@@ -791,10 +782,8 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
       ++slots;
       if (!(ok = p.warp_wait(&full[converted % kRaw], (converted / kRaw) & 1))) break;
       if (!(ok = p.warp_wait(&p.bar.v_empty[ts], ((t / kTiles) & 1) ^ 1))) break;
-      const int2 page = *reinterpret_cast<const int2*>(f.page + g);
-      const int count = f.count - g * kPageSize;
-      convert_raw<D>(ring + converted % kRaw * 2 * L::PAGE, tile, g * kPageSize,
-                     page.x >= 0 ? count : 0, page.y >= 0 ? count - kPageSize : 0);
+      convert_raw<D>(ring + converted % kRaw * L::PAGE, tile, warp * kPageSize,
+                     f.page[warp] >= 0 ? f.count - warp * kPageSize : 0);
       ++converted;
     }
     fence_proxy_async_smem();
@@ -851,7 +840,7 @@ MARS_DEV void issue_s(const Pipe& p) {
       if (!(ok = p.wait(&p.bar.k_full[st], (slots / kSlots) & 1))) break;
       tc_fence_after();
       const uint64_t kd = L::code_desc(p.smem + L::OFF_K + st * L::RAW);
-#pragma unroll
+#pragma unroll 2
       for (int k = 0; k < 2 * (D / 32); ++k) {
         const uint32_t off = k % (D / 32) * 32;
         mma_f8_ss(p.tmem + L::TM_S + sb * BKV, sdesc_advance(qd, off + k / (D / 32) * L::RAW),
@@ -884,7 +873,7 @@ MARS_DEV void issue_pv(const Pipe& p) {
     tc_fence_after();
     const uint64_t vd =
         sdesc_sw128(smem_u32(p.smem + L::OFF_V + t % kTiles * L::TILE), BKV * 128, 1024);
-#pragma unroll
+#pragma unroll 2
     for (int k = 0; k < BKV / 16; ++k)
       mma_bf16_ts(p.tmem + L::TM_O + pb * D, p.tmem + L::TM_S + pb * BKV + L::P_OFF + k * 8,
                   sdesc_advance(vd, k * 2048), idesc, k != 0 || !(flags & (kFirst | kSecond)));
@@ -912,17 +901,17 @@ MARS_DEV bool convert_q(const Pipe& p, int t, int item) {
   const H h{p.smem + L::OFF_K + f.q_slot * L::RAW, p.smem + L::OFF_K + (f.q_slot + 1) % kSlots * L::RAW};
 #pragma unroll 1
   for (int r = warp * H::kRows + h.row(); r - h.row() < rows; r += kSoftmaxWarps * H::kRows) {
-    uint4 x, y, u, v;
-    h.get(r, x, y);
-    uint32_t top = H::top(x, y);
+    const uint4 x = h.get(r);
+    uint32_t top = H::top(x);
     top = max(top >> 16, top & 0xffffu);
 #pragma unroll
     for (int o = 1; o < H::kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     // (a row of next to nothing: 2^-53)
     const int byte = top ? min(max((int)(top >> 7), 74), 253) - 7 : q8::kBias;
-    split16(x, y, q8::inverse_power(byte), u, v);
-    *reinterpret_cast<uint4*>(to + L::code_at(r, h.lane())) = u;
-    *reinterpret_cast<uint4*>(to + L::RAW + L::code_at(r, h.lane())) = v;
+    uint2 u, v;
+    split8(x, q8::inverse_power(byte), u, v);
+    *reinterpret_cast<uint2*>(to + h.code_at(r)) = u;
+    *reinterpret_cast<uint2*>(to + L::RAW + h.code_at(r)) = v;
     if (h.lane() == 0) p.bar.q_byte[item & 1][r] = (uint8_t)byte;
   }
   fence_proxy_async_smem();
@@ -1071,13 +1060,14 @@ MARS_DEV void softmax(const Pipe& p) {
     if (t >= 0 && (flags & kLast)) {
       if (busy) {
         // maxima and sums of the row's even and odd tiles, once both have left the item before
-        float (&x)[2][BQ] = p.bar.exchange;
+        float (&x)[2][BQ] = p.exchange;
         if (!meet()) return;
         x[odd][row] = m;
         if (!meet()) return;
         const float other = x[odd ^ 1][row], top = fmaxf(m, other);
         // (m = +infinity gives NaN)
-        const float w = m > -INFINITY ? exp2f(m - top) : 0.f, w_other = other > -INFINITY ? exp2f(other - top) : 0.f;
+        float w = m > -INFINITY ? flash::ex2_approx(m - top) : 0.f;
+        float w_other = other > -INFINITY ? flash::ex2_approx(other - top) : 0.f;
         if (!meet()) return;
         x[odd][row] = l * w;
         if (!meet()) return;
@@ -1091,23 +1081,24 @@ MARS_DEV void softmax(const Pipe& p) {
         if (two && !p.warp_wait(&p.bar.pv_done[second & 1], (second / kBufs) & 1)) return;
         tc_fence_after();
         // the row's O, half of the columns each: over its sum to where the row is, or into a partial
-        const float w_even = odd ? w_other : w, w_odd = odd ? w : w_other;
-        const bool even = two || !(t & 1), odds = two || (t & 1);
+        // (without tiles of its own, an O is not there: the other one takes its place, times 0)
         const int slot = f.slot;
         const float inv = slot < 0 ? reciprocal(l) : 1.f;
+        const uint32_t mine_at = o_addr + (two ? odd : t & 1) * D, other_at = o_addr + (two ? odd ^ 1 : t & 1) * D;
+        w *= inv;
+        w_other *= inv;
         float4* part = a.part + ((size_t)blockIdx.x * 2 + slot) * L::PART;
         if (slot >= 0 && has && odd == 0) reinterpret_cast<float2*>(part + BQ * D / 4)[row] = make_float2(m, l);
         uint16_t* to = a.o + (((size_t)f.base + tok) * a.hq + f.h0 + row % a.gp) * D;
 #pragma unroll 1
         for (int c = odd * (D / 2); c < (odd + 1) * (D / 2); c += 16) {
           uint32_t u[16], v[16];
-          tmem_ld16(o_addr + c, u);
-          tmem_ld16(o_addr + D + c, v);
+          tmem_ld16(mine_at + c, u);
+          tmem_ld16(other_at + c, v);
           tmem_ld_wait();
           float o[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            o[e] = ((even ? __uint_as_float(u[e]) * w_even : 0.f) + (odds ? __uint_as_float(v[e]) * w_odd : 0.f)) * inv;
+          for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(u[e]), w, __uint_as_float(v[e]) * w_other);
           if (!has) continue;
           if (slot < 0) {
 #pragma unroll
@@ -1206,7 +1197,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Pipe p{a, bar, shared.infos, smem_raw, __shfl_sync(0xffffffffu, bar.tmem_base, 0)};
+  const Pipe p{a, bar, shared.infos, shared.exchange, smem_raw, __shfl_sync(0xffffffffu, bar.tmem_base, 0)};
   if (warp < kSoftmaxWarp) {
     regs_lower<kControlRegs>();
     if (warp == 0) {
