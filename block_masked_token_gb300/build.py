@@ -20,7 +20,7 @@ CALLS = os.path.join(PKG, "_packed_calls" + sysconfig.get_config_var("EXT_SUFFIX
 SOURCES = ["mars_api.cu", "kv_commit.cu", "decode_attn.cu", "head_accept.cu", "dual_stream.cu",
            "tmap.cu", "head_accept_noalloc.cu", "ce_loss.cu", "dual_stream_grad.cu",
            "packed_attn.cu", "packed_grad.cu", "kv_append.cu", "rotary.cu",
-           "kv_append_q8.cu", "chunk_q8.cu"]
+           "kv_append_q8.cu", "chunk_q8.cu", "chunk_q8_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -203,6 +203,7 @@ struct ChunkQ8Plan {
   int gp, tpt;             // heads and tokens of a row tile
   int ctas;
   bool can_split;          // items may be divided among CTAs
+  bool few;                // chunk_q8_few.cu's kernel
   int pages;               // the wide form's pages per sequence (0: without it)
   PackedPlan wide;
   size_t ws_bytes;
