@@ -959,6 +959,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
     fence_barrier_init();
   }
+  wait_for_previous();
+  let_next_start();
   find_part(a, scan);
   if ((long long)blockIdx.x >= scan.ctas) {
     if (threadIdx.x == 0 && a.rec) a.rec[blockIdx.x] = Record{};
@@ -1071,7 +1073,7 @@ Places places(const ChunkQ8Plan& plan, int batch, int hkv, int d) {
     l.v = l.k + (size_t)batch * plan.pages * hkv * kPageSize * d * 2;
     l.rec = l.v + (l.v - l.k);
   }
-  const size_t rows = plan.few ? kFewRows : BQ;      // of a partial
+  const size_t rows = plan.few ? plan.few : BQ;      // of a partial
   l.part = l.end = l.rec;
   if (plan.can_split) {
     l.part = l.rec + packed::align256(plan.ctas * sizeof(Record));
@@ -1143,7 +1145,8 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   if (!encode_tmap_u8(&map_k, any ? p.k_pool : none, 2, dims, pitch, box) ||
       !encode_tmap_u8(&map_v, any ? p.v_pool : none, 2, dims, pitch, box))
     return cudaErrorInvalidValue;
-  if (plan.few) return launch_chunk_q8_few<D>(a, plan.ctas, map_k, map_v, stream);
+  if (plan.few == 8) return launch_chunk_q8_few<D, 8>(a, plan.ctas, map_k, map_v, stream);
+  if (plan.few == 16) return launch_chunk_q8_few<D, 16>(a, plan.ctas, map_k, map_v, stream);
   using L = Layout<D>;
   static_assert(L::TOTAL + sizeof(Shared) <= 227 * 1024,
                 "layout fits shared memory");
@@ -1161,14 +1164,14 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
       !rows(&map_own_k, t.k, t.hkv, t.k_stride, D / 2, 1, BKV) ||
       !rows(&map_own_v, t.v, t.hkv, t.v_stride, 64, 1, BKV))
     return cudaErrorInvalidValue;
-  chunk_kernel<D><<<plan.ctas, kThreads, L::TOTAL, stream>>>(map_k, map_v, map_q, map_own_k, map_own_v, a);
+  e = launch_early(chunk_kernel<D>, plan.ctas, kThreads, L::TOTAL, stream, map_k, map_v, map_q, map_own_k,
+                   map_own_v, a);
   count_launches(1);
-  e = cudaGetLastError();
   if (e != cudaSuccess || !plan.can_split) return e;
   const int most = std::min(plan.gp * std::min(plan.tpt, t.total), BQ);      // rows of an item
-  merge_kernel<D, BQ><<<dim3(plan.ctas, (most * (D / 4) + 255) / 256), 256, 0, stream>>>(a, plan.ctas);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_early(merge_kernel<D, BQ>, dim3(plan.ctas, (most * (D / 4) + 255) / 256), 256, 0, stream, a,
+                      plan.ctas);
 }
 
 }  // namespace
@@ -1179,10 +1182,11 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
   p.gp = p.wide.gp;
   p.tpt = p.wide.tpt;
   const int group = hq / hkv;
-  p.few = group <= kFewRows && total <= (long long)batch * (kFewRows / group);
+  for (int rows : {16, 8})
+    if (group <= rows && total <= (long long)batch * (rows / group)) p.few = rows;
   if (p.few) {
     p.gp = group;
-    p.tpt = kFewRows / group;
+    p.tpt = p.few / group;
   }
   // The wide form where packed_attn.cu would take pairs of row tiles (plan_packed), unless its pages
   // could not be counted or took more than 4 GB.

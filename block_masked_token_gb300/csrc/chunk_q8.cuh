@@ -33,8 +33,6 @@ constexpr long long kUnit = 8, kItemWork = 12;   // work of a key tile and of an
 constexpr float kLift = 7.f;         // log2 of what P' is multiplied by
 constexpr float kNoKeys = -1.f;      // l of a part without keys, which has no O
 
-constexpr int kFewRows = 16;         // rows of an item of chunk_q8_few.cu
-
 // float4 of a partial: D / 4 columns of an item's kRows rows, then m' and l of each.
 template <int D, int kRows>
 constexpr int kPartial = kRows * D / 4 + kRows / 2;
@@ -129,6 +127,7 @@ MARS_DEV void find_part(const Args& a, Scan<kThreads>& sc) {
   const int lo = (int)min((long long)tid * per, (long long)a.batch), hi = min(lo + per, a.batch);
   auto clamped = [&](int s) { return min(max(a.cu[s], 0), a.total); };
   int bad = 0, m = 0;
+  if (lo < hi) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seq_lens + lo));
   for (int s = lo; s < hi; ++s) m = max(m, clamped(s + 1));
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
@@ -271,6 +270,7 @@ MARS_DEV float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
 template <int D, int kRows>
 __global__ void __launch_bounds__(256) merge_kernel(Args a, int ctas) {
   constexpr int PART = kPartial<D, kRows>;
+  sm100::wait_for_previous();
   const int x = blockIdx.x, lane = threadIdx.x & 31;
   const Record rec = a.rec[x];
   if (!rec.begins) return;
@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(256) merge_kernel(Args a, int ctas) {
 
 }  // namespace q8
 
-// chunk_q8_few.cu, for items of kFewRows rows at most; k and v map the pools, pages of a KV head as boxes.
-template <int D>
+// chunk_q8_few.cu, for items of kRows rows, 8 or 16; k and v map the pools, a page of a KV head as a box.
+template <int D, int kRows>
 cudaError_t launch_chunk_q8_few(const q8::Args& a, int ctas, const CUtensorMap& k, const CUtensorMap& v,
                                 cudaStream_t stream);
 

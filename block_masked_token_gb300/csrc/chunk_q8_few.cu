@@ -3,18 +3,20 @@
 //
 // With so few rows the work is the reading of the cache: 2 D bytes per key and KV head against
 // 4 * rows * D flops. chunk_q8.cu's roles and its 128-row tiles cost more there than the reading.
-// Here a CTA's eight warps are alike and do not wait for each other: warp w takes pages w, w + 8, ..
+// Here a CTA's warps are alike and do not wait for each other: warp w takes pages w, w + kWarps, ..
 // of the CTA's part of an item (chunk_q8.cuh), copies them by TMA through a ring of its own, and
 // keeps its own running maximum, sum and O in registers, which the CTA joins at the part's end. A
-// page is a step: S = Q K^T is 16 x 16 of it, P V one product of depth 16, by mma.sync, whose
-// operands come from registers: codes are converted (e4m3 to f16, exactly) where they are used and
-// never stored again, and one warp's conversion runs beside another's products. The order of d
-// inside a product is free, and of O's columns too; both are taken so that a lane's operands are
+// page is a step: S^T = K Q^T and O^T += V^T P^T by mma.sync, with 16 keys and 16 of d as its 16 rows
+// and 8 rows of the item as its 8 columns. (The other way round half of each product would be empty
+// for the 7 or 8 rows of a single token.) Codes are converted (e4m3 to f16, exactly) where they are
+// used and never stored again, and one warp's conversion runs beside another's products. The order
+// of d inside a product is free, and of O's rows too; both are taken so that a lane's operands are
 // whole 16-byte reads of shared memory, without bank conflicts:
-//   K: lane (g, t) of key g (and 8 + g) holds d = t D/4 .. of it; four consecutive d are its part
-//      of a step of 16.
-//   V: lane (g, t) holds d = g D/8 .. of keys 2t, 2t + 1, 2t + 8, 2t + 9; byte permutations pair
-//      the codes of two keys. Column g of product j is then d = g D/8 + j.
+//   K: lane (g, t) = (lane / 4, lane % 4) of keys g and 8 + g holds d = t D/4 .. of them; four
+//      consecutive d are its part of a step of 16.
+//   V: lane (g, t) holds d = g D/8 .. of keys 2t, 2t + 1, 2t + 8, 2t + 9; byte permutations pair the
+//      codes of two keys. Rows g and 8 + g of product j are then d = g D/8 + 2j and the next.
+// A lane has the scores of keys g and 8 + g for rows 2t and 2t + 1; movmatrix turns the weights.
 #include <algorithm>
 #include <atomic>
 
@@ -25,9 +27,7 @@ namespace {
 
 using namespace q8;
 
-constexpr int kRows = kFewRows, kWarps = 8, kThreads = 32 * kWarps, kStages = 4;
 constexpr int kList = 32;            // parts found at a time
-static_assert(kRows == 16, "a product's");
 
 // A part of an item: which rows, which own keys and which cached pages.
 struct Part {
@@ -38,76 +38,92 @@ struct Part {
   MARS_DEV int units() const { return pages() + (own1 - own0 + kPageSize - 1) / kPageSize; }
 };
 
-template <int D>
+// The parts of this CTA, one after another. Whole warp; where it is stays in shared memory.
+struct Place {
+  Row q;                             // at item i, tile j of it; before the end, items and tiles too
+  int i, j, es, ei, ej;
+  bool more;
+  Record rec;
+};
+template <int kThreads>
+MARS_DEV Place first_place(const Args& a, const Scan<kThreads>& sc) {
+  Place w{sc.at[0], 0, 0, a.batch, 0, 0, true, {}};
+  if (sc.p1 < sc.total) {
+    w.es = sc.at[1].s;
+    cut_at(a, sc.at[1], sc.p1, w.ei, w.ej);
+  }
+  cut_at(a, w.q, sc.p0, w.i, w.j);
+  return w;
+}
+MARS_DEV bool next_part(const Args& a, Place& w, Window& window, Part& p) {
+  if (!w.more) return false;
+  Row& q = w.q;
+  if (w.i >= items_of(a, q)) {
+    w.i = w.j = 0;
+    do {
+      w.more = q.s + 1 < a.batch && q.s + 1 <= w.es;
+      if (w.more) q = window.after(q);
+    } while (w.more && items_of(a, q) == 0);
+  }
+  w.more = w.more && !(q.s > w.es || (q.s == w.es && (w.i > w.ei || (w.i == w.ei && w.j >= w.ej))));
+  if (!w.more) return false;
+  const int tiles = q.tiles(), jb = q.s == w.es && w.i == w.ei ? w.ej : tiles;
+  const int hg = w.i % a.heads, last_tok = min((w.i / a.heads + 1) * a.tpt, q.n) - 1;
+  p.s = q.s;
+  p.base = q.base;
+  p.tok0 = w.i / a.heads * a.tpt;
+  p.tokens = last_tok + 1 - p.tok0;
+  p.h0 = hg * a.gp;
+  p.kvh = hg / (a.heads / a.hkv);
+  p.slot = w.j > 0 ? 0 : jb < tiles ? 1 : -1;
+  if (p.slot == 1) w.rec = Record{1, w.rec.inside, p.base, p.tok0, p.tokens, p.h0, {0, 0}};
+  if (p.slot == 0 && jb < tiles) w.rec.inside = 1;
+  // own tiles [j, own), cached tiles from behind them
+  const int own = q.own();
+  p.own0 = min(min(w.j, own) * kTile, last_tok + 1);
+  p.own1 = jb < own ? min(jb * kTile, last_tok + 1) : last_tok + 1;
+  p.page0 = max(w.j - own, 0) * kPagesPerTile;
+  p.keys = q.P;
+  p.page1 = min(max(jb - own, 0) * kPagesPerTile, q.P / kPageSize + (q.P % kPageSize != 0));
+  ++w.i;
+  w.j = 0;
+  return true;
+}
+
+#ifndef FW8
+#define FW8 16
+#define FS8 2
+#define FW16 8
+#define FS16 4
+#endif
+template <int D, int kRows>
 struct Shared {
-  static constexpr int kPage = kPageSize * D, kVec = D / 8;        // kVec: float4 of O per lane
+  static constexpr int kWarps = kRows == 8 ? FW8 : FW16, kThreads = 32 * kWarps, kStages = kRows == 8 ? FS8 : FS16;
+  static constexpr int kPage = kPageSize * D;
+  static constexpr int kVec = kRows * D / 128;       // float4 of O per lane
   uint8_t ring[kWarps][kStages][2][kPage];           // codes of K and V
   float4 o[kWarps][kVec][32];
   float2 ml[kWarps][kRows];
   uint64_t full[kWarps][kStages];
   Part parts[kList];
+  Place place;
   Scan<kThreads> scan;
-  int found, abort;
+  int found;
 };
 
-// The parts of this CTA, one after another. Whole warp.
-struct Walk {
-  const Args& a;
-  Row q, last;
-  int i, j, es, ei, ej;
-  bool more;
-  Window window;
-  Record rec;
-  MARS_DEV Walk(const Args& a_, const Scan<kThreads>& sc)
-      : a(a_), q(sc.at[0]), i(0), j(0), es(a_.batch), ei(0), ej(0), more(true), window(a_), rec{} {
-    if (sc.p1 < sc.total) {
-      es = sc.at[1].s;
-      cut_at(a, sc.at[1], sc.p1, ei, ej);
-    }
-    cut_at(a, q, sc.p0, i, j);
-  }
-  MARS_DEV bool next(Part& p) {
-    if (!more) return false;
-    if (i >= items_of(a, q)) {
-      i = j = 0;
-      do {
-        more = q.s + 1 < a.batch && q.s + 1 <= es;
-        if (more) q = window.after(q);
-      } while (more && items_of(a, q) == 0);
-    }
-    more = more && !(q.s > es || (q.s == es && (i > ei || (i == ei && j >= ej))));
-    if (!more) return false;
-    const int tiles = q.tiles(), jb = q.s == es && i == ei ? ej : tiles;
-    const int hg = i % a.heads, last_tok = min((i / a.heads + 1) * a.tpt, q.n) - 1;
-    p.s = q.s;
-    p.base = q.base;
-    p.tok0 = i / a.heads * a.tpt;
-    p.tokens = last_tok + 1 - p.tok0;
-    p.h0 = hg * a.gp;
-    p.kvh = hg / (a.heads / a.hkv);
-    p.slot = j > 0 ? 0 : jb < tiles ? 1 : -1;
-    if (p.slot == 1) rec = Record{1, rec.inside, p.base, p.tok0, p.tokens, p.h0, {0, 0}};
-    if (p.slot == 0 && jb < tiles) rec.inside = 1;
-    // own tiles [j, own), cached tiles from behind them
-    const int own = q.own();
-    p.own0 = min(min(j, own) * kTile, last_tok + 1);
-    p.own1 = jb < own ? min(jb * kTile, last_tok + 1) : last_tok + 1;
-    p.page0 = max(j - own, 0) * kPagesPerTile;
-    p.keys = q.P;
-    p.page1 = min(max(jb - own, 0) * kPagesPerTile, q.P / kPageSize + (q.P % kPageSize != 0));
-    ++i;
-    j = 0;
-    return true;
-  }
-};
-
+// 8 x 8 halves, two of a row to a lane, transposed.
+MARS_DEV uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 // D += A B: 16 x 8, of depth 16, f16 operands.
-MARS_DEV void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+MARS_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // bf16 rows as f16 over a power of two that brings the largest finite magnitude into
@@ -126,12 +142,13 @@ MARS_DEV uint32_t to_f16(uint32_t word, float f) {
 constexpr int kLeastRow = -126;      // Q and K: 2^126 is the largest factor
 constexpr int kLeastV = -60;         // V: the sums of P' 2^-e stay far from the ends of the range
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int kRows>
+__global__ void __launch_bounds__(Shared<D, kRows>::kThreads, 1)
 few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Args a) {
   using namespace sm100;
-  using Sh = Shared<D>;
-  constexpr int kSteps = D / 16, kTiles = D / 8;     // products of S along d, and of O
+  using Sh = Shared<D, kRows>;
+  constexpr int kWarps = Sh::kWarps, kStages = Sh::kStages;
+  constexpr int kCols = kRows / 8, kSteps = D / 16;  // products next to each other; along d
   constexpr int kQuads = D / 32;                     // 16-byte reads of D/4 bf16
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Sh& sh = *reinterpret_cast<Sh*>(smem_raw);
@@ -141,28 +158,37 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
     return;
   }
   if (lane < kStages) mbar_init(&sh.full[warp][lane], 1);
-  if (threadIdx.x == 0) sh.abort = 0;
   fence_barrier_init();
+  if (threadIdx.x < 2) prefetch_tmap(threadIdx.x ? &tm_v : &tm_k);
+  wait_for_previous();
+  let_next_start();
   find_part(a, sh.scan);
   if ((long long)blockIdx.x >= sh.scan.ctas) {
     if (threadIdx.x == 0 && a.rec) a.rec[blockIdx.x] = Record{};
     return;
   }
-  Walk walk(a, sh.scan);                             // warp 0's is used
+  if (threadIdx.x == 0) sh.place = first_place(a, sh.scan);
   uint64_t* full = sh.full[warp];
   bool ok = true;
   int flags = 0;
   uint32_t issued = 0, used = 0;                     // stages, counted on
   uint32_t meta = 0;                                 // of stage `lane`: scale bytes of K and V, and keys
-  for (bool first = true;; first = false) {
+  for (;;) {
     if (warp == 0) {
-      int n = 0;
+      __syncwarp();
+      Place place = sh.place;
+      Window window(a);
       Part p;
-      while (n < kList && walk.next(p)) {
+      int n = 0;
+      while (n < kList && next_part(a, place, window, p)) {
         if (lane == 0) sh.parts[n] = p;
         ++n;
       }
-      if (lane == 0) sh.found = n;
+      __syncwarp();
+      if (lane == 0) {
+        sh.place = place;
+        sh.found = n;
+      }
     }
     __syncthreads();
     const int found = sh.found;
@@ -220,84 +246,98 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
     for (int part = 0; part < found; ++part) {
       const Part& p = sh.parts[part];
       const int pages = p.pages(), units = p.units();
-      // ---- Q: rows g and 8 + g, d = t D/4 ..
-      uint32_t qa[kSteps][4];
-      float factor[2];
-      int tok[2];
-      bool has[2];
+      // ---- Q: row 8n + g, d = t D/4 .. ; factors and tokens of rows 8n + 2t, 8n + 2t + 1
+      uint32_t qb[kCols][kSteps][2];
+      float factor[kCols][2];
+      int tok[kCols][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = g + 8 * h;
-        tok[h] = p.tok0 + row / a.gp;
-        has[h] = row < p.tokens * a.gp;
+      for (int n = 0; n < kCols; ++n) {
+        const int row = 8 * n + g;
+        const bool has = row < p.tokens * a.gp;
         uint4 x[kQuads];
-        const uint16_t* from_q = a.q + ((size_t)p.base + tok[h]) * a.q_stride + (p.h0 + row % a.gp) * D + t * (D / 4);
+        const uint16_t* from_q = a.q + ((size_t)p.base + p.tok0 + row / a.gp) * a.q_stride +
+                                 (p.h0 + row % a.gp) * D + t * (D / 4);
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < kQuads; ++e) {
-          x[e] = has[h] ? reinterpret_cast<const uint4*>(from_q)[e] : make_uint4(0, 0, 0, 0);
+          x[e] = has ? reinterpret_cast<const uint4*>(from_q)[e] : make_uint4(0, 0, 0, 0);
           top = word_max(x[e], top);
         }
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int ex = row_exponent(top, kLeastRow);
         const float f = power(kBias - ex);
-        factor[h] = a.scale_log2 * power(kBias + ex);
 #pragma unroll
         for (int e = 0; e < kQuads; ++e) {
-          qa[2 * e][h] = to_f16(x[e].x, f);
-          qa[2 * e][2 + h] = to_f16(x[e].y, f);
-          qa[2 * e + 1][h] = to_f16(x[e].z, f);
-          qa[2 * e + 1][2 + h] = to_f16(x[e].w, f);
+          qb[n][2 * e][0] = to_f16(x[e].x, f);
+          qb[n][2 * e][1] = to_f16(x[e].y, f);
+          qb[n][2 * e + 1][0] = to_f16(x[e].z, f);
+          qb[n][2 * e + 1][1] = to_f16(x[e].w, f);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          factor[n][r] = a.scale_log2 * power(kBias + __shfl_sync(0xffffffffu, ex, 8 * t + 4 * r));
+          tok[n][r] = p.tok0 + (8 * n + 2 * t + r) / a.gp;
         }
       }
-      float o[kTiles][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float o[kCols][kSteps][4], m[kCols][2], l[kCols][2];
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j)
+      for (int n = 0; n < kCols; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-      // Scores y (s + e; of keys 2t, 2t + 1 of row g, then of row 8 + g; then of the keys 8 on) to
-      // weights, in pa as the left operand of P V. inv: 2^-e of the lane's keys.
-      auto weights = [&](float (&y)[2][4], const float (&inv)[4], uint32_t (&pa)[4]) {
-        float top[2];
+        for (int j = 0; j < kSteps; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          top[h] = fmaxf(fmaxf(y[0][2 * h], y[0][2 * h + 1]), fmaxf(y[1][2 * h], y[1][2 * h + 1]));
+          for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
+      }
+      // Scores y (s + e; of key g and rows 8n + 2t, 8n + 2t + 1, then of key 8 + g) to weights, in pb
+      // as the right operand of V^T P^T. inv: 2^-e of the two keys.
+      auto weights = [&](float (&y)[kCols][4], float inv0, float inv1, uint32_t (&pb)[kCols][2]) {
         // the maxima of rows are only brought together where one outgrows the running one
-        const float limit0 = m[0] + flash::kRescaleLog2, limit1 = m[1] + flash::kRescaleLog2;
-        if (__any_sync(0xffffffffu, top[0] > limit0 || top[1] > limit1)) {
+        bool grows = false;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-            if (!(top[h] > m[h] + flash::kRescaleLog2)) continue;
-            if (m[h] != -INFINITY) {
-              const float alpha = flash::ex2_approx(m[h] - top[h]);
-              l[h] *= alpha;
+        for (int n = 0; n < kCols; ++n)
 #pragma unroll
-              for (int j = 0; j < kTiles; ++j) {
-                o[j][2 * h] *= alpha;
-                o[j][2 * h + 1] *= alpha;
+          for (int r = 0; r < 2; ++r) grows |= fmaxf(y[n][r], y[n][2 + r]) > m[n][r] + flash::kRescaleLog2;
+        if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+          for (int n = 0; n < kCols; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float top = fmaxf(y[n][r], y[n][2 + r]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              if (!(top > m[n][r] + flash::kRescaleLog2)) continue;
+              if (m[n][r] != -INFINITY) {
+                const float alpha = flash::ex2_approx(m[n][r] - top);
+                l[n][r] *= alpha;
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) {
+                  o[n][j][r] *= alpha;
+                  o[n][j][2 + r] *= alpha;
+                }
               }
+              m[n][r] = top;
             }
-            m[h] = top[h];
-          }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float shift = kLift - (m[h] == -INFINITY ? 0.f : m[h]);
+        for (int n = 0; n < kCols; ++n) {
+          float w[4];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float w0 = flash::ex2_approx(y[n][2 * h] + shift), w1 = flash::ex2_approx(y[n][2 * h + 1] + shift);
-            l[h] = fmaf(w0, inv[2 * n], fmaf(w1, inv[2 * n + 1], l[h]));
-            pa[2 * n + h] = pack_f16x2(w0, w1);
+          for (int r = 0; r < 2; ++r) {
+            const float shift = kLift - (m[n][r] == -INFINITY ? 0.f : m[n][r]);
+            w[r] = flash::ex2_approx(y[n][r] + shift);
+            w[2 + r] = flash::ex2_approx(y[n][2 + r] + shift);
+            l[n][r] = fmaf(w[r], inv0, fmaf(w[2 + r], inv1, l[n][r]));
           }
+          pb[n][0] = transposed(pack_f16x2(w[0], w[1]));
+          pb[n][1] = transposed(pack_f16x2(w[2], w[3]));
         }
       };
 #pragma unroll 1
       for (int u = warp; u < units; u += kWarps) {
-        float y[2][4] = {};
-        uint32_t pa[4];
+        float y[kCols][4] = {};
+        uint32_t pb[kCols][2];
         if (u < pages) {
           const int st = used % kStages;
           ok = ok && __all_sync(0xffffffffu, wait_bounded(&full[st], (used / kStages) & 1));
@@ -310,21 +350,12 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
             const uint8_t* v = sh.ring[warp][st][1];
             // 16-byte chunk c of row r, as the copies swizzle it
             auto chunk = [](int r, int c) { return r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4); };
+            uint4 kx[2][D / 64];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c) {
-                const uint4 x = *reinterpret_cast<const uint4*>(k + chunk(8 * n + g, t * (D / 64) + c));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  uint32_t b0, b1;
-                  decode4(w[e], b0, b1);
-                  mma(y[n], qa[4 * c + e], b0, b1);
-                }
-              }
-            }
-            // V's words early: their reading is done by the time that the weights are
+              for (int c = 0; c < D / 64; ++c)
+                kx[h][c] = *reinterpret_cast<const uint4*>(k + chunk(8 * h + g, t * (D / 64) + c));
             uint32_t x[4][D / 32];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -336,41 +367,54 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                     *reinterpret_cast<const uint2*>(v + chunk(row, g >> 1) + (g & 1) * 8);
               }
             }
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              const uint32_t w0[4] = {kx[0][c].x, kx[0][c].y, kx[0][c].z, kx[0][c].w};
+              const uint32_t w1[4] = {kx[1][c].x, kx[1][c].y, kx[1][c].z, kx[1][c].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t a0, a1, a2, a3;
+                decode4(w0[e], a0, a2);
+                decode4(w1[e], a1, a3);
+#pragma unroll
+                for (int n = 0; n < kCols; ++n)
+                  mma(y[n], a0, a1, a2, a3, qb[n][4 * c + e][0], qb[n][4 * c + e][1]);
+              }
+            }
             __syncwarp();
             const float e = (float)(vb - kBias), inv = inverse_power(vb);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // (never 0 or infinite: it meets infinite scores)
-              const float mul = fminf(fmaxf(factor[h] * power(kb), 1e-38f), 3e38f);
+            for (int n = 0; n < kCols; ++n)
 #pragma unroll
-              for (int n = 0; n < 2; ++n) {
-                y[n][2 * h] = fmaf(y[n][2 * h], mul, e);
-                y[n][2 * h + 1] = fmaf(y[n][2 * h + 1], mul, e);
+              for (int r = 0; r < 2; ++r) {
+                // (never 0 or infinite: it meets infinite scores)
+                const float mul = fminf(fmaxf(factor[n][r] * power(kb), 1e-38f), 3e38f);
+                y[n][r] = fmaf(y[n][r], mul, e);
+                y[n][2 + r] = fmaf(y[n][2 + r], mul, e);
               }
-            }
             if (count < kPageSize) {                 // free slots, which may hold anything
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
+              for (int n = 0; n < kCols; ++n)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                  if (8 * n + 2 * t + (c & 1) >= count) y[n][c] = -INFINITY;
+                  if (g + 4 * (c & 2) >= count) y[n][c] = -INFINITY;
 #pragma unroll
               for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int w = 0; w < D / 32; ++w)
                   if (2 * t + (r & 1) + 4 * (r & 2) >= count) x[r][w] = 0;
             }
-            weights(y, {inv, inv, inv, inv}, pa);
+            weights(y, inv, inv, pb);
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) {
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
                 const uint32_t pick = half ? 0x7362 : 0x5140;       // bytes of two keys in turn
-                uint32_t b0[2], b1[2];
-                decode4(__byte_perm(x[0][w], x[1][w], pick), b0[0], b0[1]);
-                decode4(__byte_perm(x[2][w], x[3][w], pick), b1[0], b1[1]);
-                mma(o[4 * w + 2 * half], pa, b0[0], b1[0]);
-                mma(o[4 * w + 2 * half + 1], pa, b0[1], b1[1]);
+                uint32_t a0, a1, a2, a3;
+                decode4(__byte_perm(x[0][w], x[1][w], pick), a0, a1);
+                decode4(__byte_perm(x[2][w], x[3][w], pick), a2, a3);
+#pragma unroll
+                for (int n = 0; n < kCols; ++n) mma(o[n][2 * w + half], a0, a1, a2, a3, pb[n][0], pb[n][1]);
               }
             }
           }
@@ -378,34 +422,35 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         } else {
           // ---- 16 own keys, each over powers of two of its own
           const int k0 = p.own0 + (u - pages) * kPageSize, count = min(p.own1 - k0, kPageSize);
-          float mul[2][2][2], e[4], inv[4];          // mul: [row][8 keys][key 2t, 2t + 1]
+          uint4 kx[2][kQuads];
+          float of_key[2], e[4];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int key = 8 * n + g;
+          for (int h = 0; h < 2; ++h) {
+            const int key = 8 * h + g;
             const uint16_t* row = a.k + ((size_t)p.base + k0 + key) * a.k_stride + p.kvh * D + t * (D / 4);
-            uint4 x[kQuads];
             uint32_t top = 0;
 #pragma unroll
             for (int c = 0; c < kQuads; ++c) {
-              x[c] = key < count ? reinterpret_cast<const uint4*>(row)[c] : make_uint4(0, 0, 0, 0);
-              top = word_max(x[c], top);
+              kx[h][c] = key < count ? reinterpret_cast<const uint4*>(row)[c] : make_uint4(0, 0, 0, 0);
+              top = word_max(kx[h][c], top);
             }
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int ex = row_exponent(top, kLeastRow);
             const float f = power(kBias - ex);
+            of_key[h] = power(kBias + ex);
 #pragma unroll
-            for (int c = 0; c < kQuads; ++c) {
-              mma(y[n], qa[2 * c], to_f16(x[c].x, f), to_f16(x[c].y, f));
-              mma(y[n], qa[2 * c + 1], to_f16(x[c].z, f), to_f16(x[c].w, f));
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float of_key = power(kBias + __shfl_sync(0xffffffffu, ex, 8 * t + 4 * c));
-#pragma unroll
-              for (int h = 0; h < 2; ++h) mul[h][n][c] = fminf(fmaxf(factor[h] * of_key, 1e-38f), 3e38f);
-            }
+            for (int c = 0; c < kQuads; ++c)
+              kx[h][c] = make_uint4(to_f16(kx[h][c].x, f), to_f16(kx[h][c].y, f), to_f16(kx[h][c].z, f),
+                                    to_f16(kx[h][c].w, f));
           }
+#pragma unroll
+          for (int c = 0; c < kQuads; ++c)
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) {
+              mma(y[n], kx[0][c].x, kx[1][c].x, kx[0][c].y, kx[1][c].y, qb[n][2 * c][0], qb[n][2 * c][1]);
+              mma(y[n], kx[0][c].z, kx[1][c].z, kx[0][c].w, kx[1][c].w, qb[n][2 * c + 1][0], qb[n][2 * c + 1][1]);
+            }
           uint32_t x[4][D / 16];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -423,46 +468,55 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
             const int ex = row_exponent(top, kLeastV);
             const float f = power(kBias - ex);
             e[r] = (float)ex;
-            inv[r] = f;
 #pragma unroll
             for (int w = 0; w < D / 16; ++w) x[r][w] = to_f16(x[r][w], f);
           }
+          float of_v[2];                             // exponents of keys g and 8 + g
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int h = 0; h < 2; ++h) {
+            const float even = __shfl_sync(0xffffffffu, e[2 * h], g >> 1);
+            const float odd = __shfl_sync(0xffffffffu, e[2 * h + 1], g >> 1);
+            of_v[h] = g & 1 ? odd : even;
+          }
+#pragma unroll
+          for (int n = 0; n < kCols; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const int key = 8 * n + 2 * t + (c & 1);
-              const bool sees = key < count && k0 + key <= tok[c >> 1];
-              y[n][c] = sees ? fmaf(y[n][c], mul[c >> 1][n][c & 1], e[2 * n + (c & 1)]) : -INFINITY;
+              const int key = g + 4 * (c & 2);
+              const float mul = fminf(fmaxf(factor[n][c & 1] * of_key[c >> 1], 1e-38f), 3e38f);
+              const bool sees = key < count && k0 + key <= tok[n][c & 1];
+              y[n][c] = sees ? fmaf(y[n][c], mul, of_v[c >> 1]) : -INFINITY;
             }
-          weights(y, inv, pa);
+          weights(y, power(kBias - (int)of_v[0]), power(kBias - (int)of_v[1]), pb);
 #pragma unroll
-          for (int w = 0; w < D / 16; ++w) {
-            mma(o[2 * w], pa, __byte_perm(x[0][w], x[1][w], 0x5410), __byte_perm(x[2][w], x[3][w], 0x5410));
-            mma(o[2 * w + 1], pa, __byte_perm(x[0][w], x[1][w], 0x7632), __byte_perm(x[2][w], x[3][w], 0x7632));
-          }
+          for (int w = 0; w < D / 16; ++w)
+#pragma unroll
+            for (int n = 0; n < kCols; ++n)
+              mma(o[n][w], __byte_perm(x[0][w], x[1][w], 0x5410), __byte_perm(x[0][w], x[1][w], 0x7632),
+                  __byte_perm(x[2][w], x[3][w], 0x5410), __byte_perm(x[2][w], x[3][w], 0x7632), pb[n][0],
+                  pb[n][1]);
         }
       }
       // ---- the warps' maxima, sums and O together
       __syncthreads();                               // the part before is out
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        if (t == 0) sh.ml[warp][g + 8 * h] = make_float2(m[h], l[h]);
-      }
-      // vector (w, h, c): row 8h + g, d = (2t + c) D/8 + 4w ..
+      for (int n = 0; n < kCols; ++n)
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w)
+        for (int r = 0; r < 2; ++r) {
 #pragma unroll
-        for (int hc = 0; hc < 4; ++hc)
-          sh.o[warp][4 * w + hc][lane] =
-              make_float4(o[4 * w][hc], o[4 * w + 1][hc], o[4 * w + 2][hc], o[4 * w + 3][hc]);
+          for (int x = 4; x < 32; x <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], x);
+          if (g == 0) sh.ml[warp][8 * n + 2 * t + r] = make_float2(m[n][r], l[n][r]);
+          // vector (n, r, w): row 8n + 2t + r, d = g D/8 + 4w ..
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w)
+            sh.o[warp][(2 * n + r) * (D / 32) + w][lane] = make_float4(
+                o[n][2 * w][r], o[n][2 * w][2 + r], o[n][2 * w + 1][r], o[n][2 * w + 1][2 + r]);
+        }
       __syncthreads();
       float4* to_part = a.part + ((size_t)blockIdx.x * 2 + p.slot) * kPartial<D, kRows>;
 #pragma unroll 1
       for (int i = warp; i < Sh::kVec; i += kWarps) {
-        const int row = g + 4 * (i & 2), d = (2 * t + (i & 1)) * (D / 8) + (i >> 2) * 4;
+        const int nr = i / (D / 32), row = 8 * (nr >> 1) + 2 * t + (nr & 1), d = g * (D / 8) + i % (D / 32) * 4;
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.ml[w][row].x);
@@ -497,27 +551,30 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
   }
   flags = __reduce_or_sync(0xffffffffu, (unsigned)flags);
   if (lane == 0 && flags && a.status) atomicOr(a.status, flags);
-  if (threadIdx.x == 0 && a.rec) a.rec[blockIdx.x] = walk.rec;
+  if (threadIdx.x == 0 && a.rec) a.rec[blockIdx.x] = sh.place.rec;
 }
 
 }  // namespace
 
-template <int D>
+template <int D, int kRows>
 cudaError_t launch_chunk_q8_few(const q8::Args& a, int ctas, const CUtensorMap& k, const CUtensorMap& v,
                                 cudaStream_t stream) {
-  static_assert(sizeof(Shared<D>) <= 227 * 1024, "shared memory of a CTA");
+  using Sh = Shared<D, kRows>;
+  static_assert(sizeof(Sh) <= 227 * 1024, "shared memory of a CTA");
   static std::atomic<int> attr[64];
-  cudaError_t e = set_smem_limit_once(few_kernel<D>, sizeof(Shared<D>), attr);
+  cudaError_t e = set_smem_limit_once(few_kernel<D, kRows>, sizeof(Sh), attr);
   if (e != cudaSuccess) return e;
-  few_kernel<D><<<ctas, kThreads, sizeof(Shared<D>), stream>>>(k, v, a);
   count_launches(1);
-  e = cudaGetLastError();
+  e = launch_early(few_kernel<D, kRows>, ctas, Sh::kThreads, sizeof(Sh), stream, k, v, a);
   if (e != cudaSuccess || !a.can_split) return e;
-  merge_kernel<D, kRows><<<dim3(ctas, D / 64), 256, 0, stream>>>(a, ctas);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_early(merge_kernel<D, kRows>, dim3(ctas, (kRows * D / 4 + 255) / 256), 256, 0, stream, a, ctas);
 }
-template cudaError_t launch_chunk_q8_few<64>(const q8::Args&, int, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
-template cudaError_t launch_chunk_q8_few<128>(const q8::Args&, int, const CUtensorMap&, const CUtensorMap&, cudaStream_t);
+#define MARS_FEW(D, R) \
+  template cudaError_t launch_chunk_q8_few<D, R>(const q8::Args&, int, const CUtensorMap&, const CUtensorMap&, cudaStream_t)
+MARS_FEW(64, 8);
+MARS_FEW(64, 16);
+MARS_FEW(128, 8);
+MARS_FEW(128, 16);
 
 }  // namespace mars

@@ -97,6 +97,23 @@ cudaError_t set_smem_limit_once(Kernel* fn, int bytes, std::atomic<int> (&done)[
   return e;
 }
 
+// Launch of a kernel that calls wait_for_previous (sm100.cuh) before all else that touches memory.
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem,
+                         cudaStream_t stream, const Args&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, fn, Params(args)...);
+}
+
 // ---- One CTA waiting on an mbarrier that nothing completes (the wait-limit self-check).
 cudaError_t launch_wait_timeout_check(int32_t* status, cudaStream_t stream);
 
@@ -203,7 +220,7 @@ struct ChunkQ8Plan {
   int gp, tpt;             // heads and tokens of a row tile
   int ctas;
   bool can_split;          // items may be divided among CTAs
-  bool few;                // chunk_q8_few.cu's kernel
+  int few;                 // rows of an item of chunk_q8_few.cu's kernel (0: not that)
   int pages;               // the wide form's pages per sequence (0: without it)
   PackedPlan wide;
   size_t ws_bytes;

@@ -117,26 +117,6 @@ MARS_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
   return mbar_test_wait(bar, parity) || mbar_wait_suspending(bar, parity, abort, status);
 }
 
-// The same without suspending, for waits on copies: a thread suspended on a barrier that bytes
-// complete was woken some 2 us late (a ring of four 16 KB stages of 2 KB copies took in 914 GB/s on
-// all SMs with mbar_wait and 4,280 GB/s with this).
-MARS_DEV bool mbar_wait_spinning(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                 int32_t* status) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_test_wait(bar, parity)) return true;
-    if (abort && *abort) return false;
-    if (globaltimer() - t0 > kWaitNs) {
-      if (abort) *abort = 1;
-      if (status) atomicOr(status, MARS_ST_TIMEOUT);
-      return false;
-    }
-  }
-}
-
 // ------------------------------------------------------------------------------ TMA
 
 MARS_DEV void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
@@ -233,6 +213,13 @@ MARS_DEV void regs_lower() {
   static_assert(N % 8 == 0 && N >= 24 && N <= 256, "setmaxnreg count");
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+
+// Programmatic dependent launch: a kernel that launch_early (internal.h) launched starts while the
+// kernel before it in the stream still runs, once all CTAs of that one have ended or passed
+// let_next_start. What the kernel before wrote is there after wait_for_previous, and so is all that
+// came before that one.
+MARS_DEV void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+MARS_DEV void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 MARS_DEV void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
