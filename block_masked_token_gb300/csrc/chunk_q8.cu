@@ -1074,9 +1074,10 @@ Places places(const ChunkQ8Plan& plan, int batch, int hkv, int d) {
     l.rec = l.v + (l.v - l.k);
   }
   const size_t rows = plan.few ? plan.few : BQ;      // of a partial
+  const size_t note = plan.few ? sizeof(uint32_t) : sizeof(Record);
   l.part = l.end = l.rec;
   if (plan.can_split) {
-    l.part = l.rec + packed::align256(plan.ctas * sizeof(Record));
+    l.part = l.rec + packed::align256(plan.ctas * note);
     l.end = l.part + (size_t)plan.ctas * 2 * rows * ((size_t)d + 2) * sizeof(float);
   }
   return l;
@@ -1132,7 +1133,9 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   a.skip_pages = plan.pages ? plan.pages : -1;
   a.scale_log2 = t.scale * 1.4426950408889634f;
   a.o = t.o;
-  a.rec = plan.can_split ? reinterpret_cast<Record*>(ws + l.rec) : nullptr;
+  a.item_work = plan.few ? kFewItemWork : kItemWork;
+  if (plan.can_split && plan.few) a.arrived = reinterpret_cast<uint32_t*>(ws + l.rec);
+  if (plan.can_split && !plan.few) a.rec = reinterpret_cast<Record*>(ws + l.rec);
   a.part = plan.can_split ? reinterpret_cast<float4*>(ws + l.part) : nullptr;
   a.status = t.status;
   // a page and KV head is 16 rows of the maps; an empty pool is never read (one page over q)
@@ -1182,8 +1185,18 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
   p.gp = p.wide.gp;
   p.tpt = p.wide.tpt;
   const int group = hq / hkv;
-  for (int rows : {16, 8})
-    if (group <= rows && total <= (long long)batch * (rows / group)) p.few = rows;
+  // chunk_q8_few.cu where a sequence's rows make one of its tiles (28 query over 4 KV heads of 128, 32
+  // sequences of 2,048 keys and 2 tokens each: 32 us, here 43 us with 4 tokens each); or a few of
+  // them, each of which reads the cache again, if neither are the items more than the SMs nor the
+  // keys many (8 tokens of 1 sequence, 512 keys: 14.9 against 20.2 us here; of 8 sequences, 2,048
+  // keys: 29.1 against 28.8, 8,192: 66 against 41).
+  for (int rows : {16, 8}) {
+    if (group > rows) continue;
+    const long long mine = packed::max_tiles(batch, total, rows / group) * hkv;
+    if (total <= (long long)batch * (rows / group) ||
+        (rows == 16 && total <= 4LL * batch * (rows / group) && mine <= num_sms() && max_len <= 2048))
+      p.few = rows;
+  }
   if (p.few) {
     p.gp = group;
     p.tpt = p.few / group;

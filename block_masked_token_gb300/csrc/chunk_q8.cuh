@@ -28,8 +28,12 @@ namespace q8 {
 
 constexpr int kTile = 128;           // keys of a tile
 constexpr int kPagesPerTile = kTile / kPageSize;
-constexpr int kMinPart = 4;          // key tiles of a part of a divided item
-constexpr long long kUnit = 8, kItemWork = 12;   // work of a key tile and of an item's start and end
+constexpr long long kUnit = 8;       // work of a key tile
+constexpr int kMinPart = 2;          // key tiles of a part of a divided item
+// Work of an item's start and end, in chunk_q8.cu (8 rows x 28 heads, 32 sequences of 512 .. 2,048
+// keys: 43.1 us at 96, 40.1 at 48, 45 at 12 with parts of 4 tiles; 16 rows, 128 sequences: 305, 297,
+// 305) and in chunk_q8_few.cu (single tokens, 2,048 .. 8,192 keys: 45.6 at 12, 42.7 at 32, 41.5 at 64)
+constexpr int kItemWork = 48, kFewItemWork = 64;
 constexpr float kLift = 7.f;         // log2 of what P' is multiplied by
 constexpr float kNoKeys = -1.f;      // l of a part without keys, which has no O
 
@@ -74,11 +78,13 @@ struct Args {
   const uint8_t *k_pool, *v_pool, *k_scale, *v_scale;
   int num_pages, max_pages, batch, total, hq, hkv, gp, tpt, heads;   // heads: KV heads x groups
   bool can_split;
+  int item_work;                     // work of an item's start and end
   int skip_pages;                    // sequences of more than tpt rows and at most so many pages
                                      // are left to the wide form (-1: none)
   float scale_log2;
   uint16_t* o;
-  struct Record* rec;                // [CTA]
+  struct Record* rec;                // [CTA], for merge_kernel
+  uint32_t* arrived;                 // [CTA], parts of the item that it begins (chunk_q8_few.cu)
   float4* part;                      // [CTA][2], see kPartial
   int32_t* status;
 };
@@ -96,7 +102,7 @@ struct Row {
   // own and cached tiles of every item of the sequence (an item's own tiles behind its last
   // token, which it skips, counted too)
   MARS_DEV int tiles() const { return own() + packed::key_tiles(P); }
-  MARS_DEV long long unit() const { return kUnit * tiles() + kItemWork; }
+  MARS_DEV long long unit(const Args& a) const { return kUnit * tiles() + a.item_work; }
 };
 
 MARS_DEV bool left_out(int skip_pages, int tpt, int n, int P) {
@@ -127,8 +133,10 @@ MARS_DEV void find_part(const Args& a, Scan<kThreads>& sc) {
   const int lo = (int)min((long long)tid * per, (long long)a.batch), hi = min(lo + per, a.batch);
   auto clamped = [&](int s) { return min(max(a.cu[s], 0), a.total); };
   int bad = 0, m = 0;
-  if (lo < hi) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seq_lens + lo));
-  for (int s = lo; s < hi; ++s) m = max(m, clamped(s + 1));
+  // the first sequence's, read at once: each trip to memory before the first copy is time lost
+  const int first_end = lo < hi ? a.cu[lo + 1] : 0, first_len = lo < hi ? a.seq_lens[lo] : 0;
+  const int zeroth = a.cu[0];
+  for (int s = lo; s < hi; ++s) m = max(m, s == lo ? min(max(first_end, 0), a.total) : clamped(s + 1));
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, m, o);
@@ -136,8 +144,8 @@ MARS_DEV void find_part(const Args& a, Scan<kThreads>& sc) {
   }
   if (lane == 31) sc.top[warp] = m;
   __syncthreads();
-  int lead = clamped(0);                             // the boundary before this thread's sequences
-  if (tid == 0 && lead != a.cu[0]) bad = MARS_ST_BADSEQ;
+  int lead = min(max(zeroth, 0), a.total);           // the boundary before this thread's sequences
+  if (tid == 0 && lead != zeroth) bad = MARS_ST_BADSEQ;
   for (int w = 0; w < warp; ++w) lead = max(lead, sc.top[w]);
   m = __shfl_up_sync(0xffffffffu, m, 1);
   if (lane > 0) lead = max(lead, m);
@@ -151,14 +159,15 @@ MARS_DEV void find_part(const Args& a, Scan<kThreads>& sc) {
     q.pre = pre;
 #pragma unroll 1
     for (int s = lo; s < hi; ++s) {
-      const int end = max(clamped(s + 1), q.base), len = a.seq_lens[s];
+      const int given = s == lo ? first_end : a.cu[s + 1], len = s == lo ? first_len : a.seq_lens[s];
+      const int end = max(min(max(given, 0), a.total), q.base);
       q.s = s;
       q.n = end - q.base;
       q.P = cached(a, len);
-      if (end != a.cu[s + 1]) bad |= MARS_ST_BADSEQ;
+      if (end != given) bad |= MARS_ST_BADSEQ;
       if (q.P != len && q.n > 0) bad |= MARS_ST_OVERFLOW;
       const int items = items_of(a, q);
-      const long long work = items * q.unit();
+      const long long work = items * q.unit(a);
       if (p0 >= q.pre && p0 < q.pre + work) sc.at[0] = q;
       if (p1 >= q.pre && p1 < q.pre + work) sc.at[1] = q;
       count += items;
@@ -189,7 +198,7 @@ MARS_DEV void find_part(const Args& a, Scan<kThreads>& sc) {
     }
     // as many CTAs as there are, unless that leaves less than a part each and there are fewer items
     const long long ctas =
-        min((long long)gridDim.x, max(items, total / (kUnit * kMinPart + kItemWork)));
+        min((long long)gridDim.x, max(items, total / (kUnit * kMinPart + a.item_work)));
     if (tid == 0) {
       sc.total = total;
       sc.ctas = ctas;
@@ -213,9 +222,9 @@ MARS_DEV void find_part(const Args& a, Scan<kThreads>& sc) {
 // kMinPart tiles of an item's ends.
 MARS_DEV void cut_at(const Args& a, const Row& q, long long pos, int& i, int& j) {
   const long long rem = pos - q.pre;
-  i = (int)(rem / q.unit());
+  i = (int)(rem / q.unit(a));
   const int tiles = q.tiles();
-  j = (int)min(max((rem - i * q.unit() - kItemWork / 2) / kUnit, 0LL), (long long)tiles);
+  j = (int)min(max((rem - i * q.unit(a) - a.item_work / 2) / kUnit, 0LL), (long long)tiles);
   const int least = a.can_split ? kMinPart : tiles / 2;
   if (j < least || !a.can_split) {
     const bool up = j >= least && j > 0;
@@ -265,6 +274,47 @@ struct Window {
 // +infinity.
 MARS_DEV float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
+// Joins the parts of a divided item, the k-th of which is at part(k): four columns of a row at a time.
+template <int D, int kRows, class Part>
+MARS_DEV void join(const Args& a, Part part, int parts, int rows, size_t tok, int h0, int from, int step) {
+  for (int i = from; i < rows * (D / 4); i += step) {
+    const int row = i % rows, c = i / rows;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // four at a time: a trip to the L2 cache each
+#pragma unroll 1
+    for (int k0 = 0; k0 < parts; k0 += 4) {
+      float2 ml[4];
+      float4 v[4];
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ml[k] = make_float2(-INFINITY, kNoKeys);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k >= parts) continue;
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(part(k0 + k) + kRows * D / 4) + row);
+        v[k] = __ldcg(part(k0 + k) + c * kRows + row);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+      const float w0 = m > -INFINITY ? exp2f(m - top) : 0.f;        // (+infinity gives NaN)
+      m = top;
+      l *= w0;
+      o = make_float4(o.x * w0, o.y * w0, o.z * w0, o.w * w0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (ml[k].y == kNoKeys) continue;
+        const float w = ml[k].x > -INFINITY ? exp2f(ml[k].x - top) : 0.f;
+        l = fmaf(ml[k].y, w, l);
+        o = make_float4(fmaf(v[k].x, w, o.x), fmaf(v[k].y, w, o.y), fmaf(v[k].z, w, o.z), fmaf(v[k].w, w, o.w));
+      }
+    }
+    const float inv = reciprocal(l);
+    *reinterpret_cast<uint2*>(a.o + ((tok + row / a.gp) * a.hq + h0 + row % a.gp) * D + 4 * c) =
+        make_uint2(flash::pack_bf16x2(o.x * inv, o.y * inv), flash::pack_bf16x2(o.z * inv, o.w * inv));
+  }
+}
+
 // Joins the parts of divided items. Block (x, y): the item that CTA x begins and does not end, a
 // thread per (row, four columns).
 template <int D, int kRows>
@@ -274,7 +324,6 @@ __global__ void __launch_bounds__(256) merge_kernel(Args a, int ctas) {
   const int x = blockIdx.x, lane = threadIdx.x & 31;
   const Record rec = a.rec[x];
   if (!rec.begins) return;
-  const int rows = rec.tokens * a.gp;
   // its parts: CTA x's, those that lie inside it, and the one that ends it
   int parts = 2;
   for (int c = x + 1;; c += 32) {
@@ -285,29 +334,8 @@ __global__ void __launch_bounds__(256) merge_kernel(Args a, int ctas) {
   }
   const float4* first = a.part + ((size_t)x * 2 + 1) * PART;
   auto part = [&](int k) { return k == 0 ? first : a.part + (size_t)(x + k) * 2 * PART; };
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += gridDim.y * 256) {
-    const int row = i % rows, c = i / rows;
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k)
-      m = fmaxf(m, reinterpret_cast<const float2*>(part(k) + kRows * D / 4)[row].x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float2 ml = reinterpret_cast<const float2*>(part(k) + kRows * D / 4)[row];
-      if (ml.y == kNoKeys) continue;
-      const float4 v = part(k)[c * kRows + row];
-      const float w = ml.x > -INFINITY ? exp2f(ml.x - m) : 0.f;     // m = +infinity gives NaN
-      l = fmaf(ml.y, w, l);
-      o = make_float4(fmaf(v.x, w, o.x), fmaf(v.y, w, o.y), fmaf(v.z, w, o.z), fmaf(v.w, w, o.w));
-    }
-    const float inv = reciprocal(l);
-    const size_t tok = (size_t)rec.base + rec.tok0 + row / a.gp;
-    uint32_t* to = reinterpret_cast<uint32_t*>(a.o + (tok * a.hq + rec.h0 + row % a.gp) * D + 4 * c);
-    to[0] = flash::pack_bf16x2(o.x * inv, o.y * inv);
-    to[1] = flash::pack_bf16x2(o.z * inv, o.w * inv);
-  }
+  join<D, kRows>(a, part, parts, rec.tokens * a.gp, (size_t)rec.base + rec.tok0, rec.h0,
+                 blockIdx.y * 256 + threadIdx.x, gridDim.y * 256);
 }
 
 }  // namespace q8

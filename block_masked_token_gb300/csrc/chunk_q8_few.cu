@@ -33,6 +33,7 @@ constexpr int kList = 32;            // parts found at a time
 struct Part {
   int s, base, tok0, tokens, h0, kvh, slot;
   int own0, own1, page0, page1, keys;               // keys: cached ones of the sequence
+  long long cuts0, cuts1;                           // of a divided item: where its cuts lie
   // units of work: cached pages, then 16 own keys each
   MARS_DEV int pages() const { return page1 - page0; }
   MARS_DEV int units() const { return pages() + (own1 - own0 + kPageSize - 1) / kPageSize; }
@@ -42,14 +43,15 @@ struct Part {
 struct Place {
   Row q;                             // at item i, tile j of it; before the end, items and tiles too
   int i, j, es, ei, ej;
+  long long end_pre;                 // work before sequence es
   bool more;
-  Record rec;
 };
 template <int kThreads>
 MARS_DEV Place first_place(const Args& a, const Scan<kThreads>& sc) {
-  Place w{sc.at[0], 0, 0, a.batch, 0, 0, true, {}};
+  Place w{sc.at[0], 0, 0, a.batch, 0, 0, 0, true};
   if (sc.p1 < sc.total) {
     w.es = sc.at[1].s;
+    w.end_pre = sc.at[1].pre;
     cut_at(a, sc.at[1], sc.p1, w.ei, w.ej);
   }
   cut_at(a, w.q, sc.p0, w.i, w.j);
@@ -76,8 +78,11 @@ MARS_DEV bool next_part(const Args& a, Place& w, Window& window, Part& p) {
   p.h0 = hg * a.gp;
   p.kvh = hg / (a.heads / a.hkv);
   p.slot = w.j > 0 ? 0 : jb < tiles ? 1 : -1;
-  if (p.slot == 1) w.rec = Record{1, w.rec.inside, p.base, p.tok0, p.tokens, p.h0, {0, 0}};
-  if (p.slot == 0 && jb < tiles) w.rec.inside = 1;
+  if (p.slot >= 0) {
+    // a cut divides the item if it lies in [cuts0, cuts1) (cut_at)
+    p.cuts0 = (w.j > 0 ? q.pre : w.end_pre) + w.i * q.unit(a) + a.item_work / 2 + kUnit * kMinPart;
+    p.cuts1 = p.cuts0 + kUnit * (tiles - 2 * kMinPart + 1);
+  }
   // own tiles [j, own), cached tiles from behind them
   const int own = q.own();
   p.own0 = min(min(w.j, own) * kTile, last_tok + 1);
@@ -90,15 +95,9 @@ MARS_DEV bool next_part(const Args& a, Place& w, Window& window, Part& p) {
   return true;
 }
 
-#ifndef FW8
-#define FW8 16
-#define FS8 2
-#define FW16 8
-#define FS16 4
-#endif
 template <int D, int kRows>
 struct Shared {
-  static constexpr int kWarps = kRows == 8 ? FW8 : FW16, kThreads = 32 * kWarps, kStages = kRows == 8 ? FS8 : FS16;
+  static constexpr int kWarps = kRows == 8 ? 12 : 8, kThreads = 32 * kWarps, kStages = kRows == 8 ? 2 : 4;
   static constexpr int kPage = kPageSize * D;
   static constexpr int kVec = kRows * D / 128;       // float4 of O per lane
   uint8_t ring[kWarps][kStages][2][kPage];           // codes of K and V
@@ -108,7 +107,8 @@ struct Shared {
   Part parts[kList];
   Place place;
   Scan<kThreads> scan;
-  int found;
+  int first, pieces;                                // CTAs of the divided item in work
+  int found, joins;
 };
 
 // 8 x 8 halves, two of a row to a lane, transposed.
@@ -139,6 +139,20 @@ MARS_DEV int row_exponent(uint32_t top, int least) {
 MARS_DEV uint32_t to_f16(uint32_t word, float f) {
   return pack_f16x2(__uint_as_float(word << 16) * f, __uint_as_float(word & 0xffff0000u) * f);
 }
+// A read that stays where it stands among the copies, and a read to come.
+MARS_DEV uint4 load_once(const uint16_t* p) {
+  uint4 x;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
+MARS_DEV void prefetch(const uint16_t* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// One more has arrived: what the CTA wrote before is there for whoever arrives later. Returns how many
+// were there.
+MARS_DEV uint32_t arrive(uint32_t* count) {
+  uint32_t n;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(n) : "l"(count) : "memory");
+  return n;
+}
 constexpr int kLeastRow = -126;      // Q and K: 2^126 is the largest factor
 constexpr int kLeastV = -60;         // V: the sums of P' 2^-e stay far from the ends of the range
 
@@ -163,10 +177,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
   wait_for_previous();
   let_next_start();
   find_part(a, sh.scan);
-  if ((long long)blockIdx.x >= sh.scan.ctas) {
-    if (threadIdx.x == 0 && a.rec) a.rec[blockIdx.x] = Record{};
-    return;
-  }
+  if ((long long)blockIdx.x >= sh.scan.ctas) return;
   if (threadIdx.x == 0) sh.place = first_place(a, sh.scan);
   uint64_t* full = sh.full[warp];
   bool ok = true;
@@ -208,6 +219,15 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         seq = p.s;
         kvh = p.kvh;
         keys = p.keys;
+        // its rows, for when it begins: behind the copies in flight they would take 2 us
+        const int row = lane >> 1, half = (lane & 1) * (D / 2);
+        if (cp > 0 && row < p.tokens * a.gp)
+          prefetch(a.q + ((size_t)p.base + p.tok0 + row / a.gp) * a.q_stride + (p.h0 + row % a.gp) * D + half);
+        if (cp > 0 && p.own0 + row < p.own1) {
+          const size_t key = (size_t)p.base + p.own0 + row;
+          prefetch(a.k + key * a.k_stride + kvh * D + half);
+          prefetch(a.v + key * a.v_stride + kvh * D + half);
+        }
       }
       if (from == INT_MIN || cu >= from + 32 * kWarps) {
         from = cu;
@@ -239,47 +259,51 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
       ++issued;
       cu += kWarps;
     };
-#pragma unroll 1
-    for (int k = 0; k < kStages; ++k) issue();
 
 #pragma unroll 1
     for (int part = 0; part < found; ++part) {
       const Part& p = sh.parts[part];
       const int pages = p.pages(), units = p.units();
       // ---- Q: row 8n + g, d = t D/4 .. ; factors and tokens of rows 8n + 2t, 8n + 2t + 1
-      uint32_t qb[kCols][kSteps][2];
+      uint2 qb[kCols][kSteps];
       float factor[kCols][2];
-      int tok[kCols][2];
+      int tok[kCols][2], ex[kCols];
+      uint4 x[kCols][kQuads];
 #pragma unroll
       for (int n = 0; n < kCols; ++n) {
         const int row = 8 * n + g;
-        const bool has = row < p.tokens * a.gp;
-        uint4 x[kQuads];
         const uint16_t* from_q = a.q + ((size_t)p.base + p.tok0 + row / a.gp) * a.q_stride +
                                  (p.h0 + row % a.gp) * D + t * (D / 4);
+#pragma unroll
+        for (int e = 0; e < kQuads; ++e)
+          x[n][e] = row < p.tokens * a.gp ? load_once(from_q + 8 * e) : make_uint4(0, 0, 0, 0);
+      }
+      if (part == 0) {                               // the first copies, behind these reads
+#pragma unroll 1
+        for (int k = 0; k < kStages; ++k) issue();
+      }
+#pragma unroll
+      for (int n = 0; n < kCols; ++n) {
         uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < kQuads; ++e) {
-          x[e] = has ? reinterpret_cast<const uint4*>(from_q)[e] : make_uint4(0, 0, 0, 0);
-          top = word_max(x[e], top);
-        }
+        for (int e = 0; e < kQuads; ++e) top = word_max(x[n][e], top);
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = row_exponent(top, kLeastRow);
-        const float f = power(kBias - ex);
+        ex[n] = row_exponent(top, kLeastRow);
+        const float f = power(kBias - ex[n]);
 #pragma unroll
         for (int e = 0; e < kQuads; ++e) {
-          qb[n][2 * e][0] = to_f16(x[e].x, f);
-          qb[n][2 * e][1] = to_f16(x[e].y, f);
-          qb[n][2 * e + 1][0] = to_f16(x[e].z, f);
-          qb[n][2 * e + 1][1] = to_f16(x[e].w, f);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          factor[n][r] = a.scale_log2 * power(kBias + __shfl_sync(0xffffffffu, ex, 8 * t + 4 * r));
-          tok[n][r] = p.tok0 + (8 * n + 2 * t + r) / a.gp;
+          qb[n][2 * e] = make_uint2(to_f16(x[n][e].x, f), to_f16(x[n][e].y, f));
+          qb[n][2 * e + 1] = make_uint2(to_f16(x[n][e].z, f), to_f16(x[n][e].w, f));
         }
       }
+#pragma unroll
+      for (int n = 0; n < kCols; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          factor[n][r] = a.scale_log2 * power(kBias + __shfl_sync(0xffffffffu, ex[n], 8 * t + 4 * r));
+          tok[n][r] = p.tok0 + (8 * n + 2 * t + r) / a.gp;
+        }
       float o[kCols][kSteps][4], m[kCols][2], l[kCols][2];
 #pragma unroll
       for (int n = 0; n < kCols; ++n) {
@@ -377,8 +401,10 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
                 decode4(w0[e], a0, a2);
                 decode4(w1[e], a1, a3);
 #pragma unroll
-                for (int n = 0; n < kCols; ++n)
-                  mma(y[n], a0, a1, a2, a3, qb[n][4 * c + e][0], qb[n][4 * c + e][1]);
+                for (int n = 0; n < kCols; ++n) {
+                  const uint2 b = qb[n][4 * c + e];
+                  mma(y[n], a0, a1, a2, a3, b.x, b.y);
+                }
               }
             }
             __syncwarp();
@@ -448,8 +474,9 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
           for (int c = 0; c < kQuads; ++c)
 #pragma unroll
             for (int n = 0; n < kCols; ++n) {
-              mma(y[n], kx[0][c].x, kx[1][c].x, kx[0][c].y, kx[1][c].y, qb[n][2 * c][0], qb[n][2 * c][1]);
-              mma(y[n], kx[0][c].z, kx[1][c].z, kx[0][c].w, kx[1][c].w, qb[n][2 * c + 1][0], qb[n][2 * c + 1][1]);
+              const uint2 b0 = qb[n][2 * c], b1 = qb[n][2 * c + 1];
+              mma(y[n], kx[0][c].x, kx[1][c].x, kx[0][c].y, kx[1][c].y, b0.x, b0.y);
+              mma(y[n], kx[0][c].z, kx[1][c].z, kx[0][c].w, kx[1][c].w, b1.x, b1.y);
             }
           uint32_t x[4][D / 16];
 #pragma unroll
@@ -499,6 +526,12 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
       }
       // ---- the warps' maxima, sums and O together
       __syncthreads();                               // the part before is out
+      if (p.slot >= 0 && threadIdx.x == 0) {
+        // cut x of n lies at floor(x total / n)
+        const long long n = sh.scan.ctas, total = sh.scan.total;
+        sh.first = (int)((p.cuts0 * n + total - 1) / total) - 1;
+        sh.pieces = (int)((p.cuts1 * n + total - 1) / total) - sh.first;
+      }
 #pragma unroll
       for (int n = 0; n < kCols; ++n)
 #pragma unroll
@@ -542,6 +575,18 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
               make_uint2(flash::pack_bf16x2(r.x * inv, r.y * inv), flash::pack_bf16x2(r.z * inv, r.w * inv));
         }
       }
+      if (p.slot >= 0) {                             // whoever comes last joins the item's parts
+        __syncthreads();
+        if (threadIdx.x == 0) sh.joins = arrive(&a.arrived[sh.first]) == (uint32_t)sh.pieces - 1;
+        __syncthreads();
+        if (sh.joins) {
+          constexpr int PART = kPartial<D, kRows>;
+          const float4* first = a.part + (size_t)sh.first * 2 * PART;
+          auto at = [&](int k) { return first + (k == 0 ? PART : (size_t)k * 2 * PART); };
+          join<D, kRows>(a, at, sh.pieces, p.tokens * a.gp, (size_t)p.base + p.tok0, p.h0, threadIdx.x,
+                         Sh::kThreads);
+        }
+      }
     }
     __syncthreads();                                 // the list is free again
   }
@@ -551,7 +596,13 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
   }
   flags = __reduce_or_sync(0xffffffffu, (unsigned)flags);
   if (lane == 0 && flags && a.status) atomicOr(a.status, flags);
-  if (threadIdx.x == 0 && a.rec) a.rec[blockIdx.x] = sh.place.rec;
+}
+
+// No part of an item has arrived yet.
+__global__ void clear_kernel(uint32_t* arrived, int n) {
+  sm100::let_next_start();
+  sm100::wait_for_previous();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) arrived[i] = 0;
 }
 
 }  // namespace
@@ -564,11 +615,13 @@ cudaError_t launch_chunk_q8_few(const q8::Args& a, int ctas, const CUtensorMap& 
   static std::atomic<int> attr[64];
   cudaError_t e = set_smem_limit_once(few_kernel<D, kRows>, sizeof(Sh), attr);
   if (e != cudaSuccess) return e;
+  if (a.can_split) {
+    count_launches(1);
+    e = launch_early(clear_kernel, 1, 256, 0, stream, a.arrived, ctas);
+    if (e != cudaSuccess) return e;
+  }
   count_launches(1);
-  e = launch_early(few_kernel<D, kRows>, ctas, Sh::kThreads, sizeof(Sh), stream, k, v, a);
-  if (e != cudaSuccess || !a.can_split) return e;
-  count_launches(1);
-  return launch_early(merge_kernel<D, kRows>, dim3(ctas, (kRows * D / 4 + 255) / 256), 256, 0, stream, a, ctas);
+  return launch_early(few_kernel<D, kRows>, ctas, Sh::kThreads, sizeof(Sh), stream, k, v, a);
 }
 #define MARS_FEW(D, R) \
   template cudaError_t launch_chunk_q8_few<D, R>(const q8::Args&, int, const CUtensorMap&, const CUtensorMap&, cudaStream_t)
