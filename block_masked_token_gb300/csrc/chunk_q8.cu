@@ -1018,6 +1018,7 @@ constexpr int kUnpackThreads = 256;
 // rows is written over.
 template <int D>
 __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(UnpackArgs a) {
+  sm100::wait_for_previous();
   auto cut = [&](int len) { return (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize)); };
   bool bad;
   const packed::Seq sq = packed::find_tile_by(
@@ -1092,9 +1093,9 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
                  reinterpret_cast<uint16_t*>(ws + l.k), reinterpret_cast<uint16_t*>(ws + l.v),
                  reinterpret_cast<int32_t*>(ws + l.lens), reinterpret_cast<int32_t*>(ws + l.table),
                  t.status, t.num_pages, t.max_pages, plan.pages, plan.tpt, t.batch, t.total, t.hkv};
-    unpack_kernel<D><<<(unsigned)((long long)t.batch * plan.pages), kUnpackThreads, 0, stream>>>(u);
     count_launches(1);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_early(unpack_kernel<D>, (unsigned)((long long)t.batch * plan.pages), kUnpackThreads, 0,
+                                 stream, u);
     if (e != cudaSuccess) return e;
     PackedAttn wide = t;
     wide.k_pool = u.k_out;

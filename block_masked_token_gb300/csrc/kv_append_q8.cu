@@ -13,6 +13,7 @@
 #include "cache_q8.cuh"
 #include "internal.h"
 #include "packed.cuh"
+#include "sm100.cuh"
 
 namespace mars {
 
@@ -100,6 +101,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(AppendQ8 a) {
   __shared__ int s_bad;                  // first logical page that is not mapped
   bool bad;
+  sm100::wait_for_previous();
+  sm100::let_next_start();
   const packed::Seq sq = packed::find_tile_by(
       a.cu, a.batch, a.total, (long long)blockIdx.x, bad, a.seq_lens,
       [&](int s, int n, int len) { return pages_of(rows_of(a, s, n, len), len); });
@@ -161,12 +164,8 @@ long long append_q8_ctas(int batch, int total) { return (long long)total / kPage
 
 cudaError_t launch_kv_append_q8(const AppendQ8& a, int d, cudaStream_t stream) {
   const unsigned ctas = (unsigned)append_q8_ctas(a.batch, a.total);
-  if (d == 64)
-    kv_append_q8_kernel<64><<<ctas, kThreads, 0, stream>>>(a);
-  else
-    kv_append_q8_kernel<128><<<ctas, kThreads, 0, stream>>>(a);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_early(d == 64 ? kv_append_q8_kernel<64> : kv_append_q8_kernel<128>, ctas, kThreads, 0, stream, a);
 }
 
 }  // namespace mars

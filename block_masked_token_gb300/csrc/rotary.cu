@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "packed.cuh"
+#include "sm100.cuh"
 
 namespace mars {
 
@@ -34,6 +35,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary a) {
   // of unit u at v * units + u: the lanes of a head then read consecutive vectors
   __shared__ float4 turns[kRows][kMaxPairs / 2];
   bool bad;
+  sm100::wait_for_previous();
+  sm100::let_next_start();
   const packed::Seq sq = packed::find_tile(a.cu, a.batch, a.total, kRows, 0, (long long)blockIdx.x,
                                            bad, a.seq_lens);
   if (bad && threadIdx.x == 0 && a.status) atomicOr(a.status, MARS_ST_BADSEQ);
@@ -135,12 +138,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary a) {
 
 cudaError_t launch_rotary(const Rotary& a, bool interleaved, cudaStream_t stream) {
   const unsigned ctas = (unsigned)packed::max_tiles(a.batch, a.total, kRows);
-  if (interleaved)
-    rotary_kernel<true><<<ctas, kThreads, 0, stream>>>(a);
-  else
-    rotary_kernel<false><<<ctas, kThreads, 0, stream>>>(a);
   count_launches(1);
-  return cudaGetLastError();
+  return launch_early(interleaved ? rotary_kernel<true> : rotary_kernel<false>, ctas, kThreads, 0, stream, a);
 }
 
 }  // namespace mars
