@@ -52,10 +52,12 @@ constexpr int kControlRegs = 72, kSoftmaxRegs = 136, kConvertRegs = 64;
 static_assert(128 * (kControlRegs + 2 * kSoftmaxRegs + 2 * kConvertRegs) <=
                   kThreads * (65536 / kThreads / 8 * 8),
               "the register split fits the launch's register pool");
-constexpr int kRaw = 4;              // ring of raw tiles of V
+constexpr int kGroupWarps = kConvertWarps / 2, kPages = kPagesPerTile / kGroupWarps;   // of even or odd
+                                     // tiles; pages of a warp
+constexpr int kRaw = 2;              // ring of a converter warp's raw pages, kPages at a time
 constexpr int kSlots = 4;            // ring of tiles of K's codes; an own tile takes two slots, and so
                                      // does an item's Q in bf16, before its first tile
-constexpr int kAhead = 3;            // tiles that copies may be ahead of the conversion
+constexpr int kAhead = 2;            // tiles that copies may be ahead of the conversion
 constexpr int kTiles = 2;            // f16 tiles of V
 constexpr int kBufs = 2;             // S buffers, and O's, in TMEM: of even and odd tiles
 // Tiles that the walk may be ahead. It publishes up to four at once, the converters wait for up to
@@ -75,8 +77,8 @@ struct alignas(16) Info {
   int base, n, tok0, h0, kvh;        // its item
   int slot;                          // of the partial, -1: the item is whole
   int k0, count;                     // first key (own: token of the sequence), keys that there are
-  int q_slot;                        // first tile of a part: where its Q lies in K's ring
-  int pad[2];
+  int q_slot, k_slot;                // where a part's first tile has its Q in K's ring, an own one its K
+  int pad;
   alignas(16) int page[kPagesPerTile];         // -1: not to be read
   alignas(8) uint8_t k_byte[kPagesPerTile];    // scale bytes; own tiles: written by the converters
   alignas(8) uint8_t v_byte[kPagesPerTile];    // 0: no such keys
@@ -84,10 +86,10 @@ struct alignas(16) Info {
 
 struct Bar {
   uint64_t info_full[kInfos], info_empty[kInfos];
-  uint64_t raw_full[kConvertWarps][kRaw];              // of a warp's page
+  uint64_t raw_full[kConvertWarps][kRaw];              // of a warp's pages
   // own_raw: an own tile's K in bf16 is in its two slots, own_full: its scales and its two parts are.
   // (Barriers of their own: a wait for a phase of a ring whose last one is still open would pass at
-  // once. Two of each: the slots let two own tiles be under way.)
+  // once. One of each for even and for odd tiles: the slots let two own tiles be under way.)
   uint64_t k_full[kSlots], k_empty[kSlots], own_raw[2], own_full[2], own_v[2];
   uint64_t v_full[kTiles], v_empty[kTiles];
   uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
@@ -116,7 +118,7 @@ struct Layout {
   // both parts of Q; K's codes; f16 tiles of V; raw ones
   static constexpr int OFF_Q = 0, OFF_K = 2 * RAW, OFF_V = OFF_K + kSlots * RAW;
   static constexpr int OFF_RAW = OFF_V + kTiles * TILE;
-  static constexpr int TOTAL = OFF_RAW + kRaw * RAW;
+  static constexpr int TOTAL = OFF_RAW + 2 * kRaw * RAW;
   static constexpr int TM_S = 0, TM_O = kBufs * BKV, P_OFF = BKV / 2;    // O: D columns each
   static constexpr int PART = kPartial<D, BQ>;
   // 8-bit operands: rows of D bytes, 16-byte chunk c of row r, swizzled over D bytes
@@ -244,6 +246,7 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
       e.k0 = k0;
       e.count = count;
       e.q_slot = slots % kSlots;
+      e.k_slot = (slots + (f & kFirst ? 2 : 0)) % kSlots;
     };
     for (int x = j; x < own && ok; ++x) {
       if (!(ok = room(1))) break;
@@ -294,9 +297,9 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
     }
     if (!ok) break;
   }
-  if (ok && room(1)) {
-    if (lane == 0) p.info(t).flags = kEnd;
-    publish(1);
+  if (ok && room(2)) {                               // for the converters of even and of odd tiles
+    if (lane < 2) p.info(t + lane).flags = kEnd;
+    publish(2);
   }
   if (lane == 0 && a.rec) a.rec[blockIdx.x] = rec;
   if (flags && a.status) atomicOr(a.status, flags);
@@ -316,7 +319,7 @@ MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& m
   using L = Layout<D>;
   const Args& a = p.a;
   const int lane = threadIdx.x & 31;
-  int c = 0, own = 0, qs = 0;                        // slots taken, own tiles, items
+  int c = 0, own[2] = {0, 0}, qs = 0;                // slots taken, even and odd own tiles, items
   bool ok = true;
   for (int t = 0; ok && p.warp_wait_info(t); ++t) {
     const Info& f = p.info(t);
@@ -340,13 +343,17 @@ MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& m
       if (lane == 0) mbar_arrive_expect_tx(&p.bar.k_full[st], halves ? 0 : pages * L::PAGE);
       __syncwarp();
       if (halves) {
-        uint64_t* raw = i < 0 ? &p.bar.q_raw : &p.bar.own_raw[own & 1];
+        uint64_t* raw = i < 0 ? &p.bar.q_raw : &p.bar.own_raw[t & 1];
         if (lane == 0) {
           if (!half) mbar_arrive_expect_tx(raw, (i < 0 ? a.gp * a.tpt : BKV) * D * 2);
           tma_load_3d(dst, i < 0 ? &map_q : &map_own, raw, half * (D / 2), i < 0 ? f.h0 : f.kvh,
                       f.base + (i < 0 ? f.tok0 : f.k0));
         }
-        if (half) (i < 0 ? qs : own) += 1;
+        if (half) {
+          qs += i < 0;
+          own[0] += i >= 0 && !(t & 1);
+          own[1] += i >= 0 && (t & 1);
+        }
       } else if (page >= 0) {
         tma_load_2d(dst + lane * L::PAGE, &map, &p.bar.k_full[st], 0, row);
       }
@@ -360,8 +367,9 @@ MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& m
       p.drain(&p.bar.k_full[i % kSlots], (i / kSlots) & 1);
   if (lane == 0) {
     if (qs > 0) p.drain(&p.bar.q_raw, (qs - 1) & 1);
-#pragma unroll 1
-    for (int i = max(0, own - 2); i < own; ++i) p.drain(&p.bar.own_raw[i & 1], (i >> 1) & 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (own[i] > 0) p.drain(&p.bar.own_raw[i], (own[i] - 1) & 1);
   }
   __syncwarp();
 }
@@ -501,73 +509,77 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
   using L = Layout<D>;
   const Args& a = p.a;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp;
-  static_assert(kConvertWarps == kPagesPerTile, "a page a warp");
+  // of every other tile: pages page0 ..
+  const int odd = warp / kGroupWarps, page0 = warp % kGroupWarps * kPages;
   uint64_t* const full = p.bar.raw_full[warp];
-  uint8_t* const ring = p.smem + L::OFF_RAW + warp * kRaw * L::PAGE;
-  // the next copy: its number and tile; `converted`: copies that have left the ring
-  int copies = 0, next = 0, converted = 0, slots = 0, own = 0, own_copies = 0;
+  uint8_t* const ring = p.smem + L::OFF_RAW + warp * kRaw * kPages * L::PAGE;
+  // the next copies: their number and tile; `converted`: those that have left the ring
+  int copies = 0, next = odd, converted = 0, own = 0;
   bool more = true, ok = true;
   auto copy_ahead = [&](int t) {
     while (more && next <= t + kAhead && copies < converted + kRaw) {
       if (!(ok = p.warp_wait_info(next))) break;
       const Info& f = p.info(next);
       const int flags = f.flags;
-      ++next;
+      next += 2;
       if (flags & kEnd) more = false;
       if (flags & (kEnd | kOwn)) continue;
-      if (lane == 0) {
-        const int page = f.page[warp], st = copies % kRaw;
-        mbar_arrive_expect_tx(&full[st], page >= 0 ? L::PAGE : 0);
-        if (page >= 0) tma_load_2d(ring + st * L::PAGE, &map, &full[st], 0, (page * a.hkv + f.kvh) * kPageSize);
-      }
+      const int st = copies % kRaw, page = lane < kPages ? f.page[page0 + lane] : -1;
+      const int pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], pages * L::PAGE);
+      __syncwarp();
+      if (page >= 0)
+        tma_load_2d(ring + (st * kPages + lane) * L::PAGE, &map, &full[st], 0, (page * a.hkv + f.kvh) * kPageSize);
       ++copies;
     }
   };
-  for (int t = 0;; ++t) {
+  for (int t = odd;; t += 2) {
     copy_ahead(t);                                   // has waited for tile t, if not earlier
     if (!ok) break;
     Info& f = p.info(t);
-    const int flags = f.flags, ts = t % kTiles;
+    const int flags = f.flags;
+    static_assert(kTiles == 2, "of even and odd tiles");
     if (flags & kEnd) break;
-    if (flags & kFirst) slots += 2;                  // Q's
-    uint8_t* tile = p.smem + L::OFF_V + ts * L::TILE;
+    uint8_t* tile = p.smem + L::OFF_V + odd * L::TILE;
+    if (!(ok = p.warp_wait(&p.bar.v_empty[odd], ((t / kTiles) & 1) ^ 1))) break;
     if (flags & kOwn) {
       // warp 1 has brought K. V's copy goes to its place in the tile; S also waits for V's scales,
       // which its softmax needs
-      if (!(ok = p.warp_wait(&p.bar.v_empty[ts], ((t / kTiles) & 1) ^ 1))) break;
-      if (warp == 0 && lane == 0) {
-        ++own_copies;
-        mbar_arrive_expect_tx(&p.bar.own_v[own & 1], BKV * D * 2);
+      const uint32_t parity = own++ & 1;
+      if (page0 == 0 && lane == 0) {
+        mbar_arrive_expect_tx(&p.bar.own_v[odd], BKV * D * 2);
 #pragma unroll
         for (int x = 0; x < D / 64; ++x)
-          tma_load_3d(tile + x * (BKV * 128), &map_own, &p.bar.own_v[own & 1], x * 64, f.kvh, f.base + f.k0);
+          tma_load_3d(tile + x * (BKV * 128), &map_own, &p.bar.own_v[odd], x * 64, f.kvh, f.base + f.k0);
       }
-      if (!(ok = p.warp_wait(&p.bar.own_raw[own & 1], (own >> 1) & 1))) break;
-      const int k_byte = own_k<D>(p.smem + L::OFF_K + slots % kSlots * L::RAW,
-                                  p.smem + L::OFF_K + (slots + 1) % kSlots * L::RAW, warp * kPageSize, f.count);
-      if (!(ok = p.warp_wait(&p.bar.own_v[own & 1], (own >> 1) & 1))) break;
-      const int v_byte = own_v<D>(tile, warp * kPageSize, f.count);
-      if (lane == 0) {
-        f.k_byte[warp] = (uint8_t)k_byte;
-        f.v_byte[warp] = (uint8_t)v_byte;
+      if (!(ok = p.warp_wait(&p.bar.own_raw[odd], parity))) break;
+      if (!(ok = p.warp_wait(&p.bar.own_v[odd], parity))) break;
+#pragma unroll 1
+      for (int g = page0; g < page0 + kPages; ++g) {
+        const int k_byte = own_k<D>(p.smem + L::OFF_K + f.k_slot * L::RAW,
+                                    p.smem + L::OFF_K + (f.k_slot + 1) % kSlots * L::RAW, g * kPageSize, f.count);
+        const int v_byte = own_v<D>(tile, g * kPageSize, f.count);
+        if (lane == 0) {
+          f.k_byte[g] = (uint8_t)k_byte;
+          f.v_byte[g] = (uint8_t)v_byte;
+        }
       }
-      slots += 2;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p.bar.own_full[own & 1]);
-      ++own;
+      if (lane == 0) mbar_arrive(&p.bar.own_full[odd]);
     } else {
-      ++slots;
-      if (!(ok = p.warp_wait(&full[converted % kRaw], (converted / kRaw) & 1))) break;
-      if (!(ok = p.warp_wait(&p.bar.v_empty[ts], ((t / kTiles) & 1) ^ 1))) break;
-      convert_raw<D>(ring + converted % kRaw * L::PAGE, tile, warp * kPageSize,
-                     f.page[warp] >= 0 ? f.count - warp * kPageSize : 0);
+      const int st = converted % kRaw;
+      if (!(ok = p.warp_wait(&full[st], (converted / kRaw) & 1))) break;
+#pragma unroll 1
+      for (int g = 0; g < kPages; ++g)
+        convert_raw<D>(ring + (st * kPages + g) * L::PAGE, tile, (page0 + g) * kPageSize,
+                       f.page[page0 + g] >= 0 ? f.count - (page0 + g) * kPageSize : 0);
       ++converted;
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&p.bar.v_full[ts]);
+      mbar_arrive(&p.bar.v_full[odd]);
       mbar_arrive(&p.bar.info_empty[t % kInfos]);
     }
   }
@@ -576,7 +588,7 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
   if (lane == 0)
 #pragma unroll 1
     for (int i = converted; i < copies; ++i) p.drain(&full[i % kRaw], (i / kRaw) & 1);
-  if (lane == 0 && own_copies > 0) p.drain(&p.bar.own_v[(own_copies - 1) & 1], ((own_copies - 1) >> 1) & 1);
+  if (lane == 0 && page0 == 0 && own > 0) p.drain(&p.bar.own_v[odd], (own - 1) & 1);
   __syncwarp();
 }
 
@@ -587,7 +599,8 @@ MARS_DEV void issue_s(const Pipe& p) {
   using L = Layout<D>;
   const uint32_t idesc = idesc_e4m3_f32(BQ, BKV);
   const uint64_t qd = L::code_desc(p.smem + L::OFF_Q);
-  int slots = 0, items = 0, own = 0;
+  int slots = 0, items = 0;
+  uint32_t own = 0;                                  // parities of even and odd own tiles' counts
   for (int t = 0; p.wait_info(t); ++t) {
     const int flags = p.info(t).flags;
     if (flags & kEnd) break;
@@ -605,8 +618,8 @@ MARS_DEV void issue_s(const Pipe& p) {
       if (!here) break;
     }
     if (flags & kOwn) {
-      if (!p.wait(&p.bar.own_full[own & 1], (own >> 1) & 1)) break;
-      ++own;
+      if (!p.wait(&p.bar.own_full[t & 1], (own >> (t & 1)) & 1)) break;
+      own ^= 1u << (t & 1);
     }
     // S buffer sb last held tile t - 2, whose P the PV of that tile read from it
     if (t >= kBufs && !p.wait(&p.bar.pv_done[sb], (t / kBufs - 1) & 1)) break;
@@ -618,7 +631,7 @@ MARS_DEV void issue_s(const Pipe& p) {
       if (!(ok = p.wait(&p.bar.k_full[st], (slots / kSlots) & 1))) break;
       tc_fence_after();
       const uint64_t kd = L::code_desc(p.smem + L::OFF_K + st * L::RAW);
-#pragma unroll 2
+#pragma unroll
       for (int k = 0; k < 2 * (D / 32); ++k) {
         const uint32_t off = k % (D / 32) * 32;
         mma_f8_ss(p.tmem + L::TM_S + sb * BKV, sdesc_advance(qd, off + k / (D / 32) * L::RAW),
@@ -746,17 +759,16 @@ MARS_DEV void softmax(const Pipe& p) {
       const uint2 kbs = *reinterpret_cast<const uint2*>(f.k_byte);
       const uint2 vbs = *reinterpret_cast<const uint2*>(f.v_byte);
       const bool masked = __any_sync(0xffffffffu, limit < BKV) || (flags & kHoles);
-      // the largest s + e
-      float top = -INFINITY;
+      // Halves of the tile, the second first: its P' lies over its scores and makes room for the other's
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 1; h >= 0; --h) {
         const uint32_t kb = h ? kbs.y : kbs.x, vb = h ? vbs.y : vbs.x;
-        uint32_t r[kKeys];
+        uint32_t r[kKeys], packed[kKeys / 2];
 #pragma unroll
         for (int c = 0; c < kKeys / 32; ++c)
           tmem_ld32(s_addr + h * kKeys + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
         tmem_ld_wait();
-        if (masked) {                                // once, for the second pass too
+        if (masked) {
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
             const int seen = ((vb >> (8 * g)) & 255) ? limit - h * kKeys - 16 * g : 0;
@@ -764,11 +776,9 @@ MARS_DEV void softmax(const Pipe& p) {
             for (int e = 0; e < 16; ++e)
               if (e >= seen) r[16 * g + e] = 0xff800000u;
           }
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c)
-            tmem_st32(s_addr + h * kKeys + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
-          tmem_st_wait();
         }
+        // the largest s + e
+        float top = -INFINITY;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           float x[16];
@@ -779,35 +789,41 @@ MARS_DEV void softmax(const Pipe& p) {
           const float z = flash::max3f(flash::max3f(x[9], x[10], x[11]), flash::max3f(x[12], x[13], x[14]), x[15]);
           top = fmaxf(top, fmaf(fmaxf(y, z), k_factor(factor, kb >> (8 * g)), v_exponent(vb >> (8 * g))));
         }
-      }
-      // lazy rescale (flash_tc.cuh); the PV of this O's last tile came before S of this one
-      const bool raise = top > m + flash::kRescaleLog2;
-      const bool rescale = raise && m != -INFINITY;
-      if (__any_sync(0xffffffffu, rescale)) {
-        const float alpha = rescale ? flash::ex2_approx(m - top) : 1.f;
-        l *= alpha;
+        // lazy rescale (flash_tc.cuh) of O (the PV of its last tile came before S of this one; an
+        // item's first two tiles find none), and of the other half's P'
+        const bool raise = top > m + flash::kRescaleLog2;
+        if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
+          const float alpha = raise && m != -INFINITY ? flash::ex2_approx(m - top) : 1.f;
+          l *= alpha;
+          if (!(flags & (kFirst | kSecond))) {
 #pragma unroll 1
-        for (int c = odd * D; c < odd * D + D; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(o_addr + c, o);
-          tmem_ld_wait();
+            for (int c = odd * D; c < odd * D + D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_addr + c, o);
+              tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st16(o_addr + c, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(o_addr + c, o);
+            }
+          }
+          tmem_st_wait();
+          if (h == 0) {
+#pragma unroll 1
+            for (int c = kKeys / 2; c < kKeys; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(s_addr + L::P_OFF + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 w = q8::halves(o[e]);
+                o[e] = q8::pack_f16x2(w.x * alpha, w.y * alpha);
+              }
+              tmem_st16(s_addr + L::P_OFF + c, o);
+            }
+          }
         }
-        tmem_st_wait();
-      }
-      if (raise) m = top;
-      const float shift = kLift - (m == -INFINITY ? 0.f : m);
-      // P', the second half first: it lies over the scores of the second half
-#pragma unroll 1
-      for (int h = 1; h >= 0; --h) {
-        const uint32_t kb = h ? kbs.y : kbs.x, vb = h ? vbs.y : vbs.x;
-        uint32_t r[kKeys], packed[kKeys / 2];
-#pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c)
-          tmem_ld32(s_addr + h * kKeys + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
-        tmem_ld_wait();
+        if (raise) m = top;
+        const float shift = kLift - (m == -INFINITY ? 0.f : m);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           const float mul = k_factor(factor, kb >> (8 * g)), add = v_exponent(vb >> (8 * g)) + shift;
@@ -930,8 +946,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     bar.abort = 0;
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&bar.info_full[i], 1);
-      // the copies of K, both issuers, the converters' warps, the softmax's
-      mbar_init(&bar.info_empty[i], 3 + kConvertWarps + kSoftmaxWarps);
+      // the copies of K, both issuers, the tile's converters, the softmax's warps
+      mbar_init(&bar.info_empty[i], 3 + kGroupWarps + kSoftmaxWarps);
     }
     for (int i = 0; i < kConvertWarps * kRaw; ++i) mbar_init(&bar.raw_full[i / kRaw][i % kRaw], 1);
     for (int i = 0; i < kSlots; ++i) {
@@ -941,10 +957,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.own_raw[i], 1);
       mbar_init(&bar.own_v[i], 1);
-      mbar_init(&bar.own_full[i], kConvertWarps);
+      mbar_init(&bar.own_full[i], kGroupWarps);
     }
     for (int i = 0; i < kTiles; ++i) {
-      mbar_init(&bar.v_full[i], kConvertWarps);
+      mbar_init(&bar.v_full[i], kGroupWarps);
       mbar_init(&bar.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&bar.drain[i], 1);

@@ -17,7 +17,7 @@ namespace mars {
 
 namespace {
 
-constexpr int kRows = 8;
+constexpr int kRows = 4;
 constexpr int kThreads = 256;
 constexpr int kUnit = 16;            // elements that a thread takes at a time: eight pairs
 constexpr int kMaxPairs = 64;        // pairs of a head
