@@ -278,7 +278,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         for (int e = 0; e < kQuads; ++e)
           x[n][e] = row < p.tokens * a.gp ? load_once(from_q + 8 * e) : make_uint4(0, 0, 0, 0);
       }
-      if (part == 0) {                               // the first copies, behind these reads
+      if (part == 0 && ok) {                         // the first copies, behind these reads
 #pragma unroll 1
         for (int k = 0; k < kStages; ++k) issue();
       }
