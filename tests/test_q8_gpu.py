@@ -233,6 +233,90 @@ def test_chunk_scales_far_apart(lens, heads):
         assert st == 0
         check_chunk8(y, o, rows=[0, 1, 600, 1299])
 
+# Rows (token, head) of a KV head around what one tile of the few-row kernel holds, 8 and 16, and four
+# such tiles; sequences of many rows among empty ones.
+FEW = [([1] * 5, (8, 1, 128)), ([2, 1, 2], (8, 2, 64)), ([3, 1], (12, 3, 128)), ([4] * 3, (16, 4, 64)),
+       ([5] * 3, (16, 4, 128)), ([8, 0, 8], (1, 1, 128)), ([9, 8], (1, 1, 64)), ([16, 16], (2, 2, 128)),
+       ([17, 16], (1, 1, 128)), ([1] * 4, (16, 1, 128)), ([1] * 3, (9, 1, 64)), ([2] * 3, (9, 1, 128)),
+       ([8, 8], (28, 4, 128)), ([16], (14, 2, 64)), ([64], (1, 1, 128)), ([65], (1, 1, 64)),
+       ([300] + [0] * 39, (2, 2, 128)), ([0] * 30 + [140, 0, 0, 1], (4, 4, 64)), ([150] + [0] * 80, (14, 2, 64))]
+
+
+@pytest.mark.parametrize("lens, heads", FEW, ids=lambda v: str(v)[:30])
+def test_chunk_of_few_rows(lens, heads):
+    old = [(211 * i + 17) % 700 for i in range(len(lens))]
+    x = make8(lens, *heads, old, seed=len(lens) + heads[0], tail=1)
+    o, st = run_chunk8(cuda(x))
+    assert st == 0
+    check_chunk8(x, o)
+    again, _ = run_chunk8(cuda(x))
+    assert same(o, again)
+
+
+@pytest.mark.parametrize("lens, old, heads", [([1] * 2500, [(i * 7) % 40 for i in range(2500)], (4, 4, 64)),
+                                              ([1], [33000], (14, 2, 64)), ([2, 1], [40001, 16], (8, 1, 128)),
+                                              ([1] * 3, [9000, 0, 12345], (7, 1, 128))], ids=lambda v: str(v)[:24])
+def test_chunk_of_few_rows_in_many_parts(lens, old, heads):
+    """More items than a CTA lists at a time, and items that many CTAs share."""
+    x = make8(lens, *heads, old, seed=6)
+    o, st = run_chunk8(cuda(x))
+    assert st == 0
+    check_chunk8(x, o)
+    again, _ = run_chunk8(cuda(x))
+    assert same(o, again)
+
+
+def test_chunk_of_a_page_mapped_twice():
+    x = make8([1, 2], 8, 2, 64, [90, 200], seed=7)
+    x["table"][0, 3] = x["table"][0, 1]
+    x["table"][1, :4] = x["table"][0, :4]
+    o, st = run_chunk8(cuda(x))
+    assert st == 0
+    check_chunk8(x, o)
+
+
+@pytest.mark.parametrize("heads", [(7, 1, 128), (14, 2, 64)], ids=str)
+def test_chunk_calls_in_a_row_share_a_workspace(heads):
+    """Calls whose kernels start early, each over its own data, without a wait between them."""
+    sets = [make8(lens, *heads, old, seed=50 + i) for i, (lens, old) in enumerate(
+        [([1, 1], [5000, 3000]), ([2, 1], [100, 6000]), ([1, 9], [900, 1]), ([30, 1], [700, 2500]), ([1], [7777])])]
+    on = [cuda(x) for x in sets]
+    size = max(packed.mars_packed_workspace_bytes(packed.OP_ATTN_CHUNK_Q8, len(y["cu"]) - 1, y["q"].shape[0], *heads,
+                                                  hint_of(y)) for y in on)
+    ws = torch.full((size,), 0xa5, dtype=torch.uint8, device="cuda")
+    outs = [[torch.full_like(y["q"].contiguous(), 7.0) for y in on] for _ in range(6)]
+    st = status()
+    hints = [hint_of(y) for y in on]
+    for o in outs:
+        for y, out, hint in zip(on, o, hints):
+            packed.mars_attn_chunk_q8(y["q"], y["k"], y["v"], y["cu"], y["k_pool"], y["v_pool"], y["k_scale"],
+                                      y["v_scale"], y["table"], y["old"], hint, out, ws, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for x, out in zip(sets, outs[0]):
+        check_chunk8(x, out)
+    for o in outs[1:]:
+        assert all(same(a, b) for a, b in zip(o, outs[0]))
+
+
+def test_chunk_replayed_with_other_lengths():
+    """A captured call is replayed while the cached lengths change: the parts are cut elsewhere."""
+    x = make8([1, 1, 1], 7, 1, 128, [6000, 2000, 400], seed=8)
+    y = cuda(x)
+    ws = workspace(packed.OP_ATTN_CHUNK_Q8, 3, y["q"].shape[0], 7, 1, 128, 6001)
+    o = torch.full_like(y["q"].contiguous(), 7.0)
+    run_chunk8(y, hint=6001, ws=ws, o=o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        packed.mars_attn_chunk_q8(y["q"], y["k"], y["v"], y["cu"], y["k_pool"], y["v_pool"], y["k_scale"], y["v_scale"],
+                                  y["table"], y["old"], 6001, o, ws)
+    for old in ([6000, 2000, 400], [10, 1999, 0], [5999, 0, 17], [6000, 2000, 400]):
+        y["old"].copy_(torch.tensor(old, dtype=torch.int32))
+        o.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_chunk8({**x, "old": torch.tensor(old, dtype=torch.int32)}, o)
+
 
 def test_chunk_scale_argument_and_other_stream():
     x = make8([3, 1], 14, 2, 64, [150, 600], seed=49)
