@@ -509,7 +509,18 @@ int mars_kv_append_q8(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_
 /* mars_attn_chunk over the 8-bit cache: row i of sequence s attends to the P_s = seq_lens[s]
  * cached tokens and to the chunk's rows 0 .. i, given in k and v in bf16. Arguments, errors and
  * what other keys may hold as mars_attn_chunk; the pools and scales as above.
- *   workspace >= mars_packed_workspace_bytes(MARS_OP_ATTN_CHUNK_Q8, ...) bytes (NULL if 0) */
+ *   workspace >= mars_packed_workspace_bytes(MARS_OP_ATTN_CHUNK_Q8, ...) bytes (NULL if 0)
+ * Codes and scales enter the products exactly, scores, statistics and sums are held in 32 bits, and
+ * the weights are rounded to f16, over the page's scale, for the product with V (many rows: to bf16,
+ * the keys and values being unpacked to bf16 first, which holds them exactly). By the number of rows
+ * per sequence, q and the chunk's own rows are held
+ *   in f16 over a power of two per row, exact down to 2^-39 of the row's largest magnitude (few
+ *   rows: a tile of 8 or 16 (token, head) rows of a KV head per sequence, by batch and total);
+ *   as sums of two e4m3 numbers over a power of two per row of q and per 16 own keys, exact to 2^-17
+ *   of the largest magnitude there, and own values in f16 over one per 16 keys (these powers reach
+ *   from 2^-40 to 2^80: beyond 2^88 values saturate, and an infinity in q or an own k is NaN there);
+ *   in bf16 (many rows).
+ * Each result is the same, bit by bit, from call to call. */
 int mars_attn_chunk_q8(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
                        const int32_t* cu_seqlens, const uint8_t* k_pool, const uint8_t* v_pool,
                        const uint8_t* k_scale, const uint8_t* v_scale, int num_pages,
