@@ -55,8 +55,7 @@ static_assert(128 * (kControlRegs + 2 * kSoftmaxRegs + 2 * kConvertRegs) <=
 constexpr int kGroupWarps = kConvertWarps / 2, kPages = kPagesPerTile / kGroupWarps;   // of even or odd
                                      // tiles; pages of a warp
 constexpr int kRaw = 2;              // ring of a converter warp's raw pages, kPages at a time
-constexpr int kSlots = 4;            // ring of tiles of K's codes; an own tile takes two slots, and so
-                                     // does an item's Q in bf16, before its first tile
+constexpr int kSlots = 4;            // ring of tiles of K's codes; an own tile takes two slots
 constexpr int kAhead = 2;            // tiles that copies may be ahead of the conversion
 constexpr int kTiles = 2;            // f16 tiles of V
 constexpr int kBufs = 2;             // S buffers, and O's, in TMEM: of even and odd tiles
@@ -77,27 +76,22 @@ struct alignas(16) Info {
   int base, n, tok0, h0, kvh;        // its item
   int slot;                          // of the partial, -1: the item is whole
   int k0, count;                     // first key (own: token of the sequence), keys that there are
-  int q_slot, k_slot;                // where a part's first tile has its Q in K's ring, an own one its K
-  int pad;
-  alignas(16) int page[kPagesPerTile];         // -1: not to be read
-  alignas(8) uint8_t k_byte[kPagesPerTile];    // scale bytes; own tiles: written by the converters
+  int pad[3];
+  alignas(16) int page[kPagesPerTile];         // own tiles: groups of own rows; -1: not to be read
+  alignas(8) uint8_t k_byte[kPagesPerTile];    // scale bytes
   alignas(8) uint8_t v_byte[kPagesPerTile];    // 0: no such keys
 };
 
 struct Bar {
   uint64_t info_full[kInfos], info_empty[kInfos];
   uint64_t raw_full[kConvertWarps][kRaw];              // of a warp's pages
-  // own_raw: an own tile's K in bf16 is in its two slots, own_full: its scales and its two parts are.
-  // (Barriers of their own: a wait for a phase of a ring whose last one is still open would pass at
-  // once. One of each for even and for odd tiles: the slots let two own tiles be under way.)
-  uint64_t k_full[kSlots], k_empty[kSlots], own_raw[2], own_full[2], own_v[2];
+  uint64_t k_full[kSlots], k_empty[kSlots];
   uint64_t v_full[kTiles], v_empty[kTiles];
   uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
-  uint64_t q_raw, q_full, o_free, drain[2];
+  uint64_t q_full, q_free, o_free, drain[2];
   uint64_t pair[4];                  // the two warps of 32 rows
   uint32_t tmem_base;
   int abort;
-  uint8_t q_byte[2][BQ];             // [item][row]: scale bytes of Q
 };
 
 // All that is not a tile. Its size keeps what follows, the tiles, aligned to 1024 bytes: they leave
@@ -110,7 +104,7 @@ struct alignas(1024) Shared {
     float exchange[2][BQ];           // [even or odd tiles][row], at the end of items
   };
 };
-static_assert(sizeof(Shared) == 3072, "with the tiles, all of the shared memory of a CTA");
+static_assert(sizeof(Shared) <= 3072, "with the tiles, the shared memory of a CTA");
 
 template <int D>
 struct Layout {
@@ -180,7 +174,7 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
   const Args& a = p.a;
   const int lane = threadIdx.x & 31;
   Record rec{};
-  int t = 0, flags = 0, slots = 0;
+  int t = 0, flags = 0;
   bool ok = true;
   // wait until `n` entries from t on are free
   auto room = [&](int n) {
@@ -245,15 +239,25 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
       e.slot = slot;
       e.k0 = k0;
       e.count = count;
-      e.q_slot = slots % kSlots;
-      e.k_slot = (slots + (f & kFirst ? 2 : 0)) % kSlots;
     };
     for (int x = j; x < own && ok; ++x) {
+      const int count = min(last_tok + 1 - x * BKV, BKV);
+      const bool needed = lane < kPagesPerTile && lane * kPageSize < count;
+      const int group = own_group(q.base, q.s) + x * kPagesPerTile + lane;
+      uint8_t kb = 127, vb = 0;
+      if (needed) {
+        const size_t at = (size_t)group * a.hkv + kvh;
+        kb = a.own_k_byte[at];
+        vb = a.own_v_byte[at];
+      }
       if (!(ok = room(1))) break;
-      if (lane == 0)
-        entry(p.info(t), x * BKV, min(last_tok + 1 - x * BKV, BKV),
-              kOwn | first | (left == 1 ? kLast : 0));
-      slots += first & kFirst ? 4 : 2;
+      Info& f = p.info(t);
+      if (lane < kPagesPerTile) {
+        f.page[lane] = needed ? group : -1;
+        f.k_byte[lane] = kb;
+        f.v_byte[lane] = vb;
+      }
+      if (lane == 0) entry(f, x * BKV, count, kOwn | first | (left == 1 ? kLast : 0));
       first = first & kFirst ? kSecond : 0;
       --left;
       publish(1);
@@ -290,7 +294,6 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
                 (u == 0 ? first : u == 1 && first == kFirst ? kSecond : 0) | (u + 1 == left ? kLast : 0) |
                     (((holes >> lane) & 0xffu) ? kHoles : 0));
       }
-      slots += first & kFirst ? n + 2 : n;
       first = first & kFirst && n == 1 ? kSecond : 0;
       left -= n;
       publish(n);
@@ -310,8 +313,8 @@ MARS_DEV uint8_t* chunk_at(uint8_t* tile, int r, int c) {
   return tile + (c >> 3) * (BKV * 128) + flash::sw_off(r, c & 7);
 }
 
-// Warp 1: K's codes, a copy per page. Before an item's first tile its Q, and for an own tile K, in
-// bf16: half of the elements of the rows in either of two slots.
+// Warp 1: K's codes, a copy per page, an own tile's in two parts; and an item's Q, once every S of the
+// item before is done.
 template <int D>
 MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& map_q,
                      const CUtensorMap& map_own) {
@@ -319,57 +322,44 @@ MARS_DEV void load_k(const Pipe& p, const CUtensorMap& map, const CUtensorMap& m
   using L = Layout<D>;
   const Args& a = p.a;
   const int lane = threadIdx.x & 31;
-  int c = 0, own[2] = {0, 0}, qs = 0;                // slots taken, even and odd own tiles, items
+  int c = 0, items = 0;                              // slots taken
   bool ok = true;
   for (int t = 0; ok && p.warp_wait_info(t); ++t) {
     const Info& f = p.info(t);
     const int flags = f.flags;
     if (flags & kEnd) break;
-    const int page = lane < kPagesPerTile && !(flags & kOwn) ? f.page[lane] : -1;
+    const bool own = flags & kOwn;
+    const int page = lane < kPagesPerTile ? f.page[lane] : -1;
     const int pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
-    const int row = (max(page, 0) * a.hkv + f.kvh) * kPageSize;
-    // slots for: halves of Q (i < 0), then the tile, or halves of own rows
-    const int q = flags & kFirst ? 2 : 0;
+    int row = (max(page, 0) * a.hkv + f.kvh) * kPageSize;
 #pragma unroll 1
-    for (int i = -q; i < (flags & kOwn ? 2 : 1); ++i, ++c) {
-      const int st = c % kSlots, half = i & 1;
-      const bool halves = i < 0 || (flags & kOwn);
-      uint8_t* dst = p.smem + L::OFF_K + st * L::RAW;
+    for (int i = 0; i <= own; ++i, ++c, row += a.own_groups * a.hkv * kPageSize) {
+      const int st = c % kSlots;
       if (!(ok = p.warp_wait(&p.bar.k_empty[st], ((c / kSlots) & 1) ^ 1))) break;
-      // both slots before the first half, so that the second always follows
-      if (halves && !half &&
-          !(ok = p.warp_wait(&p.bar.k_empty[(c + 1) % kSlots], (((c + 1) / kSlots) & 1) ^ 1)))
-        break;
-      if (lane == 0) mbar_arrive_expect_tx(&p.bar.k_full[st], halves ? 0 : pages * L::PAGE);
+      if (lane == 0) mbar_arrive_expect_tx(&p.bar.k_full[st], pages * L::PAGE);
       __syncwarp();
-      if (halves) {
-        uint64_t* raw = i < 0 ? &p.bar.q_raw : &p.bar.own_raw[t & 1];
-        if (lane == 0) {
-          if (!half) mbar_arrive_expect_tx(raw, (i < 0 ? a.gp * a.tpt : BKV) * D * 2);
-          tma_load_3d(dst, i < 0 ? &map_q : &map_own, raw, half * (D / 2), i < 0 ? f.h0 : f.kvh,
-                      f.base + (i < 0 ? f.tok0 : f.k0));
-        }
-        if (half) {
-          qs += i < 0;
-          own[0] += i >= 0 && !(t & 1);
-          own[1] += i >= 0 && (t & 1);
-        }
-      } else if (page >= 0) {
-        tma_load_2d(dst + lane * L::PAGE, &map, &p.bar.k_full[st], 0, row);
-      }
+      if (page >= 0)
+        tma_load_2d(p.smem + L::OFF_K + st * L::RAW + lane * L::PAGE, own ? &map_own : &map, &p.bar.k_full[st], 0, row);
     }
-    if (ok) p.warp_done(t);
+    if (!ok) break;
+    if (flags & kFirst) {
+      if (items > 0 && !(ok = p.warp_wait(&p.bar.q_free, (items - 1) & 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&p.bar.q_full, 2 * a.gp * a.tpt * D);
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i)
+          tma_load_3d(p.smem + L::OFF_Q + i * L::RAW, &map_q, &p.bar.q_full, 0, f.h0, i * a.total + f.base + f.tok0);
+      }
+      ++items;
+    }
+    p.warp_done(t);
   }
   // no copy is in flight when the CTA ends
-  if (lane == 0)
+  if (lane == 0) {
 #pragma unroll 1
     for (int i = max(0, c - kSlots); i < c; ++i)
       p.drain(&p.bar.k_full[i % kSlots], (i / kSlots) & 1);
-  if (lane == 0) {
-    if (qs > 0) p.drain(&p.bar.q_raw, (qs - 1) & 1);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (own[i] > 0) p.drain(&p.bar.own_raw[i], (own[i] - 1) & 1);
+    if (items > 0) p.drain(&p.bar.q_full, (items - 1) & 1);
   }
   __syncwarp();
 }
@@ -399,110 +389,7 @@ MARS_DEV void convert_raw(const uint8_t* raw, uint8_t* tile, int r0, int valid) 
   }
 }
 
-// Eight bf16 times f as two e4m3 numbers each: the nearest, and the nearest to what that leaves. An
-// infinity becomes NaN (a finite value's second product adds nothing).
-MARS_DEV void split8(const uint4& x, float f, uint2& first, uint2& second) {
-  float e[8];
-  unpack8(x, e);
-  uint32_t u[2], v[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float* w = e + 4 * i;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = fmaf(w[k], 0.f, w[k] * f);
-    u[i] = q8::encode2(w[0], w[1]) | (q8::encode2(w[2], w[3]) << 16);
-    uint32_t lo, hi;
-    q8::decode4(u[i], lo, hi);
-    const float2 p = q8::halves(lo), q = q8::halves(hi);
-    v[i] = q8::encode2(w[0] - p.x, w[1] - p.y) | (q8::encode2(w[2] - q.x, w[3] - q.y) << 16);
-  }
-  first = make_uint2(u[0], u[1]);
-  second = make_uint2(v[0], v[1]);
-}
-
-// Rows in bf16 as two slots of K's ring hold them: the first half of a row's elements in either one's
-// row. Lane c of a row's D / 8 has 8 of them, and its place among the codes of either part.
-template <int D>
-struct Halves {
-  using L = Layout<D>;
-  static constexpr int kLanes = D / 8, kRows = 32 / kLanes;          // lanes of a row, rows of a warp
-  const uint8_t *lo, *hi;
-  MARS_DEV int lane() const { return threadIdx.x % kLanes; }
-  MARS_DEV int row() const { return threadIdx.x % 32 / kLanes; }
-  MARS_DEV uint4 get(int r) const {
-    return *reinterpret_cast<const uint4*>((lane() < kLanes / 2 ? lo : hi) +
-                                           L::code_at(r, lane() % (kLanes / 2)));
-  }
-  MARS_DEV uint32_t code_at(int r) const { return L::code_at(r, lane() / 2) + (lane() & 1) * 8; }
-  static MARS_DEV uint32_t top(const uint4& x) {
-    return finite_max(finite_max(finite_max(finite_max(0u, x.x), x.y), x.z), x.w);
-  }
-};
-
-// The power of two over which 16 own rows with a largest finite magnitude of `top` (bf16 bits, of
-// either half of a lane's word) go, as a scale byte: it then lies in [2^less, 2^(less + 1)). Whole warp.
-MARS_DEV int own_byte(uint32_t top, int less) {
-  top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
-  return min(max((int)(top >> 7) - less, q8::kLeast), kOwnMost);
-}
-
-// Rows r0 .. r0 + 15 of an own tile's K, in place: two parts in e4m3, the first in `lo`. Those from
-// `count` on are not keys and stay what they are. Returns the scale byte.
-template <int D>
-MARS_DEV int own_k(uint8_t* lo, uint8_t* hi, int r0, int count) {
-  using H = Halves<D>;
-  const H h{lo, hi};
-  const int end = min(r0 + kPageSize, count);
-  uint32_t top = 0;
-#pragma unroll 1
-  for (int r = r0 + h.row(); r < end; r += H::kRows) top = __vmaxu2(top, H::top(h.get(r)));
-  __syncwarp();
-  const int byte = own_byte(top, 7);
-  const float f = q8::inverse_power(byte);
-#pragma unroll 1
-  for (int r = r0 + h.row(); r - h.row() < end; r += H::kRows) {
-    uint2 u, v;
-    split8(h.get(r), f, u, v);                       // of 16 rows that a tile has, whatever they hold
-    __syncwarp();                                    // all of the rows has been read
-    *reinterpret_cast<uint2*>(lo + h.code_at(r)) = u;
-    *reinterpret_cast<uint2*>(hi + h.code_at(r)) = v;
-  }
-  return byte;
-}
-
-// Rows r0 .. r0 + 15 of an own tile's V, in place: bf16 to f16, zero from `count` on. Returns the
-// scale byte.
-template <int D>
-MARS_DEV int own_v(uint8_t* tile, int r0, int count) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-  const int lane = threadIdx.x & 31, c = lane % kLanes, first = r0 + lane / kLanes;
-  const int end = min(r0 + kPageSize, count);
-  uint32_t top = 0;
-#pragma unroll 1
-  for (int r = first; r < end; r += kRows) {
-    const uint4 x = *reinterpret_cast<const uint4*>(chunk_at(tile, r, c));
-    top = finite_max(finite_max(finite_max(finite_max(top, x.x), x.y), x.z), x.w);
-  }
-  __syncwarp();
-  const int byte = own_byte(top, 8);
-  const float f = q8::inverse_power(byte);
-#pragma unroll 1
-  for (int r = first; r < r0 + kPageSize; r += kRows) {
-    uint4* at = reinterpret_cast<uint4*>(chunk_at(tile, r, c));
-    uint4 y = make_uint4(0, 0, 0, 0);
-    if (r < end) {
-      float e[8];
-      unpack8(*at, e);
-      y = make_uint4(q8::pack_f16x2(e[0] * f, e[1] * f), q8::pack_f16x2(e[2] * f, e[3] * f),
-                     q8::pack_f16x2(e[4] * f, e[5] * f), q8::pack_f16x2(e[6] * f, e[7] * f));
-    }
-    *at = y;
-  }
-  return byte;
-}
-
-// Warps 12 ..: copies of their page of every tile of V and f16 tiles from them, and the sequence's own
-// K and V.
+// Warps 12 ..: copies of their pages of V and f16 tiles from them; own V is in f16.
 template <int D>
 MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& map_own) {
   using namespace sm100;
@@ -514,7 +401,7 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
   uint64_t* const full = p.bar.raw_full[warp];
   uint8_t* const ring = p.smem + L::OFF_RAW + warp * kRaw * kPages * L::PAGE;
   // the next copies: their number and tile; `converted`: those that have left the ring
-  int copies = 0, next = odd, converted = 0, own = 0;
+  int copies = 0, next = odd, converted = 0, own_copies = -1;
   bool more = true, ok = true;
   auto copy_ahead = [&](int t) {
     while (more && next <= t + kAhead && copies < converted + kRaw) {
@@ -542,31 +429,13 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
     if (flags & kEnd) break;
     uint8_t* tile = p.smem + L::OFF_V + odd * L::TILE;
     if (!(ok = p.warp_wait(&p.bar.v_empty[odd], ((t / kTiles) & 1) ^ 1))) break;
+    uint32_t bytes = 0;                              // that a copy puts there
     if (flags & kOwn) {
-      // warp 1 has brought K. V's copy goes to its place in the tile; S also waits for V's scales,
-      // which its softmax needs
-      const uint32_t parity = own++ & 1;
-      if (page0 == 0 && lane == 0) {
-        mbar_arrive_expect_tx(&p.bar.own_v[odd], BKV * D * 2);
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-          tma_load_3d(tile + x * (BKV * 128), &map_own, &p.bar.own_v[odd], x * 64, f.kvh, f.base + f.k0);
-      }
-      if (!(ok = p.warp_wait(&p.bar.own_raw[odd], parity))) break;
-      if (!(ok = p.warp_wait(&p.bar.own_v[odd], parity))) break;
 #pragma unroll 1
       for (int g = page0; g < page0 + kPages; ++g) {
-        const int k_byte = own_k<D>(p.smem + L::OFF_K + f.k_slot * L::RAW,
-                                    p.smem + L::OFF_K + (f.k_slot + 1) % kSlots * L::RAW, g * kPageSize, f.count);
-        const int v_byte = own_v<D>(tile, g * kPageSize, f.count);
-        if (lane == 0) {
-          f.k_byte[g] = (uint8_t)k_byte;
-          f.v_byte[g] = (uint8_t)v_byte;
-        }
+        if (f.page[g] >= 0) bytes += 2 * L::PAGE;
+        else convert_raw<D>(ring, tile, g * kPageSize, 0);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p.bar.own_full[odd]);
     } else {
       const int st = converted % kRaw;
       if (!(ok = p.warp_wait(&full[st], (converted / kRaw) & 1))) break;
@@ -579,7 +448,13 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&p.bar.v_full[odd]);
+      mbar_arrive_expect_tx(&p.bar.v_full[odd], bytes);
+#pragma unroll 1
+      for (int g = page0; bytes && g < page0 + kPages; ++g)
+        for (int x = 0; x < D / 64 && f.page[g] >= 0; ++x)
+          tma_load_2d(tile + x * (BKV * 128) + g * kPageSize * 128, &map_own, &p.bar.v_full[odd], x * 64,
+                      (f.page[g] * a.hkv + f.kvh) * kPageSize);
+      own_copies = bytes ? t : own_copies;
       mbar_arrive(&p.bar.info_empty[t % kInfos]);
     }
   }
@@ -588,7 +463,8 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
   if (lane == 0)
 #pragma unroll 1
     for (int i = converted; i < copies; ++i) p.drain(&full[i % kRaw], (i / kRaw) & 1);
-  if (lane == 0 && page0 == 0 && own > 0) p.drain(&p.bar.own_v[odd], (own - 1) & 1);
+  // (where all went well, the last P V has waited for own ones)
+  if (lane == 0 && !ok && own_copies >= 0) p.drain(&p.bar.v_full[odd], (own_copies / kTiles) & 1);
   __syncwarp();
 }
 
@@ -600,27 +476,12 @@ MARS_DEV void issue_s(const Pipe& p) {
   const uint32_t idesc = idesc_e4m3_f32(BQ, BKV);
   const uint64_t qd = L::code_desc(p.smem + L::OFF_Q);
   int slots = 0, items = 0;
-  uint32_t own = 0;                                  // parities of even and odd own tiles' counts
   for (int t = 0; p.wait_info(t); ++t) {
     const int flags = p.info(t).flags;
     if (flags & kEnd) break;
     mbar_arrive(&p.bar.info_empty[t % kInfos]);
     const int sb = t % kBufs;
-    if (flags & kFirst) {
-      // the softmax has turned Q's two slots into its parts
-      if (!p.wait(&p.bar.q_full, items++ & 1)) break;
-      bool here = true;
-#pragma unroll 1
-      for (int i = 0; here && i < 2; ++i, ++slots) {
-        here = p.wait(&p.bar.k_full[slots % kSlots], (slots / kSlots) & 1);
-        mbar_arrive(&p.bar.k_empty[slots % kSlots]);
-      }
-      if (!here) break;
-    }
-    if (flags & kOwn) {
-      if (!p.wait(&p.bar.own_full[t & 1], (own >> (t & 1)) & 1)) break;
-      own ^= 1u << (t & 1);
-    }
+    if ((flags & kFirst) && !p.wait(&p.bar.q_full, items++ & 1)) break;
     // S buffer sb last held tile t - 2, whose P the PV of that tile read from it
     if (t >= kBufs && !p.wait(&p.bar.pv_done[sb], (t / kBufs - 1) & 1)) break;
     const int parts = flags & kOwn ? 2 : 1;
@@ -641,6 +502,7 @@ MARS_DEV void issue_s(const Pipe& p) {
     }
     if (!ok) break;
     mma_commit(&p.bar.s_full[sb]);
+    if (flags & kLast) mma_commit(&p.bar.q_free);
   }
   mma_commit(&p.bar.drain[0]);
   p.drain(&p.bar.drain[0], 0);
@@ -675,42 +537,6 @@ MARS_DEV void issue_pv(const Pipe& p) {
   p.drain(&p.bar.drain[1], 0);
 }
 
-// Q of the item that tile t begins (its `item`-th), out of K's ring: each row over the power of two
-// that brings its largest finite magnitude into [128, 256), as two e4m3 numbers. Rows without a token
-// stay what they are.
-template <int D>
-MARS_DEV bool convert_q(const Pipe& p, int t, int item) {
-  using namespace sm100;
-  using L = Layout<D>;
-  using H = Halves<D>;
-  const Args& a = p.a;
-  const Info& f = p.info(t);
-  const int warp = (threadIdx.x >> 5) - kSoftmaxWarp, lane = threadIdx.x & 31;
-  if (!p.warp_wait(&p.bar.q_raw, item & 1)) return false;
-  const int rows = a.gp * min(a.tpt, f.n - f.tok0);
-  uint8_t* to = p.smem + L::OFF_Q;
-  const H h{p.smem + L::OFF_K + f.q_slot * L::RAW, p.smem + L::OFF_K + (f.q_slot + 1) % kSlots * L::RAW};
-#pragma unroll 1
-  for (int r = warp * H::kRows + h.row(); r - h.row() < rows; r += kSoftmaxWarps * H::kRows) {
-    const uint4 x = h.get(r);
-    uint32_t top = H::top(x);
-    top = max(top >> 16, top & 0xffffu);
-#pragma unroll
-    for (int o = 1; o < H::kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // (a row of next to nothing: 2^-53)
-    const int byte = top ? min(max((int)(top >> 7), 74), 253) - 7 : q8::kBias;
-    uint2 u, v;
-    split8(x, q8::inverse_power(byte), u, v);
-    *reinterpret_cast<uint2*>(to + h.code_at(r)) = u;
-    *reinterpret_cast<uint2*>(to + L::RAW + h.code_at(r)) = v;
-    if (h.lane() == 0) p.bar.q_byte[item & 1][r] = (uint8_t)byte;
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(&p.bar.q_full);
-  return p.warp_wait(&p.bar.q_full, item & 1);
-}
-
 // Factor of the scores of 16 keys (never 0 or infinite: it meets infinite scores), and the exponent
 // of their V; by their scale bytes, the low ones of k and v.
 MARS_DEV float k_factor(float factor, uint32_t k) {
@@ -733,7 +559,7 @@ MARS_DEV void softmax(const Pipe& p) {
   const uint32_t s_addr = p.tmem + L::TM_S + odd * BKV + lane_off;
   const uint32_t o_addr = p.tmem + L::TM_O + lane_off;              // of even tiles
   float factor = 0.f, m = -INFINITY, l = 0.f;
-  int tok = 0, tiles = 0, items = 0, flags = kLast, uses = 0;
+  int tok = 0, tiles = 0, flags = 0, uses = 0;
   bool has = false, busy = false;
   // The two warps of 32 rows meet; what either wrote before is there after.
   auto meet = [&]() -> bool {
@@ -743,14 +569,9 @@ MARS_DEV void softmax(const Pipe& p) {
   };
   for (int t = -1;;) {                               // before the first tile t = -1
     const bool mine = t >= 0 && (t & 1) == odd;
-    if (mine || (t >= 0 && (flags & kLast))) {
+    if (mine) {
       if (!p.warp_wait(&p.bar.s_full[t & 1], (t / kBufs) & 1)) return;
       tc_fence_after();
-    }
-    if (flags & kLast) {
-      // every S of the item is done: the next one's Q, so that its S runs beside what follows here
-      if (!p.warp_wait_info(t + 1)) return;
-      if (!(p.info(t + 1).flags & kEnd) && !convert_q<D>(p, t + 1, items++)) return;
     }
     const Info& f = p.info(max(t, 0));
     if (mine && busy) {
@@ -921,7 +742,8 @@ MARS_DEV void softmax(const Pipe& p) {
       tok = n.tok0 + row / a.gp;
       has = row < a.gp * a.tpt && tok < n.n;
       busy = __any_sync(0xffffffffu, has);       // warps without rows only keep step
-      factor = has ? a.scale_log2 * q8::power(p.bar.q_byte[(items - 1) & 1][row]) : 1.f;
+      factor = 1.f;
+      if (has) factor = a.scale_log2 * q8::power(a.q_byte[((size_t)n.base + tok) * a.hq + n.h0 + row % a.gp]);
     }
   }
 }
@@ -954,11 +776,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       mbar_init(&bar.k_full[i], 1);
       mbar_init(&bar.k_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.own_raw[i], 1);
-      mbar_init(&bar.own_v[i], 1);
-      mbar_init(&bar.own_full[i], kGroupWarps);
-    }
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(&bar.v_full[i], kGroupWarps);
       mbar_init(&bar.v_empty[i], 1);
@@ -969,8 +786,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       mbar_init(&bar.p_full[i], 128);
       mbar_init(&bar.pv_done[i], 1);
     }
-    mbar_init(&bar.q_raw, 1);
-    mbar_init(&bar.q_full, kSoftmaxWarps);
+    mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.q_free, 1);
     mbar_init(&bar.o_free, kSoftmaxWarps);
     for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
     fence_barrier_init();
@@ -1015,59 +832,169 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
   }
 }
 
-// ------------------------------------------------------------------------------ the wide form
+// ------------------------------------------------------------------------- what comes before
+//
+// A kernel before chunk_kernel turns Q and the sequences' own rows into what its products take: it
+// would otherwise do so at the start of every item, with the code for it out of the instruction cache
+// (17,000 cycles an item, in which nothing else ran).
 //
 // Where the rows are many, a sequence's pages are written out in bf16 (exact too), once, and
-// attended to by packed_attn.cu, whose CTAs would otherwise each convert them again.
+// attended to by packed_attn.cu, whose CTAs would otherwise each convert them again (the wide form).
 
-struct UnpackArgs {
+struct ReadyArgs {
+  const uint16_t *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
   const int32_t *cu, *seq_lens, *block_table;
   const uint8_t *k_pool, *v_pool, *k_scale, *v_scale;
+  int num_pages, max_pages, pages, tpt, batch, total, hq, hkv, own_groups;
+  // the wide form's pages, lengths and table
   uint16_t *k_out, *v_out;
-  int32_t *lens, *table, *status;
-  int num_pages, max_pages, pages, tpt, batch, total, hkv;
+  int32_t *lens, *table;
+  // chunk_kernel's: Q as [2][total][hq][D], scale bytes [total][hq]; groups of 16 own rows, K as
+  // [2][groups][hkv][16][D] and V in f16 as [groups][hkv][16][D], scale bytes [groups][hkv] each
+  uint8_t *q_parts, *q_byte, *k_parts, *k_byte, *v_byte;
+  uint16_t* v_half;
 };
-constexpr int kUnpackThreads = 256;
+constexpr int kReadyThreads = 256;
 
-// A CTA writes one page of a sequence out: page j of sequence s becomes page s * pages + j.
-// Sequences that chunk_kernel takes get no keys here; what the wide kernels then make of their
-// rows is written over.
+// Eight bf16 times f as two e4m3 numbers each: the nearest, and the nearest to what that leaves. An
+// infinity becomes NaN (a finite value's second product adds nothing).
+MARS_DEV void split8(const uint4& x, float f, uint2& first, uint2& second) {
+  float e[8];
+  unpack8(x, e);
+  uint32_t u[2], v[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float* w = e + 4 * i;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = fmaf(w[k], 0.f, w[k] * f);
+    u[i] = q8::encode2(w[0], w[1]) | (q8::encode2(w[2], w[3]) << 16);
+    uint32_t lo, hi;
+    q8::decode4(u[i], lo, hi);
+    const float2 p = q8::halves(lo), q = q8::halves(hi);
+    v[i] = q8::encode2(w[0] - p.x, w[1] - p.y) | (q8::encode2(w[2] - q.x, w[3] - q.y) << 16);
+  }
+  first = make_uint2(u[0], u[1]);
+  second = make_uint2(v[0], v[1]);
+}
+
+// Head w of q, k and v for 16 rows from r0 on of a sequence, rows from nr on zero. Whole warp.
 template <int D>
-__global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(UnpackArgs a) {
+MARS_DEV void split_rows(const ReadyArgs& a, const packed::Seq& sq, int r0, int nr, int w) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIts = kPageSize / kRows;     // rows at a time
+  const int lane = threadIdx.x & 31, c = lane % kLanes, r = lane / kLanes;
+  const bool is_q = w < a.hq, is_v = w >= a.hq + a.hkv;
+  const int h = is_q ? w : is_v ? w - a.hq - a.hkv : w - a.hq;
+  const long long stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+  const size_t row0 = (size_t)sq.base + r0;
+  const uint16_t* from = (is_q ? a.q : is_v ? a.v : a.k) + row0 * stride + h * D + c * 8;
+  uint4 x[kIts];
+#pragma unroll
+  for (int i = 0; i < kIts; ++i)
+    x[i] = r + i * kRows < nr ? *reinterpret_cast<const uint4*>(from + (r + i * kRows) * stride)
+                              : make_uint4(0, 0, 0, 0);
+  auto top_of = [&](const uint4& y, uint32_t top) {
+    return finite_max(finite_max(finite_max(finite_max(top, y.x), y.y), y.z), y.w);
+  };
+  if (is_q) {
+#pragma unroll
+    for (int i = 0; i < kIts; ++i) {
+      uint32_t top = top_of(x[i], 0);
+      top = max(top >> 16, top & 0xffffu);
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // the row's largest magnitude into [128, 256) (a row of next to nothing: 2^-53)
+      const int byte = top ? min(max((int)(top >> 7), 74), 253) - 7 : kBias;
+      if (r + i * kRows >= nr) continue;
+      uint2 u, v;
+      split8(x[i], inverse_power(byte), u, v);
+      const size_t at = (row0 + r + i * kRows) * a.hq + h;
+      *reinterpret_cast<uint2*>(a.q_parts + at * D + c * 8) = u;
+      *reinterpret_cast<uint2*>(a.q_parts + ((size_t)a.total * a.hq + at) * D + c * 8) = v;
+      if (c == 0) a.q_byte[at] = (uint8_t)byte;
+    }
+    return;
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kIts; ++i) top = top_of(x[i], top);
+  top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+  // the largest magnitude of the 16 rows into [128, 256), V's into [256, 512)
+  const int byte = min(max((int)(top >> 7) - (is_v ? 8 : 7), kLeast), kOwnMost);
+  const float f = inverse_power(byte);
+  const size_t at = (size_t)(own_group(sq.base, sq.s) + sq.tile) * a.hkv + h;
+  if (lane == 0) (is_v ? a.v_byte : a.k_byte)[at] = (uint8_t)byte;
+  const size_t second = (size_t)a.own_groups * a.hkv * kPageSize * D;
+#pragma unroll
+  for (int i = 0; i < kIts; ++i) {
+    const size_t to = (at * kPageSize + r + i * kRows) * D + c * 8;
+    if (is_v) {
+      float e[8];
+      unpack8(x[i], e);
+      *reinterpret_cast<uint4*>(a.v_half + to) =
+          make_uint4(pack_f16x2(e[0] * f, e[1] * f), pack_f16x2(e[2] * f, e[3] * f),
+                     pack_f16x2(e[4] * f, e[5] * f), pack_f16x2(e[6] * f, e[7] * f));
+    } else {
+      uint2 u, v;
+      split8(x[i], f, u, v);
+      *reinterpret_cast<uint2*>(a.k_parts + to) = u;
+      *reinterpret_cast<uint2*>(a.k_parts + second + to) = v;
+    }
+  }
+}
+
+// Block (x, y): 16 own rows of a sequence, or where it is left to the wide form a page of it (page j
+// of sequence s becomes page s * pages + j); every gridDim.y-th eight heads. Sequences that chunk_kernel takes have no
+// keys in the wide form, and what that then makes of their rows is written over.
+template <int D>
+__global__ void __launch_bounds__(kReadyThreads) ready_kernel(ReadyArgs a) {
   sm100::wait_for_previous();
+  sm100::let_next_start();
+  const int skip = a.pages ? a.pages : -1;
   auto cut = [&](int len) { return (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize)); };
+  auto tiles = [](int rows) { return rows / kPageSize + (rows % kPageSize != 0); };
   bool bad;
   const packed::Seq sq = packed::find_tile_by(
       a.cu, a.batch, a.total, (long long)blockIdx.x, bad, a.seq_lens, [&](int, int n, int len) {
         const int P = cut(len);
-        return left_out(a.pages, a.tpt, n, P) ? max(1, (P + kPageSize - 1) / kPageSize) : 1;
+        return max(left_out(skip, a.tpt, n, P) ? tiles(P) : tiles(n), a.pages ? 1 : 0);
       });
   if (sq.s < 0) return;
-  const int P = left_out(a.pages, a.tpt, sq.n, cut(sq.len)) ? cut(sq.len) : 0;
-  if (sq.tile == 0 && threadIdx.x == 0) a.lens[sq.s] = P;
+  const int P = cut(sq.len);
+  const bool wide = left_out(skip, a.tpt, sq.n, P);
+  if (a.pages && sq.tile == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.lens[sq.s] = wide ? P : 0;
+  if (!wide) {
+    const int r0 = sq.tile * kPageSize;
+    if (r0 >= sq.n) return;
+#pragma unroll 1
+    for (int w = (blockIdx.y * kReadyThreads + threadIdx.x) / 32; w < a.hq + 2 * a.hkv;
+         w += gridDim.y * (kReadyThreads / 32))
+      split_rows<D>(a, sq, r0, min(sq.n - r0, kPageSize), w);
+    return;
+  }
   if (sq.tile * kPageSize >= P) return;
   const int page = a.block_table[(size_t)sq.s * a.max_pages + sq.tile];
   const bool mapped = page >= 0 && page < a.num_pages;
   const size_t out_page = (size_t)sq.s * a.pages + sq.tile;
-  if (threadIdx.x == 0) a.table[out_page] = mapped ? (int)out_page : -1;
+  if (threadIdx.x == 0 && blockIdx.y == 0) a.table[out_page] = mapped ? (int)out_page : -1;
   if (!mapped) return;
   constexpr int kVectors = kPageSize * D / 16;     // of 16 codes, per head
-  for (int i = threadIdx.x; i < 2 * a.hkv * kVectors; i += kUnpackThreads) {
-    const int w = i / kVectors, c = i - w * kVectors;
+  for (int i = blockIdx.y * kReadyThreads + threadIdx.x; i < 2 * a.hkv * kVectors; i += gridDim.y * kReadyThreads) {
+    const int w = i / kVectors, c = i % kVectors;
     const bool is_v = w >= a.hkv;
     const int h = is_v ? w - a.hkv : w;
     const size_t at = (size_t)page * a.hkv + h, to = out_page * a.hkv + h;
     const uint4 x = reinterpret_cast<const uint4*>((is_v ? a.v_pool : a.k_pool) + at * (kPageSize * D))[c];
-    const float f = q8::power(q8::scale_byte((is_v ? a.v_scale : a.k_scale)[at]));
+    const float f = power(scale_byte((is_v ? a.v_scale : a.k_scale)[at]));
     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
     uint32_t out[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t h[2];
-      q8::decode4(in[e], h[0], h[1]);
+      decode4(in[e], h[0], h[1]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float2 v = q8::halves(h[k]);
+        const float2 v = halves(h[k]);
         out[2 * e + k] = flash::pack_bf16x2(v.x * f, v.y * f);
       }
     }
@@ -1077,51 +1004,98 @@ __global__ void __launch_bounds__(kUnpackThreads) unpack_kernel(UnpackArgs a) {
   }
 }
 
-// Parts of the workspace, in bytes from its start: the wide form's, then chunk_kernel's.
+// Parts of the workspace, in bytes from its start: the wide form's, what ready_kernel makes, and what
+// divided items leave.
 struct Places {
-  size_t lens, table, k, v, rec, part, end;
+  size_t lens, table, k, v, q_parts, q_byte, k_parts, k_byte, v_half, v_byte, rec, part, end;
 };
-Places places(const ChunkQ8Plan& plan, int batch, int hkv, int d) {
+Places places(const ChunkQ8Plan& plan, int batch, int total, int hq, int hkv, int d) {
   Places l{};
+  size_t end = 0;
+  auto take = [&](size_t& at, size_t bytes) {
+    at = end;
+    end += packed::align256(bytes);
+  };
   if (plan.pages) {
-    l.lens = packed::align256(plan.wide.ws_bytes);
-    l.table = l.lens + packed::align256((size_t)batch * sizeof(int32_t));
-    l.k = l.table + packed::align256((size_t)batch * plan.pages * sizeof(int32_t));
-    l.v = l.k + (size_t)batch * plan.pages * hkv * kPageSize * d * 2;
-    l.rec = l.v + (l.v - l.k);
+    end = packed::align256(plan.wide.ws_bytes);
+    const size_t bytes = (size_t)batch * plan.pages * hkv * kPageSize * d * 2;
+    take(l.lens, (size_t)batch * sizeof(int32_t));
+    take(l.table, (size_t)batch * plan.pages * sizeof(int32_t));
+    take(l.k, bytes);
+    take(l.v, bytes);
   }
-  const size_t rows = plan.few ? plan.few : BQ;      // of a partial
-  const size_t note = plan.few ? sizeof(uint32_t) : sizeof(Record);
-  l.part = l.end = l.rec;
+  if (!plan.few) {
+    const size_t groups = (size_t)own_groups(batch, total) * hkv, rows = (size_t)total * hq;
+    take(l.q_parts, 2 * rows * d);
+    take(l.q_byte, rows);
+    take(l.k_parts, 2 * groups * kPageSize * d);
+    take(l.k_byte, groups);
+    take(l.v_half, groups * kPageSize * d * 2);
+    take(l.v_byte, groups);
+  }
   if (plan.can_split) {
-    l.part = l.rec + packed::align256(plan.ctas * note);
-    l.end = l.part + (size_t)plan.ctas * 2 * rows * ((size_t)d + 2) * sizeof(float);
+    const int rows = plan.few ? plan.few : BQ;       // of a partial
+    take(l.rec, plan.ctas * (plan.few ? sizeof(uint32_t) : sizeof(Record)));
+    take(l.part, (size_t)plan.ctas * 2 * rows * (d + 2) * sizeof(float));
   }
+  l.end = end;
   return l;
 }
 
 template <int D>
 cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaStream_t stream) {
   const PackedAttn& t = p.attn;
-  const Places l = places(plan, t.batch, t.hkv, D);
-  if (plan.pages) {
-    UnpackArgs u{t.cu, t.seq_lens, t.block_table, p.k_pool, p.v_pool, p.k_scale, p.v_scale,
-                 reinterpret_cast<uint16_t*>(ws + l.k), reinterpret_cast<uint16_t*>(ws + l.v),
-                 reinterpret_cast<int32_t*>(ws + l.lens), reinterpret_cast<int32_t*>(ws + l.table),
-                 t.status, t.num_pages, t.max_pages, plan.pages, plan.tpt, t.batch, t.total, t.hkv};
+  const Places l = places(plan, t.batch, t.total, t.hq, t.hkv, D);
+  cudaError_t e;
+  if (!plan.few) {
+    ReadyArgs u{};
+    u.q = t.q;
+    u.k = t.k;
+    u.v = t.v;
+    u.q_stride = t.q_stride;
+    u.k_stride = t.k_stride;
+    u.v_stride = t.v_stride;
+    u.cu = t.cu;
+    u.seq_lens = t.seq_lens;
+    u.block_table = t.block_table;
+    u.k_pool = p.k_pool;
+    u.v_pool = p.v_pool;
+    u.k_scale = p.k_scale;
+    u.v_scale = p.v_scale;
+    u.num_pages = t.num_pages;
+    u.max_pages = t.max_pages;
+    u.pages = plan.pages;
+    u.tpt = plan.tpt;
+    u.batch = t.batch;
+    u.total = t.total;
+    u.hq = t.hq;
+    u.hkv = t.hkv;
+    u.own_groups = own_groups(t.batch, t.total);
+    u.k_out = reinterpret_cast<uint16_t*>(ws + l.k);
+    u.v_out = reinterpret_cast<uint16_t*>(ws + l.v);
+    u.lens = reinterpret_cast<int32_t*>(ws + l.lens);
+    u.table = reinterpret_cast<int32_t*>(ws + l.table);
+    u.q_parts = ws + l.q_parts;
+    u.q_byte = ws + l.q_byte;
+    u.k_parts = ws + l.k_parts;
+    u.k_byte = ws + l.k_byte;
+    u.v_byte = ws + l.v_byte;
+    u.v_half = reinterpret_cast<uint16_t*>(ws + l.v_half);
+    const long long tiles = (long long)t.batch * plan.pages + u.own_groups;
     count_launches(1);
-    cudaError_t e = launch_early(unpack_kernel<D>, (unsigned)((long long)t.batch * plan.pages), kUnpackThreads, 0,
-                                 stream, u);
+    e = launch_early(ready_kernel<D>, dim3((unsigned)tiles, plan.pages ? 1 : (t.hq + 2 * t.hkv + 7) / 8), kReadyThreads, 0, stream, u);
     if (e != cudaSuccess) return e;
-    PackedAttn wide = t;
-    wide.k_pool = u.k_out;
-    wide.v_pool = u.v_out;
-    wide.seq_lens = u.lens;
-    wide.block_table = u.table;
-    wide.num_pages = t.batch * plan.pages;
-    wide.max_pages = plan.pages;
-    e = launch_packed_attn(wide, plan.wide, ws, stream);
-    if (e != cudaSuccess) return e;
+    if (plan.pages) {
+      PackedAttn wide = t;
+      wide.k_pool = u.k_out;
+      wide.v_pool = u.v_out;
+      wide.seq_lens = u.lens;
+      wide.block_table = u.table;
+      wide.num_pages = t.batch * plan.pages;
+      wide.max_pages = plan.pages;
+      e = launch_packed_attn(wide, plan.wide, ws, stream);
+      if (e != cudaSuccess) return e;
+    }
   }
   Args a{};
   a.q = t.q;
@@ -1152,6 +1126,12 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   a.o = t.o;
   a.item_work = plan.few ? kFewItemWork : kItemWork;
   if (plan.can_split && plan.few) a.arrived = reinterpret_cast<uint32_t*>(ws + l.rec);
+  if (!plan.few) {
+    a.q_byte = ws + l.q_byte;
+    a.own_k_byte = ws + l.k_byte;
+    a.own_v_byte = ws + l.v_byte;
+    a.own_groups = own_groups(t.batch, t.total);
+  }
   if (plan.can_split && !plan.few) a.rec = reinterpret_cast<Record*>(ws + l.rec);
   a.part = plan.can_split ? reinterpret_cast<float4*>(ws + l.part) : nullptr;
   a.status = t.status;
@@ -1171,18 +1151,19 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   static_assert(L::TOTAL + sizeof(Shared) <= 227 * 1024,
                 "layout fits shared memory");
   static std::atomic<int> attr[64];
-  cudaError_t e = set_smem_limit_once(chunk_kernel<D>, L::TOTAL, attr);
+  e = set_smem_limit_once(chunk_kernel<D>, L::TOTAL, attr);
   if (e != cudaSuccess) return e;
-  auto rows = [&](CUtensorMap* m, const uint16_t* base, int heads, long long stride, int elements,
-                  int box_heads, int box_rows) {
-    const uint64_t dims3[3] = {(uint64_t)D, (uint64_t)heads, (uint64_t)t.total};
-    const uint64_t pitch2[2] = {(uint64_t)D * 2, (uint64_t)stride * 2};
-    const uint32_t box3[3] = {(uint32_t)elements, (uint32_t)box_heads, (uint32_t)box_rows};
-    return encode_tmap_bf16_rows(m, base, 3, dims3, pitch2, box3);
-  };
-  if (!rows(&map_q, t.q, t.hq, t.q_stride, D / 2, plan.gp, plan.tpt) ||
-      !rows(&map_own_k, t.k, t.hkv, t.k_stride, D / 2, 1, BKV) ||
-      !rows(&map_own_v, t.v, t.hkv, t.v_stride, 64, 1, BKV))
+  // groups of 16 own rows as pages: a KV head is 16 rows of these maps too
+  const uint64_t own_rows = (uint64_t)a.own_groups * t.hkv * kPageSize;
+  const uint64_t dims_k[2] = {(uint64_t)D, 2 * own_rows}, dims_v[2] = {(uint64_t)D, own_rows};
+  const uint64_t pitch_v[1] = {(uint64_t)D * 2};
+  const uint32_t box_v[2] = {64, (uint32_t)kPageSize};
+  const uint64_t dims_q[3] = {(uint64_t)D, (uint64_t)t.hq, 2 * (uint64_t)t.total};
+  const uint64_t pitch_q[2] = {(uint64_t)D, (uint64_t)t.hq * D};
+  const uint32_t box_q[3] = {(uint32_t)D, (uint32_t)plan.gp, (uint32_t)plan.tpt};
+  if (!encode_tmap_u8(&map_q, ws + l.q_parts, 3, dims_q, pitch_q, box_q) ||
+      !encode_tmap_u8(&map_own_k, ws + l.k_parts, 2, dims_k, pitch, box) ||
+      !encode_tmap_bf16_rows(&map_own_v, reinterpret_cast<const uint16_t*>(ws + l.v_half), 2, dims_v, pitch_v, box_v))
     return cudaErrorInvalidValue;
   e = launch_early(chunk_kernel<D>, plan.ctas, kThreads, L::TOTAL, stream, map_k, map_v, map_q, map_own_k,
                    map_own_v, a);
@@ -1228,7 +1209,7 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
   const long long items = packed::max_tiles(batch, total, p.tpt) * (hq / p.gp);
   p.can_split = tiles >= 2 * kMinPart;
   p.ctas = (int)std::min<long long>(num_sms(), items * std::max(1, tiles / kMinPart));
-  p.ws_bytes = places(p, batch, hkv, d).end;
+  p.ws_bytes = places(p, batch, total, hq, hkv, d).end;
   return p;
 }
 

@@ -83,6 +83,9 @@ struct Args {
                                      // are left to the wide form (-1: none)
   float scale_log2;
   uint16_t* o;
+  // for chunk_q8.cu, what its first kernel makes: scale bytes of Q's rows, and of groups of 16 own rows
+  const uint8_t *q_byte, *own_k_byte, *own_v_byte;
+  int own_groups;
   struct Record* rec;                // [CTA], for merge_kernel
   uint32_t* arrived;                 // [CTA], parts of the item that it begins (chunk_q8_few.cu)
   float4* part;                      // [CTA][2], see kPartial
@@ -104,6 +107,10 @@ struct Row {
   MARS_DEV int tiles() const { return own() + packed::key_tiles(P); }
   MARS_DEV long long unit(const Args& a) const { return kUnit * tiles() + a.item_work; }
 };
+
+// Number of the first group of 16 of a sequence's own rows, among those of all sequences.
+MARS_DEV int own_group(int base, int s) { return base / kPageSize + s; }
+inline int own_groups(int batch, int total) { return total / kPageSize + batch; }
 
 MARS_DEV bool left_out(int skip_pages, int tpt, int n, int P) {
   return n > tpt && P / kPageSize + (P % kPageSize != 0) <= skip_pages;
