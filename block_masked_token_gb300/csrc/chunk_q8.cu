@@ -792,9 +792,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
     fence_barrier_init();
   }
+  // Every CTA of ready_kernel has let this one start, after its own wait: what came before that is
+  // there already, what it makes is after the wait here.
+  find_part(a, scan);
   wait_for_previous();
   let_next_start();
-  find_part(a, scan);
   if ((long long)blockIdx.x >= scan.ctas) {
     if (threadIdx.x == 0 && a.rec) a.rec[blockIdx.x] = Record{};
     return;

@@ -174,10 +174,15 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
   if (lane < kStages) mbar_init(&sh.full[warp][lane], 1);
   fence_barrier_init();
   if (threadIdx.x < 2) prefetch_tmap(threadIdx.x ? &tm_v : &tm_k);
-  wait_for_previous();
+  // clear_kernel has let this one start after its own wait: what came before that is there already, what
+  // it clears is after the wait where parts arrive.
+  if (!a.arrived) wait_for_previous();
   let_next_start();
   find_part(a, sh.scan);
-  if ((long long)blockIdx.x >= sh.scan.ctas) return;
+  if ((long long)blockIdx.x >= sh.scan.ctas) {
+    wait_for_previous();
+    return;
+  }
   if (threadIdx.x == 0) sh.place = first_place(a, sh.scan);
   uint64_t* full = sh.full[warp];
   bool ok = true;
@@ -576,6 +581,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         }
       }
       if (p.slot >= 0) {                             // whoever comes last joins the item's parts
+        wait_for_previous();
         __syncthreads();
         if (threadIdx.x == 0) sh.joins = arrive(&a.arrived[sh.first]) == (uint32_t)sh.pieces - 1;
         __syncthreads();
@@ -590,6 +596,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
     }
     __syncthreads();                                 // the list is free again
   }
+  wait_for_previous();
   if (!ok) {                                         // a wait gave up: what is in flight ends first
     for (; used != issued; ++used) wait_bounded(&full[used % kStages], (used / kStages) & 1);
     flags |= MARS_ST_TIMEOUT;
@@ -600,8 +607,8 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
 
 // No part of an item has arrived yet.
 __global__ void clear_kernel(uint32_t* arrived, int n) {
-  sm100::let_next_start();
   sm100::wait_for_previous();
+  sm100::let_next_start();
   for (int i = threadIdx.x; i < n; i += blockDim.x) arrived[i] = 0;
 }
 
