@@ -4,35 +4,45 @@
 //   P = seq_lens[s] cached keys, each its code times its page's scale, and the sequence's own keys
 //   0 .. i in bf16.
 //
+// Three forms, by rows per sequence (plan_chunk_q8): chunk_q8_few.cu for the fewest, chunk_kernel here,
+// and the wide form for many (packed_attn.cu over pages that ready_kernel unpacks).
+//
 // chunk_kernel works on the codes. A persistent CTA per SM takes an equal part of all key tiles of
-// all items; an item is a tile of up to 128 (token, query head) rows that share a KV head, as in
-// packed_attn.cu, with the 128-key tiles that its rows see: the sequence's own keys first, then the
-// cached ones.
+// all items (chunk_q8.cuh); an item is a tile of up to 128 (token, query head) rows that share a KV
+// head, as in packed_attn.cu, with the 128-key tiles that its rows see: the sequence's own keys
+// first, then the cached ones.
 //   - S = Q K^T takes K's codes as they are, in 8 bits. A row of Q, over a power of two that brings
 //     its largest magnitude into [128, 256), is the sum of two e4m3 numbers (bf16 has 8 significant
 //     bits, e4m3 4): exactly down to 2^-10 of that magnitude, to 2^-17 of it below. Own keys are two
-//     such numbers too, over a power of two per 16 tokens.
+//     such numbers too, over a power of two per 16 tokens. ready_kernel, before this one, makes both.
 //   - Scores get the row's power and the K scale of their 16 keys as one factor in 32 bits.
-//   - O += P V runs on f16, which holds every code exactly (bf16 would too, but takes five
-//     instructions for what one conversion does), and own values over a power of two per 16 tokens.
-//     With V = 2^e c, a weight's power goes the other way: P' = 2^(s + e - m') is the A operand,
-//     m' the running maximum of s + e instead of s, and the row sum takes P' 2^-e. P' is then as
-//     large as what it contributes, whatever the pages' scales are; 2^7 P' is stored, so that small
-//     ones keep their bits.
+//   - O += P V runs on f16 (chunk_q8.cuh says over what), and own values over a power of two per 16
+//     tokens.
 // Shared memory moves 128 bytes per cycle: the copies of a tile's codes take 256 cycles, S 512, the
 // conversion of V 384, P V 256. (With K converted to f16 as well, 1,800 cycles per tile.)
 //
-// Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
-// (infos); warp 1 copies K; warps 12..19 copy a page of V each into a ring of their own and turn
-// it into 16 rows of a swizzled f16 tile, zero where no key may be read; warps 2 and 3 issue
-// S and O += P' V; warps 4..7 run the softmax of even tiles, 8..11 that of odd ones, a thread per
-// row, each with an S buffer, an O, a maximum and a sum of its own, which are joined at an item's end.
-// (With half of every tile's keys each, the exchange of maxima and the waits took longer than the
-// softmax.) What a warp runs per tile is kept short: the code of all roles has to stay in some 32 KB
-// of instruction cache. When it did not, a tile took 5,000 cycles; and what runs once per item
-// costs some 40 cycles per instruction.
+// What bounds it: a tile takes 2,900 cycles, twice what its copies take at the rate of the memory. S of
+// tile t + 2 waits for P V of tile t, whose P lies in its buffer, so that the chain S (1,000 with its
+// waits), softmax (2,300), P V (700), waits (1,900) takes 5,800 cycles for each of the two buffers;
+// TMEM has no room for a third beside two O of 128 columns.
 //
-// A cut inside an item leaves partials (m', l, O) that merge_kernel joins in the order of the keys.
+// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 1,024 .. 8,192 keys): 270 us,
+// 0.37 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 41 us, of which the three
+// launches and the start and end of every CTA are about 25.
+//
+// Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
+// (infos); warp 1 copies K and Q; warps 12..15 copy V of even tiles, 16..19 of odd ones, two pages each
+// into a ring of their own, and turn them into 32 rows of a swizzled f16 tile, zero where no key may be
+// read; warps 2 and 3 issue S and O += P' V; warps 4..7 run the softmax of even tiles, 8..11 that of odd
+// ones, a thread per row, each with an S buffer, an O, a maximum and a sum of its own, which are joined
+// at an item's end. (With half of every tile's keys each, the exchange of maxima and the waits took
+// longer than the softmax.) What a warp runs per tile is kept short: the code of all roles has to stay
+// in some 32 KB of instruction cache. When it did not, a tile took 5,000 cycles; and what runs once per
+// item costs some 40 cycles per instruction. (Hence ready_kernel; with Q and own rows turned into
+// operands here, an item's start took 17,000 cycles instead of 9,000.)
+//
+// merge_kernel joins the parts of divided items. (Joined by the warps that come last, as
+// chunk_q8_few.cu does it, blocks of 8 took 44 us: more of that code.)
 #include <algorithm>
 #include <climits>
 
@@ -134,8 +144,7 @@ struct Pipe {
   uint32_t tmem;
 
   // Waits of one thread, and of a whole warp (by all lanes: behind a test of the lane a wait that is
-  // over takes 250 cycles instead of 100). Where one gives up, the kernel's end sets the status. These instructions are at thirty places of code that
-  // has to stay in the instruction cache.
+  // over takes 250 cycles instead of 100). Where one gives up, the kernel's end sets the status.
   MARS_DEV bool wait(uint64_t* b, uint32_t parity) const {
     const bool ok = wait_bounded(b, parity);
     if (!ok) *(volatile int*)&bar.abort = 1;
@@ -1085,7 +1094,9 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
     u.v_half = reinterpret_cast<uint16_t*>(ws + l.v_half);
     const long long tiles = (long long)t.batch * plan.pages + u.own_groups;
     count_launches(1);
-    e = launch_early(ready_kernel<D>, dim3((unsigned)tiles, plan.pages ? 1 : (t.hq + 2 * t.hkv + 7) / 8), kReadyThreads, 0, stream, u);
+    // (where there are many tiles, one CTA for each: mixed rows 148 us with five, 133 with one)
+    const unsigned y = plan.pages ? 1 : (t.hq + 2 * t.hkv + 7) / 8;
+    e = launch_early(ready_kernel<D>, dim3((unsigned)tiles, y), kReadyThreads, 0, stream, u);
     if (e != cudaSuccess) return e;
     if (plan.pages) {
       PackedAttn wide = t;
@@ -1201,11 +1212,14 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
     p.gp = group;
     p.tpt = p.few / group;
   }
-  // The wide form where packed_attn.cu would take pairs of row tiles (plan_packed), unless its pages
-  // could not be counted or took more than 4 GB.
+  // The wide form where packed_attn.cu would take pairs of row tiles (plan_packed) and sequences have more
+  // than four row tiles on average, unless its pages could not be counted or took more than 4 GB. 28
+  // query over 4 KV heads of 128, 2,048 cached keys, chunk_kernel against the wide form: 20 rows of 32
+  // sequences (2 tiles) 78 and 107 us, 50 of 16 (3) 65 and 83, 64 of 32 (4) 130 and 139, 200 of 8 (12)
+  // 101 and 93, 1,400 of 1 (78) 110 and 80; 14 over 2 of 64: 64 of 32 61 and 65.
   const long long pages = std::max(1, max_len / kPageSize + (max_len % kPageSize != 0));
   const long long rows = pages * batch * hkv * kPageSize;
-  if (p.wide.pair && !p.few && rows <= INT_MAX && rows * d * 4 <= 1LL << 32) p.pages = (int)pages;
+  if (p.wide.pair && !p.few && total > 4LL * batch * p.tpt && rows <= INT_MAX && rows * d * 4 <= 1LL << 32) p.pages = (int)pages;
   // CTAs: as many as the items and their parts can keep busy, by the hint
   const int tiles = packed::key_tiles(max_len) + 1;
   const long long items = packed::max_tiles(batch, total, p.tpt) * (hq / p.gp);
