@@ -964,12 +964,18 @@ __global__ void __launch_bounds__(kReadyThreads) ready_kernel(ReadyArgs a) {
   const int skip = a.pages ? a.pages : -1;
   auto cut = [&](int len) { return (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize)); };
   auto tiles = [](int rows) { return rows / kPageSize + (rows % kPageSize != 0); };
-  bool bad;
-  const packed::Seq sq = packed::find_tile_by(
-      a.cu, a.batch, a.total, (long long)blockIdx.x, bad, a.seq_lens, [&](int, int n, int len) {
-        const int P = cut(len);
-        return max(left_out(skip, a.tpt, n, P) ? tiles(P) : tiles(n), a.pages ? 1 : 0);
-      });
+  __shared__ packed::Seq found;
+  if (threadIdx.x < 32) {                            // (by every warp it was a third of all instructions)
+    bool bad;
+    const packed::Seq sq = packed::find_tile_by(
+        a.cu, a.batch, a.total, (long long)blockIdx.x, bad, a.seq_lens, [&](int, int n, int len) {
+          const int P = cut(len);
+          return max(left_out(skip, a.tpt, n, P) ? tiles(P) : tiles(n), a.pages ? 1 : 0);
+        });
+    if (threadIdx.x == 0) found = sq;
+  }
+  __syncthreads();
+  const packed::Seq sq = found;
   if (sq.s < 0) return;
   const int P = cut(sq.len);
   const bool wide = left_out(skip, a.tpt, sq.n, P);

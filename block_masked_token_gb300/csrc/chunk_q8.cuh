@@ -282,20 +282,20 @@ struct Window {
 MARS_DEV float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 // Joins the parts of a divided item, the k-th of which is at part(k): four columns of a row at a time.
-template <int D, int kRows, class Part>
+template <int D, int kRows, int kAtOnce, class Part>
 MARS_DEV void join(const Args& a, Part part, int parts, int rows, size_t tok, int h0, int from, int step) {
   for (int i = from; i < rows * (D / 4); i += step) {
     const int row = i % rows, c = i / rows;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    // four at a time: a trip to the L2 cache each
+    // kAtOnce at a time: a trip to the L2 cache each
 #pragma unroll 1
-    for (int k0 = 0; k0 < parts; k0 += 4) {
-      float2 ml[4];
-      float4 v[4];
+    for (int k0 = 0; k0 < parts; k0 += kAtOnce) {
+      float2 ml[kAtOnce];
+      float4 v[kAtOnce];
       float top = m;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAtOnce; ++k) {
         ml[k] = make_float2(-INFINITY, kNoKeys);
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k0 + k >= parts) continue;
@@ -303,13 +303,13 @@ MARS_DEV void join(const Args& a, Part part, int parts, int rows, size_t tok, in
         v[k] = __ldcg(part(k0 + k) + c * kRows + row);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+      for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
       const float w0 = m > -INFINITY ? exp2f(m - top) : 0.f;        // (+infinity gives NaN)
       m = top;
       l *= w0;
       o = make_float4(o.x * w0, o.y * w0, o.z * w0, o.w * w0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAtOnce; ++k) {
         if (ml[k].y == kNoKeys) continue;
         const float w = ml[k].x > -INFINITY ? exp2f(ml[k].x - top) : 0.f;
         l = fmaf(ml[k].y, w, l);
@@ -325,7 +325,7 @@ MARS_DEV void join(const Args& a, Part part, int parts, int rows, size_t tok, in
 // Joins the parts of divided items. Block (x, y): the item that CTA x begins and does not end, a
 // thread per (row, four columns).
 template <int D, int kRows>
-__global__ void __launch_bounds__(256) merge_kernel(Args a, int ctas) {
+__global__ void __launch_bounds__(256, 6) merge_kernel(Args a, int ctas) {
   constexpr int PART = kPartial<D, kRows>;
   sm100::wait_for_previous();
   const int x = blockIdx.x, lane = threadIdx.x & 31;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(256) merge_kernel(Args a, int ctas) {
   }
   const float4* first = a.part + ((size_t)x * 2 + 1) * PART;
   auto part = [&](int k) { return k == 0 ? first : a.part + (size_t)(x + k) * 2 * PART; };
-  join<D, kRows>(a, part, parts, rec.tokens * a.gp, (size_t)rec.base + rec.tok0, rec.h0,
+  join<D, kRows, 2>(a, part, parts, rec.tokens * a.gp, (size_t)rec.base + rec.tok0, rec.h0,
                  blockIdx.y * 256 + threadIdx.x, gridDim.y * 256);
 }
 

@@ -597,7 +597,7 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
           constexpr int PART = kPartial<D, kRows>;
           const float4* first = a.part + (size_t)sh.first * 2 * PART;
           auto at = [&](int k) { return first + (k == 0 ? PART : (size_t)k * 2 * PART); };
-          join<D, kRows>(a, at, sh.pieces, p.tokens * a.gp, (size_t)p.base + p.tok0, p.h0, threadIdx.x,
+          join<D, kRows, 4>(a, at, sh.pieces, p.tokens * a.gp, (size_t)p.base + p.tok0, p.h0, threadIdx.x,
                          Sh::kThreads);
         }
       }

@@ -9,10 +9,10 @@
 // loads the rows, finds their largest magnitude and writes their codes, so that each element is
 // read once. 2 bytes read and 1 written per element.
 //
-// Prompts of 10,590 rows of 4 heads of 128 (28 MB): 9.5 us, 0.43 of the copy bandwidth: the launch (2 us)
-// and the chain of boundary, length, page and row reads (some 4) come before the first byte; it was
-// 12.2 before it started while the kernel before it ended. A few rows: 6.5 us, the host's and the
-// launch's.
+// Prompts of 9,050 rows of 4 heads of 128 (28 MB): 8.3 us, 0.49 of the copy bandwidth: the launch (2 us)
+// and the chain of boundary, length, page and row reads (some 4) come before the first byte. It was
+// 9.5 with the old codes read ahead of the scales (128 registers, two waves of CTAs; now one), 12.2
+// when it did not start while the kernel before it ended. A few rows: 6.5 us, the host's and the launch's.
 #include <climits>
 
 #include "cache_q8.cuh"
@@ -43,27 +43,24 @@ MARS_DEV void append_head(const uint16_t* __restrict__ rows, long long stride, u
   const int lane = threadIdx.x & 31, c = lane % kChunks, r0 = lane / kChunks;
   // slots [held, end) get rows[0 ..], slots below held keep their tokens
   uint4 x[kIts];
-  uint2 old[kIts];
   // lane 0 alone reads and writes the scale
   int byte0 = lane == 0 && held > 0 ? q8::scale_byte(*scale) : q8::kLeast;
 #pragma unroll
   for (int i = 0; i < kIts; ++i) {
     const int slot = r0 + i * kStep;
     x[i] = make_uint4(0, 0, 0, 0);
-    old[i] = make_uint2(0, 0);
     if (slot >= held && slot < end)
       x[i] = *reinterpret_cast<const uint4*>(rows + (long long)(slot - held) * stride + c * 8);
-    else if (slot < held)
-      old[i] = *reinterpret_cast<const uint2*>(codes + slot * D + c * 8);
   }
-  uint32_t top = 0;                              // largest finite magnitude, in each half
+  uint32_t top = 0, endless = 0;                 // largest finite magnitude, in each half; infinities, NaN
 #pragma unroll
   for (int i = 0; i < kIts; ++i) {
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t m = w[e] & 0x7fff7fffu;
-      top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+      const uint32_t m = w[e] & 0x7fff7fffu, no = __vcmpgeu2(m, 0x7f807f80u);
+      top = __vmaxu2(top, m & ~no);
+      endless |= no;
     }
   }
   byte0 = __shfl_sync(0xffffffffu, byte0, 0);
@@ -78,11 +75,15 @@ MARS_DEV void append_head(const uint16_t* __restrict__ rows, long long stride, u
     float e[8];
     if (slot >= held && slot < end) {
       unpack8(x[i], e);
-      // an infinity becomes NaN, which stays; a finite value's second product adds nothing
+      if (endless) {                             // an infinity becomes NaN, which stays
 #pragma unroll
-      for (int k = 0; k < 8; ++k) e[k] = fmaf(e[k], 0.f, e[k] * f);
+        for (int k = 0; k < 8; ++k) e[k] = fmaf(e[k], 0.f, e[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] *= f;
     } else if (slot < held && byte > byte0) {
-      const uint32_t w[2] = {old[i].x, old[i].y};
+      const uint2 old = *reinterpret_cast<const uint2*>(codes + slot * D + c * 8);
+      const uint32_t w[2] = {old.x, old.y};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         uint32_t lo, hi;
@@ -103,7 +104,7 @@ MARS_DEV void append_head(const uint16_t* __restrict__ rows, long long stride, u
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(AppendQ8 a) {
+__global__ void __launch_bounds__(kThreads, 4) kv_append_q8_kernel(AppendQ8 a) {
   __shared__ int s_bad;                  // first logical page that is not mapped
   bool bad;
   sm100::wait_for_previous();
