@@ -26,8 +26,8 @@
 // waits), softmax (2,300), P V (700), waits (1,900) takes 5,800 cycles for each of the two buffers;
 // TMEM has no room for a third beside two O of 128 columns.
 //
-// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 1,024 .. 8,192 keys): 270 us,
-// 0.37 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 41 us, of which the three
+// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 2,048 .. 8,192 keys): 269 us,
+// 0.41 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 41 us, of which the three
 // launches and the start and end of every CTA are about 25.
 //
 // Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
@@ -114,7 +114,7 @@ struct alignas(1024) Shared {
     float exchange[2][BQ];           // [even or odd tiles][row], at the end of items
   };
 };
-static_assert(sizeof(Shared) <= 3072, "with the tiles, the shared memory of a CTA");
+static_assert(sizeof(Shared) <= 3 * 1024, "with the tiles, the shared memory of a CTA");
 
 template <int D>
 struct Layout {

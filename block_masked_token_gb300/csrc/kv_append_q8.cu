@@ -9,7 +9,7 @@
 // loads the rows, finds their largest magnitude and writes their codes, so that each element is
 // read once. 2 bytes read and 1 written per element.
 //
-// Prompts of 9,050 rows of 4 heads of 128 (28 MB): 8.3 us, 0.49 of the copy bandwidth: the launch (2 us)
+// Prompts of 9,055 rows of 4 heads of 128 (28 MB): 8.3 us, 0.49 of the copy bandwidth: the launch (2 us)
 // and the chain of boundary, length, page and row reads (some 4) come before the first byte. It was
 // 9.5 with the old codes read ahead of the scales (128 registers, two waves of CTAs; now one), 12.2
 // when it did not start while the kernel before it ended. A few rows: 6.5 us, the host's and the launch's.

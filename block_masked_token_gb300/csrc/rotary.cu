@@ -9,7 +9,7 @@
 // position, modulo 1 by itself, is exact up to 2^-52 of a turn per position, and sincospi gets the
 // upper 32 bits of it.
 //
-// Prompts of 12,790 rows of 28 + 4 heads of 128 (164 MB moved): 31.1 us, 0.82 of the copy bandwidth; the
+// Prompts of 10,586 rows of 28 + 4 heads of 128 (173 MB moved): 31.1 us, 0.82 of the copy bandwidth; the
 // gradient over 8,191 long rows 24.7 us, 0.80. With 8 rows per CTA 31.2 and 27.6 (fewer CTAs to even out
 // at the end), with 16 32.7 and 26.9, with 4 and 128 threads 30.5 and 26.0.
 #include "common.cuh"
