@@ -1182,7 +1182,7 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
   const uint32_t box_q[3] = {(uint32_t)D, (uint32_t)plan.gp, (uint32_t)plan.tpt};
   if (!encode_tmap_u8(&map_q, ws + l.q_parts, 3, dims_q, pitch_q, box_q) ||
       !encode_tmap_u8(&map_own_k, ws + l.k_parts, 2, dims_k, pitch, box) ||
-      !encode_tmap_bf16_rows(&map_own_v, reinterpret_cast<const uint16_t*>(ws + l.v_half), 2, dims_v, pitch_v, box_v))
+      !encode_tmap_bf16(&map_own_v, ws + l.v_half, 2, dims_v, pitch_v, box_v))
     return cudaErrorInvalidValue;
   e = launch_early(chunk_kernel<D>, plan.ctas, kThreads, L::TOTAL, stream, map_k, map_v, map_q, map_own_k,
                    map_own_v, a);

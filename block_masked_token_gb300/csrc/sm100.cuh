@@ -496,9 +496,6 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64
                       const uint64_t* strides_bytes, const uint32_t* box);
 bool encode_tmap_f32(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                      const uint64_t* strides_bytes, const uint32_t* box);
-// bf16 in boxes whose rows are box[0] = 32 or 64 elements, swizzled over as many bytes.
-bool encode_tmap_bf16_rows(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
-                           const uint64_t* strides_bytes, const uint32_t* box);
 // Bytes, in boxes whose rows are box[0] bytes (64 or 128), swizzled over as many.
 bool encode_tmap_u8(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                     const uint64_t* strides_bytes, const uint32_t* box);
