@@ -607,68 +607,78 @@ MARS_DEV void softmax(const Pipe& p) {
               if (e >= seen) r[16 * g + e] = 0xff800000u;
           }
         }
-        // the largest s + e
-        float top = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          float x[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[16 * g + e]);
-          const float y = flash::max3f(flash::max3f(x[0], x[1], x[2]), flash::max3f(x[3], x[4], x[5]),
-                                       flash::max3f(x[6], x[7], x[8]));
-          const float z = flash::max3f(flash::max3f(x[9], x[10], x[11]), flash::max3f(x[12], x[13], x[14]), x[15]);
-          top = fmaxf(top, fmaf(fmaxf(y, z), k_factor(factor, kb >> (8 * g)), v_exponent(vb >> (8 * g))));
-        }
-        // lazy rescale (flash_tc.cuh) of O (the PV of its last tile came before S of this one; an
-        // item's first two tiles find none), and of the other half's P'
-        const bool raise = top > m + flash::kRescaleLog2;
-        if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
-          const float alpha = raise && m != -INFINITY ? flash::ex2_approx(m - top) : 1.f;
-          l *= alpha;
-          if (!(flags & (kFirst | kSecond))) {
+        float sum, part;                             // of the P', and of P' 2^-e
 #pragma unroll 1
-            for (int c = odd * D; c < odd * D + D; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(o_addr + c, o);
-              tmem_ld_wait();
+        for (bool again = false;; again = true) {
+          const float shift = kLift - (m == -INFINITY ? 0.f : m);
+          sum = part = 0.f;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st16(o_addr + c, o);
+          for (int g = 0; g < kGroups; ++g) {
+            const float mul = k_factor(factor, kb >> (8 * g)), add = v_exponent(vb >> (8 * g)) + shift;
+            const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), mul2, add2);
+              const float2 w = make_float2(flash::ex2_approx(x.x), flash::ex2_approx(x.y));
+              packed[e / 2] = q8::pack_f16x2(w.x, w.y);
+              acc = __fadd2_rn(acc, w);
             }
+            sum += acc.x + acc.y;
+            // 2^-e; where there are no keys, the bits of some finite number, times 0
+            part = fmaf(acc.x + acc.y, q8::inverse_power((vb >> (8 * g)) & 255), part);
           }
-          tmem_st_wait();
-          if (h == 0) {
-#pragma unroll 1
-            for (int c = kKeys / 2; c < kKeys; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(s_addr + L::P_OFF + c, o);
-              tmem_ld_wait();
+          // A maximum is only looked for where there is none as yet, or where it has been outgrown by so
+          // much that f16 might end: the P' of a half are 2^15 together at most. (Looked for in every
+          // half it took a fifth of the softmax.)
+          if (again || !__any_sync(0xffffffffu, has && (m == -INFINITY || sum > 32768.f))) break;
+          float top = -INFINITY;                     // the largest s + e
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float2 w = q8::halves(o[e]);
-                o[e] = q8::pack_f16x2(w.x * alpha, w.y * alpha);
+          for (int g = 0; g < kGroups; ++g) {
+            float x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[16 * g + e]);
+            const float y = flash::max3f(flash::max3f(x[0], x[1], x[2]), flash::max3f(x[3], x[4], x[5]),
+                                         flash::max3f(x[6], x[7], x[8]));
+            const float z = flash::max3f(flash::max3f(x[9], x[10], x[11]), flash::max3f(x[12], x[13], x[14]), x[15]);
+            top = fmaxf(top, fmaf(fmaxf(y, z), k_factor(factor, kb >> (8 * g)), v_exponent(vb >> (8 * g))));
+          }
+          // O (the PV of its last tile came before S of this one; an item's first two tiles find none)
+          // and the other half's P' go over the new maximum
+          const bool raise = top > m;
+          if (__any_sync(0xffffffffu, raise && m != -INFINITY)) {
+            const float alpha = raise && m != -INFINITY ? flash::ex2_approx(m - top) : 1.f;
+            l *= alpha;
+            if (!(flags & (kFirst | kSecond))) {
+#pragma unroll 1
+              for (int c = odd * D; c < odd * D + D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_addr + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st16(o_addr + c, o);
               }
-              tmem_st16(s_addr + L::P_OFF + c, o);
+            }
+            tmem_st_wait();
+            if (h == 0) {
+#pragma unroll 1
+              for (int c = kKeys / 2; c < kKeys; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(s_addr + L::P_OFF + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const float2 w = q8::halves(o[e]);
+                  o[e] = q8::pack_f16x2(w.x * alpha, w.y * alpha);
+                }
+                tmem_st16(s_addr + L::P_OFF + c, o);
+              }
             }
           }
+          if (raise) m = top;
         }
-        if (raise) m = top;
-        const float shift = kLift - (m == -INFINITY ? 0.f : m);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const float mul = k_factor(factor, kb >> (8 * g)), add = v_exponent(vb >> (8 * g)) + shift;
-          const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
-          float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), mul2, add2);
-            const float2 w = make_float2(flash::ex2_approx(x.x), flash::ex2_approx(x.y));
-            packed[e / 2] = q8::pack_f16x2(w.x, w.y);
-            acc = __fadd2_rn(acc, w);
-          }
-          // 2^-e; where there are no keys, the bits of some finite number, times 0
-          l = fmaf(acc.x + acc.y, q8::inverse_power((vb >> (8 * g)) & 255), l);
-        }
+        l += part;
         tmem_st32(s_addr + L::P_OFF + h * (kKeys / 2), packed);
       }
       tmem_st_wait();

@@ -621,6 +621,54 @@ def test_a_serving_step(heads):
     assert lens.tolist() == [190 + 21, 27 + 21, 19 + 21]
 
 
+@pytest.mark.parametrize("lens, old, heads", [([1, 2], [3000, 90], (7, 1, 128)), ([20, 3], [400, 900], (28, 4, 128))],
+                         ids=["few", "more"])
+def test_a_captured_step_over_two_streams(lens, old, heads):
+    """q is turned on one stream and k on another, each by a call that writes both; attention waits for the two.
+    Every kernel starts early behind the ones before it, so that a missing wait would read what is not there yet."""
+    x = make8(lens, *heads, old, seed=70)
+    y = cuda(x)
+    freq, _ = packed.rotary_frequencies(heads[2])
+    freq, cu, n = freq.cuda(), y["cu"], y["q"].shape[0]
+    hint = hint_of(y)
+    ws = workspace(packed.OP_ATTN_CHUNK_Q8, len(lens), n, *heads, hint)
+    bufs = [torch.zeros_like(t.contiguous()) for t in (y["q"], y["k"], y["q"], y["k"], y["q"])]
+    q_in, k_in = y["q"].clone(), y["k"].clone()
+    other = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            packed.mars_rotary(q_in, k_in, cu, freq, bufs[2], bufs[3], y["old"])
+        packed.mars_rotary(q_in, k_in, cu, freq, bufs[0], bufs[1], y["old"])
+        here.wait_stream(other)
+        packed.mars_attn_chunk_q8(bufs[0], bufs[3], y["v"], cu, y["k_pool"], y["v_pool"], y["k_scale"], y["v_scale"],
+                                  y["table"], y["old"], hint, bufs[4], ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    rng = torch.Generator(device="cuda").manual_seed(5)
+    for _ in range(4):
+        for t in (q_in, k_in):
+            t.copy_(torch.randn(t.shape, generator=rng, device="cuda"))
+        for b in bufs:
+            b.fill_(7.0)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [b.clone() for b in bufs]
+        for b in bufs:
+            b.fill_(3.0)
+        step()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, bufs))
+        check_chunk8({**x, "q": bufs[0].cpu(), "k": bufs[3].cpu()}, got[4])
+
+
 def test_rows_and_pools_whose_offsets_pass_32_bits():
     """A pool of 5.4 GB whose last pages are in use, and rows of a tensor of 4.6 GB."""
     hq, hkv, d = 8, 8, 128
