@@ -21,13 +21,13 @@
 // Shared memory moves 128 bytes per cycle: the copies of a tile's codes take 256 cycles, S 512, the
 // conversion of V 384, P V 256. (With K converted to f16 as well, 1,800 cycles per tile.)
 //
-// What bounds it: a tile takes 2,900 cycles, twice what its copies take at the rate of the memory. S of
-// tile t + 2 waits for P V of tile t, whose P lies in its buffer, so that the chain S (1,000 with its
-// waits), softmax (2,300), P V (700), waits (1,900) takes 5,800 cycles for each of the two buffers;
-// TMEM has no room for a third beside two O of 128 columns.
+// What bounds it: a tile takes 2,500 cycles, 1.7 times what its copies take at the rate of the memory. S
+// of tile t + 2 waits for P V of tile t, whose P lies in its buffer, so that the chain S (1,000 with its
+// waits), softmax (2,300), P V (700), waits (1,000) takes 5,000 cycles for each of the two buffers; TMEM
+// has no room for a third beside two O of 128 columns.
 //
-// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 2,048 .. 8,192 keys): 269 us,
-// 0.41 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 41 us, of which the three
+// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 2,048 .. 8,192 keys): 238 us,
+// 0.47 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 38 us, of which the three
 // launches and the start and end of every CTA are about 25.
 //
 // Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
@@ -381,7 +381,7 @@ MARS_DEV void convert_raw(const uint8_t* raw, uint8_t* tile, int r0, int valid) 
   // lanes of the second region store their chunks in the other order: the eight lanes of a row
   // then hit eight different chunks
   const int up = D == 128 ? c >> 2 : 0;
-#pragma unroll
+#pragma unroll 2
   for (int i = 0; i < kIts; ++i) {
     const int r = lane / kLanes + i * kStep;
     uint4 x = make_uint4(0, 0, 0, 0);
@@ -501,7 +501,7 @@ MARS_DEV void issue_s(const Pipe& p) {
       if (!(ok = p.wait(&p.bar.k_full[st], (slots / kSlots) & 1))) break;
       tc_fence_after();
       const uint64_t kd = L::code_desc(p.smem + L::OFF_K + st * L::RAW);
-#pragma unroll
+#pragma unroll 2
       for (int k = 0; k < 2 * (D / 32); ++k) {
         const uint32_t off = k % (D / 32) * 32;
         mma_f8_ss(p.tmem + L::TM_S + sb * BKV, sdesc_advance(qd, off + k / (D / 32) * L::RAW),
