@@ -1229,13 +1229,14 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
     p.tpt = p.few / group;
   }
   // The wide form where packed_attn.cu would take pairs of row tiles (plan_packed) and sequences have more
-  // than four row tiles on average, unless its pages could not be counted or took more than 4 GB. 28
-  // query over 4 KV heads of 128, 2,048 cached keys, chunk_kernel against the wide form: 20 rows of 32
-  // sequences (2 tiles) 78 and 107 us, 50 of 16 (3) 65 and 83, 64 of 32 (4) 130 and 139, 200 of 8 (12)
-  // 101 and 93, 1,400 of 1 (78) 110 and 80; 14 over 2 of 64: 64 of 32 61 and 65.
+  // than ten row tiles on average, unless its pages could not be counted or took more than 4 GB. 28
+  // query over 4 KV heads of 128, 2,048 cached keys, chunk_kernel against the wide form: 50 rows of 16
+  // sequences (3 tiles) 57 and 83 us, 120 of 32 (7) 181 and 190, 200 of 8 (11) 94 and 94, 300 of 32 (17)
+  // 434 and 341, 1,400 of 1 (78) 102 and 80; 14 over 2 of 64: 120 of 32 (7) 79 and 92, 300 of 32 (17)
+  // 179 and 155.
   const long long pages = std::max(1, max_len / kPageSize + (max_len % kPageSize != 0));
   const long long rows = pages * batch * hkv * kPageSize;
-  if (p.wide.pair && !p.few && total > 4LL * batch * p.tpt && rows <= INT_MAX && rows * d * 4 <= 1LL << 32) p.pages = (int)pages;
+  if (p.wide.pair && !p.few && total > 10LL * batch * p.tpt && rows <= INT_MAX && rows * d * 4 <= 1LL << 32) p.pages = (int)pages;
   // CTAs: as many as the items and their parts can keep busy, by the hint
   const int tiles = packed::key_tiles(max_len) + 1;
   const long long items = packed::max_tiles(batch, total, p.tpt) * (hq / p.gp);
