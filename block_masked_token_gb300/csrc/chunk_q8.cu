@@ -26,9 +26,9 @@
 // waits), softmax (2,300), P V (700), waits (1,000) takes 5,000 cycles for each of the two buffers; TMEM
 // has no room for a third beside two O of 128 columns.
 //
-// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 2,048 .. 8,192 keys): 238 us,
-// 0.47 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 38 us, of which the three
-// launches and the start and end of every CTA are about 25.
+// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 2,048 .. 8,192 keys): 241 us,
+// 0.46 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 35 us, of which the three
+// launches and the start and end of every CTA are about 22.
 //
 // Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
 // (infos); warp 1 copies K and Q; warps 12..15 copy V of even tiles, 16..19 of odd ones, two pages each
