@@ -1097,7 +1097,7 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
     u.total = t.total;
     u.hq = t.hq;
     u.hkv = t.hkv;
-    u.own_groups = own_groups(t.batch, t.total);
+    u.own_groups = (int)own_groups(t.batch, t.total);
     u.k_out = reinterpret_cast<uint16_t*>(ws + l.k);
     u.v_out = reinterpret_cast<uint16_t*>(ws + l.v);
     u.lens = reinterpret_cast<int32_t*>(ws + l.lens);
@@ -1108,11 +1108,10 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
     u.k_byte = ws + l.k_byte;
     u.v_byte = ws + l.v_byte;
     u.v_half = reinterpret_cast<uint16_t*>(ws + l.v_half);
-    const long long tiles = (long long)t.batch * plan.pages + u.own_groups;
     count_launches(1);
     // (where there are many tiles, one CTA for each: mixed rows 148 us with five, 133 with one)
     const unsigned y = plan.pages ? 1 : (t.hq + 2 * t.hkv + 7) / 8;
-    e = launch_early(ready_kernel<D>, dim3((unsigned)tiles, y), kReadyThreads, 0, stream, u);
+    e = launch_early(ready_kernel<D>, dim3((unsigned)plan.tiles, y), kReadyThreads, 0, stream, u);
     if (e != cudaSuccess) return e;
     if (plan.pages) {
       PackedAttn wide = t;
@@ -1159,7 +1158,7 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
     a.q_byte = ws + l.q_byte;
     a.own_k_byte = ws + l.k_byte;
     a.own_v_byte = ws + l.v_byte;
-    a.own_groups = own_groups(t.batch, t.total);
+    a.own_groups = (int)own_groups(t.batch, t.total);
   }
   if (plan.can_split && !plan.few) a.rec = reinterpret_cast<Record*>(ws + l.rec);
   a.part = plan.can_split ? reinterpret_cast<float4*>(ws + l.part) : nullptr;
@@ -1242,6 +1241,7 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
   const long long items = packed::max_tiles(batch, total, p.tpt) * (hq / p.gp);
   p.can_split = tiles >= 2 * kMinPart;
   p.ctas = (int)std::min<long long>(num_sms(), items * std::max(1, tiles / kMinPart));
+  p.tiles = (long long)batch * p.pages + own_groups(batch, total);
   p.ws_bytes = places(p, batch, total, hq, hkv, d).end;
   return p;
 }

@@ -111,7 +111,7 @@ struct Row {
 
 // Number of the first group of 16 of a sequence's own rows, among those of all sequences.
 MARS_DEV int own_group(int base, int s) { return base / kPageSize + s; }
-inline int own_groups(int batch, int total) { return total / kPageSize + batch; }
+inline long long own_groups(int batch, int total) { return (long long)total / kPageSize + batch; }
 
 MARS_DEV bool left_out(int skip_pages, int tpt, int n, int P) {
   return n > tpt && P / kPageSize + (P % kPageSize != 0) <= skip_pages;
@@ -137,7 +137,7 @@ struct Scan {
 template <int kThreads>
 MARS_DEV void find_part(const Args& a, Scan<kThreads>& sc) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.batch + kThreads - 1) / kThreads;
+  const int per = a.batch / kThreads + (a.batch % kThreads != 0);
   const int lo = (int)min((long long)tid * per, (long long)a.batch), hi = min(lo + per, a.batch);
   auto clamped = [&](int s) { return min(max(a.cu[s], 0), a.total); };
   int bad = 0, m = 0;

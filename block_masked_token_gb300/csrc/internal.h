@@ -198,6 +198,7 @@ struct Rotary {
   bool inverse, in_place;               // in place: what is not rotated is not copied
   int32_t* status;
 };
+long long rotary_ctas(int batch, int total);
 cudaError_t launch_rotary(const Rotary& a, bool interleaved, cudaStream_t stream);
 
 // ---- K/V rows of packed sequences into the 8-bit paged cache.
@@ -223,6 +224,7 @@ struct ChunkQ8Plan {
   bool can_split;          // items may be divided among CTAs
   int few;                 // rows of an item of chunk_q8_few.cu's kernel (0: not that)
   int pages;               // the wide form's pages per sequence (0: without it)
+  long long tiles;         // of own rows and pages that come before the attention
   PackedPlan wide;
   size_t ws_bytes;
 };

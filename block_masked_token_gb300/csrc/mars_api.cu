@@ -583,6 +583,7 @@ int mars_rotary(const mars_bf16* q, const mars_bf16* k, const int32_t* cu_seqlen
   const void* ptr[4] = {q, k, q_out, k_out};
   for (const void* x : ptr)
     if (!aligned16(x)) return MARS_EALIGN;
+  if ((rc = grid_fits(mars::rotary_ctas(batch, total)))) return rc;
   const mars::Rotary a{q,        k,        q_out,        k_out, q_stride, k_stride, q_out_stride,
                        k_out_stride, cu_seqlens, seq_lens, inv_freq, batch,    total, hq,
                        hkv,      d,        rot,          factor, inverse != 0,
@@ -665,6 +666,7 @@ int mars_attn_chunk_q8(const mars_bf16* q, const mars_bf16* k, const mars_bf16* 
   p.v_scale = v_scale;
   if ((rc = check_attn(p.attn, workspace))) return rc;
   const mars::ChunkQ8Plan plan = mars::plan_chunk_q8(batch, total, hq, hkv, d, max_len_hint);
+  if ((rc = grid_fits(plan.tiles))) return rc;
   if (ws_bytes < plan.ws_bytes) return MARS_ENOSPACE;
   if (plan.ws_bytes && !workspace) return MARS_EINVAL;
   return cuda_rc(mars::launch_chunk_q8(p, plan, workspace, static_cast<cudaStream_t>(stream)));

@@ -140,8 +140,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary a) {
 
 }  // namespace
 
+long long rotary_ctas(int batch, int total) { return packed::max_tiles(batch, total, kRows); }
+
 cudaError_t launch_rotary(const Rotary& a, bool interleaved, cudaStream_t stream) {
-  const unsigned ctas = (unsigned)packed::max_tiles(a.batch, a.total, kRows);
+  const unsigned ctas = (unsigned)rotary_ctas(a.batch, a.total);
   count_launches(1);
   return launch_early(interleaved ? rotary_kernel<true> : rotary_kernel<false>, ctas, kThreads, 0, stream, a);
 }

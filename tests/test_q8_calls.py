@@ -196,3 +196,17 @@ def test_workspace_sizes(hq, hkv, d):
         sizes = [size(batch, total, hq, hkv, d, n) for n in (0, 100, 1000, 20000, 1 << 30, 2 ** 31 - 1)]
         assert all(0 <= s < 1 << 40 for s in sizes) and sizes[-1] > 0
     assert size(0, 1, hq, hkv, d, 1) == size(1, 0, hq, hkv, d, 1) == size(2, 9, hq, hkv, 96, 100) == 0
+
+
+def test_more_sequences_than_a_grid_has_places():
+    """2^31 - 1 sequences of as many rows: refused before anything is launched, and sizes that do not wrap."""
+    big = 2 ** 31 - 1
+    rotary = [P()] * 7 + [big, big, 1, 1, 64, 64, 0, 0, 1.0, 64, 64, 64, 64, None, None]
+    append = [P(), P(), P(), P(), None, None, P(), 4, P(), P(), P(), P(), 9, None, big, big, 1, 64, 16, 64, 64, None, None]
+    chunk = [P()] * 8 + [9, P(), 4, P(), 100, P(), big, big, 1, 1, 64, 16, 64, 64, 64, 0.0, P(256), (1 << 63) - 1, None,
+                         None]
+    for name, a in (("mars_rotary", rotary), ("mars_kv_append_q8", append), ("mars_attn_chunk_q8", chunk)):
+        assert code(name, a) in (mars.EINVAL, mars.EUNSUPPORTED)
+    for batch, total in ((big, big), (big - 1, 1), (1, big - 1), (1 << 20, 1 << 30)):
+        size = packed.mars_packed_workspace_bytes(packed.OP_ATTN_CHUNK_Q8, batch, total, 1, 1, 64, 100)
+        assert 0 <= size < 1 << 50
