@@ -26,9 +26,9 @@
 // waits), softmax (2,300), P V (700), waits (1,000) takes 5,000 cycles for each of the two buffers; TMEM
 // has no room for a third beside two O of 128 columns.
 //
-// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 2,048 .. 8,192 keys): 241 us,
-// 0.46 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 35 us, of which the three
-// launches and the start and end of every CTA are about 22.
+// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 2,048 .. 8,192 keys): 244 us,
+// 0.45 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 37 us, of which the three
+// launches and the start and end of every CTA are about 24.
 //
 // Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
 // (infos); warp 1 copies K and Q; warps 12..15 copy V of even tiles, 16..19 of odd ones, two pages each
@@ -811,11 +811,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
     fence_barrier_init();
   }
-  // Every CTA of ready_kernel has let this one start, after its own wait: what came before that is
-  // there already, what it makes is after the wait here.
-  find_part(a, scan);
-  wait_for_previous();
   let_next_start();
+  wait_for_previous();
+  find_part(a, scan);
   if ((long long)blockIdx.x >= scan.ctas) {
     if (threadIdx.x == 0 && a.rec) a.rec[blockIdx.x] = Record{};
     return;
@@ -969,8 +967,8 @@ MARS_DEV void split_rows(const ReadyArgs& a, const packed::Seq& sq, int r0, int 
 // keys in the wide form, and what that then makes of their rows is written over.
 template <int D>
 __global__ void __launch_bounds__(kReadyThreads) ready_kernel(ReadyArgs a) {
-  sm100::wait_for_previous();
   sm100::let_next_start();
+  sm100::wait_for_previous();
   const int skip = a.pages ? a.pages : -1;
   auto cut = [&](int len) { return (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize)); };
   auto tiles = [](int rows) { return rows / kPageSize + (rows % kPageSize != 0); };

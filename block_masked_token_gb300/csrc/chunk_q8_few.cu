@@ -18,7 +18,7 @@
 //      codes of two keys. Rows g and 8 + g of product j are then d = g D/8 + 2j and the next.
 // A lane has the scores of keys g and 8 + g for rows 2t and 2t + 1; movmatrix turns the weights.
 //
-// Single tokens of 32 sequences of 2,048 .. 8,192 keys (28 query over 4 KV heads of 128): 40.9 us, 0.63 of
+// Single tokens of 32 sequences of 2,048 .. 8,192 keys (28 query over 4 KV heads of 128): 41.3 us, 0.63 of
 // the copy bandwidth (the first form, rows as the 16 rows of a product, 55.4; chunk_kernel 87.8). From
 // 4,096 to 16,384 keys each it gains on them at 7 TB/s, the memory's rate; what is left is the launches
 // (3 us), 6 us before the first copy (boundaries, the part, a page's entry, its scales, in turn) and
@@ -182,15 +182,10 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
   if (lane < kStages) mbar_init(&sh.full[warp][lane], 1);
   fence_barrier_init();
   if (threadIdx.x < 2) prefetch_tmap(threadIdx.x ? &tm_v : &tm_k);
-  // clear_kernel has let this one start after its own wait: what came before that is there already, what
-  // it clears is after the wait where parts arrive.
-  if (!a.arrived) wait_for_previous();
   let_next_start();
+  wait_for_previous();
   find_part(a, sh.scan);
-  if ((long long)blockIdx.x >= sh.scan.ctas) {
-    wait_for_previous();
-    return;
-  }
+  if ((long long)blockIdx.x >= sh.scan.ctas) return;
   if (threadIdx.x == 0) sh.place = first_place(a, sh.scan);
   uint64_t* full = sh.full[warp];
   bool ok = true;
@@ -589,7 +584,6 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
         }
       }
       if (p.slot >= 0) {                             // whoever comes last joins the item's parts
-        wait_for_previous();
         __syncthreads();
         if (threadIdx.x == 0) sh.joins = arrive(&a.arrived[sh.first]) == (uint32_t)sh.pieces - 1;
         __syncthreads();
@@ -604,7 +598,6 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
     }
     __syncthreads();                                 // the list is free again
   }
-  wait_for_previous();
   if (!ok) {                                         // a wait gave up: what is in flight ends first
     for (; used != issued; ++used) wait_bounded(&full[used % kStages], (used / kStages) & 1);
     flags |= MARS_ST_TIMEOUT;
@@ -615,8 +608,8 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
 
 // No part of an item has arrived yet.
 __global__ void clear_kernel(uint32_t* arrived, int n) {
-  sm100::wait_for_previous();
   sm100::let_next_start();
+  sm100::wait_for_previous();
   for (int i = threadIdx.x; i < n; i += blockDim.x) arrived[i] = 0;
 }
 

@@ -97,8 +97,7 @@ cudaError_t set_smem_limit_once(Kernel* fn, int bytes, std::atomic<int> (&done)[
   return e;
 }
 
-// Launch of a kernel that calls wait_for_previous (sm100.cuh) before it touches what the kernel before it
-// writes, or, unless that one too let it start only after such a wait, before all else.
+// Launch of a kernel that calls wait_for_previous (sm100.cuh) before all else that touches memory.
 template <class... Params, class... Args>
 cudaError_t launch_early(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem,
                          cudaStream_t stream, const Args&... args) {

@@ -107,8 +107,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 4) kv_append_q8_kernel(AppendQ8 a) {
   __shared__ int s_bad;                  // first logical page that is not mapped
   bool bad;
-  sm100::wait_for_previous();
   sm100::let_next_start();
+  sm100::wait_for_previous();
   const packed::Seq sq = packed::find_tile_by(
       a.cu, a.batch, a.total, (long long)blockIdx.x, bad, a.seq_lens,
       [&](int s, int n, int len) { return pages_of(rows_of(a, s, n, len), len); });

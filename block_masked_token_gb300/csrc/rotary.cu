@@ -39,8 +39,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(Rotary a) {
   // of unit u at v * units + u: the lanes of a head then read consecutive vectors
   __shared__ float4 turns[kRows][kMaxPairs / 2];
   bool bad;
-  sm100::wait_for_previous();
   sm100::let_next_start();
+  sm100::wait_for_previous();
   const packed::Seq sq = packed::find_tile(a.cu, a.batch, a.total, kRows, 0, (long long)blockIdx.x,
                                            bad, a.seq_lens);
   if (bad && threadIdx.x == 0 && a.status) atomicOr(a.status, MARS_ST_BADSEQ);
