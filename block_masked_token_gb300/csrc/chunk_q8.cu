@@ -1233,7 +1233,8 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
   // 179 and 155.
   const long long pages = std::max(1, max_len / kPageSize + (max_len % kPageSize != 0));
   const long long rows = pages * batch * hkv * kPageSize;
-  if (p.wide.pair && !p.few && total > 10LL * batch * p.tpt && rows <= INT_MAX && rows * d * 4 <= 1LL << 32) p.pages = (int)pages;
+  if (p.wide.pair && !p.few && total > 10LL * batch * p.tpt && rows <= INT_MAX && rows * d * 4 <= 1LL << 32)
+    p.pages = (int)pages;
   // CTAs: as many as the items and their parts can keep busy, by the hint
   const int tiles = packed::key_tiles(max_len) + 1;
   const long long items = packed::max_tiles(batch, total, p.tpt) * (hq / p.gp);

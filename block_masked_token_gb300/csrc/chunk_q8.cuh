@@ -4,8 +4,8 @@
 // An item is a tile of (token, query head) rows of one sequence that share a KV head, with the 128-key
 // tiles that its rows see: the sequence's own keys first, then the cached ones. The items of all
 // sequences are laid out on a line, each as long as its work; CTA c of E takes the part from c/E to
-// (c + 1)/E of it. A cut inside an item leaves partials (m', l, O), which merge_kernel joins in the order
-// of the keys.
+// (c + 1)/E of it. A cut inside an item leaves partials (m', l, O), which are joined in the order of the keys:
+// by merge_kernel, or in chunk_q8_few.cu by the CTA that is the last to leave one.
 //
 // With V = 2^e c (a scale and a code), a weight's power goes the other way: P' = 2^(s + e - m') is what
 // multiplies the codes, m' the running maximum of s + e instead of s, and the row sum takes P' 2^-e. P' is
