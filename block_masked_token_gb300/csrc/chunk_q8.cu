@@ -1210,15 +1210,15 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
   p.tpt = p.wide.tpt;
   const int group = hq / hkv;
   // chunk_q8_few.cu where a sequence's rows make one of its tiles (28 query over 4 KV heads of 128, 32
-  // sequences of 2,048 keys and 2 tokens each: 32 us, here 43 us with 4 tokens each); or a few of
-  // them, each of which reads the cache again, if neither are the items more than the SMs nor the
-  // keys many (8 tokens of 1 sequence, 512 keys: 14.9 against 20.2 us here; of 8 sequences, 2,048
-  // keys: 29.1 against 28.8, 8,192: 66 against 41).
+  // sequences of 2,048 keys and 2 tokens each: 32 us, here 43 us with 4 tokens each); or several, each of
+  // which reads the cache again, where neither are they more than the SMs nor their keys many: 4 tokens of
+  // 8 sequences over 512 keys 15.7 us against 23.6 here, 64 of 1 15.6 and 24.9, 16 of 4 over 1,024 24.5 and
+  // 25.9, over 2,000 29.2 and 24.8, 16 of 2 over 2,000 22.3 and 23.9, 8 of 1 over 8,192 23.3 and 23.6.
   for (int rows : {16, 8}) {
     if (group > rows) continue;
     const long long mine = packed::max_tiles(batch, total, rows / group) * hkv;
     if (total <= (long long)batch * (rows / group) ||
-        (rows == 16 && total <= 4LL * batch * (rows / group) && mine <= num_sms() && max_len <= 2048))
+        (rows == 16 && mine <= num_sms() && max_len <= 2048 && mine * max_len <= num_sms() * 1024LL))
       p.few = rows;
   }
   if (p.few) {

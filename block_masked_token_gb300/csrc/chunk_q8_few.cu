@@ -1,5 +1,5 @@
 // Attention over the 8-bit paged cache for few rows: single tokens, and blocks whose (token, query
-// head) rows of a KV head are 16 at most (or where it is soon done, 64: plan_chunk_q8).
+// head) rows of a KV head are 16 at most (or more, where there is little to do: plan_chunk_q8).
 //
 // With so few rows the work is the reading of the cache: 2 D bytes per key and KV head against
 // 4 * rows * D flops. chunk_q8.cu's roles and its 128-row tiles cost more there than the reading.

@@ -12,6 +12,7 @@ from parity_util import U_BF16, assert_within_bound
 pytestmark = pytest.mark.gpu
 
 HEADS = [(4, 2, 64), (7, 1, 128), (28, 4, 128), (14, 2, 64)]
+WIDE_HEADS = [(24, 1, 64), (48, 2, 128)]            # more query heads per KV head than a tile of few rows holds
 
 
 def status():
@@ -88,7 +89,7 @@ CHUNKS = [([1], [0]), ([1], [1]), ([1], [50]), ([1, 1, 1], [15, 16, 17]), ([0, 3
           ([8, 8], [129, 1000]), ([18, 19, 37], [3, 700, 255]), ([150, 1], [0, 300]), ([300], [40])]
 
 
-@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("heads", HEADS + WIDE_HEADS, ids=str)
 @pytest.mark.parametrize("lens, old", CHUNKS, ids=str)
 def test_chunk_matches_the_definition(lens, old, heads):
     x = make8(lens, *heads, old, seed=len(lens), tail=3, lead=1, fused=heads[0] != 4)
@@ -120,7 +121,9 @@ def test_chunk_of_many_items(lens, old, heads):
 
 @pytest.mark.parametrize("hint", [0, 1, 100, 900, 5000, 2 ** 31 - 1])
 @pytest.mark.parametrize("lens, old, heads", [([1, 4], [800, 60], (28, 4, 128)),
-                                              ([700, 1, 800], [500, 900, 20], (28, 4, 128))], ids=["few", "many"])
+                                              ([3, 4], [800, 60], (24, 1, 128)),
+                                              ([700, 1, 800], [500, 900, 20], (28, 4, 128))],
+                         ids=["few", "middle", "many"])
 def test_chunk_hint_is_no_bound(lens, old, heads, hint):
     x = make8(lens, *heads, old, seed=42)
     o, st = run_chunk8(cuda(x), hint=hint)
@@ -129,7 +132,8 @@ def test_chunk_hint_is_no_bound(lens, old, heads, hint):
 
 
 @pytest.mark.parametrize("lens, old, heads", [([2, 20], [400, 90], (7, 1, 128)),
-                                              ([900, 700], [400, 90], (28, 4, 128))], ids=["few", "many"])
+                                              ([2, 20], [400, 90], (24, 1, 128)),
+                                              ([900, 700], [400, 90], (28, 4, 128))], ids=["few", "middle", "many"])
 def test_chunk_unmapped_pages_and_cut_lengths(lens, old, heads):
     x = make8(lens, *heads, old, seed=43)
     x["table"][0, 3], x["table"][0, 24], x["table"][1, :] = -1, 1 << 20, -7
@@ -147,7 +151,7 @@ def test_chunk_unmapped_pages_and_cut_lengths(lens, old, heads):
     check_chunk8(x, o, rows=[0, 1, 500])
 
 
-@pytest.mark.parametrize("lens, heads", [([3], (7, 1, 128)), ([1400], (28, 4, 128))], ids=["few", "many"])
+@pytest.mark.parametrize("lens, heads", [([3], (7, 1, 128)), ([3], (24, 1, 128)), ([1400], (28, 4, 128))], ids=["few", "middle", "many"])
 def test_chunk_empty_pool(lens, heads):
     x = make8(lens, *heads, [0], seed=44)
     for c in ("k", "v"):
@@ -163,7 +167,8 @@ def test_chunk_empty_pool(lens, heads):
 
 
 @pytest.mark.parametrize("lens, old, heads", [([3, 1], [200, 37], (14, 2, 64)),
-                                              ([1400, 1], [200, 37], (28, 4, 128))], ids=["few", "many"])
+                                              ([3, 20], [200, 37], (24, 1, 128)),
+                                              ([1400, 1], [200, 37], (28, 4, 128))], ids=["few", "middle", "many"])
 def test_chunk_what_no_row_may_read_has_no_effect(lens, old, heads):
     """NaN codes in free slots and unused pages, scales of pages that hold nothing, other rows."""
     x = make8(lens, *heads, old, seed=45, tail=9, spare_pages=3)
@@ -182,7 +187,7 @@ def test_chunk_what_no_row_may_read_has_no_effect(lens, old, heads):
     assert same(o[:sum(lens)], o2[:sum(lens)])
 
 
-@pytest.mark.parametrize("lens, heads", [([3], (7, 1, 128)), ([1400], (28, 4, 128))], ids=["few", "many"])
+@pytest.mark.parametrize("lens, heads", [([3], (7, 1, 128)), ([3], (24, 1, 128)), ([1400], (28, 4, 128))], ids=["few", "middle", "many"])
 def test_chunk_nan_codes_are_not_lost(lens, heads):
     x = make8(lens, *heads, [300], seed=46)
     for c in ("k", "v"):
@@ -201,7 +206,7 @@ def test_chunk_nan_codes_are_not_lost(lens, heads):
 
 
 @pytest.mark.parametrize("profile", ["rising", "falling", "peak"])
-@pytest.mark.parametrize("lens, heads", [([2], (7, 1, 128)), ([1300], (28, 4, 128))], ids=["few", "many"])
+@pytest.mark.parametrize("lens, heads", [([2], (7, 1, 128)), ([2], (24, 1, 128)), ([1300], (28, 4, 128))], ids=["few", "middle", "many"])
 def test_chunk_maxima_that_grow_and_fall(lens, heads, profile):
     """Scores that grow by far more than the lazy rescaling lets pass, page by page."""
     x = make8(lens, *heads, [1000], seed=47, k_spread=0.0)
@@ -217,7 +222,7 @@ def test_chunk_maxima_that_grow_and_fall(lens, heads, profile):
     check_chunk8(x, o, rows=[0, 1, 600, 1299], slack=slack)
 
 
-@pytest.mark.parametrize("lens, heads", [([2], (7, 1, 128)), ([1300], (28, 4, 128))], ids=["few", "many"])
+@pytest.mark.parametrize("lens, heads", [([2], (7, 1, 128)), ([2], (24, 1, 128)), ([1300], (28, 4, 128))], ids=["few", "middle", "many"])
 def test_chunk_scales_far_apart(lens, heads):
     """V scales over the whole range page by page (the tiny ones first, last and in between), a
     zero page, and new V rows of another size than the cache's."""
@@ -239,6 +244,7 @@ FEW = [([1] * 5, (8, 1, 128)), ([2, 1, 2], (8, 2, 64)), ([3, 1], (12, 3, 128)), 
        ([5] * 3, (16, 4, 128)), ([8, 0, 8], (1, 1, 128)), ([9, 8], (1, 1, 64)), ([16, 16], (2, 2, 128)),
        ([17, 16], (1, 1, 128)), ([1] * 4, (16, 1, 128)), ([1] * 3, (9, 1, 64)), ([2] * 3, (9, 1, 128)),
        ([8, 8], (28, 4, 128)), ([16], (14, 2, 64)), ([64], (1, 1, 128)), ([65], (1, 1, 64)),
+       ([64], (28, 4, 128)), ([40, 3], (14, 2, 64)),
        ([300] + [0] * 39, (2, 2, 128)), ([0] * 30 + [140, 0, 0, 1], (4, 4, 64)), ([150] + [0] * 80, (14, 2, 64))]
 
 
