@@ -74,7 +74,7 @@ constexpr int kBufs = 2;             // S buffers, and O's, in TMEM: of even and
 // tiles that every converter has released.
 constexpr int kInfos = 8;
 static_assert(kInfos > kAhead + 4, "the walk and the converters do not wait for each other");
-constexpr int kOwnMost = 207;        // largest scale byte of 16 own rows: 2^80
+constexpr int kOwnMost = 207;        // largest scale byte of 16 own rows of K: 2^80
 
 // --------------------------------------------------------------------------------- the pipeline
 
@@ -936,10 +936,14 @@ MARS_DEV void split_rows(const ReadyArgs& a, const packed::Seq& sq, int r0, int 
   }
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kIts; ++i) top = top_of(x[i], top);
+  for (int i = 0; i < kIts; ++i) {
+    if (is_v) x[i] = cap_values(x[i]);
+    top = top_of(x[i], top);
+  }
   top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
-  // the largest magnitude of the 16 rows into [128, 256), V's into [256, 512)
-  const int byte = min(max((int)(top >> 7) - (is_v ? 8 : 7), kLeast), kOwnMost);
+  // the largest magnitude of the 16 rows into [128, 256), V's as high as f16 lets it: what is far
+  // below it keeps its bits
+  const int byte = is_v ? max((int)(top >> 7) - kTop, kLeast) : min(max((int)(top >> 7) - 7, kLeast), kOwnMost);
   const float f = inverse_power(byte);
   const size_t at = (size_t)(own_group(sq.base, sq.s) + sq.tile) * a.hkv + h;
   if (lane == 0) (is_v ? a.v_byte : a.k_byte)[at] = (uint8_t)byte;

@@ -48,6 +48,24 @@ MARS_DEV uint32_t finite_max(uint32_t top, uint32_t word) {
   return __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
 }
 
+// Rows in f16 stand over a power of two that brings their largest finite magnitude into [2^kTop,
+// 2^(kTop + 1)).
+constexpr int kTop = 14;
+// Own values from 2^88 on count as the largest bf16 below (infinities and NaN stay), so that their powers
+// end at 2^73. P' = 2^(s + e - m' + 7) with m' at most that of the largest weight times 2^73; a key over
+// the smallest scale, 2^-40, then keeps its part of the row sum, P' 2^40, while its weight is above 2^-20 of
+// the largest: below that P' leaves the range of 32 bits. (Without a cap that began at weights as large as
+// any, and f16 values beyond the range became infinite, NaN with the weight 0 of a row that does not see them.)
+constexpr uint32_t kMostValue = 0x6b7f;            // bf16
+MARS_DEV uint32_t cap_values(uint32_t word) {
+  const uint32_t m = word & 0x7fff7fffu, most = kMostValue << 16 | kMostValue;
+  const uint32_t beyond = __vcmpgtu2(m, most) & ~__vcmpgeu2(m, 0x7f807f80u) & 0x7fff7fffu;
+  return (word & ~beyond) | (most & beyond);
+}
+MARS_DEV uint4 cap_values(const uint4& x) {
+  return make_uint4(cap_values(x.x), cap_values(x.y), cap_values(x.z), cap_values(x.w));
+}
+
 // Wait of one thread for the phase with `parity`. Gives up (false) after 2^20 attempts of a
 // microsecond at most.
 MARS_DEV bool wait_bounded(uint64_t* b, uint32_t parity) {

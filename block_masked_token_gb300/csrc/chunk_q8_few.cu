@@ -134,9 +134,7 @@ MARS_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// bf16 rows as f16 over a power of two that brings the largest finite magnitude into
-// [2^14, 2^15): what f16 then loses lies below 2^-39 of that.
-constexpr int kTop = 14;
+// bf16 rows as f16 (kTop): what f16 loses lies below 2^-39 of the largest magnitude.
 MARS_DEV uint32_t word_max(const uint4& x, uint32_t top) {
   return finite_max(finite_max(finite_max(finite_max(top, x.x), x.y), x.z), x.w);
 }
@@ -162,7 +160,7 @@ MARS_DEV uint32_t arrive(uint32_t* count) {
   return n;
 }
 constexpr int kLeastRow = -126;      // Q and K: 2^126 is the largest factor
-constexpr int kLeastV = -60;         // V: the sums of P' 2^-e stay far from the ends of the range
+constexpr int kLeastV = -40;         // V: as low as the pages' scales (and to 2^73: cap_values)
 
 template <int D, int kRows>
 __global__ void __launch_bounds__(Shared<D, kRows>::kThreads, 1)
@@ -494,7 +492,8 @@ few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUt
             uint32_t top = 0;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
-              const uint4 in = key < count ? reinterpret_cast<const uint4*>(row)[c] : make_uint4(0, 0, 0, 0);
+              const uint4 in =
+                  key < count ? cap_values(reinterpret_cast<const uint4*>(row)[c]) : make_uint4(0, 0, 0, 0);
               *reinterpret_cast<uint4*>(&x[r][4 * c]) = in;
               top = word_max(in, top);
             }

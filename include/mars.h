@@ -517,9 +517,12 @@ int mars_kv_append_q8(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_
  *   in f16 over a power of two per row, exact down to 2^-39 of the row's largest magnitude (few
  *   rows: a tile of 8 or 16 (token, head) rows of a KV head per sequence, by batch and total);
  *   as sums of two e4m3 numbers over a power of two per row of q and per 16 own keys, exact to 2^-17
- *   of the largest magnitude there, and own values in f16 over one per 16 keys (these powers reach
- *   from 2^-40 to 2^80: beyond 2^88 values saturate, and an infinity in q or an own k is NaN there);
+ *   of the largest magnitude there, and own values in f16 over one per 16 keys (the powers of k reach
+ *   from 2^-40 to 2^80: beyond 2^88 keys saturate, and an infinity in q or an own k is NaN there);
  *   in bf16 (many rows).
+ * In the first two forms the powers of own values begin at 2^-40 (what lies below 2^-64 is lost) and
+ * finite ones from 2^88 on count as the largest bf16 below; in all forms a key whose weight is below
+ * 2^-20 of the row's largest may miss in the row sum where values differ by more than 2^100.
  * Each result is the same, bit by bit, from call to call. */
 int mars_attn_chunk_q8(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
                        const int32_t* cu_seqlens, const uint8_t* k_pool, const uint8_t* v_pool,
