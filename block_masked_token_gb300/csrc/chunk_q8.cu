@@ -18,6 +18,11 @@
 //   - Scores get the row's power and the K scale of their 16 keys as one factor in 32 bits.
 //   - O += P V runs on f16 (chunk_q8.cuh says over what), and own values over a power of two per 16
 //     tokens.
+//   - Where 16 own rows differ much in size (kApartK, kApartV), each has a power of its own: one for all
+//     would go by rows that a row may not see (a key 2^10 times the 15 before it took 0.8 % of
+//     their rows' results, from 2^20 on everything). The converter warps then take those into an own
+//     tile's scores, before the softmax sees them. (With the code for it in the softmax, although not
+//     run, the 128 blocks of 16 took 254 to 278 us; so 245, and 240 without any of it.)
 // Shared memory moves 128 bytes per cycle: the copies of a tile's codes take 256 cycles, S 512, the
 // conversion of V 384, P V 256. (With K converted to f16 as well, 1,800 cycles per tile.)
 //
@@ -74,11 +79,16 @@ constexpr int kBufs = 2;             // S buffers, and O's, in TMEM: of even and
 // tiles that every converter has released.
 constexpr int kInfos = 8;
 static_assert(kInfos > kAhead + 4, "the walk and the converters do not wait for each other");
-constexpr int kOwnMost = 207;        // largest scale byte of 16 own rows of K: 2^80
+
+// 16 own rows share a power while the exponents of their largest magnitudes differ by at most so much.
+constexpr int kApartK = 3, kApartV = 10;
+// What the scores of an own tile with more powers than that become (own_scores): s + e, over a V of this
+// scale byte. Its 2^-e is 0 in 32 bits, so that the row sum takes nothing from these weights.
+constexpr int kMixedByte = 254;
 
 // --------------------------------------------------------------------------------- the pipeline
 
-enum : int { kFirst = 1, kLast = 2, kOwn = 4, kEnd = 8, kHoles = 16, kSecond = 32 };
+enum : int { kFirst = 1, kLast = 2, kOwn = 4, kEnd = 8, kHoles = 16, kSecond = 32, kMixed = 64, kMixedEven = 128, kMixedOdd = 256 };
 
 // A key tile as the walk hands it to the other warps.
 struct alignas(16) Info {
@@ -86,7 +96,9 @@ struct alignas(16) Info {
   int base, n, tok0, h0, kvh;        // its item
   int slot;                          // of the partial, -1: the item is whole
   int k0, count;                     // first key (own: token of the sequence), keys that there are
-  int pad[3];
+  int item;                          // of this CTA
+  int again;                         // mixed: not the first such of the even or odd tiles of its item
+  int pad;
   alignas(16) int page[kPagesPerTile];         // own tiles: groups of own rows; -1: not to be read
   alignas(8) uint8_t k_byte[kPagesPerTile];    // scale bytes
   alignas(8) uint8_t v_byte[kPagesPerTile];    // 0: no such keys
@@ -98,6 +110,7 @@ struct Bar {
   uint64_t k_full[kSlots], k_empty[kSlots];
   uint64_t v_full[kTiles], v_empty[kTiles];
   uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
+  uint64_t s_raw[kBufs], own_done[kBufs];              // of mixed tiles, before s_full
   uint64_t q_full, q_free, o_free, drain[2];
   uint64_t pair[4];                  // the two warps of 32 rows
   uint32_t tmem_base;
@@ -111,7 +124,7 @@ struct alignas(1024) Shared {
   Info infos[kInfos];
   union {
     Scan<kThreads> scan;             // until the walk has published its first tile
-    float exchange[2][BQ];           // [even or odd tiles][row], at the end of items
+    float exchange[2][BQ];           // [even or odd tiles][row], at the end of items (and see own_scores)
   };
 };
 static_assert(sizeof(Shared) <= 3 * 1024, "with the tiles, the shared memory of a CTA");
@@ -183,7 +196,7 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
   const Args& a = p.a;
   const int lane = threadIdx.x & 31;
   Record rec{};
-  int t = 0, flags = 0;
+  int t = 0, flags = 0, items = 0;
   bool ok = true;
   // wait until `n` entries from t on are free
   auto room = [&](int n) {
@@ -237,8 +250,10 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
       for (int r = lane; r < BQ; r += 32) ml[r] = make_float2(-INFINITY, kNoKeys);
       continue;
     }
-    int first = kFirst;
+    int first = kFirst, last = kLast;
+    const int item = items++;
     auto entry = [&](Info& e, int k0, int count, int f) {
+      e.item = item;
       e.flags = f;
       e.base = q.base;
       e.n = q.n;
@@ -253,20 +268,24 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
       const int count = min(last_tok + 1 - x * BKV, BKV);
       const bool needed = lane < kPagesPerTile && lane * kPageSize < count;
       const int group = own_group(q.base, q.s) + x * kPagesPerTile + lane;
-      uint8_t kb = 127, vb = 0;
+      uint8_t kb = kBias, vb = 0;
       if (needed) {
         const size_t at = (size_t)group * a.hkv + kvh;
         kb = a.own_k_byte[at];
         vb = a.own_v_byte[at];
       }
+      const bool mixed = __any_sync(0xffffffffu, needed && (kb == 0 || vb == 0));
       if (!(ok = room(1))) break;
       Info& f = p.info(t);
       if (lane < kPagesPerTile) {
         f.page[lane] = needed ? group : -1;
-        f.k_byte[lane] = kb;
-        f.v_byte[lane] = vb;
+        f.k_byte[lane] = mixed ? kBias : kb;
+        f.v_byte[lane] = mixed && needed ? kMixedByte : vb;
       }
-      if (lane == 0) entry(f, x * BKV, count, kOwn | first | (left == 1 ? kLast : 0));
+      const int bit = t & 1 ? kMixedOdd : kMixedEven;
+      if (lane == 0) f.again = (last & bit) != 0;
+      if (mixed) last |= bit;
+      if (lane == 0) entry(f, x * BKV, count, kOwn | first | (left == 1 ? last : 0) | (mixed ? kMixed : 0));
       first = first & kFirst ? kSecond : 0;
       --left;
       publish(1);
@@ -300,7 +319,7 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
         f.v_byte[g] = vb;
         if (g == 0)
           entry(f, mine * BKV, min(q.P - mine * BKV, BKV),
-                (u == 0 ? first : u == 1 && first == kFirst ? kSecond : 0) | (u + 1 == left ? kLast : 0) |
+                (u == 0 ? first : u == 1 && first == kFirst ? kSecond : 0) | (u + 1 == left ? last : 0) |
                     (((holes >> lane) & 0xffu) ? kHoles : 0));
       }
       first = first & kFirst && n == 1 ? kSecond : 0;
@@ -315,6 +334,77 @@ MARS_DEV void walk(const Pipe& p, const Scan<kThreads>& sc) {
   }
   if (lane == 0 && a.rec) a.rec[blockIdx.x] = rec;
   if (flags && a.status) atomicOr(a.status, flags);
+}
+
+// Factor of a row's scores (one of 1e-30 makes them 0; own_scores divides by it).
+MARS_DEV float row_factor(const Args& a, const Info& f, int tok, int row) {
+  return fmaxf(a.scale_log2 * q8::power(a.q_byte[((size_t)f.base + tok) * a.hq + f.h0 + row % a.gp]), 1e-30f);
+}
+
+// Converter warps, a row per thread: the scores of a mixed own tile, whose keys and values have powers of
+// their own, to what softmax() takes like a cached tile's: (s + e - 127) / factor in place, for a V of
+// kMixedByte. The row sum cannot come from these weights, no 16 of which share an e: log2 of the sum of
+// 2^s is left in exchange, where the softmax's thread finds it at the item's end. `uses`: mixed tiles before.
+template <int D>
+MARS_DEV bool own_scores(const Pipe& p, const Info& f, int t, int uses) {
+  using namespace sm100;
+  using L = Layout<D>;
+  const Args& a = p.a;
+  const int odd = t & 1, quad = (threadIdx.x >> 5) & 3, row = quad * 32 + (int)(threadIdx.x & 31);
+  const uint32_t s_addr = p.tmem + L::TM_S + odd * BKV + ((uint32_t)(quad * 32) << 16);
+  const int tok = f.tok0 + row / a.gp;
+  const bool has = row < a.gp * a.tpt && tok < f.n;
+  const int limit = min(f.count, tok + 1 - f.k0);
+  const float factor = has ? row_factor(a, f, tok, row) : 1.f, inv = 1.f / factor;
+  float* const kept = &p.exchange[odd][row];
+  // The softmax has left the item before, and this tile's scores are there. (The P V of the tile before has
+  // waited for the softmax to leave the item before its own: o_free is at most one phase behind then.)
+  if (f.item > 0 && !(p.warp_wait(&p.bar.pv_done[odd ^ 1], ((t - 1) / kBufs) & 1) &&
+                      p.warp_wait(&p.bar.o_free, (f.item - 1) & 1)))
+    return false;
+  if (!p.warp_wait(&p.bar.s_raw[odd], uses & 1)) return false;
+  tc_fence_after();
+  float top = -INFINITY, sum = 0.f;
+  if (f.again) {                                     // the sum so far
+    top = *kept;
+    sum = 1.f;
+  }
+#pragma unroll 1
+  for (int c = 0; c < f.count; c += 4) {
+    uint32_t r[4];
+    tmem_ld4(s_addr + c, r);
+    // a group's byte, or where that is 0 those of its rows
+    const int group = f.page[0] + c / kPageSize;
+    const size_t at = (size_t)group * a.hkv + f.kvh, of_rows = ((size_t)f.kvh * a.own_groups + group) * kPageSize + c % kPageSize;
+    uint32_t kb = a.own_k_byte[at] * 0x01010101u, vb = a.own_v_byte[at] * 0x01010101u;
+    if (!kb) kb = *reinterpret_cast<const uint32_t*>(a.own_k_bytes + of_rows);
+    if (!vb) vb = *reinterpret_cast<const uint32_t*>(a.own_v_bytes + of_rows);
+    tmem_ld_wait();
+    float s[4], m = top;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[e] = __uint_as_float(r[e]) * fminf(factor * power((int)(kb >> (8 * e) & 255u)), 3e38f);
+      if (c + e >= limit) s[e] = -INFINITY;
+      r[e] = __float_as_uint((s[e] + (float)((int)(vb >> (8 * e) & 255u) - kMixedByte)) * inv);
+      m = fmaxf(m, s[e]);
+    }
+    tmem_st4(s_addr + c, r);
+    const float base = m == -INFINITY ? 0.f : m;     // (+infinity gives NaN)
+    sum *= flash::ex2_approx(top - base);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += flash::ex2_approx(s[e] - base);
+    top = m;
+  }
+  tmem_st_wait();
+  *kept = (top == -INFINITY ? 0.f : top) + log2f(sum);
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&p.bar.own_done[odd]);
+  if (quad == 0) {
+    if (!p.warp_wait(&p.bar.own_done[odd], uses & 1)) return false;
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&p.bar.s_full[odd]);
+  }
+  return true;
 }
 
 // 16 bytes of an f16 tile: chunk c (8 elements) of row r. Regions of 64 elements, 128-byte swizzle.
@@ -410,7 +500,7 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
   uint64_t* const full = p.bar.raw_full[warp];
   uint8_t* const ring = p.smem + L::OFF_RAW + warp * kRaw * kPages * L::PAGE;
   // the next copies: their number and tile; `converted`: those that have left the ring
-  int copies = 0, next = odd, converted = 0, own_copies = -1;
+  int copies = 0, next = odd, converted = 0, own_copies = -1, mixed = 0;
   bool more = true, ok = true;
   auto copy_ahead = [&](int t) {
     while (more && next <= t + kAhead && copies < converted + kRaw) {
@@ -464,8 +554,9 @@ MARS_DEV void convert(const Pipe& p, const CUtensorMap& map, const CUtensorMap& 
           tma_load_2d(tile + x * (BKV * 128) + g * kPageSize * 128, &map_own, &p.bar.v_full[odd], x * 64,
                       (f.page[g] * a.hkv + f.kvh) * kPageSize);
       own_copies = bytes ? t : own_copies;
-      mbar_arrive(&p.bar.info_empty[t % kInfos]);
     }
+    if ((flags & kMixed) && !(ok = own_scores<D>(p, f, t, mixed++))) break;
+    p.warp_done(t);
   }
   // no copy is in flight when the CTA ends
   __syncwarp();
@@ -510,7 +601,7 @@ MARS_DEV void issue_s(const Pipe& p) {
       mma_commit(&p.bar.k_empty[st]);
     }
     if (!ok) break;
-    mma_commit(&p.bar.s_full[sb]);
+    mma_commit(flags & kMixed ? &p.bar.s_raw[sb] : &p.bar.s_full[sb]);
     if (flags & kLast) mma_commit(&p.bar.q_free);
   }
   mma_commit(&p.bar.drain[0]);
@@ -691,6 +782,7 @@ MARS_DEV void softmax(const Pipe& p) {
       if (busy) {
         // maxima and sums of the row's even and odd tiles, once both have left the item before
         float (&x)[2][BQ] = p.exchange;
+        if (flags & (kMixedEven << odd)) l += flash::ex2_approx(x[odd][row] + kLift - (m == -INFINITY ? 0.f : m));
         if (!meet()) return;
         x[odd][row] = m;
         if (!meet()) return;
@@ -762,7 +854,7 @@ MARS_DEV void softmax(const Pipe& p) {
       has = row < a.gp * a.tpt && tok < n.n;
       busy = __any_sync(0xffffffffu, has);       // warps without rows only keep step
       factor = 1.f;
-      if (has) factor = a.scale_log2 * q8::power(a.q_byte[((size_t)n.base + tok) * a.hq + n.h0 + row % a.gp]);
+      if (has) factor = row_factor(a, n, tok, row);
     }
   }
 }
@@ -802,6 +894,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     for (int i = 0; i < 2; ++i) mbar_init(&bar.drain[i], 1);
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.s_raw[i], 1);
+      mbar_init(&bar.own_done[i], kGroupWarps);
       mbar_init(&bar.p_full[i], 128);
       mbar_init(&bar.pv_done[i], 1);
     }
@@ -870,8 +964,9 @@ struct ReadyArgs {
   uint16_t *k_out, *v_out;
   int32_t *lens, *table;
   // chunk_kernel's: Q as [2][total][hq][D], scale bytes [total][hq]; groups of 16 own rows, K as
-  // [2][groups][hkv][16][D] and V in f16 as [groups][hkv][16][D], scale bytes [groups][hkv] each
-  uint8_t *q_parts, *q_byte, *k_parts, *k_byte, *v_byte;
+  // [2][groups][hkv][16][D] and V in f16 as [groups][hkv][16][D], scale bytes [groups][hkv] each, 0 where
+  // the rows have their own, [hkv][groups][16]
+  uint8_t *q_parts, *q_byte, *k_parts, *k_byte, *v_byte, *k_bytes, *v_bytes;
   uint16_t* v_half;
 };
 constexpr int kReadyThreads = 256;
@@ -897,7 +992,7 @@ MARS_DEV void split8(const uint4& x, float f, uint2& first, uint2& second) {
   second = make_uint2(v[0], v[1]);
 }
 
-// Head w of q, k and v for 16 rows from r0 on of a sequence, rows from nr on zero. Whole warp.
+// Head w of q, k and v for 16 rows from r0 on of a sequence, rows of k and v from nr on zero. Whole warp.
 template <int D>
 MARS_DEV void split_rows(const ReadyArgs& a, const packed::Seq& sq, int r0, int nr, int w) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIts = kPageSize / kRows;     // rows at a time
@@ -912,18 +1007,23 @@ MARS_DEV void split_rows(const ReadyArgs& a, const packed::Seq& sq, int r0, int 
   for (int i = 0; i < kIts; ++i)
     x[i] = r + i * kRows < nr ? *reinterpret_cast<const uint4*>(from + (r + i * kRows) * stride)
                               : make_uint4(0, 0, 0, 0);
-  auto top_of = [&](const uint4& y, uint32_t top) {
-    return finite_max(finite_max(finite_max(finite_max(top, y.x), y.y), y.z), y.w);
+  // largest finite magnitude of row i, as bf16 bits: this lane's part, in both halves, and all of it
+  auto row_max = [&](int i) {
+    return finite_max(finite_max(finite_max(finite_max(0, x[i].x), x[i].y), x[i].z), x[i].w);
   };
+  auto top_of = [&](int i) {
+    uint32_t top = row_max(i);
+    top = max(top >> 16, top & 0xffffu);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top;
+  };
+  // q, k: the row's largest magnitude into [128, 256) (a row of next to nothing: 2^-53)
+  auto byte_of = [](uint32_t top) { return top ? min(max((int)(top >> 7), 74), 253) - 7 : kBias; };
   if (is_q) {
 #pragma unroll
     for (int i = 0; i < kIts; ++i) {
-      uint32_t top = top_of(x[i], 0);
-      top = max(top >> 16, top & 0xffffu);
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // the row's largest magnitude into [128, 256) (a row of next to nothing: 2^-53)
-      const int byte = top ? min(max((int)(top >> 7), 74), 253) - 7 : kBias;
+      const int byte = byte_of(top_of(i));
       if (r + i * kRows >= nr) continue;
       uint2 u, v;
       split8(x[i], inverse_power(byte), u, v);
@@ -934,23 +1034,35 @@ MARS_DEV void split_rows(const ReadyArgs& a, const packed::Seq& sq, int r0, int 
     }
     return;
   }
-  uint32_t top = 0;
+  // the same of rows i and i + 1 in the halves of tops[i / 2]; rows of zeros go by any power
+  uint32_t tops[kIts / 2] = {}, most = 0, least = UINT_MAX;
 #pragma unroll
   for (int i = 0; i < kIts; ++i) {
     if (is_v) x[i] = cap_values(x[i]);
-    top = top_of(x[i], top);
+    const uint32_t top = row_max(i);
+    tops[i / 2] |= max(top >> 16, top & 0xffffu) << (i % 2 * 16);
   }
-  top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
-  // the largest magnitude of the 16 rows into [128, 256), V's as high as f16 lets it: what is far
-  // below it keeps its bits
-  const int byte = is_v ? max((int)(top >> 7) - kTop, kLeast) : min(max((int)(top >> 7) - 7, kLeast), kOwnMost);
-  const float f = inverse_power(byte);
-  const size_t at = (size_t)(own_group(sq.base, sq.s) + sq.tile) * a.hkv + h;
-  if (lane == 0) (is_v ? a.v_byte : a.k_byte)[at] = (uint8_t)byte;
-  const size_t second = (size_t)a.own_groups * a.hkv * kPageSize * D;
 #pragma unroll
-  for (int i = 0; i < kIts; ++i) {
-    const size_t to = (at * kPageSize + r + i * kRows) * D + c * 8;
+  for (int i = 0; i < kIts / 2; ++i) {
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) tops[i] = __vmaxu2(tops[i], __shfl_xor_sync(0xffffffffu, tops[i], o));
+    most = __vmaxu2(most, tops[i]);
+    least = __vminu2(least, __vsub2(tops[i], 0x00010001u));
+  }
+  most = __reduce_max_sync(0xffffffffu, max(most >> 16, most & 0xffffu));
+  least = __reduce_min_sync(0xffffffffu, min(least >> 16, least & 0xffffu)) + 1;
+  // V's largest magnitude as high as f16 lets it: what is far below it keeps its bits
+  auto of = [&](uint32_t top) { return is_v ? max((int)(top >> 7) - kTop, kLeast) : byte_of(top); };
+  const bool mixed = most && (int)(most >> 7) - (int)(least >> 7) > (is_v ? kApartV : kApartK);
+  const int shared = of(most), group = own_group(sq.base, sq.s) + sq.tile;
+  if (lane == 0) (is_v ? a.v_byte : a.k_byte)[(size_t)group * a.hkv + h] = mixed ? 0 : (uint8_t)shared;
+  const size_t second = (size_t)a.own_groups * a.hkv * kPageSize * D;
+  size_t to = (((size_t)group * a.hkv + h) * kPageSize + r) * D + c * 8;
+  uint8_t* bytes = (is_v ? a.v_bytes : a.k_bytes) + ((size_t)h * a.own_groups + group) * kPageSize + r;
+#pragma unroll
+  for (int i = 0; i < kIts; ++i, to += kRows * D, bytes += kRows) {
+    const int byte = mixed ? of(tops[i / 2] >> (i % 2 * 16) & 0xffffu) : shared;
+    const float f = inverse_power(byte);
     if (is_v) {
       float e[8];
       unpack8(x[i], e);
@@ -963,6 +1075,7 @@ MARS_DEV void split_rows(const ReadyArgs& a, const packed::Seq& sq, int r0, int 
       *reinterpret_cast<uint2*>(a.k_parts + to) = u;
       *reinterpret_cast<uint2*>(a.k_parts + second + to) = v;
     }
+    if (mixed && c == 0) *bytes = (uint8_t)byte;
   }
 }
 
@@ -970,7 +1083,7 @@ MARS_DEV void split_rows(const ReadyArgs& a, const packed::Seq& sq, int r0, int 
 // of sequence s becomes page s * pages + j); every gridDim.y-th eight heads. Sequences that chunk_kernel takes have no
 // keys in the wide form, and what that then makes of their rows is written over.
 template <int D>
-__global__ void __launch_bounds__(kReadyThreads) ready_kernel(ReadyArgs a) {
+__global__ void __launch_bounds__(kReadyThreads, 4) ready_kernel(ReadyArgs a) {
   sm100::let_next_start();
   sm100::wait_for_previous();
   const int skip = a.pages ? a.pages : -1;
@@ -1036,7 +1149,7 @@ __global__ void __launch_bounds__(kReadyThreads) ready_kernel(ReadyArgs a) {
 // Parts of the workspace, in bytes from its start: the wide form's, what ready_kernel makes, and what
 // divided items leave.
 struct Places {
-  size_t lens, table, k, v, q_parts, q_byte, k_parts, k_byte, v_half, v_byte, rec, part, end;
+  size_t lens, table, k, v, q_parts, q_byte, k_parts, k_byte, v_half, v_byte, k_bytes, v_bytes, rec, part, end;
 };
 Places places(const ChunkQ8Plan& plan, int batch, int total, int hq, int hkv, int d) {
   Places l{};
@@ -1061,6 +1174,8 @@ Places places(const ChunkQ8Plan& plan, int batch, int total, int hq, int hkv, in
     take(l.k_byte, groups);
     take(l.v_half, groups * kPageSize * d * 2);
     take(l.v_byte, groups);
+    take(l.k_bytes, groups * kPageSize);
+    take(l.v_bytes, groups * kPageSize);
   }
   if (plan.can_split) {
     const int rows = plan.few ? plan.few : BQ;       // of a partial
@@ -1109,6 +1224,8 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
     u.k_parts = ws + l.k_parts;
     u.k_byte = ws + l.k_byte;
     u.v_byte = ws + l.v_byte;
+    u.k_bytes = ws + l.k_bytes;
+    u.v_bytes = ws + l.v_bytes;
     u.v_half = reinterpret_cast<uint16_t*>(ws + l.v_half);
     count_launches(1);
     // (where there are many tiles, one CTA for each: mixed rows 148 us with five, 133 with one)
@@ -1160,6 +1277,8 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
     a.q_byte = ws + l.q_byte;
     a.own_k_byte = ws + l.k_byte;
     a.own_v_byte = ws + l.v_byte;
+    a.own_k_bytes = ws + l.k_bytes;
+    a.own_v_bytes = ws + l.v_bytes;
     a.own_groups = (int)own_groups(t.batch, t.total);
   }
   if (plan.can_split && !plan.few) a.rec = reinterpret_cast<Record*>(ws + l.rec);

@@ -102,8 +102,9 @@ struct Args {
                                      // are left to the wide form (-1: none)
   float scale_log2;
   uint16_t* o;
-  // for chunk_q8.cu, what its first kernel makes: scale bytes of Q's rows, and of groups of 16 own rows
-  const uint8_t *q_byte, *own_k_byte, *own_v_byte;
+  // for chunk_q8.cu, what its first kernel makes: scale bytes of Q's rows, of groups of 16 own rows, and of
+  // the rows of those that share none
+  const uint8_t *q_byte, *own_k_byte, *own_v_byte, *own_k_bytes, *own_v_bytes;
   int own_groups;
   struct Record* rec;                // [CTA], for merge_kernel
   uint32_t* arrived;                 // [CTA], parts of the item that it begins (chunk_q8_few.cu)

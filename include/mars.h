@@ -380,7 +380,8 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
  *     NaN included. A NaN or infinity in a sequence's own rows can reach the outputs of
  *     that sequence up to 127 rows before or after the rows that the formulas reach. It never
  *     vanishes: a row one of whose scores is NaN or +infinity is NaN in o and lse. A row all
- *     of whose scores are -infinity has lse -infinity and weights of 0. */
+ *     of whose scores are -infinity has lse -infinity and weights of 0. Finite scores of 2^30 and
+ *     more are rounded by more than exp2 can take: their rows may be NaN. */
 
 /* Workspace (device scratch, >= 256-byte aligned) of `op` (MARS_OP_ATTN_PACKED,
  * MARS_OP_ATTN_CHUNK, MARS_OP_ATTN_PACKED_GRAD, MARS_OP_ATTN_CHUNK_Q8) for `total` rows of
@@ -516,9 +517,9 @@ int mars_kv_append_q8(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_
  * per sequence, q and the chunk's own rows are held
  *   in f16 over a power of two per row, exact down to 2^-39 of the row's largest magnitude (few
  *   rows: a tile of 8 or 16 (token, head) rows of a KV head per sequence, by batch and total);
- *   as sums of two e4m3 numbers over a power of two per row of q and per 16 own keys, exact to 2^-17
- *   of the largest magnitude there, and own values in f16 over one per 16 keys (the powers of k reach
- *   from 2^-40 to 2^80: beyond 2^88 keys saturate, and an infinity in q or an own k is NaN there);
+ *   as sums of two e4m3 numbers over powers of two, exact to 2^-17 of the largest magnitude of a row of q,
+ *   2^-14 of that of an own key (rows of less than 2^-53 are taken with that as their largest, and an
+ *   infinity in q or an own k is NaN), and own values in f16, exact to 2^-29 of the row's largest;
  *   in bf16 (many rows).
  * In the first two forms the powers of own values begin at 2^-40 (what lies below 2^-64 is lost) and
  * finite ones from 2^88 on count as the largest bf16 below; in all forms a key whose weight is below
