@@ -970,6 +970,7 @@ struct ReadyArgs {
   uint16_t* v_half;
 };
 constexpr int kReadyThreads = 256;
+constexpr size_t kWideBytes = (size_t)1 << 31;       // pages of the wide form
 
 // Eight bf16 times f as two e4m3 numbers each: the nearest, and the nearest to what that leaves. An
 // infinity becomes NaN (a finite value's second product adds nothing).
@@ -1146,10 +1147,10 @@ __global__ void __launch_bounds__(kReadyThreads, 4) ready_kernel(ReadyArgs a) {
   }
 }
 
-// Parts of the workspace, in bytes from its start: the wide form's, what ready_kernel makes, and what
-// divided items leave.
+// Parts of the workspace, in bytes from its start: what ready_kernel makes, what divided items leave, and
+// the wide form's.
 struct Places {
-  size_t lens, table, k, v, q_parts, q_byte, k_parts, k_byte, v_half, v_byte, k_bytes, v_bytes, rec, part, end;
+  size_t wide, lens, table, k, v, q_parts, q_byte, k_parts, k_byte, v_half, v_byte, k_bytes, v_bytes, rec, part, end;
 };
 Places places(const ChunkQ8Plan& plan, int batch, int total, int hq, int hkv, int d) {
   Places l{};
@@ -1158,14 +1159,6 @@ Places places(const ChunkQ8Plan& plan, int batch, int total, int hq, int hkv, in
     at = end;
     end += packed::align256(bytes);
   };
-  if (plan.pages) {
-    end = packed::align256(plan.wide.ws_bytes);
-    const size_t bytes = (size_t)batch * plan.pages * hkv * kPageSize * d * 2;
-    take(l.lens, (size_t)batch * sizeof(int32_t));
-    take(l.table, (size_t)batch * plan.pages * sizeof(int32_t));
-    take(l.k, bytes);
-    take(l.v, bytes);
-  }
   if (!plan.few) {
     const size_t groups = (size_t)own_groups(batch, total) * hkv, rows = (size_t)total * hq;
     take(l.q_parts, 2 * rows * d);
@@ -1181,6 +1174,15 @@ Places places(const ChunkQ8Plan& plan, int batch, int total, int hq, int hkv, in
     const int rows = plan.few ? plan.few : BQ;       // of a partial
     take(l.rec, plan.ctas * (plan.few ? sizeof(uint32_t) : sizeof(Record)));
     take(l.part, (size_t)plan.ctas * 2 * rows * (d + 2) * sizeof(float));
+  }
+  if (plan.pages) {
+    end = std::max(end, plan.least);                 // (where the other forms' parts may end)
+    const size_t bytes = (size_t)batch * plan.pages * hkv * kPageSize * d * 2;
+    take(l.wide, plan.wide.ws_bytes);
+    take(l.lens, (size_t)batch * sizeof(int32_t));
+    take(l.table, (size_t)batch * plan.pages * sizeof(int32_t));
+    take(l.k, bytes);
+    take(l.v, bytes);
   }
   l.end = end;
   return l;
@@ -1240,7 +1242,7 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
       wide.block_table = u.table;
       wide.num_pages = t.batch * plan.pages;
       wide.max_pages = plan.pages;
-      e = launch_packed_attn(wide, plan.wide, ws, stream);
+      e = launch_packed_attn(wide, plan.wide, ws + l.wide, stream);
       if (e != cudaSuccess) return e;
     }
   }
@@ -1326,7 +1328,7 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
 
 }  // namespace
 
-ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_len) {
+ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_len, size_t ws_bytes) {
   ChunkQ8Plan p{};
   p.wide = plan_packed(batch, total, hq, hkv, d, max_len);
   p.gp = p.wide.gp;
@@ -1348,23 +1350,40 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
     p.gp = group;
     p.tpt = p.few / group;
   }
+  // CTAs: as many as the items and their parts can keep busy, by the hint
+  const int tiles = packed::key_tiles(max_len) + 1;
+  auto ctas = [&](int gp, int tpt) {
+    const long long items = packed::max_tiles(batch, total, tpt) * (hq / gp);
+    return (int)std::min<long long>(num_sms(), items * std::max(1, tiles / kMinPart));
+  };
+  p.can_split = tiles >= 2 * kMinPart;
+  p.ctas = ctas(p.gp, p.tpt);
+  // What every form but the wide one can do with. Each of these grows with batch, total and max_len, so that
+  // a workspace for the largest call is enough for all, whatever forms they take.
+  for (int rows : {0, 8, 16}) {
+    if (rows && group > rows) continue;
+    ChunkQ8Plan f{};
+    f.few = rows;
+    f.can_split = p.can_split;
+    f.ctas = rows ? ctas(group, rows / group) : ctas(p.wide.gp, p.wide.tpt);
+    p.least = std::max(p.least, places(f, batch, total, hq, hkv, d).end);
+  }
   // The wide form where packed_attn.cu would take pairs of row tiles (plan_packed) and sequences have more
-  // than ten row tiles on average, unless its pages could not be counted or took more than 4 GB. 28
+  // than ten row tiles on average. 28
   // query over 4 KV heads of 128, 2,048 cached keys, chunk_kernel against the wide form: 50 rows of 16
   // sequences (3 tiles) 57 and 83 us, 120 of 32 (7) 181 and 190, 200 of 8 (11) 94 and 94, 300 of 32 (17)
   // 434 and 341, 1,400 of 1 (78) 102 and 80; 14 over 2 of 64: 120 of 32 (7) 79 and 92, 300 of 32 (17)
-  // 179 and 155.
-  const long long pages = std::max(1, max_len / kPageSize + (max_len % kPageSize != 0));
-  const long long rows = pages * batch * hkv * kPageSize;
-  if (p.wide.pair && !p.few && total > 10LL * batch * p.tpt && rows <= INT_MAX && rows * d * 4 <= 1LL << 32)
-    p.pages = (int)pages;
-  // CTAs: as many as the items and their parts can keep busy, by the hint
-  const int tiles = packed::key_tiles(max_len) + 1;
-  const long long items = packed::max_tiles(batch, total, p.tpt) * (hq / p.gp);
-  p.can_split = tiles >= 2 * kMinPart;
-  p.ctas = (int)std::min<long long>(num_sms(), items * std::max(1, tiles / kMinPart));
+  // 179 and 155. Its pages: by the hint, in kWideBytes and in what the workspace has beyond the rest
+  // (sequences of more keys are left to chunk_kernel).
+  if (p.wide.pair && !p.few && total > 10LL * batch * p.tpt) {
+    const long long pages = std::max(1, max_len / kPageSize + (max_len % kPageSize != 0));
+    const long long per_page = (long long)batch * (hkv * kPageSize * d * 4LL + (long long)sizeof(int32_t));
+    const size_t besides = p.least + packed::align256(p.wide.ws_bytes) + 4 * 256 + (size_t)batch * sizeof(int32_t);
+    const long long room = ws_bytes > besides ? (long long)std::min(ws_bytes - besides, kWideBytes) : 0;
+    p.pages = (int)std::min(pages, room / per_page);
+  }
   p.tiles = (long long)batch * p.pages + own_groups(batch, total);
-  p.ws_bytes = places(p, batch, total, hq, hkv, d).end;
+  p.ws_bytes = std::max(p.least, places(p, batch, total, hq, hkv, d).end);
   return p;
 }
 

@@ -225,9 +225,10 @@ struct ChunkQ8Plan {
   int pages;               // the wide form's pages per sequence (0: without it)
   long long tiles;         // of own rows and pages that come before the attention
   PackedPlan wide;
-  size_t ws_bytes;
+  size_t least, ws_bytes;  // what has to be there; what the call makes use of
 };
-ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_len);
+// ws_bytes: what there is for the wide form's pages and all else.
+ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_len, size_t ws_bytes = SIZE_MAX);
 cudaError_t launch_chunk_q8(const ChunkQ8& p, const ChunkQ8Plan& plan, void* workspace,
                             cudaStream_t stream);
 

@@ -665,10 +665,10 @@ int mars_attn_chunk_q8(const mars_bf16* q, const mars_bf16* k, const mars_bf16* 
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   if ((rc = check_attn(p.attn, workspace))) return rc;
-  const mars::ChunkQ8Plan plan = mars::plan_chunk_q8(batch, total, hq, hkv, d, max_len_hint);
+  const mars::ChunkQ8Plan plan = mars::plan_chunk_q8(batch, total, hq, hkv, d, max_len_hint, ws_bytes);
   if ((rc = grid_fits(plan.tiles))) return rc;
-  if (ws_bytes < plan.ws_bytes) return MARS_ENOSPACE;
-  if (plan.ws_bytes && !workspace) return MARS_EINVAL;
+  if (ws_bytes < plan.least) return MARS_ENOSPACE;
+  if (plan.least && !workspace) return MARS_EINVAL;
   return cuda_rc(mars::launch_chunk_q8(p, plan, workspace, static_cast<cudaStream_t>(stream)));
 }
 

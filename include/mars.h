@@ -387,7 +387,8 @@ int mars_dual_stream_ce_loss_grad(const mars_bf16* h, const mars_bf16* w,
  * MARS_OP_ATTN_CHUNK, MARS_OP_ATTN_PACKED_GRAD, MARS_OP_ATTN_CHUNK_Q8) for `total` rows of
  * `batch` sequences; max_len: the max_len_hint of a mars_attn_chunk or mars_attn_chunk_q8 call,
  * ignored by the others. 0 for an
- * unknown op, invalid sizes, or an op that needs none. Calls whose kernels may overlap on the
+ * unknown op, invalid sizes, or an op that needs none. The size need not grow with its arguments (ask for
+ * each call's, or take the largest), but for MARS_OP_ATTN_CHUNK_Q8, see there. Calls whose kernels may overlap on the
  * GPU, graph replays among them, each need a workspace of their own. */
 size_t mars_packed_workspace_bytes(int op, int batch, int total, int hq, int hkv, int d,
                                    int max_len);
@@ -510,7 +511,11 @@ int mars_kv_append_q8(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_
 /* mars_attn_chunk over the 8-bit cache: row i of sequence s attends to the P_s = seq_lens[s]
  * cached tokens and to the chunk's rows 0 .. i, given in k and v in bf16. Arguments, errors and
  * what other keys may hold as mars_attn_chunk; the pools and scales as above.
- *   workspace >= mars_packed_workspace_bytes(MARS_OP_ATTN_CHUNK_Q8, ...) bytes (NULL if 0)
+ *   workspace >= mars_packed_workspace_bytes(MARS_OP_ATTN_CHUNK_Q8, ...) bytes (NULL if 0) of this call's
+ *            batch, total and max_len_hint or of larger ones. Where sequences have many rows on average
+ *            (more than ten tiles of 128 (token, head) rows of a KV head) that has room, 2 GB at most, to
+ *            unpack batch * max_len_hint cached tokens. Sequences of more tokens than there is room for are
+ *            computed from the codes, more slowly: a smaller max_len_hint saves memory.
  * Codes and scales enter the products exactly, scores, statistics and sums are held in 32 bits, and
  * the weights are rounded to f16, over the page's scale, for the product with V (many rows: to bf16,
  * the keys and values being unpacked to bf16 first, which holds them exactly). By the number of rows

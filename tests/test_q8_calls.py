@@ -210,3 +210,34 @@ def test_more_sequences_than_a_grid_has_places():
     for batch, total in ((big, big), (big - 1, 1), (1, big - 1), (1 << 20, 1 << 30)):
         size = packed.mars_packed_workspace_bytes(packed.OP_ATTN_CHUNK_Q8, batch, total, 1, 1, 64, 100)
         assert 0 <= size < 1 << 50
+
+
+def fits(batch, total, hq, hkv, d, hint, ws_bytes):
+    """Whether a call takes a workspace of so many bytes. Without its address it then ends as EINVAL, before
+    anything is launched."""
+    a = [P()] * 8 + [9, P(), 4, P(), hint, P(), batch, total, hq, hkv, d, 16, hq * d, hkv * d, hkv * d, 0.0, None,
+                     ws_bytes, None, None]
+    rc = code("mars_attn_chunk_q8", a)
+    assert rc in (mars.EINVAL, mars.ENOSPACE)
+    return rc == mars.EINVAL
+
+
+def test_a_workspace_for_the_largest_call_is_enough_for_all():
+    """Of no more sequences, rows and cached tokens, whatever forms the calls take; and what a call asks for grows
+    with the hint, to 2 GB and some at most."""
+    import random
+    rng = random.Random(3)
+    size = lambda *a: packed.mars_packed_workspace_bytes(packed.OP_ATTN_CHUNK_Q8, *a)   # noqa: E731
+    for i in range(4000):
+        heads = rng.choice([(28, 4, 128), (4, 2, 64), (96, 1, 64), (16, 16, 128), (14, 2, 64), (130, 1, 64)])
+        batch, total, hint = (int(2 ** rng.uniform(0, m)) for m in (9, 14, 20))
+        most = size(batch, total, *heads, hint)
+        assert most <= size(batch, total, *heads, hint + int(2 ** rng.uniform(0, 22)))
+        assert most < (1 << 31) + (1 << 30)
+        b, t, h = rng.randint(1, batch), rng.randint(1, total), rng.randint(0, hint)
+        assert fits(batch, total, *heads, hint, most) and fits(b, t, *heads, h, most), (heads, batch, total, hint, b, t, h)
+    # rows that take the few-row form in one batch and a larger tile in the next; pages beyond the limit
+    for large, small in (((128, 256, 4096), (64, 256, 4096)), ((128, 23041, 16384), (128, 23041, 16385)),
+                         ((12, 5532, 131072), (12, 5532, 2600)), ((12, 5532, 2600), (1, 5532, 2600))):
+        args = lambda s: (s[0], s[1], 28, 4, 128, s[2])                                # noqa: E731
+        assert fits(*args(small), size(*args(large)))
