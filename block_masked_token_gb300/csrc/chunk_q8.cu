@@ -960,6 +960,7 @@ struct ReadyArgs {
   const int32_t *cu, *seq_lens, *block_table;
   const uint8_t *k_pool, *v_pool, *k_scale, *v_scale;
   int num_pages, max_pages, pages, tpt, batch, total, hq, hkv, own_groups;
+  long long tiles;
   // the wide form's pages, lengths and table
   uint16_t *k_out, *v_out;
   int32_t *lens, *table;
@@ -970,6 +971,9 @@ struct ReadyArgs {
   uint16_t* v_half;
 };
 constexpr int kReadyThreads = 256;
+// CTAs per SM where sequences may be unpacked. A hint may be far above what is cached: with a CTA for each tile
+// that there could be, 12 chunks of up to 700 rows over 2,048 keys took 205 us at a hint of 131,072, 132 at 2,380.
+constexpr int kReadyCtas = 16;
 constexpr size_t kWideBytes = (size_t)1 << 31;       // pages of the wide form
 
 // Eight bf16 times f as two e4m3 numbers each: the nearest, and the nearest to what that leaves. An
@@ -1080,31 +1084,11 @@ MARS_DEV void split_rows(const ReadyArgs& a, const packed::Seq& sq, int r0, int 
   }
 }
 
-// Block (x, y): 16 own rows of a sequence, or where it is left to the wide form a page of it (page j
+// A tile: 16 own rows of a sequence of P cached keys, or where it is left to the wide form a page of it (page j
 // of sequence s becomes page s * pages + j); every gridDim.y-th eight heads. Sequences that chunk_kernel takes have no
 // keys in the wide form, and what that then makes of their rows is written over.
 template <int D>
-__global__ void __launch_bounds__(kReadyThreads, 4) ready_kernel(ReadyArgs a) {
-  sm100::let_next_start();
-  sm100::wait_for_previous();
-  const int skip = a.pages ? a.pages : -1;
-  auto cut = [&](int len) { return (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize)); };
-  auto tiles = [](int rows) { return rows / kPageSize + (rows % kPageSize != 0); };
-  __shared__ packed::Seq found;
-  if (threadIdx.x < 32) {                            // (by every warp it was a third of all instructions)
-    bool bad;
-    const packed::Seq sq = packed::find_tile_by(
-        a.cu, a.batch, a.total, (long long)blockIdx.x, bad, a.seq_lens, [&](int, int n, int len) {
-          const int P = cut(len);
-          return max(left_out(skip, a.tpt, n, P) ? tiles(P) : tiles(n), a.pages ? 1 : 0);
-        });
-    if (threadIdx.x == 0) found = sq;
-  }
-  __syncthreads();
-  const packed::Seq sq = found;
-  if (sq.s < 0) return;
-  const int P = cut(sq.len);
-  const bool wide = left_out(skip, a.tpt, sq.n, P);
+MARS_DEV void ready_tile(const ReadyArgs& a, const packed::Seq& sq, int P, bool wide) {
   if (a.pages && sq.tile == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.lens[sq.s] = wide ? P : 0;
   if (!wide) {
     const int r0 = sq.tile * kPageSize;
@@ -1144,6 +1128,35 @@ __global__ void __launch_bounds__(kReadyThreads, 4) ready_kernel(ReadyArgs a) {
     uint4* dst = reinterpret_cast<uint4*>((is_v ? a.v_out : a.k_out) + to * (kPageSize * D)) + 2 * c;
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
     dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  }
+}
+
+// Block (x, y): tiles x, x + gridDim.x, .. of those that there are, of `a.tiles` that there could be by the hint.
+template <int D>
+__global__ void __launch_bounds__(kReadyThreads, 4) ready_kernel(ReadyArgs a) {
+  sm100::let_next_start();
+  sm100::wait_for_previous();
+  const int skip = a.pages ? a.pages : -1;
+  auto cut = [&](int len) { return (int)max(0LL, min((long long)len, (long long)a.max_pages * kPageSize)); };
+  auto tiles = [](int rows) { return rows / kPageSize + (rows % kPageSize != 0); };
+  __shared__ packed::Seq found;
+#pragma unroll 1
+  for (long long i = blockIdx.x; i < a.tiles; i += gridDim.x) {
+    if (threadIdx.x < 32) {                          // (by every warp it was a third of all instructions)
+      bool bad;
+      const packed::Seq sq = packed::find_tile_by(
+          a.cu, a.batch, a.total, i, bad, a.seq_lens, [&](int, int n, int len) {
+            const int P = cut(len);
+            return max(left_out(skip, a.tpt, n, P) ? tiles(P) : tiles(n), a.pages ? 1 : 0);
+          });
+      if (threadIdx.x == 0) found = sq;
+    }
+    __syncthreads();
+    const packed::Seq sq = found;
+    if (sq.s < 0) return;
+    const int P = cut(sq.len);
+    ready_tile<D>(a, sq, P, left_out(skip, a.tpt, sq.n, P));
+    __syncthreads();                                 // `found` is free again
   }
 }
 
@@ -1217,6 +1230,7 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
     u.hq = t.hq;
     u.hkv = t.hkv;
     u.own_groups = (int)own_groups(t.batch, t.total);
+    u.tiles = plan.tiles;
     u.k_out = reinterpret_cast<uint16_t*>(ws + l.k);
     u.v_out = reinterpret_cast<uint16_t*>(ws + l.v);
     u.lens = reinterpret_cast<int32_t*>(ws + l.lens);
@@ -1232,7 +1246,8 @@ cudaError_t launch(const ChunkQ8& p, const ChunkQ8Plan& plan, uint8_t* ws, cudaS
     count_launches(1);
     // (where there are many tiles, one CTA for each: mixed rows 148 us with five, 133 with one)
     const unsigned y = plan.pages ? 1 : (t.hq + 2 * t.hkv + 7) / 8;
-    e = launch_early(ready_kernel<D>, dim3((unsigned)plan.tiles, y), kReadyThreads, 0, stream, u);
+    const long long most = plan.pages ? (long long)num_sms() * kReadyCtas : plan.tiles;
+    e = launch_early(ready_kernel<D>, dim3((unsigned)std::min(plan.tiles, most), y), kReadyThreads, 0, stream, u);
     if (e != cudaSuccess) return e;
     if (plan.pages) {
       PackedAttn wide = t;

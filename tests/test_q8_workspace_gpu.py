@@ -64,3 +64,14 @@ def test_the_bindings_refuse_a_workspace_that_is_too_small(lens, old, hint):
             run_chunk8(y, hint=hint, ws=ws)
         with pytest.raises(mars.MarsError):
             run_chunk8(y, hint=hint, ws=ws, stream=torch.cuda.current_stream())
+
+
+def test_more_tiles_than_ctas_make_ready():
+    """Own rows and pages of more than 3,100 groups of 16, which 16 CTAs per SM take in turn."""
+    lens, old = [190 + i for i in range(12)], [4000 + 13 * i for i in range(12)]
+    x = make8(lens, *HEADS, old, seed=930)
+    y = cuda(x)
+    for hint in (hint_of(x), 131072):
+        o, st = run_chunk8(y, hint=hint)
+        assert st == 0
+        check_chunk8(x, o, rows=[0, 17, 100, 189])
