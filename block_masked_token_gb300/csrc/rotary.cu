@@ -5,9 +5,10 @@
 // A pass over memory: 4 (hq + hkv) d bytes per row, read and written once. A CTA takes kRows rows
 // of one sequence; the sines and cosines of its rows, the same for every head, are formed once
 // into shared memory. t reaches far beyond what 32 bits resolve (position 131,072 at f = 1 is off
-// by 0.008 in fp32), so f / 2 pi is kept as a 64-bit fraction of a turn: its product with the
-// position, modulo 1 by itself, is exact up to 2^-52 of a turn per position, and sincospi gets the
-// upper 32 bits of it.
+// by 0.008 in fp32), so f / 2 pi is kept as a 64-bit fraction of a turn, off by 2^-52 of f / 2 pi at most:
+// its product with the position is modulo 1 by itself. sincospi gets the upper 32 bits as a float
+// of half turns in [-1, 1), which keeps 24 of them: pi 2^-25 off at most, to which a position adds itself times
+// f 2^-52 radians.
 //
 // Prompts of 10,586 rows of 28 + 4 heads of 128 (173 MB moved): 31.1 us, 0.82 of the copy bandwidth; the
 // gradient over 8,191 long rows 24.7 us, 0.80. With 8 rows per CTA 31.2 and 27.6 (fewer CTAs to even out

@@ -285,7 +285,10 @@ def rotary_frequencies(rot, base: float = 10000.0, scaling=None, stretch: float 
                  fastest not at all
       "parts"    a pair that turns fewer than `low` times over the `trained` positions is divided
                  by stretch, one that turns more than `high` times is not, and between the two the
-                 share falls linearly; factor = 1 + 0.1 ln(stretch) keeps the softmax as sharp."""
+                 share falls linearly in the number of turns; factor = 1 + 0.1 ln(stretch) keeps the
+                 softmax as sharp.
+    A model that was trained with another scaling, one whose share falls linearly in j among them, needs
+    its own table: mars_rotary takes any."""
     if rot < 2 or rot % 2:
         raise ValueError(f"rot is {rot}: it must be even and at least 2")
     if not base > 0 or not stretch >= 1:
