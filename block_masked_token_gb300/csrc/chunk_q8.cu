@@ -31,9 +31,9 @@
 // waits), softmax (2,300), P V (700), waits (1,000) takes 5,000 cycles for each of the two buffers; TMEM
 // has no room for a third beside two O of 128 columns.
 //
-// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 2,048 .. 8,192 keys): 244 us,
-// 0.45 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 37 us, of which the three
-// launches and the start and end of every CTA are about 24.
+// Blocks of 16 positions (28 query over 4 KV heads of 128, 128 sequences of 2,048 .. 8,192 keys): 246 us,
+// 0.45 of the copy bandwidth; of 8, 32 sequences of 512 .. 2,048 keys: 39 us, of which the three
+// launches and the start and end of every CTA are about 25.
 //
 // Roles (640 threads): warp 0 walks the items and reads block table and scales ahead of the others
 // (infos); warp 1 copies K and Q; warps 12..15 copy V of even tiles, 16..19 of odd ones, two pages each
@@ -1349,11 +1349,12 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
   p.gp = p.wide.gp;
   p.tpt = p.wide.tpt;
   const int group = hq / hkv;
-  // chunk_q8_few.cu where a sequence's rows make one of its tiles (28 query over 4 KV heads of 128, 32
-  // sequences of 2,048 keys and 2 tokens each: 32 us, here 43 us with 4 tokens each); or several, each of
-  // which reads the cache again, where neither are they more than the SMs nor their keys many: 4 tokens of
-  // 8 sequences over 512 keys 15.7 us against 23.6 here, 64 of 1 15.6 and 24.9, 16 of 4 over 1,024 24.5 and
-  // 25.9, over 2,000 29.2 and 24.8, 16 of 2 over 2,000 22.3 and 23.9, 8 of 1 over 8,192 23.3 and 23.6.
+  // chunk_q8_few.cu where a sequence's rows make one of its tiles, on average (28 query over 4 KV heads of 128, 32
+  // sequences of 2,048 keys and 2 tokens each: 31 us against 44 here; with 4 tokens each, two tiles, 48 and 45); or
+  // several, each of which reads the cache again, where neither are they more than the SMs nor their keys many:
+  // 4 tokens of 8 sequences over 512 keys 17.2 us against 25.3 here, 64 of 1 17.5 and 26.9, 16 of 4 over 1,024
+  // 26.3 and 26.9, over 2,000 30.8 and 26.5, 16 of 2 over 2,000 23.8 and 25.4, 8 of 1 over 8,192 24.7 and 28.8 (which
+  // the bound on the keys leaves here).
   for (int rows : {16, 8}) {
     if (group > rows) continue;
     const long long mine = packed::max_tiles(batch, total, rows / group) * hkv;
@@ -1384,12 +1385,11 @@ ChunkQ8Plan plan_chunk_q8(int batch, int total, int hq, int hkv, int d, int max_
     p.least = std::max(p.least, places(f, batch, total, hq, hkv, d).end);
   }
   // The wide form where packed_attn.cu would take pairs of row tiles (plan_packed) and sequences have more
-  // than ten row tiles on average. 28
-  // query over 4 KV heads of 128, 2,048 cached keys, chunk_kernel against the wide form: 50 rows of 16
-  // sequences (3 tiles) 57 and 83 us, 120 of 32 (7) 181 and 190, 200 of 8 (11) 94 and 94, 300 of 32 (17)
-  // 434 and 341, 1,400 of 1 (78) 102 and 80; 14 over 2 of 64: 120 of 32 (7) 79 and 92, 300 of 32 (17)
-  // 179 and 155. Its pages: by the hint, in kWideBytes and in what the workspace has beyond the rest
-  // (sequences of more keys are left to chunk_kernel).
+  // than ten row tiles on average. 28 query over 4 KV heads of 128, 2,048 cached keys, chunk_kernel against
+  // the wide form: 50 rows of 16 sequences (3 tiles) 61 and 82 us, 120 of 32 (7) 199 and 190, 200 of 8 (11) 99
+  // and 92, 300 of 32 (17) 475 and 335, 1,400 of 1 (78) 106 and 79; 14 over 2 of 64: 120 of 32 (7) 87 and 91, 300
+  // of 32 (17) 199 and 157. Its pages: by the hint, in kWideBytes and in what the workspace has beyond
+  // the rest (sequences of more keys are left to chunk_kernel).
   if (p.wide.pair && !p.few && total > 10LL * batch * p.tpt) {
     const long long pages = std::max(1, max_len / kPageSize + (max_len % kPageSize != 0));
     const long long per_page = (long long)batch * (hkv * kPageSize * d * 4LL + (long long)sizeof(int32_t));

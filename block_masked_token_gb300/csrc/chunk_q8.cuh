@@ -31,8 +31,8 @@ constexpr int kPagesPerTile = kTile / kPageSize;
 constexpr long long kUnit = 8;       // work of a key tile
 constexpr int kMinPart = 2;          // key tiles of a part of a divided item
 // Work of an item's start and end, in chunk_q8.cu (8 positions, 28 query over 4 KV heads, 32 sequences of
-// 512 .. 2,048 keys: 35.8 us at 4, 35.0 at 24, 38.5 at 48, 40.5 at 64; 16 positions, 128 sequences of
-// 2,048 .. 8,192: 252, 241, 237, 238) and in chunk_q8_few.cu (single tokens, 32 sequences of 2,048 .. 8,192:
+// 512 .. 2,048 keys: 40.2 us at 4, 39.4 at 24, 41.9 at 48, 44.7 at 64; 16 positions, 128 sequences of
+// 2,048 .. 8,192: 256, 246, 244, 247) and in chunk_q8_few.cu (single tokens, 32 sequences of 2,048 .. 8,192:
 // 45.6 at 12, 42.7 at 32, 41.5 at 64, 41.6 at 80)
 constexpr int kItemWork = 24, kFewItemWork = 64;
 constexpr float kLift = 7.f;         // log2 of what P' is multiplied by

@@ -18,7 +18,7 @@
 //      codes of two keys. Rows g and 8 + g of product j are then d = g D/8 + 2j and the next.
 // A lane has the scores of keys g and 8 + g for rows 2t and 2t + 1; movmatrix turns the weights.
 //
-// Single tokens of 32 sequences of 2,048 .. 8,192 keys (28 query over 4 KV heads of 128): 41.3 us, 0.63 of
+// Single tokens of 32 sequences of 2,048 .. 8,192 keys (28 query over 4 KV heads of 128): 42 us, 0.62 of
 // the copy bandwidth (the first form, rows as the 16 rows of a product, 55.4; chunk_kernel 87.8). From
 // 4,096 to 16,384 keys each it gains on them at 7 TB/s, the memory's rate; what is left is the launches
 // (3 us), 6 us before the first copy (boundaries, the part, a page's entry, its scales, in turn) and

@@ -528,9 +528,11 @@ int mars_kv_append_q8(const mars_bf16* k, const mars_bf16* v, const int32_t* cu_
  *   infinity in q or an own k is NaN), and own values in f16, exact to 2^-29 of the row's largest;
  *   in bf16 (many rows).
  * In the first two forms the powers of own values begin at 2^-40 (what lies below 2^-64 is lost) and
- * finite ones from 2^88 on count as the largest bf16 below; in all forms a key whose weight is below
- * 2^-20 of the row's largest may miss in the row sum where values differ by more than 2^100.
- * Each result is the same, bit by bit, from call to call. */
+ * finite ones from 2^88 on count as the largest bf16 below; beside values 2^100 times its page's scale a
+ * key whose weight is below 2^-20 of the row's largest may miss in the row sum.
+ * The form is the whole call's, by the average of its rows, max_len_hint and the room in the workspace: with
+ * these equal each result is the same, bit by bit, from call to call, and changes within the roundings above
+ * with the other sequences of a call. */
 int mars_attn_chunk_q8(const mars_bf16* q, const mars_bf16* k, const mars_bf16* v,
                        const int32_t* cu_seqlens, const uint8_t* k_pool, const uint8_t* v_pool,
                        const uint8_t* k_scale, const uint8_t* v_scale, int num_pages,
